@@ -30,6 +30,9 @@ PATH_AUTO, PATH_GEMV, PATH_TENSOR = 0, 1, 2
 FLAG_CONST_WEIGHTS = 1
 FLAG_INDEPENDENT = 2
 ID_SLOTTED = 1
+DTYPE_F32, DTYPE_BF16 = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 _PATHS = {"auto": PATH_AUTO, "gemv": PATH_GEMV, "tensor": PATH_TENSOR,
           PATH_AUTO: PATH_AUTO, PATH_GEMV: PATH_GEMV, PATH_TENSOR: PATH_TENSOR}
 
@@ -81,6 +84,19 @@ class MatmulCall(ctypes.Structure):
 class EmbeddingParams(ctypes.Structure):
     _fields_ = [("vocab_size", ctypes.c_uint32), ("embed_dim", ctypes.c_uint32),
                 ("n_tokens", ctypes.c_uint32), ("ggml_type", ctypes.c_uint32)]
+
+
+class GatedFfnParams(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("k", ctypes.c_uint32),
+                ("ggml_type", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("act", ctypes.c_uint32)]
+
+
+class LoraParams(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("k", ctypes.c_uint32),
+                ("ggml_type", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("rank", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
 
 
 _lock = threading.Lock()
@@ -147,12 +163,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.q2k_matmul_ex_batch.argtypes = [ctypes.POINTER(MatmulCall), sz, vp, sz, vp]
         lib.q2k_matmul_batch_scratch_bytes.argtypes = [ctypes.POINTER(MatmulCall), sz]
         lib.q2k_matmul_batch_scratch_bytes.restype = sz
+        gfp, lop, u32 = ctypes.POINTER(GatedFfnParams), ctypes.POINTER(LoraParams), ctypes.c_uint32
+        lib.q2k_gated_ffn.argtypes = [ctypes.c_int, u32, vp, sz, vp, sz, vp, sz, vp, sz, vp, vp,
+                                      gfp, vp, sz, vp]
+        lib.q2k_gated_ffn_workspace_bytes.argtypes = [ctypes.c_int, gfp]
+        lib.q2k_gated_ffn_workspace_bytes.restype = sz
+        lib.q2k_gated_ffn_backward.argtypes = [vp, vp, vp, sz, vp, sz, vp, sz, vp, sz, vp, vp,
+                                               gfp, vp, sz, vp]
+        lib.q2k_gated_ffn_backward_workspace_bytes.argtypes = [gfp]
+        lib.q2k_gated_ffn_backward_workspace_bytes.restype = sz
+        lib.q2k_matmul_lora.argtypes = [ctypes.c_int, u32, vp, sz, vp, sz, vp, sz, vp, sz, vp, vp,
+                                        vp, sz, lop, vp, vp, sz, vp]
+        lib.q2k_matmul_lora_workspace_bytes.argtypes = [ctypes.c_int, lop]
+        lib.q2k_matmul_lora_workspace_bytes.restype = sz
         lib.q2k_device_error.argtypes = [u32p, vp]
         lib.q2k_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
         for fn in ("q2k_dequantize", "q2k_embedding_gather", "q2k_matmul", "q2k_matmul_path",
                    "q2k_matmul_ex", "q2k_matmul_ex_batch", "q2k_matmul_batched_mv", "q2k_matmul_id",
                    "q2k_matmul_id_slotted", "q2k_matmul_id_pair", "q2k_matmul_id_ex",
-                   "q2k_matmul_id_pair_ex", "q2k_device_error",
+                   "q2k_matmul_id_pair_ex", "q2k_gated_ffn", "q2k_gated_ffn_backward",
+                   "q2k_matmul_lora", "q2k_device_error",
                    "q2k_selftest_wait_timeout", "q2k_gguf_open", "q2k_gguf_tensor_info",
                    "q2k_gguf_read_tensor"):
             getattr(lib, fn).restype = ctypes.c_int
@@ -648,6 +678,177 @@ def matmul_id_workspace_bytes(n_tokens: int, top_k: int, n: int, k: int, n_exper
     p = MatmulIdParams(n_tokens, top_k, n, k, n_experts, GGML_TYPE_Q2_K, expert_stride)
     return int(load().q2k_matmul_id_workspace_bytes(_PATHS[path], ID_SLOTTED if slotted else 0,
                                                     ctypes.byref(p)))
+
+
+def _activations(t, name, shape=None, like=None):
+    """The dtype code of a contiguous f32 or bf16 CUDA tensor, its shape, device
+    and (with ``like``) dtype checked."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if like is not None:
+        _require_cuda(t, name, like.dtype)
+        _same_device(t, name, like)
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+
+
+def _same_device(t, name, like):
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _workspace(workspace, need, like):
+    """(tensor or None, pointer, bytes): "auto" takes one from PyTorch's allocator."""
+    torch = _torch()
+    if isinstance(workspace, str):
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    if workspace is None:
+        return None, None, 0
+    _require_cuda(workspace, "workspace", torch.uint8)
+    _same_device(workspace, "workspace", like)
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None, path="auto",
+              const_weights: bool = False, workspace="auto"):
+    """The gated feed-forward block ``h = act(x Wg^T) * (x Wu^T)``: both
+    projections, the activation and the product in one kernel.
+
+    ``x`` f32 or bf16 ``[m, k]``; ``w_gate``, ``w_up`` uint8, ``n`` rows of Q2_K
+    blocks each; ``act`` "silu" or "gelu" (the tanh form).  Returns h ``[m, n]``
+    in x's dtype, or with ``save`` ``(h, gate, up)`` with the two projections
+    that ``gated_ffn_backward`` reads.  ``path``, ``const_weights`` and
+    ``workspace`` as in ``matmul``: up to 16 bf16 or 8 f32 tokens the weights
+    are exact, above that x and W are rounded to bf16 for the tensor cores.
+    """
+    torch = _torch()
+    dtype = _activations(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [m, k]")
+    m, k = x.shape
+    for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
+        _require_cuda(t, name, torch.uint8)
+        _same_device(t, name, x)
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    _activations(out, "out", (m, n), like=x)
+    gate = torch.empty_like(out) if save else None
+    up = torch.empty_like(out) if save else None
+    p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, dtype, _ACTS[act])
+    lib = _lib if _lib is not None else load()
+    pcode = _PATHS[path]
+    need = lib.q2k_gated_ffn_workspace_bytes(pcode, ctypes.byref(p))
+    _keep, ws, ws_bytes = _workspace(workspace, need, x)
+    with _on_device(x):
+        _check(lib, lib.q2k_gated_ffn(pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
+                                      x.data_ptr(), x.numel(), w_gate.data_ptr(), w_gate.numel(),
+                                      w_up.data_ptr(), w_up.numel(), out.data_ptr(), out.numel(),
+                                      gate.data_ptr() if save else None,
+                                      up.data_ptr() if save else None, ctypes.byref(p), ws,
+                                      ws_bytes, _stream_handle(x)))
+    return (out, gate, up) if save else out
+
+
+def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace="auto"):
+    """The backward pass of ``gated_ffn`` with its weights frozen, bf16 only.
+
+    ``dh``, ``gate``, ``up`` bf16 ``[m, n]`` (the gradient of h and the saved
+    projections); returns ``(dx, dgate, dup)``: ``dx = dgate Wg + dup Wu``
+    ``[m, k]`` and the gradients ``[m, n]`` of the two projections.
+    """
+    torch = _torch()
+    _require_cuda(dh, "dh", torch.bfloat16)
+    if dh.dim() != 2:
+        raise ValueError("dh must be [m, n]")
+    m, n = dh.shape
+    _activations(gate, "gate", (m, n), like=dh)
+    _activations(up, "up", (m, n), like=dh)
+    for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
+        _require_cuda(t, name, torch.uint8)
+        _same_device(t, name, dh)
+    dx = torch.empty((m, k), dtype=dh.dtype, device=dh.device)
+    dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
+    p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, DTYPE_BF16, _ACTS[act])
+    lib = _lib if _lib is not None else load()
+    need = lib.q2k_gated_ffn_backward_workspace_bytes(ctypes.byref(p))
+    _keep, ws, ws_bytes = _workspace(workspace, need, dh)
+    with _on_device(dh):
+        _check(lib, lib.q2k_gated_ffn_backward(dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
+                                               dh.numel(), w_gate.data_ptr(), w_gate.numel(),
+                                               w_up.data_ptr(), w_up.numel(), dx.data_ptr(),
+                                               dx.numel(), dgate.data_ptr(), dup.data_ptr(),
+                                               ctypes.byref(p), ws, ws_bytes, _stream_handle(dh)))
+    return dx, dgate, dup
+
+
+def matmul_lora(x, w, n: int, lora_a, lora_b, ids, scales=None, out=None, path="auto",
+                const_weights: bool = False, workspace="auto", check: bool = True):
+    """A shared projection with low-rank adapters of many requests at once:
+    ``y_i = W x_i + s_a B_a (A_a x_i)`` with ``a = ids[i]``, -1 for none.
+
+    ``x`` f32 or bf16 ``[m, k]``; ``w`` uint8, ``n`` rows of Q2_K blocks;
+    ``lora_a`` bf16 ``[n_adapters, rank, k]``, ``lora_b`` bf16 ``[n_adapters, n,
+    rank]`` (rank a multiple of 8, lower ranks padded with zeros); ``ids`` int32
+    ``[m]``; ``scales`` f32 ``[n_adapters]`` or None.  Returns ``[m, n]`` in x's
+    dtype.  With ``check`` the call waits and raises ``InvalidArgument`` if an
+    id was neither -1 nor below n_adapters; with ``check=False`` it returns
+    ``(out, bad_id_count)`` without waiting (such a token's row is zero).
+    ``path``, ``const_weights`` and ``workspace`` as in ``gated_ffn``.
+    """
+    torch = _torch()
+    dtype = _activations(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [m, k]")
+    m, k = x.shape
+    _require_cuda(w, "w", torch.uint8)
+    _require_cuda(lora_a, "lora_a", torch.bfloat16)
+    _require_cuda(lora_b, "lora_b", torch.bfloat16)
+    _require_cuda(ids, "ids", torch.int32)
+    if lora_a.dim() != 3 or lora_a.shape[2] != k:
+        raise ValueError(f"lora_a must be [n_adapters, rank, {k}], got {list(lora_a.shape)}")
+    n_adapters, rank = lora_a.shape[:2]
+    if tuple(lora_b.shape) != (n_adapters, n, rank):
+        raise ValueError(f"lora_b must be {[n_adapters, n, rank]}, got {list(lora_b.shape)}")
+    if tuple(ids.shape) != (m,):
+        raise ValueError(f"ids must be [{m}], got {list(ids.shape)}")
+    if scales is not None:
+        _require_cuda(scales, "scales", torch.float32)
+        if tuple(scales.shape) != (n_adapters,):
+            raise ValueError(f"scales must be [{n_adapters}], got {list(scales.shape)}")
+    for t, name in ((w, "w"), (lora_a, "lora_a"), (lora_b, "lora_b"), (ids, "ids"),
+                    (scales, "scales")):
+        if t is not None:
+            _same_device(t, name, x)
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    _activations(out, "out", (m, n), like=x)
+    bad = torch.empty(1, dtype=torch.int32, device=x.device)
+    p = LoraParams(m, n, k, GGML_TYPE_Q2_K, dtype, rank, n_adapters, 0)
+    lib = _lib if _lib is not None else load()
+    pcode = _PATHS[path]
+    need = lib.q2k_matmul_lora_workspace_bytes(pcode, ctypes.byref(p))
+    _keep, ws, ws_bytes = _workspace(workspace, need, x)
+    with _on_device(x):
+        _check(lib, lib.q2k_matmul_lora(pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
+                                        x.data_ptr(), x.numel(), w.data_ptr(), w.numel(),
+                                        lora_a.data_ptr(), lora_a.numel(), lora_b.data_ptr(),
+                                        lora_b.numel(),
+                                        scales.data_ptr() if scales is not None else None,
+                                        ids.data_ptr(), out.data_ptr(), out.numel(),
+                                        ctypes.byref(p), bad.data_ptr(), ws, ws_bytes,
+                                        _stream_handle(x)))
+    if not check:
+        return out, bad
+    n_bad = int(bad.item())
+    if n_bad:
+        raise InvalidArgument(1, f"{n_bad} adapter id(s) outside -1..{n_adapters - 1}")
+    return out
 
 
 class GgufFile:

@@ -952,3 +952,330 @@ q2k_status q2k_device_error(uint32_t* out, q2k_stream_t stream) {
 }
 
 }  // extern "C"
+
+// ---- feed-forward operators ---------------------------------------------------
+
+namespace {
+
+struct Span {
+    const void* p;
+    size_t bytes;
+    const char* name;
+};
+
+// Every buffer of a call: the writable ones may overlap nothing else.
+q2k_status check_disjoint(const Span* out, int n_out, const Span* in, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                return fail(Q2K_ERR_INVALID_ARGUMENT, "%s must not alias %s", out[i].name, in[j].name);
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return fail(Q2K_ERR_INVALID_ARGUMENT, "%s must not alias %s", out[i].name, out[j].name);
+    }
+    return Q2K_OK;
+}
+
+// A call's geometry: sizes in elements and bytes, or the reason it is refused.
+struct FfnShape {
+    size_t mk, mn, w_bytes;
+    size_t elem;  // bytes of an activation
+};
+
+q2k_status check_ffn_shape(uint32_t m, uint32_t n, uint32_t k, uint32_t ggml_type, uint32_t dtype,
+                           FfnShape* s) {
+    if (ggml_type != Q2K_GGML_TYPE_Q2_K)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "ggml_type %u is not Q2_K (10)", ggml_type);
+    if (m == 0 || n == 0 || k == 0)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "m, n, k must be >= 1 (got %u, %u, %u)", m, n, k);
+    if (k % Q2K_QK_K != 0)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "k = %u is not a multiple of 256", k);
+    // tiles of tokens and rows are counted in grid dimensions of 16 bits
+    if (m > Q2K_FFN_MAX_TOKENS || n > Q2K_FFN_MAX_WIDTH || k > Q2K_FFN_MAX_WIDTH)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "m must be <= %d and n, k <= %d (got %u, %u, %u)",
+                    Q2K_FFN_MAX_TOKENS, Q2K_FFN_MAX_WIDTH, m, n, k);
+    if (dtype != Q2K_DTYPE_F32 && dtype != Q2K_DTYPE_BF16)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown dtype %u", dtype);
+    // (no product overflows: m k, m n and n k are below 2^41)
+    s->mk = static_cast<size_t>(m) * k;
+    s->mn = static_cast<size_t>(m) * n;
+    s->w_bytes = static_cast<size_t>(n) * (k / Q2K_QK_K) * Q2K_BLOCK_BYTES;
+    s->elem = dtype == Q2K_DTYPE_F32 ? 4 : 2;
+    return Q2K_OK;
+}
+
+q2k_status check_elems(const char* name, size_t got, size_t want) {
+    if (got != want)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "%s has %zu elements, expected %zu", name, got, want);
+    return Q2K_OK;
+}
+
+q2k_status check_weights(const char* name, const void* w, size_t got, size_t want) {
+    if (got != want)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "%s has %zu bytes, expected n*k/256*84 = %zu", name, got, want);
+    if (!aligned(w, 4)) return fail(Q2K_ERR_INVALID_ARGUMENT, "%s must be 4-byte aligned", name);
+    return Q2K_OK;
+}
+
+q2k_status check_ffn_workspace(const void* workspace, size_t got, size_t need) {
+    if (need == 0) return Q2K_OK;
+    if (workspace == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "workspace is NULL, needs %zu bytes", need);
+    if (got < need)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "workspace has %zu bytes, needs %zu", got, need);
+    if (!aligned(workspace, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+    return Q2K_OK;
+}
+
+q2k_status check_path_flags(q2k_path path, uint32_t flags) {
+    if (path != Q2K_PATH_AUTO && path != Q2K_PATH_GEMV && path != Q2K_PATH_TENSOR)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown path %d", static_cast<int>(path));
+    if ((flags & ~uint32_t(Q2K_FLAG_CONST_WEIGHTS)) != 0)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown flag bits 0x%x", flags);
+    return Q2K_OK;
+}
+
+bool takes_tensor_path(q2k_path path, uint32_t m, uint32_t dtype) {
+    if (path != Q2K_PATH_AUTO) return path == Q2K_PATH_TENSOR;
+    return !q2k::ffn_rows_path(static_cast<int>(m), dtype == Q2K_DTYPE_BF16);
+}
+
+q2k::GatedArgs gated_args(q2k_path path, const q2k_gated_ffn_params* p) {
+    q2k::GatedArgs a = {};
+    a.M = static_cast<int>(p->m);
+    a.N = static_cast<int>(p->n);
+    a.K = static_cast<int>(p->k);
+    a.act = static_cast<int>(p->act);
+    a.bf16 = p->dtype == Q2K_DTYPE_BF16;
+    a.tensor = takes_tensor_path(path, p->m, p->dtype);
+    return a;
+}
+
+q2k::GatedBackwardArgs gated_backward_args(const q2k_gated_ffn_params* p) {
+    q2k::GatedBackwardArgs a = {};
+    a.M = static_cast<int>(p->m);
+    a.N = static_cast<int>(p->n);
+    a.K = static_cast<int>(p->k);
+    a.act = static_cast<int>(p->act);
+    return a;
+}
+
+q2k::LoraArgs lora_args(q2k_path path, const q2k_lora_params* p) {
+    q2k::LoraArgs a = {};
+    a.M = static_cast<int>(p->m);
+    a.N = static_cast<int>(p->n);
+    a.K = static_cast<int>(p->k);
+    a.R = static_cast<int>(p->rank);
+    a.n_adapters = static_cast<int>(p->n_adapters);
+    a.bf16 = p->dtype == Q2K_DTYPE_BF16;
+    a.tensor = takes_tensor_path(path, p->m, p->dtype);
+    return a;
+}
+
+q2k_status check_gated(const q2k_gated_ffn_params* p, FfnShape* s) {
+    if (p == nullptr) return fail(Q2K_ERR_INVALID_ARGUMENT, "params is NULL");
+    q2k_status st = check_ffn_shape(p->m, p->n, p->k, p->ggml_type, p->dtype, s);
+    if (st != Q2K_OK) return st;
+    if (p->act != Q2K_ACT_SILU && p->act != Q2K_ACT_GELU)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown act %u", p->act);
+    return Q2K_OK;
+}
+
+q2k_status check_lora(const q2k_lora_params* p, FfnShape* s) {
+    if (p == nullptr) return fail(Q2K_ERR_INVALID_ARGUMENT, "params is NULL");
+    q2k_status st = check_ffn_shape(p->m, p->n, p->k, p->ggml_type, p->dtype, s);
+    if (st != Q2K_OK) return st;
+    if (p->rank == 0 || p->rank % 8 != 0 || p->rank > Q2K_LORA_MAX_RANK)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "rank = %u is not a multiple of 8 in 8..%d", p->rank,
+                    Q2K_LORA_MAX_RANK);
+    if (p->n_adapters == 0 || p->n_adapters > Q2K_LORA_MAX_ADAPTERS)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "n_adapters must be in 1..%d, got %u",
+                    Q2K_LORA_MAX_ADAPTERS, p->n_adapters);
+    if (p->reserved != 0) return fail(Q2K_ERR_INVALID_ARGUMENT, "reserved must be 0");
+    return Q2K_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params* p) {
+    FfnShape s;
+    if (check_path_flags(path, 0) != Q2K_OK || check_gated(p, &s) != Q2K_OK) return 0;
+    return q2k::gated_workspace_bytes(gated_args(path, p));
+}
+
+q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void* x, size_t x_elems,
+                         const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                         size_t w_up_bytes, void* h, size_t h_elems, void* gate, void* up,
+                         const q2k_gated_ffn_params* p, void* workspace, size_t workspace_bytes,
+                         q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    FfnShape s;
+    q2k_status st = check_gated(p, &s);
+    if (st == Q2K_OK) st = check_path_flags(path, flags);
+    if (st != Q2K_OK) return st;
+    if (x == nullptr || w_gate == nullptr || w_up == nullptr || h == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, w_gate, w_up and h must be non-NULL");
+    if ((gate == nullptr) != (up == nullptr))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "gate and up must both be NULL or both non-NULL");
+    if ((st = check_elems("x", x_elems, s.mk)) != Q2K_OK ||
+        (st = check_weights("w_gate", w_gate, w_gate_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_weights("w_up", w_up, w_up_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_elems("h", h_elems, s.mn)) != Q2K_OK)
+        return st;
+    if (!aligned(x, 16) || !aligned(h, 16) || !aligned(gate, 16) || !aligned(up, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, h, gate and up must be 16-byte aligned");
+    q2k::GatedArgs a = gated_args(path, p);
+    const size_t need = q2k::gated_workspace_bytes(a);
+    if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
+    const size_t out_bytes = s.mn * s.elem, save_bytes = gate != nullptr ? out_bytes : 0;
+    const Span out[] = {{h, out_bytes, "h"}, {gate, save_bytes, "gate"}, {up, save_bytes, "up"},
+                        {workspace, need, "workspace"}};
+    const Span in[] = {{x, s.mk * s.elem, "x"}, {w_gate, s.w_bytes, "w_gate"},
+                       {w_up, s.w_bytes, "w_up"}};
+    if ((st = check_disjoint(out, 4, in, 3)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    a.x = x;
+    a.wg = static_cast<const uint8_t*>(w_gate);
+    a.wu = static_cast<const uint8_t*>(w_up);
+    a.h = h;
+    a.gate = gate;
+    a.up = up;
+    a.const_weights = (flags & Q2K_FLAG_CONST_WEIGHTS) != 0;
+    a.device = dev.device;
+    a.sm_count = dev.sm_count;
+    const cudaError_t e =
+        q2k::launch_gated(a, need ? workspace : nullptr, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_gated_ffn launch");
+}
+
+size_t q2k_gated_ffn_backward_workspace_bytes(const q2k_gated_ffn_params* p) {
+    FfnShape s;
+    if (check_gated(p, &s) != Q2K_OK) return 0;
+    return q2k::gated_backward_workspace_bytes(gated_backward_args(p));
+}
+
+q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* up, size_t h_elems,
+                                  const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                                  size_t w_up_bytes, void* dx, size_t dx_elems, void* dgate,
+                                  void* dup, const q2k_gated_ffn_params* p, void* workspace,
+                                  size_t workspace_bytes, q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    FfnShape s;
+    q2k_status st = check_gated(p, &s);
+    if (st != Q2K_OK) return st;
+    if (p->dtype != Q2K_DTYPE_BF16)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "the backward pass takes bf16 activations only");
+    if (dh == nullptr || gate == nullptr || up == nullptr || w_gate == nullptr || w_up == nullptr ||
+        dx == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "dh, gate, up, w_gate, w_up and dx must be non-NULL");
+    if ((dgate == nullptr) != (dup == nullptr))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "dgate and dup must both be NULL or both non-NULL");
+    if ((st = check_elems("dh", h_elems, s.mn)) != Q2K_OK ||
+        (st = check_weights("w_gate", w_gate, w_gate_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_weights("w_up", w_up, w_up_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_elems("dx", dx_elems, s.mk)) != Q2K_OK)
+        return st;
+    if (!aligned(dh, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(dx, 16) ||
+        !aligned(dgate, 16) || !aligned(dup, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT,
+                    "dh, gate, up, dx, dgate and dup must be 16-byte aligned");
+    q2k::GatedBackwardArgs a = gated_backward_args(p);
+    const size_t need = q2k::gated_backward_workspace_bytes(a);
+    if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
+    const size_t mn_bytes = s.mn * 2, save_bytes = dgate != nullptr ? mn_bytes : 0;
+    const Span out[] = {{dx, s.mk * 2, "dx"}, {dgate, save_bytes, "dgate"}, {dup, save_bytes, "dup"},
+                        {workspace, need, "workspace"}};
+    const Span in[] = {{dh, mn_bytes, "dh"}, {gate, mn_bytes, "gate"}, {up, mn_bytes, "up"},
+                       {w_gate, s.w_bytes, "w_gate"}, {w_up, s.w_bytes, "w_up"}};
+    if ((st = check_disjoint(out, 4, in, 5)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    a.dh = static_cast<const __nv_bfloat16*>(dh);
+    a.gate = static_cast<const __nv_bfloat16*>(gate);
+    a.up = static_cast<const __nv_bfloat16*>(up);
+    a.wg = static_cast<const uint8_t*>(w_gate);
+    a.wu = static_cast<const uint8_t*>(w_up);
+    a.dx = static_cast<__nv_bfloat16*>(dx);
+    a.dgate = static_cast<__nv_bfloat16*>(dgate);
+    a.dup = static_cast<__nv_bfloat16*>(dup);
+    a.device = dev.device;
+    a.sm_count = dev.sm_count;
+    const cudaError_t e =
+        q2k::launch_gated_backward(a, workspace, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_gated_ffn_backward launch");
+}
+
+size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params* p) {
+    FfnShape s;
+    if (check_path_flags(path, 0) != Q2K_OK || check_lora(p, &s) != Q2K_OK) return 0;
+    return q2k::lora_workspace_bytes(lora_args(path, p));
+}
+
+q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void* x, size_t x_elems,
+                           const void* w, size_t w_bytes, const void* a, size_t a_elems,
+                           const void* b, size_t b_elems, const float* scales, const int32_t* ids,
+                           void* y, size_t y_elems, const q2k_lora_params* p,
+                           uint32_t* bad_id_count, void* workspace, size_t workspace_bytes,
+                           q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    FfnShape s;
+    q2k_status st = check_lora(p, &s);
+    if (st == Q2K_OK) st = check_path_flags(path, flags);
+    if (st != Q2K_OK) return st;
+    if (x == nullptr || w == nullptr || a == nullptr || b == nullptr || ids == nullptr || y == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, w, a, b, ids and y must be non-NULL");
+    // (n_adapters * rank * k < 2^16 * 2^8 * 2^21)
+    const size_t a_want = static_cast<size_t>(p->n_adapters) * p->rank * p->k;
+    const size_t b_want = static_cast<size_t>(p->n_adapters) * p->rank * p->n;
+    if ((st = check_elems("x", x_elems, s.mk)) != Q2K_OK ||
+        (st = check_weights("w", w, w_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_elems("a", a_elems, a_want)) != Q2K_OK ||
+        (st = check_elems("b", b_elems, b_want)) != Q2K_OK ||
+        (st = check_elems("y", y_elems, s.mn)) != Q2K_OK)
+        return st;
+    if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, a, b and y must be 16-byte aligned");
+    if (!aligned(scales, 4) || !aligned(ids, 4) || !aligned(bad_id_count, 4))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "scales, ids and bad_id_count must be 4-byte aligned");
+    q2k::LoraArgs l = lora_args(path, p);
+    const size_t need = q2k::lora_workspace_bytes(l);
+    if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
+    const Span out[] = {{y, s.mn * s.elem, "y"}, {workspace, need, "workspace"},
+                        {bad_id_count, bad_id_count != nullptr ? size_t(4) : 0, "bad_id_count"}};
+    const Span in[] = {{x, s.mk * s.elem, "x"},
+                       {w, s.w_bytes, "w"},
+                       {a, a_want * 2, "a"},
+                       {b, b_want * 2, "b"},
+                       {scales, scales != nullptr ? size_t(p->n_adapters) * 4 : 0, "scales"},
+                       {ids, size_t(p->m) * 4, "ids"}};
+    if ((st = check_disjoint(out, 3, in, 6)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    unsigned int* word = nullptr;
+    int slot = -1;
+    if (bad_id_count == nullptr && (st = acquire_status_word(dev.device, cs, &word, &slot)) != Q2K_OK)
+        return st;
+    l.x = x;
+    l.w = static_cast<const uint8_t*>(w);
+    l.a = static_cast<const __nv_bfloat16*>(a);
+    l.b = static_cast<const __nv_bfloat16*>(b);
+    l.scales = scales;
+    l.ids = ids;
+    l.y = y;
+    l.bad_ids = bad_id_count != nullptr ? bad_id_count : word;
+    l.const_weights = (flags & Q2K_FLAG_CONST_WEIGHTS) != 0;
+    l.device = dev.device;
+    l.sm_count = dev.sm_count;
+    const cudaError_t e = q2k::launch_lora(l, need ? workspace : nullptr, cs);
+    if (word != nullptr)
+        return finish_status_word(dev.device, slot, word, cs, e, "q2k_matmul_lora", "n_adapters",
+                                  p->n_adapters);
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_matmul_lora launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,52 @@
+// Device helpers of the feed-forward operators: 32-bit arithmetic on f32 or
+// bf16 activations and the two activations with their slopes.
+#pragma once
+
+#include <cuda_bf16.h>
+
+namespace q2k {
+
+constexpr int kActSilu = 0;
+constexpr int kActGelu = 1;  // the tanh form
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// act(g) = g p and act'(g) = p + g (1 - p) p z'(g), with p = 1 / (1 + e^-z):
+//   silu  z = g                                     z' = 1
+//   gelu  z = 2 sqrt(2/pi) (g + 0.044715 g^3)       z' = 2 sqrt(2/pi) (1 + 3 * 0.044715 g^2)
+// ((1 + tanh y) / 2 = 1 / (1 + e^-2y), so the tanh form is a logistic too.)
+// For the tanh form g is held to |g| <= 30 inside z and z', where p is 0 or 1
+// to f32 already: no power of g overflows, and 0 * inf does not arise.
+__device__ __forceinline__ void act_logistic(float g, int act, float& p, float& dz) {
+    constexpr float kC = 1.5957691216057308f;  // 2 sqrt(2/pi)
+    float z = g;
+    dz = 1.0f;
+    if (act == kActGelu) {
+        const float c = fminf(fmaxf(g, -30.0f), 30.0f);
+        z = kC * (c + 0.044715f * c * c * c);
+        dz = kC * (1.0f + 3.0f * 0.044715f * c * c);
+    }
+    p = 1.0f / (1.0f + expf(-z));
+}
+__device__ __forceinline__ float act_value(float g, int act) {
+    float p, dz;
+    act_logistic(g, act, p, dz);
+    return g * p;
+}
+__device__ __forceinline__ void act_value_slope(float g, int act, float& value, float& slope) {
+    float p, dz;
+    act_logistic(g, act, p, dz);
+    value = g * p;
+    slope = p + g * (1.0f - p) * p * dz;
+}
+
+}  // namespace q2k

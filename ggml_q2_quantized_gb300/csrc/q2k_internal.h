@@ -1,6 +1,7 @@
 // Launchers shared between the libq2k translation units (not part of the ABI).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -160,5 +161,66 @@ cudaError_t launch_gemm_tc_plain(const float* x, const uint8_t* w, float* y, int
 
 // Read and clear the tensor-core kernels' device error word (synchronises `stream`).
 cudaError_t read_and_clear_tc_error(uint32_t* out, cudaStream_t stream);
+
+// ---- feed-forward operators (q2k_ffn.cu) -------------------------------------
+
+// Whether a call of m tokens takes the exact-weights kernel (q2k_ffn.cu) by
+// itself, rather than the tensor path.
+bool ffn_rows_path(int m, bool bf16);
+
+// h = act(x Wg^T) * (x Wu^T); gate and up (both or neither) get the projections.
+// Activations f32 or bf16 (one type for all).
+struct GatedArgs {
+    const void* x;
+    const uint8_t* wg;
+    const uint8_t* wu;
+    void* h;
+    void* gate;
+    void* up;
+    int M, N, K, act;
+    bool bf16;
+    bool tensor;         // the tensor path
+    bool const_weights;  // the kernel before does not write Wg or Wu
+    int device, sm_count;
+};
+size_t gated_workspace_bytes(const GatedArgs& a);
+cudaError_t launch_gated(const GatedArgs& a, void* workspace, cudaStream_t stream);
+
+// dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu; dgate and dup (both or
+// neither) get dg and du.
+struct GatedBackwardArgs {
+    const __nv_bfloat16* dh;
+    const __nv_bfloat16* gate;
+    const __nv_bfloat16* up;
+    const uint8_t* wg;
+    const uint8_t* wu;
+    __nv_bfloat16* dx;
+    __nv_bfloat16* dgate;
+    __nv_bfloat16* dup;
+    int M, N, K, act;
+    int device, sm_count;
+};
+size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a);
+cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream);
+
+// y_i = W x_i + s_a B_a (A_a x_i) with a = ids[i]; -1: no adapter, any other id
+// out of range: a zero row, counted in *bad_ids (written, not added to).
+struct LoraArgs {
+    const void* x;
+    const uint8_t* w;
+    const __nv_bfloat16* a;  // [n_adapters, R, K]
+    const __nv_bfloat16* b;  // [n_adapters, N, R]
+    const float* scales;     // [n_adapters] or null (all 1)
+    const int* ids;          // [M]
+    void* y;
+    unsigned int* bad_ids;
+    int M, N, K, R, n_adapters;
+    bool bf16;
+    bool tensor;
+    bool const_weights;
+    int device, sm_count;
+};
+size_t lora_workspace_bytes(const LoraArgs& a);
+cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream);
 
 }  // namespace q2k

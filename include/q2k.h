@@ -512,6 +512,106 @@ int q2k_abi_version(void);
 
 #define Q2K_ABI_VERSION 1
 
+/* ---- feed-forward operators ----------------------------------------------
+ * The two halves of a feed-forward layer with frozen Q2_K weights, for serving
+ * and for training what stands around them.  Activations are f32 or bf16
+ * (params.dtype, one type for all of a call's activations), row-major and
+ * 16-byte aligned; sums are f32 and results are rounded once.  Calls are
+ * asynchronous on `stream`, allocate nothing and may be captured; a workspace
+ * (device, 16-byte aligned, of at least the size the *_workspace_bytes call
+ * returns for the same arguments; NULL when that is 0) must not be used by
+ * another call until this one has finished.  Repeated calls on the same inputs
+ * give the same bits.
+ *
+ * Paths (Q2K_PATH_AUTO picks by m):
+ *   Q2K_PATH_GEMV    every weight exact; x exact when bf16, else to 22 bits
+ *                    relative to each element; products summed in f32, so the
+ *                    error is a few f32 roundings of sum_k |x| (dl q + ml).
+ *   Q2K_PATH_TENSOR  x and W rounded to bf16 (error within 8e-3 * sum_k |x w|,
+ *                    as q2k_matmul's tensor path). */
+typedef enum q2k_dtype { Q2K_DTYPE_F32 = 0, Q2K_DTYPE_BF16 = 1 } q2k_dtype;
+enum {
+    Q2K_FFN_MAX_TOKENS = 1 << 20, /* most tokens of a feed-forward call */
+    Q2K_FFN_MAX_WIDTH = 1 << 20,  /* largest n and k of one */
+    Q2K_LORA_MAX_RANK = 256,
+    Q2K_LORA_MAX_ADAPTERS = 65535
+};
+typedef enum q2k_act {
+    Q2K_ACT_SILU = 0, /* g / (1 + e^-g) */
+    Q2K_ACT_GELU = 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} q2k_act;
+
+typedef struct q2k_gated_ffn_params {
+    uint32_t m;         /* tokens, >= 1 */
+    uint32_t n;         /* rows of each weight matrix (the block's inner width), >= 1 */
+    uint32_t k;         /* columns of each (the hidden width), a positive multiple of 256 */
+    uint32_t ggml_type; /* must be Q2K_GGML_TYPE_Q2_K */
+    uint32_t dtype;     /* q2k_dtype */
+    uint32_t act;       /* q2k_act */
+} q2k_gated_ffn_params;
+
+/* q2k_gated_ffn - h = act(x Wg^T) * (x Wu^T), the gated feed-forward block's
+ * two projections, activation and product in one kernel.
+ *   flags        Q2K_FLAG_CONST_WEIGHTS or 0 (as q2k_matmul_ex)
+ *   x            [m, k]
+ *   w_gate,w_up  device, n * k/256 * 84 bytes each, 4-byte aligned
+ *   h            [m, n]; fully overwritten
+ *   gate, up     [m, n] each, both or neither NULL: the two projections, which
+ *                q2k_gated_ffn_backward reads
+ * No output may alias an input, the workspace or another output. */
+q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void *x, size_t x_elems,
+                         const void *w_gate, size_t w_gate_bytes, const void *w_up,
+                         size_t w_up_bytes, void *h, size_t h_elems, void *gate, void *up,
+                         const q2k_gated_ffn_params *params, void *workspace,
+                         size_t workspace_bytes, q2k_stream_t stream);
+size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params *params);
+
+/* q2k_gated_ffn_backward - the gated block's backward pass with its weights
+ * frozen: dgate = dh * up * act'(gate), dup = dh * act(gate) and
+ * dx = dgate Wg + dup Wu.  bf16 only (params.dtype); the product runs on the
+ * tensor cores with dgate, dup and W rounded to bf16.
+ *   dh, gate, up  [m, n] each (h_elems elements each)
+ *   dx            [m, k]; fully overwritten
+ *   dgate, dup    [m, n] each, both or neither NULL (e.g. for the gradients of
+ *                 adapters on the two projections) */
+q2k_status q2k_gated_ffn_backward(const void *dh, const void *gate, const void *up,
+                                  size_t h_elems, const void *w_gate, size_t w_gate_bytes,
+                                  const void *w_up, size_t w_up_bytes, void *dx, size_t dx_elems,
+                                  void *dgate, void *dup, const q2k_gated_ffn_params *params,
+                                  void *workspace, size_t workspace_bytes, q2k_stream_t stream);
+size_t q2k_gated_ffn_backward_workspace_bytes(const q2k_gated_ffn_params *params);
+
+typedef struct q2k_lora_params {
+    uint32_t m;          /* tokens, >= 1 */
+    uint32_t n;          /* weight rows = output columns, >= 1 */
+    uint32_t k;          /* reduction length, a positive multiple of 256 */
+    uint32_t ggml_type;  /* must be Q2K_GGML_TYPE_Q2_K */
+    uint32_t dtype;      /* q2k_dtype of x and y */
+    uint32_t rank;       /* rank of every adapter, a multiple of 8 in 8..Q2K_LORA_MAX_RANK */
+    uint32_t n_adapters; /* adapters in a and b, 1..Q2K_LORA_MAX_ADAPTERS */
+    uint32_t reserved;   /* must be 0 */
+} q2k_lora_params;
+
+/* q2k_matmul_lora - a shared projection with low-rank adapters of many requests
+ * at once: y_i = W x_i + s_a B_a (A_a x_i) with a = ids[i].
+ *   x        [m, k]
+ *   w        device, n * k/256 * 84 bytes, 4-byte aligned
+ *   a, b     device bf16, 16-byte aligned: A_a at a + a_index * rank * k, rows of
+ *            k; B_a at b + a_index * n * rank, rows of rank.  An adapter of a
+ *            lower rank is padded with zeros.
+ *   scales   device f32 [n_adapters], or NULL (all 1)
+ *   ids      device i32 [m]; -1: the token has no adapter
+ *   y        [m, n]; fully overwritten
+ *   bad_id_count  device u32 or NULL, as q2k_embedding_gather's: an id that is
+ *            neither -1 nor below n_adapters gives a zero row and is counted. */
+q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void *x, size_t x_elems,
+                           const void *w, size_t w_bytes, const void *a, size_t a_elems,
+                           const void *b, size_t b_elems, const float *scales,
+                           const int32_t *ids, void *y, size_t y_elems,
+                           const q2k_lora_params *params, uint32_t *bad_id_count,
+                           void *workspace, size_t workspace_bytes, q2k_stream_t stream);
+size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *params);
+
 #ifdef __cplusplus
 }
 #endif
