@@ -124,6 +124,7 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
                    const float* __restrict__ scales, const int* __restrict__ ids,
                    float* __restrict__ t, unsigned int* __restrict__ bad_ids, int M, int K, int R,
                    int n_adapters) {
+    pdl_allow_dependents();
     const int i = blockIdx.y;
     const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -186,6 +187,7 @@ bool ffn_rows_path(int m, bool bf16) { return m <= (bf16 ? 16 : 8); }
 size_t gated_workspace_bytes(const GatedArgs&) { return 0; }
 
 cudaError_t launch_gated(const GatedArgs& a, void*, cudaStream_t stream) {
+    if (!a.tensor) return launch_gated_rows(a, stream);
     const int blocks = (a.N + 7) / 8;
     if (a.bf16)
         gated_rows_kernel<<<blocks, 256, 0, stream>>>(
@@ -226,6 +228,7 @@ static cudaError_t launch_lora_as(const LoraArgs& a, void* workspace, cudaStream
         static_cast<const T*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (!a.tensor) return launch_lora_rows(a, t, stream);
     lora_rows_kernel<<<(a.N + 7) / 8, 256, 0, stream>>>(
         static_cast<const T*>(a.x), a.w, a.b, a.ids, t, static_cast<T*>(a.y), a.M, a.N, a.K, a.R,
         a.n_adapters);

@@ -223,4 +223,9 @@ struct LoraArgs {
 size_t lora_workspace_bytes(const LoraArgs& a);
 cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream);
 
+// The exact-weights kernels (q2k_ffn_rows.cu).  t: f32 [M, R], s_a A_a x_i,
+// written by the grid before (zeros for a token without an adapter).
+cudaError_t launch_gated_rows(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t stream);
+
 }  // namespace q2k
