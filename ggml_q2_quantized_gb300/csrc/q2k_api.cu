@@ -944,10 +944,11 @@ q2k_status q2k_device_error(uint32_t* out, q2k_stream_t stream) {
     DeviceInfo dev;
     q2k_status st = current_device(&dev);
     if (st != Q2K_OK) return st;
-    uint32_t tc = 0, gemv = 0;
+    uint32_t tc = 0, gemv = 0, ffn = 0;
     cudaError_t e = q2k::read_and_clear_tc_error(&tc, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = q2k::read_and_clear_gemv_error(&gemv, reinterpret_cast<cudaStream_t>(stream));
-    *out = tc | gemv;
+    if (e == cudaSuccess) e = q2k::read_and_clear_ffn_error(&ffn, reinterpret_cast<cudaStream_t>(stream));
+    *out = tc | gemv | ffn;
     return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_device_error");
 }
 

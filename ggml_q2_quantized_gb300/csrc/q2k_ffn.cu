@@ -18,7 +18,7 @@ namespace q2k {
 
 namespace {
 
-constexpr int kTok = 8;  // tokens per pass over a weight row
+constexpr int kTok = 8;  // tokens a thread of the backward product takes
 
 // Weight `i` (0..255) of the block at `blk`.
 __device__ __forceinline__ float block_weight(const uint8_t* blk, int i) {
@@ -29,49 +29,6 @@ __device__ __forceinline__ float block_weight(const uint8_t* blk, int i) {
     const float dl = f16_bits_to_float(dd) * static_cast<float>(sc & 15u);
     const float ml = f16_bits_to_float(dd >> 16) * static_cast<float>(sc >> 4);
     return fmaf(dl, static_cast<float>(q), -ml);
-}
-
-// One warp: the dot products of weight row `row` with tokens m0 .. m0 + count - 1.
-template <typename T>
-__device__ __forceinline__ void row_dots(const T* x, const uint8_t* row, int K, int m0, int count,
-                                         float (&acc)[kTok]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int t = 0; t < kTok; ++t) acc[t] = 0.f;
-    for (int b = 0; b < K / kQK; ++b)
-        for (int i = lane; i < kQK; i += 32) {
-            const float w = block_weight(row + static_cast<size_t>(b) * kBlockBytes, i);
-            for (int t = 0; t < count; ++t)
-                acc[t] = fmaf(w, to_float(x[static_cast<size_t>(m0 + t) * K + b * kQK + i]), acc[t]);
-        }
-    for (int t = 0; t < count; ++t)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-gated_rows_kernel(const T* __restrict__ x, const uint8_t* __restrict__ wg,
-                  const uint8_t* __restrict__ wu, T* __restrict__ h, T* __restrict__ gate,
-                  T* __restrict__ up, int M, int N, int K, int act) {
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (n >= N) return;
-    const size_t off = static_cast<size_t>(n) * (K / kQK) * kBlockBytes;
-    for (int m0 = 0; m0 < M; m0 += kTok) {
-        const int count = min(kTok, M - m0);
-        float g[kTok], u[kTok];
-        row_dots(x, wg + off, K, m0, count, g);
-        row_dots(x, wu + off, K, m0, count, u);
-        if ((threadIdx.x & 31) == 0)
-            for (int t = 0; t < count; ++t) {
-                const size_t o = static_cast<size_t>(m0 + t) * N + n;
-                h[o] = from_float<T>(act_value(g[t], act) * u[t]);
-                if (gate != nullptr) {
-                    gate[o] = from_float<T>(g[t]);
-                    up[o] = from_float<T>(u[t]);
-                }
-            }
-    }
 }
 
 // dg, du (f32, [m, n] each) and their copies for the caller.
@@ -116,65 +73,152 @@ gated_dx_kernel(const float* __restrict__ dg, const float* __restrict__ du,
         dx[static_cast<size_t>(m0 + t) * K + k] = from_float<__nv_bfloat16>(acc[t]);
 }
 
-// t[i, r] = s_a sum_k A_a[r, k] x[i, k], one warp per (token, r); tokens without
-// an adapter get zeros.  The first block also counts the ids out of range.
+// ---- t = s_a A_a x ---------------------------------------------------------------
+//
+// One cluster of eight CTAs takes eight consecutive tokens and one adapter that
+// occurs among them (64 rows of A_a at most): A_a's rows are the MMA's rows, the
+// tokens its columns, and the cluster's 64 warps divide K, so that even one
+// token's A_a (128 KB at rank 16, K = 4096) is read by eight SMs at once.  Sums
+// meet in shared memory, then over the cluster, in a fixed order.  A token
+// takes only its own adapter's column.  An f32 x is three bf16 parts (24 bits).
+constexpr int kShrinkWarps = 8;
+constexpr int kShrinkCtas = 8;
+constexpr int kShrinkRows = 64;
+// Up to this many tokens a cluster is launched per token, and the first token
+// with an adapter among its eight does the work: eight tokens with eight
+// adapters then run at once.  Above, a cluster loops over its tokens' adapters.
+constexpr int kShrinkPerToken = 64;
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The parts of eight consecutive x as B fragments of two K-steps.
 template <typename T>
-__global__ void __launch_bounds__(256)
+struct XParts;
+template <>
+struct XParts<__nv_bfloat16> {
+    static constexpr int kParts = 1;
+    uint32_t v[1][4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        v[0][0] = a.x, v[0][1] = a.y, v[0][2] = a.z, v[0][3] = a.w;
+    }
+    __device__ __forceinline__ void zero() { v[0][0] = v[0][1] = v[0][2] = v[0][3] = 0u; }
+};
+template <>
+struct XParts<float> {
+    static constexpr int kParts = 3;
+    uint32_t v[3][4];
+    __device__ __forceinline__ void load(const float* p) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+                v[q][e] = *reinterpret_cast<const uint32_t*>(&h);
+                f[2 * e] -= __uint_as_float(v[q][e] << 16);
+                f[2 * e + 1] -= __uint_as_float(v[q][e] & 0xFFFF0000u);
+            }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) v[q][0] = v[q][1] = v[q][2] = v[q][3] = 0u;
+    }
+};
+
+template <typename T>
+__global__ void __cluster_dims__(1, 1, kShrinkCtas) __launch_bounds__(kShrinkWarps * 32)
 lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
                    const float* __restrict__ scales, const int* __restrict__ ids,
                    float* __restrict__ t, unsigned int* __restrict__ bad_ids, int M, int K, int R,
-                   int n_adapters) {
+                   int n_adapters, bool per_token) {
+    __shared__ float red[kShrinkWarps][16][32];
+    __shared__ float part[16 * 32];
     pdl_allow_dependents();
-    const int i = blockIdx.y;
-    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (bad_ids != nullptr && blockIdx.x == 0 && i == 0 && threadIdx.x < 32) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.z;  // = the rank in the cluster
+    if (blockIdx.x == 0 && blockIdx.y == 0 && rank == 0 && warp == 0) {
         unsigned int bad = 0;
         for (int c = lane; c < M; c += 32) bad += ids[c] < -1 || ids[c] >= n_adapters;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) bad += __shfl_xor_sync(0xFFFFFFFFu, bad, o);
         if (lane == 0) *bad_ids = bad;
     }
-    if (r >= R) return;
-    const int id = ids[i];
-    float acc = 0.f;
-    if (id >= 0 && id < n_adapters) {
-        const __nv_bfloat16* row = a + (static_cast<size_t>(id) * R + r) * K;
-        for (int k = lane; k < K; k += 32)
-            acc = fmaf(to_float(row[k]), to_float(x[static_cast<size_t>(i) * K + k]), acc);
+    const int g = lane >> 2, q4 = lane & 3;
+    const int m0 = per_token ? static_cast<int>(blockIdx.x) & ~7 : 8 * static_cast<int>(blockIdx.x);
+    const int r0 = blockIdx.y * kShrinkRows;
+    const int tiles = min(kShrinkRows / 16, (R - r0 + 15) / 16);
+    const int m = m0 + g;  // this lane's column
+    int id = m < M ? ids[m] : -1;
+    if (id >= n_adapters) id = -1;
+    // lane 4 c holds token c's id: bit c of todo, the tokens with an adapter
+    unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0) & 0x11111111u;
+    while (todo != 0) {
+        const int first = __ffs(todo) - 1;
+        const int ad = __shfl_sync(0xFFFFFFFFu, id, first);
+        todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
+        if (per_token && m0 + (first >> 2) != static_cast<int>(blockIdx.x)) continue;
+        float acc[4][4] = {};
+        const __nv_bfloat16* arow = a + (static_cast<size_t>(ad) * R + r0 + g) * K + 8 * q4;
+        const T* xrow = x + static_cast<size_t>(min(m, M - 1)) * K + 8 * q4;
+        for (int k = 32 * (rank * kShrinkWarps + warp); k < K; k += 32 * kShrinkWarps * kShrinkCtas) {
+            XParts<T> xp;
+            if (id == ad) xp.load(xrow + k);
+            else xp.zero();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
-        if (scales != nullptr) acc *= scales[id];
-    }
-    if (lane == 0) t[static_cast<size_t>(i) * R + r] = acc;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-lora_rows_kernel(const T* __restrict__ x, const uint8_t* __restrict__ w,
-                 const __nv_bfloat16* __restrict__ b, const int* __restrict__ ids,
-                 const float* __restrict__ t, T* __restrict__ y, int M, int N, int K, int R,
-                 int n_adapters) {
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (n >= N) return;
-    const uint8_t* row = w + static_cast<size_t>(n) * (K / kQK) * kBlockBytes;
-    for (int m0 = 0; m0 < M; m0 += kTok) {
-        const int count = min(kTok, M - m0);
-        float acc[kTok];
-        row_dots(x, row, K, m0, count, acc);
-        if ((threadIdx.x & 31) == 0)
-            for (int c = 0; c < count; ++c) {
-                const int m = m0 + c, id = ids[m];
-                float v = acc[c];
-                if (id >= 0 && id < n_adapters) {
-                    const __nv_bfloat16* br = b + (static_cast<size_t>(id) * N + n) * R;
-                    for (int r = 0; r < R; ++r)
-                        v = fmaf(to_float(br[r]), t[static_cast<size_t>(m) * R + r], v);
-                } else if (id != -1) {
-                    v = 0.f;  // an id out of range: a zero row, counted by the first kernel
+            for (int rt = 0; rt < 4; ++rt) {
+                if (rt >= tiles) break;
+                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                if (r0 + 16 * rt + g < R)
+                    lo = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt) * K + k));
+                if (r0 + 16 * rt + 8 + g < R)
+                    hi = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt + 8) * K + k));
+#pragma unroll
+                for (int p = XParts<T>::kParts - 1; p >= 0; --p) {
+                    mma_bf16_16816(acc[rt], lo.x, hi.x, lo.y, hi.y, xp.v[p][0], xp.v[p][1]);
+                    mma_bf16_16816(acc[rt], lo.z, hi.z, lo.w, hi.w, xp.v[p][2], xp.v[p][3]);
                 }
-                y[static_cast<size_t>(m) * N + n] = from_float<T>(v);
             }
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) red[warp][4 * rt + c][lane] = acc[rt][c];
+        __syncthreads();
+        for (int i = tid; i < 16 * 32; i += kShrinkWarps * 32) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kShrinkWarps; ++w) v += red[w][i >> 5][i & 31];
+            part[i] = v;
+        }
+        cluster_sync();
+        // each CTA of the cluster adds an eighth of the values over the CTAs
+        constexpr int kEach = 16 * 32 / kShrinkCtas;
+        if (tid < kEach) {
+            const int i = rank * kEach + tid;
+            const uint32_t mine = smem_u32(part + i);
+            float v = 0.f;
+#pragma unroll
+            for (int c = 0; c < kShrinkCtas; ++c) {
+                uint32_t addr;
+                float u;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(mine), "r"(c));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(addr) : "memory");
+                v += u;
+            }
+            // value c of tile rt, lane l: row 16 rt + l / 4 + 8 (c / 2), column 2 (l % 4) + c % 2
+            const int f = i >> 5, l = i & 31;
+            const int r = r0 + 16 * (f >> 2) + (l >> 2) + 8 * ((f >> 1) & 1);
+            const int col = m0 + 2 * (l & 3) + (f & 1);
+            if (r < R && col < M && ids[col] == ad)
+                t[static_cast<size_t>(col) * R + r] = scales != nullptr ? v * scales[ad] : v;
+        }
+        cluster_sync();  // the values are read before any CTA leaves or goes on
     }
 }
 
@@ -184,21 +228,12 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 bool ffn_rows_path(int m, bool bf16) { return m <= (bf16 ? 16 : 8); }
 
-size_t gated_workspace_bytes(const GatedArgs&) { return 0; }
+size_t gated_workspace_bytes(const GatedArgs& a) {
+    return a.tensor ? gated_tc_workspace_bytes(a) : 0;
+}
 
-cudaError_t launch_gated(const GatedArgs& a, void*, cudaStream_t stream) {
-    if (!a.tensor) return launch_gated_rows(a, stream);
-    const int blocks = (a.N + 7) / 8;
-    if (a.bf16)
-        gated_rows_kernel<<<blocks, 256, 0, stream>>>(
-            static_cast<const __nv_bfloat16*>(a.x), a.wg, a.wu, static_cast<__nv_bfloat16*>(a.h),
-            static_cast<__nv_bfloat16*>(a.gate), static_cast<__nv_bfloat16*>(a.up), a.M, a.N, a.K,
-            a.act);
-    else
-        gated_rows_kernel<<<blocks, 256, 0, stream>>>(
-            static_cast<const float*>(a.x), a.wg, a.wu, static_cast<float*>(a.h),
-            static_cast<float*>(a.gate), static_cast<float*>(a.up), a.M, a.N, a.K, a.act);
-    return cudaGetLastError();
+cudaError_t launch_gated(const GatedArgs& a, void* workspace, cudaStream_t stream) {
+    return a.tensor ? launch_gated_tc(a, workspace, stream) : launch_gated_rows(a, stream);
 }
 
 size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
@@ -219,25 +254,29 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     return cudaGetLastError();
 }
 
-size_t lora_workspace_bytes(const LoraArgs& a) { return static_cast<size_t>(a.M) * a.R * 4; }
+// Workspace: t, then the tensor path's.
+static size_t lora_t_bytes(const LoraArgs& a) { return align256(static_cast<size_t>(a.M) * a.R * 4); }
 
-template <typename T>
-static cudaError_t launch_lora_as(const LoraArgs& a, void* workspace, cudaStream_t stream) {
-    float* t = static_cast<float*>(workspace);
-    lora_shrink_kernel<<<dim3((a.R + 7) / 8, a.M), 256, 0, stream>>>(
-        static_cast<const T*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (!a.tensor) return launch_lora_rows(a, t, stream);
-    lora_rows_kernel<<<(a.N + 7) / 8, 256, 0, stream>>>(
-        static_cast<const T*>(a.x), a.w, a.b, a.ids, t, static_cast<T*>(a.y), a.M, a.N, a.K, a.R,
-        a.n_adapters);
-    return cudaGetLastError();
+size_t lora_workspace_bytes(const LoraArgs& a) {
+    return lora_t_bytes(a) + (a.tensor ? lora_tc_workspace_bytes(a) : 0);
 }
 
 cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream) {
-    return a.bf16 ? launch_lora_as<__nv_bfloat16>(a, workspace, stream)
-                  : launch_lora_as<float>(a, workspace, stream);
+    float* t = static_cast<float*>(workspace);
+    const bool per_token = a.M <= kShrinkPerToken;
+    const dim3 grid(per_token ? a.M : (a.M + 7) / 8, (a.R + kShrinkRows - 1) / kShrinkRows, kShrinkCtas);
+    if (a.bf16)
+        lora_shrink_kernel<<<grid, kShrinkWarps * 32, 0, stream>>>(
+            static_cast<const __nv_bfloat16*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K,
+            a.R, a.n_adapters, per_token);
+    else
+        lora_shrink_kernel<<<grid, kShrinkWarps * 32, 0, stream>>>(
+            static_cast<const float*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R,
+            a.n_adapters, per_token);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (!a.tensor) return launch_lora_rows(a, t, stream);
+    return launch_lora_tc(a, t, static_cast<uint8_t*>(workspace) + lora_t_bytes(a), stream);
 }
 
 }  // namespace q2k

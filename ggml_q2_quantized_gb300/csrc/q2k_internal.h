@@ -228,4 +228,13 @@ cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream)
 cudaError_t launch_gated_rows(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t stream);
 
+// The tensor path (q2k_ffn_tc.cu).  t as above, written by the grid before,
+// which must let its dependents start only when x is complete.
+size_t gated_tc_workspace_bytes(const GatedArgs& a);
+cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream);
+size_t lora_tc_workspace_bytes(const LoraArgs& a);
+cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, cudaStream_t stream);
+// Read and clear those kernels' device error word (synchronises `stream`).
+cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream);
+
 }  // namespace q2k
