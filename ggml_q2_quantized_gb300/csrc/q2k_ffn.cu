@@ -18,61 +18,6 @@ namespace q2k {
 
 namespace {
 
-constexpr int kTok = 8;  // tokens a thread of the backward product takes
-
-// Weight `i` (0..255) of the block at `blk`.
-__device__ __forceinline__ float block_weight(const uint8_t* blk, int i) {
-    const int h = i >> 7, j = (i >> 5) & 3, seg = (i >> 4) & 1, l = i & 15;
-    const uint32_t sc = blk[8 * h + 2 * j + seg];
-    const uint32_t q = (blk[16 + 32 * h + 16 * seg + l] >> (2 * j)) & 3u;
-    const uint32_t dd = ld_u32(blk + 80);
-    const float dl = f16_bits_to_float(dd) * static_cast<float>(sc & 15u);
-    const float ml = f16_bits_to_float(dd >> 16) * static_cast<float>(sc >> 4);
-    return fmaf(dl, static_cast<float>(q), -ml);
-}
-
-// dg, du (f32, [m, n] each) and their copies for the caller.
-__global__ void __launch_bounds__(256)
-gated_grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ gate,
-                  const __nv_bfloat16* __restrict__ up, float* __restrict__ dg,
-                  float* __restrict__ du, __nv_bfloat16* __restrict__ dgate,
-                  __nv_bfloat16* __restrict__ dup, size_t count, int act) {
-    for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < count;
-         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-        float v, s;
-        act_value_slope(to_float(gate[i]), act, v, s);
-        const float d = to_float(dh[i]);
-        dg[i] = d * to_float(up[i]) * s;
-        du[i] = d * v;
-        if (dgate != nullptr) {
-            dgate[i] = from_float<__nv_bfloat16>(dg[i]);
-            dup[i] = from_float<__nv_bfloat16>(du[i]);
-        }
-    }
-}
-
-// dx[m0.., k] for one column k per thread: a sum over the rows of Wg and Wu.
-__global__ void __launch_bounds__(128)
-gated_dx_kernel(const float* __restrict__ dg, const float* __restrict__ du,
-                const uint8_t* __restrict__ wg, const uint8_t* __restrict__ wu,
-                __nv_bfloat16* __restrict__ dx, int M, int N, int K) {
-    const int k = blockIdx.x * blockDim.x + threadIdx.x;  // K is a multiple of 128
-    const int m0 = blockIdx.y * kTok;
-    const int count = min(kTok, M - m0);
-    const size_t row_bytes = static_cast<size_t>(K / kQK) * kBlockBytes;
-    float acc[kTok] = {};
-    for (int n = 0; n < N; ++n) {
-        const size_t off = n * row_bytes + static_cast<size_t>(k / kQK) * kBlockBytes;
-        const float a = block_weight(wg + off, k % kQK), b = block_weight(wu + off, k % kQK);
-        for (int t = 0; t < count; ++t) {
-            const size_t o = static_cast<size_t>(m0 + t) * N + n;
-            acc[t] = fmaf(dg[o], a, fmaf(du[o], b, acc[t]));
-        }
-    }
-    for (int t = 0; t < count; ++t)
-        dx[static_cast<size_t>(m0 + t) * K + k] = from_float<__nv_bfloat16>(acc[t]);
-}
-
 // ---- t = s_a A_a x ---------------------------------------------------------------
 //
 // One cluster of eight CTAs takes eight consecutive tokens and one adapter that
@@ -234,24 +179,6 @@ size_t gated_workspace_bytes(const GatedArgs& a) {
 
 cudaError_t launch_gated(const GatedArgs& a, void* workspace, cudaStream_t stream) {
     return a.tensor ? launch_gated_tc(a, workspace, stream) : launch_gated_rows(a, stream);
-}
-
-size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
-    return 2 * align256(static_cast<size_t>(a.M) * a.N * 4);
-}
-
-cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream) {
-    const size_t count = static_cast<size_t>(a.M) * a.N;
-    float* dg = static_cast<float*>(workspace);
-    float* du = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(count * 4));
-    const size_t blocks = std::min<size_t>((count + 255) / 256, static_cast<size_t>(a.sm_count) * 8);
-    gated_grad_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        a.dh, a.gate, a.up, dg, du, a.dgate, a.dup, count, a.act);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    gated_dx_kernel<<<dim3(a.K / 128, (a.M + kTok - 1) / kTok), 128, 0, stream>>>(
-        dg, du, a.wg, a.wu, a.dx, a.M, a.N, a.K);
-    return cudaGetLastError();
 }
 
 // Workspace: t, then the tensor path's.

@@ -1,20 +1,29 @@
 // Many tokens times Q2_K weights on the tensor cores (tcgen05): the gated
-// feed-forward block, and a projection with low-rank adapters.
+// feed-forward block, its backward product, and a projection with low-rank
+// adapters.
 //
-// A prepass writes x as bf16 in the swizzled tile image that the MMA reads.  A
-// CTA then computes 128 weight rows x up to 256 tokens over K: 16 warps decode
-// Q2_K blocks into tensor memory (the MMA's A operand: one weight row per
-// lane), x stages arrive by bulk copies (the B operand), and f32 sums build up
-// in tensor memory.  For the gated block the 128 rows are 64 rows of Wg and the
-// same 64 rows of Wu, so one tile holds both projections of its outputs and the
-// MMAs run as for a single matrix; g and u then meet in shared memory, where
-// the activation and the product are taken before anything is stored.
-// With few tiles, K is split over CTAs whose sums the last one to finish adds
-// in a fixed order.
+// A CTA computes 128 rows of a product x up to 256 tokens: 16 warps decode Q2_K
+// blocks into tensor memory (the MMA's A operand, one row of the product per
+// lane), token stages of 64 K arrive by TMA in the 128-byte-swizzled layout that
+// the MMA reads (the B operand; f32 tokens come from a bf16 image that a prepass
+// writes in that layout), and f32 sums build up in tensor memory.
 //
-// What bounds it: at 256 tokens a tile the MMAs (512 clocks per 64 weights of
-// K) and the decode (about as long) run side by side; below, the decode alone,
-// whatever the tokens.
+// Gated: the 128 rows are 64 rows of Wg and the same 64 rows of Wu, so one tile
+// holds both projections of its outputs and the MMAs run as for one matrix; g
+// and u then meet in shared memory, where the activation and the product are
+// taken before anything is stored.
+//
+// Backward: dx = [dg du] [Wg; Wu], a product over the weights' rows.  A tile's
+// 128 rows are half a block of columns (k), a stage is 64 weight rows: the
+// decoders transpose those rows' quant bytes four by four in shared memory, so
+// that a lane reads the codes of its column over 32 weight rows as eight words,
+// and pick each code's value from the row's table there.
+//
+// With few tiles, K is split over a cluster of CTAs whose sums meet through
+// distributed shared memory in a fixed order.
+//
+// What bounds it: at 256 tokens a tile the MMAs (512 clocks per 64 K) and the
+// decode (about as long) run side by side; below, the decode alone.
 //
 // Every wait is bounded (about a second); on time-out the kernel records a bit
 // in the device error word, drains its MMAs, frees TMEM and returns.
@@ -74,41 +83,62 @@ constexpr int kThreads = 32 * (kDecWarps + 5);
 constexpr int kMaxParts = 8;
 constexpr int kPlanSms = 152;  // K parts are planned for the whole GPU, whatever the device
 
+// Backward, per stage: the codes of 32 columns (lane l of the four shifts) over
+// 64 weight rows, 80 bytes a column (eight lanes' 16-byte reads fall on
+// different banks), and for each (shift, segment) 64 tables of four bf16, 16
+// bytes between one (shift, segment) and the next.
+constexpr int kCodePitch = kStageK + 16;
+constexpr int kCodeBytes = 32 * kCodePitch;
+constexpr int kTablePitch = 8 * kStageK + 16;
+constexpr int kTableBytes = 8 * kTablePitch;
+
+enum class Tc { kGated, kLora, kBackward };
+
 // Tiles of kX tokens.  256: one accumulator, one thread issues the MMAs.  128
 // and fewer: narrow MMAs issue at half the rate the tensor core takes them, so
-// two threads issue, each into its own accumulator; x and A rings are equally
-// deep, and one release serves a pair of stages of both.
-template <int kX, bool kTma>
+// two threads issue, each into its own accumulator; the token ring and the A
+// ring are equally deep then, and one release serves a pair of stages of both.
+template <int kX, bool kTma, Tc kMode>
 struct Cfg {
+    static constexpr bool kBack = kMode == Tc::kBackward;
     static constexpr int kIssuers = kX == 256 ? 1 : 2;
     static constexpr int kHand = kX == 256 ? 2 : 4;  // stages handed to the issuers at a time
     static constexpr bool kPairs = kIssuers == 2;    // stages released in pairs
     static constexpr int kXStage = kX * kStageK * 2;
-    static constexpr int kXStages = kX == 256 ? 6 : 8;
+    static constexpr int kXStages = kX < 256 ? 8 : !kBack ? 6 : kTma ? 5 : 4;
     static constexpr int kAStages = 8;
     static constexpr uint32_t kColA = kX * kIssuers;
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr int kRawBytes = kRows * (kTma ? kBoxBytes : kBlockBytes);
-    static constexpr int kRaw = kTma ? 2 : 3;        // raw blocks in flight
+    // raw slots: a block column of 128 weight rows, or (backward) of 64 for a stage
+    static constexpr int kRawRows = kBack ? kStageK : kRows;
+    static constexpr int kRawPitch = kTma || kBack ? kBoxBytes : kBlockBytes;
+    static constexpr int kRawBytes = kRawRows * kRawPitch;
+    static constexpr int kRaw = kBack ? (kTma ? 4 : 6) : (kTma ? 2 : 3);
     static constexpr int kOffRaw = kXStages * kXStage;
+    // backward: transposed codes and value tables, two of each per decoder group
+    static constexpr int kOffCodes = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kOffTables = kOffCodes + (kBack ? 4 * kCodeBytes : 0);
     // bars: x_full, x_empty [kXStages], a_full, a_empty [kAStages], raw_full,
     //       raw_empty [kRaw], accum, drain
     static constexpr int kNumBars = 2 * kXStages + 2 * kAStages + 2 * kRaw + 2;
-    static constexpr int kOffBar = (kOffRaw + kRaw * kRawBytes + 7) & ~7;
+    static constexpr int kOffBar = (kOffTables + (kBack ? 4 * kTableBytes : 0) + 7) & ~7;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
-    static_assert(kOffRaw >= kRows * kX * 4, "the sums of a tile reuse the x ring");
+    static_assert(kSmemBytes <= 232448, "shared memory");
+    static_assert(kOffRaw >= kRows * kX * 4, "the sums of a tile reuse the token ring");
     static_assert(kColA + 32 * kAStages <= kTmemCols, "tensor memory");
-    static_assert(kOffRaw % 1024 == 0, "TMA destination alignment");
+    static_assert(kOffRaw % 1024 == 0 && kOffCodes % 16 == 0 && kOffTables % 16 == 0, "alignment");
 };
 
 struct TcArgs {
-    const uint8_t* xa;  // x image
-    const uint8_t* w0;  // gated: Wg; else W
-    const uint8_t* w1;  // gated: Wu
-    int M, N, K;
-    float* partial;     // [tile][part][token][128], with more than one part
-    unsigned int* tile_count;
+    const uint8_t* xa;   // bf16 image of the tokens, or null: they come by the token maps
+    const uint8_t* w0;   // Wg, or W
+    const uint8_t* w1;   // Wu
+    int M, N, K;         // N, K: the weight matrices' rows and columns
+    int stages;          // 64-K stages of the whole product
+    int half_stages;     // backward: those of Wg
+    bool const_weights;  // the grid before does not write the weights
+    bool tokens_ready;   // nor the tokens
     // gated
     void* h;
     void* gate;
@@ -118,11 +148,14 @@ struct TcArgs {
     const __nv_bfloat16* b;
     const float* t;
     const int* ids;
-    void* y;
+    void* y;             // adapters: y; backward: dx
     int R, n_adapters;
 };
 
-enum class Tc { kGated, kLora };
+struct TcMaps {
+    CUtensorMap w0, w1;  // weights, 112-byte boxes of 64 or 128 rows
+    CUtensorMap x0, x1;  // tokens, boxes of kX rows x 64 (backward: dg and du)
+};
 
 // Stage Cp (0, 1) of one half of a block for one thread: the two K-steps of
 // quant segment `seg` at shifts J = 2 Cp + {0, 1}.  qh: the thread's four quant
@@ -174,12 +207,13 @@ __device__ __forceinline__ void dec_barrier() {
 // s_a B_a t of each token's adapter: per 16 rows and eight tokens, one product
 // (m16n8k16) for each adapter that occurs among them, B_a as stored and t split
 // into two bf16 (16 bits); a token's sum takes only its own adapter's product.
+// Tokens [first, tokens), first a multiple of 8.
 __device__ __forceinline__ void add_adapters(float* sums, const TcArgs& p, int n0, int m0,
-                                             int tokens, int warp, int lane) {
+                                             int first, int tokens, int warp, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int row = 16 * (warp & 7) + g;  // this lane's rows: row, row + 8
     const bool ok0 = n0 + row < p.N, ok1 = n0 + row + 8 < p.N;
-    for (int c0 = 8 * (warp >> 3); c0 < tokens; c0 += 16) {
+    for (int c0 = first + 8 * (warp >> 3); c0 < tokens; c0 += 16) {
         const int m = m0 + c0 + g;  // column g of the product
         int id = c0 + g < tokens ? p.ids[m] : -1;
         const bool bad = id < -1 || id >= p.n_adapters;
@@ -261,28 +295,134 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* dst, float a, float b,
     }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// Backward, non-TMA: the words of 64 weight rows that a stage needs (two of
+// scales, eight of codes, d and dmin) at their places in a raw slot, by the 256
+// threads of a decoder group.  Rows past N are zero (their tables are zero).
+__device__ __forceinline__ void issue_raw_rows(const TcArgs& p, uint32_t dst, int stage, int block,
+                                               int half, int tg) {
+    const bool up = stage >= p.half_stages;
+    const int n0 = kStageK * (up ? stage - p.half_stages : stage);
+    const uint8_t* w = up ? p.w1 : p.w0;
+    const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
+    for (int f = tg; f < kStageK * 11; f += 256) {
+        const int r = f / 11, i = f - 11 * r;
+        const int word = i < 2 ? 2 * half + i : i < 10 ? 4 + 8 * half + (i - 2) : 20;
+        const bool ok = n0 + r < p.N;
+        const uint8_t* src = w + (ok ? static_cast<size_t>(n0 + r) * row_bytes +
+                                           static_cast<size_t>(block) * kBlockBytes + 4 * word
+                                     : 0);
+        cp_async_4(dst + r * kBoxBytes + 4 * word, src, ok ? 4u : 0u);
+    }
+    cp_async_commit();
+}
+
+// Backward decode, first half of a stage (thread tg of the group's 256): value
+// tables of 64 weight rows at one shift (both segments), and the codes of the
+// half block's 32 byte columns, transposed.  raw: slot + offset of the block.
+__device__ __forceinline__ void transpose_stage(uint32_t raw, int half, uint32_t codes,
+                                                uint32_t tables, int tg) {
+    {
+        const int r = tg & 63, j = tg >> 6;
+        const uint32_t row = raw + r * kBoxBytes;
+        const uint32_t word = ld_shared_u32(row + 8 * half + 4 * (j >> 1)) >> (16 * (j & 1));
+        const uint32_t dd = ld_shared_u32(row + 80);
+        const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+#pragma unroll
+        for (int seg = 0; seg < 2; ++seg) {
+            uint32_t lo, hi;
+            weight_table((word >> (8 * seg)) & 0xFFu, d, dmin, lo, hi);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tables + (2 * j + seg) * kTablePitch +
+                                                                    8 * r),
+                         "r"(lo), "r"(hi)
+                         : "memory");
+        }
+    }
+    if (tg < 128) {
+        const int cw = tg & 7, rq = tg >> 3;  // byte columns 4 cw .., weight rows 4 rq ..
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w[q] = ld_shared_u32(raw + (4 * rq + q) * kBoxBytes + 16 + 32 * half + 4 * cw);
+        const uint32_t t0 = __byte_perm(w[0], w[1], 0x5140), t1 = __byte_perm(w[2], w[3], 0x5140);
+        const uint32_t t2 = __byte_perm(w[0], w[1], 0x7362), t3 = __byte_perm(w[2], w[3], 0x7362);
+        const uint32_t o[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632),
+                               __byte_perm(t2, t3, 0x5410), __byte_perm(t2, t3, 0x7632)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(codes + (4 * cw + q) * kCodePitch + 4 * rq),
+                         "r"(o[q])
+                         : "memory");
+    }
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Second half: 16 bf16 pairs of column `lane` of shift j over weight rows 32 nh
+// .. + 31.  A pair takes each row's value from that row's table by byte permute.
+__device__ __forceinline__ void decode_column(uint32_t codes, uint32_t tables, int j, int nh,
+                                              int lane, uint32_t (&o)[2][8]) {
+    const uint32_t cp = codes + lane * kCodePitch + 32 * nh;
+    const uint32_t tp = tables + (2 * j + (lane >> 4)) * kTablePitch + 8 * 32 * nh;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 c = ld_shared_v4(cp + 16 * h);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // byte i -> nibbles (2 q_i, 2 q_i + 1)
+            const uint32_t sel = ((cw[e] >> (2 * j)) & 0x03030303u) * 0x22u + 0x10101010u;
+            const uint4 a = ld_shared_v4(tp + 32 * (4 * h + e));
+            const uint4 b = ld_shared_v4(tp + 32 * (4 * h + e) + 16);
+            const uint32_t s2 = sel >> 16;
+            o[h][2 * e] = __byte_perm(__byte_perm(a.x, a.y, sel), __byte_perm(a.z, a.w, sel), 0x7610);
+            o[h][2 * e + 1] = __byte_perm(__byte_perm(b.x, b.y, s2), __byte_perm(b.z, b.w, s2), 0x7610);
+        }
+    }
+}
+
 template <int kX, bool kTma, Tc kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
-              const __grid_constant__ CUtensorMap map1) {
-    using C = Cfg<kX, kTma>;
+ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
+    using C = Cfg<kX, kTma, kMode>;
+    constexpr bool kBack = kMode == Tc::kBackward;
     constexpr int kSplit0 = kMode == Tc::kGated ? kRows / 2 : kRows;  // tile rows of w0
-    constexpr int kRawDepth = C::kRaw, kRawBytes = C::kRawBytes;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * kSplit0;
+    const int n0 = blockIdx.x * kSplit0;  // first row of the product (backward: column k)
+    const int rows = kBack ? p.K : p.N;   // rows of the product
     const int m0 = blockIdx.y * kX;
     const int tokens = min(kX, p.M - m0);
     const int nx = (tokens + 15) & ~15;  // MMA N
-    const int blocks = p.K / kQK;
-    const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
-    const int parts = gridDim.z;
-    const int kb0 = static_cast<int>(static_cast<long>(blockIdx.z) * blocks / parts);
-    const int n_blocks = static_cast<int>(static_cast<long>(blockIdx.z + 1) * blocks / parts) - kb0;
-    const int n_iters = 4 * n_blocks;
+    // K parts in whole blocks (backward: four stages, 256 weight rows)
+    const int parts = gridDim.z, quads = p.stages / 4;
+    const int q0 = static_cast<int>(static_cast<long>(blockIdx.z) * quads / parts);
+    const int n_quads = static_cast<int>(static_cast<long>(blockIdx.z + 1) * quads / parts) - q0;
+    const int n_iters = 4 * n_quads;
 
     const uint32_t bar_xfull = sbase + C::kOffBar;
     const uint32_t bar_xempty = bar_xfull + 8 * C::kXStages;
@@ -294,7 +434,6 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
     const uint32_t bar_drain = bar_accum + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    volatile int* last_part = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
     unsigned int* err = &g_ffn_error;
 
     if (warp == 0) {
@@ -308,7 +447,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
-            mbar_init(bar_rawempty + 8 * r, kDecWarps);
+            mbar_init(bar_rawempty + 8 * r, kBack ? kDecWarps / 2 : kDecWarps);
         }
         if (lane == 0) {
             mbar_init(bar_accum, C::kIssuers);
@@ -322,93 +461,148 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
     __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    float* sums = reinterpret_cast<float*>(smem);  // token c, row r at word 128 c + r
 
     if (warp < kDecWarps) {
         // ---------------- weight decoders ----------------
         const int td = threadIdx.x;
-        const int quarter = warp & 3, seg = (warp >> 2) & 1, half = warp >> 3;
+        const int quarter = warp & 3, sub = (warp >> 2) & 1, group = warp >> 3;
         const int row = 32 * quarter + lane;
         const uint32_t raw0 = sbase + C::kOffRaw;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-        const uint32_t a_col0 = t_lane + C::kColA + 8u * seg;
-        if constexpr (!kTma) {
-            for (int b = 0; b < kRawDepth - 1; ++b) {
-                if (b < n_blocks)
-                    issue_raw(p.w0, p.w1, kSplit0, raw0 + b * kRawBytes, n0, p.N, row_bytes, kb0 + b, td);
-                else
-                    cp_async_commit();
-            }
-        }
-        bool ok = true;
-        for (int b = 0; b < n_blocks && ok; ++b) {
-            const int buf = b % kRawDepth;
-            uint32_t mine;
+        if (!kTma && !p.const_weights) pdl_wait_prerequisites();
+        // Publish a stage decoded into two runs of eight columns.
+        auto publish = [&](int i, uint32_t col0, const uint32_t (&o0)[8], uint32_t col1,
+                           const uint32_t (&o1)[8]) -> bool {
+            const int s = i % C::kAStages;
+            const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
+            if (i >= C::kAStages &&
+                !__all_sync(0xFFFFFFFFu,
+                            mbar_wait_bounded(bar_aempty + 8 * rel, ((i / C::kAStages) - 1) & 1,
+                                              abort_flag, err, kErrTimeoutEmpty)))
+                return false;
+            fence_after();  // the MMAs that read this stage are done
+            tmem_store8(t_lane + C::kColA + 32u * s + col0, o0);
+            tmem_store8(t_lane + C::kColA + 32u * s + col1, o1);
+            tmem_store_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_afull + 8 * s);
+            return true;
+        };
+        if constexpr (kBack) {
+            const int tg = td & 255;
+            const int block = n0 / kQK, half = (n0 / kRows) & 1;
+            constexpr int kOwn = C::kRaw / 2;  // raw slots of a group
             if constexpr (!kTma) {
-                cp_async_wait<kRawDepth - 2>();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_raw + 8 * buf);
-            }
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_raw + 8 * buf, (b / kRawDepth) & 1,
-                                                           abort_flag, err, kErrTimeoutEmpty)))
-                break;
-            if constexpr (kTma) {
-                // the box starts at the 16-byte boundary at or below the block
-                mine = raw0 + buf * kRawBytes + row * kBoxBytes + 4 * ((kb0 + b) & 3);
-            } else {
-                // every decoder has read block b - 1: its slab takes block b + depth - 1
-                const int nb = b + kRawDepth - 1;
-                if (nb < n_blocks)
-                    issue_raw(p.w0, p.w1, kSplit0, raw0 + (nb % kRawDepth) * kRawBytes, n0, p.N,
-                              row_bytes, kb0 + nb, td);
-                else
-                    cp_async_commit();
-                mine = raw0 + buf * kRawBytes + row * kBlockBytes;
-            }
-            uint32_t sh[2], qh[4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) sh[q] = ld_shared_u32(mine + 8 * half + 4 * q) >> (8 * seg);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                qh[e] = ld_shared_u32(mine + 16 + 32 * half + 16 * seg + 4 * e);
-            const uint32_t dd = ld_shared_u32(mine + 80);
-            if constexpr (kTma) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_rawempty + 8 * buf);
-            }
-            const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
-#pragma unroll
-            for (int cp = 0; cp < 2; ++cp) {
-                const int i = 4 * b + 2 * half + cp;
-                const int s = i % C::kAStages;
-                uint32_t o0[8], o1[8];
-                if (cp == 0) decode_half_stage<0>(qh, sh, d, dmin, o0, o1);
-                else decode_half_stage<1>(qh, sh, d, dmin, o0, o1);
-                const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
-                if (i >= C::kAStages &&
-                    !__all_sync(0xFFFFFFFFu,
-                                mbar_wait_bounded(bar_aempty + 8 * rel, ((i / C::kAStages) - 1) & 1,
-                                                  abort_flag, err, kErrTimeoutEmpty))) {
-                    ok = false;
-                    break;
+                for (int i = 0; i < kOwn - 1; ++i) {
+                    if (2 * i + group < n_iters)
+                        issue_raw_rows(p, raw0 + (2 * i + group) * C::kRawBytes,
+                                       4 * q0 + 2 * i + group, block, half, tg);
+                    else
+                        cp_async_commit();
                 }
-                fence_after();  // the MMAs that read this stage are done
-                tmem_store8(a_col0 + 32u * s, o0);
-                tmem_store8(a_col0 + 32u * s + 16u, o1);
-                tmem_store_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_afull + 8 * s);
+            }
+            bool ok = true;  // a warp that gave up still passes the group's barriers
+            for (int i = group; i < n_iters; i += 2) {
+                const int slot = i % C::kRaw;
+                uint32_t raw = raw0 + slot * C::kRawBytes;
+                if constexpr (kTma) {
+                    ok = ok && __all_sync(0xFFFFFFFFu,
+                                          mbar_wait_bounded(bar_raw + 8 * slot, (i / C::kRaw) & 1,
+                                                            abort_flag, err, kErrTimeoutEmpty));
+                    raw += (kBlockBytes * block) & 15;  // the box starts at a 16-byte boundary
+                } else {
+                    cp_async_wait<kOwn - 2>();
+                    asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
+                    // the group is past the slot that the stage after next takes
+                    const int next = i + 2 * (kOwn - 1);
+                    if (next < n_iters)
+                        issue_raw_rows(p, raw0 + (next % C::kRaw) * C::kRawBytes, 4 * q0 + next,
+                                       block, half, tg);
+                    else
+                        cp_async_commit();
+                }
+                // two buffers: the one written now was last read two of the
+                // group's stages ago, before the barrier of the stage between
+                const int buf = 2 * group + ((i >> 1) & 1);
+                const uint32_t codes = sbase + C::kOffCodes + buf * kCodeBytes;
+                const uint32_t tables = sbase + C::kOffTables + buf * kTableBytes;
+                if (ok) transpose_stage(raw, half, codes, tables, tg);
+                if constexpr (kTma) {
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
+                }
+                asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
+                if (!ok) continue;
+                uint32_t o[2][8];
+                decode_column(codes, tables, quarter, sub, lane, o);
+                ok = publish(i, 16u * sub, o[0], 16u * sub + 8u, o[1]);
+            }
+        } else {
+            const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
+            if constexpr (!kTma) {
+                for (int b = 0; b < C::kRaw - 1; ++b) {
+                    if (b < n_quads)
+                        issue_raw(p.w0, p.w1, kSplit0, raw0 + b * C::kRawBytes, n0, p.N, row_bytes,
+                                  q0 + b, td);
+                    else
+                        cp_async_commit();
+                }
+            }
+            bool ok = true;
+            for (int b = 0; b < n_quads && ok; ++b) {
+                const int buf = b % C::kRaw;
+                uint32_t mine = raw0 + buf * C::kRawBytes + row * C::kRawPitch;
+                if constexpr (!kTma) {
+                    cp_async_wait<C::kRaw - 2>();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_raw + 8 * buf);
+                }
+                if (!__all_sync(0xFFFFFFFFu,
+                                mbar_wait_bounded(bar_raw + 8 * buf, (b / C::kRaw) & 1, abort_flag,
+                                                  err, kErrTimeoutEmpty)))
+                    break;
+                if constexpr (kTma) {
+                    mine += 4 * ((q0 + b) & 3);  // the box starts at a 16-byte boundary
+                } else {
+                    // every decoder has read block b - 1: its slot takes block b + kRaw - 1
+                    const int nb = b + C::kRaw - 1;
+                    if (nb < n_quads)
+                        issue_raw(p.w0, p.w1, kSplit0, raw0 + (nb % C::kRaw) * C::kRawBytes, n0, p.N,
+                                  row_bytes, q0 + nb, td);
+                    else
+                        cp_async_commit();
+                }
+                uint32_t sh[2], qh[4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) sh[q] = ld_shared_u32(mine + 8 * group + 4 * q) >> (8 * sub);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    qh[e] = ld_shared_u32(mine + 16 + 32 * group + 16 * sub + 4 * e);
+                const uint32_t dd = ld_shared_u32(mine + 80);
+                if constexpr (kTma) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_rawempty + 8 * buf);
+                }
+                const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+#pragma unroll
+                for (int cp = 0; cp < 2; ++cp) {
+                    uint32_t o0[8], o1[8];
+                    if (cp == 0) decode_half_stage<0>(qh, sh, d, dmin, o0, o1);
+                    else decode_half_stage<1>(qh, sh, d, dmin, o0, o1);
+                    if (!publish(4 * b + 2 * group + cp, 8u * sub, o0, 8u * sub + 16u, o1)) {
+                        ok = false;
+                        break;
+                    }
+                }
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
 
-        // ---------------- epilogue ----------------
-        const bool done = __all_sync(
-            0xFFFFFFFFu, mbar_wait_backoff(bar_accum, 0, abort_flag, err, kErrTimeoutAccum, 512));
-        float* sums = reinterpret_cast<float*>(smem);  // token c, row r at word 128 c + r
-        const size_t tile = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-        float* part0 = p.partial + tile * parts * (kX * kRows);
-        if (done) {
+        // ---------------- the tile's sums to shared memory ----------------
+        if (__all_sync(0xFFFFFFFFu, mbar_wait_backoff(bar_accum, 0, abort_flag, err,
+                                                      kErrTimeoutAccum, 512))) {
             fence_after();
 #pragma unroll 1
             for (int c0 = 16 * (warp >> 2); c0 < nx; c0 += 64) {
@@ -420,85 +614,9 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
 #pragma unroll
                     for (int q = 0; q < 16; ++q) v[q] += u[q];
                 }
-                float* dst = parts == 1 ? sums : part0 + blockIdx.z * (kX * kRows);
 #pragma unroll
                 for (int q = 0; q < 16; ++q)
-                    if (c0 + q < tokens) dst[(c0 + q) * kRows + row] = v[q];
-            }
-        }
-        // (a CTA that timed out still takes part in every barrier and count;
-        // past this barrier no wait is left that could raise the flag)
-        dec_barrier();
-        bool mine_to_store = *abort_flag == 0;
-        if (parts > 1) {
-            // The part that counts last adds the parts in order.  The barrier
-            // and the fence order every thread's stores before the count; the
-            // second fence orders the count before the loads.
-            if (td == 0) {
-                __threadfence();
-                pdl_wait_prerequisites();  // the prepass zeroed the counts
-                const unsigned prev = atomicAdd(&p.tile_count[tile], 1u);
-                __threadfence();
-                *last_part = prev == static_cast<unsigned>(parts) - 1u;
-            }
-            dec_barrier();
-            mine_to_store = *last_part != 0;
-            if (mine_to_store) {
-                const int quads = tokens * (kRows / 4);
-                for (int i = td; i < quads; i += kDecThreads) {
-                    float4 v[kMaxParts];
-#pragma unroll
-                    for (int z = 0; z < kMaxParts; ++z)
-                        if (z < parts)
-                            v[z] = __ldcg(reinterpret_cast<const float4*>(part0 + z * (kX * kRows)) + i);
-                    float4 s = v[0];
-#pragma unroll
-                    for (int z = 1; z < kMaxParts; ++z)
-                        if (z < parts) {
-                            s.x += v[z].x;
-                            s.y += v[z].y;
-                            s.z += v[z].z;
-                            s.w += v[z].w;
-                        }
-                    reinterpret_cast<float4*>(sums)[i] = s;
-                }
-            }
-            dec_barrier();
-        }
-        if (mine_to_store) {
-            const bool vec = (p.N & 1) == 0;  // (n0 is even: pairs are aligned)
-            if constexpr (kMode == Tc::kGated) {
-                // a warp takes a token at a time, a lane the rows 2 lane, 2 lane + 1
-                for (int c = warp; c < tokens; c += kDecWarps) {
-                    const float2 g = *reinterpret_cast<const float2*>(sums + c * kRows + 2 * lane);
-                    const float2 u =
-                        *reinterpret_cast<const float2*>(sums + c * kRows + kSplit0 + 2 * lane);
-                    const int n = n0 + 2 * lane;
-                    const int valid = p.N - n;
-                    if (valid <= 0) continue;
-                    const size_t at = static_cast<size_t>(m0 + c) * p.N + n;
-                    store_pair(static_cast<T*>(p.h) + at, act_value(g.x, p.act) * u.x,
-                               act_value(g.y, p.act) * u.y, valid, vec);
-                    if (p.gate != nullptr) {
-                        store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
-                        store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
-                    }
-                }
-            } else {
-                // (t is written before the image, whose grid waited for it)
-                pdl_wait_prerequisites();
-                add_adapters(sums, p, n0, m0, tokens, warp, lane);
-                dec_barrier();
-                for (int c = warp; c < tokens; c += kDecWarps)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int r = 64 * q + 2 * lane;
-                        const float2 v = *reinterpret_cast<const float2*>(sums + c * kRows + r);
-                        const int valid = p.N - (n0 + r);
-                        if (valid > 0)
-                            store_pair(static_cast<T*>(p.y) + static_cast<size_t>(m0 + c) * p.N + n0 + r,
-                                       v.x, v.y, valid, vec);
-                    }
+                    if (c0 + q < tokens) sums[(c0 + q) * kRows + row] = v[q];
             }
         }
     } else if (warp == kMmaWarp || (C::kIssuers == 2 && warp == kWaitWarp)) {
@@ -580,34 +698,50 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
     } else if (warp == kWWarp) {
         // ---------------- raw weight blocks ----------------
         if (kTma && lane == 0) {
-            tma_prefetch_map(&map0);
-            if (kSplit0 < kRows) tma_prefetch_map(&map1);
-            for (int b = 0; b < n_blocks; ++b) {
-                const int buf = b % kRawDepth;
-                if (b >= kRawDepth &&
-                    !mbar_wait_bounded(bar_rawempty + 8 * buf, ((b / kRawDepth) - 1) & 1, abort_flag,
+            tma_prefetch_map(&maps.w0);
+            if (kMode != Tc::kLora) tma_prefetch_map(&maps.w1);
+            if (!p.const_weights) pdl_wait_prerequisites();
+            const int n_raw = kBack ? n_iters : n_quads;
+            for (int b = 0; b < n_raw; ++b) {
+                const int buf = b % C::kRaw;
+                if (b >= C::kRaw &&
+                    !mbar_wait_bounded(bar_rawempty + 8 * buf, ((b / C::kRaw) - 1) & 1, abort_flag,
                                        err, kErrTimeoutEmpty))
                     break;
-                const uint32_t dst = sbase + C::kOffRaw + buf * kRawBytes;
-                const int x = (kBlockBytes * (kb0 + b)) & ~15;
-                mbar_arrive_expect_tx(bar_raw + 8 * buf, kRawBytes);
-                tma_load_2d(dst, &map0, x, n0, bar_raw + 8 * buf);
-                if (kSplit0 < kRows)
-                    tma_load_2d(dst + kSplit0 * kBoxBytes, &map1, x, n0, bar_raw + 8 * buf);
+                const uint32_t dst = sbase + C::kOffRaw + buf * C::kRawBytes;
+                const uint32_t bar = bar_raw + 8 * buf;
+                mbar_arrive_expect_tx(bar, C::kRawBytes);
+                if constexpr (kBack) {
+                    const int stage = 4 * q0 + b;
+                    const bool up = stage >= p.half_stages;
+                    tma_load_2d(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
+                                kStageK * (up ? stage - p.half_stages : stage), bar);
+                } else {
+                    const int x = (kBlockBytes * (q0 + b)) & ~15;
+                    tma_load_2d(dst, &maps.w0, x, n0, bar);
+                    if (kMode == Tc::kGated)
+                        tma_load_2d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, bar);
+                }
             }
             if (*abort_flag) linger();
         }
         __syncwarp();
     } else {
-        // ---------------- x stages, even and odd ----------------
+        // ---------------- token stages, even and odd ----------------
         if (lane == 0) {
             const uint8_t* src = p.xa +
-                                 (static_cast<size_t>(m0 / kSuperRows) * (p.K / kStageK) + 4 * kb0) *
+                                 (static_cast<size_t>(m0 / kSuperRows) * p.stages + 4 * q0) *
                                      kSuperBytes +
                                  static_cast<size_t>(m0 % kSuperRows) * (kStageK * 2);
-            const uint32_t bytes = static_cast<uint32_t>(nx) * (kStageK * 2);
-            pdl_wait_prerequisites();  // the image
-            pdl_allow_dependents();
+            const uint32_t bytes = p.xa != nullptr ? nx * (kStageK * 2) : C::kXStage;
+            if (p.xa == nullptr) {
+                tma_prefetch_map(&maps.x0);
+                if (kBack) tma_prefetch_map(&maps.x1);
+            }
+            if (!p.tokens_ready) {
+                pdl_wait_prerequisites();  // the tokens
+                pdl_allow_dependents();
+            }
             for (int i = warp - kXWarp0; i < n_iters; i += 2) {
                 const int s = i % C::kXStages;
                 if (i >= C::kXStages &&
@@ -615,15 +749,100 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
                                                  : bar_xempty + 8 * s,
                                        ((i / C::kXStages) - 1) & 1, abort_flag, err, kErrTimeoutEmpty))
                     break;
-                mbar_arrive_expect_tx(bar_xfull + 8 * s, bytes);
-                bulk_copy_g2s(sbase + s * C::kXStage, src + static_cast<size_t>(i) * kSuperBytes,
-                              bytes, bar_xfull + 8 * s);
+                const uint32_t dst = sbase + s * C::kXStage, bar = bar_xfull + 8 * s;
+                mbar_arrive_expect_tx(bar, bytes);
+                if (p.xa != nullptr) {
+                    bulk_copy_g2s(dst, src + static_cast<size_t>(i) * kSuperBytes, bytes, bar);
+                } else {
+                    // (tokens past M and, backward, weight rows past N read as zeros)
+                    const int stage = 4 * q0 + i;
+                    const bool up = kBack && stage >= p.half_stages;
+                    tma_load_2d(dst, up ? &maps.x1 : &maps.x0,
+                                kStageK * (up ? stage - p.half_stages : stage), m0, bar);
+                }
             }
             if (*abort_flag) linger();
         }
         __syncwarp();
     }
 
+    // ---------------- epilogue ----------------
+    // Every thread of every CTA of a cluster passes its barriers, whatever
+    // happened before.  Part r takes its share of the tile's tokens (whole
+    // groups of eight) and adds them over the parts in order; the second
+    // cluster barrier keeps every part's sums alive until all are read.
+    int first = 0, end = tokens;
+    if (parts > 1) {
+        const int groups = (tokens + 7) / 8, z = blockIdx.z;
+        first = 8 * (z * groups / parts);
+        end = min(tokens, 8 * ((z + 1) * groups / parts));
+        __syncwarp();
+        cluster_sync();
+    } else if (warp < kDecWarps) {
+        dec_barrier();
+    }
+    // past these barriers no wait is left that could raise the flag
+    const bool done = *abort_flag == 0;
+    if (warp < kDecWarps && parts > 1) {
+        for (int i = first * (kRows / 4) + threadIdx.x; i < end * (kRows / 4); i += kDecThreads) {
+            float4 v[kMaxParts];
+#pragma unroll
+            for (int z = 0; z < kMaxParts; ++z)
+                if (z < parts) v[z] = load_cluster4(sbase + 16 * i, z);
+            float4 a = v[0];
+#pragma unroll
+            for (int z = 1; z < kMaxParts; ++z)
+                if (z < parts) {
+                    a.x += v[z].x;
+                    a.y += v[z].y;
+                    a.z += v[z].z;
+                    a.w += v[z].w;
+                }
+            reinterpret_cast<float4*>(sums)[i] = a;
+        }
+        dec_barrier();
+    }
+    if (warp < kDecWarps && done) {
+        const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
+        if constexpr (kMode == Tc::kGated) {
+            // a warp takes a token at a time, a lane the rows 2 lane, 2 lane + 1
+            for (int c = first + warp; c < end; c += kDecWarps) {
+                const float2 g = *reinterpret_cast<const float2*>(sums + c * kRows + 2 * lane);
+                const float2 u =
+                    *reinterpret_cast<const float2*>(sums + c * kRows + kSplit0 + 2 * lane);
+                const int n = n0 + 2 * lane;
+                const int valid = rows - n;
+                if (valid <= 0) continue;
+                const size_t at = static_cast<size_t>(m0 + c) * rows + n;
+                store_pair(static_cast<T*>(p.h) + at, act_value(g.x, p.act) * u.x,
+                           act_value(g.y, p.act) * u.y, valid, vec);
+                if (p.gate != nullptr) {
+                    store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
+                    store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
+                }
+            }
+        } else {
+            if constexpr (kMode == Tc::kLora) {
+                pdl_wait_prerequisites();  // t (written by this grid or one before)
+                add_adapters(sums, p, n0, m0, first, end, warp, lane);
+                dec_barrier();
+            }
+            for (int c = first + warp; c < end; c += kDecWarps)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int r = 64 * q + 2 * lane;
+                    const float2 v = *reinterpret_cast<const float2*>(sums + c * kRows + r);
+                    const int valid = rows - (n0 + r);
+                    if (valid > 0)
+                        store_pair(static_cast<T*>(p.y) + static_cast<size_t>(m0 + c) * rows + n0 + r,
+                                   v.x, v.y, valid, vec);
+                }
+        }
+    }
+    if (parts > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
     fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -632,19 +851,15 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ CUtensorMap map0,
     }
 }
 
-// x [M, K] -> the bf16 tile image; rows past M up to a multiple of 16 are zeros
-// (they are MMA columns whose sums are dropped, but a NaN there would be read).
-// One thread writes one 16-byte chunk.  Also zeroes the tile counts.
-template <typename T>
+// x (f32 [M, K]) -> the bf16 tile image; rows past M up to a multiple of 16 are
+// zeros (their sums are dropped, but the MMA reads them).  One thread writes
+// 16-byte chunks, four per pass with their loads issued together.
 __global__ void __launch_bounds__(256)
-x_image_kernel(const T* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, size_t chunks,
-               unsigned int* __restrict__ tile_count, int tiles) {
+x_image_kernel(const float* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, size_t chunks) {
     pdl_allow_dependents();
     const int per_row = K / 8, stages = K / kStageK;
     const size_t stride = static_cast<size_t>(gridDim.x) * blockDim.x;
-    for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < tiles; t += stride)
-        tile_count[t] = 0u;
-    constexpr int kPer = 4;  // chunks per pass, their loads issued together
+    constexpr int kPer = 4;
     for (size_t base = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; base < chunks;
          base += kPer * stride) {
         uint4 v[kPer];
@@ -653,14 +868,10 @@ x_image_kernel(const T* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, 
             const size_t id = base + u * stride;
             v[u] = make_uint4(0u, 0u, 0u, 0u);
             if (id < static_cast<size_t>(M) * per_row) {
-                if constexpr (sizeof(T) == 2) {
-                    v[u] = __ldg(reinterpret_cast<const uint4*>(x) + id);
-                } else {
-                    const float4 a = __ldg(reinterpret_cast<const float4*>(x) + 2 * id);
-                    const float4 b = __ldg(reinterpret_cast<const float4*>(x) + 2 * id + 1);
-                    v[u] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y),
-                                      pack_bf16(b.z, b.w));
-                }
+                const float4 a = __ldg(reinterpret_cast<const float4*>(x) + 2 * id);
+                const float4 b = __ldg(reinterpret_cast<const float4*>(x) + 2 * id + 1);
+                v[u] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y),
+                                  pack_bf16(b.z, b.w));
             }
         }
 #pragma unroll
@@ -677,102 +888,142 @@ x_image_kernel(const T* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, 
     pdl_wait_prerequisites();
 }
 
-// ---- plan ----------------------------------------------------------------------
-
-// Tokens per tile: as few as hold them all up to 128; 256 (each decoded weight
-// then serves twice the MMA work) once tiles of 128 would take more than one
-// wave of CTAs.
-int tile_tokens(int M, int row_tiles) {
-    if (M <= 32) return 32;
-    if (M <= 64) return 64;
-    const long ctas = static_cast<long>(row_tiles) * ((M + 127) / 128);
-    return ctas > kPlanSms ? 256 : 128;
+// dg = dh u act'(g) and du = dh act(g), rounded to bf16 as the MMA's operands:
+// rows of `pitch` (the products' token matrices) and, where the caller's own
+// rows are not those, of N.  A thread takes eight consecutive n of a row.
+__global__ void __launch_bounds__(256)
+grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ gate,
+            const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
+            __nv_bfloat16* __restrict__ du, int pitch, __nv_bfloat16* __restrict__ dgate,
+            __nv_bfloat16* __restrict__ dup, int M, int N, int act) {
+    pdl_allow_dependents();
+    const int per_row = pitch / 8;
+    const bool vec = (N & 7) == 0;
+    const size_t chunks = static_cast<size_t>(M) * per_row;
+    for (size_t id = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; id < chunks;
+         id += static_cast<size_t>(gridDim.x) * blockDim.x) {
+        const int m = static_cast<int>(id / per_row);
+        const int n = 8 * static_cast<int>(id - static_cast<size_t>(m) * per_row);
+        const size_t at = static_cast<size_t>(m) * N + n;
+        __nv_bfloat16 h[8], g[8], u[8], a[8], b[8];
+        if (vec) {
+            *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(dh + at));
+            *reinterpret_cast<uint4*>(g) = __ldg(reinterpret_cast<const uint4*>(gate + at));
+            *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(up + at));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool ok = n + e < N;
+                h[e] = ok ? dh[at + e] : __float2bfloat16_rn(0.f);
+                g[e] = ok ? gate[at + e] : __float2bfloat16_rn(0.f);
+                u[e] = ok ? up[at + e] : __float2bfloat16_rn(0.f);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float value, slope;
+            act_value_slope(to_float(g[e]), act, value, slope);
+            a[e] = __float2bfloat16_rn(to_float(h[e]) * to_float(u[e]) * slope);
+            b[e] = __float2bfloat16_rn(to_float(h[e]) * value);
+        }
+        const size_t to = static_cast<size_t>(m) * pitch + n;
+        *reinterpret_cast<uint4*>(dg + to) = *reinterpret_cast<const uint4*>(a);
+        *reinterpret_cast<uint4*>(du + to) = *reinterpret_cast<const uint4*>(b);
+        if (dgate != nullptr) {
+            for (int e = 0; e < 8 && n + e < N; ++e) {
+                dgate[at + e] = a[e];
+                dup[at + e] = b[e];
+            }
+        }
+    }
 }
+
+// ---- plan ----------------------------------------------------------------------
 
 struct Plan {
     int x_rows, row_tiles, token_tiles, parts;
-    size_t image, partial, counts;  // bytes
 };
 
-Plan make_plan(int M, int N, int K, bool gated) {
+// rows: those of the product's row tiles; quads: its K in parts of four stages.
+// Tokens per tile: as few as hold them all up to 128; 256 (each decoded weight
+// then serves twice the MMA work) once tiles of 128 would take more than one
+// wave of CTAs.  K parts while the tiles leave half of the GPU or more idle.
+Plan make_plan(int M, int rows, int tile_rows, int quads) {
     Plan p;
-    const int rows = gated ? kRows / 2 : kRows;
-    p.row_tiles = (N + rows - 1) / rows;
-    p.x_rows = tile_tokens(M, p.row_tiles);
+    p.row_tiles = (rows + tile_rows - 1) / tile_rows;
+    const long ctas = static_cast<long>(p.row_tiles) * ((M + 127) / 128);
+    p.x_rows = M <= 32 ? 32 : M <= 64 ? 64 : ctas > kPlanSms ? 256 : 128;
     p.token_tiles = (M + p.x_rows - 1) / p.x_rows;
     const long tiles = static_cast<long>(p.row_tiles) * p.token_tiles;
-    // K parts while the tiles leave half of the GPU or more idle
-    p.parts = static_cast<int>(std::max(1L, std::min<long>(std::min(kMaxParts, K / kQK), kPlanSms / tiles)));
-    const size_t m_pad = static_cast<size_t>((M + kSuperRows - 1) / kSuperRows) * kSuperRows;
-    p.image = m_pad * K * 2;
-    p.partial = p.parts > 1 ? static_cast<size_t>(tiles) * p.parts * p.x_rows * kRows * 4 : 0;
-    p.counts = p.parts > 1 ? ((static_cast<size_t>(tiles) * 4 + 255) & ~size_t(255)) : 0;
+    p.parts = static_cast<int>(std::max(1L, std::min<long>(std::min(kMaxParts, quads), kPlanSms / tiles)));
     return p;
 }
 
-size_t plan_bytes(const Plan& p) { return p.image + p.partial + p.counts; }
+// A bf16 [rows, cols] matrix with rows `pitch` apart, in boxes of box_rows x 64
+// columns, 128-byte swizzled.
+bool make_token_map(CUtensorMap* map, const void* x, int rows, int cols, int pitch, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kStageK), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t elem[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box,
+                  elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int kX, bool kTma, Tc kMode, typename T>
-cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const CUtensorMap& m0,
-                         const CUtensorMap& m1, int device, cudaStream_t stream) {
-    using C = Cfg<kX, kTma>;
-    constexpr int kSmem = C::kSmemBytes;
-    static_assert(kSmem <= 232448, "shared memory");
+cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, int device,
+                         cudaStream_t stream) {
+    using C = Cfg<kX, kTma, kMode>;
     static bool attr_done[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!attr_done[device]) {
         const cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<kX, kTma, kMode, T>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   C::kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_done[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.row_tiles, plan.token_tiles, plan.parts);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kX, kTma, kMode, T>, a, m0, m1);
+    if (plan.parts > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = static_cast<unsigned>(plan.parts);
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kX, kTma, kMode, T>, a, maps);
 }
 
+// T: the type of the results.  x0, x1: bf16 token matrices [M, x_cols] with rows
+// `x_pitch` apart (x1: backward, du), or null with a.xa an image.
 template <Tc kMode, typename T>
-cudaError_t launch_tc(TcArgs a, const T* x, void* workspace, int device, int sm_count,
-                      bool behind_grid, cudaStream_t stream) {
-    const Plan plan = make_plan(a.M, a.N, a.K, kMode == Tc::kGated);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.xa = ws;
-    a.partial = reinterpret_cast<float*>(ws + plan.image);
-    a.tile_count = reinterpret_cast<unsigned int*>(ws + plan.image + plan.partial);
-    const size_t chunks = static_cast<size_t>((a.M + 15) & ~15) * (a.K / 8);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, sm_count * 4)));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    // behind one of this call's own grids (which does not write x) the prepass
-    // may start early; otherwise it starts when all before it is complete
-    cfg.numAttrs = behind_grid ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, x_image_kernel<T>, x, ws, a.M, a.K, chunks,
-                                       a.tile_count,
-                                       plan.parts > 1 ? plan.row_tiles * plan.token_tiles : 0);
-    if (e != cudaSuccess) return e;
-    alignas(64) CUtensorMap m0, m1;
-    memset(&m0, 0, sizeof m0);
-    memset(&m1, 0, sizeof m1);
-    const int rows = kMode == Tc::kGated ? kRows / 2 : kRows;
-    const bool tma = make_weight_map(&m0, a.w0, a.N, a.K, rows) &&
-                     (kMode != Tc::kGated || make_weight_map(&m1, a.w1, a.N, a.K, rows));
-#define Q2K_TC_CASE(X)                                                                          \
-    case X:                                                                                     \
-        return tma ? launch_tc_as<X, true, kMode, T>(a, plan, m0, m1, device, stream)           \
-                   : launch_tc_as<X, false, kMode, T>(a, plan, m0, m1, device, stream);
+cudaError_t launch_tc(const TcArgs& a, const Plan& plan, const void* x0, const void* x1, int x_cols,
+                      int x_pitch, int device, cudaStream_t stream) {
+    alignas(64) TcMaps maps;
+    memset(&maps, 0, sizeof maps);
+    const int rows = kMode == Tc::kLora ? kRows : 64;
+    const bool tma = make_weight_map(&maps.w0, a.w0, a.N, a.K, rows) &&
+                     (kMode == Tc::kLora || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows));
+    if (a.xa == nullptr &&
+        (!make_token_map(&maps.x0, x0, a.M, x_cols, x_pitch, plan.x_rows) ||
+         (kMode == Tc::kBackward && !make_token_map(&maps.x1, x1, a.M, x_cols, x_pitch, plan.x_rows))))
+        return cudaErrorNotSupported;
+#define Q2K_TC_CASE(X)                                                              \
+    case X:                                                                         \
+        return tma ? launch_tc_as<X, true, kMode, T>(a, plan, maps, device, stream) \
+                   : launch_tc_as<X, false, kMode, T>(a, plan, maps, device, stream);
     switch (plan.x_rows) {
         Q2K_TC_CASE(32)
         Q2K_TC_CASE(64)
@@ -783,11 +1034,48 @@ cudaError_t launch_tc(TcArgs a, const T* x, void* workspace, int device, int sm_
     return cudaErrorInvalidValue;
 }
 
+size_t image_bytes(int M, int K) {
+    return static_cast<size_t>((M + kSuperRows - 1) / kSuperRows) * kSuperRows * K * 2;
+}
+
+// x W^T: bf16 tokens go to the kernel by their own tensor map, f32 tokens by an
+// image.  behind_grid: one of this call's own grids (which does not write x) is
+// before, and lets its dependents start only when x is complete.
+template <Tc kMode>
+cudaError_t launch_forward(TcArgs a, bool bf16, const void* x, void* workspace, int device,
+                           int sm_count, bool behind_grid, cudaStream_t stream) {
+    const Plan plan = make_plan(a.M, a.N, kMode == Tc::kGated ? 64 : kRows, a.K / kQK);
+    a.stages = a.K / kStageK;
+    a.tokens_ready = bf16 && behind_grid;
+    if (bf16)
+        return launch_tc<kMode, __nv_bfloat16>(a, plan, x, nullptr, a.K, a.K, device, stream);
+    a.xa = static_cast<const uint8_t*>(workspace);
+    // the image's grid started when all before it was complete: the weights are
+    a.const_weights = true;
+    const size_t chunks = static_cast<size_t>((a.M + 15) & ~15) * (a.K / 8);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, sm_count * 4)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind_grid ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, x_image_kernel, static_cast<const float*>(x),
+                                             static_cast<uint8_t*>(workspace), a.M, a.K, chunks);
+    if (e != cudaSuccess) return e;
+    return launch_tc<kMode, float>(a, plan, nullptr, nullptr, 0, 0, device, stream);
+}
+
+// Columns of dg and du as the product's K: whole parts of two stages each.
+int backward_cols(int N) { return (N + 2 * kStageK - 1) / (2 * kStageK) * (2 * kStageK); }
+// Their rows' pitch: the caller's own when those are whole 16 bytes.
+int backward_pitch(int N) { return (N + 7) & ~7; }
+
 }  // namespace
 
-size_t gated_tc_workspace_bytes(const GatedArgs& a) {
-    return plan_bytes(make_plan(a.M, a.N, a.K, true));
-}
+size_t gated_tc_workspace_bytes(const GatedArgs& a) { return a.bf16 ? 0 : image_bytes(a.M, a.K); }
 
 cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream) {
     TcArgs t = {};
@@ -796,20 +1084,15 @@ cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t st
     t.M = a.M;
     t.N = a.N;
     t.K = a.K;
+    t.const_weights = a.const_weights;
     t.h = a.h;
     t.gate = a.gate;
     t.up = a.up;
     t.act = a.act;
-    if (a.bf16)
-        return launch_tc<Tc::kGated>(t, static_cast<const __nv_bfloat16*>(a.x), workspace, a.device,
-                                     a.sm_count, false, stream);
-    return launch_tc<Tc::kGated>(t, static_cast<const float*>(a.x), workspace, a.device, a.sm_count,
-                                 false, stream);
+    return launch_forward<Tc::kGated>(t, a.bf16, a.x, workspace, a.device, a.sm_count, false, stream);
 }
 
-size_t lora_tc_workspace_bytes(const LoraArgs& a) {
-    return plan_bytes(make_plan(a.M, a.N, a.K, false));
-}
+size_t lora_tc_workspace_bytes(const LoraArgs& a) { return a.bf16 ? 0 : image_bytes(a.M, a.K); }
 
 cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, cudaStream_t stream) {
     TcArgs c = {};
@@ -817,17 +1100,48 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, c
     c.M = a.M;
     c.N = a.N;
     c.K = a.K;
+    c.const_weights = true;  // the grid before started when all before it was complete
     c.b = a.b;
     c.t = t;
     c.ids = a.ids;
     c.y = a.y;
     c.R = a.R;
     c.n_adapters = a.n_adapters;
-    if (a.bf16)
-        return launch_tc<Tc::kLora>(c, static_cast<const __nv_bfloat16*>(a.x), workspace, a.device,
-                                    a.sm_count, true, stream);
-    return launch_tc<Tc::kLora>(c, static_cast<const float*>(a.x), workspace, a.device, a.sm_count,
-                                true, stream);
+    return launch_forward<Tc::kLora>(c, a.bf16, a.x, workspace, a.device, a.sm_count, true, stream);
+}
+
+// Workspace: dg and du, unless the caller takes them in rows of whole 16 bytes.
+size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
+    return 2 * ((static_cast<size_t>(a.M) * backward_pitch(a.N) * 2 + 255) & ~size_t(255));
+}
+
+cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream) {
+    const int pitch = backward_pitch(a.N), cols = backward_cols(a.N);
+    const bool own = a.dgate != nullptr && pitch == a.N;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(ws);
+    __nv_bfloat16* du = own ? a.dup
+                            : reinterpret_cast<__nv_bfloat16*>(ws + gated_backward_workspace_bytes(a) / 2);
+    const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
+    const unsigned blocks =
+        static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));
+    grad_kernel<<<blocks, 256, 0, stream>>>(a.dh, a.gate, a.up, dg, du, pitch,
+                                            own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
+                                            a.act);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    TcArgs t = {};
+    t.w0 = a.wg;
+    t.w1 = a.wu;
+    t.M = a.M;
+    t.N = a.N;
+    t.K = a.K;
+    t.const_weights = true;  // the grid before started when all before it was complete
+    t.half_stages = cols / kStageK;
+    t.stages = 2 * t.half_stages;
+    t.y = a.dx;
+    const Plan plan = make_plan(a.M, a.K, kRows, t.stages / 4);
+    return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, dg, du, a.N, pitch, a.device, stream);
 }
 
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream) {
