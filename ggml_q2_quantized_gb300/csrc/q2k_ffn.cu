@@ -20,18 +20,20 @@ namespace {
 
 // ---- t = s_a A_a x ---------------------------------------------------------------
 //
-// One cluster of eight CTAs takes eight consecutive tokens and one adapter that
-// occurs among them (64 rows of A_a at most): A_a's rows are the MMA's rows, the
-// tokens its columns, and the cluster's 64 warps divide K, so that even one
-// token's A_a (128 KB at rank 16, K = 4096) is read by eight SMs at once.  Sums
-// meet in shared memory, then over the cluster, in a fixed order.  A token
-// takes only its own adapter's column.  An f32 x is three bf16 parts (24 bits).
+// One cluster of eight CTAs takes one adapter's rows (64 at most) and the
+// tokens with that adapter among eight or 32 consecutive ones: A_a's rows are
+// the MMA's rows, eight tokens its columns, and the cluster's 64 warps divide K,
+// so that even one token's A_a (128 KB at rank 16, K = 4096) is read by eight
+// SMs at once.  Sums meet in shared memory, then over the cluster, in a fixed
+// order.  A token takes only its own adapter's column.  An f32 x is three bf16
+// parts (24 bits).
 constexpr int kShrinkWarps = 8;
 constexpr int kShrinkCtas = 8;
 constexpr int kShrinkRows = 64;
 // Up to this many tokens a cluster is launched per token, and the first token
 // with an adapter among its eight does the work: eight tokens with eight
-// adapters then run at once.  Above, a cluster loops over its tokens' adapters.
+// adapters then run at once.  Above, a cluster takes 32 tokens and loops over
+// their adapters, which reads A_a a quarter as often (prompts of one adapter).
 constexpr int kShrinkPerToken = 64;
 
 __device__ __forceinline__ void cluster_sync() {
@@ -76,14 +78,15 @@ struct XParts<float> {
     }
 };
 
-template <typename T>
+// kGroups: groups of eight tokens per cluster (1: launched per token).
+template <typename T, int kGroups>
 __global__ void __cluster_dims__(1, 1, kShrinkCtas) __launch_bounds__(kShrinkWarps * 32)
 lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
                    const float* __restrict__ scales, const int* __restrict__ ids,
                    float* __restrict__ t, unsigned int* __restrict__ bad_ids, int M, int K, int R,
-                   int n_adapters, bool per_token) {
+                   int n_adapters) {
     __shared__ float red[kShrinkWarps][16][32];
-    __shared__ float part[16 * 32];
+    __shared__ float part[kGroups * 16 * 32];
     pdl_allow_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.z;  // = the rank in the cluster
@@ -95,76 +98,117 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
         if (lane == 0) *bad_ids = bad;
     }
     const int g = lane >> 2, q4 = lane & 3;
-    const int m0 = per_token ? static_cast<int>(blockIdx.x) & ~7 : 8 * static_cast<int>(blockIdx.x);
+    const int block = static_cast<int>(blockIdx.x);
+    const int m0 = kGroups == 1 ? block & ~7 : 8 * kGroups * block;
     const int r0 = blockIdx.y * kShrinkRows;
     const int tiles = min(kShrinkRows / 16, (R - r0 + 15) / 16);
-    const int m = m0 + g;  // this lane's column
-    int id = m < M ? ids[m] : -1;
-    if (id >= n_adapters) id = -1;
-    // lane 4 c holds token c's id: bit c of todo, the tokens with an adapter
-    unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0) & 0x11111111u;
-    while (todo != 0) {
-        const int first = __ffs(todo) - 1;
-        const int ad = __shfl_sync(0xFFFFFFFFu, id, first);
-        todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
-        if (per_token && m0 + (first >> 2) != static_cast<int>(blockIdx.x)) continue;
-        float acc[4][4] = {};
+    int id[kGroups];  // of this lane's column in each group; -1 once done
+#pragma unroll
+    for (int n = 0; n < kGroups; ++n) {
+        const int m = m0 + 8 * n + g;
+        id[n] = m < M ? ids[m] : -1;
+        if (id[n] >= n_adapters || id[n] < 0) id[n] = -1;
+    }
+    while (true) {
+        // the first adapter left, and its first token
+        int ad = -1, token = 0;
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+            const unsigned has = __ballot_sync(0xFFFFFFFFu, id[n] >= 0);
+            if (has != 0 && ad < 0) {
+                const int l = __ffs(has) - 1;  // (lane 4 c holds token c's id)
+                ad = __shfl_sync(0xFFFFFFFFu, id[n], l);
+                token = m0 + 8 * n + (l >> 2);
+            }
+        }
+        if (ad < 0) break;
+        bool mine[kGroups];
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+            mine[n] = id[n] == ad;
+            if (mine[n]) id[n] = -1;
+        }
+        if (kGroups == 1 && token != block) continue;
+        float acc[4][kGroups][4] = {};
         const __nv_bfloat16* arow = a + (static_cast<size_t>(ad) * R + r0 + g) * K + 8 * q4;
-        const T* xrow = x + static_cast<size_t>(min(m, M - 1)) * K + 8 * q4;
         for (int k = 32 * (rank * kShrinkWarps + warp); k < K; k += 32 * kShrinkWarps * kShrinkCtas) {
-            XParts<T> xp;
-            if (id == ad) xp.load(xrow + k);
-            else xp.zero();
+            uint4 lo[4], hi[4];
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                if (rt >= tiles) break;
-                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                lo[rt] = hi[rt] = make_uint4(0u, 0u, 0u, 0u);
                 if (r0 + 16 * rt + g < R)
-                    lo = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt) * K + k));
+                    lo[rt] = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt) * K + k));
                 if (r0 + 16 * rt + 8 + g < R)
-                    hi = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt + 8) * K + k));
+                    hi[rt] = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt + 8) * K + k));
+            }
 #pragma unroll
-                for (int p = XParts<T>::kParts - 1; p >= 0; --p) {
-                    mma_bf16_16816(acc[rt], lo.x, hi.x, lo.y, hi.y, xp.v[p][0], xp.v[p][1]);
-                    mma_bf16_16816(acc[rt], lo.z, hi.z, lo.w, hi.w, xp.v[p][2], xp.v[p][3]);
+            for (int n = 0; n < kGroups; ++n) {
+                XParts<T> xp;
+                if (mine[n]) xp.load(x + static_cast<size_t>(m0 + 8 * n + g) * K + 8 * q4 + k);
+                else xp.zero();
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    if (rt >= tiles) break;
+#pragma unroll
+                    for (int p = XParts<T>::kParts - 1; p >= 0; --p) {
+                        mma_bf16_16816(acc[rt][n], lo[rt].x, hi[rt].x, lo[rt].y, hi[rt].y, xp.v[p][0], xp.v[p][1]);
+                        mma_bf16_16816(acc[rt][n], lo[rt].z, hi[rt].z, lo[rt].w, hi[rt].w, xp.v[p][2], xp.v[p][3]);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+        for (int n = 0; n < kGroups; ++n) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) red[warp][4 * rt + c][lane] = acc[rt][c];
-        __syncthreads();
-        for (int i = tid; i < 16 * 32; i += kShrinkWarps * 32) {
-            float v = 0.f;
+            for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int w = 0; w < kShrinkWarps; ++w) v += red[w][i >> 5][i & 31];
-            part[i] = v;
+                for (int c = 0; c < 4; ++c) red[warp][4 * rt + c][lane] = acc[rt][n][c];
+            __syncthreads();
+            for (int i = tid; i < 16 * 32; i += kShrinkWarps * 32) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kShrinkWarps; ++w) v += red[w][i >> 5][i & 31];
+                part[512 * n + i] = v;
+            }
+            if (n + 1 < kGroups) __syncthreads();
         }
         cluster_sync();
         // each CTA of the cluster adds an eighth of the values over the CTAs
-        constexpr int kEach = 16 * 32 / kShrinkCtas;
+        constexpr int kEach = kGroups * 16 * 32 / kShrinkCtas;
         if (tid < kEach) {
             const int i = rank * kEach + tid;
-            const uint32_t mine = smem_u32(part + i);
+            const uint32_t at = smem_u32(part + i);
             float v = 0.f;
 #pragma unroll
             for (int c = 0; c < kShrinkCtas; ++c) {
                 uint32_t addr;
                 float u;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(mine), "r"(c));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(at), "r"(c));
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(addr) : "memory");
                 v += u;
             }
-            // value c of tile rt, lane l: row 16 rt + l / 4 + 8 (c / 2), column 2 (l % 4) + c % 2
-            const int f = i >> 5, l = i & 31;
+            // value f of lane l: row 16 (f / 4) + l / 4 + 8 (f / 2 % 2), column 2 (l % 4) + f % 2
+            const int f = (i >> 5) & 15, l = i & 31;
             const int r = r0 + 16 * (f >> 2) + (l >> 2) + 8 * ((f >> 1) & 1);
-            const int col = m0 + 2 * (l & 3) + (f & 1);
+            const int col = m0 + 8 * (i >> 9) + 2 * (l & 3) + (f & 1);
             if (r < R && col < M && ids[col] == ad)
                 t[static_cast<size_t>(col) * R + r] = scales != nullptr ? v * scales[ad] : v;
         }
         cluster_sync();  // the values are read before any CTA leaves or goes on
     }
+}
+
+template <typename T>
+cudaError_t launch_shrink(const LoraArgs& a, float* t, cudaStream_t stream) {
+    const T* x = static_cast<const T*>(a.x);
+    const unsigned rows = (a.R + kShrinkRows - 1) / kShrinkRows;
+    if (a.M <= kShrinkPerToken)
+        lora_shrink_kernel<T, 1><<<dim3(a.M, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
+            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
+    else
+        lora_shrink_kernel<T, 4><<<dim3((a.M + 31) / 32, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
+            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
+    return cudaGetLastError();
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -190,17 +234,8 @@ size_t lora_workspace_bytes(const LoraArgs& a) {
 
 cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream) {
     float* t = static_cast<float*>(workspace);
-    const bool per_token = a.M <= kShrinkPerToken;
-    const dim3 grid(per_token ? a.M : (a.M + 7) / 8, (a.R + kShrinkRows - 1) / kShrinkRows, kShrinkCtas);
-    if (a.bf16)
-        lora_shrink_kernel<<<grid, kShrinkWarps * 32, 0, stream>>>(
-            static_cast<const __nv_bfloat16*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K,
-            a.R, a.n_adapters, per_token);
-    else
-        lora_shrink_kernel<<<grid, kShrinkWarps * 32, 0, stream>>>(
-            static_cast<const float*>(a.x), a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R,
-            a.n_adapters, per_token);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a.bf16 ? launch_shrink<__nv_bfloat16>(a, t, stream)
+                                 : launch_shrink<float>(a, t, stream);
     if (e != cudaSuccess) return e;
     if (!a.tensor) return launch_lora_rows(a, t, stream);
     return launch_lora_tc(a, t, static_cast<uint8_t*>(workspace) + lora_t_bytes(a), stream);

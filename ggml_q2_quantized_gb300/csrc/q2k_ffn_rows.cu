@@ -67,28 +67,40 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+// A thread's 64 values of one block of x as loaded (j: shift, 16 values each).
+template <typename T>
+struct RawX {
+    uint4 v[4][sizeof(T) == 4 ? 4 : 2];
+    __device__ __forceinline__ void load(const T* p, bool ok) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 t = __ldg(reinterpret_cast<const float4*>(p) + q);
-        v[4 * q] = t.x;
-        v[4 * q + 1] = t.y;
-        v[4 * q + 2] = t.z;
-        v[4 * q + 3] = t.w;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < (sizeof(T) == 4 ? 4 : 2); ++q)
+                v[j][q] = ok ? __ldg(reinterpret_cast<const uint4*>(p + 32 * j) + q)
+                             : make_uint4(0u, 0u, 0u, 0u);
     }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+    __device__ __forceinline__ void get(int j, float (&f)[16]) const {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + q);
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+            for (int q = 0; q < 4; ++q) {
+                f[4 * q] = __uint_as_float(v[j][q].x);
+                f[4 * q + 1] = __uint_as_float(v[j][q].y);
+                f[4 * q + 2] = __uint_as_float(v[j][q].z);
+                f[4 * q + 3] = __uint_as_float(v[j][q].w);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[8 * q + 2 * e] = __uint_as_float(w[e] << 16);
-            v[8 * q + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t w[4] = {v[j][q].x, v[j][q].y, v[j][q].z, v[j][q].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[8 * q + 2 * e] = __uint_as_float(w[e] << 16);
+                    f[8 * q + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                }
+            }
         }
     }
-}
+};
 
 // One block of x for eight columns (B fragments of its 16 weight steps and of
 // the group sums), and the powers of two that undo its scaling for the two
@@ -109,13 +121,13 @@ __device__ __forceinline__ void load_x_block(const T* x, int K, int block, int m
     const int g = lane >> 2, t = lane & 3;
     const int token = m0 + (kSplit ? g >> 1 : g);
     const T* p = x + static_cast<size_t>(token) * K + 256 * block + 128 * (t >> 1) + 16 * (t & 1);
-    // (x is read twice rather than held: 64 values a thread beside the
-    // fragments of other blocks would not fit its registers)
+    RawX<T> raw;
+    raw.load(p, token < M);
     float top = 0.f;
-#pragma unroll 1
-    for (int j = 0; j < 4 && token < M; ++j) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
         float v[16];
-        load16(p + 32 * j, v);
+        raw.get(j, v);
 #pragma unroll
         for (int l = 0; l < 16; ++l) top = fmaxf(top, fabsf(v[l]));
     }
@@ -131,12 +143,7 @@ __device__ __forceinline__ void load_x_block(const T* x, int K, int block, int m
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float v[16];
-        if (token < M) {
-            load16(p + 32 * j, v);
-        } else {
-#pragma unroll
-            for (int l = 0; l < 16; ++l) v[l] = 0.f;
-        }
+        raw.get(j, v);
         sum[j] = 0.f;
 #pragma unroll
         for (int l = 0; l < 16; ++l) {
@@ -287,7 +294,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     constexpr int kFrag = NT * (kSplit ? 2 : 4);    // a thread's sums of one tile
     constexpr int kOut = 32 * kFrag;                // sums of one tile
     extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a shuffle tells the compiler that the warp's index is uniform)
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
     const int group = warp / p.kw, kw = warp - group * p.kw;
     pdl_allow_dependents();
     if (group >= p.groups) return;  // (no barrier counts these warps)
@@ -307,15 +316,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     const int group_threads = 32 * p.kw;
     const int gt = kw * 32 + lane;  // thread within the group
 
-    // the words of an item that this lane copies: word f = lane + 32 i is word
-    // f % 21 of row f / 21; the low two bits hold (f / 21) / 4 (the bank skew)
-    uint32_t off[11];
-#pragma unroll
-    for (int i = 0; i < 11; ++i) {
-        const int f = lane + 32 * i, r = f / kWordsPerBlock;
-        off[i] = static_cast<uint32_t>(r * row_bytes + 4 * (f - r * kWordsPerBlock)) | (r >> 2);
-    }
-
     bool waited = false;
     for (int u0 = 0; u0 < my_units; u0 += (p.passes > 1 ? kGroupUnits : my_units)) {
         const int u1 = p.passes > 1 ? min(my_units, u0 + kGroupUnits) : my_units;
@@ -334,15 +334,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                     const uint8_t* src = (it ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes +
                                          static_cast<size_t>(first + is) * kBlockBytes;
                     const uint32_t dst = ring + (issued % kDepth) * kItemBytes + 4 * lane;
-                    const int words = max(0, min(kUnitRows, p.N - row0)) * kWordsPerBlock;
+                    const int valid = p.N - row0;
+                    // one row per copy, a word per lane; rows past N read as
+                    // zero bytes (d = dmin = 0)
+                    if (lane < kWordsPerBlock) {
+                        if (valid >= kUnitRows) {
 #pragma unroll
-                    for (int i = 0; i < 11; ++i) {
-                        const int f = lane + 32 * i;
-                        if (i < 10 || lane < 16) {
-                            // rows past N read as zero bytes (d = dmin = 0)
-                            const bool ok = f < words;
-                            cp_async_word(dst + 128 * i + 112 * (off[i] & 3u),
-                                          ok ? src + (off[i] & ~3u) : p.w0, ok ? 4u : 0u);
+                            for (int r = 0; r < kUnitRows; ++r)
+                                cp_async_word(dst + 84 * r + 112 * (r >> 2),
+                                              src + static_cast<size_t>(r) * row_bytes + 4 * lane, 4u);
+                        } else {
+#pragma unroll 1
+                            for (int r = 0; r < kUnitRows; ++r)
+                                cp_async_word(dst + 84 * r + 112 * (r >> 2),
+                                              r < valid ? src + static_cast<size_t>(r) * row_bytes + 4 * lane
+                                                        : p.w0,
+                                              r < valid ? 4u : 0u);
                         }
                     }
                     ++issued;

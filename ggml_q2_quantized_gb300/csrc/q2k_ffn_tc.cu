@@ -125,7 +125,9 @@ struct Cfg {
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
-    static_assert(kOffRaw >= kRows * kX * 4, "the sums of a tile reuse the token ring");
+    // the epilogue's sums, and with adapters 64 t a token, reuse the token ring
+    // (and the adapters' ids a raw slot)
+    static_assert(kOffRaw >= (kRows + (kMode == Tc::kLora ? 64 : 0)) * kX * 4, "epilogue");
     static_assert(kColA + 32 * kAStages <= kTmemCols, "tensor memory");
     static_assert(kOffRaw % 1024 == 0 && kOffCodes % 16 == 0 && kOffTables % 16 == 0, "alignment");
 };
@@ -207,70 +209,94 @@ __device__ __forceinline__ void dec_barrier() {
 // s_a B_a t of each token's adapter: per 16 rows and eight tokens, one product
 // (m16n8k16) for each adapter that occurs among them, B_a as stored and t split
 // into two bf16 (16 bits); a token's sum takes only its own adapter's product.
-// Tokens [first, tokens), first a multiple of 8.
-__device__ __forceinline__ void add_adapters(float* sums, const TcArgs& p, int n0, int m0,
-                                             int first, int tokens, int warp, int lane) {
+// Tokens [first, end), first a multiple of 8.  t comes through shared memory 64
+// values a token at a time (tbuf; value r of token c at word 64 c + (r ^ 8 (c %
+// 4)), so that the eight tokens a warp reads together fall on different banks),
+// B_a's fragments stay in registers from one token group to the next with the
+// same adapter: reading both per group cost 40 us of an 85 us call (512 tokens,
+// 7168 x 7168, rank 64).
+__device__ __forceinline__ void add_adapters(float* sums, float* tbuf, int* id_buf, const TcArgs& p,
+                                             int n0, int m0, int first, int end) {
+    const int td = threadIdx.x, warp = td >> 5, lane = td & 31;
     const int g = lane >> 2, t = lane & 3;
     const int row = 16 * (warp & 7) + g;  // this lane's rows: row, row + 8
     const bool ok0 = n0 + row < p.N, ok1 = n0 + row + 8 < p.N;
-    for (int c0 = first + 8 * (warp >> 3); c0 < tokens; c0 += 16) {
-        const int m = m0 + c0 + g;  // column g of the product
-        int id = c0 + g < tokens ? p.ids[m] : -1;
-        const bool bad = id < -1 || id >= p.n_adapters;
-        if (bad) id = -1;
-        // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
-        const int id0 = __shfl_sync(0xFFFFFFFFu, id, 8 * t);
-        const int id1 = __shfl_sync(0xFFFFFFFFu, id, 8 * t + 4);
-        const int bad0 = __shfl_sync(0xFFFFFFFFu, int(bad), 8 * t);
-        const int bad1 = __shfl_sync(0xFFFFFFFFu, int(bad), 8 * t + 4);
-        float* s0 = sums + (c0 + 2 * t) * kRows + row;
-        float* s1 = s0 + kRows;
-        if (bad0) s0[0] = s0[8] = 0.f;  // an id out of range: a zero row
-        if (bad1) s1[0] = s1[8] = 0.f;
-        unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
-        while (todo != 0) {
-            const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
-            todo &= ~__ballot_sync(0xFFFFFFFFu, id == a);
-            const __nv_bfloat16* b0 = p.b + (static_cast<size_t>(a) * p.N + n0 + row) * p.R;
-            const __nv_bfloat16* b1 = b0 + static_cast<size_t>(8) * p.R;
-            const float* tr = p.t + static_cast<size_t>(m) * p.R;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = 0; r < p.R; r += 16) {
-                // K slots 2 t, 2 t + 1 and 2 t + 8, 2 t + 9 of the step
-                uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0, h0 = 0, h1 = 0, l0 = 0, l1 = 0;
-                const bool wide = r + 8 < p.R;  // (the rank is a multiple of 8)
-                if (ok0) {
-                    a0 = __ldg(reinterpret_cast<const uint32_t*>(b0 + r) + t);
-                    if (wide) a2 = __ldg(reinterpret_cast<const uint32_t*>(b0 + r + 8) + t);
+    // ids: -1 none, -2 out of range (a zero row)
+    for (int c = first + td; c < end; c += kDecThreads) {
+        const int id = p.ids[m0 + c];
+        id_buf[c] = id < -1 || id >= p.n_adapters ? -2 : id;
+    }
+    for (int r0 = 0; r0 < p.R; r0 += 64) {
+        const int width = min(64, p.R - r0);  // a multiple of 8
+        for (int i = 16 * first + td; i < 16 * end; i += kDecThreads) {
+            const int c = i >> 4, r = 4 * (i & 15);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < width)
+                v = *reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m0 + c) * p.R + r0 + r);
+            *reinterpret_cast<float4*>(tbuf + 64 * c + (r ^ (8 * (c & 3)))) = v;
+        }
+        dec_barrier();
+        int cur = -1;
+        uint32_t a[4][4];
+        for (int c0 = first + 8 * (warp >> 3); c0 < end; c0 += 16) {
+            const int id = c0 + g < end ? id_buf[c0 + g] : -1;
+            // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
+            const int id0 = __shfl_sync(0xFFFFFFFFu, id, 8 * t);
+            const int id1 = __shfl_sync(0xFFFFFFFFu, id, 8 * t + 4);
+            float* s0 = sums + (c0 + 2 * t) * kRows + row;
+            float* s1 = s0 + kRows;
+            if (id0 == -2) s0[0] = s0[8] = 0.f;
+            if (id1 == -2) s1[0] = s1[8] = 0.f;
+            unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
+            while (todo != 0) {
+                const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
+                todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
+                if (ad != cur) {
+                    cur = ad;
+                    const __nv_bfloat16* b0 =
+                        p.b + (static_cast<size_t>(ad) * p.N + n0 + row) * p.R + r0;
+                    const __nv_bfloat16* b1 = b0 + static_cast<size_t>(8) * p.R;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        a[q][0] = a[q][1] = a[q][2] = a[q][3] = 0u;
+                        const bool in0 = 16 * q < width, in1 = 16 * q + 8 < width;
+                        if (ok0 && in0) a[q][0] = __ldg(reinterpret_cast<const uint32_t*>(b0 + 16 * q) + t);
+                        if (ok1 && in0) a[q][1] = __ldg(reinterpret_cast<const uint32_t*>(b1 + 16 * q) + t);
+                        if (ok0 && in1) a[q][2] = __ldg(reinterpret_cast<const uint32_t*>(b0 + 16 * q + 8) + t);
+                        if (ok1 && in1) a[q][3] = __ldg(reinterpret_cast<const uint32_t*>(b1 + 16 * q + 8) + t);
+                    }
                 }
-                if (ok1) {
-                    a1 = __ldg(reinterpret_cast<const uint32_t*>(b1 + r) + t);
-                    if (wide) a3 = __ldg(reinterpret_cast<const uint32_t*>(b1 + r + 8) + t);
-                }
-                if (id == a) {
-                    const float2 u = reinterpret_cast<const float2*>(tr + r)[t];
-                    h0 = pack_bf16(u.x, u.y);
-                    l0 = pack_bf16(u.x - __uint_as_float(h0 << 16),
-                                   u.y - __uint_as_float(h0 & 0xFFFF0000u));
-                    if (wide) {
-                        const float2 v = reinterpret_cast<const float2*>(tr + r + 8)[t];
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (16 * q >= width) break;
+                    uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0;
+                    if (id == ad) {
+                        const float* tr = tbuf + 64 * (c0 + g);
+                        const int x = 8 * ((c0 + g) & 3);
+                        const float2 u = *reinterpret_cast<const float2*>(tr + ((16 * q + 2 * t) ^ x));
+                        const float2 v = *reinterpret_cast<const float2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
+                        h0 = pack_bf16(u.x, u.y);
                         h1 = pack_bf16(v.x, v.y);
+                        l0 = pack_bf16(u.x - __uint_as_float(h0 << 16),
+                                       u.y - __uint_as_float(h0 & 0xFFFF0000u));
                         l1 = pack_bf16(v.x - __uint_as_float(h1 << 16),
                                        v.y - __uint_as_float(h1 & 0xFFFF0000u));
                     }
+                    mma_bf16_16816(d, a[q][0], a[q][1], a[q][2], a[q][3], h0, h1);
+                    mma_bf16_16816(d, a[q][0], a[q][1], a[q][2], a[q][3], l0, l1);
                 }
-                mma_bf16_16816(d, a0, a1, a2, a3, h0, h1);
-                mma_bf16_16816(d, a0, a1, a2, a3, l0, l1);
-            }
-            if (id0 == a) {
-                s0[0] += d[0];
-                s0[8] += d[2];
-            }
-            if (id1 == a) {
-                s1[0] += d[1];
-                s1[8] += d[3];
+                if (id0 == ad) {
+                    s0[0] += d[0];
+                    s0[8] += d[2];
+                }
+                if (id1 == ad) {
+                    s1[0] += d[1];
+                    s1[8] += d[3];
+                }
             }
         }
+        dec_barrier();
     }
 }
 
@@ -824,8 +850,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         } else {
             if constexpr (kMode == Tc::kLora) {
                 pdl_wait_prerequisites();  // t (written by this grid or one before)
-                add_adapters(sums, p, n0, m0, first, end, warp, lane);
-                dec_barrier();
+                add_adapters(sums, sums + kX * kRows, reinterpret_cast<int*>(smem + C::kOffRaw), p,
+                             n0, m0, first, end);
             }
             for (int c = first + warp; c < end; c += kDecWarps)
 #pragma unroll
