@@ -14,10 +14,12 @@
 // taken before anything is stored.
 //
 // Backward: dx = [dg du] [Wg; Wu], a product over the weights' rows.  A tile's
-// 128 rows are half a block of columns (k), a stage is 64 weight rows: the
-// decoders transpose those rows' quant bytes four by four in shared memory, so
-// that a lane reads the codes of its column over 32 weight rows as eight words,
-// and pick each code's value from the row's table there.
+// 128 rows are half a block of columns (k), a stage is 64 weight rows.  A thread
+// decodes a weight row as above (one table serves 16 codes) and stores it as
+// stored, k running, which is the MMA's A operand "MN-major" in shared memory:
+// the transposition costs nothing.  (Transposing the codes first, so that a lane
+// could write its own column to tensor memory, took 2200 warp instructions a
+// stage against 900, and 198 us instead of 110 for 512 tokens x 14336 x 4096.)
 //
 // With few tiles, K is split over a cluster of CTAs whose sums meet through
 // distributed shared memory in a fixed order.
@@ -82,15 +84,9 @@ constexpr int kMmaWarp = kDecWarps, kWaitWarp = kDecWarps + 1, kWWarp = kDecWarp
 constexpr int kThreads = 32 * (kDecWarps + 5);
 constexpr int kMaxParts = 8;
 constexpr int kPlanSms = 152;  // K parts are planned for the whole GPU, whatever the device
+constexpr int kTileStages = 20;  // a tile's set-up and epilogue, in stages of its K loop
 
-// Backward, per stage: the codes of 32 columns (lane l of the four shifts) over
-// 64 weight rows, 80 bytes a column (eight lanes' 16-byte reads fall on
-// different banks), and for each (shift, segment) 64 tables of four bf16, 16
-// bytes between one (shift, segment) and the next.
-constexpr int kCodePitch = kStageK + 16;
-constexpr int kCodeBytes = 32 * kCodePitch;
-constexpr int kTablePitch = 8 * kStageK + 16;
-constexpr int kTableBytes = 8 * kTablePitch;
+constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memory
 
 enum class Tc { kGated, kLora, kBackward };
 
@@ -102,34 +98,36 @@ template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
     static constexpr int kIssuers = kX == 256 ? 1 : 2;
-    static constexpr int kHand = kX == 256 ? 2 : 4;  // stages handed to the issuers at a time
+    static constexpr int kHand = kX == 256 || kBack ? 2 : 4;  // stages handed over at a time
     static constexpr bool kPairs = kIssuers == 2;    // stages released in pairs
     static constexpr int kXStage = kX * kStageK * 2;
-    static constexpr int kXStages = kX < 256 ? 8 : !kBack ? 6 : kTma ? 5 : 4;
-    static constexpr int kAStages = 8;
+    static constexpr int kXStages = kBack ? (kX == 256 ? 4 : kX == 128 ? 6 : 8) : kX == 256 ? 6 : 8;
+    static constexpr int kAStages = kBack ? kXStages : 8;
+    // decoders: groups of warps on stages (backward) or block halves in turn
+    static constexpr int kGroupWarps = kBack ? 4 : 8;
     static constexpr uint32_t kColA = kX * kIssuers;
     static constexpr uint32_t kTmemCols = 512;
-    // raw slots: a block column of 128 weight rows, or (backward) of 64 for a stage
+    // raw slots: a block column of 128 weight rows, or (backward) of 64 for a
+    // stage, without TMA only the 11 words of the half block that it needs
     static constexpr int kRawRows = kBack ? kStageK : kRows;
-    static constexpr int kRawPitch = kTma || kBack ? kBoxBytes : kBlockBytes;
+    static constexpr int kRawPitch = kTma ? kBoxBytes : kBack ? 44 : kBlockBytes;
     static constexpr int kRawBytes = kRawRows * kRawPitch;
-    static constexpr int kRaw = kBack ? (kTma ? 4 : 6) : (kTma ? 2 : 3);
-    static constexpr int kOffRaw = kXStages * kXStage;
-    // backward: transposed codes and value tables, two of each per decoder group
-    static constexpr int kOffCodes = kOffRaw + kRaw * kRawBytes;
-    static constexpr int kOffTables = kOffCodes + (kBack ? 4 * kCodeBytes : 0);
+    static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : (kTma ? 2 : 3);
+    // backward: decoded stages in shared memory, 64 weight rows x 128 columns
+    static constexpr int kOffA = kXStages * kXStage;
+    static constexpr int kOffRaw = kOffA + (kBack ? kAStages * kABytes : 0);
     // bars: x_full, x_empty [kXStages], a_full, a_empty [kAStages], raw_full,
     //       raw_empty [kRaw], accum, drain
     static constexpr int kNumBars = 2 * kXStages + 2 * kAStages + 2 * kRaw + 2;
-    static constexpr int kOffBar = (kOffTables + (kBack ? 4 * kTableBytes : 0) + 7) & ~7;
+    static constexpr int kOffBar = (kOffRaw + kRaw * kRawBytes + 7) & ~7;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
     // the epilogue's sums, and with adapters 64 t a token, reuse the token ring
     // (and the adapters' ids a raw slot)
-    static_assert(kOffRaw >= (kRows + (kMode == Tc::kLora ? 64 : 0)) * kX * 4, "epilogue");
-    static_assert(kColA + 32 * kAStages <= kTmemCols, "tensor memory");
-    static_assert(kOffRaw % 1024 == 0 && kOffCodes % 16 == 0 && kOffTables % 16 == 0, "alignment");
+    static_assert(kOffA >= (kRows + (kMode == Tc::kLora ? 64 : 0)) * kX * 4, "epilogue");
+    static_assert(kColA + (kBack ? 0 : 32 * kAStages) <= kTmemCols, "tensor memory");
+    static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0, "swizzle and TMA alignment");
 };
 
 struct TcArgs {
@@ -337,94 +335,38 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
 }
 
 // Backward, non-TMA: the words of 64 weight rows that a stage needs (two of
-// scales, eight of codes, d and dmin) at their places in a raw slot, by the 256
-// threads of a decoder group.  Rows past N are zero (their tables are zero).
+// scales, eight of codes, d and dmin) packed into a raw slot, by the 128 threads
+// of a decoder group.  Rows past N are zero (they decode to 0).
 __device__ __forceinline__ void issue_raw_rows(const TcArgs& p, uint32_t dst, int stage, int block,
                                                int half, int tg) {
     const bool up = stage >= p.half_stages;
     const int n0 = kStageK * (up ? stage - p.half_stages : stage);
     const uint8_t* w = up ? p.w1 : p.w0;
     const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
-    for (int f = tg; f < kStageK * 11; f += 256) {
+    for (int f = tg; f < kStageK * 11; f += 128) {
         const int r = f / 11, i = f - 11 * r;
         const int word = i < 2 ? 2 * half + i : i < 10 ? 4 + 8 * half + (i - 2) : 20;
         const bool ok = n0 + r < p.N;
         const uint8_t* src = w + (ok ? static_cast<size_t>(n0 + r) * row_bytes +
                                            static_cast<size_t>(block) * kBlockBytes + 4 * word
                                      : 0);
-        cp_async_4(dst + r * kBoxBytes + 4 * word, src, ok ? 4u : 0u);
+        cp_async_4(dst + 4 * f, src, ok ? 4u : 0u);
     }
     cp_async_commit();
 }
 
-// Backward decode, first half of a stage (thread tg of the group's 256): value
-// tables of 64 weight rows at one shift (both segments), and the codes of the
-// half block's 32 byte columns, transposed.  raw: slot + offset of the block.
-__device__ __forceinline__ void transpose_stage(uint32_t raw, int half, uint32_t codes,
-                                                uint32_t tables, int tg) {
-    {
-        const int r = tg & 63, j = tg >> 6;
-        const uint32_t row = raw + r * kBoxBytes;
-        const uint32_t word = ld_shared_u32(row + 8 * half + 4 * (j >> 1)) >> (16 * (j & 1));
-        const uint32_t dd = ld_shared_u32(row + 80);
-        const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+// The weights of segment `seg` of a half block of one row at shift J: words 0..3
+// of `q` -> 16 bf16 (k running).
+template <int J>
+__device__ __forceinline__ void decode_segment(const uint32_t (&q)[4], uint32_t sc, float d, float dmin,
+                                               uint32_t (&o)[8]) {
+    uint32_t lo, hi;
+    weight_table(sc, d, dmin, lo, hi);
 #pragma unroll
-        for (int seg = 0; seg < 2; ++seg) {
-            uint32_t lo, hi;
-            weight_table((word >> (8 * seg)) & 0xFFu, d, dmin, lo, hi);
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tables + (2 * j + seg) * kTablePitch +
-                                                                    8 * r),
-                         "r"(lo), "r"(hi)
-                         : "memory");
-        }
-    }
-    if (tg < 128) {
-        const int cw = tg & 7, rq = tg >> 3;  // byte columns 4 cw .., weight rows 4 rq ..
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            w[q] = ld_shared_u32(raw + (4 * rq + q) * kBoxBytes + 16 + 32 * half + 4 * cw);
-        const uint32_t t0 = __byte_perm(w[0], w[1], 0x5140), t1 = __byte_perm(w[2], w[3], 0x5140);
-        const uint32_t t2 = __byte_perm(w[0], w[1], 0x7362), t3 = __byte_perm(w[2], w[3], 0x7362);
-        const uint32_t o[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632),
-                               __byte_perm(t2, t3, 0x5410), __byte_perm(t2, t3, 0x7632)};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(codes + (4 * cw + q) * kCodePitch + 4 * rq),
-                         "r"(o[q])
-                         : "memory");
-    }
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Second half: 16 bf16 pairs of column `lane` of shift j over weight rows 32 nh
-// .. + 31.  A pair takes each row's value from that row's table by byte permute.
-__device__ __forceinline__ void decode_column(uint32_t codes, uint32_t tables, int j, int nh,
-                                              int lane, uint32_t (&o)[2][8]) {
-    const uint32_t cp = codes + lane * kCodePitch + 32 * nh;
-    const uint32_t tp = tables + (2 * j + (lane >> 4)) * kTablePitch + 8 * 32 * nh;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint4 c = ld_shared_v4(cp + 16 * h);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // byte i -> nibbles (2 q_i, 2 q_i + 1)
-            const uint32_t sel = ((cw[e] >> (2 * j)) & 0x03030303u) * 0x22u + 0x10101010u;
-            const uint4 a = ld_shared_v4(tp + 32 * (4 * h + e));
-            const uint4 b = ld_shared_v4(tp + 32 * (4 * h + e) + 16);
-            const uint32_t s2 = sel >> 16;
-            o[h][2 * e] = __byte_perm(__byte_perm(a.x, a.y, sel), __byte_perm(a.z, a.w, sel), 0x7610);
-            o[h][2 * e + 1] = __byte_perm(__byte_perm(b.x, b.y, s2), __byte_perm(b.z, b.w, s2), 0x7610);
-        }
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t sel = code_selectors<J>(q[e]);
+        o[2 * e] = __byte_perm(lo, hi, sel);
+        o[2 * e + 1] = __byte_perm(lo, hi, __umulhi(sel, 0x10000u));  // sel >> 16
     }
 }
 
@@ -468,12 +410,12 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             mbar_init(bar_xempty + 8 * s, 1);  // MMA commit
         }
         for (int s = lane; s < C::kAStages; s += 32) {
-            mbar_init(bar_afull + 8 * s, kDecWarps / 2);  // the warps of its group
+            mbar_init(bar_afull + 8 * s, C::kGroupWarps);  // the warps of its group
             mbar_init(bar_aempty + 8 * s, C::kPairs ? C::kIssuers : 1);
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
-            mbar_init(bar_rawempty + 8 * r, kBack ? kDecWarps / 2 : kDecWarps);
+            mbar_init(bar_rawempty + 8 * r, kBack ? C::kGroupWarps : kDecWarps);
         }
         if (lane == 0) {
             mbar_init(bar_accum, C::kIssuers);
@@ -497,8 +439,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         const uint32_t raw0 = sbase + C::kOffRaw;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         if (!kTma && !p.const_weights) pdl_wait_prerequisites();
-        // Publish a stage decoded into two runs of eight columns.
-        auto publish = [&](int i, uint32_t col0, const uint32_t (&o0)[8], uint32_t col1,
+        // Publish a stage decoded into two runs of eight columns of tensor memory.
+        [[maybe_unused]] auto publish = [&](int i, uint32_t col0, const uint32_t (&o0)[8], uint32_t col1,
                            const uint32_t (&o1)[8]) -> bool {
             const int s = i % C::kAStages;
             const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
@@ -517,53 +459,79 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             return true;
         };
         if constexpr (kBack) {
-            const int tg = td & 255;
+            // group (four warps) takes every fourth stage: warp = 32 weight rows
+            // and a segment, lane = the row, all four shifts
+            const int own = warp >> 2, tg = td & 127;
+            const int seg = warp & 1, n = 32 * ((warp >> 1) & 1) + lane;
             const int block = n0 / kQK, half = (n0 / kRows) & 1;
-            constexpr int kOwn = C::kRaw / 2;  // raw slots of a group
             if constexpr (!kTma) {
-                for (int i = 0; i < kOwn - 1; ++i) {
-                    if (2 * i + group < n_iters)
-                        issue_raw_rows(p, raw0 + (2 * i + group) * C::kRawBytes,
-                                       4 * q0 + 2 * i + group, block, half, tg);
-                    else
-                        cp_async_commit();
-                }
+                if (own < n_iters)
+                    issue_raw_rows(p, raw0 + own * C::kRawBytes, 4 * q0 + own, block, half, tg);
+                else
+                    cp_async_commit();
             }
             bool ok = true;  // a warp that gave up still passes the group's barriers
-            for (int i = group; i < n_iters; i += 2) {
+            for (int i = own; i < n_iters; i += 4) {
                 const int slot = i % C::kRaw;
-                uint32_t raw = raw0 + slot * C::kRawBytes;
+                const uint32_t raw = raw0 + slot * C::kRawBytes + n * C::kRawPitch;
+                uint32_t at_sc = raw, at_q = raw + 8, at_d = raw + 40;
                 if constexpr (kTma) {
                     ok = ok && __all_sync(0xFFFFFFFFu,
                                           mbar_wait_bounded(bar_raw + 8 * slot, (i / C::kRaw) & 1,
                                                             abort_flag, err, kErrTimeoutEmpty));
-                    raw += (kBlockBytes * block) & 15;  // the box starts at a 16-byte boundary
+                    const uint32_t at = raw + ((kBlockBytes * block) & 15);  // (a 16-byte boundary)
+                    at_sc = at + 8 * half;
+                    at_q = at + 16 + 32 * half;
+                    at_d = at + 80;
                 } else {
-                    cp_async_wait<kOwn - 2>();
-                    asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
-                    // the group is past the slot that the stage after next takes
-                    const int next = i + 2 * (kOwn - 1);
-                    if (next < n_iters)
-                        issue_raw_rows(p, raw0 + (next % C::kRaw) * C::kRawBytes, 4 * q0 + next,
+                    // the group's other slot was read before this barrier
+                    if (i + 4 < n_iters) {
+                        asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
+                        issue_raw_rows(p, raw0 + ((i + 4) % C::kRaw) * C::kRawBytes, 4 * q0 + i + 4,
                                        block, half, tg);
-                    else
-                        cp_async_commit();
+                        cp_async_wait<1>();
+                    } else {
+                        cp_async_wait<0>();
+                    }
+                    asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
                 }
-                // two buffers: the one written now was last read two of the
-                // group's stages ago, before the barrier of the stage between
-                const int buf = 2 * group + ((i >> 1) & 1);
-                const uint32_t codes = sbase + C::kOffCodes + buf * kCodeBytes;
-                const uint32_t tables = sbase + C::kOffTables + buf * kTableBytes;
-                if (ok) transpose_stage(raw, half, codes, tables, tg);
+                if (!ok) continue;
+                uint32_t q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[e] = ld_shared_u32(at_q + 16 * seg + 4 * e);
+                const uint32_t sc0 = ld_shared_u32(at_sc) >> (8 * seg);
+                const uint32_t sc1 = ld_shared_u32(at_sc + 4) >> (8 * seg);
+                const uint32_t dd = ld_shared_u32(at_d);
                 if constexpr (kTma) {
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
+                    if (lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
                 }
-                asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
+                const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+                uint32_t o[4][8];
+                decode_segment<0>(q, sc0 & 0xFFu, d, dmin, o[0]);
+                decode_segment<1>(q, (sc0 >> 16) & 0xFFu, d, dmin, o[1]);
+                decode_segment<2>(q, sc1 & 0xFFu, d, dmin, o[2]);
+                decode_segment<3>(q, (sc1 >> 16) & 0xFFu, d, dmin, o[3]);
+                const int s = i % C::kAStages;
+                const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
+                if (i >= C::kAStages)
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    mbar_wait_bounded(bar_aempty + 8 * rel, ((i / C::kAStages) - 1) & 1,
+                                                      abort_flag, err, kErrTimeoutEmpty));
                 if (!ok) continue;
-                uint32_t o[2][8];
-                decode_column(codes, tables, quarter, sub, lane, o);
-                ok = publish(i, 16u * sub, o[0], 16u * sub + 8u, o[1]);
+                // row n of the tile: 128 bytes of columns 64 c .. at 8192 c +
+                // 128 n, its 16-byte chunks swizzled by n % 8
+                const uint32_t dst = sbase + C::kOffA + s * kABytes + 128 * n;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        st_shared_v4(dst + 8192 * (j >> 1) +
+                                         (((4 * (j & 1) + 2 * seg + c) ^ (n & 7)) << 4),
+                                     o[j][4 * c], o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
+                fence_async_smem();  // this thread's stores -> visible to the MMA
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_afull + 8 * s);
             }
         } else {
             const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
@@ -652,8 +620,9 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         // With two issuers the MMA warp takes the even stages into accumulator
         // 0, the waiter the odd ones into accumulator 1.
         const int me = warp == kMmaWarp ? 0 : 1;
-        const uint32_t idesc = bf16_idesc(nx);
+        const uint32_t idesc = bf16_idesc(nx) | (kBack ? kIdescAMnMajor : 0u);
         const uint64_t xdesc0 = sw128_desc(sbase);
+        const uint64_t adesc0 = sw128_mn_desc(sbase + C::kOffA, 8192);
         const uint32_t acc = tmem + static_cast<uint32_t>(me * kX);
         for (int i0 = 0; i0 < n_iters; i0 += C::kHand) {
             if (C::kIssuers == 2 && me == 1 && lane == 0 && !*abort_flag) {
@@ -678,9 +647,15 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     const int sx = i % C::kXStages, sa = i % C::kAStages;
                     const uint64_t xdesc = xdesc0 + static_cast<uint64_t>(sx * (C::kXStage >> 4));
                     const uint32_t a_s = tmem + C::kColA + 32u * sa;
+                    const uint64_t adesc = adesc0 + static_cast<uint64_t>(sa * (kABytes >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kStageK / 16; ++kk)
-                        mma(acc, a_s + 8u * kk, xdesc + 2u * kk, idesc, i >= C::kIssuers || kk > 0);
+                    for (int kk = 0; kk < kStageK / 16; ++kk) {
+                        const uint32_t add = i >= C::kIssuers || kk > 0;
+                        if (kBack)  // (a K-step is 16 rows of 128 bytes)
+                            mma_smem(acc, adesc + 128u * kk, xdesc + 2u * kk, idesc, add);
+                        else
+                            mma(acc, a_s + 8u * kk, xdesc + 2u * kk, idesc, add);
+                    }
                     // a stage is released when a later one takes its place
                     if (C::kPairs) {
                         if ((i & ~1) + C::kAStages < n_iters)
@@ -971,18 +946,33 @@ struct Plan {
 };
 
 // rows: those of the product's row tiles; quads: its K in parts of four stages.
-// Tokens per tile: as few as hold them all up to 128; 256 (each decoded weight
-// then serves twice the MMA work) once tiles of 128 would take more than one
-// wave of CTAs.  K parts while the tiles leave half of the GPU or more idle.
+// Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,
+// whichever is expected to end first: waves of CTAs times stages of a K part
+// times the time of a stage, about 1 : 0.7 for 256 and 128 tokens (512 tokens x
+// 14336 x 4096 backwards: 110 us in tiles of 256 and two K parts, 150 us in
+// tiles of 128).  K parts while the tiles leave half of the GPU or more idle.
 Plan make_plan(int M, int rows, int tile_rows, int quads) {
-    Plan p;
-    p.row_tiles = (rows + tile_rows - 1) / tile_rows;
-    const long ctas = static_cast<long>(p.row_tiles) * ((M + 127) / 128);
-    p.x_rows = M <= 32 ? 32 : M <= 64 ? 64 : ctas > kPlanSms ? 256 : 128;
-    p.token_tiles = (M + p.x_rows - 1) / p.x_rows;
-    const long tiles = static_cast<long>(p.row_tiles) * p.token_tiles;
-    p.parts = static_cast<int>(std::max(1L, std::min<long>(std::min(kMaxParts, quads), kPlanSms / tiles)));
-    return p;
+    Plan best = {};
+    double best_cost = 0;
+    for (int x_rows : {32, 64, 128, 256}) {
+        if (x_rows < 128 && x_rows < M) continue;
+        Plan p;
+        p.x_rows = x_rows;
+        p.row_tiles = (rows + tile_rows - 1) / tile_rows;
+        p.token_tiles = (M + x_rows - 1) / x_rows;
+        const long tiles = static_cast<long>(p.row_tiles) * p.token_tiles;
+        p.parts = static_cast<int>(
+            std::max(1L, std::min<long>(std::min(kMaxParts, quads), kPlanSms / tiles)));
+        const long waves = (tiles * p.parts + kPlanSms - 1) / kPlanSms;
+        const double stages = 4.0 * quads / p.parts;
+        const double cost = waves * (stages + kTileStages) * (x_rows == 256 ? 1.0 : 0.7);
+        if (best_cost == 0 || cost < best_cost) {
+            best = p;
+            best_cost = cost;
+        }
+        if (x_rows >= M) break;  // a wider tile would be empty columns
+    }
+    return best;
 }
 
 // A bf16 [rows, cols] matrix with rows `pitch` apart, in boxes of box_rows x 64

@@ -46,6 +46,14 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) |
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+// The same for an operand stored with its rows (M) running: 64 rows are 128
+// contiguous bytes, eight K steps of those 1024 bytes (swizzled as above), the
+// next eight K right behind, the next 64 rows `mn_step` bytes further.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t mn_step) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (uint64_t(mn_step >> 4) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+constexpr uint32_t kIdescAMnMajor = 1u << 15;
 // Instruction descriptor, kind::f16: D f32, A and B bf16, both K-major, M = 128.
 __device__ __forceinline__ uint32_t bf16_idesc(int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -58,6 +66,15 @@ __device__ __forceinline__ void mma(uint32_t tmem_d, uint32_t tmem_a, uint64_t b
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in shared memory.
+__device__ __forceinline__ void mma_smem(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
