@@ -680,39 +680,89 @@ def matmul_id_workspace_bytes(n_tokens: int, top_k: int, n: int, k: int, n_exper
                                                     ctypes.byref(p)))
 
 
-def _activations(t, name, shape=None, like=None):
-    """The dtype code of a contiguous f32 or bf16 CUDA tensor, its shape, device
-    and (with ``like``) dtype checked."""
+def _need_activations(t, name, dtype=None):
+    """Raise unless ``t`` is a contiguous f32 or bf16 CUDA tensor (of ``dtype``)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if like is not None:
-        _require_cuda(t, name, like.dtype)
-        _same_device(t, name, like)
-    elif not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
 
 
-def _same_device(t, name, like):
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+def _need_like(x, **tensors):
+    """Raise unless every tensor (dtype, shape or None, tensor) fits and is on x's device."""
+    for name, (dtype, shape, t) in tensors.items():
+        _require_cuda(t, name, dtype)
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
 
 
-def _workspace(workspace, need, like):
-    """(tensor or None, pointer, bytes): "auto" takes one from PyTorch's allocator."""
+def _fits(dev, dtype, *tensors):
+    """Whether every tensor is a contiguous ``dtype`` tensor on CUDA device ``dev``
+    (the quick form of ``_need_like``, which says what is wrong)."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return dev >= 0
+
+
+# A call's parameter block (by reference), workspace bytes and path code, by its
+# geometry: what depends on neither the tensors nor their contents.
+_ffn_plans: dict = {}
+
+
+def _ffn_plan(key):
+    """``key``: (kind, path, dtype, m, n, k, act) or ("lora", path, dtype, m, n, k,
+    rank, n_adapters)."""
+    lib, torch = load(), _torch()
+    kind, path, dtype, m, n, k = key[:6]
+    pcode, code = _PATHS[path], DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
+    if kind == "lora":
+        p = LoraParams(m, n, k, GGML_TYPE_Q2_K, code, *key[6:], 0)
+        need = lib.q2k_matmul_lora_workspace_bytes(pcode, ctypes.byref(p))
+    else:
+        p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, code, _ACTS[key[6]])
+        need = (lib.q2k_gated_ffn_backward_workspace_bytes(ctypes.byref(p))
+                if kind == "backward"
+                else lib.q2k_gated_ffn_workspace_bytes(pcode, ctypes.byref(p)))
+    if len(_ffn_plans) >= 4096:  # (geometries, not tensors: a bound for long runs)
+        _ffn_plans.clear()
+    plan = _ffn_plans[key] = (ctypes.byref(p), need, pcode)
+    return plan
+
+
+def _ffn_workspace(workspace, need, x):
+    """(tensor, pointer, bytes) of a call's workspace: "auto" takes one from
+    PyTorch's allocator."""
+    if workspace is None or (need == 0 and isinstance(workspace, str)):
+        return None, None, 0
     torch = _torch()
     if isinstance(workspace, str):
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
-    if workspace is None:
-        return None, None, 0
-    _require_cuda(workspace, "workspace", torch.uint8)
-    _same_device(workspace, "workspace", like)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _need_like(x, workspace=(torch.uint8, None, workspace))
     return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _ffn_call(dev, fn, *args):
+    """Call ``fn`` with the current stream of CUDA device ``dev``, ``dev`` current."""
+    cuda = _torch_mod.cuda
+    if cuda.current_device() == dev:
+        status = fn(*args, _raw_stream(dev) if _raw_stream else cuda.current_stream(dev).cuda_stream)
+    else:
+        with cuda.device(dev):
+            status = fn(*args, cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(_lib, status)
 
 
 def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None, path="auto",
@@ -727,31 +777,27 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     ``workspace`` as in ``matmul``: up to 16 bf16 or 8 f32 tokens the weights
     are exact, above that x and W are rounded to bf16 for the tensor cores.
     """
-    torch = _torch()
-    dtype = _activations(x, "x")
+    torch = _torch_mod or _torch()
+    _need_activations(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [m, k]")
     m, k = x.shape
-    for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
-        _require_cuda(t, name, torch.uint8)
-        _same_device(t, name, x)
+    dt, dev = x.dtype, x.get_device()
+    if not _fits(dev, torch.uint8, w_gate, w_up):
+        _need_like(x, w_gate=(torch.uint8, None, w_gate), w_up=(torch.uint8, None, w_up))
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    _activations(out, "out", (m, n), like=x)
+        out = torch.empty((m, n), dtype=dt, device=x.device)
+    else:
+        _need_like(x, out=(dt, (m, n), out))
     gate = torch.empty_like(out) if save else None
     up = torch.empty_like(out) if save else None
-    p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, dtype, _ACTS[act])
-    lib = _lib if _lib is not None else load()
-    pcode = _PATHS[path]
-    need = lib.q2k_gated_ffn_workspace_bytes(pcode, ctypes.byref(p))
-    _keep, ws, ws_bytes = _workspace(workspace, need, x)
-    with _on_device(x):
-        _check(lib, lib.q2k_gated_ffn(pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
-                                      x.data_ptr(), x.numel(), w_gate.data_ptr(), w_gate.numel(),
-                                      w_up.data_ptr(), w_up.numel(), out.data_ptr(), out.numel(),
-                                      gate.data_ptr() if save else None,
-                                      up.data_ptr() if save else None, ctypes.byref(p), ws,
-                                      ws_bytes, _stream_handle(x)))
+    key = ("gated", path, dt, m, n, k, act)
+    params, need, pcode = _ffn_plans.get(key) or _ffn_plan(key)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, need, x)
+    _ffn_call(dev, _lib.q2k_gated_ffn, pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
+              x.data_ptr(), m * k, w_gate.data_ptr(), w_gate.numel(), w_up.data_ptr(),
+              w_up.numel(), out.data_ptr(), m * n, gate.data_ptr() if save else None,
+              up.data_ptr() if save else None, params, ws, ws_bytes)
     return (out, gate, up) if save else out
 
 
@@ -762,28 +808,26 @@ def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace
     projections); returns ``(dx, dgate, dup)``: ``dx = dgate Wg + dup Wu``
     ``[m, k]`` and the gradients ``[m, n]`` of the two projections.
     """
-    torch = _torch()
-    _require_cuda(dh, "dh", torch.bfloat16)
+    torch = _torch_mod or _torch()
+    bf16, u8 = torch.bfloat16, torch.uint8
+    _need_activations(dh, "dh", bf16)
     if dh.dim() != 2:
         raise ValueError("dh must be [m, n]")
-    m, n = dh.shape
-    _activations(gate, "gate", (m, n), like=dh)
-    _activations(up, "up", (m, n), like=dh)
-    for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
-        _require_cuda(t, name, torch.uint8)
-        _same_device(t, name, dh)
-    dx = torch.empty((m, k), dtype=dh.dtype, device=dh.device)
+    m, n = shape = dh.shape
+    dev = dh.get_device()
+    if not (_fits(dev, bf16, gate, up) and gate.shape == shape == up.shape
+            and _fits(dev, u8, w_gate, w_up)):
+        _need_like(dh, gate=(bf16, shape, gate), up=(bf16, shape, up),
+                   w_gate=(u8, None, w_gate), w_up=(u8, None, w_up))
+    dx = torch.empty((m, k), dtype=bf16, device=dh.device)
     dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
-    p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, DTYPE_BF16, _ACTS[act])
-    lib = _lib if _lib is not None else load()
-    need = lib.q2k_gated_ffn_backward_workspace_bytes(ctypes.byref(p))
-    _keep, ws, ws_bytes = _workspace(workspace, need, dh)
-    with _on_device(dh):
-        _check(lib, lib.q2k_gated_ffn_backward(dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
-                                               dh.numel(), w_gate.data_ptr(), w_gate.numel(),
-                                               w_up.data_ptr(), w_up.numel(), dx.data_ptr(),
-                                               dx.numel(), dgate.data_ptr(), dup.data_ptr(),
-                                               ctypes.byref(p), ws, ws_bytes, _stream_handle(dh)))
+    key = ("backward", "auto", bf16, m, n, k, act)
+    params, need, _ = _ffn_plans.get(key) or _ffn_plan(key)
+    # (with dgate and dup given, rows of whole 16 bytes need no copy of them)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, 0 if n % 8 == 0 else need, dh)
+    _ffn_call(dev, _lib.q2k_gated_ffn_backward, dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
+              m * n, w_gate.data_ptr(), w_gate.numel(), w_up.data_ptr(), w_up.numel(),
+              dx.data_ptr(), m * k, dgate.data_ptr(), dup.data_ptr(), params, ws, ws_bytes)
     return dx, dgate, dup
 
 
@@ -801,48 +845,36 @@ def matmul_lora(x, w, n: int, lora_a, lora_b, ids, scales=None, out=None, path="
     ``(out, bad_id_count)`` without waiting (such a token's row is zero).
     ``path``, ``const_weights`` and ``workspace`` as in ``gated_ffn``.
     """
-    torch = _torch()
-    dtype = _activations(x, "x")
+    torch = _torch_mod or _torch()
+    _need_activations(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [m, k]")
     m, k = x.shape
-    _require_cuda(w, "w", torch.uint8)
-    _require_cuda(lora_a, "lora_a", torch.bfloat16)
-    _require_cuda(lora_b, "lora_b", torch.bfloat16)
-    _require_cuda(ids, "ids", torch.int32)
-    if lora_a.dim() != 3 or lora_a.shape[2] != k:
-        raise ValueError(f"lora_a must be [n_adapters, rank, {k}], got {list(lora_a.shape)}")
-    n_adapters, rank = lora_a.shape[:2]
-    if tuple(lora_b.shape) != (n_adapters, n, rank):
-        raise ValueError(f"lora_b must be {[n_adapters, n, rank]}, got {list(lora_b.shape)}")
-    if tuple(ids.shape) != (m,):
-        raise ValueError(f"ids must be [{m}], got {list(ids.shape)}")
+    bf16, dt, dev = torch.bfloat16, x.dtype, x.get_device()
+    if not isinstance(lora_a, torch.Tensor) or lora_a.dim() != 3:
+        raise ValueError("lora_a must be [n_adapters, rank, k]")
+    n_adapters, rank, _ = lora_a.shape
+    if not (_fits(dev, bf16, lora_a, lora_b) and lora_a.shape == (n_adapters, rank, k)
+            and lora_b.shape == (n_adapters, n, rank) and _fits(dev, torch.int32, ids)
+            and ids.shape == (m,) and _fits(dev, torch.uint8, w)):
+        _need_like(x, w=(torch.uint8, None, w), lora_a=(bf16, (n_adapters, rank, k), lora_a),
+                   lora_b=(bf16, (n_adapters, n, rank), lora_b), ids=(torch.int32, (m,), ids))
     if scales is not None:
-        _require_cuda(scales, "scales", torch.float32)
-        if tuple(scales.shape) != (n_adapters,):
-            raise ValueError(f"scales must be [{n_adapters}], got {list(scales.shape)}")
-    for t, name in ((w, "w"), (lora_a, "lora_a"), (lora_b, "lora_b"), (ids, "ids"),
-                    (scales, "scales")):
-        if t is not None:
-            _same_device(t, name, x)
+        if not (_fits(dev, torch.float32, scales) and scales.shape == (n_adapters,)):
+            _need_like(x, scales=(torch.float32, (n_adapters,), scales))
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    _activations(out, "out", (m, n), like=x)
+        out = torch.empty((m, n), dtype=dt, device=x.device)
+    else:
+        _need_like(x, out=(dt, (m, n), out))
     bad = torch.empty(1, dtype=torch.int32, device=x.device)
-    p = LoraParams(m, n, k, GGML_TYPE_Q2_K, dtype, rank, n_adapters, 0)
-    lib = _lib if _lib is not None else load()
-    pcode = _PATHS[path]
-    need = lib.q2k_matmul_lora_workspace_bytes(pcode, ctypes.byref(p))
-    _keep, ws, ws_bytes = _workspace(workspace, need, x)
-    with _on_device(x):
-        _check(lib, lib.q2k_matmul_lora(pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
-                                        x.data_ptr(), x.numel(), w.data_ptr(), w.numel(),
-                                        lora_a.data_ptr(), lora_a.numel(), lora_b.data_ptr(),
-                                        lora_b.numel(),
-                                        scales.data_ptr() if scales is not None else None,
-                                        ids.data_ptr(), out.data_ptr(), out.numel(),
-                                        ctypes.byref(p), bad.data_ptr(), ws, ws_bytes,
-                                        _stream_handle(x)))
+    key = ("lora", path, dt, m, n, k, rank, n_adapters)
+    params, need, pcode = _ffn_plans.get(key) or _ffn_plan(key)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, need, x)
+    _ffn_call(dev, _lib.q2k_matmul_lora, pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
+              x.data_ptr(), m * k, w.data_ptr(), w.numel(), lora_a.data_ptr(),
+              lora_a.numel(), lora_b.data_ptr(), lora_b.numel(),
+              scales.data_ptr() if scales is not None else None, ids.data_ptr(), out.data_ptr(),
+              m * n, params, bad.data_ptr(), ws, ws_bytes)
     if not check:
         return out, bad
     n_bad = int(bad.item())

@@ -1185,6 +1185,7 @@ q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* 
         return fail(Q2K_ERR_INVALID_ARGUMENT,
                     "dh, gate, up, dx, dgate and dup must be 16-byte aligned");
     q2k::GatedBackwardArgs a = gated_backward_args(p);
+    a.dgate = static_cast<__nv_bfloat16*>(dgate);
     const size_t need = q2k::gated_backward_workspace_bytes(a);
     if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
     const size_t mn_bytes = s.mn * 2, save_bytes = dgate != nullptr ? mn_bytes : 0;

@@ -37,6 +37,9 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
 // ((1 + tanh y) / 2 = 1 / (1 + e^-2y), so the tanh form is a logistic too.)
 // For the tanh form g is held to |g| <= 30 inside z and z', where p is 0 or 1
 // to f32 already: no power of g overflows, and 0 * inf does not arise.
+// kFast: e^-z and the quotient by the short instruction sequences, a few units
+// in the last place of f32 each; for results that are rounded to bf16.
+template <bool kFast>
 __device__ __forceinline__ void act_logistic(float g, int act, float& p, float& dz) {
     constexpr float kC = 1.5957691216057308f;  // 2 sqrt(2/pi)
     float z = g;
@@ -46,16 +49,18 @@ __device__ __forceinline__ void act_logistic(float g, int act, float& p, float& 
         z = kC * (c + 0.044715f * c * c * c);
         dz = kC * (1.0f + 3.0f * 0.044715f * c * c);
     }
-    p = 1.0f / (1.0f + expf(-z));
+    p = kFast ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
 }
+template <bool kFast>
 __device__ __forceinline__ float act_value(float g, int act) {
     float p, dz;
-    act_logistic(g, act, p, dz);
+    act_logistic<kFast>(g, act, p, dz);
     return g * p;
 }
+template <bool kFast>
 __device__ __forceinline__ void act_value_slope(float g, int act, float& value, float& slope) {
     float p, dz;
-    act_logistic(g, act, p, dz);
+    act_logistic<kFast>(g, act, p, dz);
     value = g * p;
     slope = p + g * (1.0f - p) * p * dz;
 }

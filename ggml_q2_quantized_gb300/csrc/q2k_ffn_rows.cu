@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                     if (kMode == Rows::kGated) {
                         if (n >= p.N) continue;
                         const size_t at = static_cast<size_t>(m) * p.N + n;
-                        static_cast<T*>(p.h)[at] = from_float<T>(act_value(v[0], p.act) * v[1]);
+                        static_cast<T*>(p.h)[at] = from_float<T>(act_value<!kSplit>(v[0], p.act) * v[1]);
                         if (p.gate != nullptr) {
                             static_cast<T*>(p.gate)[at] = from_float<T>(v[0]);
                             static_cast<T*>(p.up)[at] = from_float<T>(v[1]);

@@ -90,19 +90,25 @@ constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memor
 
 enum class Tc { kGated, kLora, kBackward };
 
-// Tiles of kX tokens.  256: one accumulator, one thread issues the MMAs.  128
-// and fewer: narrow MMAs issue at half the rate the tensor core takes them, so
-// two threads issue, each into its own accumulator; the token ring and the A
-// ring are equally deep then, and one release serves a pair of stages of both.
+// Tiles of kX tokens.
+// 256: two CTAs of a cluster (neighbouring row tiles) form one MMA of 256 rows
+// x 256 tokens, issued by one thread of the first (cta_group::2).  Each holds
+// half of the tokens' stage, so a stage is half as large and crosses from L2
+// once per pair, and its ring is twice as deep in time.
+// 128 and fewer: narrow MMAs issue at half the rate the tensor core takes them,
+// so two threads issue, each into its own accumulator; the token ring and the A
+// ring are equally deep then, and one release serves two stages of both.
 template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
-    static constexpr int kIssuers = kX == 256 ? 1 : 2;
-    static constexpr int kHand = kX == 256 || kBack ? 2 : 4;  // stages handed over at a time
-    static constexpr bool kPairs = kIssuers == 2;    // stages released in pairs
-    static constexpr int kXStage = kX * kStageK * 2;
-    static constexpr int kXStages = kBack ? (kX == 256 ? 4 : kX == 128 ? 6 : 8) : kX == 256 ? 6 : 8;
-    static constexpr int kAStages = kBack ? kXStages : 8;
+    static constexpr bool kDuo = kX == 256;
+    static constexpr int kIssuers = kDuo ? 1 : 2;
+    static constexpr int kHand = kDuo || kBack ? 2 : 4;  // stages handed over at a time
+    static constexpr bool kPairs = kIssuers == 2;        // stages released two at a time
+    static constexpr int kHold = kDuo ? kX / 2 : kX;     // tokens of a stage in this CTA
+    static constexpr int kXStage = kHold * kStageK * 2;
+    static constexpr int kXStages = kDuo ? (kBack ? 8 : 12) : kBack && kX == 128 ? 6 : 8;
+    static constexpr int kAStages = kBack ? (kDuo ? 4 : kXStages) : 8;
     // decoders: groups of warps on stages (backward) or block halves in turn
     static constexpr int kGroupWarps = kBack ? 4 : 8;
     static constexpr uint32_t kColA = kX * kIssuers;
@@ -116,9 +122,9 @@ struct Cfg {
     // backward: decoded stages in shared memory, 64 weight rows x 128 columns
     static constexpr int kOffA = kXStages * kXStage;
     static constexpr int kOffRaw = kOffA + (kBack ? kAStages * kABytes : 0);
-    // bars: x_full, x_empty [kXStages], a_full, a_empty [kAStages], raw_full,
-    //       raw_empty [kRaw], accum, drain
-    static constexpr int kNumBars = 2 * kXStages + 2 * kAStages + 2 * kRaw + 2;
+    // bars: x_full, x_empty [kXStages], a_full, a_empty, peer_full [kAStages],
+    //       raw_full, raw_empty [kRaw], accum, drain
+    static constexpr int kNumBars = 2 * kXStages + 3 * kAStages + 2 * kRaw + 2;
     static constexpr int kOffBar = (kOffRaw + kRaw * kRawBytes + 7) & ~7;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
@@ -375,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     using C = Cfg<kX, kTma, kMode>;
     constexpr bool kBack = kMode == Tc::kBackward;
+    constexpr bool kDuo = C::kDuo;
     constexpr int kSplit0 = kMode == Tc::kGated ? kRows / 2 : kRows;  // tile rows of w0
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -385,7 +392,11 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     const int rows = kBack ? p.K : p.N;   // rows of the product
     const int m0 = blockIdx.y * kX;
     const int tokens = min(kX, p.M - m0);
-    const int nx = (tokens + 15) & ~15;  // MMA N
+    const int nx = kDuo ? (tokens + 31) & ~31 : (tokens + 15) & ~15;  // MMA N
+    // two CTAs: this one holds tokens [peer nx / 2, peer nx / 2 + nx / 2)
+    const int peer = kDuo ? static_cast<int>(blockIdx.x & 1) : 0;
+    const int held = kDuo ? nx / 2 : nx;
+    const int m_held = m0 + peer * held;
     // K parts in whole blocks (backward: four stages, 256 weight rows)
     const int parts = gridDim.z, quads = p.stages / 4;
     const int q0 = static_cast<int>(static_cast<long>(blockIdx.z) * quads / parts);
@@ -396,7 +407,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     const uint32_t bar_xempty = bar_xfull + 8 * C::kXStages;
     const uint32_t bar_afull = bar_xempty + 8 * C::kXStages;
     const uint32_t bar_aempty = bar_afull + 8 * C::kAStages;
-    const uint32_t bar_raw = bar_aempty + 8 * C::kAStages;
+    const uint32_t bar_peer = bar_aempty + 8 * C::kAStages;  // (of the first CTA)
+    const uint32_t bar_raw = bar_peer + 8 * C::kAStages;
     const uint32_t bar_rawempty = bar_raw + 8 * C::kRaw;
     const uint32_t bar_accum = bar_rawempty + 8 * C::kRaw;
     const uint32_t bar_drain = bar_accum + 8;
@@ -412,6 +424,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         for (int s = lane; s < C::kAStages; s += 32) {
             mbar_init(bar_afull + 8 * s, C::kGroupWarps);  // the warps of its group
             mbar_init(bar_aempty + 8 * s, C::kPairs ? C::kIssuers : 1);
+            mbar_init(bar_peer + 8 * s, 1);  // the second CTA's waiter
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
@@ -424,9 +437,10 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc<kDuo>(smem_u32(tmem_slot), C::kTmemCols);
     fence_before();
-    __syncthreads();
+    if (kDuo) cluster_sync();  // the other CTA's barriers are set up
+    else __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
     float* sums = reinterpret_cast<float*>(smem);  // token c, row r at word 128 c + r
@@ -613,14 +627,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     if (c0 + q < tokens) sums[(c0 + q) * kRows + row] = v[q];
             }
         }
-    } else if (warp == kMmaWarp || (C::kIssuers == 2 && warp == kWaitWarp)) {
+    } else if ((warp == kMmaWarp && peer == 0) || (C::kIssuers == 2 && warp == kWaitWarp)) {
         // ---------------- MMA issuers ----------------
         // The waiter waits for the next kHand stages and meets the MMA warp at
         // named barrier 1; both pass it n_iters / kHand times whatever happens.
         // With two issuers the MMA warp takes the even stages into accumulator
         // 0, the waiter the odd ones into accumulator 1.
         const int me = warp == kMmaWarp ? 0 : 1;
-        const uint32_t idesc = bf16_idesc(nx) | (kBack ? kIdescAMnMajor : 0u);
+        const uint32_t idesc = bf16_idesc(kDuo ? 2 * kRows : kRows, nx) | (kBack ? kIdescAMnMajor : 0u);
         const uint64_t xdesc0 = sw128_desc(sbase);
         const uint64_t adesc0 = sw128_mn_desc(sbase + C::kOffA, 8192);
         const uint32_t acc = tmem + static_cast<uint32_t>(me * kX);
@@ -652,17 +666,17 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     for (int kk = 0; kk < kStageK / 16; ++kk) {
                         const uint32_t add = i >= C::kIssuers || kk > 0;
                         if (kBack)  // (a K-step is 16 rows of 128 bytes)
-                            mma_smem(acc, adesc + 128u * kk, xdesc + 2u * kk, idesc, add);
+                            mma_smem<kDuo>(acc, adesc + 128u * kk, xdesc + 2u * kk, idesc, add);
                         else
-                            mma(acc, a_s + 8u * kk, xdesc + 2u * kk, idesc, add);
+                            mma<kDuo>(acc, a_s + 8u * kk, xdesc + 2u * kk, idesc, add);
                     }
                     // a stage is released when a later one takes its place
                     if (C::kPairs) {
                         if ((i & ~1) + C::kAStages < n_iters)
-                            commit(bar_aempty + 8 * ((i | 1) % C::kAStages));
+                            commit<kDuo>(bar_aempty + 8 * ((i | 1) % C::kAStages));
                     } else {
-                        if (i + C::kAStages < n_iters) commit(bar_aempty + 8 * sa);
-                        commit(bar_xempty + 8 * sx);
+                        if (i + C::kAStages < n_iters) commit<kDuo>(bar_aempty + 8 * sa);
+                        if (i + C::kXStages < n_iters) commit<kDuo>(bar_xempty + 8 * sx);
                     }
                 }
             }
@@ -670,31 +684,41 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         }
         if (lane == 0) {
             if (!*abort_flag) {
-                commit(bar_accum);
+                commit<kDuo>(bar_accum);
             } else {
                 // no MMA may still write TMEM when it is freed
-                commit(bar_drain);
+                commit<kDuo>(bar_drain);
                 volatile int no_abort = 0;
                 mbar_wait_bounded(bar_drain, 0, &no_abort, err, kErrTimeoutDrain);
             }
         }
         __syncwarp();
-    } else if (warp == kWaitWarp) {
-        // ---------------- stage waiter of a single issuer ----------------
+    } else if (kDuo && warp == kWaitWarp) {
+        // ---------------- stage waiters of a pair of CTAs ----------------
+        // The second CTA's waiter reports each of its stages to the first's,
+        // which waits for both CTAs' and hands them to the MMA warp.
         for (int i0 = 0; i0 < n_iters; i0 += C::kHand) {
             if (lane == 0 && !*abort_flag) {
 #pragma unroll
                 for (int u = 0; u < C::kHand; ++u) {
-                    const int i = i0 + u;
+                    const int i = i0 + u, sa = i % C::kAStages;
+                    const uint32_t phase = (i / C::kAStages) & 1;
                     if (!mbar_wait_bounded(bar_xfull + 8 * (i % C::kXStages), (i / C::kXStages) & 1,
                                            abort_flag, err, kErrTimeoutFull) ||
-                        !mbar_wait_bounded(bar_afull + 8 * (i % C::kAStages), (i / C::kAStages) & 1,
-                                           abort_flag, err, kErrTimeoutFull))
+                        !mbar_wait_bounded(bar_afull + 8 * sa, phase, abort_flag, err, kErrTimeoutFull))
                         break;
+                    if (peer == 1) {
+                        fence_after();
+                        fence_before();
+                        arrive_first_of_pair(bar_peer + 8 * sa);
+                    } else if (!wait_peer_bounded(bar_peer + 8 * sa, phase, abort_flag, err,
+                                                  kErrTimeoutFull)) {
+                        break;
+                    }
                 }
             }
             __syncwarp();
-            asm volatile("bar.sync 1, 64;" ::: "memory");
+            if (peer == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
         }
     } else if (warp == kWWarp) {
         // ---------------- raw weight blocks ----------------
@@ -727,14 +751,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             if (*abort_flag) linger();
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kXWarp0) {
         // ---------------- token stages, even and odd ----------------
         if (lane == 0) {
             const uint8_t* src = p.xa +
                                  (static_cast<size_t>(m0 / kSuperRows) * p.stages + 4 * q0) *
                                      kSuperBytes +
-                                 static_cast<size_t>(m0 % kSuperRows) * (kStageK * 2);
-            const uint32_t bytes = p.xa != nullptr ? nx * (kStageK * 2) : C::kXStage;
+                                 static_cast<size_t>(m_held % kSuperRows) * (kStageK * 2);
+            const uint32_t bytes = p.xa != nullptr ? held * (kStageK * 2) : C::kXStage;
             if (p.xa == nullptr) {
                 tma_prefetch_map(&maps.x0);
                 if (kBack) tma_prefetch_map(&maps.x1);
@@ -759,7 +783,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     const int stage = 4 * q0 + i;
                     const bool up = kBack && stage >= p.half_stages;
                     tma_load_2d(dst, up ? &maps.x1 : &maps.x0,
-                                kStageK * (up ? stage - p.half_stages : stage), m0, bar);
+                                kStageK * (up ? stage - p.half_stages : stage), m_held, bar);
                 }
             }
             if (*abort_flag) linger();
@@ -773,7 +797,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     // groups of eight) and adds them over the parts in order; the second
     // cluster barrier keeps every part's sums alive until all are read.
     int first = 0, end = tokens;
-    if (parts > 1) {
+    if (parts > 1) {  // (cluster rank: row tile of the pair + 2 part, or the part)
         const int groups = (tokens + 7) / 8, z = blockIdx.z;
         first = 8 * (z * groups / parts);
         end = min(tokens, 8 * ((z + 1) * groups / parts));
@@ -789,7 +813,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             float4 v[kMaxParts];
 #pragma unroll
             for (int z = 0; z < kMaxParts; ++z)
-                if (z < parts) v[z] = load_cluster4(sbase + 16 * i, z);
+                if (z < parts) v[z] = load_cluster4(sbase + 16 * i, kDuo ? 2 * z + peer : z);
             float4 a = v[0];
 #pragma unroll
             for (int z = 1; z < kMaxParts; ++z)
@@ -815,8 +839,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 const int valid = rows - n;
                 if (valid <= 0) continue;
                 const size_t at = static_cast<size_t>(m0 + c) * rows + n;
-                store_pair(static_cast<T*>(p.h) + at, act_value(g.x, p.act) * u.x,
-                           act_value(g.y, p.act) * u.y, valid, vec);
+                store_pair(static_cast<T*>(p.h) + at, act_value<sizeof(T) == 2>(g.x, p.act) * u.x,
+                           act_value<sizeof(T) == 2>(g.y, p.act) * u.y, valid, vec);
                 if (p.gate != nullptr) {
                     store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
                     store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
@@ -840,15 +864,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 }
         }
     }
-    if (parts > 1) {
-        __syncwarp();
-        cluster_sync();
-    }
     fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (kDuo || parts > 1) cluster_sync();
+    else __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
-        tmem_free(tmem, C::kTmemCols);
+        tmem_free<kDuo>(tmem, C::kTmemCols);
     }
 }
 
@@ -923,7 +945,7 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float value, slope;
-            act_value_slope(to_float(g[e]), act, value, slope);
+            act_value_slope<true>(to_float(g[e]), act, value, slope);
             a[e] = __float2bfloat16_rn(to_float(h[e]) * to_float(u[e]) * slope);
             b[e] = __float2bfloat16_rn(to_float(h[e]) * value);
         }
@@ -959,10 +981,12 @@ Plan make_plan(int M, int rows, int tile_rows, int quads) {
         Plan p;
         p.x_rows = x_rows;
         p.row_tiles = (rows + tile_rows - 1) / tile_rows;
+        if (x_rows == 256) p.row_tiles += p.row_tiles & 1;  // pairs
         p.token_tiles = (M + x_rows - 1) / x_rows;
         const long tiles = static_cast<long>(p.row_tiles) * p.token_tiles;
         p.parts = static_cast<int>(
-            std::max(1L, std::min<long>(std::min(kMaxParts, quads), kPlanSms / tiles)));
+            std::max(1L, std::min<long>(std::min(x_rows == 256 ? kMaxParts / 2 : kMaxParts, quads),
+                                        kPlanSms / tiles)));
         const long waves = (tiles * p.parts + kPlanSms - 1) / kPlanSms;
         const double stages = 4.0 * quads / p.parts;
         const double cost = waves * (stages + kTileStages) * (x_rows == 256 ? 1.0 : 0.7);
@@ -1012,9 +1036,9 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (plan.parts > 1) {
+    if (C::kDuo || plan.parts > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.x = C::kDuo ? 2 : 1;
         attr[1].val.clusterDim.y = 1;
         attr[1].val.clusterDim.z = static_cast<unsigned>(plan.parts);
         cfg.numAttrs = 2;
@@ -1032,9 +1056,10 @@ cudaError_t launch_tc(const TcArgs& a, const Plan& plan, const void* x0, const v
     const int rows = kMode == Tc::kLora ? kRows : 64;
     const bool tma = make_weight_map(&maps.w0, a.w0, a.N, a.K, rows) &&
                      (kMode == Tc::kLora || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows));
+    const int held = std::min(plan.x_rows, 128);  // tokens of a stage in one CTA
     if (a.xa == nullptr &&
-        (!make_token_map(&maps.x0, x0, a.M, x_cols, x_pitch, plan.x_rows) ||
-         (kMode == Tc::kBackward && !make_token_map(&maps.x1, x1, a.M, x_cols, x_pitch, plan.x_rows))))
+        (!make_token_map(&maps.x0, x0, a.M, x_cols, x_pitch, held) ||
+         (kMode == Tc::kBackward && !make_token_map(&maps.x1, x1, a.M, x_cols, x_pitch, held))))
         return cudaErrorNotSupported;
 #define Q2K_TC_CASE(X)                                                              \
     case X:                                                                         \
@@ -1127,17 +1152,23 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, c
 }
 
 // Workspace: dg and du, unless the caller takes them in rows of whole 16 bytes.
+static bool backward_in_place(const GatedBackwardArgs& a) {
+    return a.dgate != nullptr && backward_pitch(a.N) == a.N;
+}
+static size_t backward_matrix_bytes(const GatedBackwardArgs& a) {
+    return (static_cast<size_t>(a.M) * backward_pitch(a.N) * 2 + 255) & ~size_t(255);
+}
 size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
-    return 2 * ((static_cast<size_t>(a.M) * backward_pitch(a.N) * 2 + 255) & ~size_t(255));
+    return backward_in_place(a) ? 0 : 2 * backward_matrix_bytes(a);
 }
 
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream) {
     const int pitch = backward_pitch(a.N), cols = backward_cols(a.N);
-    const bool own = a.dgate != nullptr && pitch == a.N;
+    const bool own = backward_in_place(a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(ws);
     __nv_bfloat16* du = own ? a.dup
-                            : reinterpret_cast<__nv_bfloat16*>(ws + gated_backward_workspace_bytes(a) / 2);
+                            : reinterpret_cast<__nv_bfloat16*>(ws + backward_matrix_bytes(a));
     const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
     const unsigned blocks =
         static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));

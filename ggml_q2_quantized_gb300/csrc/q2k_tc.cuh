@@ -12,7 +12,7 @@
 namespace q2k {
 namespace tc {
 
-constexpr int kRows = 128;             // rows of an MMA tile = TMEM lanes
+constexpr int kRows = 128;             // rows of a CTA's tile = TMEM lanes
 constexpr int kStageK = 64;            // K elements per stage: one 128-byte swizzle row
 constexpr int kBoxBytes = 112;         // bytes per row of a raw-weight TMA box
 // bf16 tile image of a [rows, K] matrix: super-tiles of 256 rows x 64 K (32 KB,
@@ -29,15 +29,30 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// Tensor memory, MMAs and commits come in two forms: of one CTA, or (kDuo) of a
+// pair of CTAs whose cluster ranks differ in the lowest bit (cta_group::2).
+template <bool kDuo>
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (kDuo) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
+template <bool kDuo>
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
-                 : "memory");
+    if constexpr (kDuo)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                     : "memory");
 }
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
@@ -54,32 +69,97 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t mn_st
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 constexpr uint32_t kIdescAMnMajor = 1u << 15;
-// Instruction descriptor, kind::f16: D f32, A and B bf16, both K-major, M = 128.
-__device__ __forceinline__ uint32_t bf16_idesc(int n) {
+// Instruction descriptor, kind::f16: D f32, A and B bf16, both K-major.
+__device__ __forceinline__ uint32_t bf16_idesc(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(kRows >> 4) << 24);
+           (static_cast<uint32_t>(m >> 4) << 24);
 }
-// D[tmem_d] (+)= A[tmem_a] * B[bdesc]^T, A in tensor memory.
+// D[tmem_d] (+)= A[tmem_a] * B[bdesc]^T, A in tensor memory.  A pair's MMA takes
+// its rows, and half of its columns' B, from the same places of both CTAs.
+template <bool kDuo>
 __device__ __forceinline__ void mma(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
                                     uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (kDuo)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 // The same with A in shared memory.
+template <bool kDuo>
 __device__ __forceinline__ void mma_smem(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (kDuo)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Arrive at `bar` (of a pair: in both CTAs) when this thread's MMAs are done.
+template <bool kDuo>
 __device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (kDuo) {
+        const uint16_t both = static_cast<uint16_t>(3u << (cluster_rank() & ~1u));
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;" ::"r"(bar), "h"(both)
+            : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+    }
+}
+// As mbar_wait_bounded, for a barrier that another CTA of the cluster arrives at.
+__device__ __forceinline__ bool wait_peer_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  unsigned int* err, uint32_t err_bit) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (it == 1) t0 = global_timer_ns();
+        if ((it & 7u) == 0u) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > 1000000000ull) {
+                atomicOr(err, err_bit);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+// Arrive at the first CTA's barrier at this CTA's address `bar`.
+__device__ __forceinline__ void arrive_first_of_pair(uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}"
+        ::"r"(bar), "r"(cluster_rank() & ~1u)
         : "memory");
 }
 // Eight consecutive 32-bit columns of this thread's TMEM lane.

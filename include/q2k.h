@@ -573,7 +573,9 @@ size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params *
  *   dh, gate, up  [m, n] each (h_elems elements each)
  *   dx            [m, k]; fully overwritten
  *   dgate, dup    [m, n] each, both or neither NULL (e.g. for the gradients of
- *                 adapters on the two projections) */
+ *                 adapters on the two projections)
+ * The workspace holds dgate and dup as the product reads them; with both given
+ * and n a multiple of 8 it is not needed (NULL). */
 q2k_status q2k_gated_ffn_backward(const void *dh, const void *gate, const void *up,
                                   size_t h_elems, const void *w_gate, size_t w_gate_bytes,
                                   const void *w_up, size_t w_up_bytes, void *dx, size_t dx_elems,
