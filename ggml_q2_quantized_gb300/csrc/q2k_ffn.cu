@@ -20,16 +20,17 @@ namespace {
 
 // ---- t = s_a A_a x ---------------------------------------------------------------
 //
-// One cluster of eight CTAs takes one adapter's rows (64 at most) and the
-// tokens with that adapter among eight or 32 consecutive ones: A_a's rows are
-// the MMA's rows, eight tokens its columns, and the cluster's 64 warps divide K,
-// so that even one token's A_a (128 KB at rank 16, K = 4096) is read by eight
-// SMs at once.  Sums meet in shared memory, then over the cluster, in a fixed
-// order.  A token takes only its own adapter's column.  An f32 x is three bf16
-// parts (24 bits).
+// One cluster of eight CTAs takes 16 of an adapter's rows and the tokens with
+// that adapter among eight or 32 consecutive ones: A_a's rows are the MMA's rows,
+// eight tokens its columns, and the cluster's 64 warps divide K, so that even one
+// token's A_a (128 KB at rank 16, K = 4096) is read by eight SMs at once.  Sums
+// meet in shared memory, then over the cluster, in a fixed order.  A token takes
+// only its own adapter's column.  An f32 x is three bf16 parts (24 bits).  The
+// time is the latency of a few dependent loads: a warp asks for four of its
+// K-steps at once.
 constexpr int kShrinkWarps = 8;
 constexpr int kShrinkCtas = 8;
-constexpr int kShrinkRows = 64;
+constexpr int kShrinkRows = 16;
 // Up to this many tokens a cluster is launched per token, and the first token
 // with an adapter among its eight does the work: eight tokens with eight
 // adapters then run at once.  Above, a cluster takes 32 tokens and loops over
@@ -85,23 +86,24 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
                    const float* __restrict__ scales, const int* __restrict__ ids,
                    float* __restrict__ t, unsigned int* __restrict__ bad_ids, int M, int K, int R,
                    int n_adapters) {
-    __shared__ float red[kShrinkWarps][16][32];
-    __shared__ float part[kGroups * 16 * 32];
+    constexpr int kSums = kGroups * 4 * 32;  // of a warp: groups x fragment x lanes
+    __shared__ float red[kShrinkWarps][kSums];
+    __shared__ float part[kSums];
     pdl_allow_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.z;  // = the rank in the cluster
-    if (blockIdx.x == 0 && blockIdx.y == 0 && rank == 0 && warp == 0) {
-        unsigned int bad = 0;
-        for (int c = lane; c < M; c += 32) bad += ids[c] < -1 || ids[c] >= n_adapters;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) bad += __shfl_xor_sync(0xFFFFFFFFu, bad, o);
-        if (lane == 0) *bad_ids = bad;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && rank == kShrinkCtas - 1) {
+        int bad = 0;
+        for (int c0 = 0; c0 < M; c0 += kShrinkWarps * 32) {
+            const int id = c0 + tid < M ? ids[c0 + tid] : -1;
+            bad += __syncthreads_count(id < -1 || id >= n_adapters);
+        }
+        if (tid == 0) *bad_ids = static_cast<unsigned>(bad);
     }
     const int g = lane >> 2, q4 = lane & 3;
     const int block = static_cast<int>(blockIdx.x);
     const int m0 = kGroups == 1 ? block & ~7 : 8 * kGroups * block;
     const int r0 = blockIdx.y * kShrinkRows;
-    const int tiles = min(kShrinkRows / 16, (R - r0 + 15) / 16);
     int id[kGroups];  // of this lane's column in each group; -1 once done
 #pragma unroll
     for (int n = 0; n < kGroups; ++n) {
@@ -129,70 +131,77 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
             if (mine[n]) id[n] = -1;
         }
         if (kGroups == 1 && token != block) continue;
-        float acc[4][kGroups][4] = {};
+        float acc[kGroups][4] = {};
+        const bool ok0 = r0 + g < R, ok1 = r0 + g + 8 < R;
         const __nv_bfloat16* arow = a + (static_cast<size_t>(ad) * R + r0 + g) * K + 8 * q4;
-        for (int k = 32 * (rank * kShrinkWarps + warp); k < K; k += 32 * kShrinkWarps * kShrinkCtas) {
-            uint4 lo[4], hi[4];
+        const T* xrow[kGroups];
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                lo[rt] = hi[rt] = make_uint4(0u, 0u, 0u, 0u);
-                if (r0 + 16 * rt + g < R)
-                    lo[rt] = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt) * K + k));
-                if (r0 + 16 * rt + 8 + g < R)
-                    hi[rt] = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(16 * rt + 8) * K + k));
-            }
+        for (int n = 0; n < kGroups; ++n)
+            xrow[n] = x + static_cast<size_t>(mine[n] ? m0 + 8 * n + g : 0) * K + 8 * q4;
+        constexpr int kStep = 32 * kShrinkWarps * kShrinkCtas;
+        constexpr int kAhead = kGroups == 1 ? 4 : 2;
+        for (int k0 = 32 * (rank * kShrinkWarps + warp); k0 < K; k0 += kAhead * kStep) {
+            uint4 lo[kAhead], hi[kAhead];
+            XParts<T> xp[kAhead][kGroups];
 #pragma unroll
-            for (int n = 0; n < kGroups; ++n) {
-                XParts<T> xp;
-                if (mine[n]) xp.load(x + static_cast<size_t>(m0 + 8 * n + g) * K + 8 * q4 + k);
-                else xp.zero();
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = k0 + u * kStep;
+                lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (k < K && ok0) lo[u] = __ldg(reinterpret_cast<const uint4*>(arow + k));
+                if (k < K && ok1)
+                    hi[u] = __ldg(reinterpret_cast<const uint4*>(arow + static_cast<size_t>(8) * K + k));
 #pragma unroll
-                for (int rt = 0; rt < 4; ++rt) {
-                    if (rt >= tiles) break;
-#pragma unroll
-                    for (int p = XParts<T>::kParts - 1; p >= 0; --p) {
-                        mma_bf16_16816(acc[rt][n], lo[rt].x, hi[rt].x, lo[rt].y, hi[rt].y, xp.v[p][0], xp.v[p][1]);
-                        mma_bf16_16816(acc[rt][n], lo[rt].z, hi[rt].z, lo[rt].w, hi[rt].w, xp.v[p][2], xp.v[p][3]);
-                    }
+                for (int n = 0; n < kGroups; ++n) {
+                    if (k < K && mine[n]) xp[u][n].load(xrow[n] + k);
+                    else xp[u][n].zero();
                 }
             }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+                    for (int p = XParts<T>::kParts - 1; p >= 0; --p) {
+                        const auto& v = xp[u][n].v[p];
+                        mma_bf16_16816(acc[n], lo[u].x, hi[u].x, lo[u].y, hi[u].y, v[0], v[1]);
+                        mma_bf16_16816(acc[n], lo[u].z, hi[u].z, lo[u].w, hi[u].w, v[2], v[3]);
+                    }
         }
 #pragma unroll
-        for (int n = 0; n < kGroups; ++n) {
+        for (int n = 0; n < kGroups; ++n)
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt)
+            for (int c = 0; c < 4; ++c) red[warp][(4 * n + c) * 32 + lane] = acc[n][c];
+        __syncthreads();
+        for (int i = tid; i < kSums; i += kShrinkWarps * 32) {
+            float v = 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) red[warp][4 * rt + c][lane] = acc[rt][n][c];
-            __syncthreads();
-            for (int i = tid; i < 16 * 32; i += kShrinkWarps * 32) {
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kShrinkWarps; ++w) v += red[w][i >> 5][i & 31];
-                part[512 * n + i] = v;
-            }
-            if (n + 1 < kGroups) __syncthreads();
+            for (int w = 0; w < kShrinkWarps; ++w) v += red[w][i];
+            part[i] = v;
         }
         cluster_sync();
         // each CTA of the cluster adds an eighth of the values over the CTAs
-        constexpr int kEach = kGroups * 16 * 32 / kShrinkCtas;
+        constexpr int kEach = kSums / kShrinkCtas;
         if (tid < kEach) {
             const int i = rank * kEach + tid;
             const uint32_t at = smem_u32(part + i);
-            float v = 0.f;
+            float v[kShrinkCtas];
 #pragma unroll
-            for (int c = 0; c < kShrinkCtas; ++c) {
-                uint32_t addr;
-                float u;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(at), "r"(c));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(addr) : "memory");
-                v += u;
-            }
-            // value f of lane l: row 16 (f / 4) + l / 4 + 8 (f / 2 % 2), column 2 (l % 4) + f % 2
-            const int f = (i >> 5) & 15, l = i & 31;
-            const int r = r0 + 16 * (f >> 2) + (l >> 2) + 8 * ((f >> 1) & 1);
-            const int col = m0 + 8 * (i >> 9) + 2 * (l & 3) + (f & 1);
+            for (int c = 0; c < kShrinkCtas; ++c)
+                asm volatile(
+                    "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+                    "ld.shared::cluster.f32 %0, [ra];\n\t}"
+                    : "=f"(v[c])
+                    : "r"(at), "r"(c)
+                    : "memory");
+#pragma unroll
+            for (int c = 1; c < kShrinkCtas; ++c) v[0] += v[c];
+            // value f of lane l: row l / 4 + 8 (f / 2 % 2), column 2 (l % 4) + f % 2
+            // of group f / 4
+            const int f = i >> 5, l = i & 31;
+            const int r = r0 + (l >> 2) + 8 * ((f >> 1) & 1);
+            const int col = m0 + 8 * (f >> 2) + 2 * (l & 3) + (f & 1);
             if (r < R && col < M && ids[col] == ad)
-                t[static_cast<size_t>(col) * R + r] = scales != nullptr ? v * scales[ad] : v;
+                t[static_cast<size_t>(col) * R + r] = scales != nullptr ? v[0] * scales[ad] : v[0];
         }
         cluster_sync();  // the values are read before any CTA leaves or goes on
     }

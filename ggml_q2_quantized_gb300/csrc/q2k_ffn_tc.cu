@@ -87,6 +87,9 @@ constexpr int kPlanSms = 152;  // K parts are planned for the whole GPU, whateve
 constexpr int kTileStages = 20;  // a tile's set-up and epilogue, in stages of its K loop
 
 constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memory
+// Sums of a tile in shared memory: token c, row r at word 132 c + r (132: lanes
+// that read two tokens apart fall on different banks).
+constexpr int kSumPitch = kRows + 4;
 
 enum class Tc { kGated, kLora, kBackward };
 
@@ -129,9 +132,8 @@ struct Cfg {
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
-    // the epilogue's sums, and with adapters 64 t a token, reuse the token ring
-    // (and the adapters' ids a raw slot)
-    static_assert(kOffA >= (kRows + (kMode == Tc::kLora ? 64 : 0)) * kX * 4, "epilogue");
+    // the epilogue's sums, and with adapters 64 t and an id a token, reuse the rings
+    static_assert(kOffBar >= (kSumPitch + (kMode == Tc::kLora ? 65 : 0)) * kX * 4, "epilogue");
     static_assert(kColA + (kBack ? 0 : 32 * kAStages) <= kTmemCols, "tensor memory");
     static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0, "swizzle and TMA alignment");
 };
@@ -209,18 +211,18 @@ __device__ __forceinline__ void dec_barrier() {
     asm volatile("bar.sync 2, %0;" ::"n"(kDecThreads) : "memory");
 }
 
-// Sums of a tile in shared memory: token c, row r at word 128 c + r.  Adds
-// s_a B_a t of each token's adapter: per 16 rows and eight tokens, one product
-// (m16n8k16) for each adapter that occurs among them, B_a as stored and t split
-// into two bf16 (16 bits); a token's sum takes only its own adapter's product.
-// Tokens [first, end), first a multiple of 8.  t comes through shared memory 64
-// values a token at a time (tbuf; value r of token c at word 64 c + (r ^ 8 (c %
-// 4)), so that the eight tokens a warp reads together fall on different banks),
-// B_a's fragments stay in registers from one token group to the next with the
-// same adapter: reading both per group cost 40 us of an 85 us call (512 tokens,
-// 7168 x 7168, rank 64).
-__device__ __forceinline__ void add_adapters(float* sums, float* tbuf, int* id_buf, const TcArgs& p,
-                                             int n0, int m0, int first, int end) {
+// Adds s_a B_a t of each token's adapter to the sums: per 16 rows and eight
+// tokens, one product (m16n8k16) for each adapter that occurs among them, B_a as
+// stored and t split into two bf16 (16 bits); a token's sum takes only its own
+// adapter's product.  Tokens [first, end), first a multiple of 8.
+// t comes through shared memory 64 values a token at a time, already split: the
+// two bf16 of value pair j (hi, lo) of token c at words 64 c + (2 j ^ 8 (c % 4)),
+// so that the eight tokens a warp reads together fall on different banks.  B_a's
+// fragments stay in registers from one token group to the next with the same
+// adapter.  (Reading t and B per group from L2 took 40 us of an 85 us call: 512
+// tokens, 7168 x 7168, rank 64; splitting t per group of rows 14 us; this 5 us.)
+__device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* id_buf,
+                                             const TcArgs& p, int n0, int m0, int first, int end) {
     const int td = threadIdx.x, warp = td >> 5, lane = td & 31;
     const int g = lane >> 2, t = lane & 3;
     const int row = 16 * (warp & 7) + g;  // this lane's rows: row, row + 8
@@ -232,12 +234,29 @@ __device__ __forceinline__ void add_adapters(float* sums, float* tbuf, int* id_b
     }
     for (int r0 = 0; r0 < p.R; r0 += 64) {
         const int width = min(64, p.R - r0);  // a multiple of 8
-        for (int i = 16 * first + td; i < 16 * end; i += kDecThreads) {
-            const int c = i >> 4, r = 4 * (i & 15);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < width)
-                v = *reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m0 + c) * p.R + r0 + r);
-            *reinterpret_cast<float4*>(tbuf + 64 * c + (r ^ (8 * (c & 3)))) = v;
+        for (int base = 16 * first + td; base < 16 * end; base += 4 * kDecThreads) {
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = base + u * kDecThreads, r = 4 * (i & 15);
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < 16 * end && r < width)
+                    v[u] = *reinterpret_cast<const float4*>(
+                        p.t + static_cast<size_t>(m0 + (i >> 4)) * p.R + r0 + r);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = base + u * kDecThreads, c = i >> 4, r = 4 * (i & 15);
+                if (i >= 16 * end) break;
+                uint4 w;
+                w.x = pack_bf16(v[u].x, v[u].y);
+                w.z = pack_bf16(v[u].z, v[u].w);
+                w.y = pack_bf16(v[u].x - __uint_as_float(w.x << 16),
+                                v[u].y - __uint_as_float(w.x & 0xFFFF0000u));
+                w.w = pack_bf16(v[u].z - __uint_as_float(w.z << 16),
+                                v[u].w - __uint_as_float(w.z & 0xFFFF0000u));
+                *reinterpret_cast<uint4*>(tbuf + 64 * c + (r ^ (8 * (c & 3)))) = w;
+            }
         }
         dec_barrier();
         int cur = -1;
@@ -247,8 +266,8 @@ __device__ __forceinline__ void add_adapters(float* sums, float* tbuf, int* id_b
             // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
             const int id0 = __shfl_sync(0xFFFFFFFFu, id, 8 * t);
             const int id1 = __shfl_sync(0xFFFFFFFFu, id, 8 * t + 4);
-            float* s0 = sums + (c0 + 2 * t) * kRows + row;
-            float* s1 = s0 + kRows;
+            float* s0 = sums + (c0 + 2 * t) * kSumPitch + row;
+            float* s1 = s0 + kSumPitch;
             if (id0 == -2) s0[0] = s0[8] = 0.f;
             if (id1 == -2) s1[0] = s1[8] = 0.f;
             unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
@@ -270,26 +289,26 @@ __device__ __forceinline__ void add_adapters(float* sums, float* tbuf, int* id_b
                         if (ok1 && in1) a[q][3] = __ldg(reinterpret_cast<const uint32_t*>(b1 + 16 * q + 8) + t);
                     }
                 }
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                // (four chains of two products, added at the end: a product
+                // takes as long as dozens of other instructions to return)
+                float e[4][4] = {};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (16 * q >= width) break;
-                    uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0;
-                    if (id == ad) {
-                        const float* tr = tbuf + 64 * (c0 + g);
+                    uint2 u = make_uint2(0u, 0u), v = u;
+                    if (id == ad && 16 * q < width) {
+                        const uint32_t* tr = tbuf + 64 * (c0 + g);
                         const int x = 8 * ((c0 + g) & 3);
-                        const float2 u = *reinterpret_cast<const float2*>(tr + ((16 * q + 2 * t) ^ x));
-                        const float2 v = *reinterpret_cast<const float2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
-                        h0 = pack_bf16(u.x, u.y);
-                        h1 = pack_bf16(v.x, v.y);
-                        l0 = pack_bf16(u.x - __uint_as_float(h0 << 16),
-                                       u.y - __uint_as_float(h0 & 0xFFFF0000u));
-                        l1 = pack_bf16(v.x - __uint_as_float(h1 << 16),
-                                       v.y - __uint_as_float(h1 & 0xFFFF0000u));
+                        u = *reinterpret_cast<const uint2*>(tr + ((16 * q + 2 * t) ^ x));
+                        v = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
                     }
-                    mma_bf16_16816(d, a[q][0], a[q][1], a[q][2], a[q][3], h0, h1);
-                    mma_bf16_16816(d, a[q][0], a[q][1], a[q][2], a[q][3], l0, l1);
+                    if (16 * q < width) {
+                        mma_bf16_16816(e[q], a[q][0], a[q][1], a[q][2], a[q][3], u.x, v.x);
+                        mma_bf16_16816(e[q], a[q][0], a[q][1], a[q][2], a[q][3], u.y, v.y);
+                    }
                 }
+                float d[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) d[c] = (e[0][c] + e[1][c]) + (e[2][c] + e[3][c]);
                 if (id0 == ad) {
                     s0[0] += d[0];
                     s0[8] += d[2];
@@ -443,7 +462,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     else __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-    float* sums = reinterpret_cast<float*>(smem);  // token c, row r at word 128 c + r
+    float* sums = reinterpret_cast<float*>(smem);
 
     if (warp < kDecWarps) {
         // ---------------- weight decoders ----------------
@@ -624,7 +643,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 }
 #pragma unroll
                 for (int q = 0; q < 16; ++q)
-                    if (c0 + q < tokens) sums[(c0 + q) * kRows + row] = v[q];
+                    if (c0 + q < tokens) sums[(c0 + q) * kSumPitch + row] = v[q];
             }
         }
     } else if ((warp == kMmaWarp && peer == 0) || (C::kIssuers == 2 && warp == kWaitWarp)) {
@@ -809,7 +828,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     // past these barriers no wait is left that could raise the flag
     const bool done = *abort_flag == 0;
     if (warp < kDecWarps && parts > 1) {
-        for (int i = first * (kRows / 4) + threadIdx.x; i < end * (kRows / 4); i += kDecThreads) {
+        for (int j = first * (kRows / 4) + threadIdx.x; j < end * (kRows / 4); j += kDecThreads) {
+            const int i = j / (kRows / 4) * (kSumPitch / 4) + j % (kRows / 4);
             float4 v[kMaxParts];
 #pragma unroll
             for (int z = 0; z < kMaxParts; ++z)
@@ -832,9 +852,9 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         if constexpr (kMode == Tc::kGated) {
             // a warp takes a token at a time, a lane the rows 2 lane, 2 lane + 1
             for (int c = first + warp; c < end; c += kDecWarps) {
-                const float2 g = *reinterpret_cast<const float2*>(sums + c * kRows + 2 * lane);
+                const float2 g = *reinterpret_cast<const float2*>(sums + c * kSumPitch + 2 * lane);
                 const float2 u =
-                    *reinterpret_cast<const float2*>(sums + c * kRows + kSplit0 + 2 * lane);
+                    *reinterpret_cast<const float2*>(sums + c * kSumPitch + kSplit0 + 2 * lane);
                 const int n = n0 + 2 * lane;
                 const int valid = rows - n;
                 if (valid <= 0) continue;
@@ -849,14 +869,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         } else {
             if constexpr (kMode == Tc::kLora) {
                 pdl_wait_prerequisites();  // t (written by this grid or one before)
-                add_adapters(sums, sums + kX * kRows, reinterpret_cast<int*>(smem + C::kOffRaw), p,
-                             n0, m0, first, end);
+                uint32_t* tbuf = reinterpret_cast<uint32_t*>(sums + kX * kSumPitch);
+                add_adapters(sums, tbuf, reinterpret_cast<int*>(tbuf + kX * 64), p, n0, m0, first, end);
             }
             for (int c = first + warp; c < end; c += kDecWarps)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int r = 64 * q + 2 * lane;
-                    const float2 v = *reinterpret_cast<const float2*>(sums + c * kRows + r);
+                    const float2 v = *reinterpret_cast<const float2*>(sums + c * kSumPitch + r);
                     const int valid = rows - (n0 + r);
                     if (valid > 0)
                         store_pair(static_cast<T*>(p.y) + static_cast<size_t>(m0 + c) * rows + n0 + r,
