@@ -823,8 +823,7 @@ def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace
     dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
     key = ("backward", "auto", bf16, m, n, k, act)
     params, need, _ = _ffn_plans.get(key) or _ffn_plan(key)
-    # (with dgate and dup given, rows of whole 16 bytes need no copy of them)
-    _keep, ws, ws_bytes = _ffn_workspace(workspace, 0 if n % 8 == 0 else need, dh)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, need, dh)
     _ffn_call(dev, _lib.q2k_gated_ffn_backward, dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
               m * n, w_gate.data_ptr(), w_gate.numel(), w_up.data_ptr(), w_up.numel(),
               dx.data_ptr(), m * k, dgate.data_ptr(), dup.data_ptr(), params, ws, ws_bytes)

@@ -85,7 +85,7 @@ __global__ void __cluster_dims__(1, 1, kShrinkCtas) __launch_bounds__(kShrinkWar
 lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
                    const float* __restrict__ scales, const int* __restrict__ ids,
                    float* __restrict__ t, unsigned int* __restrict__ bad_ids, int M, int K, int R,
-                   int n_adapters) {
+                   int n_adapters, unsigned int* __restrict__ counts, int n_counts) {
     constexpr int kSums = kGroups * 4 * 32;  // of a warp: groups x fragment x lanes
     __shared__ float red[kShrinkWarps][kSums];
     __shared__ float part[kSums];
@@ -99,6 +99,7 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
             bad += __syncthreads_count(id < -1 || id >= n_adapters);
         }
         if (tid == 0) *bad_ids = static_cast<unsigned>(bad);
+        for (int c = tid; c < n_counts; c += kShrinkWarps * 32) counts[c] = 0u;
     }
     const int g = lane >> 2, q4 = lane & 3;
     const int block = static_cast<int>(blockIdx.x);
@@ -208,15 +209,16 @@ lora_shrink_kernel(const T* __restrict__ x, const __nv_bfloat16* __restrict__ a,
 }
 
 template <typename T>
-cudaError_t launch_shrink(const LoraArgs& a, float* t, cudaStream_t stream) {
+cudaError_t launch_shrink(const LoraArgs& a, float* t, unsigned int* counts, int n_counts,
+                          cudaStream_t stream) {
     const T* x = static_cast<const T*>(a.x);
     const unsigned rows = (a.R + kShrinkRows - 1) / kShrinkRows;
     if (a.M <= kShrinkPerToken)
         lora_shrink_kernel<T, 1><<<dim3(a.M, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
-            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
+            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
     else
         lora_shrink_kernel<T, 4><<<dim3((a.M + 31) / 32, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
-            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters);
+            x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
     return cudaGetLastError();
 }
 
@@ -243,11 +245,15 @@ size_t lora_workspace_bytes(const LoraArgs& a) {
 
 cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream) {
     float* t = static_cast<float*>(workspace);
-    const cudaError_t e = a.bf16 ? launch_shrink<__nv_bfloat16>(a, t, stream)
-                                 : launch_shrink<float>(a, t, stream);
+    uint8_t* rest = static_cast<uint8_t*>(workspace) + lora_t_bytes(a);
+    unsigned int* counts = nullptr;
+    int n_counts = 0;
+    if (a.tensor) lora_tc_counts(a, rest, &counts, &n_counts);
+    const cudaError_t e = a.bf16 ? launch_shrink<__nv_bfloat16>(a, t, counts, n_counts, stream)
+                                 : launch_shrink<float>(a, t, counts, n_counts, stream);
     if (e != cudaSuccess) return e;
     if (!a.tensor) return launch_lora_rows(a, t, stream);
-    return launch_lora_tc(a, t, static_cast<uint8_t*>(workspace) + lora_t_bytes(a), stream);
+    return launch_lora_tc(a, t, rest, stream);
 }
 
 }  // namespace q2k

@@ -3,10 +3,12 @@
 // adapters.
 //
 // A CTA computes 128 rows of a product x up to 256 tokens: 16 warps decode Q2_K
-// blocks into tensor memory (the MMA's A operand, one row of the product per
-// lane), token stages of 64 K arrive by TMA in the 128-byte-swizzled layout that
-// the MMA reads (the B operand; f32 tokens come from a bf16 image that a prepass
-// writes in that layout), and f32 sums build up in tensor memory.
+// blocks into shared memory (the MMA's A operand), token stages of 64 K arrive by
+// TMA in the 128-byte-swizzled layout that the MMA reads (the B operand; f32
+// tokens come from a bf16 image that a prepass writes in that layout), and f32
+// sums build up in tensor memory, in two sets: four warps bring one tile's sums
+// out while the next tile is multiplied into the other (gated, 512 tokens x 14336
+// x 4096: a tile's set-up and epilogue took 8 of its 33 us before).
 //
 // Gated: the 128 rows are 64 rows of Wg and the same 64 rows of Wu, so one tile
 // holds both projections of its outputs and the MMAs run as for one matrix; g
@@ -16,16 +18,19 @@
 // Backward: dx = [dg du] [Wg; Wu], a product over the weights' rows.  A tile's
 // 128 rows are half a block of columns (k), a stage is 64 weight rows.  A thread
 // decodes a weight row as above (one table serves 16 codes) and stores it as
-// stored, k running, which is the MMA's A operand "MN-major" in shared memory:
-// the transposition costs nothing.  (Transposing the codes first, so that a lane
-// could write its own column to tensor memory, took 2200 warp instructions a
-// stage against 900, and 198 us instead of 110 for 512 tokens x 14336 x 4096.)
+// stored, k running, which is the MMA's A operand "MN-major": the transposition
+// costs nothing.  (Transposing the codes first, so that a lane could write its
+// own column to tensor memory, took 2200 warp instructions a stage against 680.)
 //
-// With few tiles, K is split over a cluster of CTAs whose sums meet through
-// distributed shared memory in a fixed order.
+// Work split: the grid is as many CTAs as the GPU holds.  Whole tiles go to them
+// in turn; what is left over, less than a tile each, is cut into equal runs of K
+// (in blocks; backward, of 256 weight rows), so that all end together.  A tile's
+// runs leave their sums in the workspace, and the CTA that finishes last adds
+// them, in the order of K whoever that is, and writes the results: no CTA waits
+// for another.
 //
-// What bounds it: at 256 tokens a tile the MMAs (512 clocks per 64 K) and the
-// decode (about as long) run side by side; below, the decode alone.
+// What bounds it: at 256 tokens a tile the MMAs (740 clocks per stage as measured,
+// of 630 for a plain bf16 matrix product at the measured peak); below, the decode.
 //
 // Every wait is bounded (about a second); on time-out the kernel records a bit
 // in the device error word, drains its MMAs, frees TMEM and returns.
@@ -77,19 +82,18 @@ namespace {
 
 using namespace tc;
 
-constexpr int kDecWarps = 16;  // two groups of 8, one per half of a block
+constexpr int kDecWarps = 16;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kMmaWarp = kDecWarps, kWaitWarp = kDecWarps + 1, kWWarp = kDecWarps + 2,
-              kXWarp0 = kDecWarps + 3;
-constexpr int kThreads = 32 * (kDecWarps + 5);
-constexpr int kMaxParts = 8;
-constexpr int kPlanSms = 152;  // K parts are planned for the whole GPU, whatever the device
-constexpr int kTileStages = 20;  // a tile's set-up and epilogue, in stages of its K loop
+              kXWarp = kDecWarps + 3, kEpiWarp0 = kDecWarps + 4;  // (a multiple of 4)
+constexpr int kThreads = 32 * (kDecWarps + 8);
+constexpr int kPlanSms = 152;  // the work is cut for the whole GPU, whatever the device
 
 constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memory
-// Sums of a tile in shared memory: token c, row r at word 132 c + r (132: lanes
-// that read two tokens apart fall on different banks).
+// Sums of 32 tokens on their way out: token c, row r at word 132 c + r (132:
+// lanes that read two tokens apart fall on different banks).
 constexpr int kSumPitch = kRows + 4;
+constexpr int kChunk = 32;
 
 enum class Tc { kGated, kLora, kBackward };
 
@@ -97,45 +101,46 @@ enum class Tc { kGated, kLora, kBackward };
 // 256: two CTAs of a cluster (neighbouring row tiles) form one MMA of 256 rows
 // x 256 tokens, issued by one thread of the first (cta_group::2).  Each holds
 // half of the tokens' stage, so a stage is half as large and crosses from L2
-// once per pair, and its ring is twice as deep in time.
+// once per pair.
 // 128 and fewer: narrow MMAs issue at half the rate the tensor core takes them,
-// so two threads issue, each into its own accumulator; the token ring and the A
-// ring are equally deep then, and one release serves two stages of both.
+// so two threads issue, each into its own accumulator (stages in turn).
 template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
     static constexpr bool kDuo = kX == 256;
+    static constexpr int kCtas = kDuo ? 2 : 1;
     static constexpr int kIssuers = kDuo ? 1 : 2;
-    static constexpr int kHand = kDuo || kBack ? 2 : 4;  // stages handed over at a time
-    static constexpr bool kPairs = kIssuers == 2;        // stages released two at a time
-    static constexpr int kHold = kDuo ? kX / 2 : kX;     // tokens of a stage in this CTA
+    static constexpr int kHand = 2;                      // stages handed over at a time
+    static constexpr int kHold = kX / kCtas;             // tokens of a stage in this CTA
     static constexpr int kXStage = kHold * kStageK * 2;
-    static constexpr int kXStages = kDuo ? (kBack ? 8 : 12) : kBack && kX == 128 ? 6 : 8;
-    static constexpr int kAStages = kBack ? (kDuo ? 4 : kXStages) : 8;
-    // decoders: groups of warps on stages (backward) or block halves in turn
-    static constexpr int kGroupWarps = kBack ? 4 : 8;
-    static constexpr uint32_t kColA = kX * kIssuers;
+    // stages in flight, tokens and decoded weights alike (one release for both)
+    static constexpr int kStages = kX >= 128 ? 5 : kX == 64 ? 7 : 8;
+    static constexpr int kGroupWarps = 4;  // decoders: four groups, a stage each in turn
+    static constexpr uint32_t kAccCols = kX * kIssuers;  // a tile's sums; two sets
     static constexpr uint32_t kTmemCols = 512;
+    static_assert(2 * kAccCols <= kTmemCols, "tensor memory");
     // raw slots: a block column of 128 weight rows, or (backward) of 64 for a
     // stage, without TMA only the 11 words of the half block that it needs
     static constexpr int kRawRows = kBack ? kStageK : kRows;
     static constexpr int kRawPitch = kTma ? kBoxBytes : kBack ? 44 : kBlockBytes;
     static constexpr int kRawBytes = kRawRows * kRawPitch;
     static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : (kTma ? 2 : 3);
-    // backward: decoded stages in shared memory, 64 weight rows x 128 columns
-    static constexpr int kOffA = kXStages * kXStage;
-    static constexpr int kOffRaw = kOffA + (kBack ? kAStages * kABytes : 0);
-    // bars: x_full, x_empty [kXStages], a_full, a_empty, peer_full [kAStages],
-    //       raw_full, raw_empty [kRaw], accum, drain
-    static constexpr int kNumBars = 2 * kXStages + 3 * kAStages + 2 * kRaw + 2;
-    static constexpr int kOffBar = (kOffRaw + kRaw * kRawBytes + 7) & ~7;
+    static constexpr int kOffA = kStages * kXStage;
+    static constexpr int kOffRaw = kOffA + kStages * kABytes;
+    static constexpr int kOffSums = kOffRaw + kRaw * kRawBytes;
+    // with adapters: 64 t and an id for each token of the chunk
+    static constexpr int kOffT = kOffSums + kChunk * kSumPitch * 4;
+    static constexpr int kOffIds = kOffT + (kMode == Tc::kLora ? kChunk * 64 * 4 : 0);
+    // bars: x_full, a_full, peer_full, empty [kStages], raw_full, raw_empty
+    //       [kRaw], acc_full, acc_empty [2], drain
+    static constexpr int kNumBars = 4 * kStages + 2 * kRaw + 5;
+    static constexpr int kOffBar = (kOffIds + (kMode == Tc::kLora ? kChunk * 4 : 0) + 7) & ~7;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
-    // the epilogue's sums, and with adapters 64 t and an id a token, reuse the rings
-    static_assert(kOffBar >= (kSumPitch + (kMode == Tc::kLora ? 65 : 0)) * kX * 4, "epilogue");
-    static_assert(kColA + (kBack ? 0 : 32 * kAStages) <= kTmemCols, "tensor memory");
-    static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0, "swizzle and TMA alignment");
+    static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0 && kOffSums % 16 == 0, "alignment");
+    // the last tile's sums, t and ids for all its tokens, take the rings' place
+    static_assert(kX * (kSumPitch + (kMode == Tc::kLora ? 65 : 0)) * 4 <= kOffBar, "epilogue");
 };
 
 struct TcArgs {
@@ -143,8 +148,12 @@ struct TcArgs {
     const uint8_t* w0;   // Wg, or W
     const uint8_t* w1;   // Wu
     int M, N, K;         // N, K: the weight matrices' rows and columns
-    int stages;          // 64-K stages of the whole product
-    int half_stages;     // backward: those of Wg
+    int quads;           // the product's K in blocks (backward: 256 weight rows)
+    int half_stages;     // backward: 64-row stages of Wg
+    int tiles, row_units;  // tiles, row tiles (256 tokens: pairs of them) first
+    int whole;           // tiles [0, whole) go to the workers in turn, the rest is cut
+    float* partial;      // sums of a cut tile's runs, two slots per CTA
+    unsigned int* counts;  // per cut tile and CTA of a worker: runs finished (zeroed)
     bool const_weights;  // the grid before does not write the weights
     bool tokens_ready;   // nor the tokens
     // gated
@@ -164,28 +173,6 @@ struct TcMaps {
     CUtensorMap w0, w1;  // weights, 112-byte boxes of 64 or 128 rows
     CUtensorMap x0, x1;  // tokens, boxes of kX rows x 64 (backward: dg and du)
 };
-
-// Stage Cp (0, 1) of one half of a block for one thread: the two K-steps of
-// quant segment `seg` at shifts J = 2 Cp + {0, 1}.  qh: the thread's four quant
-// words, sh: the half's two scale words shifted right by 8 seg.
-template <int Cp>
-__device__ __forceinline__ void decode_half_stage(const uint32_t* qh, const uint32_t* sh, float d,
-                                                  float dmin, uint32_t (&o0)[8], uint32_t (&o1)[8]) {
-#pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-        constexpr int kJ0 = 2 * Cp;
-        const int j = kJ0 + jj;
-        uint32_t lo, hi;
-        weight_table((sh[j >> 1] >> (16 * (j & 1))) & 0xFFu, d, dmin, lo, hi);
-        uint32_t* o = jj == 0 ? o0 : o1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t sel = jj == 0 ? code_selectors<kJ0>(qh[e]) : code_selectors<kJ0 + 1>(qh[e]);
-            o[2 * e] = __byte_perm(lo, hi, sel);
-            o[2 * e + 1] = __byte_perm(lo, hi, __umulhi(sel, 0x10000u));  // sel >> 16
-        }
-    }
-}
 
 // Block b of the tile's 128 rows (row r < split0 from w0, the others from w1)
 // into a raw slab; rows past N are zero-filled (they decode to 0).
@@ -207,47 +194,56 @@ __device__ __forceinline__ void issue_raw(const uint8_t* w0, const uint8_t* w1, 
     cp_async_commit();
 }
 
-__device__ __forceinline__ void dec_barrier() {
-    asm volatile("bar.sync 2, %0;" ::"n"(kDecThreads) : "memory");
-}
+// The threads that bring a tile's sums out: the epilogue's four warps while the
+// next tile is being multiplied, those and the decoders for the CTA's last tile.
+// Warp w of a team has TMEM lanes (rows) 32 (w % 4) ..
+struct Team {
+    int thread, threads, barrier;
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+    }
+};
 
-// Adds s_a B_a t of each token's adapter to the sums: per 16 rows and eight
-// tokens, one product (m16n8k16) for each adapter that occurs among them, B_a as
-// stored and t split into two bf16 (16 bits); a token's sum takes only its own
-// adapter's product.  Tokens [first, end), first a multiple of 8.
-// t comes through shared memory 64 values a token at a time, already split: the
-// two bf16 of value pair j (hi, lo) of token c at words 64 c + (2 j ^ 8 (c % 4)),
-// so that the eight tokens a warp reads together fall on different banks.  B_a's
-// fragments stay in registers from one token group to the next with the same
-// adapter.  (Reading t and B per group from L2 took 40 us of an 85 us call: 512
-// tokens, 7168 x 7168, rank 64; splitting t per group of rows 14 us; this 5 us.)
-__device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* id_buf,
-                                             const TcArgs& p, int n0, int m0, int first, int end) {
-    const int td = threadIdx.x, warp = td >> 5, lane = td & 31;
+// Adds s_a B_a t of each token's adapter to the sums of `count` tokens from m on:
+// per 16 rows and eight tokens, one product (m16n8k16) for each adapter that
+// occurs among them, B_a as stored and t split into two bf16 (16 bits); a token's
+// sum takes only its own adapter's product.  t comes through shared memory 64
+// values a token at a time, already split: the two bf16 of value pair j (hi, lo)
+// of token c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
+// reads together fall on different banks.  A warp has 32 rows, and keeps B_a's
+// fragments in registers (`b`, of adapter `cur` and its values from `cur_r0` on)
+// from one token group and chunk to the next.  These products bound it: one takes
+// 32 clocks of a quarter SM, 17000 clocks for 128 rows x 256 tokens at rank 64.
+struct AdapterFragments {
+    uint32_t b[2][4][4];
+    int cur = -1, cur_r0 = 0;
+};
+__device__ __forceinline__ void add_adapters(AdapterFragments& f, float* sums, uint32_t* tbuf,
+                                             int* id_buf, const TcArgs& p, int n0, int m, int count,
+                                             const Team& team) {
+    const int et = team.thread, quarter = (et >> 5) & 3, lane = et & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int row = 16 * (warp & 7) + g;  // this lane's rows: row, row + 8
-    const bool ok0 = n0 + row < p.N, ok1 = n0 + row + 8 < p.N;
+    const int slots = (count + 7) & ~7;
     // ids: -1 none, -2 out of range (a zero row)
-    for (int c = first + td; c < end; c += kDecThreads) {
-        const int id = p.ids[m0 + c];
+    for (int c = et; c < slots; c += team.threads) {
+        const int id = c < count ? p.ids[m + c] : -1;
         id_buf[c] = id < -1 || id >= p.n_adapters ? -2 : id;
     }
     for (int r0 = 0; r0 < p.R; r0 += 64) {
         const int width = min(64, p.R - r0);  // a multiple of 8
-        for (int base = 16 * first + td; base < 16 * end; base += 4 * kDecThreads) {
+        for (int base = et; base < 16 * slots; base += 4 * team.threads) {
             float4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = base + u * kDecThreads, r = 4 * (i & 15);
+                const int i = base + team.threads * u, r = 4 * (i & 15);
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < 16 * end && r < width)
-                    v[u] = *reinterpret_cast<const float4*>(
-                        p.t + static_cast<size_t>(m0 + (i >> 4)) * p.R + r0 + r);
+                if ((i >> 4) < count && r < width)
+                    v[u] = *reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m + (i >> 4)) * p.R + r0 + r);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = base + u * kDecThreads, c = i >> 4, r = 4 * (i & 15);
-                if (i >= 16 * end) break;
+                const int i = base + team.threads * u, c = i >> 4, r = 4 * (i & 15);
+                if (c >= slots) break;
                 uint4 w;
                 w.x = pack_bf16(v[u].x, v[u].y);
                 w.z = pack_bf16(v[u].z, v[u].w);
@@ -258,68 +254,77 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* i
                 *reinterpret_cast<uint4*>(tbuf + 64 * c + (r ^ (8 * (c & 3)))) = w;
             }
         }
-        dec_barrier();
-        int cur = -1;
-        uint32_t a[4][4];
-        for (int c0 = first + 8 * (warp >> 3); c0 < end; c0 += 16) {
-            const int id = c0 + g < end ? id_buf[c0 + g] : -1;
+        team.sync();
+#pragma unroll 1
+        for (int c0 = 8 * (et >> 7); c0 < slots; c0 += 8 * (team.threads >> 7)) {
+            const int id = id_buf[c0 + g];
             // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
-            const int id0 = __shfl_sync(0xFFFFFFFFu, id, 8 * t);
-            const int id1 = __shfl_sync(0xFFFFFFFFu, id, 8 * t + 4);
-            float* s0 = sums + (c0 + 2 * t) * kSumPitch + row;
+            const int id0 = id_buf[c0 + 2 * t], id1 = id_buf[c0 + 2 * t + 1];
+            float* s0 = sums + (c0 + 2 * t) * kSumPitch + 32 * quarter + g;
             float* s1 = s0 + kSumPitch;
-            if (id0 == -2) s0[0] = s0[8] = 0.f;
-            if (id1 == -2) s1[0] = s1[8] = 0.f;
+            if (r0 == 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (id0 == -2) s0[8 * q] = 0.f;
+                    if (id1 == -2) s1[8 * q] = 0.f;
+                }
+            }
             unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
             while (todo != 0) {
                 const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
                 todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
-                if (ad != cur) {
-                    cur = ad;
-                    const __nv_bfloat16* b0 =
-                        p.b + (static_cast<size_t>(ad) * p.N + n0 + row) * p.R + r0;
-                    const __nv_bfloat16* b1 = b0 + static_cast<size_t>(8) * p.R;
+                if (ad != f.cur || r0 != f.cur_r0) {
+                    f.cur = ad;
+                    f.cur_r0 = r0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        a[q][0] = a[q][1] = a[q][2] = a[q][3] = 0u;
-                        const bool in0 = 16 * q < width, in1 = 16 * q + 8 < width;
-                        if (ok0 && in0) a[q][0] = __ldg(reinterpret_cast<const uint32_t*>(b0 + 16 * q) + t);
-                        if (ok1 && in0) a[q][1] = __ldg(reinterpret_cast<const uint32_t*>(b1 + 16 * q) + t);
-                        if (ok0 && in1) a[q][2] = __ldg(reinterpret_cast<const uint32_t*>(b0 + 16 * q + 8) + t);
-                        if (ok1 && in1) a[q][3] = __ldg(reinterpret_cast<const uint32_t*>(b1 + 16 * q + 8) + t);
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = n0 + 32 * quarter + 16 * h + g;
+                        const uint32_t* b0 = reinterpret_cast<const uint32_t*>(
+                            p.b + (static_cast<size_t>(ad) * p.N + n) * p.R + r0) + t;
+                        const uint32_t* b1 = b0 + 4 * p.R;  // eight rows on
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const bool in0 = 16 * q < width, in1 = 16 * q + 8 < width;
+                            f.b[h][q][0] = n < p.N && in0 ? __ldg(b0 + 8 * q) : 0u;
+                            f.b[h][q][1] = n + 8 < p.N && in0 ? __ldg(b1 + 8 * q) : 0u;
+                            f.b[h][q][2] = n < p.N && in1 ? __ldg(b0 + 8 * q + 4) : 0u;
+                            f.b[h][q][3] = n + 8 < p.N && in1 ? __ldg(b1 + 8 * q + 4) : 0u;
+                        }
                     }
                 }
-                // (four chains of two products, added at the end: a product
-                // takes as long as dozens of other instructions to return)
-                float e[4][4] = {};
+                // (four chains of four products, two per half of the rows)
+                float e[2][2][4] = {};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint2 u = make_uint2(0u, 0u), v = u;
-                    if (id == ad && 16 * q < width) {
+                    if (16 * q >= width) break;
+                    uint2 u = make_uint2(0u, 0u), w = u;
+                    if (id == ad) {
                         const uint32_t* tr = tbuf + 64 * (c0 + g);
-                        const int x = 8 * ((c0 + g) & 3);
+                        const int x = 8 * (g & 3);
                         u = *reinterpret_cast<const uint2*>(tr + ((16 * q + 2 * t) ^ x));
-                        v = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
+                        w = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
                     }
-                    if (16 * q < width) {
-                        mma_bf16_16816(e[q], a[q][0], a[q][1], a[q][2], a[q][3], u.x, v.x);
-                        mma_bf16_16816(e[q], a[q][0], a[q][1], a[q][2], a[q][3], u.y, v.y);
-                    }
-                }
-                float d[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) d[c] = (e[0][c] + e[1][c]) + (e[2][c] + e[3][c]);
-                if (id0 == ad) {
-                    s0[0] += d[0];
-                    s0[8] += d[2];
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t(&b)[4] = f.b[h][q];
+                        mma_bf16_16816(e[h][0], b[0], b[1], b[2], b[3], u.x, w.x);
+                        mma_bf16_16816(e[h][1], b[0], b[1], b[2], b[3], u.y, w.y);
+                    }
                 }
-                if (id1 == ad) {
-                    s1[0] += d[1];
-                    s1[8] += d[3];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (id0 == ad) {
+                        s0[16 * h] += e[h][0][0] + e[h][1][0];
+                        s0[16 * h + 8] += e[h][0][2] + e[h][1][2];
+                    }
+                    if (id1 == ad) {
+                        s1[16 * h] += e[h][0][1] + e[h][1][1];
+                        s1[16 * h + 8] += e[h][0][3] + e[h][1][3];
+                    }
                 }
             }
         }
-        dec_barrier();
+        team.sync();
     }
 }
 
@@ -348,16 +353,58 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile(
-        "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
+// One worker's share of the product (a CTA, or a pair): first its runs of the cut
+// tiles (two at most), then its whole tiles.
+struct Segment {
+    int tile, q0, q1;
+    int run;  // -1: a whole tile; else which of the worker's runs
+};
+struct Work {
+    int w, workers, quads, tiles, whole;
+    // quads [begin(w), begin(w + 1)) of the cut tiles, counted through
+    __device__ __forceinline__ int begin(int w) const {
+        return static_cast<int>(static_cast<long long>(tiles - whole) * quads * w / workers);
+    }
+    __device__ __forceinline__ bool segment(int index, Segment& s) const {
+        const int a0 = begin(w), a1 = begin(w + 1);
+        int runs = 0;
+        if (a1 > a0) {
+            const int t0 = a0 / quads, t1 = (a1 - 1) / quads;
+            runs = t1 - t0 + 1;
+            if (index < runs) {
+                s.tile = whole + t0 + index;
+                s.q0 = index == 0 ? a0 - t0 * quads : 0;
+                s.q1 = index == runs - 1 ? a1 - t1 * quads : quads;
+                s.run = index;
+                return true;
+            }
+        }
+        s.tile = w + (index - runs) * workers;
+        s.q0 = 0;
+        s.q1 = quads;
+        s.run = -1;
+        return s.tile < whole;
+    }
+    __device__ __forceinline__ int count() const {
+        const int a0 = begin(w), a1 = begin(w + 1);
+        return (a1 > a0 ? (a1 - 1) / quads - a0 / quads + 1 : 0) +
+               (w < whole ? (whole - 1 - w) / workers + 1 : 0);
+    }
+    // The workers with a run of cut tile `tile`.
+    __device__ __forceinline__ void sharers(int tile, int& first, int& last) const {
+        const long long q = static_cast<long long>(tile - whole) * quads;
+        const long long total = static_cast<long long>(tiles - whole) * quads;
+        first = static_cast<int>(q * workers / total);
+        while (first > 0 && begin(first) > q) --first;
+        while (begin(first + 1) <= q) ++first;
+        last = first;
+        while (last + 1 < workers && begin(last + 1) < q + quads) ++last;
+    }
+    // Which of worker v's runs is of cut tile `tile`.
+    __device__ __forceinline__ int run_of(int v, int tile) const {
+        return tile - whole - begin(v) / quads;
+    }
+};
 
 // Backward, non-TMA: the words of 64 weight rows that a stage needs (two of
 // scales, eight of codes, d and dmin) packed into a raw slot, by the 128 threads
@@ -380,8 +427,8 @@ __device__ __forceinline__ void issue_raw_rows(const TcArgs& p, uint32_t dst, in
     cp_async_commit();
 }
 
-// The weights of segment `seg` of a half block of one row at shift J: words 0..3
-// of `q` -> 16 bf16 (k running).
+// The 16 weights of a segment of one row at shift J: its four quant words -> bf16,
+// k running.
 template <int J>
 __device__ __forceinline__ void decode_segment(const uint32_t (&q)[4], uint32_t sc, float d, float dmin,
                                                uint32_t (&o)[8]) {
@@ -395,62 +442,98 @@ __device__ __forceinline__ void decode_segment(const uint32_t (&q)[4], uint32_t 
     }
 }
 
+// Results of `count` tokens (m0 on) of a tile from their sums.
+template <Tc kMode, typename T>
+__device__ __forceinline__ void emit(const TcArgs& p, const float* sums, int n0, int rows, int m0,
+                                     int count, const Team& team) {
+    const int lane = team.thread & 31;
+    const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
+    // a warp takes a token at a time, a lane neighbouring rows
+    for (int c = team.thread >> 5; c < count; c += team.threads >> 5) {
+        const float* row = sums + c * kSumPitch + 2 * lane;
+        const size_t at = static_cast<size_t>(m0 + c) * rows + n0 + 2 * lane;
+        const int valid = rows - (n0 + 2 * lane);
+        if constexpr (kMode == Tc::kGated) {
+            if (valid <= 0) continue;
+            const float2 g = *reinterpret_cast<const float2*>(row);
+            const float2 u = *reinterpret_cast<const float2*>(row + kRows / 2);
+            store_pair(static_cast<T*>(p.h) + at, act_value<sizeof(T) == 2>(g.x, p.act) * u.x,
+                       act_value<sizeof(T) == 2>(g.y, p.act) * u.y, valid, vec);
+            if (p.gate != nullptr) {
+                store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
+                store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float2 v = *reinterpret_cast<const float2*>(row + 64 * q);
+                if (valid - 64 * q > 0)
+                    store_pair(static_cast<T*>(p.y) + at + 64 * q, v.x, v.y, valid - 64 * q, vec);
+            }
+        }
+    }
+}
+
 template <int kX, bool kTma, Tc kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     using C = Cfg<kX, kTma, kMode>;
     constexpr bool kBack = kMode == Tc::kBackward;
     constexpr bool kDuo = C::kDuo;
+    constexpr int S = C::kStages;
     constexpr int kSplit0 = kMode == Tc::kGated ? kRows / 2 : kRows;  // tile rows of w0
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * kSplit0;  // first row of the product (backward: column k)
-    const int rows = kBack ? p.K : p.N;   // rows of the product
-    const int m0 = blockIdx.y * kX;
-    const int tokens = min(kX, p.M - m0);
-    const int nx = kDuo ? (tokens + 31) & ~31 : (tokens + 15) & ~15;  // MMA N
-    // two CTAs: this one holds tokens [peer nx / 2, peer nx / 2 + nx / 2)
+    const int rows = kBack ? p.K : p.N;  // rows of the product
     const int peer = kDuo ? static_cast<int>(blockIdx.x & 1) : 0;
-    const int held = kDuo ? nx / 2 : nx;
-    const int m_held = m0 + peer * held;
-    // K parts in whole blocks (backward: four stages, 256 weight rows)
-    const int parts = gridDim.z, quads = p.stages / 4;
-    const int q0 = static_cast<int>(static_cast<long>(blockIdx.z) * quads / parts);
-    const int n_quads = static_cast<int>(static_cast<long>(blockIdx.z + 1) * quads / parts) - q0;
-    const int n_iters = 4 * n_quads;
+    Work work;
+    work.w = blockIdx.x / C::kCtas;
+    work.workers = gridDim.x / C::kCtas;
+    work.quads = p.quads;
+    work.tiles = p.tiles;
+    work.whole = p.whole;
+    Segment sg;
+    // first row (backward: column k) and first token of a tile, its MMA N
+    auto row0 = [&](int tile) { return (C::kCtas * (tile % p.row_units) + peer) * kSplit0; };
+    auto token0 = [&](int tile) { return tile / p.row_units * kX; };
+    auto mma_n = [&](int tile) {
+        const int tokens = min(kX, p.M - token0(tile));
+        return kDuo ? (tokens + 31) & ~31 : (tokens + 15) & ~15;
+    };
 
     const uint32_t bar_xfull = sbase + C::kOffBar;
-    const uint32_t bar_xempty = bar_xfull + 8 * C::kXStages;
-    const uint32_t bar_afull = bar_xempty + 8 * C::kXStages;
-    const uint32_t bar_aempty = bar_afull + 8 * C::kAStages;
-    const uint32_t bar_peer = bar_aempty + 8 * C::kAStages;  // (of the first CTA)
-    const uint32_t bar_raw = bar_peer + 8 * C::kAStages;
+    const uint32_t bar_afull = bar_xfull + 8 * S;
+    const uint32_t bar_peer = bar_afull + 8 * S;  // (of the first CTA)
+    const uint32_t bar_empty = bar_peer + 8 * S;
+    const uint32_t bar_raw = bar_empty + 8 * S;
     const uint32_t bar_rawempty = bar_raw + 8 * C::kRaw;
-    const uint32_t bar_accum = bar_rawempty + 8 * C::kRaw;
-    const uint32_t bar_drain = bar_accum + 8;
+    const uint32_t bar_accfull = bar_rawempty + 8 * C::kRaw;
+    const uint32_t bar_accempty = bar_accfull + 16;  // (of the first CTA)
+    const uint32_t bar_drain = bar_accempty + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    volatile int* shared_word = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
     unsigned int* err = &g_ffn_error;
 
     if (warp == 0) {
-        for (int s = lane; s < C::kXStages; s += 32) {
-            mbar_init(bar_xfull + 8 * s, 1);   // the producer's expect-tx arrival
-            mbar_init(bar_xempty + 8 * s, 1);  // MMA commit
-        }
-        for (int s = lane; s < C::kAStages; s += 32) {
+        for (int s = lane; s < S; s += 32) {
+            mbar_init(bar_xfull + 8 * s, 1);               // the producer's expect-tx arrival
             mbar_init(bar_afull + 8 * s, C::kGroupWarps);  // the warps of its group
-            mbar_init(bar_aempty + 8 * s, C::kPairs ? C::kIssuers : 1);
-            mbar_init(bar_peer + 8 * s, 1);  // the second CTA's waiter
+            mbar_init(bar_peer + 8 * s, 1);                // the second CTA's waiter
+            mbar_init(bar_empty + 8 * s, 1);               // MMA commit of the stage's issuer
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
             mbar_init(bar_rawempty + 8 * r, kBack ? C::kGroupWarps : kDecWarps);
         }
+        if (lane < 2) {
+            mbar_init(bar_accfull + 8 * lane, C::kIssuers);
+            mbar_init(bar_accempty + 8 * lane, 4 * C::kCtas);  // epilogue warps
+        }
         if (lane == 0) {
-            mbar_init(bar_accum, C::kIssuers);
             mbar_init(bar_drain, C::kIssuers);
             *abort_flag = 0;
         }
@@ -462,282 +545,270 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     else __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-    float* sums = reinterpret_cast<float*>(smem);
 
     if (warp < kDecWarps) {
         // ---------------- weight decoders ----------------
         const int td = threadIdx.x;
-        const int quarter = warp & 3, sub = (warp >> 2) & 1, group = warp >> 3;
-        const int row = 32 * quarter + lane;
         const uint32_t raw0 = sbase + C::kOffRaw;
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         if (!kTma && !p.const_weights) pdl_wait_prerequisites();
-        // Publish a stage decoded into two runs of eight columns of tensor memory.
-        [[maybe_unused]] auto publish = [&](int i, uint32_t col0, const uint32_t (&o0)[8], uint32_t col1,
-                           const uint32_t (&o1)[8]) -> bool {
-            const int s = i % C::kAStages;
-            const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
-            if (i >= C::kAStages &&
-                !__all_sync(0xFFFFFFFFu,
-                            mbar_wait_bounded(bar_aempty + 8 * rel, ((i / C::kAStages) - 1) & 1,
-                                              abort_flag, err, kErrTimeoutEmpty)))
-                return false;
-            fence_after();  // the MMAs that read this stage are done
-            tmem_store8(t_lane + C::kColA + 32u * s + col0, o0);
-            tmem_store8(t_lane + C::kColA + 32u * s + col1, o1);
-            tmem_store_wait();
-            fence_before();
+        // wait for stage i's place, counted over all segments
+        auto stage_free = [&](int i) -> bool {
+            return i < S || __all_sync(0xFFFFFFFFu,
+                                       mbar_wait_bounded(bar_empty + 8 * (i % S), ((i / S) - 1) & 1,
+                                                         abort_flag, err, kErrTimeoutEmpty));
+        };
+        auto publish = [&](int i) {
+            fence_async_smem();  // this thread's stores -> visible to the MMA
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_afull + 8 * s);
-            return true;
+            if (lane == 0) mbar_arrive(bar_afull + 8 * (i % S));
         };
         if constexpr (kBack) {
             // group (four warps) takes every fourth stage: warp = 32 weight rows
             // and a segment, lane = the row, all four shifts
             const int own = warp >> 2, tg = td & 127;
             const int seg = warp & 1, n = 32 * ((warp >> 1) & 1) + lane;
-            const int block = n0 / kQK, half = (n0 / kRows) & 1;
-            if constexpr (!kTma) {
-                if (own < n_iters)
-                    issue_raw_rows(p, raw0 + own * C::kRawBytes, 4 * q0 + own, block, half, tg);
-                else
-                    cp_async_commit();
-            }
             bool ok = true;  // a warp that gave up still passes the group's barriers
-            for (int i = own; i < n_iters; i += 4) {
-                const int slot = i % C::kRaw;
-                const uint32_t raw = raw0 + slot * C::kRawBytes + n * C::kRawPitch;
-                uint32_t at_sc = raw, at_q = raw + 8, at_d = raw + 40;
-                if constexpr (kTma) {
-                    ok = ok && __all_sync(0xFFFFFFFFu,
-                                          mbar_wait_bounded(bar_raw + 8 * slot, (i / C::kRaw) & 1,
-                                                            abort_flag, err, kErrTimeoutEmpty));
-                    const uint32_t at = raw + ((kBlockBytes * block) & 15);  // (a 16-byte boundary)
-                    at_sc = at + 8 * half;
-                    at_q = at + 16 + 32 * half;
-                    at_d = at + 80;
-                } else {
-                    // the group's other slot was read before this barrier
-                    if (i + 4 < n_iters) {
-                        asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
-                        issue_raw_rows(p, raw0 + ((i + 4) % C::kRaw) * C::kRawBytes, 4 * q0 + i + 4,
-                                       block, half, tg);
-                        cp_async_wait<1>();
-                    } else {
-                        cp_async_wait<0>();
+            int i = own;     // this group's stages, counted over all segments
+            // without TMA: the next stage to fetch (a slot ahead of the decode)
+            Segment fetch;
+            int fetch_index = 0, fetch_q = 0, fetched = own;
+            bool more = false;
+            [[maybe_unused]] auto fetch_next = [&]() {
+                if (more) {
+                    issue_raw_rows(p, raw0 + (fetched % C::kRaw) * C::kRawBytes, 4 * fetch_q + own,
+                                   row0(fetch.tile) / kQK, (row0(fetch.tile) / kRows) & 1, tg);
+                    fetched += 4;
+                    if (++fetch_q == fetch.q1) {
+                        more = work.segment(++fetch_index, fetch);
+                        fetch_q = fetch.q0;
                     }
-                    asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
+                } else {
+                    cp_async_commit();
                 }
-                if (!ok) continue;
-                uint32_t q[4];
+            };
+            if constexpr (!kTma) {
+                more = work.segment(0, fetch);
+                fetch_q = fetch.q0;
+                fetch_next();
+            }
+            for (int index = 0; work.segment(index, sg); ++index) {
+                const int block = row0(sg.tile) / kQK, half = (row0(sg.tile) / kRows) & 1;
+                for (int q = sg.q0; q < sg.q1; ++q, i += 4) {
+                    const int slot = i % C::kRaw;
+                    const uint32_t raw = raw0 + slot * C::kRawBytes + n * C::kRawPitch;
+                    uint32_t at_sc = raw, at_q = raw + 8, at_d = raw + 40;
+                    if constexpr (kTma) {
+                        ok = ok && __all_sync(0xFFFFFFFFu,
+                                              mbar_wait_bounded(bar_raw + 8 * slot, (i / C::kRaw) & 1,
+                                                                abort_flag, err, kErrTimeoutEmpty));
+                        const uint32_t at = raw + ((kBlockBytes * block) & 15);  // (a 16-byte boundary)
+                        at_sc = at + 8 * half;
+                        at_q = at + 16 + 32 * half;
+                        at_d = at + 80;
+                    } else {
+                        // the group's other slot was read before this barrier
+                        asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
+                        fetch_next();
+                        cp_async_wait<1>();
+                        asm volatile("bar.sync %0, 128;" ::"r"(3 + own) : "memory");
+                    }
+                    if (!ok) continue;
+                    uint32_t qw[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) q[e] = ld_shared_u32(at_q + 16 * seg + 4 * e);
-                const uint32_t sc0 = ld_shared_u32(at_sc) >> (8 * seg);
-                const uint32_t sc1 = ld_shared_u32(at_sc + 4) >> (8 * seg);
-                const uint32_t dd = ld_shared_u32(at_d);
-                if constexpr (kTma) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
+                    for (int e = 0; e < 4; ++e) qw[e] = ld_shared_u32(at_q + 16 * seg + 4 * e);
+                    const uint32_t sc0 = ld_shared_u32(at_sc) >> (8 * seg);
+                    const uint32_t sc1 = ld_shared_u32(at_sc + 4) >> (8 * seg);
+                    const uint32_t dd = ld_shared_u32(at_d);
+                    if constexpr (kTma) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
+                    }
+                    const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+                    uint32_t o[4][8];
+                    decode_segment<0>(qw, sc0 & 0xFFu, d, dmin, o[0]);
+                    decode_segment<1>(qw, (sc0 >> 16) & 0xFFu, d, dmin, o[1]);
+                    decode_segment<2>(qw, sc1 & 0xFFu, d, dmin, o[2]);
+                    decode_segment<3>(qw, (sc1 >> 16) & 0xFFu, d, dmin, o[3]);
+                    ok = stage_free(i);
+                    if (!ok) continue;
+                    // row n of the stage: 128 bytes of columns 64 c .. at 8192 c +
+                    // 128 n, its 16-byte chunks swizzled by n % 8
+                    const uint32_t dst = sbase + C::kOffA + (i % S) * kABytes + 128 * n;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            st_shared_v4(dst + 8192 * (j >> 1) +
+                                             (((4 * (j & 1) + 2 * seg + c) ^ (n & 7)) << 4),
+                                         o[j][4 * c], o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
+                    publish(i);
                 }
-                const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
-                uint32_t o[4][8];
-                decode_segment<0>(q, sc0 & 0xFFu, d, dmin, o[0]);
-                decode_segment<1>(q, (sc0 >> 16) & 0xFFu, d, dmin, o[1]);
-                decode_segment<2>(q, sc1 & 0xFFu, d, dmin, o[2]);
-                decode_segment<3>(q, (sc1 >> 16) & 0xFFu, d, dmin, o[3]);
-                const int s = i % C::kAStages;
-                const int rel = (C::kPairs ? (i | 1) : i) % C::kAStages;
-                if (i >= C::kAStages)
-                    ok = __all_sync(0xFFFFFFFFu,
-                                    mbar_wait_bounded(bar_aempty + 8 * rel, ((i / C::kAStages) - 1) & 1,
-                                                      abort_flag, err, kErrTimeoutEmpty));
-                if (!ok) continue;
-                // row n of the tile: 128 bytes of columns 64 c .. at 8192 c +
-                // 128 n, its 16-byte chunks swizzled by n % 8
-                const uint32_t dst = sbase + C::kOffA + s * kABytes + 128 * n;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        st_shared_v4(dst + 8192 * (j >> 1) +
-                                         (((4 * (j & 1) + 2 * seg + c) ^ (n & 7)) << 4),
-                                     o[j][4 * c], o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
-                fence_async_smem();  // this thread's stores -> visible to the MMA
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_afull + 8 * s);
             }
         } else {
+            // group (four warps) takes stage `own` of every block, thread = a
+            // weight row: shifts 2 (own % 2) and + 1 of half own / 2, both segments
+            const int row = 32 * (warp & 3) + lane, own = warp >> 2;
             const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
-            if constexpr (!kTma) {
-                for (int b = 0; b < C::kRaw - 1; ++b) {
-                    if (b < n_quads)
-                        issue_raw(p.w0, p.w1, kSplit0, raw0 + b * C::kRawBytes, n0, p.N, row_bytes,
-                                  q0 + b, td);
-                    else
-                        cp_async_commit();
+            // without TMA: the next block to fetch (kRaw - 1 ahead of the decode)
+            Segment fetch;
+            int fetch_index = 0, fetch_q = 0, fetched = 0;
+            bool more = false;
+            [[maybe_unused]] auto fetch_next = [&]() {
+                if (more) {
+                    issue_raw(p.w0, p.w1, kSplit0, raw0 + (fetched % C::kRaw) * C::kRawBytes,
+                              row0(fetch.tile), p.N, row_bytes, fetch_q, td);
+                    ++fetched;
+                    if (++fetch_q == fetch.q1) {
+                        more = work.segment(++fetch_index, fetch);
+                        fetch_q = fetch.q0;
+                    }
+                } else {
+                    cp_async_commit();
                 }
+            };
+            if constexpr (!kTma) {
+                more = work.segment(0, fetch);
+                fetch_q = fetch.q0;
+                for (int r = 0; r < C::kRaw - 1; ++r) fetch_next();
             }
             bool ok = true;
-            for (int b = 0; b < n_quads && ok; ++b) {
-                const int buf = b % C::kRaw;
-                uint32_t mine = raw0 + buf * C::kRawBytes + row * C::kRawPitch;
-                if constexpr (!kTma) {
-                    cp_async_wait<C::kRaw - 2>();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_raw + 8 * buf);
-                }
-                if (!__all_sync(0xFFFFFFFFu,
-                                mbar_wait_bounded(bar_raw + 8 * buf, (b / C::kRaw) & 1, abort_flag,
-                                                  err, kErrTimeoutEmpty)))
-                    break;
-                if constexpr (kTma) {
-                    mine += 4 * ((q0 + b) & 3);  // the box starts at a 16-byte boundary
-                } else {
-                    // every decoder has read block b - 1: its slot takes block b + kRaw - 1
-                    const int nb = b + C::kRaw - 1;
-                    if (nb < n_quads)
-                        issue_raw(p.w0, p.w1, kSplit0, raw0 + (nb % C::kRaw) * C::kRawBytes, n0, p.N,
-                                  row_bytes, q0 + nb, td);
-                    else
-                        cp_async_commit();
-                }
-                uint32_t sh[2], qh[4];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) sh[q] = ld_shared_u32(mine + 8 * group + 4 * q) >> (8 * sub);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    qh[e] = ld_shared_u32(mine + 16 + 32 * group + 16 * sub + 4 * e);
-                const uint32_t dd = ld_shared_u32(mine + 80);
-                if constexpr (kTma) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_rawempty + 8 * buf);
-                }
-                const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
-#pragma unroll
-                for (int cp = 0; cp < 2; ++cp) {
-                    uint32_t o0[8], o1[8];
-                    if (cp == 0) decode_half_stage<0>(qh, sh, d, dmin, o0, o1);
-                    else decode_half_stage<1>(qh, sh, d, dmin, o0, o1);
-                    if (!publish(4 * b + 2 * group + cp, 8u * sub, o0, 8u * sub + 16u, o1)) {
-                        ok = false;
-                        break;
+            int b = 0;  // blocks, counted over all segments
+            for (int index = 0; ok && work.segment(index, sg); ++index) {
+                for (int q = sg.q0; q < sg.q1 && ok; ++q, ++b) {
+                    const int buf = b % C::kRaw;
+                    uint32_t mine = raw0 + buf * C::kRawBytes + row * C::kRawPitch;
+                    if constexpr (!kTma) {
+                        cp_async_wait<C::kRaw - 2>();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_raw + 8 * buf);
                     }
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_raw + 8 * buf, (b / C::kRaw) & 1,
+                                                                   abort_flag, err, kErrTimeoutEmpty));
+                    if (!ok) break;
+                    if constexpr (kTma) mine += 4 * (q & 3);  // the box starts at a 16-byte boundary
+                    else fetch_next();  // every decoder has read block b - 1: its slot is free
+                    const int half = own >> 1;
+                    const uint32_t sc = ld_shared_u32(mine + 8 * half + 4 * (own & 1));
+                    uint32_t qw[2][4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        qw[e >> 2][e & 3] = ld_shared_u32(mine + 16 + 32 * half + 4 * e);
+                    const uint32_t dd = ld_shared_u32(mine + 80);
+                    if constexpr (kTma) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_rawempty + 8 * buf);
+                    }
+                    const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
+                    uint32_t o[4][8];  // (shift, segment)
+                    if (own & 1) {
+                        decode_segment<2>(qw[0], sc & 0xFFu, d, dmin, o[0]);
+                        decode_segment<2>(qw[1], (sc >> 8) & 0xFFu, d, dmin, o[1]);
+                        decode_segment<3>(qw[0], (sc >> 16) & 0xFFu, d, dmin, o[2]);
+                        decode_segment<3>(qw[1], sc >> 24, d, dmin, o[3]);
+                    } else {
+                        decode_segment<0>(qw[0], sc & 0xFFu, d, dmin, o[0]);
+                        decode_segment<0>(qw[1], (sc >> 8) & 0xFFu, d, dmin, o[1]);
+                        decode_segment<1>(qw[0], (sc >> 16) & 0xFFu, d, dmin, o[2]);
+                        decode_segment<1>(qw[1], sc >> 24, d, dmin, o[3]);
+                    }
+                    const int i = 4 * b + own;
+                    ok = stage_free(i);
+                    if (!ok) break;
+                    const uint32_t dst = sbase + C::kOffA + (i % S) * kABytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            st_shared_v4(dst + sw128_offset(row, 2 * j + c), o[j][4 * c],
+                                         o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
+                    publish(i);
                 }
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
-
-        // ---------------- the tile's sums to shared memory ----------------
-        if (__all_sync(0xFFFFFFFFu, mbar_wait_backoff(bar_accum, 0, abort_flag, err,
-                                                      kErrTimeoutAccum, 512))) {
-            fence_after();
-#pragma unroll 1
-            for (int c0 = 16 * (warp >> 2); c0 < nx; c0 += 64) {
-                float v[16];
-                tmem_load16(t_lane + c0, v);
-                if (C::kIssuers == 2) {
-                    float u[16];
-                    tmem_load16(t_lane + kX + c0, u);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] += u[q];
-                }
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    if (c0 + q < tokens) sums[(c0 + q) * kSumPitch + row] = v[q];
-            }
-        }
     } else if ((warp == kMmaWarp && peer == 0) || (C::kIssuers == 2 && warp == kWaitWarp)) {
         // ---------------- MMA issuers ----------------
-        // The waiter waits for the next kHand stages and meets the MMA warp at
-        // named barrier 1; both pass it n_iters / kHand times whatever happens.
-        // With two issuers the MMA warp takes the even stages into accumulator
-        // 0, the waiter the odd ones into accumulator 1.
+        // The waiter waits for the next two stages and meets the MMA warp at named
+        // barrier 1; both pass it once for every two stages, whatever happens.
+        // With two issuers the MMA warp takes the even stages into one
+        // accumulator, the waiter the odd ones into another.
         const int me = warp == kMmaWarp ? 0 : 1;
-        const uint32_t idesc = bf16_idesc(kDuo ? 2 * kRows : kRows, nx) | (kBack ? kIdescAMnMajor : 0u);
         const uint64_t xdesc0 = sw128_desc(sbase);
-        const uint64_t adesc0 = sw128_mn_desc(sbase + C::kOffA, 8192);
-        const uint32_t acc = tmem + static_cast<uint32_t>(me * kX);
-        for (int i0 = 0; i0 < n_iters; i0 += C::kHand) {
-            if (C::kIssuers == 2 && me == 1 && lane == 0 && !*abort_flag) {
+        const uint64_t adesc0 = kBack ? sw128_mn_desc(sbase + C::kOffA, 8192)
+                                      : sw128_desc(sbase + C::kOffA);
+        int i0 = 0;  // stages, counted over all segments
+        for (int index = 0; work.segment(index, sg); ++index) {
+            const uint32_t idesc = bf16_idesc(C::kCtas * kRows, mma_n(sg.tile)) | (kBack ? kIdescAMnMajor : 0u);
+            const uint32_t acc = tmem + (index & 1) * C::kAccCols + static_cast<uint32_t>(me * kX);
+            const int n_iters = 4 * (sg.q1 - sg.q0);
+            for (int l0 = 0; l0 < n_iters; l0 += C::kHand, i0 += C::kHand) {
+                if (C::kIssuers == 2 && me == 1 && lane == 0 && !*abort_flag) {
+                    bool ok = l0 > 0 || index < 2 ||
+                              mbar_wait_bounded(bar_accempty + 8 * (index & 1), ((index >> 1) - 1) & 1,
+                                                abort_flag, err, kErrTimeoutAccum);
 #pragma unroll
-                for (int u = 0; u < C::kHand; ++u) {
-                    const int i = i0 + u;
-                    if (!mbar_wait_bounded(bar_xfull + 8 * (i % C::kXStages), (i / C::kXStages) & 1,
-                                           abort_flag, err, kErrTimeoutFull) ||
-                        !mbar_wait_bounded(bar_afull + 8 * (i % C::kAStages), (i / C::kAStages) & 1,
-                                           abort_flag, err, kErrTimeoutFull))
-                        break;
-                }
-            }
-            __syncwarp();
-            asm volatile("bar.sync 1, 64;" ::: "memory");
-            if (lane == 0 && !*abort_flag) {
-                fence_after();
-#pragma unroll
-                for (int u = 0; u < C::kHand; ++u) {
-                    if (C::kIssuers == 2 && (u & 1) != me) continue;
-                    const int i = i0 + u;
-                    const int sx = i % C::kXStages, sa = i % C::kAStages;
-                    const uint64_t xdesc = xdesc0 + static_cast<uint64_t>(sx * (C::kXStage >> 4));
-                    const uint32_t a_s = tmem + C::kColA + 32u * sa;
-                    const uint64_t adesc = adesc0 + static_cast<uint64_t>(sa * (kABytes >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < kStageK / 16; ++kk) {
-                        const uint32_t add = i >= C::kIssuers || kk > 0;
-                        if (kBack)  // (a K-step is 16 rows of 128 bytes)
-                            mma_smem<kDuo>(acc, adesc + 128u * kk, xdesc + 2u * kk, idesc, add);
-                        else
-                            mma<kDuo>(acc, a_s + 8u * kk, xdesc + 2u * kk, idesc, add);
-                    }
-                    // a stage is released when a later one takes its place
-                    if (C::kPairs) {
-                        if ((i & ~1) + C::kAStages < n_iters)
-                            commit<kDuo>(bar_aempty + 8 * ((i | 1) % C::kAStages));
-                    } else {
-                        if (i + C::kAStages < n_iters) commit<kDuo>(bar_aempty + 8 * sa);
-                        if (i + C::kXStages < n_iters) commit<kDuo>(bar_xempty + 8 * sx);
+                    for (int u = 0; u < C::kHand; ++u) {
+                        const int i = i0 + u;
+                        ok = ok && mbar_wait_bounded(bar_xfull + 8 * (i % S), (i / S) & 1, abort_flag,
+                                                     err, kErrTimeoutFull) &&
+                             mbar_wait_bounded(bar_afull + 8 * (i % S), (i / S) & 1, abort_flag, err,
+                                               kErrTimeoutFull);
                     }
                 }
+                __syncwarp();
+                asm volatile("bar.sync 1, 64;" ::: "memory");
+                if (lane == 0 && !*abort_flag) {
+                    fence_after();
+#pragma unroll
+                    for (int u = 0; u < C::kHand; ++u) {
+                        if (C::kIssuers == 2 && u != me) continue;
+                        const int s = (i0 + u) % S;
+                        const uint64_t xdesc = xdesc0 + static_cast<uint64_t>(s * (C::kXStage >> 4));
+                        const uint64_t adesc = adesc0 + static_cast<uint64_t>(s * (kABytes >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < kStageK / 16; ++kk)  // (backward: a K-step is 16 rows)
+                            mma<kDuo>(acc, adesc + (kBack ? 128u : 2u) * kk, xdesc + 2u * kk, idesc,
+                                      l0 + u >= C::kIssuers || kk > 0);
+                        commit<kDuo>(bar_empty + 8 * s);
+                    }
+                    if (l0 + C::kHand == n_iters) commit<kDuo>(bar_accfull + 8 * (index & 1));
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
-        if (lane == 0) {
-            if (!*abort_flag) {
-                commit<kDuo>(bar_accum);
-            } else {
-                // no MMA may still write TMEM when it is freed
-                commit<kDuo>(bar_drain);
-                volatile int no_abort = 0;
-                mbar_wait_bounded(bar_drain, 0, &no_abort, err, kErrTimeoutDrain);
-            }
+        if (lane == 0 && *abort_flag) {
+            // no MMA may still write TMEM when it is freed
+            commit<kDuo>(bar_drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(bar_drain, 0, &no_abort, err, kErrTimeoutDrain);
         }
         __syncwarp();
     } else if (kDuo && warp == kWaitWarp) {
         // ---------------- stage waiters of a pair of CTAs ----------------
         // The second CTA's waiter reports each of its stages to the first's,
         // which waits for both CTAs' and hands them to the MMA warp.
-        for (int i0 = 0; i0 < n_iters; i0 += C::kHand) {
-            if (lane == 0 && !*abort_flag) {
+        int i0 = 0;
+        for (int index = 0; work.segment(index, sg); ++index) {
+            const int n_iters = 4 * (sg.q1 - sg.q0);
+            for (int l0 = 0; l0 < n_iters; l0 += C::kHand, i0 += C::kHand) {
+                if (lane == 0 && !*abort_flag) {
+                    bool ok = peer == 1 || l0 > 0 || index < 2 ||
+                              wait_peer_bounded(bar_accempty + 8 * (index & 1), ((index >> 1) - 1) & 1,
+                                                abort_flag, err, kErrTimeoutAccum);
 #pragma unroll
-                for (int u = 0; u < C::kHand; ++u) {
-                    const int i = i0 + u, sa = i % C::kAStages;
-                    const uint32_t phase = (i / C::kAStages) & 1;
-                    if (!mbar_wait_bounded(bar_xfull + 8 * (i % C::kXStages), (i / C::kXStages) & 1,
-                                           abort_flag, err, kErrTimeoutFull) ||
-                        !mbar_wait_bounded(bar_afull + 8 * sa, phase, abort_flag, err, kErrTimeoutFull))
-                        break;
-                    if (peer == 1) {
-                        fence_after();
-                        fence_before();
-                        arrive_first_of_pair(bar_peer + 8 * sa);
-                    } else if (!wait_peer_bounded(bar_peer + 8 * sa, phase, abort_flag, err,
-                                                  kErrTimeoutFull)) {
-                        break;
+                    for (int u = 0; u < C::kHand; ++u) {
+                        const int i = i0 + u;
+                        const uint32_t at = 8 * (i % S), phase = (i / S) & 1;
+                        ok = ok && mbar_wait_bounded(bar_xfull + at, phase, abort_flag, err, kErrTimeoutFull) &&
+                             mbar_wait_bounded(bar_afull + at, phase, abort_flag, err, kErrTimeoutFull);
+                        if (ok && peer == 1) arrive_first_of_pair(bar_peer + at);
+                        if (peer == 0)
+                            ok = ok && wait_peer_bounded(bar_peer + at, phase, abort_flag, err, kErrTimeoutFull);
                     }
                 }
+                __syncwarp();
+                if (peer == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
             }
-            __syncwarp();
-            if (peer == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
         }
     } else if (warp == kWWarp) {
         // ---------------- raw weight blocks ----------------
@@ -745,39 +816,38 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             tma_prefetch_map(&maps.w0);
             if (kMode != Tc::kLora) tma_prefetch_map(&maps.w1);
             if (!p.const_weights) pdl_wait_prerequisites();
-            const int n_raw = kBack ? n_iters : n_quads;
-            for (int b = 0; b < n_raw; ++b) {
-                const int buf = b % C::kRaw;
-                if (b >= C::kRaw &&
-                    !mbar_wait_bounded(bar_rawempty + 8 * buf, ((b / C::kRaw) - 1) & 1, abort_flag,
-                                       err, kErrTimeoutEmpty))
-                    break;
-                const uint32_t dst = sbase + C::kOffRaw + buf * C::kRawBytes;
-                const uint32_t bar = bar_raw + 8 * buf;
-                mbar_arrive_expect_tx(bar, C::kRawBytes);
-                if constexpr (kBack) {
-                    const int stage = 4 * q0 + b;
-                    const bool up = stage >= p.half_stages;
-                    tma_load_2d(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
-                                kStageK * (up ? stage - p.half_stages : stage), bar);
-                } else {
-                    const int x = (kBlockBytes * (q0 + b)) & ~15;
-                    tma_load_2d(dst, &maps.w0, x, n0, bar);
-                    if (kMode == Tc::kGated)
-                        tma_load_2d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, bar);
+            int b = 0;
+            bool ok = true;
+            for (int index = 0; ok && work.segment(index, sg); ++index) {
+                const int n0 = row0(sg.tile);
+                for (int r = 0; ok && r < (sg.q1 - sg.q0) * (kBack ? 4 : 1); ++r, ++b) {
+                    const int buf = b % C::kRaw;
+                    ok = b < C::kRaw ||
+                         mbar_wait_bounded(bar_rawempty + 8 * buf, ((b / C::kRaw) - 1) & 1, abort_flag,
+                                           err, kErrTimeoutEmpty);
+                    if (!ok) break;
+                    const uint32_t dst = sbase + C::kOffRaw + buf * C::kRawBytes;
+                    const uint32_t bar = bar_raw + 8 * buf;
+                    mbar_arrive_expect_tx(bar, C::kRawBytes);
+                    if constexpr (kBack) {
+                        const int stage = 4 * sg.q0 + r;
+                        const bool up = stage >= p.half_stages;
+                        tma_load_2d(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
+                                    kStageK * (up ? stage - p.half_stages : stage), bar);
+                    } else {
+                        const int x = (kBlockBytes * (sg.q0 + r)) & ~15;
+                        tma_load_2d(dst, &maps.w0, x, n0, bar);
+                        if (kMode == Tc::kGated)
+                            tma_load_2d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, bar);
+                    }
                 }
             }
             if (*abort_flag) linger();
         }
         __syncwarp();
-    } else if (warp >= kXWarp0) {
-        // ---------------- token stages, even and odd ----------------
+    } else if (warp == kXWarp) {
+        // ---------------- token stages ----------------
         if (lane == 0) {
-            const uint8_t* src = p.xa +
-                                 (static_cast<size_t>(m0 / kSuperRows) * p.stages + 4 * q0) *
-                                     kSuperBytes +
-                                 static_cast<size_t>(m_held % kSuperRows) * (kStageK * 2);
-            const uint32_t bytes = p.xa != nullptr ? held * (kStageK * 2) : C::kXStage;
             if (p.xa == nullptr) {
                 tma_prefetch_map(&maps.x0);
                 if (kBack) tma_prefetch_map(&maps.x1);
@@ -786,107 +856,179 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 pdl_wait_prerequisites();  // the tokens
                 pdl_allow_dependents();
             }
-            for (int i = warp - kXWarp0; i < n_iters; i += 2) {
-                const int s = i % C::kXStages;
-                if (i >= C::kXStages &&
-                    !mbar_wait_bounded(C::kPairs ? bar_aempty + 8 * ((i | 1) % C::kAStages)
-                                                 : bar_xempty + 8 * s,
-                                       ((i / C::kXStages) - 1) & 1, abort_flag, err, kErrTimeoutEmpty))
-                    break;
-                const uint32_t dst = sbase + s * C::kXStage, bar = bar_xfull + 8 * s;
-                mbar_arrive_expect_tx(bar, bytes);
-                if (p.xa != nullptr) {
-                    bulk_copy_g2s(dst, src + static_cast<size_t>(i) * kSuperBytes, bytes, bar);
-                } else {
-                    // (tokens past M and, backward, weight rows past N read as zeros)
-                    const int stage = 4 * q0 + i;
-                    const bool up = kBack && stage >= p.half_stages;
-                    tma_load_2d(dst, up ? &maps.x1 : &maps.x0,
-                                kStageK * (up ? stage - p.half_stages : stage), m_held, bar);
+            int i = 0;
+            bool ok = true;
+            for (int index = 0; ok && work.segment(index, sg); ++index) {
+                // two CTAs: this one holds tokens [peer N / 2, peer N / 2 + N / 2)
+                const int held = mma_n(sg.tile) / C::kCtas;
+                const int m_held = token0(sg.tile) + peer * held;
+                const uint8_t* src = p.xa +
+                                     static_cast<size_t>(m_held / kSuperRows) * 4 * p.quads * kSuperBytes +
+                                     static_cast<size_t>(m_held % kSuperRows) * (kStageK * 2);
+                const uint32_t bytes = p.xa != nullptr ? held * (kStageK * 2) : C::kXStage;
+                for (int stage = 4 * sg.q0; stage < 4 * sg.q1; ++stage, ++i) {
+                    ok = i < S || mbar_wait_bounded(bar_empty + 8 * (i % S), ((i / S) - 1) & 1, abort_flag,
+                                                    err, kErrTimeoutEmpty);
+                    if (!ok) break;
+                    const uint32_t dst = sbase + (i % S) * C::kXStage, bar = bar_xfull + 8 * (i % S);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (p.xa != nullptr) {
+                        bulk_copy_g2s(dst, src + static_cast<size_t>(stage) * kSuperBytes, bytes, bar);
+                    } else {
+                        // (tokens past M and, backward, weight rows past N read as zeros)
+                        const bool up = kBack && stage >= p.half_stages;
+                        tma_load_2d(dst, up ? &maps.x1 : &maps.x0,
+                                    kStageK * (up ? stage - p.half_stages : stage), m_held, bar);
+                    }
                 }
             }
             if (*abort_flag) linger();
         }
         __syncwarp();
     }
+    if (warp >= kEpiWarp0 || warp < kDecWarps) {
+        // ---------------- epilogue: sums -> results ----------------
+        // (what is written here, and t, may still be in use by the grid before)
+        pdl_wait_prerequisites();
+        if (p.tokens_ready) pdl_allow_dependents();
+        const int segments = work.count();
+        [[maybe_unused]] AdapterFragments fragments;
+        // the decoders come for the last segment
+        for (int index = warp < kDecWarps ? segments - 1 : 0; work.segment(index, sg); ++index) {
+            const bool final = index == segments - 1;
+            Team team;
+            team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
+                                           : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
+            team.threads = final ? 128 + kDecThreads : 128;
+            team.barrier = final ? 7 : 2;
+            mbar_wait_backoff(bar_accfull + 8 * (index & 1), (index >> 1) & 1, abort_flag, err,
+                              kErrTimeoutAccum, 512);
+            // all of the team go on, or none (after a time-out they still meet
+            // the decoders at the last segment)
+            team.sync();
+            if (team.thread == 0) *shared_word = *abort_flag;
+            team.sync();
+            const bool stop = *shared_word != 0;
+            team.sync();
+            if (stop) continue;
+            fence_after();
+            // the last tile's sums take the place of the rings
+            float* sums = reinterpret_cast<float*>(smem + (final ? 0 : C::kOffSums));
+            const int chunk = final ? kX : kChunk;
+            const int n0 = row0(sg.tile), m0 = token0(sg.tile);
+            const int tokens = min(kX, p.M - m0);
+            const int quarter = (team.thread >> 5) & 3, my_row = 32 * quarter + lane;
+            const int strip = 16 * (team.thread >> 7), strips = 16 * (team.threads >> 7);
+            const uint32_t t_lane = tmem + (index & 1) * C::kAccCols +
+                                    (static_cast<uint32_t>(32 * quarter) << 16);
+            // 16 tokens of this lane's row, from c0 on
+            auto load_sums = [&](int c0, float (&v)[16]) {
+                tmem_load16(t_lane + c0, v);
+                if (C::kIssuers == 2) {
+                    float u[16];
+                    tmem_load16(t_lane + kX + c0, u);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] += u[q];
+                }
+            };
+            auto release = [&]() {  // the sums are read: their set may be reused
+                if (final) return;  // (by none)
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kDuo) arrive_first_of_pair(bar_accempty + 8 * (index & 1));
+                    else mbar_arrive(bar_accempty + 8 * (index & 1));
+                }
+            };
+            int first = 0, last = 0;
+            if (sg.run >= 0) {
+                // A run of a cut tile: its sums go to the workspace, and the CTA
+                // that counts last adds the runs.  The barrier and the fence
+                // order every thread's stores before the count; the second fence
+                // orders the count before the loads.
+                float* mine = p.partial + static_cast<size_t>((2 * work.w + sg.run) * C::kCtas + peer) * (kX * kRows);
+                for (int c0 = strip; c0 < tokens; c0 += strips) {
+                    float v[16];
+                    load_sums(c0, v);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (c0 + q < tokens) mine[(c0 + q) * kRows + my_row] = v[q];
+                }
+                release();
+                work.sharers(sg.tile, first, last);
+                team.sync();
+                if (team.thread == 0) {
+                    __threadfence();
+                    const unsigned before =
+                        atomicAdd(p.counts + (sg.tile - p.whole) * C::kCtas + peer, 1u);
+                    __threadfence();
+                    *shared_word = before == static_cast<unsigned>(last - first);
+                }
+                team.sync();
+                const bool add = *shared_word != 0;
+                team.sync();  // (the word is read before the next segment writes it)
+                if (!add) continue;
+            }
+            for (int c0 = 0; c0 < tokens; c0 += chunk) {
+                const int count = min(chunk, tokens - c0);
+                if (sg.run < 0) {
+                    for (int h = strip; h < count; h += strips) {
+                        float v[16];
+                        load_sums(c0 + h, v);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sums[(h + q) * kSumPitch + my_row] = v[q];
+                    }
+                    if (c0 + chunk >= tokens) release();
+                } else {
+                    const int quads = count * (kRows / 4);
+                    for (int i0 = team.thread; i0 < quads; i0 += 4 * team.threads) {
+                        float4 a[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int v = first; v <= last; ++v) {
+                            const float4* src = reinterpret_cast<const float4*>(
+                                p.partial + static_cast<size_t>((2 * v + work.run_of(v, sg.tile)) * C::kCtas + peer) *
+                                                (kX * kRows)) + c0 * (kRows / 4);
+                            float4 x[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                x[u] = i0 + team.threads * u < quads ? __ldcg(src + i0 + team.threads * u)
+                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                a[u].x += x[u].x;
+                                a[u].y += x[u].y;
+                                a[u].z += x[u].z;
+                                a[u].w += x[u].w;
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int i = i0 + team.threads * u;
+                            if (i < quads)
+                                *reinterpret_cast<float4*>(sums + (i / (kRows / 4)) * kSumPitch +
+                                                           4 * (i % (kRows / 4))) = a[u];
+                        }
+                    }
+                }
+                team.sync();
+                if constexpr (kMode == Tc::kLora) {
+                    uint32_t* tbuf = final ? reinterpret_cast<uint32_t*>(sums + kX * kSumPitch)
+                                           : reinterpret_cast<uint32_t*>(smem + C::kOffT);
+                    int* id_buf = final ? reinterpret_cast<int*>(tbuf + 64 * kX)
+                                        : reinterpret_cast<int*>(smem + C::kOffIds);
+                    add_adapters(fragments, sums, tbuf, id_buf, p, n0, m0 + c0, count, team);
+                }
+                emit<kMode, T>(p, sums, n0, rows, m0 + c0, count, team);
+                team.sync();
+            }
+            fragments.cur = -1;  // (another tile has other rows)
+        }
+    }
 
-    // ---------------- epilogue ----------------
-    // Every thread of every CTA of a cluster passes its barriers, whatever
-    // happened before.  Part r takes its share of the tile's tokens (whole
-    // groups of eight) and adds them over the parts in order; the second
-    // cluster barrier keeps every part's sums alive until all are read.
-    int first = 0, end = tokens;
-    if (parts > 1) {  // (cluster rank: row tile of the pair + 2 part, or the part)
-        const int groups = (tokens + 7) / 8, z = blockIdx.z;
-        first = 8 * (z * groups / parts);
-        end = min(tokens, 8 * ((z + 1) * groups / parts));
-        __syncwarp();
-        cluster_sync();
-    } else if (warp < kDecWarps) {
-        dec_barrier();
-    }
-    // past these barriers no wait is left that could raise the flag
-    const bool done = *abort_flag == 0;
-    if (warp < kDecWarps && parts > 1) {
-        for (int j = first * (kRows / 4) + threadIdx.x; j < end * (kRows / 4); j += kDecThreads) {
-            const int i = j / (kRows / 4) * (kSumPitch / 4) + j % (kRows / 4);
-            float4 v[kMaxParts];
-#pragma unroll
-            for (int z = 0; z < kMaxParts; ++z)
-                if (z < parts) v[z] = load_cluster4(sbase + 16 * i, kDuo ? 2 * z + peer : z);
-            float4 a = v[0];
-#pragma unroll
-            for (int z = 1; z < kMaxParts; ++z)
-                if (z < parts) {
-                    a.x += v[z].x;
-                    a.y += v[z].y;
-                    a.z += v[z].z;
-                    a.w += v[z].w;
-                }
-            reinterpret_cast<float4*>(sums)[i] = a;
-        }
-        dec_barrier();
-    }
-    if (warp < kDecWarps && done) {
-        const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
-        if constexpr (kMode == Tc::kGated) {
-            // a warp takes a token at a time, a lane the rows 2 lane, 2 lane + 1
-            for (int c = first + warp; c < end; c += kDecWarps) {
-                const float2 g = *reinterpret_cast<const float2*>(sums + c * kSumPitch + 2 * lane);
-                const float2 u =
-                    *reinterpret_cast<const float2*>(sums + c * kSumPitch + kSplit0 + 2 * lane);
-                const int n = n0 + 2 * lane;
-                const int valid = rows - n;
-                if (valid <= 0) continue;
-                const size_t at = static_cast<size_t>(m0 + c) * rows + n;
-                store_pair(static_cast<T*>(p.h) + at, act_value<sizeof(T) == 2>(g.x, p.act) * u.x,
-                           act_value<sizeof(T) == 2>(g.y, p.act) * u.y, valid, vec);
-                if (p.gate != nullptr) {
-                    store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
-                    store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
-                }
-            }
-        } else {
-            if constexpr (kMode == Tc::kLora) {
-                pdl_wait_prerequisites();  // t (written by this grid or one before)
-                uint32_t* tbuf = reinterpret_cast<uint32_t*>(sums + kX * kSumPitch);
-                add_adapters(sums, tbuf, reinterpret_cast<int*>(tbuf + kX * 64), p, n0, m0, first, end);
-            }
-            for (int c = first + warp; c < end; c += kDecWarps)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int r = 64 * q + 2 * lane;
-                    const float2 v = *reinterpret_cast<const float2*>(sums + c * kSumPitch + r);
-                    const int valid = rows - (n0 + r);
-                    if (valid > 0)
-                        store_pair(static_cast<T*>(p.y) + static_cast<size_t>(m0 + c) * rows + n0 + r,
-                                   v.x, v.y, valid, vec);
-                }
-        }
-    }
     fence_before();
     __syncwarp();
-    if (kDuo || parts > 1) cluster_sync();
+    if (kDuo) cluster_sync();
     else __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
@@ -898,8 +1040,11 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
 // zeros (their sums are dropped, but the MMA reads them).  One thread writes
 // 16-byte chunks, four per pass with their loads issued together.
 __global__ void __launch_bounds__(256)
-x_image_kernel(const float* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, size_t chunks) {
+x_image_kernel(const float* __restrict__ x, uint8_t* __restrict__ xa, int M, int K, size_t chunks,
+               unsigned int* __restrict__ counts, int n_counts) {
     pdl_allow_dependents();
+    if (blockIdx.x == 0)
+        for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
     const int per_row = K / 8, stages = K / kStageK;
     const size_t stride = static_cast<size_t>(gridDim.x) * blockDim.x;
     constexpr int kPer = 4;
@@ -938,8 +1083,11 @@ __global__ void __launch_bounds__(256)
 grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ gate,
             const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
             __nv_bfloat16* __restrict__ du, int pitch, __nv_bfloat16* __restrict__ dgate,
-            __nv_bfloat16* __restrict__ dup, int M, int N, int act) {
+            __nv_bfloat16* __restrict__ dup, int M, int N, int act,
+            unsigned int* __restrict__ counts, int n_counts) {
     pdl_allow_dependents();
+    if (blockIdx.x == 0)
+        for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
     const int per_row = pitch / 8;
     const bool vec = (N & 7) == 0;
     const size_t chunks = static_cast<size_t>(M) * per_row;
@@ -984,40 +1132,54 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 // ---- plan ----------------------------------------------------------------------
 
 struct Plan {
-    int x_rows, row_tiles, token_tiles, parts;
+    int x_rows, row_units, tiles, whole, workers, ctas;
+    size_t partial, counts;  // bytes of workspace
 };
 
-// rows: those of the product's row tiles; quads: its K in parts of four stages.
+// rows: those of the product; quads: its K in blocks (backward: 256 weight rows).
 // Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,
-// whichever is expected to end first: waves of CTAs times stages of a K part
-// times the time of a stage, about 1 : 0.7 for 256 and 128 tokens (512 tokens x
-// 14336 x 4096 backwards: 110 us in tiles of 256 and two K parts, 150 us in
-// tiles of 128).  K parts while the tiles leave half of the GPU or more idle.
+// whichever is expected to end first: a worker's stages times the time of a
+// stage, about 1 : 0.7 for 256 and 128 tokens, and eight stages' time for adding
+// the runs of cut tiles.  A worker has two quads at least.
 Plan make_plan(int M, int rows, int tile_rows, int quads) {
     Plan best = {};
     double best_cost = 0;
     for (int x_rows : {32, 64, 128, 256}) {
         if (x_rows < 128 && x_rows < M) continue;
-        Plan p;
+        Plan p = {};
         p.x_rows = x_rows;
-        p.row_tiles = (rows + tile_rows - 1) / tile_rows;
-        if (x_rows == 256) p.row_tiles += p.row_tiles & 1;  // pairs
-        p.token_tiles = (M + x_rows - 1) / x_rows;
-        const long tiles = static_cast<long>(p.row_tiles) * p.token_tiles;
-        p.parts = static_cast<int>(
-            std::max(1L, std::min<long>(std::min(x_rows == 256 ? kMaxParts / 2 : kMaxParts, quads),
-                                        kPlanSms / tiles)));
-        const long waves = (tiles * p.parts + kPlanSms - 1) / kPlanSms;
-        const double stages = 4.0 * quads / p.parts;
-        const double cost = waves * (stages + kTileStages) * (x_rows == 256 ? 1.0 : 0.7);
+        p.ctas = x_rows == 256 ? 2 : 1;
+        const int row_tiles = (rows + tile_rows - 1) / tile_rows;
+        p.row_units = (row_tiles + p.ctas - 1) / p.ctas;
+        p.tiles = p.row_units * ((M + x_rows - 1) / x_rows);
+        const long all = static_cast<long>(p.tiles) * quads;
+        p.workers = static_cast<int>(std::min<long>(kPlanSms / p.ctas, std::max(1L, all / 2)));
+        // whole tiles only, or what is left after full rounds of them cut evenly
+        const int rounds = p.tiles / p.workers;
+        const double uncut = static_cast<double>(quads) * ((p.tiles + p.workers - 1) / p.workers);
+        const double cut = static_cast<double>(all) / p.workers + 2;
+        // (a cut gives every worker a quad at least)
+        const long left = static_cast<long>(p.tiles - rounds * p.workers) * quads;
+        const bool cuts = left >= p.workers && cut < uncut;
+        p.whole = cuts ? rounds * p.workers : p.tiles;
+        const double cost = 4 * (cuts ? cut : uncut) * (x_rows == 256 ? 1.0 : 0.7);
         if (best_cost == 0 || cost < best_cost) {
             best = p;
             best_cost = cost;
         }
         if (x_rows >= M) break;  // a wider tile would be empty columns
     }
+    if (best.whole == best.tiles) {
+        best.workers = std::min(best.workers, best.tiles);
+    } else {
+        best.partial = static_cast<size_t>(2) * best.workers * best.ctas * best.x_rows * kRows * 4;
+        best.counts = (static_cast<size_t>(best.tiles - best.whole) * best.ctas * 4 + 255) & ~size_t(255);
+    }
     return best;
 }
+
+size_t plan_bytes(const Plan& p) { return p.partial + p.counts; }
+int count_words(const Plan& p) { return static_cast<int>(p.counts / 4); }
 
 // A bf16 [rows, cols] matrix with rows `pitch` apart, in boxes of box_rows x 64
 // columns, 128-byte swizzled.
@@ -1047,30 +1209,32 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
         attr_done[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.row_tiles, plan.token_tiles, plan.parts);
+    cfg.gridDim = dim3(plan.workers * plan.ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (C::kDuo || plan.parts > 1) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = C::kDuo ? 2 : 1;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = static_cast<unsigned>(plan.parts);
-        cfg.numAttrs = 2;
-    }
+    cfg.numAttrs = C::kDuo ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kX, kTma, kMode, T>, a, maps);
 }
 
-// T: the type of the results.  x0, x1: bf16 token matrices [M, x_cols] with rows
+// T: the type of the results.  workspace: plan_bytes, the counts zeroed.  x0, x1: bf16 token matrices [M, x_cols] with rows
 // `x_pitch` apart (x1: backward, du), or null with a.xa an image.
 template <Tc kMode, typename T>
-cudaError_t launch_tc(const TcArgs& a, const Plan& plan, const void* x0, const void* x1, int x_cols,
-                      int x_pitch, int device, cudaStream_t stream) {
+cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void* x0, const void* x1,
+                      int x_cols, int x_pitch, int device, cudaStream_t stream) {
+    a.tiles = plan.tiles;
+    a.row_units = plan.row_units;
+    a.whole = plan.whole;
+    a.partial = reinterpret_cast<float*>(workspace);
+    a.counts = reinterpret_cast<unsigned int*>(workspace + plan.partial);
     alignas(64) TcMaps maps;
     memset(&maps, 0, sizeof maps);
     const int rows = kMode == Tc::kLora ? kRows : 64;
@@ -1099,18 +1263,31 @@ size_t image_bytes(int M, int K) {
     return static_cast<size_t>((M + kSuperRows - 1) / kSuperRows) * kSuperRows * K * 2;
 }
 
+Plan forward_plan(int M, int N, int K, bool gated) {
+    return make_plan(M, N, gated ? kRows / 2 : kRows, K / kQK);
+}
+
 // x W^T: bf16 tokens go to the kernel by their own tensor map, f32 tokens by an
-// image.  behind_grid: one of this call's own grids (which does not write x) is
-// before, and lets its dependents start only when x is complete.
+// image.  behind_grid: one of this call's own grids (which does not write x, and
+// zeroes the counts) is before, and lets its dependents start only when x is
+// complete.  Workspace: plan_bytes, then (f32) the image.
 template <Tc kMode>
 cudaError_t launch_forward(TcArgs a, bool bf16, const void* x, void* workspace, int device,
                            int sm_count, bool behind_grid, cudaStream_t stream) {
-    const Plan plan = make_plan(a.M, a.N, kMode == Tc::kGated ? 64 : kRows, a.K / kQK);
-    a.stages = a.K / kStageK;
+    const Plan plan = forward_plan(a.M, a.N, a.K, kMode == Tc::kGated);
+    a.quads = a.K / kQK;
     a.tokens_ready = bf16 && behind_grid;
-    if (bf16)
-        return launch_tc<kMode, __nv_bfloat16>(a, plan, x, nullptr, a.K, a.K, device, stream);
-    a.xa = static_cast<const uint8_t*>(workspace);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    unsigned int* counts = reinterpret_cast<unsigned int*>(ws + plan.partial);
+    if (bf16) {
+        if (!behind_grid && plan.counts != 0) {
+            const cudaError_t e = cudaMemsetAsync(counts, 0, plan.counts, stream);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_tc<kMode, __nv_bfloat16>(a, plan, ws, x, nullptr, a.K, a.K, device, stream);
+    }
+    uint8_t* image = ws + plan_bytes(plan);
+    a.xa = image;
     // the image's grid started when all before it was complete: the weights are
     a.const_weights = true;
     const size_t chunks = static_cast<size_t>((a.M + 15) & ~15) * (a.K / 8);
@@ -1123,10 +1300,10 @@ cudaError_t launch_forward(TcArgs a, bool bf16, const void* x, void* workspace, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = behind_grid ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, x_image_kernel, static_cast<const float*>(x),
-                                             static_cast<uint8_t*>(workspace), a.M, a.K, chunks);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, x_image_kernel, static_cast<const float*>(x), image,
+                                             a.M, a.K, chunks, counts, count_words(plan));
     if (e != cudaSuccess) return e;
-    return launch_tc<kMode, float>(a, plan, nullptr, nullptr, 0, 0, device, stream);
+    return launch_tc<kMode, float>(a, plan, ws, nullptr, nullptr, 0, 0, device, stream);
 }
 
 // Columns of dg and du as the product's K: whole parts of two stages each.
@@ -1136,7 +1313,9 @@ int backward_pitch(int N) { return (N + 7) & ~7; }
 
 }  // namespace
 
-size_t gated_tc_workspace_bytes(const GatedArgs& a) { return a.bf16 ? 0 : image_bytes(a.M, a.K); }
+size_t gated_tc_workspace_bytes(const GatedArgs& a) {
+    return plan_bytes(forward_plan(a.M, a.N, a.K, true)) + (a.bf16 ? 0 : image_bytes(a.M, a.K));
+}
 
 cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream) {
     TcArgs t = {};
@@ -1153,7 +1332,15 @@ cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t st
     return launch_forward<Tc::kGated>(t, a.bf16, a.x, workspace, a.device, a.sm_count, false, stream);
 }
 
-size_t lora_tc_workspace_bytes(const LoraArgs& a) { return a.bf16 ? 0 : image_bytes(a.M, a.K); }
+size_t lora_tc_workspace_bytes(const LoraArgs& a) {
+    return plan_bytes(forward_plan(a.M, a.N, a.K, false)) + (a.bf16 ? 0 : image_bytes(a.M, a.K));
+}
+
+void lora_tc_counts(const LoraArgs& a, void* workspace, unsigned int** counts, int* n_counts) {
+    const Plan plan = forward_plan(a.M, a.N, a.K, false);
+    *counts = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(workspace) + plan.partial);
+    *n_counts = count_words(plan);
+}
 
 cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, cudaStream_t stream) {
     TcArgs c = {};
@@ -1171,30 +1358,36 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, c
     return launch_forward<Tc::kLora>(c, a.bf16, a.x, workspace, a.device, a.sm_count, true, stream);
 }
 
-// Workspace: dg and du, unless the caller takes them in rows of whole 16 bytes.
+// Workspace: plan_bytes; then dg and du, unless the caller takes them in rows of
+// whole 16 bytes.
 static bool backward_in_place(const GatedBackwardArgs& a) {
     return a.dgate != nullptr && backward_pitch(a.N) == a.N;
 }
 static size_t backward_matrix_bytes(const GatedBackwardArgs& a) {
     return (static_cast<size_t>(a.M) * backward_pitch(a.N) * 2 + 255) & ~size_t(255);
 }
+static Plan backward_plan(const GatedBackwardArgs& a) {
+    return make_plan(a.M, a.K, kRows, 2 * backward_cols(a.N) / (4 * kStageK));
+}
 size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
-    return backward_in_place(a) ? 0 : 2 * backward_matrix_bytes(a);
+    return plan_bytes(backward_plan(a)) + (backward_in_place(a) ? 0 : 2 * backward_matrix_bytes(a));
 }
 
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream) {
+    const Plan plan = backward_plan(a);
     const int pitch = backward_pitch(a.N), cols = backward_cols(a.N);
     const bool own = backward_in_place(a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(ws);
+    uint8_t* copies = ws + plan_bytes(plan);
+    __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(copies);
     __nv_bfloat16* du = own ? a.dup
-                            : reinterpret_cast<__nv_bfloat16*>(ws + backward_matrix_bytes(a));
+                            : reinterpret_cast<__nv_bfloat16*>(copies + backward_matrix_bytes(a));
     const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
     const unsigned blocks =
         static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));
-    grad_kernel<<<blocks, 256, 0, stream>>>(a.dh, a.gate, a.up, dg, du, pitch,
-                                            own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
-                                            a.act);
+    grad_kernel<<<blocks, 256, 0, stream>>>(
+        a.dh, a.gate, a.up, dg, du, pitch, own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
+        a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     TcArgs t = {};
@@ -1205,10 +1398,9 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     t.K = a.K;
     t.const_weights = true;  // the grid before started when all before it was complete
     t.half_stages = cols / kStageK;
-    t.stages = 2 * t.half_stages;
+    t.quads = 2 * t.half_stages / 4;
     t.y = a.dx;
-    const Plan plan = make_plan(a.M, a.K, kRows, t.stages / 4);
-    return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, dg, du, a.N, pitch, a.device, stream);
+    return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, ws, dg, du, a.N, pitch, a.device, stream);
 }
 
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream) {

@@ -233,6 +233,8 @@ cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t str
 size_t gated_tc_workspace_bytes(const GatedArgs& a);
 cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream);
 size_t lora_tc_workspace_bytes(const LoraArgs& a);
+// words of its workspace that must be zero (none: *n_counts = 0)
+void lora_tc_counts(const LoraArgs& a, void* workspace, unsigned int** counts, int* n_counts);
 cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, cudaStream_t stream);
 // Read and clear those kernels' device error word (synchronises `stream`).
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream);

@@ -74,28 +74,11 @@ __device__ __forceinline__ uint32_t bf16_idesc(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
-// D[tmem_d] (+)= A[tmem_a] * B[bdesc]^T, A in tensor memory.  A pair's MMA takes
-// its rows, and half of its columns' B, from the same places of both CTAs.
+// D[tmem_d] (+)= A * B^T, both in shared memory.  A pair's MMA takes its rows, and
+// half of its columns' B, from the same places of both CTAs.
 template <bool kDuo>
-__device__ __forceinline__ void mma(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                    uint32_t idesc, uint32_t accumulate) {
-    if constexpr (kDuo)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-            ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-            ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-// The same with A in shared memory.
-template <bool kDuo>
-__device__ __forceinline__ void mma_smem(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                    uint32_t accumulate) {
     if constexpr (kDuo)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -162,17 +145,7 @@ __device__ __forceinline__ void arrive_first_of_pair(uint32_t bar) {
         ::"r"(bar), "r"(cluster_rank() & ~1u)
         : "memory");
 }
-// Eight consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-          "r"(v[6]), "r"(v[7])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_store_wait() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
+// Sixteen consecutive columns (f32) of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&f)[16]) {
     uint32_t v[16];
     asm volatile(
