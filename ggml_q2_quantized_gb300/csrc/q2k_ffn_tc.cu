@@ -22,12 +22,17 @@
 // costs nothing.  (Transposing the codes first, so that a lane could write its
 // own column to tensor memory, took 2200 warp instructions a stage against 680.)
 //
-// Work split: the grid is as many CTAs as the GPU holds.  Whole tiles go to them
-// in turn; what is left over, less than a tile each, is cut into equal runs of K
-// (in blocks; backward, of 256 weight rows), so that all end together.  A tile's
-// runs leave their sums in the workspace, and the CTA that finishes last adds
-// them, in the order of K whoever that is, and writes the results: no CTA waits
-// for another.
+// Work split, K in blocks (backward: in 256 weight rows):
+// - fewer tiles than half of the workers (CTAs, or pairs, that the GPU holds): a
+//   cluster of up to eight CTAs divides a tile's K; the parts' sums meet through
+//   distributed shared memory, each part bringing out a share of the tokens;
+// - more tiles than workers: whole tiles go to the workers in turn, and what is
+//   left over, less than a tile each, is cut into equal runs of K, so that all
+//   end together.  The runs come first: their sums go to the workspace, the CTA
+//   that finishes last adds them, in the order of K whoever that is, and all of
+//   that happens while whole tiles are multiplied.  No CTA waits for another.
+//   (2048 tokens backwards: 256 tiles for 152 CTAs, 302 us against 356 in two
+//   rounds.  Cutting without whole tiles behind it exposes 14 us of adding.)
 //
 // What bounds it: at 256 tokens a tile the MMAs (740 clocks per stage as measured,
 // of 630 for a plain bf16 matrix product at the measured peak); below, the decode.
@@ -87,6 +92,7 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kMmaWarp = kDecWarps, kWaitWarp = kDecWarps + 1, kWWarp = kDecWarps + 2,
               kXWarp = kDecWarps + 3, kEpiWarp0 = kDecWarps + 4;  // (a multiple of 4)
 constexpr int kThreads = 32 * (kDecWarps + 8);
+constexpr int kMaxParts = 8;   // of K (the largest portable cluster)
 constexpr int kPlanSms = 152;  // the work is cut for the whole GPU, whatever the device
 
 constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memory
@@ -152,6 +158,7 @@ struct TcArgs {
     int half_stages;     // backward: 64-row stages of Wg
     int tiles, row_units;  // tiles, row tiles (256 tokens: pairs of them) first
     int whole;           // tiles [0, whole) go to the workers in turn, the rest is cut
+    int parts;           // CTAs (pairs) of a cluster that divide K (then one tile each)
     float* partial;      // sums of a cut tile's runs, two slots per CTA
     unsigned int* counts;  // per cut tile and CTA of a worker: runs finished (zeroed)
     bool const_weights;  // the grid before does not write the weights
@@ -210,18 +217,14 @@ struct Team {
 // sum takes only its own adapter's product.  t comes through shared memory 64
 // values a token at a time, already split: the two bf16 of value pair j (hi, lo)
 // of token c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
-// reads together fall on different banks.  A warp has 32 rows, and keeps B_a's
-// fragments in registers (`b`, of adapter `cur` and its values from `cur_r0` on)
-// from one token group and chunk to the next.  These products bound it: one takes
-// 32 clocks of a quarter SM, 17000 clocks for 128 rows x 256 tokens at rank 64.
-struct AdapterFragments {
-    uint32_t b[2][4][4];
-    int cur = -1, cur_r0 = 0;
-};
-__device__ __forceinline__ void add_adapters(AdapterFragments& f, float* sums, uint32_t* tbuf,
-                                             int* id_buf, const TcArgs& p, int n0, int m, int count,
+// reads together fall on different banks.  A warp has 16 rows at a time, and keeps
+// B_a's fragments in registers from one token group to the next with the same
+// adapter.  These products bound it: one takes 32 clocks of a quarter SM, 17000
+// clocks for 128 rows x 256 tokens at rank 64.
+__device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* id_buf,
+                                             const TcArgs& p, int n0, int m, int count,
                                              const Team& team) {
-    const int et = team.thread, quarter = (et >> 5) & 3, lane = et & 31;
+    const int et = team.thread, lane = et & 31;
     const int g = lane >> 2, t = lane & 3;
     const int slots = (count + 7) & ~7;
     // ids: -1 none, -2 out of range (a zero row)
@@ -255,71 +258,68 @@ __device__ __forceinline__ void add_adapters(AdapterFragments& f, float* sums, u
             }
         }
         team.sync();
+        // row tile % 8 of warp % 8; the team's other warps take other tokens
+        const int warp = et >> 5, warps = team.threads >> 5;
+        const int sets = max(1, warps >> 3);
 #pragma unroll 1
-        for (int c0 = 8 * (et >> 7); c0 < slots; c0 += 8 * (team.threads >> 7)) {
-            const int id = id_buf[c0 + g];
-            // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
-            const int id0 = id_buf[c0 + 2 * t], id1 = id_buf[c0 + 2 * t + 1];
-            float* s0 = sums + (c0 + 2 * t) * kSumPitch + 32 * quarter + g;
-            float* s1 = s0 + kSumPitch;
-            if (r0 == 0) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (id0 == -2) s0[8 * q] = 0.f;
-                    if (id1 == -2) s1[8 * q] = 0.f;
-                }
-            }
-            unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
-            while (todo != 0) {
-                const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
-                todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
-                if (ad != f.cur || r0 != f.cur_r0) {
-                    f.cur = ad;
-                    f.cur_r0 = r0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = n0 + 32 * quarter + 16 * h + g;
+        for (int rt = warp & 7; rt < 8 && (warp >> 3) < sets; rt += min(warps, 8)) {
+            const int n = n0 + 16 * rt + g;  // this lane's rows: n, n + 8
+            int cur = -1;
+            uint32_t b[4][4];
+#pragma unroll 1
+            for (int c0 = 8 * (warp >> 3); c0 < slots; c0 += 8 * sets) {
+                const int id = id_buf[c0 + g];
+                // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
+                const int id0 = id_buf[c0 + 2 * t], id1 = id_buf[c0 + 2 * t + 1];
+                float* s0 = sums + (c0 + 2 * t) * kSumPitch + 16 * rt + g;
+                float* s1 = s0 + kSumPitch;
+                if (id0 == -2) s0[0] = s0[8] = 0.f;
+                if (id1 == -2) s1[0] = s1[8] = 0.f;
+                unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
+                while (todo != 0) {
+                    const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
+                    todo &= ~__ballot_sync(0xFFFFFFFFu, id == ad);
+                    if (ad != cur) {
+                        cur = ad;
                         const uint32_t* b0 = reinterpret_cast<const uint32_t*>(
                             p.b + (static_cast<size_t>(ad) * p.N + n) * p.R + r0) + t;
                         const uint32_t* b1 = b0 + 4 * p.R;  // eight rows on
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const bool in0 = 16 * q < width, in1 = 16 * q + 8 < width;
-                            f.b[h][q][0] = n < p.N && in0 ? __ldg(b0 + 8 * q) : 0u;
-                            f.b[h][q][1] = n + 8 < p.N && in0 ? __ldg(b1 + 8 * q) : 0u;
-                            f.b[h][q][2] = n < p.N && in1 ? __ldg(b0 + 8 * q + 4) : 0u;
-                            f.b[h][q][3] = n + 8 < p.N && in1 ? __ldg(b1 + 8 * q + 4) : 0u;
+                            b[q][0] = n < p.N && in0 ? __ldg(b0 + 8 * q) : 0u;
+                            b[q][1] = n + 8 < p.N && in0 ? __ldg(b1 + 8 * q) : 0u;
+                            b[q][2] = n < p.N && in1 ? __ldg(b0 + 8 * q + 4) : 0u;
+                            b[q][3] = n + 8 < p.N && in1 ? __ldg(b1 + 8 * q + 4) : 0u;
                         }
                     }
-                }
-                // (four chains of four products, two per half of the rows)
-                float e[2][2][4] = {};
+                    // (four chains of two products: one takes as long as dozens
+                    // of other instructions to return)
+                    float e[4][4] = {};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (16 * q >= width) break;
-                    uint2 u = make_uint2(0u, 0u), w = u;
-                    if (id == ad) {
-                        const uint32_t* tr = tbuf + 64 * (c0 + g);
-                        const int x = 8 * (g & 3);
-                        u = *reinterpret_cast<const uint2*>(tr + ((16 * q + 2 * t) ^ x));
-                        w = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
+                    for (int q = 0; q < 4; ++q) {
+                        uint2 u = make_uint2(0u, 0u), w = u;
+                        if (id == ad && 16 * q < width) {
+                            const uint32_t* tr = tbuf + 64 * (c0 + g);
+                            const int x = 8 * (g & 3);
+                            u = *reinterpret_cast<const uint2*>(tr + ((16 * q + 2 * t) ^ x));
+                            w = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
+                        }
+                        if (16 * q < width) {
+                            mma_bf16_16816(e[q], b[q][0], b[q][1], b[q][2], b[q][3], u.x, w.x);
+                            mma_bf16_16816(e[q], b[q][0], b[q][1], b[q][2], b[q][3], u.y, w.y);
+                        }
                     }
+                    float d[4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t(&b)[4] = f.b[h][q];
-                        mma_bf16_16816(e[h][0], b[0], b[1], b[2], b[3], u.x, w.x);
-                        mma_bf16_16816(e[h][1], b[0], b[1], b[2], b[3], u.y, w.y);
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                    for (int c = 0; c < 4; ++c) d[c] = (e[0][c] + e[1][c]) + (e[2][c] + e[3][c]);
                     if (id0 == ad) {
-                        s0[16 * h] += e[h][0][0] + e[h][1][0];
-                        s0[16 * h + 8] += e[h][0][2] + e[h][1][2];
+                        s0[0] += d[0];
+                        s0[8] += d[2];
                     }
                     if (id1 == ad) {
-                        s1[16 * h] += e[h][0][1] + e[h][1][1];
-                        s1[16 * h + 8] += e[h][0][3] + e[h][1][3];
+                        s1[0] += d[1];
+                        s1[8] += d[3];
                     }
                 }
             }
@@ -353,6 +353,17 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // One worker's share of the product (a CTA, or a pair): first its runs of the cut
 // tiles (two at most), then its whole tiles.
 struct Segment {
@@ -361,6 +372,7 @@ struct Segment {
 };
 struct Work {
     int w, workers, quads, tiles, whole;
+    int part, parts;  // of K, for the CTAs of a cluster
     // quads [begin(w), begin(w + 1)) of the cut tiles, counted through
     __device__ __forceinline__ int begin(int w) const {
         return static_cast<int>(static_cast<long long>(tiles - whole) * quads * w / workers);
@@ -380,8 +392,8 @@ struct Work {
             }
         }
         s.tile = w + (index - runs) * workers;
-        s.q0 = 0;
-        s.q1 = quads;
+        s.q0 = quads * part / parts;
+        s.q1 = quads * (part + 1) / parts;
         s.run = -1;
         return s.tile < whole;
     }
@@ -490,8 +502,10 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     const int rows = kBack ? p.K : p.N;  // rows of the product
     const int peer = kDuo ? static_cast<int>(blockIdx.x & 1) : 0;
     Work work;
-    work.w = blockIdx.x / C::kCtas;
-    work.workers = gridDim.x / C::kCtas;
+    work.parts = p.parts;
+    work.part = blockIdx.x / C::kCtas % p.parts;
+    work.w = blockIdx.x / (C::kCtas * p.parts);
+    work.workers = gridDim.x / (C::kCtas * p.parts);
     work.quads = p.quads;
     work.tiles = p.tiles;
     work.whole = p.whole;
@@ -886,13 +900,24 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         }
         __syncwarp();
     }
+    // Results of `count` tokens (from m on) of a tile from their sums; the last
+    // tile's (`final`) lie where the rings were, from token slot `slot` on.
+    auto bring_out = [&](float* base, bool final, int n0, int m, int count, const Team& team, int slot = 0) {
+        if constexpr (kMode == Tc::kLora) {
+            uint32_t* tbuf = reinterpret_cast<uint32_t*>(final ? base + kX * kSumPitch
+                                                               : reinterpret_cast<float*>(smem + C::kOffT));
+            int* id_buf = reinterpret_cast<int*>(final ? tbuf + 64 * kX
+                                                       : reinterpret_cast<uint32_t*>(smem + C::kOffIds));
+            add_adapters(base + slot * kSumPitch, tbuf, id_buf, p, n0, m + slot, count, team);
+        }
+        emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
+    };
     if (warp >= kEpiWarp0 || warp < kDecWarps) {
         // ---------------- epilogue: sums -> results ----------------
         // (what is written here, and t, may still be in use by the grid before)
         pdl_wait_prerequisites();
         if (p.tokens_ready) pdl_allow_dependents();
         const int segments = work.count();
-        [[maybe_unused]] AdapterFragments fragments;
         // the decoders come for the last segment
         for (int index = warp < kDecWarps ? segments - 1 : 0; work.segment(index, sg); ++index) {
             const bool final = index == segments - 1;
@@ -969,7 +994,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 team.sync();  // (the word is read before the next segment writes it)
                 if (!add) continue;
             }
-            for (int c0 = 0; c0 < tokens; c0 += chunk) {
+            for (int c0 = 0; c0 < tokens && !(final && p.parts > 1); c0 += chunk) {
                 const int count = min(chunk, tokens - c0);
                 if (sg.run < 0) {
                     for (int h = strip; h < count; h += strips) {
@@ -980,31 +1005,40 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     }
                     if (c0 + chunk >= tokens) release();
                 } else {
+                    // two float4 of up to three runs at a time: latency bounds it
                     const int quads = count * (kRows / 4);
-                    for (int i0 = team.thread; i0 < quads; i0 += 4 * team.threads) {
-                        float4 a[4];
+                    auto run_sums = [&](int v) {
+                        return reinterpret_cast<const float4*>(
+                                   p.partial + static_cast<size_t>((2 * v + work.run_of(v, sg.tile)) * C::kCtas + peer) *
+                                                   (kX * kRows)) + c0 * (kRows / 4);
+                    };
+                    for (int i0 = team.thread; i0 < quads; i0 += 2 * team.threads) {
+                        const int i1 = i0 + team.threads;
+                        float4 a[2];
+                        a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int v = first; v <= last; v += 3) {
+                            float4 x[3][2];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int v = first; v <= last; ++v) {
-                            const float4* src = reinterpret_cast<const float4*>(
-                                p.partial + static_cast<size_t>((2 * v + work.run_of(v, sg.tile)) * C::kCtas + peer) *
-                                                (kX * kRows)) + c0 * (kRows / 4);
-                            float4 x[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                x[u] = i0 + team.threads * u < quads ? __ldcg(src + i0 + team.threads * u)
-                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                a[u].x += x[u].x;
-                                a[u].y += x[u].y;
-                                a[u].z += x[u].z;
-                                a[u].w += x[u].w;
+                            for (int z = 0; z < 3; ++z) {
+                                x[z][0] = x[z][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (v + z > last) continue;
+                                const float4* src = run_sums(v + z);
+                                x[z][0] = __ldcg(src + i0);
+                                if (i1 < quads) x[z][1] = __ldcg(src + i1);
                             }
+#pragma unroll
+                            for (int z = 0; z < 3; ++z)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    a[u].x += x[z][u].x;
+                                    a[u].y += x[z][u].y;
+                                    a[u].z += x[z][u].z;
+                                    a[u].w += x[z][u].w;
+                                }
                         }
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int i = i0 + team.threads * u;
+                        for (int u = 0; u < 2; ++u) {
+                            const int i = u ? i1 : i0;
                             if (i < quads)
                                 *reinterpret_cast<float4*>(sums + (i / (kRows / 4)) * kSumPitch +
                                                            4 * (i % (kRows / 4))) = a[u];
@@ -1012,23 +1046,67 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     }
                 }
                 team.sync();
-                if constexpr (kMode == Tc::kLora) {
-                    uint32_t* tbuf = final ? reinterpret_cast<uint32_t*>(sums + kX * kSumPitch)
-                                           : reinterpret_cast<uint32_t*>(smem + C::kOffT);
-                    int* id_buf = final ? reinterpret_cast<int*>(tbuf + 64 * kX)
-                                        : reinterpret_cast<int*>(smem + C::kOffIds);
-                    add_adapters(fragments, sums, tbuf, id_buf, p, n0, m0 + c0, count, team);
-                }
-                emit<kMode, T>(p, sums, n0, rows, m0 + c0, count, team);
+                bring_out(sums, final, n0, m0 + c0, count, team);
                 team.sync();
             }
-            fragments.cur = -1;  // (another tile has other rows)
+            if (final && p.parts > 1 && sg.run < 0) {
+                // parts of K: the sums wait here for the cluster
+                for (int h = strip; h < tokens; h += strips) {
+                    float v[16];
+                    load_sums(h, v);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) sums[(h + q) * kSumPitch + my_row] = v[q];
+                }
+            }
+        }
+    }
+    if (p.parts > 1) {
+        // Every thread of the cluster passes its barriers, whatever happened
+        // before.  Part z adds its share of the tokens (whole groups of eight)
+        // over the parts in order and brings them out; the barrier at the end
+        // keeps every part's sums alive until all are read.
+        fence_before();
+        __syncwarp();
+        cluster_sync();
+        if (warp >= kEpiWarp0 || warp < kDecWarps) {
+            Team team;
+            team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
+                                           : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
+            team.threads = 128 + kDecThreads;
+            team.barrier = 7;
+            work.segment(0, sg);
+            const int n0 = row0(sg.tile), m0 = token0(sg.tile);
+            const int tokens = min(kX, p.M - m0), groups = (tokens + 7) / 8;
+            const int first = 8 * (work.part * groups / p.parts);
+            const int count = min(tokens, 8 * ((work.part + 1) * groups / p.parts)) - first;
+            float* sums = reinterpret_cast<float*>(smem) + first * kSumPitch;
+            for (int j = team.thread; j < count * (kRows / 4); j += team.threads) {
+                const int i = j / (kRows / 4) * (kSumPitch / 4) + j % (kRows / 4);
+                const uint32_t at = smem_u32(sums) + 16 * i;
+                float4 v[kMaxParts];
+#pragma unroll
+                for (int z = 0; z < kMaxParts; ++z)
+                    if (z < p.parts) v[z] = load_cluster4(at, C::kCtas * z + peer);
+                float4 a = v[0];
+#pragma unroll
+                for (int z = 1; z < kMaxParts; ++z)
+                    if (z < p.parts) {
+                        a.x += v[z].x;
+                        a.y += v[z].y;
+                        a.z += v[z].z;
+                        a.w += v[z].w;
+                    }
+                reinterpret_cast<float4*>(sums)[i] = a;
+            }
+            team.sync();
+            if (*abort_flag == 0 && count > 0)
+                bring_out(reinterpret_cast<float*>(smem), true, n0, m0, count, team, first);
         }
     }
 
     fence_before();
     __syncwarp();
-    if (kDuo) cluster_sync();
+    if (kDuo || p.parts > 1) cluster_sync();
     else __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
@@ -1132,15 +1210,14 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 // ---- plan ----------------------------------------------------------------------
 
 struct Plan {
-    int x_rows, row_units, tiles, whole, workers, ctas;
+    int x_rows, row_units, tiles, whole, workers, ctas, parts;
     size_t partial, counts;  // bytes of workspace
 };
 
 // rows: those of the product; quads: its K in blocks (backward: 256 weight rows).
 // Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,
 // whichever is expected to end first: a worker's stages times the time of a
-// stage, about 1 : 0.7 for 256 and 128 tokens, and eight stages' time for adding
-// the runs of cut tiles.  A worker has two quads at least.
+// stage, about 1 : 0.7 for 256 and 128 tokens.
 Plan make_plan(int M, int rows, int tile_rows, int quads) {
     Plan best = {};
     double best_cost = 0;
@@ -1152,26 +1229,33 @@ Plan make_plan(int M, int rows, int tile_rows, int quads) {
         const int row_tiles = (rows + tile_rows - 1) / tile_rows;
         p.row_units = (row_tiles + p.ctas - 1) / p.ctas;
         p.tiles = p.row_units * ((M + x_rows - 1) / x_rows);
-        const long all = static_cast<long>(p.tiles) * quads;
-        p.workers = static_cast<int>(std::min<long>(kPlanSms / p.ctas, std::max(1L, all / 2)));
-        // whole tiles only, or what is left after full rounds of them cut evenly
-        const int rounds = p.tiles / p.workers;
-        const double uncut = static_cast<double>(quads) * ((p.tiles + p.workers - 1) / p.workers);
-        const double cut = static_cast<double>(all) / p.workers + 2;
-        // (a cut gives every worker a quad at least)
-        const long left = static_cast<long>(p.tiles - rounds * p.workers) * quads;
-        const bool cuts = left >= p.workers && cut < uncut;
-        p.whole = cuts ? rounds * p.workers : p.tiles;
-        const double cost = 4 * (cuts ? cut : uncut) * (x_rows == 256 ? 1.0 : 0.7);
+        const int most = kPlanSms / p.ctas;
+        const int rounds = p.tiles / most;
+        p.parts = 1;
+        p.whole = p.tiles;
+        p.workers = std::min(p.tiles, most);
+        double cost;
+        if (rounds == 0) {
+            p.parts = std::max(1, std::min({kMaxParts / p.ctas, quads, most / p.tiles}));
+            cost = static_cast<double>(quads) / p.parts + 1;
+        } else {
+            // whole tiles only, or what is left after full rounds of them cut
+            // evenly (a quad for every worker at least)
+            const long left = static_cast<long>(p.tiles - rounds * most) * quads;
+            const double uncut = static_cast<double>(quads) * ((p.tiles + most - 1) / most);
+            const double cut = static_cast<double>(p.tiles) * quads / most + 1;
+            const bool cuts = left >= most && cut < uncut;
+            if (cuts) p.whole = rounds * most;
+            cost = cuts ? cut : uncut;
+        }
+        cost *= x_rows == 256 ? 1.0 : 0.7;
         if (best_cost == 0 || cost < best_cost) {
             best = p;
             best_cost = cost;
         }
         if (x_rows >= M) break;  // a wider tile would be empty columns
     }
-    if (best.whole == best.tiles) {
-        best.workers = std::min(best.workers, best.tiles);
-    } else {
+    if (best.whole < best.tiles) {
         best.partial = static_cast<size_t>(2) * best.workers * best.ctas * best.x_rows * kRows * 4;
         best.counts = (static_cast<size_t>(best.tiles - best.whole) * best.ctas * 4 + 255) & ~size_t(255);
     }
@@ -1209,7 +1293,7 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
         attr_done[device] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.workers * plan.ctas);
+    cfg.gridDim = dim3(plan.workers * plan.ctas * plan.parts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
@@ -1217,11 +1301,11 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.ctas * plan.parts);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = C::kDuo ? 2 : 1;
+    cfg.numAttrs = plan.ctas * plan.parts > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kX, kTma, kMode, T>, a, maps);
 }
 
@@ -1233,6 +1317,7 @@ cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void
     a.tiles = plan.tiles;
     a.row_units = plan.row_units;
     a.whole = plan.whole;
+    a.parts = plan.parts;
     a.partial = reinterpret_cast<float*>(workspace);
     a.counts = reinterpret_cast<unsigned int*>(workspace + plan.partial);
     alignas(64) TcMaps maps;
