@@ -122,6 +122,12 @@ struct Cfg {
     // stages in flight, tokens and decoded weights alike (one release for both)
     static constexpr int kStages = kX >= 128 ? 5 : kX == 64 ? 7 : 8;
     static constexpr int kGroupWarps = 4;  // decoders: four groups, a stage each in turn
+    // A decoder waits for the MMAs of stage i - kStages by its barrier's parity,
+    // which is right only if those of i - 2 kStages are known to be done: its
+    // wait before covered stage i - 4 - kStages.  Two issuers' MMAs of one
+    // hand-over end in any order, so where both stages may belong to the same
+    // one, each issuer releases both of a hand-over's stages.
+    static constexpr bool kJointRelease = kIssuers == 2 && kStages - 4 < kHand;
     static constexpr uint32_t kAccCols = kX * kIssuers;  // a tile's sums; two sets
     static constexpr uint32_t kTmemCols = 512;
     static_assert(2 * kAccCols <= kTmemCols, "tensor memory");
@@ -537,7 +543,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             mbar_init(bar_xfull + 8 * s, 1);               // the producer's expect-tx arrival
             mbar_init(bar_afull + 8 * s, C::kGroupWarps);  // the warps of its group
             mbar_init(bar_peer + 8 * s, 1);                // the second CTA's waiter
-            mbar_init(bar_empty + 8 * s, 1);               // MMA commit of the stage's issuer
+            mbar_init(bar_empty + 8 * s, C::kJointRelease ? 2 : 1);  // MMA commits
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
@@ -576,6 +582,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_afull + 8 * (i % S));
         };
+        // This warp is done with a raw slot: called when the words read from it
+        // have been used, since loads still on their way when the slot is given
+        // back were seen to bring the next block's bytes.
+        [[maybe_unused]] auto raw_read = [&](uint32_t bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         if constexpr (kBack) {
             // group (four warps) takes every fourth stage: warp = 32 weight rows
             // and a segment, lane = the row, all four shifts
@@ -584,7 +597,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             bool ok = true;  // a warp that gave up still passes the group's barriers
             int i = own;     // this group's stages, counted over all segments
             // without TMA: the next stage to fetch (a slot ahead of the decode)
-            Segment fetch;
+            Segment fetch = {};
             int fetch_index = 0, fetch_q = 0, fetched = own;
             bool more = false;
             [[maybe_unused]] auto fetch_next = [&]() {
@@ -633,16 +646,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     const uint32_t sc0 = ld_shared_u32(at_sc) >> (8 * seg);
                     const uint32_t sc1 = ld_shared_u32(at_sc + 4) >> (8 * seg);
                     const uint32_t dd = ld_shared_u32(at_d);
-                    if constexpr (kTma) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_rawempty + 8 * slot);
-                    }
                     const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
                     uint32_t o[4][8];
                     decode_segment<0>(qw, sc0 & 0xFFu, d, dmin, o[0]);
                     decode_segment<1>(qw, (sc0 >> 16) & 0xFFu, d, dmin, o[1]);
                     decode_segment<2>(qw, sc1 & 0xFFu, d, dmin, o[2]);
                     decode_segment<3>(qw, (sc1 >> 16) & 0xFFu, d, dmin, o[3]);
+                    if constexpr (kTma) raw_read(bar_rawempty + 8 * slot);
                     ok = stage_free(i);
                     if (!ok) continue;
                     // row n of the stage: 128 bytes of columns 64 c .. at 8192 c +
@@ -664,7 +674,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             const int row = 32 * (warp & 3) + lane, own = warp >> 2;
             const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
             // without TMA: the next block to fetch (kRaw - 1 ahead of the decode)
-            Segment fetch;
+            Segment fetch = {};
             int fetch_index = 0, fetch_q = 0, fetched = 0;
             bool more = false;
             [[maybe_unused]] auto fetch_next = [&]() {
@@ -708,10 +718,6 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     for (int e = 0; e < 8; ++e)
                         qw[e >> 2][e & 3] = ld_shared_u32(mine + 16 + 32 * half + 4 * e);
                     const uint32_t dd = ld_shared_u32(mine + 80);
-                    if constexpr (kTma) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_rawempty + 8 * buf);
-                    }
                     const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
                     uint32_t o[4][8];  // (shift, segment)
                     if (own & 1) {
@@ -725,6 +731,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         decode_segment<1>(qw[0], (sc >> 16) & 0xFFu, d, dmin, o[2]);
                         decode_segment<1>(qw[1], sc >> 24, d, dmin, o[3]);
                     }
+                    if constexpr (kTma) raw_read(bar_rawempty + 8 * buf);
                     const int i = 4 * b + own;
                     ok = stage_free(i);
                     if (!ok) break;
@@ -783,7 +790,11 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         for (int kk = 0; kk < kStageK / 16; ++kk)  // (backward: a K-step is 16 rows)
                             mma<kDuo>(acc, adesc + (kBack ? 128u : 2u) * kk, xdesc + 2u * kk, idesc,
                                       l0 + u >= C::kIssuers || kk > 0);
-                        commit<kDuo>(bar_empty + 8 * s);
+                        if (!C::kJointRelease) commit<kDuo>(bar_empty + 8 * s);
+                    }
+                    if (C::kJointRelease) {
+#pragma unroll
+                        for (int u = 0; u < C::kHand; ++u) commit<kDuo>(bar_empty + 8 * ((i0 + u) % S));
                     }
                     if (l0 + C::kHand == n_iters) commit<kDuo>(bar_accfull + 8 * (index & 1));
                 }
