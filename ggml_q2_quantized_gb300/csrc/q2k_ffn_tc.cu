@@ -108,19 +108,24 @@ enum class Tc { kGated, kLora, kBackward };
 // x 256 tokens, issued by one thread of the first (cta_group::2).  Each holds
 // half of the tokens' stage, so a stage is half as large and crosses from L2
 // once per pair.
-// 128 and fewer: narrow MMAs issue at half the rate the tensor core takes them,
-// so two threads issue, each into its own accumulator (stages in turn).
+// 128 and fewer: the decode bounds, and narrow MMAs that read A from shared
+// memory take as long as wide ones (100 clocks each, measured), so decoded
+// weights go to tensor memory (not backward, where they would have to be
+// transposed).  Narrow MMAs issue at half the rate the tensor core takes them:
+// two threads issue, each into its own accumulator, where tensor memory has room
+// (14336 x 4096, 64 tokens: 55 us with A in shared memory).
 template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
     static constexpr bool kDuo = kX == 256;
     static constexpr int kCtas = kDuo ? 2 : 1;
-    static constexpr int kIssuers = kDuo ? 1 : 2;
+    static constexpr bool kTmemA = !kBack && !kDuo;
+    static constexpr int kIssuers = kDuo || (kTmemA && kX == 128) ? 1 : 2;
     static constexpr int kHand = 2;                      // stages handed over at a time
     static constexpr int kHold = kX / kCtas;             // tokens of a stage in this CTA
     static constexpr int kXStage = kHold * kStageK * 2;
     // stages in flight, tokens and decoded weights alike (one release for both)
-    static constexpr int kStages = kX >= 128 ? 5 : kX == 64 ? 7 : 8;
+    static constexpr int kStages = kTmemA ? 8 : kX >= 128 ? 5 : kX == 64 ? 7 : 8;
     static constexpr int kGroupWarps = 4;  // decoders: four groups, a stage each in turn
     // A decoder waits for the MMAs of stage i - kStages by its barrier's parity,
     // which is right only if those of i - 2 kStages are known to be done: its
@@ -130,15 +135,16 @@ struct Cfg {
     static constexpr bool kJointRelease = kIssuers == 2 && kStages - 4 < kHand;
     static constexpr uint32_t kAccCols = kX * kIssuers;  // a tile's sums; two sets
     static constexpr uint32_t kTmemCols = 512;
-    static_assert(2 * kAccCols <= kTmemCols, "tensor memory");
+    static constexpr uint32_t kColA = 2 * kAccCols;      // 32 columns per decoded stage
+    static_assert(kColA + (kTmemA ? 32 * kStages : 0) <= kTmemCols, "tensor memory");
     // raw slots: a block column of 128 weight rows, or (backward) of 64 for a
     // stage, without TMA only the 11 words of the half block that it needs
     static constexpr int kRawRows = kBack ? kStageK : kRows;
     static constexpr int kRawPitch = kTma ? kBoxBytes : kBack ? 44 : kBlockBytes;
     static constexpr int kRawBytes = kRawRows * kRawPitch;
-    static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : (kTma ? 2 : 3);
+    static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : kTmemA ? 4 : (kTma ? 2 : 3);
     static constexpr int kOffA = kStages * kXStage;
-    static constexpr int kOffRaw = kOffA + kStages * kABytes;
+    static constexpr int kOffRaw = kOffA + (kTmemA ? 0 : kStages * kABytes);
     static constexpr int kOffSums = kOffRaw + kRaw * kRawBytes;
     // with adapters: 64 t and an id for each token of the chunk
     static constexpr int kOffT = kOffSums + kChunk * kSumPitch * 4;
@@ -735,19 +741,31 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     const int i = 4 * b + own;
                     ok = stage_free(i);
                     if (!ok) break;
-                    const uint32_t dst = sbase + C::kOffA + (i % S) * kABytes;
+                    if constexpr (C::kTmemA) {
+                        fence_after();  // the MMAs that read this stage are done
+                        const uint32_t col = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) +
+                                             C::kColA + 32u * (i % S);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 4; ++j) tmem_store8(col + 8u * j, o[j]);
+                        tmem_store_wait();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_afull + 8 * (i % S));
+                    } else {
+                        const uint32_t dst = sbase + C::kOffA + (i % S) * kABytes;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            st_shared_v4(dst + sw128_offset(row, 2 * j + c), o[j][4 * c],
-                                         o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
-                    publish(i);
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                st_shared_v4(dst + sw128_offset(row, 2 * j + c), o[j][4 * c],
+                                             o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
+                        publish(i);
+                    }
                 }
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if ((warp == kMmaWarp && peer == 0) || (C::kIssuers == 2 && warp == kWaitWarp)) {
+    } else if ((warp == kMmaWarp && peer == 0) || (!kDuo && warp == kWaitWarp)) {
         // ---------------- MMA issuers ----------------
         // The waiter waits for the next two stages and meets the MMA warp at named
         // barrier 1; both pass it once for every two stages, whatever happens.
@@ -763,7 +781,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             const uint32_t acc = tmem + (index & 1) * C::kAccCols + static_cast<uint32_t>(me * kX);
             const int n_iters = 4 * (sg.q1 - sg.q0);
             for (int l0 = 0; l0 < n_iters; l0 += C::kHand, i0 += C::kHand) {
-                if (C::kIssuers == 2 && me == 1 && lane == 0 && !*abort_flag) {
+                if (!kDuo && me == 1 && lane == 0 && !*abort_flag) {
                     bool ok = l0 > 0 || index < 2 ||
                               mbar_wait_bounded(bar_accempty + 8 * (index & 1), ((index >> 1) - 1) & 1,
                                                 abort_flag, err, kErrTimeoutAccum);
@@ -778,7 +796,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 }
                 __syncwarp();
                 asm volatile("bar.sync 1, 64;" ::: "memory");
-                if (lane == 0 && !*abort_flag) {
+                if (me < C::kIssuers && lane == 0 && !*abort_flag) {
                     fence_after();
 #pragma unroll
                     for (int u = 0; u < C::kHand; ++u) {
@@ -787,9 +805,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         const uint64_t xdesc = xdesc0 + static_cast<uint64_t>(s * (C::kXStage >> 4));
                         const uint64_t adesc = adesc0 + static_cast<uint64_t>(s * (kABytes >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < kStageK / 16; ++kk)  // (backward: a K-step is 16 rows)
-                            mma<kDuo>(acc, adesc + (kBack ? 128u : 2u) * kk, xdesc + 2u * kk, idesc,
-                                      l0 + u >= C::kIssuers || kk > 0);
+                        for (int kk = 0; kk < kStageK / 16; ++kk) {
+                            const uint32_t add = l0 + u >= C::kIssuers || kk > 0;
+                            if constexpr (C::kTmemA)
+                                mma_tmem_a(acc, tmem + C::kColA + 32u * s + 8u * kk, xdesc + 2u * kk,
+                                           idesc, add);
+                            else  // (backward: a K-step is 16 rows)
+                                mma<kDuo>(acc, adesc + (kBack ? 128u : 2u) * kk, xdesc + 2u * kk, idesc, add);
+                        }
                         if (!C::kJointRelease) commit<kDuo>(bar_empty + 8 * s);
                     }
                     if (C::kJointRelease) {
@@ -801,7 +824,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 __syncwarp();
             }
         }
-        if (lane == 0 && *abort_flag) {
+        if (me < C::kIssuers && lane == 0 && *abort_flag) {
             // no MMA may still write TMEM when it is freed
             commit<kDuo>(bar_drain);
             volatile int no_abort = 0;
