@@ -111,29 +111,23 @@ enum class Tc { kGated, kLora, kBackward };
 // 128 and fewer: the decode bounds, and narrow MMAs that read A from shared
 // memory take as long as wide ones (100 clocks each, measured), so decoded
 // weights go to tensor memory (not backward, where they would have to be
-// transposed).  Narrow MMAs issue at half the rate the tensor core takes them:
-// two threads issue, each into its own accumulator, where tensor memory has room
-// (14336 x 4096, 64 tokens: 55 us with A in shared memory).
+// transposed).  (14336 x 4096, 64 tokens: 55 us with A in shared memory.)
 template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
     static constexpr bool kDuo = kX == 256;
     static constexpr int kCtas = kDuo ? 2 : 1;
     static constexpr bool kTmemA = !kBack && !kDuo;
-    static constexpr int kIssuers = kDuo || (kTmemA && kX == 128) ? 1 : 2;
     static constexpr int kHand = 2;                      // stages handed over at a time
     static constexpr int kHold = kX / kCtas;             // tokens of a stage in this CTA
     static constexpr int kXStage = kHold * kStageK * 2;
     // stages in flight, tokens and decoded weights alike (one release for both)
     static constexpr int kStages = kTmemA ? 8 : kX >= 128 ? 5 : kX == 64 ? 7 : 8;
     static constexpr int kGroupWarps = 4;  // decoders: four groups, a stage each in turn
-    // A decoder waits for the MMAs of stage i - kStages by its barrier's parity,
-    // which is right only if those of i - 2 kStages are known to be done: its
-    // wait before covered stage i - 4 - kStages.  Two issuers' MMAs of one
-    // hand-over end in any order, so where both stages may belong to the same
-    // one, each issuer releases both of a hand-over's stages.
-    static constexpr bool kJointRelease = kIssuers == 2 && kStages - 4 < kHand;
-    static constexpr uint32_t kAccCols = kX * kIssuers;  // a tile's sums; two sets
+    // (MMAs end in the order of their issue: a decoder's wait for those of stage
+    // i - kStages by its barrier's parity is right because its wait before, for
+    // stage i - 4 - kStages, covered i - 2 kStages)
+    static constexpr uint32_t kAccCols = kX;             // a tile's sums; two sets
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColA = 2 * kAccCols;      // 32 columns per decoded stage
     static_assert(kColA + (kTmemA ? 32 * kStages : 0) <= kTmemCols, "tensor memory");
@@ -510,7 +504,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = kBack ? p.K : p.N;  // rows of the product
     const int peer = kDuo ? static_cast<int>(blockIdx.x & 1) : 0;
     Work work;
@@ -549,18 +543,18 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             mbar_init(bar_xfull + 8 * s, 1);               // the producer's expect-tx arrival
             mbar_init(bar_afull + 8 * s, C::kGroupWarps);  // the warps of its group
             mbar_init(bar_peer + 8 * s, 1);                // the second CTA's waiter
-            mbar_init(bar_empty + 8 * s, C::kJointRelease ? 2 : 1);  // MMA commits
+            mbar_init(bar_empty + 8 * s, 1);  // MMA commits
         }
         for (int r = lane; r < C::kRaw; r += 32) {
             mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
             mbar_init(bar_rawempty + 8 * r, kBack ? C::kGroupWarps : kDecWarps);
         }
         if (lane < 2) {
-            mbar_init(bar_accfull + 8 * lane, C::kIssuers);
+            mbar_init(bar_accfull + 8 * lane, 1);
             mbar_init(bar_accempty + 8 * lane, 4 * C::kCtas);  // epilogue warps
         }
         if (lane == 0) {
-            mbar_init(bar_drain, C::kIssuers);
+            mbar_init(bar_drain, 1);
             *abort_flag = 0;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -571,6 +565,9 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     else __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    auto hand_over = [&]() {  // the waiter and the issuer
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+    };
 
     if (warp < kDecWarps) {
         // ---------------- weight decoders ----------------
@@ -765,76 +762,59 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if ((warp == kMmaWarp && peer == 0) || (!kDuo && warp == kWaitWarp)) {
-        // ---------------- MMA issuers ----------------
-        // The waiter waits for the next two stages and meets the MMA warp at named
-        // barrier 1; both pass it once for every two stages, whatever happens.
-        // With two issuers the MMA warp takes the even stages into one
-        // accumulator, the waiter the odd ones into another.
-        const int me = warp == kMmaWarp ? 0 : 1;
+    } else if (warp == kMmaWarp && peer == 0) {
+        // ---------------- MMA issuer ----------------
+        // It meets the waiter at named barrier 1 once for every two stages, when
+        // both are filled and, at a tile's first, its set of sums is free; both
+        // pass it the same number of times, whatever happens.  Nothing but MMAs
+        // and commits stands between its MMAs.  The thread comes from
+        // elect.sync, not from a test of its lane: only so are an MMA's
+        // descriptors computed in uniform registers, without a transfer each
+        // before every MMA (512 tokens, 14336 x 4096: 82 us against 93).
         const uint64_t xdesc0 = sw128_desc(sbase);
         const uint64_t adesc0 = kBack ? sw128_mn_desc(sbase + C::kOffA, 8192)
                                       : sw128_desc(sbase + C::kOffA);
         int i0 = 0;  // stages, counted over all segments
         for (int index = 0; work.segment(index, sg); ++index) {
             const uint32_t idesc = bf16_idesc(C::kCtas * kRows, mma_n(sg.tile)) | (kBack ? kIdescAMnMajor : 0u);
-            const uint32_t acc = tmem + (index & 1) * C::kAccCols + static_cast<uint32_t>(me * kX);
+            const uint32_t acc = tmem + (index & 1) * C::kAccCols;
             const int n_iters = 4 * (sg.q1 - sg.q0);
             for (int l0 = 0; l0 < n_iters; l0 += C::kHand, i0 += C::kHand) {
-                if (!kDuo && me == 1 && lane == 0 && !*abort_flag) {
-                    bool ok = l0 > 0 || index < 2 ||
-                              mbar_wait_bounded(bar_accempty + 8 * (index & 1), ((index >> 1) - 1) & 1,
-                                                abort_flag, err, kErrTimeoutAccum);
-#pragma unroll
-                    for (int u = 0; u < C::kHand; ++u) {
-                        const int i = i0 + u;
-                        ok = ok && mbar_wait_bounded(bar_xfull + 8 * (i % S), (i / S) & 1, abort_flag,
-                                                     err, kErrTimeoutFull) &&
-                             mbar_wait_bounded(bar_afull + 8 * (i % S), (i / S) & 1, abort_flag, err,
-                                               kErrTimeoutFull);
-                    }
-                }
-                __syncwarp();
-                asm volatile("bar.sync 1, 64;" ::: "memory");
-                if (me < C::kIssuers && lane == 0 && !*abort_flag) {
+                hand_over();
+                if (elect_one() && !*abort_flag) {
                     fence_after();
 #pragma unroll
                     for (int u = 0; u < C::kHand; ++u) {
-                        if (C::kIssuers == 2 && u != me) continue;
                         const int s = (i0 + u) % S;
                         const uint64_t xdesc = xdesc0 + static_cast<uint64_t>(s * (C::kXStage >> 4));
                         const uint64_t adesc = adesc0 + static_cast<uint64_t>(s * (kABytes >> 4));
 #pragma unroll
                         for (int kk = 0; kk < kStageK / 16; ++kk) {
-                            const uint32_t add = l0 + u >= C::kIssuers || kk > 0;
+                            const uint32_t add = l0 + u > 0 || kk > 0;
                             if constexpr (C::kTmemA)
                                 mma_tmem_a(acc, tmem + C::kColA + 32u * s + 8u * kk, xdesc + 2u * kk,
                                            idesc, add);
                             else  // (backward: a K-step is 16 rows)
                                 mma<kDuo>(acc, adesc + (kBack ? 128u : 2u) * kk, xdesc + 2u * kk, idesc, add);
                         }
-                        if (!C::kJointRelease) commit<kDuo>(bar_empty + 8 * s);
-                    }
-                    if (C::kJointRelease) {
-#pragma unroll
-                        for (int u = 0; u < C::kHand; ++u) commit<kDuo>(bar_empty + 8 * ((i0 + u) % S));
+                        commit<kDuo>(bar_empty + 8 * s);
                     }
                     if (l0 + C::kHand == n_iters) commit<kDuo>(bar_accfull + 8 * (index & 1));
                 }
                 __syncwarp();
             }
         }
-        if (me < C::kIssuers && lane == 0 && *abort_flag) {
+        if (elect_one() && *abort_flag) {
             // no MMA may still write TMEM when it is freed
             commit<kDuo>(bar_drain);
             volatile int no_abort = 0;
             mbar_wait_bounded(bar_drain, 0, &no_abort, err, kErrTimeoutDrain);
         }
         __syncwarp();
-    } else if (kDuo && warp == kWaitWarp) {
-        // ---------------- stage waiters of a pair of CTAs ----------------
-        // The second CTA's waiter reports each of its stages to the first's,
-        // which waits for both CTAs' and hands them to the MMA warp.
+    } else if (warp == kWaitWarp) {
+        // ---------------- stage waiter ----------------
+        // Two CTAs: the second one's waiter reports each of its stages to the
+        // first's, which waits for both.
         int i0 = 0;
         for (int index = 0; work.segment(index, sg); ++index) {
             const int n_iters = 4 * (sg.q1 - sg.q0);
@@ -849,13 +829,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         const uint32_t at = 8 * (i % S), phase = (i / S) & 1;
                         ok = ok && mbar_wait_bounded(bar_xfull + at, phase, abort_flag, err, kErrTimeoutFull) &&
                              mbar_wait_bounded(bar_afull + at, phase, abort_flag, err, kErrTimeoutFull);
-                        if (ok && peer == 1) arrive_first_of_pair(bar_peer + at);
-                        if (peer == 0)
+                        if (kDuo && ok && peer == 1) arrive_first_of_pair(bar_peer + at);
+                        if (kDuo && peer == 0)
                             ok = ok && wait_peer_bounded(bar_peer + at, phase, abort_flag, err, kErrTimeoutFull);
                     }
                 }
                 __syncwarp();
-                if (peer == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
+                if (peer == 0) hand_over();
             }
         }
     } else if (warp == kWWarp) {
@@ -946,7 +926,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         }
         emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
     };
-    if (warp >= kEpiWarp0 || warp < kDecWarps) {
+    const bool brings_out = warp < kDecWarps || warp >= kEpiWarp0;
+    if (brings_out) {
         // ---------------- epilogue: sums -> results ----------------
         // (what is written here, and t, may still be in use by the grid before)
         pdl_wait_prerequisites();
@@ -981,15 +962,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             const uint32_t t_lane = tmem + (index & 1) * C::kAccCols +
                                     (static_cast<uint32_t>(32 * quarter) << 16);
             // 16 tokens of this lane's row, from c0 on
-            auto load_sums = [&](int c0, float (&v)[16]) {
-                tmem_load16(t_lane + c0, v);
-                if (C::kIssuers == 2) {
-                    float u[16];
-                    tmem_load16(t_lane + kX + c0, u);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] += u[q];
-                }
-            };
+            auto load_sums = [&](int c0, float (&v)[16]) { tmem_load16(t_lane + c0, v); };
             auto release = [&]() {  // the sums are read: their set may be reused
                 if (final) return;  // (by none)
                 fence_before();
@@ -1102,7 +1075,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         fence_before();
         __syncwarp();
         cluster_sync();
-        if (warp >= kEpiWarp0 || warp < kDecWarps) {
+        if (brings_out) {
             Team team;
             team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
                                            : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
