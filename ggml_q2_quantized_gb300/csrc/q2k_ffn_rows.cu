@@ -43,6 +43,8 @@ constexpr int kUnitRows = 16;         // rows of an MMA tile; a unit has two til
 // Row r of an item starts at word 21 r + 28 (r / 4): the eight rows and four
 // 16-byte slices that a warp reads together then fall on 32 different banks.
 constexpr int kItemBytes = 4 * 4 * 112;
+constexpr int kMaxDepth = 8;          // units in flight of a streaming CTA
+constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int kGroupUnits = 8;        // units whose sums are kept when K takes several passes
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -208,11 +210,8 @@ __device__ __forceinline__ void scale_pairs(uint32_t sc, uint32_t (&s)[4]) {
 // One block of 16 weight rows (rows g and g + 8 of this lane) times NT columns
 // of eight: acc += d sum q sc x - dmin sum m X, scaled back.
 template <typename T, int NT>
-__device__ __forceinline__ void block_product(uint32_t item, int lane, const XBlock<T> (&x)[NT],
-                                              float (&acc)[NT][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t row = item + 84 * (g & 3) + 448 * (g >> 2);
-    const RowWords a = read_row(row, t), b = read_row(row + 896, t);
+__device__ __forceinline__ void block_product(const RowWords& a, const RowWords& b,
+                                              const XBlock<T> (&x)[NT], float (&acc)[NT][4]) {
     uint32_t sa[4], sb[4];
     scale_pairs(a.sc, sa);
     scale_pairs(b.sc, sb);
@@ -255,6 +254,129 @@ __device__ __forceinline__ void block_product(uint32_t item, int lane, const XBl
     }
 }
 
+// One block of one token as integers, for the slice t of each row that a lane has:
+// x 2^(21 - e), e the exponent of the block's largest |x|, rounded to 22 bits and
+// sign (exact for a bf16 x down to 2^-14 of the largest), its three bytes in a word
+// each for four weights that lie in one quant word at one shift; and the bytes of
+// the group sums X_g of the slice's four shifts.  The last byte is signed.
+struct XBytes {
+    uint32_t x[4][3][4];  // shift, byte, quant word
+    uint32_t s[4];
+    float undo;
+};
+constexpr int kXWords = 4 * (3 * 16 + 4) + 4;  // a block's, in shared memory (the last: undo)
+
+template <typename T>
+__device__ __forceinline__ void make_x_bytes(const T* x, int block, int lane, uint32_t* buf) {
+    // this lane's part: eight weights of slice t at shift g / 2, words 2 (g % 2) ..
+    const int g = lane >> 2, t = lane & 3, j = g >> 1, half = g & 1;
+    const T* p = x + 256 * block + 128 * (t >> 1) + 32 * j + 16 * (t & 1) + 8 * half;
+    float v[8];
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) top = fmaxf(top, fabsf(v[l]));
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 21 - e) << 23);
+    // (e = 128: an infinity or NaN in x makes every sum of the block NaN)
+    if (lane == 0)
+        buf[kXWords - 1] = e > 127 ? 0x7FC00000u : static_cast<uint32_t>(127 - 21 + e) << 23;
+    uint32_t w[8];
+    int sum = 0;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        // 1.5 2^23 + an integer of less than 2^22: its low bits are that integer's
+        w[l] = __float_as_uint(fmaf(v[l], up, 12582912.f)) - 0x4B400000u;
+        sum += static_cast<int>(w[l]);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t* a = w + 4 * q;
+        const uint32_t p01 = __byte_perm(a[0], a[1], 0x5140u), p23 = __byte_perm(a[2], a[3], 0x5140u);
+        const uint32_t h01 = __byte_perm(a[0], a[1], 0x0062u), h23 = __byte_perm(a[2], a[3], 0x0062u);
+        uint32_t* to = buf + 52 * t + 12 * j + 2 * half + q;
+        to[0] = __byte_perm(p01, p23, 0x5410u);
+        to[4] = __byte_perm(p01, p23, 0x7632u);
+        to[8] = __byte_perm(h01, h23, 0x5410u);
+    }
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+    // byte g / 2 of the four sum words is this shift's
+    if (half == 0) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            reinterpret_cast<uint8_t*>(buf + 52 * t + 48 + d)[j] = static_cast<uint8_t>(sum >> (8 * d));
+    }
+}
+
+__device__ __forceinline__ void take_x_bytes(const uint32_t* buf, int lane, XBytes& o) {
+    const uint4* from = reinterpret_cast<const uint4*>(buf + 52 * (lane & 3));
+#pragma unroll
+    for (int c = 0; c < 13; ++c) {
+        const uint4 u = from[c];
+        uint32_t* to = c < 12 ? o.x[c / 3][c % 3] : o.s;
+        to[0] = u.x, to[1] = u.y, to[2] = u.z, to[3] = u.w;
+    }
+    o.undo = __uint_as_float(buf[kXWords - 1]);
+}
+
+// c + the four products of a's unsigned bytes with b's unsigned or signed ones.
+__device__ __forceinline__ int dot4_uu(uint32_t a, uint32_t b, int c) {
+    uint32_t d;
+    asm("dp4a.u32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(static_cast<uint32_t>(c)));
+    return static_cast<int>(d);
+}
+__device__ __forceinline__ int dot4_us(uint32_t a, uint32_t b, int c) {
+    int d;
+    asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// One row's slice of a block times one token, all in integers: codes are masked in
+// place (4^j q) and meet sc_j 4^(3 - j), so every product carries 64; a byte's sum
+// over a slice is below 2^26.
+__device__ __forceinline__ float slice_product(const RowWords& r, const XBytes& x) {
+    int a0 = 0, a1 = 0, a2 = 0;
+    const int sc[4] = {static_cast<int>((r.sc << 6) & 0x3C0u), static_cast<int>((r.sc >> 4) & 0xF0u),
+                       static_cast<int>((r.sc >> 14) & 0x3Cu), static_cast<int>((r.sc >> 24) & 0xFu)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        int s0 = 0, s1 = 0, s2 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t q = r.q[i] & (0x03030303u << (2 * j));
+            s0 = dot4_uu(q, x.x[j][0][i], s0);
+            s1 = dot4_uu(q, x.x[j][1][i], s1);
+            s2 = dot4_us(q, x.x[j][2][i], s2);
+        }
+        a0 += s0 * sc[j];
+        a1 += s1 * sc[j];
+        a2 += s2 * sc[j];
+    }
+    // minima, m in the high nibbles: products carry 16
+    const uint32_t m = r.sc & 0xF0F0F0F0u;
+    const int e0 = dot4_uu(m, x.s[0], 0) + 256 * dot4_uu(m, x.s[1], 0);
+    const int e1 = dot4_uu(m, x.s[2], 0) + 256 * dot4_us(m, x.s[3], 0);
+    const float a = fmaf(65536.f, static_cast<float>(a2),
+                         fmaf(256.f, static_cast<float>(a1), static_cast<float>(a0)));
+    const float e = fmaf(65536.f, static_cast<float>(e1), static_cast<float>(e0));
+    return fmaf(f16_bits_to_float(r.dd) * 0x1p-6f, a, f16_bits_to_float(r.dd >> 16) * -0x1p-4f * e);
+}
+
 struct RowsArgs {
     const uint8_t* w0;    // tiles 0 and 1 of a unit: rows from unit * unit_step on
     const uint8_t* w1;
@@ -278,6 +400,9 @@ struct RowsArgs {
     const int* ids;
     void* y;
     int R, n_adapters;
+    // streamed tiles
+    int tile_rows, depth;  // rows of a tile; units in flight
+    unsigned int* err;
 };
 
 enum class Rows { kGated, kLora };
@@ -287,12 +412,89 @@ __device__ __forceinline__ void cp_async_word(uint32_t dst, const void* src, uin
                  : "memory");
 }
 
+template <typename T, int NT>
+struct Pass {
+    static constexpr int kTokens = NT == 0 ? 1 : NT * (sizeof(T) == 4 ? 4 : 8);
+    static constexpr int kSums = NT == 0 ? kUnitRows : 32 * NT * (sizeof(T) == 4 ? 2 : 4);  // of a tile
+};
+
+// A warp's sums of two tiles, in fragment order.
+template <typename T, int NT>
+__device__ __forceinline__ void write_sums(float* mine, int lane, const float (&acc)[2][NT][4]) {
+    constexpr int kOut = Pass<T, NT>::kSums;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (sizeof(T) == 4) {  // hi and lo columns of a token
+                mine[a * kOut + (2 * n) * 32 + lane] = acc[a][n][0] + acc[a][n][1];
+                mine[a * kOut + (2 * n + 1) * 32 + lane] = acc[a][n][2] + acc[a][n][3];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mine[a * kOut + (4 * n + c) * 32 + lane] = acc[a][n][c];
+            }
+        }
+}
+
+// Sum o of a unit's two tiles -> results.
+template <typename T, int NT, Rows kMode>
+__device__ __forceinline__ void finish_row(const RowsArgs& p, int o, float (&v)[2], int unit, int m0) {
+    constexpr bool kSplit = sizeof(T) == 4;
+    const int f = o >> 5, l = o & 31;
+    // fragment f of lane l: its row of the tile and its token
+    const int r = NT == 0 ? o : (l >> 2) + 8 * (kSplit ? f & 1 : (f >> 1) & 1);
+    const int m = m0 + (NT == 0  ? 0
+                        : kSplit ? (f >> 1) * 4 + (l & 3)
+                                 : (f >> 2) * 8 + 2 * (l & 3) + (f & 1));
+    const int n = unit * p.unit_step + r;
+    if (m >= p.M) return;
+    if (kMode == Rows::kGated) {
+        if (n >= p.N) return;
+        const size_t at = static_cast<size_t>(m) * p.N + n;
+        static_cast<T*>(p.h)[at] = from_float<T>(act_value<!kSplit>(v[0], p.act) * v[1]);
+        if (p.gate != nullptr) {
+            static_cast<T*>(p.gate)[at] = from_float<T>(v[0]);
+            static_cast<T*>(p.up)[at] = from_float<T>(v[1]);
+        }
+    } else {
+        const int id = p.ids[m];
+        const bool has = id >= 0 && id < p.n_adapters;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int na = n + a * p.tile1_row;
+            if (na >= p.N) continue;
+            if (has) {
+                const uint4* br = reinterpret_cast<const uint4*>(
+                    p.b + (static_cast<size_t>(id) * p.N + na) * p.R);
+                const float4* tr = reinterpret_cast<const float4*>(
+                    p.t + static_cast<size_t>(m) * p.R);
+                for (int c = 0; c < p.R / 8; ++c) {
+                    const uint4 bv = __ldg(br + c);
+                    const float4 t0 = tr[2 * c], t1 = tr[2 * c + 1];
+                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+                    const float tv[8] = {t0.x, t0.y, t0.z, t0.w,
+                                         t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[a] = fmaf(__uint_as_float(bw[q] << 16), tv[2 * q], v[a]);
+                        v[a] = fmaf(__uint_as_float(bw[q] & 0xFFFF0000u),
+                                    tv[2 * q + 1], v[a]);
+                    }
+                }
+            } else if (id != -1) {
+                v[a] = 0.f;  // an id out of range: a zero row
+            }
+            static_cast<T*>(p.y)[static_cast<size_t>(m) * p.N + na] =
+                from_float<T>(v[a]);
+        }
+    }
+}
+
 template <typename T, int NT, int S, Rows kMode>
 __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restrict__ x, RowsArgs p) {
     constexpr bool kSplit = sizeof(T) == 4;
-    constexpr int kTokens = NT * (kSplit ? 4 : 8);  // tokens of a pass
-    constexpr int kFrag = NT * (kSplit ? 2 : 4);    // a thread's sums of one tile
-    constexpr int kOut = 32 * kFrag;                // sums of one tile
+    constexpr int kTokens = Pass<T, NT>::kTokens;       // tokens of a pass
+    constexpr int kOut = Pass<T, NT>::kSums;            // sums of one tile
     extern __shared__ __align__(16) uint8_t smem[];
     // (a shuffle tells the compiler that the warp's index is uniform)
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -398,25 +600,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                         // item's words are in; the item before is read by all lanes
                         __syncwarp();
                         issue();
-                        block_product<T, NT>(ring + (item % kDepth) * kItemBytes, lane, xb[s], acc[a]);
+                        const uint32_t row = ring + (item % kDepth) * kItemBytes +
+                                             84 * ((lane >> 2) & 3) + 448 * (lane >> 4);
+                        block_product<T, NT>(read_row(row, lane & 3), read_row(row + 896, lane & 3), xb[s],
+                                             acc[a]);
                         ++item;
                     }
                 }
                 // this warp's sums, in fragment order
-                float* mine = red + (static_cast<size_t>(u & 1) * p.kw + kw) * (2 * kOut);
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (kSplit) {  // hi and lo columns of a token
-                            mine[a * kOut + (2 * n) * 32 + lane] = acc[a][n][0] + acc[a][n][1];
-                            mine[a * kOut + (2 * n + 1) * 32 + lane] = acc[a][n][2] + acc[a][n][3];
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                mine[a * kOut + (4 * n + c) * 32 + lane] = acc[a][n][c];
-                        }
-                    }
+                write_sums<T, NT>(red + (static_cast<size_t>(u & 1) * p.kw + kw) * (2 * kOut), lane, acc);
                 asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(group_threads) : "memory");
                 const bool last = pass == p.passes - 1;
                 if (kMode == Rows::kLora && last && !waited) {
@@ -443,53 +635,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                             continue;
                         }
                     }
-                    const int f = o >> 5, l = o & 31;
-                    // fragment f of lane l: its row of the tile and its token
-                    const int r = (l >> 2) + 8 * (kSplit ? f & 1 : (f >> 1) & 1);
-                    const int m = m0 + (kSplit ? (f >> 1) * 4 + (l & 3)
-                                               : (f >> 2) * 8 + 2 * (l & 3) + (f & 1));
-                    const int n = unit * p.unit_step + r;
-                    if (m >= p.M) continue;
-                    if (kMode == Rows::kGated) {
-                        if (n >= p.N) continue;
-                        const size_t at = static_cast<size_t>(m) * p.N + n;
-                        static_cast<T*>(p.h)[at] = from_float<T>(act_value<!kSplit>(v[0], p.act) * v[1]);
-                        if (p.gate != nullptr) {
-                            static_cast<T*>(p.gate)[at] = from_float<T>(v[0]);
-                            static_cast<T*>(p.up)[at] = from_float<T>(v[1]);
-                        }
-                    } else {
-                        const int id = p.ids[m];
-                        const bool has = id >= 0 && id < p.n_adapters;
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const int na = n + a * p.tile1_row;
-                            if (na >= p.N) continue;
-                            if (has) {
-                                const uint4* br = reinterpret_cast<const uint4*>(
-                                    p.b + (static_cast<size_t>(id) * p.N + na) * p.R);
-                                const float4* tr = reinterpret_cast<const float4*>(
-                                    p.t + static_cast<size_t>(m) * p.R);
-                                for (int c = 0; c < p.R / 8; ++c) {
-                                    const uint4 bv = __ldg(br + c);
-                                    const float4 t0 = tr[2 * c], t1 = tr[2 * c + 1];
-                                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-                                    const float tv[8] = {t0.x, t0.y, t0.z, t0.w,
-                                                         t1.x, t1.y, t1.z, t1.w};
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        v[a] = fmaf(__uint_as_float(bw[q] << 16), tv[2 * q], v[a]);
-                                        v[a] = fmaf(__uint_as_float(bw[q] & 0xFFFF0000u),
-                                                    tv[2 * q + 1], v[a]);
-                                    }
-                                }
-                            } else if (id != -1) {
-                                v[a] = 0.f;  // an id out of range: a zero row
-                            }
-                            static_cast<T*>(p.y)[static_cast<size_t>(m) * p.N + na] =
-                                from_float<T>(v[a]);
-                        }
-                    }
+                    finish_row<T, NT, kMode>(p, o, v, unit, m0);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -502,10 +648,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
 
 template <typename T, int NT, int S, Rows kMode>
 cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cudaStream_t stream) {
-    constexpr int kTokens = NT * (sizeof(T) == 4 ? 4 : 8);
-    constexpr int kOut = 32 * NT * (sizeof(T) == 4 ? 2 : 4);
-    constexpr int kSmem = kWarps * kDepth * kItemBytes + kWarps * 2 * 2 * kOut * 4 +
-                          kGroupUnits * 2 * kOut * 4;
+    constexpr int kTokens = Pass<T, NT>::kTokens;
+    constexpr int kOut = Pass<T, NT>::kSums;
+    constexpr int kSmem = kWarps * kDepth * kItemBytes + (kWarps * 2 + kGroupUnits) * 2 * kOut * 4 ;
     static_assert(kSmem <= 232448, "shared memory");
     static bool attr_done[64] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
@@ -534,12 +679,214 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode>, static_cast<const T*>(x), p);
 }
 
+// The same product where a CTA takes whole rows: a tile of 16 (or 8) rows is one
+// contiguous piece of the matrix, so one bulk copy fetches it, where 84-byte
+// columns take a word a lane (16 copy instructions for 16 rows x 256 weights,
+// which the load unit could not issue at more than 3.9 TB/s).  Warp w has blocks w,
+// w + 16, ..., and the warps' sums meet as above; the barrier there also says that
+// the unit's slot is free, so a thread that passes it refills the slot at once.
+// NT = 0: one token, as integers (see XBytes).
+template <typename T, int NT, Rows kMode>
+__global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restrict__ x, RowsArgs p) {
+    constexpr bool kBytes = NT == 0;
+    constexpr int kTokens = Pass<T, NT>::kTokens, kOut = Pass<T, NT>::kSums;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const int m0 = blockIdx.y * kTokens;
+    const int blocks = p.K / kQK, row_bytes = blocks * kBlockBytes;
+    const int tile_bytes = p.tile_rows * row_bytes;
+    float* red = reinterpret_cast<float*>(smem);
+    uint32_t* xs = reinterpret_cast<uint32_t*>(smem + kWarps * 2 * 2 * kOut * 4);
+    uint8_t* slots = reinterpret_cast<uint8_t*>(xs + (kBytes ? blocks * kXWords : 0));
+    const uint32_t bars = smem_u32(slots + static_cast<size_t>(p.depth) * 2 * tile_bytes);
+    volatile int* abort_flag =
+        reinterpret_cast<volatile int*>(slots + static_cast<size_t>(p.depth) * 2 * tile_bytes + 8 * kMaxDepth);
+    const int my_units = (p.units - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    auto issue = [&](int u) {
+        if (u >= my_units) return;
+        const int unit = static_cast<int>(blockIdx.x) + u * static_cast<int>(gridDim.x);
+        uint8_t* slot = slots + static_cast<size_t>(u % p.depth) * 2 * tile_bytes;
+        const uint32_t bar = bars + 8 * (u % p.depth);
+        const uint8_t* src[2];
+        uint32_t bytes[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int row0 = unit * p.unit_step + (a ? p.tile1_row : 0);
+            const int valid = min(max(p.N - row0, 0), p.tile_rows);
+            src[a] = (a ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes;
+            bytes[a] = static_cast<uint32_t>(valid * row_bytes);
+            // (the matrix may end off 16 bytes)
+            for (uint32_t at = bytes[a] & ~15u; at < bytes[a]; at += 4)
+                *reinterpret_cast<uint32_t*>(slot + a * tile_bytes + at) =
+                    __ldg(reinterpret_cast<const uint32_t*>(src[a] + at));
+        }
+        mbar_arrive_expect_tx(bar, (bytes[0] & ~15u) + (bytes[1] & ~15u));
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+            if ((bytes[a] & ~15u) != 0)
+                bulk_copy_g2s(smem_u32(slot + a * tile_bytes), src[a], bytes[a] & ~15u, bar);
+    };
+    pdl_allow_dependents();
+    bool waited = false;
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int d = 0; d < p.depth; ++d) mbar_init(bars + 8 * d, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (!p.const_weights) {
+            pdl_wait_prerequisites();
+            waited = true;
+        }
+        for (int d = 0; d < p.depth; ++d) issue(d);
+    }
+    if (!waited && !p.x_ready) pdl_wait_prerequisites();
+    waited = waited || !p.x_ready;
+    XBytes xi;
+    XBlock<T> xm[kBytes ? 1 : NT];
+    if constexpr (kBytes) {
+        for (int b = warp; b < blocks; b += kWarps) make_x_bytes(x, b, lane, xs + b * kXWords);
+        __syncwarp();
+        if (warp < blocks) take_x_bytes(xs + warp * kXWords, lane, xi);
+    } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (warp < blocks) load_x_block(x, p.K, warp, m0 + n * (kTokens / NT), p.M, lane, xm[n]);
+    }
+    __syncthreads();
+    for (int u = 0; u < my_units; ++u) {
+        const int unit = static_cast<int>(blockIdx.x) + u * static_cast<int>(gridDim.x);
+        const uint32_t slot = smem_u32(slots) + (u % p.depth) * 2 * tile_bytes;
+        mbar_wait_bounded(bars + 8 * (u % p.depth), (u / p.depth) & 1, abort_flag, p.err, kErrTimeoutFull);
+        float* mine = red + ((u & 1) * kWarps + warp) * (2 * kOut);
+        if constexpr (kBytes) {
+            float acc[2][2] = {};
+            for (int b = warp; b < blocks; b += kWarps) {
+                if (blocks > kWarps) take_x_bytes(xs + b * kXWords, lane, xi);
+                const uint32_t row = slot + b * kBlockBytes + (lane >> 2) * row_bytes;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (r == 0 || p.tile_rows > 8)
+                            acc[a][r] = fmaf(xi.undo,
+                                             slice_product(read_row(row + a * tile_bytes + 8 * r * row_bytes,
+                                                                    lane & 3), xi),
+                                             acc[a][r]);
+            }
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float v = acc[a][r];
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+                    if ((lane & 3) == 0) mine[a * kOut + 8 * r + (lane >> 2)] = v;
+                }
+        } else {
+            float acc[2][NT][4] = {};
+            if (warp < blocks) {
+                const uint32_t row = slot + warp * kBlockBytes + (lane >> 2) * row_bytes;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    block_product<T, NT>(read_row(row + a * tile_bytes, lane & 3),
+                                         read_row(row + a * tile_bytes + 8 * row_bytes, lane & 3), xm,
+                                         acc[a]);
+            }
+            write_sums<T, NT>(mine, lane, acc);
+        }
+        __syncthreads();
+        // the warps take turns to bring a unit out
+        const int turn = (warp + u) & (kWarps - 1);
+        if (turn == kWarps - 1 && lane == 0) issue(u + p.depth);
+        if (kMode == Rows::kLora && !waited) {
+            pdl_wait_prerequisites();  // t
+            waited = true;
+        }
+        const float* all = red + (u & 1) * kWarps * (2 * kOut);
+        for (int o = 32 * turn + lane; o < kOut; o += 32 * kWarps) {
+            if (kBytes && o >= p.tile_rows) break;
+            float v[2] = {0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                v[0] += all[w * (2 * kOut) + o];
+                v[1] += all[w * (2 * kOut) + kOut + o];
+            }
+            finish_row<T, NT, kMode>(p, o, v, unit, m0);
+        }
+    }
+    if (!waited) pdl_wait_prerequisites();
+    if (*abort_flag) {
+        // no copy may still write shared memory when it is given back
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {}
+    }
+}
+
+// Shared memory beside the slots, and whether tiles can be streamed.
+template <typename T, int NT>
+bool plan_stream(RowsArgs& p, size_t& smem) {
+    const int blocks = p.K / kQK;
+    if (blocks <= kWarps / 2 || (NT != 0 && blocks > kWarps)) return false;
+    if (((reinterpret_cast<uintptr_t>(p.w0) | reinterpret_cast<uintptr_t>(p.w1)) & 15) != 0) return false;
+    const size_t fixed = kWarps * 2 * 2 * Pass<T, NT>::kSums * 4 +
+                         (NT == 0 ? static_cast<size_t>(blocks) * kXWords * 4 : 0) + 8 * kMaxDepth + 16;
+    // rows of 16, of which three units fit; else of eight
+    for (int rows = kUnitRows; rows >= (NT == 0 ? 8 : kUnitRows); rows -= 8) {
+        const size_t unit = 2 * static_cast<size_t>(rows) * blocks * kBlockBytes;
+        if (fixed + 2 * unit > kMaxSmem) continue;
+        p.depth = static_cast<int>(std::min<size_t>(kMaxDepth, (kMaxSmem - fixed) / unit));
+        if (rows > 8 && NT == 0 && p.depth < 3) continue;
+        p.unit_step = p.unit_step / kUnitRows * rows;
+        p.tile1_row = p.tile1_row / kUnitRows * rows;
+        p.tile_rows = rows;
+        p.units = (p.N + p.unit_step - 1) / p.unit_step;
+        smem = fixed + p.depth * unit;
+        return true;
+    }
+    return false;
+}
+
+template <typename T, int NT, Rows kMode>
+cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, int sm_count,
+                          cudaStream_t stream) {
+    static bool attr_done[64] = {};
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[device]) {
+        const cudaError_t e = cudaFuncSetAttribute(stream_kernel<T, NT, kMode>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kMaxSmem);
+        if (e != cudaSuccess) return e;
+        attr_done[device] = true;
+    }
+    cudaError_t e = ffn_error_word(device, &p.err);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(sm_count, p.units), (p.M + Pass<T, NT>::kTokens - 1) / Pass<T, NT>::kTokens);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode>, static_cast<const T*>(x), p);
+}
+
 // Columns of x in registers: one tile of eight and up to two blocks a warp, or
 // two tiles (more than 8 bf16 or 4 f32 tokens) and one block.
 template <typename T, Rows kMode>
 cudaError_t launch_rows_mode(const void* x, RowsArgs& p, int device, int sm_count,
                              cudaStream_t stream) {
-    if (p.M > (sizeof(T) == 4 ? 4 : 8))
+    constexpr int kOne = sizeof(T) == 4 ? 4 : 8;
+    size_t smem = 0;
+    if (p.M == 1 && plan_stream<T, 0>(p, smem))
+        return launch_stream<T, 0, kMode>(x, p, smem, device, sm_count, stream);
+    if (p.M <= kOne && plan_stream<T, 1>(p, smem))
+        return launch_stream<T, 1, kMode>(x, p, smem, device, sm_count, stream);
+    if (p.M > kOne && plan_stream<T, 2>(p, smem))
+        return launch_stream<T, 2, kMode>(x, p, smem, device, sm_count, stream);
+    if (p.M > kOne)
         return launch_as<T, 2, 1, kMode>(x, p, device, sm_count, stream);
     if (p.K / kQK > kWarps) return launch_as<T, 1, 2, kMode>(x, p, device, sm_count, stream);
     return launch_as<T, 1, 1, kMode>(x, p, device, sm_count, stream);

@@ -40,6 +40,7 @@
 // Every wait is bounded (about a second); on time-out the kernel records a bit
 // in the device error word, drains its MMAs, frees TMEM and returns.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -1493,6 +1494,20 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     t.quads = 2 * t.half_stages / 4;
     t.y = a.dx;
     return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, ws, dg, du, a.N, pitch, a.device, stream);
+}
+
+// (the address of a module's variable: the same for a device as long as it lasts)
+cudaError_t ffn_error_word(int device, unsigned int** word) {
+    static std::atomic<unsigned int*> known[64] = {};
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    *word = known[device].load(std::memory_order_acquire);
+    if (*word != nullptr) return cudaSuccess;
+    void* at = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&at, g_ffn_error);
+    if (e != cudaSuccess) return e;
+    *word = static_cast<unsigned int*>(at);
+    known[device].store(*word, std::memory_order_release);
+    return cudaSuccess;
 }
 
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream) {

@@ -237,6 +237,8 @@ size_t lora_tc_workspace_bytes(const LoraArgs& a);
 void lora_tc_counts(const LoraArgs& a, void* workspace, unsigned int** counts, int* n_counts);
 cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, cudaStream_t stream);
 // Read and clear those kernels' device error word (synchronises `stream`).
+// Where the feed-forward kernels record a time-out on the current device.
+cudaError_t ffn_error_word(int device, unsigned int** word);
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream);
 
 }  // namespace q2k
