@@ -28,10 +28,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "q2k_device.cuh"
 #include "q2k_ffn.cuh"
 #include "q2k_internal.h"
+#include "q2k_tc.cuh"
 
 namespace q2k {
 
@@ -43,6 +45,7 @@ constexpr int kUnitRows = 16;         // rows of an MMA tile; a unit has two til
 // Row r of an item starts at word 21 r + 28 (r / 4): the eight rows and four
 // 16-byte slices that a warp reads together then fall on 32 different banks.
 constexpr int kItemBytes = 4 * 4 * 112;
+constexpr int kMaxRowParts = 8;       // (the largest portable cluster)
 constexpr int kMaxDepth = 8;          // units in flight of a streaming CTA
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int kGroupUnits = 8;        // units whose sums are kept when K takes several passes
@@ -401,7 +404,8 @@ struct RowsArgs {
     void* y;
     int R, n_adapters;
     // streamed tiles
-    int tile_rows, depth;  // rows of a tile; units in flight
+    int depth;            // units in flight
+    int parts;            // CTAs of a cluster that divide K
     unsigned int* err;
 };
 
@@ -679,12 +683,35 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode>, static_cast<const T*>(x), p);
 }
 
-// The same product where a CTA takes whole rows: a tile of 16 (or 8) rows is one
-// contiguous piece of the matrix, so one bulk copy fetches it, where 84-byte
-// columns take a word a lane (16 copy instructions for 16 rows x 256 weights,
-// which the load unit could not issue at more than 3.9 TB/s).  Warp w has blocks w,
-// w + 16, ..., and the warps' sums meet as above; the barrier there also says that
-// the unit's slot is free, so a thread that passes it refills the slot at once.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Two words into another CTA of the cluster, counted by a barrier there.
+__device__ __forceinline__ void send_pair(uint32_t addr, uint32_t bar, uint32_t rank, float a, float b) {
+    asm volatile(
+        "{\n\t.reg .u32 ra, rb;\n\tmapa.shared::cluster.u32 ra, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 rb, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [ra], {%3, %4}, [rb];\n\t}"
+        ::"r"(addr), "r"(bar), "r"(rank), "f"(a), "f"(b)
+        : "memory");
+}
+
+// The same product with a block for each warp.  A tile of 16 rows, or of a part of
+// each, comes by bulk copies, where 84-byte columns take a word a lane (16 copy
+// instructions for 16 rows x 256 weights, which the load unit could not issue at
+// more than 3.9 TB/s).  The warps' sums meet as above, but a unit late: a warp
+// multiplies unit u, then waits for the others' sums of u - 1 and brings its share
+// of them out, and only then writes its sums of u, so that two buffers of sums do
+// and no warp waits for the slowest at every unit.  That all have their sums of
+// u - 1 also says that the unit's slot is free to be refilled.
+// More than 16 blocks: a cluster's CTAs divide K (in fours of blocks, so that
+// copies start at 16 bytes).  Each has a share of a unit's outputs; the others send
+// it their sums of those, which it adds in the order of K another unit later.  A
+// CTA that sends for unit u has brought out u - 2, so its peers have sent theirs
+// for u - 2 and brought out u - 4: four buffers need no other bookkeeping.
 // NT = 0: one token, as integers (see XBytes).
 template <typename T, int NT, Rows kMode>
 __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restrict__ x, RowsArgs p) {
@@ -694,125 +721,183 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const int m0 = blockIdx.y * kTokens;
-    const int blocks = p.K / kQK, row_bytes = blocks * kBlockBytes;
-    const int tile_bytes = p.tile_rows * row_bytes;
+    const int rank = static_cast<int>(blockIdx.x) % p.parts, first_unit = static_cast<int>(blockIdx.x) / p.parts;
+    const int unit_step = static_cast<int>(gridDim.x) / p.parts;
+    const int blocks = p.K / kQK;
+    const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
+    // this CTA's blocks
+    const int b0 = p.parts == 1 ? 0 : 4 * (blocks / 4 * rank / p.parts);
+    const int nb = p.parts == 1 ? blocks : 4 * (blocks / 4 * (rank + 1) / p.parts) - b0;
+    const int pitch = nb * kBlockBytes, tile_bytes = kUnitRows * pitch;
+    const int slot_bytes = 2 * kUnitRows * min(blocks, kWarps) * kBlockBytes;
     float* red = reinterpret_cast<float*>(smem);
-    uint32_t* xs = reinterpret_cast<uint32_t*>(smem + kWarps * 2 * 2 * kOut * 4);
-    uint8_t* slots = reinterpret_cast<uint8_t*>(xs + (kBytes ? blocks * kXWords : 0));
-    const uint32_t bars = smem_u32(slots + static_cast<size_t>(p.depth) * 2 * tile_bytes);
+    // sums from the cluster's CTAs: [unit % 4][from][output of the share]
+    const int share = kOut / p.parts + 1;
+    float2* inbox = reinterpret_cast<float2*>(red + kWarps * 2 * 2 * kOut);
+    uint32_t* xs = reinterpret_cast<uint32_t*>(inbox + 4 * (kOut + kMaxRowParts));
+    uint8_t* slots = reinterpret_cast<uint8_t*>(xs + (kBytes ? kWarps * kXWords : 0));
+    const uint32_t bars = smem_u32(slots + static_cast<size_t>(p.depth) * slot_bytes);
+    const uint32_t bar_sums = bars + 8 * kMaxDepth, bar_inbox = bar_sums + 8;
     volatile int* abort_flag =
-        reinterpret_cast<volatile int*>(slots + static_cast<size_t>(p.depth) * 2 * tile_bytes + 8 * kMaxDepth);
-    const int my_units = (p.units - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+        reinterpret_cast<volatile int*>(slots + static_cast<size_t>(p.depth) * slot_bytes + 8 * (kMaxDepth + 5));
+    const int my_units = (p.units - 1 - first_unit) / unit_step + 1;
+    // by a whole warp
     auto issue = [&](int u) {
         if (u >= my_units) return;
-        const int unit = static_cast<int>(blockIdx.x) + u * static_cast<int>(gridDim.x);
-        uint8_t* slot = slots + static_cast<size_t>(u % p.depth) * 2 * tile_bytes;
+        const int unit = first_unit + u * unit_step;
+        uint8_t* slot = slots + static_cast<size_t>(u % p.depth) * slot_bytes;
         const uint32_t bar = bars + 8 * (u % p.depth);
-        const uint8_t* src[2];
-        uint32_t bytes[2];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const int row0 = unit * p.unit_step + (a ? p.tile1_row : 0);
-            const int valid = min(max(p.N - row0, 0), p.tile_rows);
-            src[a] = (a ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes;
-            bytes[a] = static_cast<uint32_t>(valid * row_bytes);
-            // (the matrix may end off 16 bytes)
-            for (uint32_t at = bytes[a] & ~15u; at < bytes[a]; at += 4)
-                *reinterpret_cast<uint32_t*>(slot + a * tile_bytes + at) =
-                    __ldg(reinterpret_cast<const uint32_t*>(src[a] + at));
+        const int tile = lane >> 4;
+        const int row0 = unit * p.unit_step + (tile ? p.tile1_row : 0);
+        const int valid = min(max(p.N - row0, 0), kUnitRows);
+        const uint8_t* src = (tile ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes;
+        uint8_t* dst = slot + tile * tile_bytes;
+        uint32_t bytes = static_cast<uint32_t>(valid * pitch);
+        if (p.parts == 1) {
+            // one copy a tile (the matrix may end off 16 bytes)
+            if ((lane & 15) == 0)
+                for (uint32_t at = bytes & ~15u; at < bytes; at += 4)
+                    *reinterpret_cast<uint32_t*>(dst + at) = __ldg(reinterpret_cast<const uint32_t*>(src + at));
+            bytes &= ~15u;
         }
-        mbar_arrive_expect_tx(bar, (bytes[0] & ~15u) + (bytes[1] & ~15u));
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-            if ((bytes[a] & ~15u) != 0)
-                bulk_copy_g2s(smem_u32(slot + a * tile_bytes), src[a], bytes[a] & ~15u, bar);
+        const uint32_t other = __shfl_sync(0xFFFFFFFFu, bytes, 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes + other);
+        __syncwarp();
+        if (p.parts == 1) {
+            if ((lane & 15) == 0 && bytes != 0) bulk_copy_g2s(smem_u32(dst), src, bytes, bar);
+        } else if ((lane & 15) < valid) {
+            bulk_copy_g2s(smem_u32(dst + (lane & 15) * pitch),
+                          src + (lane & 15) * row_bytes + static_cast<size_t>(b0) * kBlockBytes, pitch, bar);
+        }
     };
     pdl_allow_dependents();
     bool waited = false;
-    if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        for (int d = 0; d < p.depth; ++d) mbar_init(bars + 8 * d, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (warp == 0) {
+        if (lane == 0) {
+            *abort_flag = 0;
+            for (int d = 0; d < p.depth; ++d) mbar_init(bars + 8 * d, 1);
+            mbar_init(bar_sums, kWarps);
+            for (int d = 0; d < 4; ++d) mbar_init(bar_inbox + 8 * d, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
         if (!p.const_weights) {
             pdl_wait_prerequisites();
             waited = true;
         }
         for (int d = 0; d < p.depth; ++d) issue(d);
     }
-    if (!waited && !p.x_ready) pdl_wait_prerequisites();
-    waited = waited || !p.x_ready;
+    if (!waited && !p.x_ready) {
+        pdl_wait_prerequisites();
+        waited = true;
+    }
     XBytes xi;
     XBlock<T> xm[kBytes ? 1 : NT];
-    if constexpr (kBytes) {
-        for (int b = warp; b < blocks; b += kWarps) make_x_bytes(x, b, lane, xs + b * kXWords);
-        __syncwarp();
-        if (warp < blocks) take_x_bytes(xs + warp * kXWords, lane, xi);
-    } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (warp < blocks) load_x_block(x, p.K, warp, m0 + n * (kTokens / NT), p.M, lane, xm[n]);
-    }
-    __syncthreads();
-    for (int u = 0; u < my_units; ++u) {
-        const int unit = static_cast<int>(blockIdx.x) + u * static_cast<int>(gridDim.x);
-        const uint32_t slot = smem_u32(slots) + (u % p.depth) * 2 * tile_bytes;
-        mbar_wait_bounded(bars + 8 * (u % p.depth), (u / p.depth) & 1, abort_flag, p.err, kErrTimeoutFull);
-        float* mine = red + ((u & 1) * kWarps + warp) * (2 * kOut);
+    if (warp < nb) {
         if constexpr (kBytes) {
-            float acc[2][2] = {};
-            for (int b = warp; b < blocks; b += kWarps) {
-                if (blocks > kWarps) take_x_bytes(xs + b * kXWords, lane, xi);
-                const uint32_t row = slot + b * kBlockBytes + (lane >> 2) * row_bytes;
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (r == 0 || p.tile_rows > 8)
-                            acc[a][r] = fmaf(xi.undo,
-                                             slice_product(read_row(row + a * tile_bytes + 8 * r * row_bytes,
-                                                                    lane & 3), xi),
-                                             acc[a][r]);
-            }
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float v = acc[a][r];
-                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-                    if ((lane & 3) == 0) mine[a * kOut + 8 * r + (lane >> 2)] = v;
-                }
+            make_x_bytes(x, b0 + warp, lane, xs + warp * kXWords);
+            __syncwarp();
+            take_x_bytes(xs + warp * kXWords, lane, xi);
         } else {
-            float acc[2][NT][4] = {};
-            if (warp < blocks) {
-                const uint32_t row = slot + warp * kBlockBytes + (lane >> 2) * row_bytes;
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
-                    block_product<T, NT>(read_row(row + a * tile_bytes, lane & 3),
-                                         read_row(row + a * tile_bytes + 8 * row_bytes, lane & 3), xm,
-                                         acc[a]);
-            }
-            write_sums<T, NT>(mine, lane, acc);
+            for (int n = 0; n < NT; ++n)
+                load_x_block(x, p.K, b0 + warp, m0 + n * (kTokens / NT), p.M, lane, xm[n]);
         }
-        __syncthreads();
-        // the warps take turns to bring a unit out
-        const int turn = (warp + u) & (kWarps - 1);
-        if (turn == kWarps - 1 && lane == 0) issue(u + p.depth);
+    }
+    const int o_first = kOut * rank / p.parts, o_count = kOut * (rank + 1) / p.parts - o_first;
+    // the warps take turns at the outputs of a unit, and at refilling its slot
+    auto turn_at = [&](int u) { return (warp + u) & (kWarps - 1); };
+    // unit u: the warps' sums -> results, or to the CTAs that have them
+    auto bring_out = [&](int u) {
+        mbar_wait_bounded(bar_sums, u & 1, abort_flag, p.err, kErrTimeoutAccum);
+        if (turn_at(u) == kWarps - 1) issue(u + p.depth);
         if (kMode == Rows::kLora && !waited) {
             pdl_wait_prerequisites();  // t
             waited = true;
         }
         const float* all = red + (u & 1) * kWarps * (2 * kOut);
-        for (int o = 32 * turn + lane; o < kOut; o += 32 * kWarps) {
-            if (kBytes && o >= p.tile_rows) break;
+        for (int o = 32 * turn_at(u) + lane; o < kOut; o += 32 * kWarps) {
             float v[2] = {0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 v[0] += all[w * (2 * kOut) + o];
                 v[1] += all[w * (2 * kOut) + kOut + o];
             }
-            finish_row<T, NT, kMode>(p, o, v, unit, m0);
+            if (p.parts == 1) {
+                finish_row<T, NT, kMode>(p, o, v, first_unit + u * unit_step, m0);
+            } else {
+                const int to = ((o + 1) * p.parts - 1) / kOut;  // whose share o is
+                const int at = ((u & 3) * p.parts + rank) * share + o - kOut * to / p.parts;
+                send_pair(smem_u32(inbox + at), bar_inbox + 8 * (u & 3), to, v[0], v[1]);
+            }
         }
+    };
+    // unit u: the cluster's sums -> results
+    auto finish_parts = [&](int u) {
+        if (turn_at(u) == kWarps - 1 && lane == 0)
+            mbar_arrive_expect_tx(bar_inbox + 8 * (u & 3), 8 * p.parts * o_count);
+        if (32 * turn_at(u) >= o_count) return;
+        tc::wait_peer_bounded(bar_inbox + 8 * (u & 3), (u >> 2) & 1, abort_flag, p.err, kErrTimeoutFull);
+        for (int o = 32 * turn_at(u) + lane; o < o_count; o += 32 * kWarps) {
+            float v[2] = {0.f, 0.f};
+            for (int z = 0; z < p.parts; ++z) {
+                const float2 w = inbox[((u & 3) * p.parts + z) * share + o];
+                v[0] += w.x;
+                v[1] += w.y;
+            }
+            finish_row<T, NT, kMode>(p, o_first + o, v, first_unit + u * unit_step, m0);
+        }
+    };
+    __syncthreads();
+    if (p.parts > 1) {  // every CTA's barriers are there before anything is sent
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int u = 0; u < my_units; ++u) {
+        const uint32_t slot = smem_u32(slots) + (u % p.depth) * slot_bytes;
+        mbar_wait_bounded(bars + 8 * (u % p.depth), (u / p.depth) & 1, abort_flag, p.err, kErrTimeoutFull);
+        float* mine = red + ((u & 1) * kWarps + warp) * (2 * kOut);
+        const uint32_t row = slot + warp * kBlockBytes + (lane >> 2) * pitch;
+        // (one token: rows lane / 4 and 8 on of the two tiles)
+        float acc[2][kBytes ? 1 : NT][4] = {};
+        if (warp < nb) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const RowWords r0 = read_row(row + a * tile_bytes, lane & 3);
+                const RowWords r1 = read_row(row + a * tile_bytes + 8 * pitch, lane & 3);
+                if constexpr (kBytes) {
+                    acc[a][0][0] = xi.undo * slice_product(r0, xi);
+                    acc[a][0][1] = xi.undo * slice_product(r1, xi);
+                } else {
+                    block_product<T, NT>(r0, r1, xm, acc[a]);
+                }
+            }
+        }
+        if (u > 0) bring_out(u - 1);
+        if (p.parts > 1 && u > 1) finish_parts(u - 2);
+        if constexpr (kBytes) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float v = acc[a][0][r];
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+                    if ((lane & 3) == 0) mine[a * kOut + 8 * r + (lane >> 2)] = v;
+                }
+        } else {
+            write_sums<T, NT>(mine, lane, acc);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sums);
+    }
+    bring_out(my_units - 1);
+    if (p.parts > 1) {
+        if (my_units > 1) finish_parts(my_units - 2);
+        finish_parts(my_units - 1);
+        cluster_arrive();  // no CTA leaves while another may send to it
+        cluster_wait();
     }
     if (!waited) pdl_wait_prerequisites();
     if (*abort_flag) {
@@ -822,54 +907,58 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     }
 }
 
-// Shared memory beside the slots, and whether tiles can be streamed.
+// Whether the product can be streamed, and how.
 template <typename T, int NT>
 bool plan_stream(RowsArgs& p, size_t& smem) {
     const int blocks = p.K / kQK;
-    if (blocks <= kWarps / 2 || (NT != 0 && blocks > kWarps)) return false;
+    if (blocks <= kWarps / 2) return false;
     if (((reinterpret_cast<uintptr_t>(p.w0) | reinterpret_cast<uintptr_t>(p.w1)) & 15) != 0) return false;
-    const size_t fixed = kWarps * 2 * 2 * Pass<T, NT>::kSums * 4 +
-                         (NT == 0 ? static_cast<size_t>(blocks) * kXWords * 4 : 0) + 8 * kMaxDepth + 16;
-    // rows of 16, of which three units fit; else of eight
-    for (int rows = kUnitRows; rows >= (NT == 0 ? 8 : kUnitRows); rows -= 8) {
-        const size_t unit = 2 * static_cast<size_t>(rows) * blocks * kBlockBytes;
-        if (fixed + 2 * unit > kMaxSmem) continue;
-        p.depth = static_cast<int>(std::min<size_t>(kMaxDepth, (kMaxSmem - fixed) / unit));
-        if (rows > 8 && NT == 0 && p.depth < 3) continue;
-        p.unit_step = p.unit_step / kUnitRows * rows;
-        p.tile1_row = p.tile1_row / kUnitRows * rows;
-        p.tile_rows = rows;
-        p.units = (p.N + p.unit_step - 1) / p.unit_step;
-        smem = fixed + p.depth * unit;
-        return true;
-    }
-    return false;
+    p.parts = (blocks + kWarps - 1) / kWarps;
+    if (p.parts > 1 && (p.parts > kMaxRowParts || blocks % 4 != 0)) return false;
+    const size_t fixed = kWarps * 2 * 2 * Pass<T, NT>::kSums * 4 + 4 * (Pass<T, NT>::kSums + kMaxRowParts) * 8 +
+                         (NT == 0 ? static_cast<size_t>(kWarps) * kXWords * 4 : 0) + 8 * (kMaxDepth + 5) + 16;
+    const size_t unit = 2 * static_cast<size_t>(kUnitRows) * std::min(blocks, kWarps) * kBlockBytes;
+    p.depth = static_cast<int>(std::min<size_t>(kMaxDepth, (kMaxSmem - fixed) / unit));
+    smem = fixed + p.depth * unit;
+    return true;
 }
 
 template <typename T, int NT, Rows kMode>
 cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, int sm_count,
                           cudaStream_t stream) {
-    static bool attr_done[64] = {};
+    // clusters of a size that the GPU holds at once, 0: not known yet
+    static std::atomic<int> resident[64][kMaxRowParts + 1] = {};
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    if (!attr_done[device]) {
-        const cudaError_t e = cudaFuncSetAttribute(stream_kernel<T, NT, kMode>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxSmem);
-        if (e != cudaSuccess) return e;
-        attr_done[device] = true;
-    }
     cudaError_t e = ffn_error_word(device, &p.err);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::min(sm_count, p.units), (p.M + Pass<T, NT>::kTokens - 1) / Pass<T, NT>::kTokens);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.parts > 1 ? 2 : 1;
+    int most = resident[device][p.parts].load(std::memory_order_acquire);
+    if (most == 0) {
+        e = cudaFuncSetAttribute(stream_kernel<T, NT, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxSmem);
+        if (e != cudaSuccess) return e;
+        most = sm_count;
+        if (p.parts > 1) {
+            cfg.gridDim = dim3(sm_count / p.parts * p.parts);
+            e = cudaOccupancyMaxActiveClusters(&most, stream_kernel<T, NT, kMode>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        most = std::max(1, most);
+        resident[device][p.parts].store(most, std::memory_order_release);
+    }
+    cfg.gridDim = dim3(std::min(most, p.units) * p.parts,
+                       (p.M + Pass<T, NT>::kTokens - 1) / Pass<T, NT>::kTokens);
     return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode>, static_cast<const T*>(x), p);
 }
 
