@@ -1248,10 +1248,14 @@ Plan make_plan(int M, int rows, int tile_rows, int quads) {
             cost = static_cast<double>(quads) / p.parts + 1;
         } else {
             // whole tiles only, or what is left after full rounds of them cut
-            // evenly (a quad for every worker at least)
+            // evenly (a quad for every worker at least).  Bringing the runs' sums
+            // together costs as long as 15 quads or so beyond what the whole tiles
+            // behind it hide (14336 x 4096, 16 quads a tile: 256 tokens, 1.5 rounds,
+            // 55 us whole and 87 cut; 128 tokens 43 and 54.  Backwards, 112 quads a
+            // tile: 2048 tokens, 1.7 rounds, 384 and 353).
             const long left = static_cast<long>(p.tiles - rounds * most) * quads;
             const double uncut = static_cast<double>(quads) * ((p.tiles + most - 1) / most);
-            const double cut = static_cast<double>(p.tiles) * quads / most + 1;
+            const double cut = static_cast<double>(p.tiles) * quads / most + 15;
             const bool cuts = left >= most && cut < uncut;
             if (cuts) p.whole = rounds * most;
             cost = cuts ? cut : uncut;
