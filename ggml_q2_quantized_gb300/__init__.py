@@ -16,6 +16,7 @@ Names follow the mlx-native page "tests/deepseek_q2_k.rs": ``matmul`` is
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 import threading
@@ -765,6 +766,29 @@ def _ffn_call(dev, fn, *args):
         _check(_lib, status)
 
 
+_quick_mod = None
+
+
+def _quick():
+    """The compiled module for ordinary calls (q2k_torch), or False without it."""
+    global _quick_mod
+    if _quick_mod is None:
+        lib, torch = load(), _torch()
+        path = _build.torch_module_path(torch.__version__)
+        if not os.path.exists(path):
+            _quick_mod = False
+            return False
+        spec = importlib.util.spec_from_file_location("q2k_torch", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+            "q2k_gated_ffn", "q2k_gated_ffn_workspace_bytes", "q2k_gated_ffn_backward",
+            "q2k_gated_ffn_backward_workspace_bytes", "q2k_matmul_lora",
+            "q2k_matmul_lora_workspace_bytes")))
+        _quick_mod = mod
+    return _quick_mod
+
+
 def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None, path="auto",
               const_weights: bool = False, workspace="auto"):
     """The gated feed-forward block ``h = act(x Wg^T) * (x Wu^T)``: both
@@ -777,6 +801,14 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     ``workspace`` as in ``matmul``: up to 16 bf16 or 8 f32 tokens the weights
     are exact, above that x and W are rounded to bf16 for the tensor cores.
     """
+    if out is None and workspace.__class__ is str:
+        quick = _quick_mod or _quick()
+        done = (quick.gated(x, w_gate, w_up, n, act, save, path, const_weights)
+                if quick else None)
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     torch = _torch_mod or _torch()
     _need_activations(x, "x")
     if x.dim() != 2:
@@ -808,6 +840,13 @@ def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace
     projections); returns ``(dx, dgate, dup)``: ``dx = dgate Wg + dup Wu``
     ``[m, k]`` and the gradients ``[m, n]`` of the two projections.
     """
+    if workspace.__class__ is str:
+        quick = _quick_mod or _quick()
+        done = quick.backward(dh, gate, up, w_gate, w_up, k, act) if quick else None
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     torch = _torch_mod or _torch()
     bf16, u8 = torch.bfloat16, torch.uint8
     _need_activations(dh, "dh", bf16)
@@ -844,6 +883,14 @@ def matmul_lora(x, w, n: int, lora_a, lora_b, ids, scales=None, out=None, path="
     ``(out, bad_id_count)`` without waiting (such a token's row is zero).
     ``path``, ``const_weights`` and ``workspace`` as in ``gated_ffn``.
     """
+    if out is None and workspace.__class__ is str:
+        quick = _quick_mod or _quick()
+        done = (quick.lora(x, w, n, lora_a, lora_b, ids, scales, path, const_weights)
+                if quick else None)
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return _lora_result(*done, lora_a.shape[0], check)
     torch = _torch_mod or _torch()
     _need_activations(x, "x")
     if x.dim() != 2:
@@ -874,6 +921,10 @@ def matmul_lora(x, w, n: int, lora_a, lora_b, ids, scales=None, out=None, path="
               lora_a.numel(), lora_b.data_ptr(), lora_b.numel(),
               scales.data_ptr() if scales is not None else None, ids.data_ptr(), out.data_ptr(),
               m * n, params, bad.data_ptr(), ws, ws_bytes)
+    return _lora_result(out, bad, n_adapters, check)
+
+
+def _lora_result(out, bad, n_adapters, check):
     if not check:
         return out, bad
     n_bad = int(bad.item())

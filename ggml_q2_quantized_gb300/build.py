@@ -1,8 +1,10 @@
-"""Build libq2k.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Build libq2k.so in-tree with nvcc for sm_103a (no cmake).
 
 Each ``csrc/*.cu`` compiles to an object in parallel; the objects link into
 ``_build/libq2k.so`` with the CUDA runtime linked statically, so the library
-needs only the NVIDIA driver at run time.  ``python -m
+needs only the NVIDIA driver at run time.  Where PyTorch is installed, g++ builds
+the module through which its tensors reach the feed-forward calls
+(``csrc/q2k_torch.cpp``; one file for each PyTorch version).  ``python -m
 ggml_q2_quantized_gb300.build`` does the same from the command line.
 """
 
@@ -10,10 +12,12 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -63,8 +67,53 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, res.stderr
 
 
+def torch_module_path(version: str) -> str:
+    """Where the module for a PyTorch version lies."""
+    return os.path.join(BUILD_DIR, f"q2k_torch-{version}.so")
+
+
+def build_torch_module(force: bool = False) -> str | None:
+    """Compile q2k_torch for the installed PyTorch if its sources changed; return its
+    path, or None without PyTorch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    import torch
+
+    src = os.path.join(CSRC, "q2k_torch.cpp")
+    path = torch_module_path(torch.__version__)
+    deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(path) and all(
+            os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libq2k.so if any source changed; return its path."""
+    """Compile and link libq2k.so, and the module for PyTorch where that is
+    installed, if any source changed; return the library's path."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(build_torch_module, force)
+        path = _build_library(force, verbose_ptxas)
+        module.result()
+    return path
+
+
+def _build_library(force: bool, verbose_ptxas: bool) -> str:
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)

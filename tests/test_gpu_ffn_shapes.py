@@ -94,3 +94,59 @@ def test_repeats_at_size(m, n, k):
     first = run()
     for _ in range(40):
         assert all(torch.equal(p, q) for p, q in zip(first, run()))
+
+
+@pytest.mark.parametrize("m", [1, 16, 40])
+def test_explicit_buffers_give_the_same_bits(m):
+    """The compiled module's way and the one with the caller's own buffers."""
+    assert q2k._quick()
+    n, k, r, na = 96, 1024, 16, 3
+    rng = np.random.default_rng([25, m])
+    w, xt, x, at, a, bt, b, s = lora_inputs(rng, "bf16", m, n, k, r, na)
+    wd, w2 = dev(w), dev(blocks(rng, n, k))
+    ids, sd = dev(rng.integers(-1, na, m).astype(np.int32)), dev(s)
+    dh, _ = activations(rng, m, n, torch.bfloat16)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda:0")
+    h = q2k.gated_ffn(xt, wd, w2, n, act="gelu")
+    out = torch.empty_like(h)
+    assert q2k.gated_ffn(xt, wd, w2, n, act="gelu", out=out, workspace=ws) is out
+    assert torch.equal(h, out)
+    h, g, u = q2k.gated_ffn(xt, wd, w2, n, save=True)
+    for p, q in zip((h, g, u), q2k.gated_ffn(xt, wd, w2, n, save=True, workspace=ws)):
+        assert torch.equal(p, q)
+    for p, q in zip(q2k.gated_ffn_backward(dh, g, u, wd, w2, k),
+                    q2k.gated_ffn_backward(dh, g, u, wd, w2, k, workspace=ws)):
+        assert torch.equal(p, q)
+    y = q2k.matmul_lora(xt, wd, n, at, bt, ids, scales=sd)
+    assert torch.equal(y, q2k.matmul_lora(xt, wd, n, at, bt, ids, scales=sd, out=out, workspace=ws))
+
+
+def test_refusals_with_device_tensors():
+    """What the compiled module does not take is refused by name."""
+    n, k = 32, 512
+    rng = np.random.default_rng(26)
+    w = dev(blocks(rng, n, k))
+    x, _ = activations(rng, 4, k, torch.bfloat16)
+    with pytest.raises(ValueError, match="contiguous"):
+        q2k.gated_ffn(activations(rng, 4, 2 * k, torch.bfloat16)[0][:, ::2], w, w, n)
+    with pytest.raises(TypeError, match="w_up"):
+        q2k.gated_ffn(x, w, w.float(), n)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        q2k.gated_ffn(x.half(), w, w, n)
+    with pytest.raises(q2k.InvalidArgument):
+        q2k.gated_ffn(x, w, w[:-84], n)
+    with pytest.raises(q2k.InvalidArgument):
+        q2k.gated_ffn(x[:0], w, w, n)
+    with pytest.raises(KeyError):
+        q2k.gated_ffn(x, w, w, n, act="relu")
+    with pytest.raises(ValueError, match="gate"):
+        q2k.gated_ffn_backward(x[:, :n].contiguous(), x, x, w, w, k)
+    a, b = torch.zeros(2, 16, k, device="cuda:0").bfloat16(), torch.zeros(2, n, 16, device="cuda:0").bfloat16()
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda:0")
+    for bad in (ids.long(), ids[:3], ids.cpu()):
+        with pytest.raises((TypeError, ValueError), match="ids"):
+            q2k.matmul_lora(x, w, n, a, b, bad)
+    with pytest.raises(ValueError, match="lora_b"):
+        q2k.matmul_lora(x, w, n, a, b[:, :-1].contiguous(), ids)
+    with pytest.raises(ValueError, match="scales"):
+        q2k.matmul_lora(x, w, n, a, b, ids, scales=torch.ones(3, device="cuda:0"))
