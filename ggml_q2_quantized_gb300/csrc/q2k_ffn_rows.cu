@@ -462,34 +462,47 @@ __device__ __forceinline__ void finish_row(const RowsArgs& p, int o, float (&v)[
         }
     } else {
         const int id = p.ids[m];
-        const bool has = id >= 0 && id < p.n_adapters;
+        if (id >= 0 && id < p.n_adapters) {
+            // sixteen of the rank at a time, both rows': one trip to memory
+            const uint4* br[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                br[a] = reinterpret_cast<const uint4*>(
+                    p.b + (static_cast<size_t>(id) * p.N + min(n + a * p.tile1_row, p.N - 1)) * p.R);
+            const float4* tr = reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m) * p.R);
+            for (int c = 0; c < p.R / 8; c += 2) {
+                const bool two = c + 1 < p.R / 8;
+                uint4 bv[2][2];
+                float4 tv[4];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    bv[a][0] = __ldg(br[a] + c);
+                    bv[a][1] = two ? __ldg(br[a] + c + 1) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    tv[q] = q < 2 || two ? tr[2 * c + q] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t bw[4] = {bv[a][h].x, bv[a][h].y, bv[a][h].z, bv[a][h].w};
+                        const float4 t0 = tv[2 * h], t1 = tv[2 * h + 1];
+                        const float tt[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            v[a] = fmaf(__uint_as_float(bw[q] << 16), tt[2 * q], v[a]);
+                            v[a] = fmaf(__uint_as_float(bw[q] & 0xFFFF0000u), tt[2 * q + 1], v[a]);
+                        }
+                    }
+            }
+        } else if (id != -1) {
+            v[0] = v[1] = 0.f;  // an id out of range: a zero row
+        }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
             const int na = n + a * p.tile1_row;
-            if (na >= p.N) continue;
-            if (has) {
-                const uint4* br = reinterpret_cast<const uint4*>(
-                    p.b + (static_cast<size_t>(id) * p.N + na) * p.R);
-                const float4* tr = reinterpret_cast<const float4*>(
-                    p.t + static_cast<size_t>(m) * p.R);
-                for (int c = 0; c < p.R / 8; ++c) {
-                    const uint4 bv = __ldg(br + c);
-                    const float4 t0 = tr[2 * c], t1 = tr[2 * c + 1];
-                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-                    const float tv[8] = {t0.x, t0.y, t0.z, t0.w,
-                                         t1.x, t1.y, t1.z, t1.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[a] = fmaf(__uint_as_float(bw[q] << 16), tv[2 * q], v[a]);
-                        v[a] = fmaf(__uint_as_float(bw[q] & 0xFFFF0000u),
-                                    tv[2 * q + 1], v[a]);
-                    }
-                }
-            } else if (id != -1) {
-                v[a] = 0.f;  // an id out of range: a zero row
-            }
-            static_cast<T*>(p.y)[static_cast<size_t>(m) * p.N + na] =
-                from_float<T>(v[a]);
+            if (na < p.N) static_cast<T*>(p.y)[static_cast<size_t>(m) * p.N + na] = from_float<T>(v[a]);
         }
     }
 }
