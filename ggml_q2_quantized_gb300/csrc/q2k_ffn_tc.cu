@@ -141,19 +141,20 @@ struct Cfg {
     static constexpr int kOffA = kStages * kXStage;
     static constexpr int kOffRaw = kOffA + (kTmemA ? 0 : kStages * kABytes);
     static constexpr int kOffSums = kOffRaw + kRaw * kRawBytes;
-    // with adapters: 64 t and an id for each token of the chunk
+    // with adapters: 64 t for each token of a chunk; an id and whose for each of
+    // the tile
     static constexpr int kOffT = kOffSums + kChunk * kSumPitch * 4;
     static constexpr int kOffIds = kOffT + (kMode == Tc::kLora ? kChunk * 64 * 4 : 0);
     // bars: x_full, a_full, peer_full, empty [kStages], raw_full, raw_empty
     //       [kRaw], acc_full, acc_empty [2], drain
     static constexpr int kNumBars = 4 * kStages + 2 * kRaw + 5;
-    static constexpr int kOffBar = (kOffIds + (kMode == Tc::kLora ? kChunk * 4 : 0) + 7) & ~7;
+    static constexpr int kOffBar = (kOffIds + (kMode == Tc::kLora ? kX * 8 : 0) + 7) & ~7;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0 && kOffSums % 16 == 0, "alignment");
     // the last tile's sums, t and ids for all its tokens, take the rings' place
-    static_assert(kX * (kSumPitch + (kMode == Tc::kLora ? 65 : 0)) * 4 <= kOffBar, "epilogue");
+    static_assert(kX * (kSumPitch + (kMode == Tc::kLora ? 64 : 0)) * 4 <= kOffIds, "epilogue");
 };
 
 struct TcArgs {
@@ -218,27 +219,91 @@ struct Team {
     }
 };
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// The ids of a tile's tokens [lo, hi) (multiples of eight; -1 none or past `tokens`,
+// -2 out of range), and whose each is, sorted by id within every `scope` of them
+// (those without an adapter last): what add_adapters takes at a time then has few
+// adapters in a group of eight (512 tokens of four adapters in any order, rank 64:
+// 154 us in the order they came).  A token counts those before it.  For four warps,
+// while the tile is multiplied.
+template <int kX>
+__device__ __forceinline__ void sort_tokens(int* id_buf, int* order, const TcArgs& p, int m, int tokens,
+                                            int lo, int hi, int scope, int et) {
+    constexpr int kEach = (kX + 127) / 128;
+    int id[kEach], at[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int c = lo + et + 128 * u;
+        id[u] = -1;
+        if (c < min(tokens, hi)) {
+            id[u] = p.ids[m + c];
+            if (id[u] < -1 || id[u] >= p.n_adapters) id[u] = -2;
+        }
+        if (c < hi) order[c] = id[u];
+    }
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+    // (already in order: whole requests one after another)
+    uint32_t back = 0;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int c = lo + et + 128 * u;
+        at[u] = c;
+        if (c > lo && c < hi) back |= static_cast<uint32_t>(order[c - 1]) > static_cast<uint32_t>(id[u]);
+    }
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+        "bar.red.or.pred p, 2, 128, p;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "+r"(back)::"memory");
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int c = lo + et + 128 * u;
+        if (c >= hi || back == 0) break;
+        const int first = lo + (c - lo) / scope * scope, end = min(first + scope, hi);
+        const uint32_t key = static_cast<uint32_t>(id[u]);
+        at[u] = first;
+#pragma unroll 1
+        for (int j = first; j < end; j += 4) {
+            const uint4 k = *reinterpret_cast<const uint4*>(order + j);
+            at[u] += (k.x < key || (k.x == key && j < c)) + (k.y < key || (k.y == key && j + 1 < c)) +
+                     (k.z < key || (k.z == key && j + 2 < c)) + (k.w < key || (k.w == key && j + 3 < c));
+        }
+    }
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int c = lo + et + 128 * u;
+        if (c >= hi) break;
+        id_buf[at[u]] = id[u];
+        order[at[u]] = c;
+    }
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+
 // Adds s_a B_a t of each token's adapter to the sums of `count` tokens from m on:
 // per 16 rows and eight tokens, one product (m16n8k16) for each adapter that
 // occurs among them, B_a as stored and t split into two bf16 (16 bits); a token's
-// sum takes only its own adapter's product.  t comes through shared memory 64
+// sum takes only its own adapter's product.  Slot c is the token order[c] of `sums`
+// and of m.  t comes through shared memory 64
 // values a token at a time, already split: the two bf16 of value pair j (hi, lo)
-// of token c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
+// of slot c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
 // reads together fall on different banks.  A warp has 16 rows at a time, and keeps
 // B_a's fragments in registers from one token group to the next with the same
 // adapter.  These products bound it: one takes 32 clocks of a quarter SM, 17000
 // clocks for 128 rows x 256 tokens at rank 64.
-__device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* id_buf,
-                                             const TcArgs& p, int n0, int m, int count,
+__device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const int* id_buf,
+                                             const int* order, const TcArgs& p, int n0, int m, int count,
                                              const Team& team) {
     const int et = team.thread, lane = et & 31;
     const int g = lane >> 2, t = lane & 3;
     const int slots = (count + 7) & ~7;
-    // ids: -1 none, -2 out of range (a zero row)
-    for (int c = et; c < slots; c += team.threads) {
-        const int id = c < count ? p.ids[m + c] : -1;
-        id_buf[c] = id < -1 || id >= p.n_adapters ? -2 : id;
-    }
     for (int r0 = 0; r0 < p.R; r0 += 64) {
         const int width = min(64, p.R - r0);  // a multiple of 8
         for (int base = et; base < 16 * slots; base += 4 * team.threads) {
@@ -247,8 +312,8 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* i
             for (int u = 0; u < 4; ++u) {
                 const int i = base + team.threads * u, r = 4 * (i & 15);
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if ((i >> 4) < count && r < width)
-                    v[u] = *reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m + (i >> 4)) * p.R + r0 + r);
+                if ((i >> 4) < slots && r < width && id_buf[i >> 4] >= 0)
+                    v[u] = *reinterpret_cast<const float4*>(p.t + static_cast<size_t>(m + order[i >> 4]) * p.R + r0 + r);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -268,6 +333,7 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* i
         // row tile % 8 of warp % 8; the team's other warps take other tokens
         const int warp = et >> 5, warps = team.threads >> 5;
         const int sets = max(1, warps >> 3);
+        const uint32_t sums_at = smem_u32(sums) + 4 * g;
 #pragma unroll 1
         for (int rt = warp & 7; rt < 8 && (warp >> 3) < sets; rt += min(warps, 8)) {
             const int n = n0 + 16 * rt + g;  // this lane's rows: n, n + 8
@@ -278,10 +344,18 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* i
                 const int id = id_buf[c0 + g];
                 // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
                 const int id0 = id_buf[c0 + 2 * t], id1 = id_buf[c0 + 2 * t + 1];
-                float* s0 = sums + (c0 + 2 * t) * kSumPitch + 16 * rt + g;
-                float* s1 = s0 + kSumPitch;
-                if (id0 == -2) s0[0] = s0[8] = 0.f;
-                if (id1 == -2) s1[0] = s1[8] = 0.f;
+                const int2 tokens = *reinterpret_cast<const int2*>(order + c0 + 2 * t);
+                // (shared addresses: half the registers of pointers)
+                const uint32_t s0 = sums_at + 4 * (tokens.x * kSumPitch + 16 * rt);
+                const uint32_t s1 = sums_at + 4 * (tokens.y * kSumPitch + 16 * rt);
+                if (id0 == -2) {
+                    st_shared_f32(s0, 0.f);
+                    st_shared_f32(s0 + 32, 0.f);
+                }
+                if (id1 == -2) {
+                    st_shared_f32(s1, 0.f);
+                    st_shared_f32(s1 + 32, 0.f);
+                }
                 unsigned todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
                 while (todo != 0) {
                     const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
@@ -321,12 +395,12 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, int* i
 #pragma unroll
                     for (int c = 0; c < 4; ++c) d[c] = (e[0][c] + e[1][c]) + (e[2][c] + e[3][c]);
                     if (id0 == ad) {
-                        s0[0] += d[0];
-                        s0[8] += d[2];
+                        st_shared_f32(s0, ld_shared_f32(s0) + d[0]);
+                        st_shared_f32(s0 + 32, ld_shared_f32(s0 + 32) + d[2]);
                     }
                     if (id1 == ad) {
-                        s1[0] += d[1];
-                        s1[8] += d[3];
+                        st_shared_f32(s1, ld_shared_f32(s1) + d[1]);
+                        st_shared_f32(s1 + 32, ld_shared_f32(s1 + 32) + d[3]);
                     }
                 }
             }
@@ -917,13 +991,15 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     }
     // Results of `count` tokens (from m on) of a tile from their sums; the last
     // tile's (`final`) lie where the rings were, from token slot `slot` on.
-    auto bring_out = [&](float* base, bool final, int n0, int m, int count, const Team& team, int slot = 0) {
+    auto bring_out = [&](float* base, bool final, int n0, int m, int count, const Team& team, int slot = 0,
+                         int slot0 = 0) {
         if constexpr (kMode == Tc::kLora) {
             uint32_t* tbuf = reinterpret_cast<uint32_t*>(final ? base + kX * kSumPitch
                                                                : reinterpret_cast<float*>(smem + C::kOffT));
-            int* id_buf = reinterpret_cast<int*>(final ? tbuf + 64 * kX
-                                                       : reinterpret_cast<uint32_t*>(smem + C::kOffIds));
-            add_adapters(base + slot * kSumPitch, tbuf, id_buf, p, n0, m + slot, count, team);
+            const int* id_buf = reinterpret_cast<const int*>(smem + C::kOffIds);
+            // (base holds the sums of the tile's tokens from slot0 on)
+            add_adapters(base - slot0 * kSumPitch, tbuf, id_buf + slot0 + slot, id_buf + kX + slot0 + slot,
+                         p, n0, m - slot0, count, team);
         }
         emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
     };
@@ -942,6 +1018,16 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                                            : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
             team.threads = final ? 128 + kDecThreads : 128;
             team.barrier = final ? 7 : 2;
+            if constexpr (kMode == Tc::kLora) {
+                if (warp >= kEpiWarp0) {
+                    const int m0 = token0(sg.tile), tokens = min(kX, p.M - m0);
+                    int* id_buf = reinterpret_cast<int*>(smem + C::kOffIds);
+                    // (of parts of K, each has a share of the tokens)
+                    const int groups = (tokens + 7) / 8;
+                    sort_tokens<kX>(id_buf, id_buf + kX, p, m0, tokens, 8 * (work.part * groups / p.parts),
+                                    8 * ((work.part + 1) * groups / p.parts), final ? kX : kChunk, team.thread);
+                }
+            }
             mbar_wait_backoff(bar_accfull + 8 * (index & 1), (index >> 1) & 1, abort_flag, err,
                               kErrTimeoutAccum, 512);
             // all of the team go on, or none (after a time-out they still meet
@@ -1054,7 +1140,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     }
                 }
                 team.sync();
-                bring_out(sums, final, n0, m0 + c0, count, team);
+                bring_out(sums, final, n0, m0 + c0, count, team, 0, c0);
                 team.sync();
             }
             if (final && p.parts > 1 && sg.run < 0) {
