@@ -79,10 +79,14 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
+# what the measured workloads' kernels are compiled from
+TRAFFIC_SOURCES = ("q2k_device.cuh", "q2k_gemm_tc.cu", "q2k_gemv.cu")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "ggml_q2_quantized_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in TRAFFIC_SOURCES:
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]

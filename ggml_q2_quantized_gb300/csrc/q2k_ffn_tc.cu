@@ -20,7 +20,7 @@
 // decodes a weight row as above (one table serves 16 codes) and stores it as
 // stored, k running, which is the MMA's A operand "MN-major": the transposition
 // costs nothing.  (Transposing the codes first, so that a lane could write its
-// own column to tensor memory, took 2200 warp instructions a stage against 680.)
+// own column to tensor memory, took more instructions than the stores it saved.)
 //
 // Work split, K in blocks (backward: in 256 weight rows):
 // - fewer tiles than half of the workers (CTAs, or pairs, that the GPU holds): a
@@ -31,11 +31,14 @@
 //   end together.  The runs come first: their sums go to the workspace, the CTA
 //   that finishes last adds them, in the order of K whoever that is, and all of
 //   that happens while whole tiles are multiplied.  No CTA waits for another.
-//   (2048 tokens backwards: 256 tiles for 152 CTAs, 302 us against 356 in two
-//   rounds.  Cutting without whole tiles behind it exposes 14 us of adding.)
+//   (2048 tokens backwards, 14336 x 4096: 128 tiles for 76 pairs, 353 us against
+//   384 in two rounds.  Cutting without whole tiles behind it exposes the adding.)
 //
-// What bounds it: at 256 tokens a tile the MMAs (740 clocks per stage as measured,
-// of 630 for a plain bf16 matrix product at the measured peak); below, the decode.
+// What bounds it: at 256 tokens a tile the MMAs and the shared memory that feeds
+// them (per stage and SM 32 KB of operands read, 32 KB written: 512 of about 740
+// clocks at 128 bytes a clock; 0.38 us a stage of 64 K, where a plain bf16 product
+// at the measured peak takes 0.34); below, the decode (0.33 us a stage at 128
+// tokens).
 //
 // Every wait is bounded (about a second); on time-out the kernel records a bit
 // in the device error word, drains its MMAs, frees TMEM and returns.
@@ -112,7 +115,8 @@ enum class Tc { kGated, kLora, kBackward };
 // 128 and fewer: the decode bounds, and narrow MMAs that read A from shared
 // memory take as long as wide ones (100 clocks each, measured), so decoded
 // weights go to tensor memory (not backward, where they would have to be
-// transposed).  (14336 x 4096, 64 tokens: 55 us with A in shared memory.)
+// transposed).  (14336 x 4096, 64 tokens: 52 us against
+// 55 with A in shared memory; 40 since one elected thread issues the MMAs.)
 template <int kX, bool kTma, Tc kMode>
 struct Cfg {
     static constexpr bool kBack = kMode == Tc::kBackward;
@@ -296,7 +300,7 @@ __device__ __forceinline__ void sort_tokens(int* id_buf, int* order, const TcArg
 // of slot c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
 // reads together fall on different banks.  A warp has 16 rows at a time, and keeps
 // B_a's fragments in registers from one token group to the next with the same
-// adapter.  These products bound it: one takes 32 clocks of a quarter SM, 17000
+// adapter.  A product takes 16 clocks of a quarter SM, 8200
 // clocks for 128 rows x 256 tokens at rank 64.
 __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const int* id_buf,
                                              const int* order, const TcArgs& p, int n0, int m, int count,

@@ -524,9 +524,10 @@ int q2k_abi_version(void);
  * give the same bits.
  *
  * Paths (Q2K_PATH_AUTO picks by m):
- *   Q2K_PATH_GEMV    every weight exact; x exact when bf16, else to 22 bits
- *                    relative to each element; products summed in f32, so the
- *                    error is a few f32 roundings of sum_k |x| (dl q + ml).
+ *   Q2K_PATH_GEMV    every weight exact, x to 2^-22 of the largest |x| of its block
+ *                    of 256 or better; products summed in integers or f32.  The
+ *                    error is within 1e-5 * sum_k |x| (dl q + ml).  Auto takes it
+ *                    for m <= 16 (bf16) or 8 (f32).
  *   Q2K_PATH_TENSOR  x and W rounded to bf16 (error within 8e-3 * sum_k |x w|,
  *                    as q2k_matmul's tensor path). */
 typedef enum q2k_dtype { Q2K_DTYPE_F32 = 0, Q2K_DTYPE_BF16 = 1 } q2k_dtype;
@@ -574,8 +575,9 @@ size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params *
  *   dx            [m, k]; fully overwritten
  *   dgate, dup    [m, n] each, both or neither NULL (e.g. for the gradients of
  *                 adapters on the two projections)
- * The workspace holds dgate and dup as the product reads them; with both given
- * and n a multiple of 8 it is not needed (NULL). */
+ * The workspace holds dgate and dup as the product reads them, unless both are
+ * given and n is a multiple of 8, and the partial sums of tiles that several
+ * CTAs share. */
 q2k_status q2k_gated_ffn_backward(const void *dh, const void *gate, const void *up,
                                   size_t h_elems, const void *w_gate, size_t w_gate_bytes,
                                   const void *w_up, size_t w_up_bytes, void *dx, size_t dx_elems,
