@@ -71,8 +71,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows) {
-    const uint64_t row_bytes = static_cast<uint64_t>(K / kQK) * kBlockBytes;
+bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group) {
+    const uint64_t row_bytes = static_cast<uint64_t>(K / kQK) * kBlockBytes * group;
+    N /= group;
+    if (N == 0) return false;
     if (row_bytes % 16 != 0 || (reinterpret_cast<uintptr_t>(w) & 15) != 0) return false;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return false;
@@ -139,9 +141,10 @@ struct Cfg {
     // raw slots: a block column of 128 weight rows, or (backward) of 64 for a
     // stage, without TMA only the 11 words of the half block that it needs
     static constexpr int kRawRows = kBack ? kStageK : kRows;
-    static constexpr int kRawPitch = kTma ? kBoxBytes : kBack ? 44 : kBlockBytes;
-    static constexpr int kRawBytes = kRawRows * kRawPitch;
-    static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : kTmemA ? 4 : (kTma ? 2 : 3);
+    static constexpr int kRawPitch = kTma || !kBack ? kBoxBytes : 44;
+    // (forward without TMA maps of single rows: rows that no map covers beside them)
+    static constexpr int kRawBytes = (kRawRows + (kTma || kBack ? 0 : 8)) * kRawPitch;
+    static constexpr int kRaw = kBack ? (kTma ? 4 : 8) : kTmemA ? 4 : 2;
     static constexpr int kOffA = kStages * kXStage;
     static constexpr int kOffRaw = kOffA + (kTmemA ? 0 : kStages * kABytes);
     static constexpr int kOffSums = kOffRaw + kRaw * kRawBytes;
@@ -165,6 +168,7 @@ struct TcArgs {
     const uint8_t* xa;   // bf16 image of the tokens, or null: they come by the token maps
     const uint8_t* w0;   // Wg, or W
     const uint8_t* w1;   // Wu
+    int groups;          // fours of weight rows that the maps cover, 0: none
     int M, N, K;         // N, K: the weight matrices' rows and columns
     int quads;           // the product's K in blocks (backward: 256 weight rows)
     int half_stages;     // backward: 64-row stages of Wg
@@ -189,28 +193,18 @@ struct TcArgs {
 };
 
 struct TcMaps {
-    CUtensorMap w0, w1;  // weights, 112-byte boxes of 64 or 128 rows
+    // weights, 112-byte boxes of 64 or 128 rows (or of every fourth of those rows,
+    // where only four rows together are a multiple of 16 bytes)
+    CUtensorMap w0, w1;
     CUtensorMap x0, x1;  // tokens, boxes of kX rows x 64 (backward: dg and du)
 };
 
-// Block b of the tile's 128 rows (row r < split0 from w0, the others from w1)
-// into a raw slab; rows past N are zero-filled (they decode to 0).
-__device__ __forceinline__ void issue_raw(const uint8_t* w0, const uint8_t* w1, int split0,
-                                          uint32_t dst, int n0, int N, size_t row_bytes, int b,
-                                          int td) {
-#pragma unroll 3
-    for (int f = td; f < kRows * kWordsPerBlock; f += kDecThreads) {
-        const int r = f / kWordsPerBlock;
-        const int wd = f - r * kWordsPerBlock;
-        const int n = n0 + (r < split0 ? r : r - split0);
-        const bool ok = n < N;
-        const uint8_t* src = (r < split0 ? w0 : w1) +
-                             (ok ? static_cast<size_t>(n) * row_bytes +
-                                       static_cast<size_t>(b) * kBlockBytes + 4 * wd
-                                 : 0);
-        cp_async_4(dst + r * kBlockBytes + 4 * wd, src, ok ? 4u : 0u);
-    }
-    cp_async_commit();
+// Where row r of a tile lies in a raw slot whose rows came four to a group: rows of
+// one place in their group together; `word`: a row that no group covers, behind them.
+template <int kSplit0>
+__device__ __forceinline__ int raw_place(int r, bool word) {
+    const int half = r / kSplit0, rr = r % kSplit0;
+    return word ? kRows + 4 * half + (rr & 3) : kSplit0 * half + kSplit0 / 4 * (rr & 3) + (rr >> 2);
 }
 
 // The threads that bring a tile's sums out: the epilogue's four warps while the
@@ -625,7 +619,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             mbar_init(bar_empty + 8 * s, 1);  // MMA commits
         }
         for (int r = lane; r < C::kRaw; r += 32) {
-            mbar_init(bar_raw + 8 * r, kTma ? 1 : kDecWarps);
+            mbar_init(bar_raw + 8 * r, kTma || !kBack ? 1 : kDecWarps);
             mbar_init(bar_rawempty + 8 * r, kBack ? C::kGroupWarps : kDecWarps);
         }
         if (lane < 2) {
@@ -644,6 +638,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     else __syncthreads();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const uint32_t raw0 = sbase + C::kOffRaw;
     auto hand_over = [&]() {  // the waiter and the issuer
         asm volatile("bar.sync 1, 64;" ::: "memory");
     };
@@ -651,8 +646,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     if (warp < kDecWarps) {
         // ---------------- weight decoders ----------------
         const int td = threadIdx.x;
-        const uint32_t raw0 = sbase + C::kOffRaw;
-        if (!kTma && !p.const_weights) pdl_wait_prerequisites();
+        if (!kTma && kBack && !p.const_weights) pdl_wait_prerequisites();
         // wait for stage i's place, counted over all segments
         auto stage_free = [&](int i) -> bool {
             return i < S || __all_sync(0xFFFFFFFFu,
@@ -754,45 +748,25 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             // group (four warps) takes stage `own` of every block, thread = a
             // weight row: shifts 2 (own % 2) and + 1 of half own / 2, both segments
             const int row = 32 * (warp & 3) + lane, own = warp >> 2;
-            const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
-            // without TMA: the next block to fetch (kRaw - 1 ahead of the decode)
-            Segment fetch = {};
-            int fetch_index = 0, fetch_q = 0, fetched = 0;
-            bool more = false;
-            [[maybe_unused]] auto fetch_next = [&]() {
-                if (more) {
-                    issue_raw(p.w0, p.w1, kSplit0, raw0 + (fetched % C::kRaw) * C::kRawBytes,
-                              row0(fetch.tile), p.N, row_bytes, fetch_q, td);
-                    ++fetched;
-                    if (++fetch_q == fetch.q1) {
-                        more = work.segment(++fetch_index, fetch);
-                        fetch_q = fetch.q0;
-                    }
-                } else {
-                    cp_async_commit();
-                }
-            };
-            if constexpr (!kTma) {
-                more = work.segment(0, fetch);
-                fetch_q = fetch.q0;
-                for (int r = 0; r < C::kRaw - 1; ++r) fetch_next();
-            }
             bool ok = true;
             int b = 0;  // blocks, counted over all segments
             for (int index = 0; ok && work.segment(index, sg); ++index) {
+                // (without maps of single rows: the row's place in a slot, and where
+                // in its group it starts, -1 if it comes by the word)
+                [[maybe_unused]] int place = row, row_at = 0;
+                if constexpr (!kTma) {
+                    const bool word = row0(sg.tile) + row % kSplit0 >= 4 * p.groups;
+                    place = raw_place<kSplit0>(row, word && p.groups > 0);
+                    row_at = word ? -1 : (row & 3) * (p.K / kQK) * kBlockBytes;
+                }
                 for (int q = sg.q0; q < sg.q1 && ok; ++q, ++b) {
                     const int buf = b % C::kRaw;
-                    uint32_t mine = raw0 + buf * C::kRawBytes + row * C::kRawPitch;
-                    if constexpr (!kTma) {
-                        cp_async_wait<C::kRaw - 2>();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_raw + 8 * buf);
-                    }
+                    uint32_t mine = raw0 + buf * C::kRawBytes + place * C::kRawPitch;
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_raw + 8 * buf, (b / C::kRaw) & 1,
                                                                    abort_flag, err, kErrTimeoutEmpty));
                     if (!ok) break;
-                    if constexpr (kTma) mine += 4 * (q & 3);  // the box starts at a 16-byte boundary
-                    else fetch_next();  // every decoder has read block b - 1: its slot is free
+                    // (what was copied starts at a 16-byte boundary)
+                    mine += kTma ? 4 * (q & 3) : row_at < 0 ? 0 : (row_at + kBlockBytes * q) & 15;
                     const int half = own >> 1;
                     const uint32_t sc = ld_shared_u32(mine + 8 * half + 4 * (own & 1));
                     uint32_t qw[2][4];
@@ -813,7 +787,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         decode_segment<1>(qw[0], (sc >> 16) & 0xFFu, d, dmin, o[2]);
                         decode_segment<1>(qw[1], sc >> 24, d, dmin, o[3]);
                     }
-                    if constexpr (kTma) raw_read(bar_rawempty + 8 * buf);
+                    raw_read(bar_rawempty + 8 * buf);
                     const int i = 4 * b + own;
                     ok = stage_free(i);
                     if (!ok) break;
@@ -840,7 +814,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                 }
             }
         }
-        if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (!kTma && kBack) asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kMmaWarp && peer == 0) {
         // ---------------- MMA issuer ----------------
         // It meets the waiter at named barrier 1 once for every two stages, when
@@ -946,6 +920,63 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         tma_load_2d(dst, &maps.w0, x, n0, bar);
                         if (kMode == Tc::kGated)
                             tma_load_2d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, bar);
+                    }
+                }
+            }
+            if (*abort_flag) linger();
+        }
+        if constexpr (!kTma && !kBack) {
+            // Rows that do not all start at 16 bytes: every fourth row does, so a map
+            // of groups of four rows serves each row of the group by a copy of its
+            // own, and the matrix's last rows (or all, off 16 bytes) come by the
+            // word.  (The decoders' own 4-byte copies kept them in step: 4999 x 2816,
+            // 77 tokens, 22.4 us; a bulk copy for each row's block 42.)
+            if (lane == 0 && p.groups > 0) {
+                tma_prefetch_map(&maps.w0);
+                if (kMode != Tc::kLora) tma_prefetch_map(&maps.w1);
+            }
+            if (!p.const_weights) pdl_wait_prerequisites();
+            const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
+            int b = 0;
+            bool ok = true;
+            for (int index = 0; ok && work.segment(index, sg); ++index) {
+                const int n0 = row0(sg.tile);
+                const bool words = n0 + kSplit0 > 4 * p.groups;
+                for (int q = sg.q0; ok && q < sg.q1; ++q, ++b) {
+                    const int buf = b % C::kRaw;
+                    ok = b < C::kRaw ||
+                         __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_rawempty + 8 * buf,
+                                                                   ((b / C::kRaw) - 1) & 1, abort_flag, err,
+                                                                   kErrTimeoutEmpty));
+                    if (!ok) break;
+                    const uint32_t bar = bar_raw + 8 * buf, slot = raw0 + buf * C::kRawBytes;
+                    if (words) {
+                        for (int r = lane; r < kRows; r += 32) {
+                            const int n = n0 + r % kSplit0;
+                            if (n < 4 * p.groups || n >= p.N) continue;
+                            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                                (r < kSplit0 ? p.w0 : p.w1) + n * row_bytes + static_cast<size_t>(kBlockBytes) * q);
+                            const uint32_t dst = slot + raw_place<kSplit0>(r, p.groups > 0) * C::kRawPitch;
+                            uint32_t v[kWordsPerBlock];
+#pragma unroll
+                            for (int w = 0; w < kWordsPerBlock; ++w) v[w] = __ldg(src + w);
+#pragma unroll
+                            for (int w = 0; w < kWordsPerBlock; ++w)
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + 4 * w), "r"(v[w]) : "memory");
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0 && p.groups == 0) mbar_arrive(bar);
+                    if (lane == 0 && p.groups > 0) {
+                        mbar_arrive_expect_tx(bar, kRows * kBoxBytes);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int x = static_cast<int>((j * row_bytes + kBlockBytes * q) & ~size_t(15));
+                            tma_load_2d(slot + j * (kSplit0 / 4) * kBoxBytes, &maps.w0, x, n0 / 4, bar);
+                            if (kMode == Tc::kGated)
+                                tma_load_2d(slot + (kSplit0 + j * (kSplit0 / 4)) * kBoxBytes, &maps.w1, x,
+                                            n0 / 4, bar);
+                        }
                     }
                 }
             }
@@ -1425,8 +1456,12 @@ cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void
     alignas(64) TcMaps maps;
     memset(&maps, 0, sizeof maps);
     const int rows = kMode == Tc::kLora ? kRows : 64;
-    const bool tma = make_weight_map(&maps.w0, a.w0, a.N, a.K, rows) &&
-                     (kMode == Tc::kLora || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows));
+    auto make_maps = [&](int group) {
+        return make_weight_map(&maps.w0, a.w0, a.N, a.K, rows / group, group) &&
+               (kMode == Tc::kLora || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows / group, group));
+    };
+    const bool tma = make_maps(1);
+    a.groups = !tma && kMode != Tc::kBackward && make_maps(4) ? a.N / 4 : 0;
     const int held = std::min(plan.x_rows, 128);  // tokens of a stage in one CTA
     if (a.xa == nullptr &&
         (!make_token_map(&maps.x0, x0, a.M, x_cols, x_pitch, held) ||

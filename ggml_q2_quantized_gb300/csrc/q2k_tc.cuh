@@ -256,7 +256,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Raw Q2_K weights as a 2-D byte tensor (N rows of K/256 * 84 bytes) with a box
 // of `rows` rows x 112 bytes; false unless rows are multiples of 16 bytes (K a
 // multiple of 1024) and the base is 16-byte aligned.
-bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows);
+// (of `group` rows together as one of the map's; false if those do not start at 16 bytes)
+bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group);
 
 }  // namespace tc
 }  // namespace q2k
