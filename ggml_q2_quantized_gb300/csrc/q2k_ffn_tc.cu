@@ -647,6 +647,10 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         // ---------------- weight decoders ----------------
         const int td = threadIdx.x;
         if (!kTma && kBack && !p.const_weights) pdl_wait_prerequisites();
+        // Raw rows 112 bytes apart fall on eight banks: every other eight lanes take
+        // the halves of a segment's 16 bytes in the other order, and store them
+        // accordingly (where the store has an address of the lane's own).
+        const int turn = kTma && !C::kTmemA ? (lane >> 3) & 1 : 0;
         // wait for stage i's place, counted over all segments
         auto stage_free = [&](int i) -> bool {
             return i < S || __all_sync(0xFFFFFFFFu,
@@ -718,7 +722,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     if (!ok) continue;
                     uint32_t qw[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) qw[e] = ld_shared_u32(at_q + 16 * seg + 4 * e);
+                    for (int e = 0; e < 4; ++e)
+                        qw[e] = ld_shared_u32(at_q + 16 * seg + 4 * (e & 1) + 8 * ((e >> 1) ^ turn));
                     const uint32_t sc0 = ld_shared_u32(at_sc) >> (8 * seg);
                     const uint32_t sc1 = ld_shared_u32(at_sc + 4) >> (8 * seg);
                     const uint32_t dd = ld_shared_u32(at_d);
@@ -739,7 +744,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             st_shared_v4(dst + 8192 * (j >> 1) +
-                                             (((4 * (j & 1) + 2 * seg + c) ^ (n & 7)) << 4),
+                                             (((4 * (j & 1) + 2 * seg + c) ^ (n & 7) ^ turn) << 4),
                                          o[j][4 * c], o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
                     publish(i);
                 }
@@ -772,7 +777,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     uint32_t qw[2][4];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        qw[e >> 2][e & 3] = ld_shared_u32(mine + 16 + 32 * half + 4 * e);
+                        qw[e >> 2][e & 3] = ld_shared_u32(mine + 16 + 32 * half + 16 * (e >> 2) + 4 * (e & 1) +
+                                                          8 * (((e >> 1) & 1) ^ turn));
                     const uint32_t dd = ld_shared_u32(mine + 80);
                     const float d = f16_bits_to_float(dd), dmin = f16_bits_to_float(dd >> 16);
                     uint32_t o[4][8];  // (shift, segment)
@@ -807,7 +813,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
-                                st_shared_v4(dst + sw128_offset(row, 2 * j + c), o[j][4 * c],
+                                st_shared_v4(dst + 128 * row + (((2 * j + c) ^ (row & 7) ^ turn) << 4), o[j][4 * c],
                                              o[j][4 * c + 1], o[j][4 * c + 2], o[j][4 * c + 3]);
                         publish(i);
                     }
