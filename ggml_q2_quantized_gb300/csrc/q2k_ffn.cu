@@ -223,16 +223,21 @@ cudaError_t launch_shrink(const LoraArgs& a, float* t, unsigned int* counts, int
         lora_shrink_kernel<T, 1, 1><<<dim3(a.M, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
             x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
     else {
-        // two clusters for 32 tokens' adapters while all run at once (256 tokens of
-        // 16 adapters in any order, 7168 wide: 95 us with one and 79 with two; many
-        // tokens' empty clusters cost: 2048, rank 128, 446 and 453)
-        const unsigned windows = (a.M + 31) / 32;
+        // windows of 32 tokens; f32 takes 16, its three parts of x more registers
+        // (512 tokens, 7168 x 7168, rank 64: 118 us with 32, 98 with 16).  Two
+        // clusters share a window's adapters while all run at once (256 tokens of 16
+        // adapters in any order, 7168 wide: 95 us with one and 79 with two; many
+        // tokens' empty clusters cost: 2048, rank 128, 446 and 453).
+        constexpr int kGroups = sizeof(T) == 4 ? 2 : 4;
+        const unsigned windows = (a.M + 8 * kGroups - 1) / (8 * kGroups);
         if (windows * rows * kShrinkCtas <= static_cast<unsigned>(a.sm_count))
-            lora_shrink_kernel<T, 4, 2><<<dim3(2 * windows, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
-                x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
+            lora_shrink_kernel<T, kGroups, 2>
+                <<<dim3(2 * windows, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
+                    x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
         else
-            lora_shrink_kernel<T, 4, 1><<<dim3(windows, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
-                x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
+            lora_shrink_kernel<T, kGroups, 1>
+                <<<dim3(windows, rows, kShrinkCtas), kShrinkWarps * 32, 0, stream>>>(
+                    x, a.a, a.scales, a.ids, t, a.bad_ids, a.M, a.K, a.R, a.n_adapters, counts, n_counts);
     }
     return cudaGetLastError();
 }
