@@ -159,7 +159,9 @@ struct Cfg {
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
-    static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0 && kOffSums % 16 == 0, "alignment");
+    static_assert(kOffA % 1024 == 0 && kOffRaw % 1024 == 0 && kOffSums % 16 == 0 && kOffT % 64 == 0 &&
+                      kSumPitch * 32 * 4 % 64 == 0,
+                  "alignment");
     // the last tile's sums, t and ids for all its tokens, take the rings' place
     static_assert(kX * (kSumPitch + (kMode == Tc::kLora ? 64 : 0)) * 4 <= kOffIds, "epilogue");
 };
@@ -220,6 +222,11 @@ struct Team {
 __device__ __forceinline__ float ld_shared_f32(uint32_t at) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_pair(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
     return v;
 }
 __device__ __forceinline__ void st_shared_f32(uint32_t at, float v) {
@@ -331,7 +338,12 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const 
         // row tile % 8 of warp % 8; the team's other warps take other tokens
         const int warp = et >> 5, warps = team.threads >> 5;
         const int sets = max(1, warps >> 3);
+        // (shared addresses: half the registers of pointers)
         const uint32_t sums_at = smem_u32(sums) + 4 * g;
+        const uint32_t ids_at = smem_u32(id_buf), order_at = smem_u32(order);
+        // this lane's pair of step q and of the eight values on, word (16 q + 2 t) ^
+        // 8 (g % 4) and that ^ 8
+        const uint32_t t_at = smem_u32(tbuf) + 256 * g + 8 * t + 32 * (g & 1), t_swap = 64 * ((g >> 1) & 1);
 #pragma unroll 1
         for (int rt = warp & 7; rt < 8 && (warp >> 3) < sets; rt += min(warps, 8)) {
             const int n = n0 + 16 * rt + g;  // this lane's rows: n, n + 8
@@ -339,13 +351,14 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const 
             uint32_t b[4][4];
 #pragma unroll 1
             for (int c0 = 8 * (warp >> 3); c0 < slots; c0 += 8 * sets) {
-                const int id = id_buf[c0 + g];
-                // the ids of the columns 2 t, 2 t + 1 whose sums this lane holds
-                const int id0 = id_buf[c0 + 2 * t], id1 = id_buf[c0 + 2 * t + 1];
-                const int2 tokens = *reinterpret_cast<const int2*>(order + c0 + 2 * t);
-                // (shared addresses: half the registers of pointers)
+                const int id = static_cast<int>(ld_shared_u32(ids_at + 4 * (c0 + g)));
+                // the ids and tokens of the columns 2 t, 2 t + 1 whose sums this lane holds
+                const uint2 ids2 = ld_shared_pair(ids_at + 4 * (c0 + 2 * t));
+                const uint2 tokens = ld_shared_pair(order_at + 4 * (c0 + 2 * t));
+                const int id0 = static_cast<int>(ids2.x), id1 = static_cast<int>(ids2.y);
                 const uint32_t s0 = sums_at + 4 * (tokens.x * kSumPitch + 16 * rt);
                 const uint32_t s1 = sums_at + 4 * (tokens.y * kSumPitch + 16 * rt);
+                const uint32_t t_row = t_at + 256 * c0;
                 if (id0 == -2) {
                     st_shared_f32(s0, 0.f);
                     st_shared_f32(s0 + 32, 0.f);
@@ -379,10 +392,9 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const 
                     for (int q = 0; q < 4; ++q) {
                         uint2 u = make_uint2(0u, 0u), w = u;
                         if (id == ad && 16 * q < width) {
-                            const uint32_t* tr = tbuf + 64 * (c0 + g);
-                            const int x = 8 * (g & 3);
-                            u = *reinterpret_cast<const uint2*>(tr + ((16 * q + 2 * t) ^ x));
-                            w = *reinterpret_cast<const uint2*>(tr + ((16 * q + 8 + 2 * t) ^ x));
+                            const uint32_t at = (q & 1 ? t_row - t_swap : t_row + t_swap) + 64 * q;
+                            u = ld_shared_pair(at);
+                            w = ld_shared_pair(at ^ 32u);
                         }
                         if (16 * q < width) {
                             mma_bf16_16816(e[q], b[q][0], b[q][1], b[q][2], b[q][3], u.x, w.x);
