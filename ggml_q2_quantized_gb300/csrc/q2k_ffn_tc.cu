@@ -3,9 +3,9 @@
 // adapters.
 //
 // A CTA computes 128 rows of a product x up to 256 tokens: 16 warps decode Q2_K
-// blocks into shared memory (the MMA's A operand), token stages of 64 K arrive by
-// TMA in the 128-byte-swizzled layout that the MMA reads (the B operand; f32
-// tokens come from a bf16 image that a prepass writes in that layout), and f32
+// blocks into shared or tensor memory (the MMA's A operand), token stages of 64 K
+// arrive by TMA in the 128-byte-swizzled layout that the MMA reads (the B operand;
+// f32 tokens come from a bf16 image that a prepass writes in that layout), and f32
 // sums build up in tensor memory, in two sets: four warps bring one tile's sums
 // out while the next tile is multiplied into the other (gated, 512 tokens x 14336
 // x 4096: a tile's set-up and epilogue took 8 of its 33 us before).
@@ -296,13 +296,13 @@ __device__ __forceinline__ void sort_tokens(int* id_buf, int* order, const TcArg
 // per 16 rows and eight tokens, one product (m16n8k16) for each adapter that
 // occurs among them, B_a as stored and t split into two bf16 (16 bits); a token's
 // sum takes only its own adapter's product.  Slot c is the token order[c] of `sums`
-// and of m.  t comes through shared memory 64
-// values a token at a time, already split: the two bf16 of value pair j (hi, lo)
-// of slot c at words 64 c + (2 j ^ 8 (c % 4)), so that the eight tokens a warp
-// reads together fall on different banks.  A warp has 16 rows at a time, and keeps
-// B_a's fragments in registers from one token group to the next with the same
-// adapter.  A product takes 16 clocks of a quarter SM, 8200
-// clocks for 128 rows x 256 tokens at rank 64.
+// and of m.  t comes through shared memory 64 values a token at a time, already
+// split: the two bf16 of value pair j (hi, lo) of slot c at words 64 c + (2 j ^
+// 8 (c % 4)), so that the eight tokens a warp reads together fall on different
+// banks.  A warp has 16 rows at a time, and keeps B_a's fragments in registers from
+// one token group to the next with the same adapter.  128 rows x 256 tokens at rank
+// 64 take about 10 us: 3 of products, 3 of B's rows, the rest instructions around
+// them (by pointers instead of shared addresses, with spills, 15).
 __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const int* id_buf,
                                              const int* order, const TcArgs& p, int n0, int m, int count,
                                              const Team& team) {

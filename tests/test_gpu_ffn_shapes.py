@@ -58,9 +58,12 @@ def test_lora_few_tokens(dtype, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(20, 12000, 512), (100, 11000, 256), (200, 10100, 512),
-                                   (400, 9000, 256), (70, 300, 4096), (256, 130, 6144)])
+                                   (400, 9000, 256), (70, 300, 4096), (256, 130, 6144),
+                                   (20, 3, 768), (40, 6, 1280), (33, 129, 2816), (300, 515, 2816),
+                                   (150, 10103, 768)])
 def test_gated_many_tokens(m, n, k):
-    """More tiles than workers, whole and cut, and few tiles in parts of K."""
+    """More tiles than workers, whole and cut, few tiles in parts of K, and rows that
+    start off 16 bytes with one to three past the last four."""
     rng = np.random.default_rng([23, m, n, k])
     wg, wu = blocks(rng, n, k), blocks(rng, n, k)
     xt, x = activations(rng, m, k, torch.bfloat16)
