@@ -674,10 +674,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_afull + 8 * (i % S));
         };
-        // This warp is done with a raw slot: called when the words read from it
-        // have been used, since loads still on their way when the slot is given
-        // back were seen to bring the next block's bytes.
+        // This warp is done with a raw slot.  Its words are read in the generic proxy
+        // and overwritten in the async proxy (the next block's copy), so each lane
+        // orders its reads before the copy by a proxy fence: the barrier alone does
+        // not, and without it loads still on their way were seen to bring the next
+        // block's bytes.
         [[maybe_unused]] auto raw_read = [&](uint32_t bar) {
+            fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
