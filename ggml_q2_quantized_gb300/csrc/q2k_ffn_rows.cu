@@ -298,12 +298,13 @@ __device__ __forceinline__ void make_x_bytes(const T* x, int block, int lane, ui
             v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
         }
     }
-    float top = 0.f;
+    // the largest |x|, as bits: those of a NaN are above an infinity's (fmaxf would
+    // drop it, and its bits pass for an integer below)
+    uint32_t top = 0;
 #pragma unroll
-    for (int l = 0; l < 8; ++l) top = fmaxf(top, fabsf(v[l]));
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+    for (int l = 0; l < 8; ++l) top = max(top, __float_as_uint(v[l]) & 0x7FFFFFFFu);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const int e = max(static_cast<int>(top >> 23) - 127, -100);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 21 - e) << 23);
     // (e = 128: an infinity or NaN in x makes every sum of the block NaN)
     if (lane == 0)
