@@ -17,8 +17,9 @@
 // matrices of 14336 x 4096 take (16.5 us with up to 8 tokens; HBM alone would take 5.7).
 //
 // A single token has its products in integers instead, four weights an
-// instruction (dp4a): 13.3 us, 8.4 of them by the arithmetic (4.6 TB/s of weights
-// for longer matrices).
+// instruction (dp4a): 13.5 us, 8.4 of them by the arithmetic (4.6 TB/s of weights
+// for longer matrices).  Its x is rounded to 22 bits beside its block's largest
+// (XBytes below), coarser than the two f16 parts.
 //
 // x goes to f16 per (token, block), scaled by a power of two so that the
 // block's largest |x| lies in [2^10, 2^11): a bf16 x is then exact down to 2^-27
@@ -268,19 +269,83 @@ __device__ __forceinline__ void block_product(const RowWords& a, const RowWords&
 
 // One block of one token as integers, for the slice t of each row that a lane has:
 // x 2^(21 - e), e the exponent of the block's largest |x|, rounded to 22 bits and
-// sign (exact for a bf16 x down to 2^-14 of the largest), its three bytes in a word
-// each for four weights that lie in one quant word at one shift; and the bytes of
-// the group sums X_g of the slice's four shifts.  The last byte is signed.
+// sign, its three digits in a word each for four weights that lie in one quant word
+// at one shift; and the digits of the group sums X_g of the slice's four shifts.
+// Digits are signed bytes, so that a small x has small digits and its products lose
+// nothing beside a large one's.  The rounding is 2^-22 of the largest |x| (none for
+// a bf16 x down to 2^-14 of it).  A block most of whose values matter little beside
+// its largest would lose much of those: where more than a quarter of them are below
+// 2^-9 of it, what the rounding left goes through the same products as 22 bits more
+// (the block is `wide`; of 20 000 blocks of normal values none is, nor of silu(g) u
+// with g and u of deviation 1 or 1.5, and one in 40 at 4).  14336 x 4096: 13.5 us
+// without such blocks, 4 us more with one of the 16, 13 with all.  The products stand in a loop of their own: written beside
+// the ordinary ones they cost those 1 us.
 struct XBytes {
-    uint32_t x[4][3][4];  // shift, byte, quant word
+    uint32_t x[4][3][4];  // shift, digit, quant word
     uint32_t s[4];
-    float undo;
+    __device__ __forceinline__ uint4 quad(int j, int d) const {
+        return make_uint4(x[j][d][0], x[j][d][1], x[j][d][2], x[j][d][3]);
+    }
+    __device__ __forceinline__ uint4 sums() const { return make_uint4(s[0], s[1], s[2], s[3]); }
 };
-constexpr int kXWords = 4 * (3 * 16 + 4) + 4;  // a block's, in shared memory (the last: undo)
+constexpr int kXWords = 4 * (3 * 16 + 4);  // a block's, in shared memory
+constexpr float kRest = 0x1p-22f;          // a unit of the rest, in units of x
+// The same, left in shared memory.
+struct StoredXBytes {
+    const uint4* at;
+    __device__ __forceinline__ uint4 quad(int j, int d) const { return at[3 * j + d]; }
+    __device__ __forceinline__ uint4 sums() const { return at[12]; }
+};
 
+// Eight values as integers w, the rest (in units of kRest) in `rest`.
+__device__ __forceinline__ void split_integers(const float (&v)[8], float scale, uint32_t (&w)[8],
+                                               float (&rest)[8]) {
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        // 1.5 2^23 + an integer of at most 2^21 or 2^22: its low bits are that
+        // integer's; v times a power of two and the difference are exact
+        const float u = v[l] * scale, big = u + 12582912.f;
+        w[l] = __float_as_uint(big) - 0x4B400000u;
+        rest[l] = u - (big - 12582912.f);
+    }
+}
+
+// A lane's integers (eight weights of slice t at shift g / 2, words 2 (g % 2) ..)
+// into the block's words in shared memory.
+__device__ __forceinline__ void store_digits(const uint32_t (&n)[8], int lane, uint32_t* buf) {
+    const int g = lane >> 2, t = lane & 3, j = g >> 1, half = g & 1;
+    uint32_t w[8];
+    int sum = 0;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        sum += static_cast<int>(n[l]);
+        w[l] = (n[l] + 0x00808080u) ^ 0x00808080u;  // signed digits
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t* a = w + 4 * q;
+        const uint32_t p01 = __byte_perm(a[0], a[1], 0x5140u), p23 = __byte_perm(a[2], a[3], 0x5140u);
+        const uint32_t h01 = __byte_perm(a[0], a[1], 0x0062u), h23 = __byte_perm(a[2], a[3], 0x0062u);
+        uint32_t* to = buf + 52 * t + 12 * j + 2 * half + q;
+        to[0] = __byte_perm(p01, p23, 0x5410u);
+        to[4] = __byte_perm(p01, p23, 0x7632u);
+        to[8] = __byte_perm(h01, h23, 0x5410u);
+    }
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+    // byte g / 2 of the four sum words is this shift's
+    if (half == 0) {
+        const uint32_t u = (static_cast<uint32_t>(sum) + 0x80808080u) ^ 0x80808080u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            reinterpret_cast<uint8_t*>(buf + 52 * t + 48 + d)[j] = static_cast<uint8_t>(u >> (8 * d));
+    }
+}
+
+// Block `block` of a token: its integers in registers, and the value of their unit in
+// `undo`.  True if the block is wide: the rest is then in `buf`.
 template <typename T>
-__device__ __forceinline__ void make_x_bytes(const T* x, int block, int lane, uint32_t* buf) {
-    // this lane's part: eight weights of slice t at shift g / 2, words 2 (g % 2) ..
+__device__ __forceinline__ bool load_x_bytes(const T* x, int block, int lane, uint32_t* buf, XBytes& o,
+                                             float& undo) {
     const int g = lane >> 2, t = lane & 3, j = g >> 1, half = g & 1;
     const T* p = x + 256 * block + 128 * (t >> 1) + 32 * j + 16 * (t & 1) + 8 * half;
     float v[8];
@@ -305,54 +370,38 @@ __device__ __forceinline__ void make_x_bytes(const T* x, int block, int lane, ui
     for (int l = 0; l < 8; ++l) top = max(top, __float_as_uint(v[l]) & 0x7FFFFFFFu);
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     const int e = max(static_cast<int>(top >> 23) - 127, -100);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 21 - e) << 23);
     // (e = 128: an infinity or NaN in x makes every sum of the block NaN)
-    if (lane == 0)
-        buf[kXWords - 1] = e > 127 ? 0x7FC00000u : static_cast<uint32_t>(127 - 21 + e) << 23;
-    uint32_t w[8];
-    int sum = 0;
+    undo = __uint_as_float(e > 127 ? 0x7FC00000u : static_cast<uint32_t>(127 - 21 + e) << 23);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 21 - e) << 23);
+    uint32_t w[8], small = 0;
+    float rest[8], none[8];
+    split_integers(v, up, w, rest);
+    bool left = false;
 #pragma unroll
     for (int l = 0; l < 8; ++l) {
-        // 1.5 2^23 + an integer of less than 2^22: its low bits are that integer's
-        w[l] = __float_as_uint(fmaf(v[l], up, 12582912.f)) - 0x4B400000u;
-        sum += static_cast<int>(w[l]);
+        small += v[l] != 0.f && (__float_as_uint(v[l]) & 0x7FFFFFFFu) < static_cast<uint32_t>(127 - 9 + e) << 23;
+        left |= rest[l] != 0.f;
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const uint32_t* a = w + 4 * q;
-        const uint32_t p01 = __byte_perm(a[0], a[1], 0x5140u), p23 = __byte_perm(a[2], a[3], 0x5140u);
-        const uint32_t h01 = __byte_perm(a[0], a[1], 0x0062u), h23 = __byte_perm(a[2], a[3], 0x0062u);
-        uint32_t* to = buf + 52 * t + 12 * j + 2 * half + q;
-        to[0] = __byte_perm(p01, p23, 0x5410u);
-        to[4] = __byte_perm(p01, p23, 0x7632u);
-        to[8] = __byte_perm(h01, h23, 0x5410u);
-    }
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
-    // byte g / 2 of the four sum words is this shift's
-    if (half == 0) {
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-            reinterpret_cast<uint8_t*>(buf + 52 * t + 48 + d)[j] = static_cast<uint8_t>(sum >> (8 * d));
-    }
-}
-
-__device__ __forceinline__ void take_x_bytes(const uint32_t* buf, int lane, XBytes& o) {
-    const uint4* from = reinterpret_cast<const uint4*>(buf + 52 * (lane & 3));
+    store_digits(w, lane, buf);
+    __syncwarp();
+    const uint4* from = reinterpret_cast<const uint4*>(buf + 52 * t);
 #pragma unroll
     for (int c = 0; c < 13; ++c) {
         const uint4 u = from[c];
         uint32_t* to = c < 12 ? o.x[c / 3][c % 3] : o.s;
         to[0] = u.x, to[1] = u.y, to[2] = u.z, to[3] = u.w;
     }
-    o.undo = __uint_as_float(buf[kXWords - 1]);
+    const bool wide = __reduce_add_sync(0xFFFFFFFFu, small) > kQK / 4 && __any_sync(0xFFFFFFFFu, left);
+    if (wide) {
+        split_integers(rest, 1 / kRest, w, none);
+        __syncwarp();
+        store_digits(w, lane, buf);
+        __syncwarp();
+    }
+    return wide;
 }
 
-// c + the four products of a's unsigned bytes with b's unsigned or signed ones.
-__device__ __forceinline__ int dot4_uu(uint32_t a, uint32_t b, int c) {
-    uint32_t d;
-    asm("dp4a.u32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(static_cast<uint32_t>(c)));
-    return static_cast<int>(d);
-}
+// c + the four products of a's unsigned bytes with b's signed ones.
 __device__ __forceinline__ int dot4_us(uint32_t a, uint32_t b, int c) {
     int d;
     asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -360,21 +409,25 @@ __device__ __forceinline__ int dot4_us(uint32_t a, uint32_t b, int c) {
 }
 
 // One row's slice of a block times one token, all in integers: codes are masked in
-// place (4^j q) and meet sc_j 4^(3 - j), so every product carries 64; a byte's sum
-// over a slice is below 2^26.
-__device__ __forceinline__ float slice_product(const RowWords& r, const XBytes& x) {
+// place (4^j q) and meet sc_j 4^(3 - j), so every product carries 64; a digit's sum
+// over a slice is below 2^25.
+template <typename X>
+__device__ __forceinline__ float slice_product(const RowWords& r, const X& x) {
     int a0 = 0, a1 = 0, a2 = 0;
     const int sc[4] = {static_cast<int>((r.sc << 6) & 0x3C0u), static_cast<int>((r.sc >> 4) & 0xF0u),
                        static_cast<int>((r.sc >> 14) & 0x3Cu), static_cast<int>((r.sc >> 24) & 0xFu)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         int s0 = 0, s1 = 0, s2 = 0;
+        const uint4 x0 = x.quad(j, 0), x1 = x.quad(j, 1), x2 = x.quad(j, 2);
+        const uint32_t d0[4] = {x0.x, x0.y, x0.z, x0.w}, d1[4] = {x1.x, x1.y, x1.z, x1.w},
+                       d2[4] = {x2.x, x2.y, x2.z, x2.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t q = r.q[i] & (0x03030303u << (2 * j));
-            s0 = dot4_uu(q, x.x[j][0][i], s0);
-            s1 = dot4_uu(q, x.x[j][1][i], s1);
-            s2 = dot4_us(q, x.x[j][2][i], s2);
+            s0 = dot4_us(q, d0[i], s0);
+            s1 = dot4_us(q, d1[i], s1);
+            s2 = dot4_us(q, d2[i], s2);
         }
         a0 += s0 * sc[j];
         a1 += s1 * sc[j];
@@ -382,8 +435,9 @@ __device__ __forceinline__ float slice_product(const RowWords& r, const XBytes& 
     }
     // minima, m in the high nibbles: products carry 16
     const uint32_t m = r.sc & 0xF0F0F0F0u;
-    const int e0 = dot4_uu(m, x.s[0], 0) + 256 * dot4_uu(m, x.s[1], 0);
-    const int e1 = dot4_uu(m, x.s[2], 0) + 256 * dot4_us(m, x.s[3], 0);
+    const uint4 s = x.sums();
+    const int e0 = dot4_us(m, s.x, 0) + 256 * dot4_us(m, s.y, 0);
+    const int e1 = dot4_us(m, s.z, 0) + 256 * dot4_us(m, s.w, 0);
     const float a = fmaf(65536.f, static_cast<float>(a2),
                          fmaf(256.f, static_cast<float>(a1), static_cast<float>(a0)));
     const float e = fmaf(65536.f, static_cast<float>(e1), static_cast<float>(e0));
@@ -816,12 +870,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         waited = true;
     }
     XBytes xi;
+    [[maybe_unused]] float undo = 0.f;
+    [[maybe_unused]] bool wide = false;
     XBlock<T> xm[kBytes ? 1 : NT];
     if (warp < nb) {
         if constexpr (kBytes) {
-            make_x_bytes(x, b0 + warp, lane, xs + warp * kXWords);
-            __syncwarp();
-            take_x_bytes(xs + warp * kXWords, lane, xi);
+            wide = load_x_bytes(x, b0 + warp, lane, xs + warp * kXWords, xi, undo);
         } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -890,10 +944,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 const RowWords r0 = read_row(row + a * tile_bytes, lane & 3);
                 const RowWords r1 = read_row(row + a * tile_bytes + 8 * pitch, lane & 3);
                 if constexpr (kBytes) {
-                    acc[a][0][0] = xi.undo * slice_product(r0, xi);
-                    acc[a][0][1] = xi.undo * slice_product(r1, xi);
+                    acc[a][0][0] = undo * slice_product(r0, xi);
+                    acc[a][0][1] = undo * slice_product(r1, xi);
                 } else {
                     block_product<T, NT>(r0, r1, xm, acc[a]);
+                }
+            }
+            if constexpr (kBytes) {
+                if (wide) {  // (of the warp)
+                    const StoredXBytes rest = {
+                        reinterpret_cast<const uint4*>(xs + warp * kXWords + 52 * (lane & 3))};
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const RowWords r = read_row(row + (i >> 1) * tile_bytes + (i & 1) * 8 * pitch, lane & 3);
+                        const float v = undo * kRest * slice_product(r, rest);
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) acc[o >> 1][0][o & 1] += i == o ? v : 0.f;
+                    }
                 }
             }
         }

@@ -526,10 +526,14 @@ int q2k_abi_version(void);
  * formula gives an infinity: a block's sum and its minima's meet as inf - inf).
  *
  * Paths (Q2K_PATH_AUTO picks by m):
- *   Q2K_PATH_GEMV    every weight exact, x to 2^-22 of the largest |x| of its block
- *                    of 256 or better; products summed in integers or f32.  The
- *                    error is within 1e-5 * sum_k |x| (dl q + ml).  Auto takes it
- *                    for m <= 16 (bf16) or 8 (f32).
+ *   Q2K_PATH_GEMV    every weight exact; x rounded with its block of 256, products
+ *                    summed in integers or f32.  The error is within
+ *                      c * sum_k |x| w + r * sum over blocks (max |x| * sum w),
+ *                    w = dl q + ml, max |x| at least 2^-100, c = max(1e-5, k 2^-31);
+ *                    r = 2^-34, and for a single token 2^-22, or 2^-43 in a block
+ *                    more than a quarter of whose x are below 2^-9 of its largest
+ *                    (zeros not counted).  Auto takes it for m <= 16 (bf16) or 8
+ *                    (f32).
  *   Q2K_PATH_TENSOR  x and W rounded to bf16 (error within 8e-3 * sum_k |x w|,
  *                    as q2k_matmul's tensor path). */
 typedef enum q2k_dtype { Q2K_DTYPE_F32 = 0, Q2K_DTYPE_BF16 = 1 } q2k_dtype;
