@@ -991,7 +991,7 @@ q2k_status check_ffn_shape(uint32_t m, uint32_t n, uint32_t k, uint32_t ggml_typ
         return fail(Q2K_ERR_INVALID_ARGUMENT, "m, n, k must be >= 1 (got %u, %u, %u)", m, n, k);
     if (k % Q2K_QK_K != 0)
         return fail(Q2K_ERR_INVALID_ARGUMENT, "k = %u is not a multiple of 256", k);
-    // tiles of tokens and rows are counted in grid dimensions of 16 bits
+    // (a bound for the kernels' 32-bit counts of tiles)
     if (m > Q2K_FFN_MAX_TOKENS || n > Q2K_FFN_MAX_WIDTH || k > Q2K_FFN_MAX_WIDTH)
         return fail(Q2K_ERR_INVALID_ARGUMENT, "m must be <= %d and n, k <= %d (got %u, %u, %u)",
                     Q2K_FFN_MAX_TOKENS, Q2K_FFN_MAX_WIDTH, m, n, k);

@@ -727,6 +727,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     if (!waited) pdl_wait_prerequisites();
 }
 
+// The passes over tokens are a grid's y: of more than it holds, the rest go to
+// further launches (of the same kernel: a token's result is the same in each).
+constexpr int kMaxPasses = 65535;
+
+// Calls `launch(x, args)` for each run of at most kMaxPasses passes of kTokens.
+template <typename T, int kTokens, typename Launch>
+cudaError_t launch_passes(const T* x, const RowsArgs& p, Launch&& launch) {
+    for (int first = 0; first < p.M; first += kMaxPasses * kTokens) {
+        RowsArgs q = p;
+        q.M = std::min(p.M - first, kMaxPasses * kTokens);
+        const size_t at = static_cast<size_t>(first) * p.N;
+        if (p.h != nullptr) q.h = static_cast<T*>(p.h) + at;
+        if (p.gate != nullptr) q.gate = static_cast<T*>(p.gate) + at;
+        if (p.up != nullptr) q.up = static_cast<T*>(p.up) + at;
+        if (p.y != nullptr) q.y = static_cast<T*>(p.y) + at;
+        if (p.t != nullptr) q.t = p.t + static_cast<size_t>(first) * p.R;
+        if (p.ids != nullptr) q.ids = p.ids + first;
+        const cudaError_t e = launch(x + static_cast<size_t>(first) * p.K, q);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 template <typename T, int NT, int S, Rows kMode>
 cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cudaStream_t stream) {
     constexpr int kTokens = Pass<T, NT>::kTokens;
@@ -747,8 +770,6 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     p.kw = (per_pass + S - 1) / S;
     p.groups = p.passes > 1 ? 1 : kWarps / p.kw;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::min(sm_count, (p.units + p.groups - 1) / p.groups),
-                       (p.M + kTokens - 1) / kTokens);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
@@ -757,7 +778,11 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode>, static_cast<const T*>(x), p);
+    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q) {
+        cfg.gridDim = dim3(std::min(sm_count, (p.units + p.groups - 1) / p.groups),
+                           (q.M + kTokens - 1) / kTokens);
+        return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode>, xs, q);
+    });
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -1047,9 +1072,11 @@ cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, i
         most = std::max(1, most);
         resident[device][p.parts].store(most, std::memory_order_release);
     }
-    cfg.gridDim = dim3(std::min(most, p.units) * p.parts,
-                       (p.M + Pass<T, NT>::kTokens - 1) / Pass<T, NT>::kTokens);
-    return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode>, static_cast<const T*>(x), p);
+    constexpr int kTokens = Pass<T, NT>::kTokens;
+    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q) {
+        cfg.gridDim = dim3(std::min(most, p.units) * p.parts, (q.M + kTokens - 1) / kTokens);
+        return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode>, xs, q);
+    });
 }
 
 // Columns of x in registers: one tile of eight and up to two blocks a warp, or
