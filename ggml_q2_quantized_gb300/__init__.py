@@ -20,6 +20,7 @@ import importlib.util
 import os
 import re
 import threading
+import warnings
 
 from . import build as _build
 
@@ -779,8 +780,14 @@ def _quick():
             _quick_mod = False
             return False
         spec = importlib.util.spec_from_file_location("q2k_torch", path)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
+        try:
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+        except ImportError as e:
+            warnings.warn(f"the PyTorch module does not load; feed-forward calls go through ctypes: {e}",
+                          RuntimeWarning, stacklevel=3)
+            _quick_mod = False
+            return False
         mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
             "q2k_gated_ffn", "q2k_gated_ffn_workspace_bytes", "q2k_gated_ffn_backward",
             "q2k_gated_ffn_backward_workspace_bytes", "q2k_matmul_lora",
