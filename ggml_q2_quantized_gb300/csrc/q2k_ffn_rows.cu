@@ -756,13 +756,13 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     constexpr int kOut = Pass<T, NT>::kSums;
     constexpr int kSmem = kWarps * kDepth * kItemBytes + (kWarps * 2 + kGroupUnits) * 2 * kOut * 4 ;
     static_assert(kSmem <= 232448, "shared memory");
-    static bool attr_done[64] = {};
+    static std::atomic<bool> attr_done[64] = {};  // (set by any thread; setting twice does no harm)
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    if (!attr_done[device]) {
+    if (!attr_done[device].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, NT, S, kMode>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        attr_done[device] = true;
+        attr_done[device].store(true, std::memory_order_release);
     }
     const int blocks = p.K / kQK;
     p.passes = (blocks + kWarps * S - 1) / (kWarps * S);

@@ -1437,14 +1437,14 @@ template <int kX, bool kTma, Tc kMode, typename T>
 cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, int device,
                          cudaStream_t stream) {
     using C = Cfg<kX, kTma, kMode>;
-    static bool attr_done[64] = {};
+    static std::atomic<bool> attr_done[64] = {};  // (set by any thread; setting twice does no harm)
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    if (!attr_done[device]) {
+    if (!attr_done[device].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<kX, kTma, kMode, T>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    C::kSmemBytes);
         if (e != cudaSuccess) return e;
-        attr_done[device] = true;
+        attr_done[device].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.workers * plan.ctas * plan.parts);
