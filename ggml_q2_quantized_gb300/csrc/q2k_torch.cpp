@@ -104,20 +104,37 @@ struct Workspace {
     }
 };
 
+// The interpreter's lock is free while this lives, also where an exception ends it.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <typename Call>
 PyObject* finish(Call&& call, const Tensor& like, std::initializer_list<Tensor> outs) {
     const q2k_stream_t stream =
         reinterpret_cast<q2k_stream_t>(c10::cuda::getCurrentCUDAStream(like.get_device()).stream());
     int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = static_cast<int>(call(stream));
-    Py_END_ALLOW_THREADS
+    {
+        const Unlocked unlocked;
+        status = static_cast<int>(call(stream));
+    }
     if (status != 0) return PyLong_FromLong(status);
     if (outs.size() == 1) return THPVariable_Wrap(*outs.begin());
     PyObject* all = PyTuple_New(static_cast<Py_ssize_t>(outs.size()));
     if (all == nullptr) return nullptr;
     Py_ssize_t i = 0;
-    for (const Tensor& t : outs) PyTuple_SET_ITEM(all, i++, THPVariable_Wrap(t));
+    for (const Tensor& t : outs) {
+        PyObject* o = THPVariable_Wrap(t);
+        if (o == nullptr) {
+            Py_DECREF(all);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(all, i++, o);
+    }
     return all;
 }
 
@@ -167,8 +184,8 @@ PyObject* gated(PyObject*, PyObject* const* v, Py_ssize_t count) {
         }
         const Workspace ws(calls.gated_bytes(path, &p), *x);
         auto call = [&](q2k_stream_t stream) {
-            return calls.gated(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->data_ptr(), x->numel(),
-                               wg->data_ptr(), wg->numel(), wu->data_ptr(), wu->numel(), h.data_ptr(),
+            return calls.gated(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->const_data_ptr(), x->numel(),
+                               wg->const_data_ptr(), wg->numel(), wu->const_data_ptr(), wu->numel(), h.data_ptr(),
                                h.numel(), save ? g.data_ptr() : nullptr, save ? u.data_ptr() : nullptr,
                                &p, ws.at, ws.bytes, stream);
         };
@@ -199,8 +216,8 @@ PyObject* backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
         const Workspace ws(calls.backward_bytes(&p), *dh);
         return finish(
             [&](q2k_stream_t stream) {
-                return calls.backward(dh->data_ptr(), g->data_ptr(), u->data_ptr(), dh->numel(),
-                                      wg->data_ptr(), wg->numel(), wu->data_ptr(), wu->numel(),
+                return calls.backward(dh->const_data_ptr(), g->const_data_ptr(), u->const_data_ptr(), dh->numel(),
+                                      wg->const_data_ptr(), wg->numel(), wu->const_data_ptr(), wu->numel(),
                                       dx.data_ptr(), dx.numel(), dg.data_ptr(), du.data_ptr(), &p, ws.at,
                                       ws.bytes, stream);
             },
@@ -243,10 +260,10 @@ PyObject* lora(PyObject*, PyObject* const* v, Py_ssize_t count) {
         const Workspace ws(calls.lora_bytes(path, &p), *x);
         return finish(
             [&](q2k_stream_t stream) {
-                return calls.lora(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->data_ptr(), x->numel(),
-                                  w->data_ptr(), w->numel(), a->data_ptr(), a->numel(), b->data_ptr(),
-                                  b->numel(), scales != nullptr ? scales->data_ptr<float>() : nullptr,
-                                  ids->data_ptr<int32_t>(), y.data_ptr(), y.numel(), &p,
+                return calls.lora(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->const_data_ptr(), x->numel(),
+                                  w->const_data_ptr(), w->numel(), a->const_data_ptr(), a->numel(), b->const_data_ptr(),
+                                  b->numel(), scales != nullptr ? scales->const_data_ptr<float>() : nullptr,
+                                  ids->const_data_ptr<int32_t>(), y.data_ptr(), y.numel(), &p,
                                   static_cast<uint32_t*>(bad.data_ptr()), ws.at, ws.bytes, stream);
             },
             *x, {y, bad});
