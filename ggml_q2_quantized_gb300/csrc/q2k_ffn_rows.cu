@@ -808,7 +808,9 @@ __device__ __forceinline__ void send_pair(uint32_t addr, uint32_t bar, uint32_t 
 // multiplies unit u, then waits for the others' sums of u - 1 and brings its share
 // of them out, and only then writes its sums of u, so that two buffers of sums do
 // and no warp waits for the slowest at every unit.  That all have their sums of
-// u - 1 also says that the unit's slot is free to be refilled.
+// u - 1 also says that the unit's slot is free to be refilled: a warp arrives after
+// it has stored sums that every word it read went into, so no read is still on its
+// way.
 // More than 16 blocks: a cluster's CTAs divide K (in fours of blocks, so that
 // copies start at 16 bytes).  Each has a share of a unit's outputs; the others send
 // it their sums of those, which it adds in the order of K another unit later.  A
