@@ -48,6 +48,7 @@
 #include <mutex>
 
 #include "q2k_ffn.cuh"
+#include "q2k_ffn_plan.h"
 #include "q2k_internal.h"
 #include "q2k_tc.cuh"
 
@@ -98,9 +99,8 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kMmaWarp = kDecWarps, kWaitWarp = kDecWarps + 1, kWWarp = kDecWarps + 2,
               kXWarp = kDecWarps + 3, kEpiWarp0 = kDecWarps + 4;  // (a multiple of 4)
 constexpr int kThreads = 32 * (kDecWarps + 8);
-constexpr int kMaxParts = 8;   // of K (the largest portable cluster)
-constexpr int kPlanSms = 152;  // the work is cut for the whole GPU, whatever the device
 
+static_assert(kRows == kPlanRows, "a tile's rows");
 constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memory
 // Sums of 32 tokens on their way out: token c, row r at word 132 c + r (132:
 // lanes that read two tokens apart fall on different banks).
@@ -454,60 +454,6 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
         : "memory");
     return v;
 }
-
-// One worker's share of the product (a CTA, or a pair): first its runs of the cut
-// tiles (two at most), then its whole tiles.
-struct Segment {
-    int tile, q0, q1;
-    int run;  // -1: a whole tile; else which of the worker's runs
-};
-struct Work {
-    int w, workers, quads, tiles, whole;
-    int part, parts;  // of K, for the CTAs of a cluster
-    // quads [begin(w), begin(w + 1)) of the cut tiles, counted through
-    __device__ __forceinline__ int begin(int w) const {
-        return static_cast<int>(static_cast<long long>(tiles - whole) * quads * w / workers);
-    }
-    __device__ __forceinline__ bool segment(int index, Segment& s) const {
-        const int a0 = begin(w), a1 = begin(w + 1);
-        int runs = 0;
-        if (a1 > a0) {
-            const int t0 = a0 / quads, t1 = (a1 - 1) / quads;
-            runs = t1 - t0 + 1;
-            if (index < runs) {
-                s.tile = whole + t0 + index;
-                s.q0 = index == 0 ? a0 - t0 * quads : 0;
-                s.q1 = index == runs - 1 ? a1 - t1 * quads : quads;
-                s.run = index;
-                return true;
-            }
-        }
-        s.tile = w + (index - runs) * workers;
-        s.q0 = quads * part / parts;
-        s.q1 = quads * (part + 1) / parts;
-        s.run = -1;
-        return s.tile < whole;
-    }
-    __device__ __forceinline__ int count() const {
-        const int a0 = begin(w), a1 = begin(w + 1);
-        return (a1 > a0 ? (a1 - 1) / quads - a0 / quads + 1 : 0) +
-               (w < whole ? (whole - 1 - w) / workers + 1 : 0);
-    }
-    // The workers with a run of cut tile `tile`.
-    __device__ __forceinline__ void sharers(int tile, int& first, int& last) const {
-        const long long q = static_cast<long long>(tile - whole) * quads;
-        const long long total = static_cast<long long>(tiles - whole) * quads;
-        first = static_cast<int>(q * workers / total);
-        while (first > 0 && begin(first) > q) --first;
-        while (begin(first + 1) <= q) ++first;
-        last = first;
-        while (last + 1 < workers && begin(last + 1) < q + quads) ++last;
-    }
-    // Which of worker v's runs is of cut tile `tile`.
-    __device__ __forceinline__ int run_of(int v, int tile) const {
-        return tile - whole - begin(v) / quads;
-    }
-};
 
 // Backward, non-TMA: the words of 64 weight rows that a stage needs (two of
 // scales, eight of codes, d and dmin) packed into a raw slot, by the 128 threads
@@ -1358,63 +1304,6 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 }
 
 // ---- plan ----------------------------------------------------------------------
-
-struct Plan {
-    int x_rows, row_units, tiles, whole, workers, ctas, parts;
-    size_t partial, counts;  // bytes of workspace
-};
-
-// rows: those of the product; quads: its K in blocks (backward: 256 weight rows).
-// Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,
-// whichever is expected to end first: a worker's stages times the time of a
-// stage, about 1 : 0.7 for 256 and 128 tokens.
-Plan make_plan(int M, int rows, int tile_rows, int quads) {
-    Plan best = {};
-    double best_cost = 0;
-    for (int x_rows : {32, 64, 128, 256}) {
-        if (x_rows < 128 && x_rows < M) continue;
-        Plan p = {};
-        p.x_rows = x_rows;
-        p.ctas = x_rows == 256 ? 2 : 1;
-        const int row_tiles = (rows + tile_rows - 1) / tile_rows;
-        p.row_units = (row_tiles + p.ctas - 1) / p.ctas;
-        p.tiles = p.row_units * ((M + x_rows - 1) / x_rows);
-        const int most = kPlanSms / p.ctas;
-        const int rounds = p.tiles / most;
-        p.parts = 1;
-        p.whole = p.tiles;
-        p.workers = std::min(p.tiles, most);
-        double cost;
-        if (rounds == 0) {
-            p.parts = std::max(1, std::min({kMaxParts / p.ctas, quads, most / p.tiles}));
-            cost = static_cast<double>(quads) / p.parts + 1;
-        } else {
-            // whole tiles only, or what is left after full rounds of them cut
-            // evenly (a quad for every worker at least).  Bringing the runs' sums
-            // together costs as long as 15 quads or so beyond what the whole tiles
-            // behind it hide (14336 x 4096, 16 quads a tile: 256 tokens, 1.5 rounds,
-            // 55 us whole and 87 cut; 128 tokens 43 and 54.  Backwards, 112 quads a
-            // tile: 2048 tokens, 1.7 rounds, 384 and 353).
-            const long left = static_cast<long>(p.tiles - rounds * most) * quads;
-            const double uncut = static_cast<double>(quads) * ((p.tiles + most - 1) / most);
-            const double cut = static_cast<double>(p.tiles) * quads / most + 15;
-            const bool cuts = left >= most && cut < uncut;
-            if (cuts) p.whole = rounds * most;
-            cost = cuts ? cut : uncut;
-        }
-        cost *= x_rows == 256 ? 1.0 : 0.7;
-        if (best_cost == 0 || cost < best_cost) {
-            best = p;
-            best_cost = cost;
-        }
-        if (x_rows >= M) break;  // a wider tile would be empty columns
-    }
-    if (best.whole < best.tiles) {
-        best.partial = static_cast<size_t>(2) * best.workers * best.ctas * best.x_rows * kRows * 4;
-        best.counts = (static_cast<size_t>(best.tiles - best.whole) * best.ctas * 4 + 255) & ~size_t(255);
-    }
-    return best;
-}
 
 size_t plan_bytes(const Plan& p) { return p.partial + p.counts; }
 int count_words(const Plan& p) { return static_cast<int>(p.counts / 4); }
