@@ -104,13 +104,14 @@ inline Plan make_plan(int M, int rows, int tile_rows, int quads) {
         } else {
             // whole tiles only, or what is left after full rounds of them cut
             // evenly (a quad for every worker at least).  Bringing the runs' sums
-            // together costs as long as 15 quads or so beyond what the whole tiles
-            // behind it hide (14336 x 4096, 16 quads a tile: 256 tokens, 1.5 rounds,
-            // 55 us whole and 87 cut; 128 tokens 43 and 54.  Backwards, 112 quads a
-            // tile: 2048 tokens, 1.7 rounds, 384 and 353).
+            // together costs about 15 quads, and what adding a tile's runs takes (by
+            // four warps of one CTA: 6 quads for a run of 128 tokens, 7 of 256, whose
+            // quads are longer) beyond the whole tiles that are multiplied meanwhile.
             const long left = static_cast<long>(p.tiles - rounds * most) * quads;
             const double uncut = static_cast<double>(quads) * ((p.tiles + most - 1) / most);
-            const double cut = static_cast<double>(p.tiles) * quads / most + 15;
+            const double runs = static_cast<double>(quads) * most / std::max(left, 1l) + 1;
+            const double adding = runs * (x_rows == 256 ? 7 : x_rows / 21.0) - static_cast<double>(rounds) * quads;
+            const double cut = static_cast<double>(p.tiles) * quads / most + 15 + std::max(0.0, adding);
             const bool cuts = left >= most && cut < uncut;
             if (cuts) p.whole = rounds * most;
             cost = cuts ? cut : uncut;

@@ -74,7 +74,7 @@ def test_gated(m, n, k, dtype):
     assert torch.equal(h, q2k.gated_ffn(x, a.w, b.w, n))
 
 
-@pytest.mark.parametrize("m,n,k", [(2048, 14336, 4096), (600, 5000, 4096), (1000, 14000, 2816),
+@pytest.mark.parametrize("m,n,k", [(2048, 14336, 4096), (600, 14336, 4096), (600, 5000, 4096), (1000, 14000, 2816),
                                    (200, 9800, 14336), (601, 5003, 4096)])
 def test_backward(m, n, k):
     gen = torch.Generator(device="cuda:0").manual_seed(m)
@@ -92,11 +92,11 @@ def test_backward(m, n, k):
            36 * 8 * 2.0 ** -24 * (dh.double() * u.double()).abs() * (1 + gd.abs()), "bf16", "dgate")
 
 
-LORA = [("bf16", 1024, 5000, 14336, 16, 5), ("bf16", 512, 14336, 1024, 64, 7), ("bf16", 600, 5000, 4096, 8, 3),
+LORA = [("bf16", 1024, 6000, 14336, 16, 5), ("bf16", 1024, 5000, 14336, 16, 5), ("bf16", 512, 14336, 1024, 64, 7), ("bf16", 600, 5000, 4096, 8, 3),
         ("bf16", 300, 9800, 1024, 40, 9), ("bf16", 512, 14336, 4096, 16, 6), ("bf16", 70, 5000, 4096, 128, 20),
         ("f32", 9, 300, 1024, 16, 3), ("f32", 20, 1000, 2816, 8, 4), ("f32", 45, 1003, 1792, 24, 5),
         ("f32", 64, 500, 4096, 256, 2), ("f32", 100, 5000, 4096, 64, 6), ("f32", 300, 300, 1024, 16, 4),
-        ("f32", 300, 9800, 1024, 40, 9), ("f32", 600, 5000, 4096, 8, 3), ("f32", 1024, 5000, 14336, 16, 5),
+        ("f32", 300, 9800, 1024, 40, 9), ("f32", 600, 5000, 4096, 8, 3), ("f32", 1024, 6000, 14336, 16, 5),
         ("f32", 512, 7168, 7168, 64, 4)]
 
 
