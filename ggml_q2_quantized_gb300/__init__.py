@@ -807,6 +807,8 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     that ``gated_ffn_backward`` reads.  ``path``, ``const_weights`` and
     ``workspace`` as in ``matmul``: up to 16 bf16 or 8 f32 tokens the weights
     are exact, above that x and W are rounded to bf16 for the tensor cores.
+    Nothing is recorded for autograd: h does not require a gradient, even where
+    x does.
     """
     if out is None and workspace.__class__ is str:
         quick = _quick_mod or _quick()

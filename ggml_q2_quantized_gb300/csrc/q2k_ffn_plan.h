@@ -107,6 +107,10 @@ inline Plan make_plan(int M, int rows, int tile_rows, int quads) {
             // together costs about 15 quads, and what adding a tile's runs takes (by
             // four warps of one CTA: 6 quads for a run of 128 tokens, 7 of 256, whose
             // quads are longer) beyond the whole tiles that are multiplied meanwhile.
+            // Whole and cut, us: backwards 2048 tokens, 14336 x 4096, 392 and 357; 1200
+            // 367 and 260; 600, 5000 x 4096, 77 and 109; gated 100 tokens, 12000 x
+            // 16384, 148 and 105; 14336 x 4096, 128 tokens 43 and 55, 256 56 and 87;
+            // 200 tokens, 9800 x 14336, 172 and 194.
             const long left = static_cast<long>(p.tiles - rounds * most) * quads;
             const double uncut = static_cast<double>(quads) * ((p.tiles + most - 1) / most);
             const double runs = static_cast<double>(quads) * most / std::max(left, 1l) + 1;

@@ -12,12 +12,13 @@
 // thus give two exact weights, where forming dl q - ml in f32 takes three
 // instructions for each; the tensor cores (m16n8k16, f16 in, f32 sums) take the
 // products of 16 rows, 16 weights and 8 columns of x at once.  d and dmin enter
-// once per block, in f32.  One such product takes 16 clocks of an SM's quarter, 36
-// of them a block of 16 rows with 16 bf16 tokens: 13.7 of the 21.2 us that the two
-// matrices of 14336 x 4096 take (16.5 us with up to 8 tokens; HBM alone would take 5.7).
+// once per block, in f32.  The two matrices of 14336 x 4096 take 21.2 us with 16 bf16
+// tokens and 16.5 with up to 8 (HBM alone would take 5.7): with the products left out
+// (36 a block of 16 rows with 16 tokens) 11.8 us are left, with the multiplies by sc
+// left out 19.0; the tensor pipe is busy for a third of the time, issue for a half.
 //
 // A single token has its products in integers instead, four weights an
-// instruction (dp4a): 13.5 us, 8.4 of them by the arithmetic (4.6 TB/s of weights
+// instruction (dp4a): 13.5 us, 8.1 with them left out (4.6 TB/s of weights
 // for longer matrices).  Its x is rounded to 22 bits beside its block's largest
 // (XBytes below), coarser than the two f16 parts.
 //

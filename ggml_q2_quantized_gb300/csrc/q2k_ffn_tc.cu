@@ -31,8 +31,9 @@
 //   end together.  The runs come first: their sums go to the workspace, the CTA
 //   that finishes last adds them, in the order of K whoever that is, and all of
 //   that happens while whole tiles are multiplied.  No CTA waits for another.
-//   (2048 tokens backwards, 14336 x 4096: 128 tiles for 76 pairs, 353 us against
-//   384 in two rounds.  Cutting without whole tiles behind it exposes the adding.)
+//   (2048 tokens backwards, 14336 x 4096: 128 tiles for 76 pairs, the whole call 357
+//   us against 392 in two rounds.  Cutting without whole tiles behind it, or into
+//   many runs, exposes the adding.)
 //
 // What bounds it: at 256 tokens a tile the MMAs and the shared memory that feeds
 // them (per stage and SM 32 KB of operands read, 32 KB written: 512 of about 740

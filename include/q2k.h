@@ -516,7 +516,8 @@ int q2k_abi_version(void);
  * The two halves of a feed-forward layer with frozen Q2_K weights, for serving
  * and for training what stands around them.  Activations are f32 or bf16
  * (params.dtype, one type for all of a call's activations), row-major and
- * 16-byte aligned; sums are f32 and results are rounded once.  Calls are
+ * 16-byte aligned; sums are f32, and a result is rounded once at the end (what is
+ * rounded before, with each path and call below).  Calls are
  * asynchronous on `stream`, allocate nothing and may be captured; a workspace
  * (device, 16-byte aligned, of at least the size the *_workspace_bytes call
  * returns for the same arguments; NULL when that is 0) must not be used by
