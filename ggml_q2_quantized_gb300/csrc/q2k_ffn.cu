@@ -71,6 +71,8 @@ struct XParts<float> {
                 v[q][e] = *reinterpret_cast<const uint32_t*>(&h);
                 f[2 * e] -= __uint_as_float(v[q][e] << 16);
                 f[2 * e + 1] -= __uint_as_float(v[q][e] & 0xFFFF0000u);
+                // (an infinity is its first part alone: the others would be NaN, and are 2^120)
+                if (q > 0) v[q][e] = min_bf16x2(v[q][e], 0x7B807B80u);
             }
     }
     __device__ __forceinline__ void zero() {

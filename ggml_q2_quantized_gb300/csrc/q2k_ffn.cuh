@@ -31,6 +31,13 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The smaller of two pairs of bf16; of a NaN and a number, the number.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // act(g) = g p and act'(g) = p + g (1 - p) p z'(g), with p = 1 / (1 + e^-z):
 //   silu  z = g                                     z' = 1
 //   gelu  z = 2 sqrt(2/pi) (g + 0.044715 g^3)       z' = 2 sqrt(2/pi) (1 + 3 * 0.044715 g^2)

@@ -18,7 +18,7 @@
 // left out 19.0; the tensor pipe is busy for a third of the time, issue for a half.
 //
 // A single token has its products in integers instead, four weights an
-// instruction (dp4a): 13.5 us, 8.1 with them left out (4.6 TB/s of weights
+// instruction (dp4a): 13.6 us, 8.1 with them left out (4.6 TB/s of weights
 // for longer matrices).  Its x is rounded to 22 bits beside its block's largest
 // (XBytes below), coarser than the two f16 parts.
 //
@@ -505,9 +505,60 @@ __device__ __forceinline__ void write_sums(float* mine, int lane, const float (&
         }
 }
 
+// Weight k of a row of blocks.
+__device__ __forceinline__ float weight_at(const uint8_t* row, int k) {
+    const uint8_t* b = row + static_cast<size_t>(k / kQK) * kBlockBytes;
+    const int half = (k >> 7) & 1, j = (k >> 5) & 3, seg = (k >> 4) & 1;
+    const uint32_t sc = b[8 * half + 2 * j + seg];
+    const uint32_t q = (b[16 + 32 * half + 16 * seg + (k & 15)] >> (2 * j)) & 3u;
+    const uint32_t dd = ld_u32(b + 80);
+    const float dl = f16_bits_to_float(dd) * static_cast<float>(sc & 15u);
+    return fmaf(dl, static_cast<float>(q), -(f16_bits_to_float(dd >> 16) * static_cast<float>(sc >> 4)));
+}
+
+// Whether a word of x holds an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ bool special_word(uint32_t w) {
+    constexpr uint32_t kExp = 0x7F800000u;
+    return (w & kExp) == kExp || (sizeof(T) == 2 && ((w << 16) & kExp) == kExp);
+}
+
+// A sum over K that came out not finite, of one token and one row: codes and minima
+// are summed apart, and x in parts, so infinities meet as NaN where the formula has
+// one.  By the formula the sum is that of the infinities and NaNs of x times their
+// weights; with x finite the parts overflowed, and the sum is taken of x 2^-64.
+// 14336 x 4096: looking for such sums costs a call 0.2 us at one token, 0.1 at 16 bf16
+// and 0.7 at eight f32 ones; a token that has them 0.7 ms.  (In line: as a function of
+// its own, called or not, it cost every launch 0.3 us on the host.)
+template <typename T>
+__device__ __forceinline__ float sum_not_finite(const T* x, const uint8_t* row, int K) {
+    constexpr int kStep = 32 / sizeof(T);
+    float sum = 0.f;
+    bool found = false;
+#pragma unroll 1
+    for (int k = 0; k < K; k += kStep) {
+        const uint4 a = *reinterpret_cast<const uint4*>(x + k), b = *reinterpret_cast<const uint4*>(x + k + kStep / 2);
+        if (!(special_word<T>(a.x) || special_word<T>(a.y) || special_word<T>(a.z) || special_word<T>(a.w) ||
+              special_word<T>(b.x) || special_word<T>(b.y) || special_word<T>(b.z) || special_word<T>(b.w)))
+            continue;
+        found = true;
+#pragma unroll 1
+        for (int e = k; e < k + kStep; ++e) {
+            const float v = to_float(x[e]);
+            if (special_word<float>(__float_as_uint(v))) sum = fmaf(weight_at(row, e), v, sum);
+        }
+        if (sum != sum) break;
+    }
+    if (found) return sum;
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) sum = fmaf(weight_at(row, k), to_float(x[k]) * 0x1p-64f, sum);
+    return sum * 0x1p64f;
+}
+
 // Sum o of a unit's two tiles -> results.
 template <typename T, int NT, Rows kMode>
-__device__ __forceinline__ void finish_row(const RowsArgs& p, int o, float (&v)[2], int unit, int m0) {
+__device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, int o, float (&v)[2], int unit,
+                                           int m0) {
     constexpr bool kSplit = sizeof(T) == 4;
     const int f = o >> 5, l = o & 31;
     // fragment f of lane l: its row of the tile and its token
@@ -517,6 +568,19 @@ __device__ __forceinline__ void finish_row(const RowsArgs& p, int o, float (&v)[
                                  : (f >> 2) * 8 + 2 * (l & 3) + (f & 1));
     const int n = unit * p.unit_step + r;
     if (m >= p.M) return;
+    if (!(fabsf(v[0]) + fabsf(v[1]) <= 3.402823466e38f)) {
+        // (each by itself: a row past N is whatever the slot held before)
+#pragma unroll 1
+        for (int a = 0; a < 2; ++a) {
+            const int na = n + a * p.tile1_row;
+            if (fabsf(a ? v[1] : v[0]) <= 3.402823466e38f || na >= p.N) continue;
+            const float sum = sum_not_finite(x + static_cast<size_t>(m) * p.K,
+                                             (a ? p.w1 : p.w0) + static_cast<size_t>(na) * (p.K / kQK) * kBlockBytes,
+                                             p.K);
+            v[0] = a ? v[0] : sum;
+            v[1] = a ? sum : v[1];
+        }
+    }
     if (kMode == Rows::kGated) {
         if (n >= p.N) return;
         const size_t at = static_cast<size_t>(m) * p.N + n;
@@ -717,7 +781,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                             continue;
                         }
                     }
-                    finish_row<T, NT, kMode>(p, o, v, unit, m0);
+                    finish_row<T, NT, kMode>(x, p, o, v, unit, m0);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -930,7 +994,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[1] += all[w * (2 * kOut) + kOut + o];
             }
             if (p.parts == 1) {
-                finish_row<T, NT, kMode>(p, o, v, first_unit + u * unit_step, m0);
+                finish_row<T, NT, kMode>(x, p, o, v, first_unit + u * unit_step, m0);
             } else {
                 const int to = ((o + 1) * p.parts - 1) / kOut;  // whose share o is
                 const int at = ((u & 3) * p.parts + rank) * share + o - kOut * to / p.parts;
@@ -951,7 +1015,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[0] += w.x;
                 v[1] += w.y;
             }
-            finish_row<T, NT, kMode>(p, o_first + o, v, first_unit + u * unit_step, m0);
+            finish_row<T, NT, kMode>(x, p, o_first + o, v, first_unit + u * unit_step, m0);
         }
     };
     __syncthreads();

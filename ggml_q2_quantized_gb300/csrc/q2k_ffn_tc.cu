@@ -332,6 +332,9 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const 
                                 v[u].y - __uint_as_float(w.x & 0xFFFF0000u));
                 w.w = pack_bf16(v[u].z - __uint_as_float(w.z << 16),
                                 v[u].w - __uint_as_float(w.z & 0xFFFF0000u));
+                // (an infinity is its first part alone: the other would be NaN, and is 2^120)
+                w.y = min_bf16x2(w.y, 0x7B807B80u);
+                w.w = min_bf16x2(w.w, 0x7B807B80u);
                 *reinterpret_cast<uint4*>(tbuf + 64 * c + (r ^ (8 * (c & 3)))) = w;
             }
         }

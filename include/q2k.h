@@ -522,9 +522,9 @@ int q2k_abi_version(void);
  * (device, 16-byte aligned, of at least the size the *_workspace_bytes call
  * returns for the same arguments; NULL when that is 0) must not be used by
  * another call until this one has finished.  Repeated calls on the same inputs
- * give the same bits.  A token that holds a NaN has NaN results; one that holds an
- * infinity has none that are finite (on the GEMV path they are NaN, also where the
- * formula gives an infinity: a block's sum and its minima's meet as inf - inf).
+ * give the same bits.  A token that holds a NaN has NaN results, and one that holds
+ * an infinity those of the formula (infinities, and NaN where a weight is zero or
+ * infinities meet).
  *
  * Paths (Q2K_PATH_AUTO picks by m):
  *   Q2K_PATH_GEMV    every weight exact; x rounded with its block of 256, products
