@@ -727,6 +727,9 @@ def _ffn_plan(key):
     rank, n_adapters)."""
     lib, torch = load(), _torch()
     kind, path, dtype, m, n, k = key[:6]
+    for name, value, known in (("path", path, _PATHS), ("act", "silu" if kind == "lora" else key[6], _ACTS)):
+        if value not in known:
+            raise KeyError(f"{name} must be one of {', '.join(map(repr, known))}, got {value!r}")
     pcode, code = _PATHS[path], DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
     if kind == "lora":
         p = LoraParams(m, n, k, GGML_TYPE_Q2_K, code, *key[6:], 0)

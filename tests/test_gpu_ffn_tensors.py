@@ -60,3 +60,20 @@ def test_tensors_without_memory_are_refused():
         w = torch.zeros(84 * 8, dtype=torch.uint8, device="cuda:0")
         with pytest.raises((q2k.InvalidArgument, RuntimeError)):
             q2k.gated_ffn(x, w, w, 8)
+
+
+def test_unknown_names_are_said():
+    n, k = 8, 256
+    w = dev(blocks(np.random.default_rng(83), n, k))
+    x = torch.zeros(2, k, device="cuda:0")
+    a, b = torch.zeros(1, 8, k, device="cuda:0").bfloat16(), torch.zeros(1, n, 8, device="cuda:0").bfloat16()
+    dh = torch.zeros(2, n, device="cuda:0").bfloat16()
+    with pytest.raises(KeyError, match="act must be one of 'silu', 'gelu', got 'relu'"):
+        q2k.gated_ffn(x, w, w, n, act="relu")
+    with pytest.raises(KeyError, match="act must be"):
+        q2k.gated_ffn_backward(dh, dh, dh, w, w, k, act="Gelu")
+    for call in (lambda: q2k.gated_ffn(x, w, w, n, path="fast"),
+                 lambda: q2k.matmul_lora(x, w, n, a, b, torch.zeros(2, dtype=torch.int32, device="cuda:0"),
+                                         path="fast")):
+        with pytest.raises(KeyError, match="path must be one of"):
+            call()
