@@ -278,9 +278,9 @@ __device__ __forceinline__ void block_product(const RowWords& a, const RowWords&
 // its largest would lose much of those: where more than a quarter of them are below
 // 2^-9 of it, what the rounding left goes through the same products as 22 bits more
 // (the block is `wide`; of 20 000 blocks of normal values none is, nor of silu(g) u
-// with g and u of deviation 1 or 1.5, and one in 40 at 4).  14336 x 4096: 13.5 us
-// without such blocks, 4 us more with one of the 16, 13 with all.  The products stand in a loop of their own: written beside
-// the ordinary ones they cost those 1 us.
+// with g and u of deviation 1 or 1.5, and one in 40 at 4).  14336 x 4096: 13.6 us
+// without such blocks, 4 us more with one of the 16, 13 with all.  These products
+// stand in a loop of their own: beside the ordinary ones they cost every call 1 us.
 struct XBytes {
     uint32_t x[4][3][4];  // shift, digit, quant word
     uint32_t s[4];
@@ -290,7 +290,7 @@ struct XBytes {
     __device__ __forceinline__ uint4 sums() const { return make_uint4(s[0], s[1], s[2], s[3]); }
 };
 constexpr int kXWords = 4 * (3 * 16 + 4);  // a block's, in shared memory
-constexpr float kRest = 0x1p-22f;          // a unit of the rest, in units of x
+constexpr float kRest = 0x1p-22f;          // the unit of the rest's integers, in x's
 // The same, left in shared memory.
 struct StoredXBytes {
     const uint4* at;
@@ -298,7 +298,7 @@ struct StoredXBytes {
     __device__ __forceinline__ uint4 sums() const { return at[12]; }
 };
 
-// Eight values as integers w, the rest (in units of kRest) in `rest`.
+// Eight values times `scale` as integers w, what their rounding left in `rest`.
 __device__ __forceinline__ void split_integers(const float (&v)[8], float scale, uint32_t (&w)[8],
                                                float (&rest)[8]) {
 #pragma unroll
