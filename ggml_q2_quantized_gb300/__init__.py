@@ -15,6 +15,7 @@ Names follow the mlx-native page "tests/deepseek_q2_k.rs": ``matmul`` is
 
 from __future__ import annotations
 
+import collections
 import ctypes
 import importlib.util
 import os
@@ -34,6 +35,7 @@ FLAG_INDEPENDENT = 2
 ID_SLOTTED = 1
 DTYPE_F32, DTYPE_BF16 = 0, 1
 ACT_SILU, ACT_GELU = 0, 1
+MOE_MAX_EXPERTS = 4096
 _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 _PATHS = {"auto": PATH_AUTO, "gemv": PATH_GEMV, "tensor": PATH_TENSOR,
           PATH_AUTO: PATH_AUTO, PATH_GEMV: PATH_GEMV, PATH_TENSOR: PATH_TENSOR}
@@ -99,6 +101,25 @@ class LoraParams(ctypes.Structure):
                 ("ggml_type", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
                 ("rank", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class MoeParams(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_uint32), ("top_k", ctypes.c_uint32),
+                ("n_experts", ctypes.c_uint32), ("width", ctypes.c_uint32),
+                ("dtype", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class Routes(collections.namedtuple("Routes", "rows order offsets")):
+    """What ``moe_route`` returns, int32 CUDA tensors: ``rows`` ``[n_tokens, top_k]``,
+    each choice's place in expert order; ``order`` ``[n_tokens * top_k]``, the choice
+    ``token * top_k + slot`` at each place; ``offsets`` ``[n_experts + 1]``, where each
+    expert's places begin and the last one's end (behind it: choices without one)."""
+
+    __slots__ = ()
+
+    @property
+    def n_experts(self) -> int:
+        return self.offsets.shape[0] - 1
 
 
 _lock = threading.Lock()
@@ -178,13 +199,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                         vp, sz, lop, vp, vp, sz, vp]
         lib.q2k_matmul_lora_workspace_bytes.argtypes = [ctypes.c_int, lop]
         lib.q2k_matmul_lora_workspace_bytes.restype = sz
+        mop = ctypes.POINTER(MoeParams)
+        lib.q2k_moe_route.argtypes = [vp, sz, vp, vp, vp, mop, vp, vp]
+        lib.q2k_moe_sort.argtypes = [vp, sz, vp, vp, vp, sz, mop, vp]
+        lib.q2k_moe_sort_backward.argtypes = lib.q2k_moe_sort.argtypes
+        lib.q2k_moe_combine.argtypes = [vp, sz, vp, vp, vp, vp, vp, sz, mop, vp]
+        lib.q2k_moe_combine_backward.argtypes = [vp, sz, vp, sz, vp, vp, vp, vp, vp, mop, vp]
         lib.q2k_device_error.argtypes = [u32p, vp]
         lib.q2k_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
         for fn in ("q2k_dequantize", "q2k_embedding_gather", "q2k_matmul", "q2k_matmul_path",
                    "q2k_matmul_ex", "q2k_matmul_ex_batch", "q2k_matmul_batched_mv", "q2k_matmul_id",
                    "q2k_matmul_id_slotted", "q2k_matmul_id_pair", "q2k_matmul_id_ex",
                    "q2k_matmul_id_pair_ex", "q2k_gated_ffn", "q2k_gated_ffn_backward",
-                   "q2k_matmul_lora", "q2k_device_error",
+                   "q2k_matmul_lora", "q2k_moe_route", "q2k_moe_sort", "q2k_moe_sort_backward",
+                   "q2k_moe_combine", "q2k_moe_combine_backward", "q2k_device_error",
                    "q2k_selftest_wait_timeout", "q2k_gguf_open", "q2k_gguf_tensor_info",
                    "q2k_gguf_read_tensor"):
             getattr(lib, fn).restype = ctypes.c_int
@@ -943,6 +971,132 @@ def _lora_result(out, bad, n_adapters, check):
     if n_bad:
         raise InvalidArgument(1, f"{n_bad} adapter id(s) outside -1..{n_adapters - 1}")
     return out
+
+
+def moe_route(ids, n_experts: int, check: bool = True):
+    """Where a router's choices land in expert order: ``Routes(rows, order, offsets)``.
+
+    ``ids`` int32 ``[n_tokens, top_k]``, each token's experts, -1 for none; the choices
+    of one expert keep their order, those without an expert come last.  With ``check``
+    the call waits and raises ``InvalidArgument`` if an id was neither -1 nor below
+    n_experts; with ``check=False`` it returns ``(routes, bad_id_count)`` without
+    waiting (such a choice has no expert).
+    """
+    torch = _torch_mod or _torch()
+    i32 = torch.int32
+    _require_cuda(ids, "ids", i32)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [n_tokens, top_k]")
+    if not 1 <= n_experts <= MOE_MAX_EXPERTS:
+        raise ValueError(f"n_experts must be in 1..{MOE_MAX_EXPERTS}, got {n_experts}")
+    n_tokens, top_k = ids.shape
+    choices = n_tokens * top_k
+    # (one buffer: each part starts at a whole 16 bytes)
+    part = (choices + 3) // 4 * 4
+    buf = torch.empty(2 * part + n_experts + 2, dtype=i32, device=ids.device)
+    rows, order = buf[:choices].view(n_tokens, top_k), buf[part:part + choices]
+    offsets, bad = buf[2 * part:2 * part + n_experts + 1], buf[2 * part + n_experts + 1:]
+    p = MoeParams(n_tokens, top_k, n_experts, 0, 0, 0)
+    lib = _lib if _lib is not None else load()
+    _ffn_call(ids.get_device(), lib.q2k_moe_route, ids.data_ptr(), choices, rows.data_ptr(),
+              order.data_ptr(), offsets.data_ptr(), ctypes.byref(p), bad.data_ptr())
+    routes = Routes(rows, order, offsets)
+    if not check:
+        return routes, bad
+    n_bad = int(bad.item())
+    if n_bad:
+        raise InvalidArgument(1, f"{n_bad} expert id(s) outside -1..{n_experts - 1}")
+    return routes
+
+
+def _moe_params(t, routes, name, rows_of):
+    """(params, rows, offsets) of a move whose activations ``t`` have a row for each
+    token (``rows_of`` "tokens") or each choice ("choices")."""
+    torch = _torch_mod or _torch()
+    _need_activations(t, name)
+    rows, _, offsets = routes
+    dev, i32 = t.get_device(), torch.int32
+    if not _fits(dev, i32, rows, offsets):
+        _need_like(t, rows=(i32, None, rows), offsets=(i32, None, offsets))
+    if rows.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("routes must hold rows [n_tokens, top_k] and offsets [n_experts + 1]")
+    n_tokens, top_k = rows.shape
+    first = n_tokens if rows_of == "tokens" else n_tokens * top_k
+    if t.dim() != 2 or t.shape[0] != first:
+        raise ValueError(f"{name} must be [{first}, width], got {list(t.shape)}")
+    code = DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+    return MoeParams(n_tokens, top_k, offsets.shape[0] - 1, t.shape[1], code, 0), rows, offsets
+
+
+def _moe_out(out, like, shape):
+    if out is None:
+        return _torch_mod.empty(shape, dtype=like.dtype, device=like.device)
+    _need_like(like, out=(like.dtype, shape, out))
+    return out
+
+
+def moe_sort(x, routes, out=None):
+    """The tokens' rows in expert order: ``xs[routes.rows[t, s]] = x[t]``.
+
+    ``x`` f32 or bf16 ``[n_tokens, width]``; returns ``[n_tokens * top_k, width]``, the
+    rows of expert e at ``routes.offsets[e]`` up to ``offsets[e + 1]``, ready for
+    ``linear`` and ``gated_ffn`` with ``routes``; rows behind the last are zeros.
+    """
+    p, rows, offsets = _moe_params(x, routes, "x", "tokens")
+    out = _moe_out(out, x, (p.n_tokens * p.top_k, p.width))
+    lib = _lib if _lib is not None else load()
+    _ffn_call(x.get_device(), lib.q2k_moe_sort, x.data_ptr(), x.numel(), rows.data_ptr(),
+              offsets.data_ptr(), out.data_ptr(), out.numel(), ctypes.byref(p))
+    return out
+
+
+def moe_sort_backward(dxs, routes, out=None):
+    """The gradient of ``moe_sort``'s x from that of its result: ``dx[t]``, the sum of
+    ``dxs[routes.rows[t, s]]`` over the token's choices that have an expert."""
+    p, rows, offsets = _moe_params(dxs, routes, "dxs", "choices")
+    out = _moe_out(out, dxs, (p.n_tokens, p.width))
+    lib = _lib if _lib is not None else load()
+    _ffn_call(dxs.get_device(), lib.q2k_moe_sort_backward, dxs.data_ptr(), dxs.numel(),
+              rows.data_ptr(), offsets.data_ptr(), out.data_ptr(), out.numel(), ctypes.byref(p))
+    return out
+
+
+def moe_combine(ys, routes, weights=None, residual=None, out=None):
+    """The experts' rows back to their tokens: ``y[t] = residual[t] + sum_s weights[t, s]
+    ys[routes.rows[t, s]]`` over the choices that have an expert.
+
+    ``ys`` f32 or bf16 ``[n_tokens * top_k, width]``; ``weights`` f32 ``[n_tokens,
+    top_k]`` or None (all 1); ``residual`` ``[n_tokens, width]`` in ys' dtype or None.
+    """
+    torch = _torch_mod or _torch()
+    p, rows, offsets = _moe_params(ys, routes, "ys", "choices")
+    if weights is not None:
+        _need_like(ys, weights=(torch.float32, rows.shape, weights))
+    if residual is not None:
+        _need_like(ys, residual=(ys.dtype, (p.n_tokens, p.width), residual))
+    out = _moe_out(out, ys, (p.n_tokens, p.width))
+    lib = _lib if _lib is not None else load()
+    _ffn_call(ys.get_device(), lib.q2k_moe_combine, ys.data_ptr(), ys.numel(), rows.data_ptr(),
+              offsets.data_ptr(), weights.data_ptr() if weights is not None else None,
+              residual.data_ptr() if residual is not None else None, out.data_ptr(), out.numel(),
+              ctypes.byref(p))
+    return out
+
+
+def moe_combine_backward(dy, ys, routes, weights):
+    """The gradients of ``moe_combine``: ``(dys, dweights)`` from that of y.  ``dys`` as
+    ``ys`` (zeros in rows without an expert), ``dweights`` f32 as ``weights``.  The
+    residual's gradient is ``dy``."""
+    torch = _torch_mod or _torch()
+    p, rows, offsets = _moe_params(ys, routes, "ys", "choices")
+    _need_like(ys, dy=(ys.dtype, (p.n_tokens, p.width), dy),
+               weights=(torch.float32, rows.shape, weights))
+    dys, dweights = torch.empty_like(ys), torch.empty_like(weights)
+    lib = _lib if _lib is not None else load()
+    _ffn_call(ys.get_device(), lib.q2k_moe_combine_backward, dy.data_ptr(), dy.numel(),
+              ys.data_ptr(), ys.numel(), rows.data_ptr(), offsets.data_ptr(), weights.data_ptr(),
+              dys.data_ptr(), dweights.data_ptr(), ctypes.byref(p))
+    return dys, dweights
 
 
 class GgufFile:

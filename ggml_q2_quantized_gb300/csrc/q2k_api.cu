@@ -1281,3 +1281,201 @@ q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void* x, size_t 
 }
 
 }  // extern "C"
+
+// ---- tokens to their experts and back -----------------------------------------------
+
+static_assert(Q2K_MOE_MAX_EXPERTS == q2k::kMoeMaxExperts, "header and library disagree");
+static_assert(sizeof(q2k_moe_params) == 24, "q2k_moe_params layout");
+
+namespace {
+
+struct MoeShape {
+    size_t routes, in, out;  // choices; elements of [n_tokens, width] and of [routes, width]
+    size_t elem;
+};
+
+// rows_only: q2k_moe_route, which moves no rows.
+q2k_status check_moe(const q2k_moe_params* p, bool rows_only, MoeShape* s) {
+    if (p == nullptr) return fail(Q2K_ERR_INVALID_ARGUMENT, "params is NULL");
+    if (p->n_tokens == 0 || p->n_tokens > Q2K_FFN_MAX_TOKENS)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "n_tokens must be in 1..%d, got %u", Q2K_FFN_MAX_TOKENS,
+                    p->n_tokens);
+    if (p->top_k == 0 || p->top_k > Q2K_MOE_MAX_TOP_K)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "top_k must be in 1..%d, got %u", Q2K_MOE_MAX_TOP_K, p->top_k);
+    if (p->n_experts == 0 || p->n_experts > Q2K_MOE_MAX_EXPERTS)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "n_experts must be in 1..%d, got %u", Q2K_MOE_MAX_EXPERTS,
+                    p->n_experts);
+    if (p->reserved != 0) return fail(Q2K_ERR_INVALID_ARGUMENT, "reserved must be 0");
+    // (routes <= 2^28, and times width <= 2^48)
+    s->routes = static_cast<size_t>(p->n_tokens) * p->top_k;
+    s->in = s->out = s->elem = 0;
+    if (rows_only) return Q2K_OK;
+    if (p->width == 0 || p->width > Q2K_FFN_MAX_WIDTH)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "width must be in 1..%d, got %u", Q2K_FFN_MAX_WIDTH, p->width);
+    if (p->dtype != Q2K_DTYPE_F32 && p->dtype != Q2K_DTYPE_BF16)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown dtype %u", p->dtype);
+    s->in = static_cast<size_t>(p->n_tokens) * p->width;
+    s->out = s->routes * p->width;
+    s->elem = p->dtype == Q2K_DTYPE_F32 ? 4 : 2;
+    return Q2K_OK;
+}
+
+// Sort (narrow -> wide), its gradient and combine (wide -> narrow).
+q2k_status moe_move(const char* what, bool combine, const char* in_name, const void* in, size_t in_elems,
+                    const int32_t* rows, const int32_t* offsets, const float* weights,
+                    const void* residual, const char* out_name, void* out, size_t out_elems,
+                    const q2k_moe_params* p, q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    MoeShape s;
+    q2k_status st = check_moe(p, false, &s);
+    if (st != Q2K_OK) return st;
+    if (in == nullptr || rows == nullptr || offsets == nullptr || out == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "%s, rows, offsets and %s must be non-NULL", in_name, out_name);
+    const size_t in_want = combine ? s.out : s.in, out_want = combine ? s.in : s.out;
+    if ((st = check_elems(in_name, in_elems, in_want)) != Q2K_OK ||
+        (st = check_elems(out_name, out_elems, out_want)) != Q2K_OK)
+        return st;
+    if (!aligned(in, s.elem) || !aligned(out, s.elem) || !aligned(residual, s.elem))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "%s and %s must be aligned to their elements", in_name, out_name);
+    if (!aligned(rows, 4) || !aligned(offsets, 4) || !aligned(weights, 4))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "rows, offsets and weights must be 4-byte aligned");
+    const Span outs[] = {{out, out_want * s.elem, out_name}};
+    const Span ins[] = {{in, in_want * s.elem, in_name},
+                        {rows, s.routes * 4, "rows"},
+                        {offsets, (size_t(p->n_experts) + 1) * 4, "offsets"},
+                        {weights, weights != nullptr ? s.routes * 4 : 0, "weights"},
+                        {residual, residual != nullptr ? s.in * s.elem : 0, "residual"}};
+    if ((st = check_disjoint(outs, 1, ins, 5)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    q2k::MoeMoveArgs a = {};
+    a.in = in;
+    a.residual = residual;
+    a.weights = weights;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.out = out;
+    a.n_tokens = static_cast<int>(p->n_tokens);
+    a.top_k = static_cast<int>(p->top_k);
+    a.n_experts = static_cast<int>(p->n_experts);
+    a.width = static_cast<int>(p->width);
+    a.bf16 = p->dtype == Q2K_DTYPE_BF16;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = combine ? q2k::launch_moe_combine(a, cs) : q2k::launch_moe_sort(a, cs);
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, what);
+}
+
+}  // namespace
+
+extern "C" {
+
+q2k_status q2k_moe_route(const int32_t* ids, size_t n_ids, int32_t* rows, int32_t* order,
+                         int32_t* offsets, const q2k_moe_params* p, uint32_t* bad_id_count,
+                         q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    MoeShape s;
+    q2k_status st = check_moe(p, true, &s);
+    if (st != Q2K_OK) return st;
+    if (ids == nullptr || rows == nullptr || order == nullptr || offsets == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "ids, rows, order and offsets must be non-NULL");
+    if ((st = check_elems("ids", n_ids, s.routes)) != Q2K_OK) return st;
+    if (!aligned(ids, 4) || !aligned(rows, 4) || !aligned(order, 4) || !aligned(offsets, 4) ||
+        !aligned(bad_id_count, 4))
+        return fail(Q2K_ERR_INVALID_ARGUMENT,
+                    "ids, rows, order, offsets and bad_id_count must be 4-byte aligned");
+    const Span outs[] = {{rows, s.routes * 4, "rows"},
+                         {order, s.routes * 4, "order"},
+                         {offsets, (size_t(p->n_experts) + 1) * 4, "offsets"},
+                         {bad_id_count, bad_id_count != nullptr ? size_t(4) : 0, "bad_id_count"}};
+    const Span ins[] = {{ids, s.routes * 4, "ids"}};
+    if ((st = check_disjoint(outs, 4, ins, 1)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    unsigned int* word = nullptr;
+    int slot = -1;
+    if (bad_id_count == nullptr && (st = acquire_status_word(dev.device, cs, &word, &slot)) != Q2K_OK)
+        return st;
+    q2k::MoeRouteArgs a = {};
+    a.ids = ids;
+    a.rows = rows;
+    a.order = order;
+    a.offsets = offsets;
+    a.bad_ids = bad_id_count != nullptr ? bad_id_count : word;
+    a.n_tokens = static_cast<int>(p->n_tokens);
+    a.top_k = static_cast<int>(p->top_k);
+    a.n_experts = static_cast<int>(p->n_experts);
+    a.device = dev.device;
+    const cudaError_t e = q2k::launch_moe_route(a, cs);
+    if (word != nullptr)
+        return finish_status_word(dev.device, slot, word, cs, e, "q2k_moe_route", "n_experts", p->n_experts);
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_moe_route launch");
+}
+
+q2k_status q2k_moe_sort(const void* x, size_t x_elems, const int32_t* rows, const int32_t* offsets,
+                        void* xs, size_t xs_elems, const q2k_moe_params* p, q2k_stream_t stream) {
+    return moe_move("q2k_moe_sort launch", false, "x", x, x_elems, rows, offsets, nullptr, nullptr, "xs", xs,
+                    xs_elems, p, stream);
+}
+
+q2k_status q2k_moe_sort_backward(const void* dxs, size_t xs_elems, const int32_t* rows,
+                                 const int32_t* offsets, void* dx, size_t x_elems,
+                                 const q2k_moe_params* p, q2k_stream_t stream) {
+    return moe_move("q2k_moe_sort_backward launch", true, "dxs", dxs, xs_elems, rows, offsets, nullptr,
+                    nullptr, "dx", dx, x_elems, p, stream);
+}
+
+q2k_status q2k_moe_combine(const void* ys, size_t ys_elems, const int32_t* rows, const int32_t* offsets,
+                           const float* weights, const void* residual, void* y, size_t y_elems,
+                           const q2k_moe_params* p, q2k_stream_t stream) {
+    return moe_move("q2k_moe_combine launch", true, "ys", ys, ys_elems, rows, offsets, weights, residual, "y",
+                    y, y_elems, p, stream);
+}
+
+q2k_status q2k_moe_combine_backward(const void* dy, size_t dy_elems, const void* ys, size_t ys_elems,
+                                    const int32_t* rows, const int32_t* offsets, const float* weights,
+                                    void* dys, float* dweights, const q2k_moe_params* p,
+                                    q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    MoeShape s;
+    q2k_status st = check_moe(p, false, &s);
+    if (st != Q2K_OK) return st;
+    if (dy == nullptr || ys == nullptr || rows == nullptr || offsets == nullptr || weights == nullptr ||
+        dys == nullptr || dweights == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT,
+                    "dy, ys, rows, offsets, weights, dys and dweights must be non-NULL");
+    if ((st = check_elems("dy", dy_elems, s.in)) != Q2K_OK ||
+        (st = check_elems("ys", ys_elems, s.out)) != Q2K_OK)
+        return st;
+    if (!aligned(dy, s.elem) || !aligned(ys, s.elem) || !aligned(dys, s.elem))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "dy, ys and dys must be aligned to their elements");
+    if (!aligned(rows, 4) || !aligned(offsets, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "rows, offsets, weights and dweights must be 4-byte aligned");
+    const Span outs[] = {{dys, s.out * s.elem, "dys"}, {dweights, s.routes * 4, "dweights"}};
+    const Span ins[] = {{dy, s.in * s.elem, "dy"},
+                        {ys, s.out * s.elem, "ys"},
+                        {rows, s.routes * 4, "rows"},
+                        {offsets, (size_t(p->n_experts) + 1) * 4, "offsets"},
+                        {weights, s.routes * 4, "weights"}};
+    if ((st = check_disjoint(outs, 2, ins, 5)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    q2k::MoeBackArgs a = {};
+    a.dy = dy;
+    a.ys = ys;
+    a.weights = weights;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.dys = dys;
+    a.dweights = dweights;
+    a.n_tokens = static_cast<int>(p->n_tokens);
+    a.top_k = static_cast<int>(p->top_k);
+    a.n_experts = static_cast<int>(p->n_experts);
+    a.width = static_cast<int>(p->width);
+    a.bf16 = p->dtype == Q2K_DTYPE_BF16;
+    a.sm_count = dev.sm_count;
+    const cudaError_t e = q2k::launch_moe_combine_backward(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_moe_combine_backward launch");
+}
+
+}  // extern "C"

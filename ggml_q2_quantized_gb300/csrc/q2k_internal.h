@@ -241,4 +241,48 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, c
 cudaError_t ffn_error_word(int device, unsigned int** word);
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream);
 
+// ---- tokens to their experts and back (q2k_moe.cu) ----------------------------
+
+// The most experts of a call (a count for each, per warp, in shared memory).
+constexpr int kMoeMaxExperts = 4096;
+
+struct MoeRouteArgs {
+    const int* ids;   // [n_tokens, top_k]
+    int* rows;        // [n_tokens, top_k]
+    int* order;       // [n_tokens * top_k]
+    int* offsets;     // [n_experts + 1]
+    unsigned int* bad_ids;  // written, not added to
+    int n_tokens, top_k, n_experts;
+    int device;
+};
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream);
+
+// sort: in [n_tokens, width] -> out [n_tokens * top_k, width]; combine: the other way.
+struct MoeMoveArgs {
+    const void* in;
+    const void* residual;  // combine: [n_tokens, width] or null
+    const float* weights;  // combine: [n_tokens, top_k] or null (all 1)
+    const int* rows;
+    const int* offsets;
+    void* out;
+    int n_tokens, top_k, n_experts, width;
+    bool bf16;
+};
+cudaError_t launch_moe_sort(const MoeMoveArgs& a, cudaStream_t stream);
+cudaError_t launch_moe_combine(const MoeMoveArgs& a, cudaStream_t stream);
+
+struct MoeBackArgs {
+    const void* dy;
+    const void* ys;
+    const float* weights;
+    const int* rows;
+    const int* offsets;
+    void* dys;
+    float* dweights;
+    int n_tokens, top_k, n_experts, width;
+    bool bf16;
+    int sm_count;
+};
+cudaError_t launch_moe_combine_backward(const MoeBackArgs& a, cudaStream_t stream);
+
 }  // namespace q2k

@@ -623,6 +623,85 @@ q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void *x, size_t 
                            void *workspace, size_t workspace_bytes, q2k_stream_t stream);
 size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *params);
 
+/* ---- tokens to their experts and back --------------------------------------
+ * The parts of a mixture-of-experts layer around the experts' products: which
+ * place each of a router's choices has in expert order, the tokens' rows moved
+ * there, and the experts' rows brought back to their tokens, each with its
+ * gradient.  Activations are f32 or bf16 (params.dtype, one type for all of a
+ * call's), contiguous rows of `width`, aligned to their element (16-byte aligned
+ * rows are the fast ones); sums are f32, in the order of the slots, rounded once.
+ * Calls are asynchronous on `stream`, allocate nothing, take no workspace and may
+ * be captured; the same inputs give the same bits.
+ *
+ * Choice i = token * top_k + slot.  `rows` (i32 [n_tokens, top_k]) is each
+ * choice's place, `offsets` (i32 [n_experts + 1]) where each expert's places
+ * begin and the last one's end: q2k_moe_route writes them.  Choices without an
+ * expert have the places from offsets[n_experts] on, which these calls write as
+ * zeros and never read.  The other calls take any `rows` and `offsets`: a place
+ * outside 0 .. n_tokens * top_k - 1 is neither read nor written. */
+enum {
+    Q2K_MOE_MAX_TOP_K = 256,
+    Q2K_MOE_MAX_EXPERTS = 4096
+};
+
+typedef struct q2k_moe_params {
+    uint32_t n_tokens;  /* 1..Q2K_FFN_MAX_TOKENS */
+    uint32_t top_k;     /* choices of a token, 1..Q2K_MOE_MAX_TOP_K */
+    uint32_t n_experts; /* 1..Q2K_MOE_MAX_EXPERTS */
+    uint32_t width;     /* values of a row, 1..Q2K_FFN_MAX_WIDTH (q2k_moe_route: not read) */
+    uint32_t dtype;     /* q2k_dtype (q2k_moe_route: not read) */
+    uint32_t reserved;  /* must be 0 */
+} q2k_moe_params;
+
+/* q2k_moe_route - the places of a router's choices, ordered by expert; those of one
+ * expert keep their order.
+ *   ids       device i32 [n_tokens, top_k]; -1: no expert
+ *   rows      device i32 [n_tokens, top_k]: each choice's place
+ *   order     device i32 [n_tokens * top_k]: the choice at each place (its token is
+ *             order / top_k)
+ *   offsets   device i32 [n_experts + 1]
+ *   bad_id_count  device u32 or NULL, as q2k_embedding_gather's: an id that is
+ *             neither -1 nor below n_experts has no expert, and is counted. */
+q2k_status q2k_moe_route(const int32_t *ids, size_t n_ids, int32_t *rows, int32_t *order,
+                         int32_t *offsets, const q2k_moe_params *params,
+                         uint32_t *bad_id_count, q2k_stream_t stream);
+
+/* q2k_moe_sort - xs[rows[t, s]] = x[t].
+ *   x   [n_tokens, width]
+ *   xs  [n_tokens * top_k, width]; fully overwritten (with the `rows` of a route) */
+q2k_status q2k_moe_sort(const void *x, size_t x_elems, const int32_t *rows,
+                        const int32_t *offsets, void *xs, size_t xs_elems,
+                        const q2k_moe_params *params, q2k_stream_t stream);
+
+/* q2k_moe_sort_backward - dx[t] = sum over its choices with an expert of
+ * dxs[rows[t, s]]. */
+q2k_status q2k_moe_sort_backward(const void *dxs, size_t xs_elems, const int32_t *rows,
+                                 const int32_t *offsets, void *dx, size_t x_elems,
+                                 const q2k_moe_params *params, q2k_stream_t stream);
+
+/* q2k_moe_combine - y[t] = residual[t] + sum over its choices with an expert of
+ * weights[t, s] ys[rows[t, s]].
+ *   ys        [n_tokens * top_k, width]
+ *   weights   device f32 [n_tokens, top_k], or NULL (all 1)
+ *   residual  [n_tokens, width], or NULL (zeros)
+ *   y         [n_tokens, width]; fully overwritten */
+q2k_status q2k_moe_combine(const void *ys, size_t ys_elems, const int32_t *rows,
+                           const int32_t *offsets, const float *weights, const void *residual,
+                           void *y, size_t y_elems, const q2k_moe_params *params,
+                           q2k_stream_t stream);
+
+/* q2k_moe_combine_backward - dys[rows[t, s]] = weights[t, s] dy[t] and dweights[t, s]
+ * = sum over the row of dy[t] ys[rows[t, s]] (0 for a choice without an expert).  The
+ * residual's gradient is dy.
+ *   dy        [n_tokens, width]
+ *   dys       [n_tokens * top_k, width]; fully overwritten (with the `rows` of a route)
+ *   dweights  device f32 [n_tokens, top_k] */
+q2k_status q2k_moe_combine_backward(const void *dy, size_t dy_elems, const void *ys,
+                                    size_t ys_elems, const int32_t *rows,
+                                    const int32_t *offsets, const float *weights, void *dys,
+                                    float *dweights, const q2k_moe_params *params,
+                                    q2k_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
