@@ -34,9 +34,10 @@ FLAG_CONST_WEIGHTS = 1
 FLAG_INDEPENDENT = 2
 ID_SLOTTED = 1
 DTYPE_F32, DTYPE_BF16 = 0, 1
-ACT_SILU, ACT_GELU = 0, 1
+ACT_SILU, ACT_GELU, ACT_NONE = 0, 1, 2
 MOE_MAX_EXPERTS = 4096
 _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
+_LINEAR_ACTS = {**_ACTS, None: ACT_NONE}
 _PATHS = {"auto": PATH_AUTO, "gemv": PATH_GEMV, "tensor": PATH_TENSOR,
           PATH_AUTO: PATH_AUTO, PATH_GEMV: PATH_GEMV, PATH_TENSOR: PATH_TENSOR}
 
@@ -100,6 +101,13 @@ class LoraParams(ctypes.Structure):
     _fields_ = [("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("k", ctypes.c_uint32),
                 ("ggml_type", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
                 ("rank", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class LinearParams(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("k", ctypes.c_uint32),
+                ("ggml_type", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("act", ctypes.c_uint32), ("n_experts", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
 
 
@@ -199,6 +207,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                         vp, sz, lop, vp, vp, sz, vp]
         lib.q2k_matmul_lora_workspace_bytes.argtypes = [ctypes.c_int, lop]
         lib.q2k_matmul_lora_workspace_bytes.restype = sz
+        lib.q2k_gated_ffn_experts.argtypes = [ctypes.c_int, u32, vp, sz, vp, sz, vp, sz, vp, sz, vp,
+                                              vp, vp, u32, gfp, vp, sz, vp]
+        lib.q2k_gated_ffn_experts_workspace_bytes.argtypes = [ctypes.c_int, gfp, u32]
+        lib.q2k_gated_ffn_experts_workspace_bytes.restype = sz
+        lib.q2k_gated_ffn_experts_backward.argtypes = [vp, vp, vp, sz, vp, sz, vp, sz, vp, sz, vp,
+                                                       vp, vp, u32, gfp, vp, sz, vp]
+        lib.q2k_gated_ffn_experts_backward_workspace_bytes.argtypes = [gfp, u32]
+        lib.q2k_gated_ffn_experts_backward_workspace_bytes.restype = sz
+        lip = ctypes.POINTER(LinearParams)
+        lib.q2k_linear.argtypes = [ctypes.c_int, u32, vp, sz, vp, sz, vp, vp, vp, sz, vp, vp, lip, vp,
+                                   sz, vp]
+        lib.q2k_linear_workspace_bytes.argtypes = [ctypes.c_int, lip]
+        lib.q2k_linear_workspace_bytes.restype = sz
+        lib.q2k_linear_backward.argtypes = [vp, sz, vp, vp, sz, vp, sz, vp, vp, vp, lip, vp, sz, vp]
+        lib.q2k_linear_backward_workspace_bytes.argtypes = [lip]
+        lib.q2k_linear_backward_workspace_bytes.restype = sz
         mop = ctypes.POINTER(MoeParams)
         lib.q2k_moe_route.argtypes = [vp, sz, vp, vp, vp, mop, vp, vp]
         lib.q2k_moe_sort.argtypes = [vp, sz, vp, vp, vp, sz, mop, vp]
@@ -211,7 +235,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
                    "q2k_matmul_ex", "q2k_matmul_ex_batch", "q2k_matmul_batched_mv", "q2k_matmul_id",
                    "q2k_matmul_id_slotted", "q2k_matmul_id_pair", "q2k_matmul_id_ex",
                    "q2k_matmul_id_pair_ex", "q2k_gated_ffn", "q2k_gated_ffn_backward",
-                   "q2k_matmul_lora", "q2k_moe_route", "q2k_moe_sort", "q2k_moe_sort_backward",
+                   "q2k_gated_ffn_experts", "q2k_gated_ffn_experts_backward", "q2k_linear",
+                   "q2k_linear_backward", "q2k_matmul_lora", "q2k_moe_route", "q2k_moe_sort", "q2k_moe_sort_backward",
                    "q2k_moe_combine", "q2k_moe_combine_backward", "q2k_device_error",
                    "q2k_selftest_wait_timeout", "q2k_gguf_open", "q2k_gguf_tensor_info",
                    "q2k_gguf_read_tensor"):
@@ -751,26 +776,49 @@ _ffn_plans: dict = {}
 
 
 def _ffn_plan(key):
-    """``key``: (kind, path, dtype, m, n, k, act) or ("lora", path, dtype, m, n, k,
-    rank, n_adapters)."""
+    """``key``: (kind, path, dtype, m, n, k, act, n_experts), kind "gated", "backward",
+    "linear" or "linear_backward", or ("lora", path, dtype, m, n, k, rank, n_adapters)."""
     lib, torch = load(), _torch()
     kind, path, dtype, m, n, k = key[:6]
-    for name, value, known in (("path", path, _PATHS), ("act", "silu" if kind == "lora" else key[6], _ACTS)):
+    acts = _LINEAR_ACTS if kind.startswith("linear") else _ACTS
+    for name, value, known in (("path", path, _PATHS), ("act", "silu" if kind == "lora" else key[6], acts)):
         if value not in known:
             raise KeyError(f"{name} must be one of {', '.join(map(repr, known))}, got {value!r}")
     pcode, code = _PATHS[path], DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
     if kind == "lora":
         p = LoraParams(m, n, k, GGML_TYPE_Q2_K, code, *key[6:], 0)
         need = lib.q2k_matmul_lora_workspace_bytes(pcode, ctypes.byref(p))
+    elif kind.startswith("linear"):
+        p = LinearParams(m, n, k, GGML_TYPE_Q2_K, code, acts[key[6]], key[7], 0)
+        need = (lib.q2k_linear_backward_workspace_bytes(ctypes.byref(p))
+                if kind == "linear_backward"
+                else lib.q2k_linear_workspace_bytes(pcode, ctypes.byref(p)))
     else:
         p = GatedFfnParams(m, n, k, GGML_TYPE_Q2_K, code, _ACTS[key[6]])
-        need = (lib.q2k_gated_ffn_backward_workspace_bytes(ctypes.byref(p))
-                if kind == "backward"
-                else lib.q2k_gated_ffn_workspace_bytes(pcode, ctypes.byref(p)))
+        experts = key[7]
+        if kind == "backward":
+            need = (lib.q2k_gated_ffn_experts_backward_workspace_bytes(ctypes.byref(p), experts)
+                    if experts else lib.q2k_gated_ffn_backward_workspace_bytes(ctypes.byref(p)))
+        else:
+            need = (lib.q2k_gated_ffn_experts_workspace_bytes(pcode, ctypes.byref(p), experts)
+                    if experts else lib.q2k_gated_ffn_workspace_bytes(pcode, ctypes.byref(p)))
     if len(_ffn_plans) >= 4096:  # (geometries, not tensors: a bound for long runs)
         _ffn_plans.clear()
     plan = _ffn_plans[key] = (ctypes.byref(p), need, pcode)
     return plan
+
+
+def _segments(x, routes):
+    """(pointer of the offsets or None, n_experts or 0) of a call's tokens."""
+    if routes is None:
+        return None, 0
+    torch = _torch_mod or _torch()
+    offsets = routes.offsets
+    if not _fits(x.get_device(), torch.int32, offsets):
+        _need_like(x, offsets=(torch.int32, None, offsets))
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("routes.offsets must be [n_experts + 1]")
+    return offsets.data_ptr(), offsets.shape[0] - 1
 
 
 def _ffn_workspace(workspace, need, x):
@@ -828,7 +876,7 @@ def _quick():
 
 
 def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None, path="auto",
-              const_weights: bool = False, workspace="auto"):
+              const_weights: bool = False, workspace="auto", routes=None):
     """The gated feed-forward block ``h = act(x Wg^T) * (x Wu^T)``: both
     projections, the activation and the product in one kernel.
 
@@ -840,8 +888,14 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     are exact, above that x and W are rounded to bf16 for the tensor cores.
     Nothing is recorded for autograd: h does not require a gradient, even where
     x does.
+
+    ``routes`` (of ``moe_route``): x holds rows in expert order, as ``moe_sort`` makes
+    them, and each row is multiplied by its own expert's matrices; ``w_gate`` and
+    ``w_up`` then hold ``n_experts`` matrices each, one after another.  Rows behind the
+    last expert's are not read, and their results not written.  The weights are exact
+    up to four bf16 or two f32 tokens for each expert.
     """
-    if out is None and workspace.__class__ is str:
+    if routes is None and out is None and workspace.__class__ is str:
         quick = _quick_mod or _quick()
         done = (quick.gated(x, w_gate, w_up, n, act, save, path, const_weights)
                 if quick else None)
@@ -863,24 +917,29 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
         _need_like(x, out=(dt, (m, n), out))
     gate = torch.empty_like(out) if save else None
     up = torch.empty_like(out) if save else None
-    key = ("gated", path, dt, m, n, k, act)
+    segments = _segments(x, routes)
+    key = ("gated", path, dt, m, n, k, act, segments[1])
     params, need, pcode = _ffn_plans.get(key) or _ffn_plan(key)
     _keep, ws, ws_bytes = _ffn_workspace(workspace, need, x)
-    _ffn_call(dev, _lib.q2k_gated_ffn, pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
+    fn, where = ((_lib.q2k_gated_ffn, ()) if routes is None
+                 else (_lib.q2k_gated_ffn_experts, segments))
+    _ffn_call(dev, fn, pcode, FLAG_CONST_WEIGHTS if const_weights else 0,
               x.data_ptr(), m * k, w_gate.data_ptr(), w_gate.numel(), w_up.data_ptr(),
               w_up.numel(), out.data_ptr(), m * n, gate.data_ptr() if save else None,
-              up.data_ptr() if save else None, params, ws, ws_bytes)
+              up.data_ptr() if save else None, *where, params, ws, ws_bytes)
     return (out, gate, up) if save else out
 
 
-def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace="auto"):
+def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace="auto",
+                       routes=None):
     """The backward pass of ``gated_ffn`` with its weights frozen, bf16 only.
 
     ``dh``, ``gate``, ``up`` bf16 ``[m, n]`` (the gradient of h and the saved
     projections); returns ``(dx, dgate, dup)``: ``dx = dgate Wg + dup Wu``
-    ``[m, k]`` and the gradients ``[m, n]`` of the two projections.
+    ``[m, k]`` and the gradients ``[m, n]`` of the two projections.  ``routes`` as in
+    ``gated_ffn``.
     """
-    if workspace.__class__ is str:
+    if routes is None and workspace.__class__ is str:
         quick = _quick_mod or _quick()
         done = quick.backward(dh, gate, up, w_gate, w_up, k, act) if quick else None
         if done.__class__ is int:
@@ -900,13 +959,94 @@ def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace
                    w_gate=(u8, None, w_gate), w_up=(u8, None, w_up))
     dx = torch.empty((m, k), dtype=bf16, device=dh.device)
     dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
-    key = ("backward", "auto", bf16, m, n, k, act)
+    segments = _segments(dh, routes)
+    key = ("backward", "auto", bf16, m, n, k, act, segments[1])
     params, need, _ = _ffn_plans.get(key) or _ffn_plan(key)
     _keep, ws, ws_bytes = _ffn_workspace(workspace, need, dh)
-    _ffn_call(dev, _lib.q2k_gated_ffn_backward, dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
+    fn, where = ((_lib.q2k_gated_ffn_backward, ()) if routes is None
+                 else (_lib.q2k_gated_ffn_experts_backward, segments))
+    _ffn_call(dev, fn, dh.data_ptr(), gate.data_ptr(), up.data_ptr(),
               m * n, w_gate.data_ptr(), w_gate.numel(), w_up.data_ptr(), w_up.numel(),
-              dx.data_ptr(), m * k, dgate.data_ptr(), dup.data_ptr(), params, ws, ws_bytes)
+              dx.data_ptr(), m * k, dgate.data_ptr(), dup.data_ptr(), *where, params, ws, ws_bytes)
     return dx, dgate, dup
+
+
+def linear(x, w, n: int, bias=None, act=None, residual=None, save: bool = False, out=None,
+           path="auto", const_weights: bool = False, workspace="auto", routes=None):
+    """A projection with its epilogue: ``y = act(x W^T + bias) + residual`` in one kernel.
+
+    ``x`` f32 or bf16 ``[m, k]``; ``w`` uint8, ``n`` rows of Q2_K blocks; ``bias`` f32
+    ``[n]`` or None; ``act`` None, "silu" or "gelu" (the tanh form); ``residual`` ``[m,
+    n]`` in x's dtype or None.  Returns y ``[m, n]`` in x's dtype, or with ``save`` ``(y,
+    z)`` with ``z = x W^T + bias``, which ``linear_backward`` reads.  ``path``,
+    ``const_weights`` and ``workspace`` as in ``gated_ffn``; nothing is recorded for
+    autograd.  ``routes`` as in ``gated_ffn``: ``w`` then holds ``n_experts`` matrices
+    and ``bias`` is ``[n_experts, n]``.
+    """
+    torch = _torch_mod or _torch()
+    _need_activations(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [m, k]")
+    m, k = x.shape
+    dt, dev = x.dtype, x.get_device()
+    if not _fits(dev, torch.uint8, w):
+        _need_like(x, w=(torch.uint8, None, w))
+    offsets, experts = _segments(x, routes)
+    if bias is not None:
+        _need_like(x, bias=(torch.float32, (experts, n) if experts else (n,), bias))
+    if residual is not None:
+        _need_like(x, residual=(dt, (m, n), residual))
+    if out is None:
+        out = torch.empty((m, n), dtype=dt, device=x.device)
+    else:
+        _need_like(x, out=(dt, (m, n), out))
+    z = torch.empty_like(out) if save else None
+    key = ("linear", path, dt, m, n, k, act, experts)
+    params, need, pcode = _ffn_plans.get(key) or _ffn_plan(key)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, need, x)
+    _ffn_call(dev, _lib.q2k_linear, pcode, FLAG_CONST_WEIGHTS if const_weights else 0, x.data_ptr(),
+              m * k, w.data_ptr(), w.numel(), bias.data_ptr() if bias is not None else None,
+              residual.data_ptr() if residual is not None else None, out.data_ptr(), m * n,
+              z.data_ptr() if save else None, offsets, params, ws, ws_bytes)
+    return (out, z) if save else out
+
+
+def linear_backward(dy, w, k: int, z=None, act=None, bias: bool = False, workspace="auto",
+                    routes=None):
+    """The backward pass of ``linear`` with its weights frozen, bf16 only.
+
+    ``dy`` bf16 ``[m, n]``; ``z`` the saved ``[m, n]``, read where there is an
+    activation.  Returns ``(dx, dz, dbias)``: ``dx = dz W`` ``[m, k]``, ``dz = dy
+    act'(z)`` (without an activation ``dy`` itself) and with ``bias`` the sum of dz over
+    the tokens, f32 ``[n]`` (with ``routes`` over each expert's, ``[n_experts, n]``), else
+    None.  The residual's gradient is ``dy``.  ``routes`` as in ``gated_ffn``.
+    """
+    torch = _torch_mod or _torch()
+    bf16 = torch.bfloat16
+    _need_activations(dy, "dy", bf16)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [m, n]")
+    m, n = dy.shape
+    dev = dy.get_device()
+    if not _fits(dev, torch.uint8, w):
+        _need_like(dy, w=(torch.uint8, None, w))
+    if act is None:
+        z = None
+    else:
+        _need_like(dy, z=(bf16, (m, n), z))
+    offsets, experts = _segments(dy, routes)
+    dx = torch.empty((m, k), dtype=bf16, device=dy.device)
+    dz = dy if act is None else torch.empty_like(dy)
+    dbias = (torch.empty((experts, n) if experts else (n,), dtype=torch.float32, device=dy.device)
+             if bias else None)
+    key = ("linear_backward", "auto", bf16, m, n, k, act, experts)
+    params, need, _ = _ffn_plans.get(key) or _ffn_plan(key)
+    _keep, ws, ws_bytes = _ffn_workspace(workspace, need, dy)
+    _ffn_call(dev, _lib.q2k_linear_backward, dy.data_ptr(), m * n,
+              z.data_ptr() if z is not None else None, w.data_ptr(), w.numel(), dx.data_ptr(), m * k,
+              dz.data_ptr() if z is not None else None, dbias.data_ptr() if bias else None, offsets,
+              params, ws, ws_bytes)
+    return dx, dz, dbias
 
 
 def matmul_lora(x, w, n: int, lora_a, lora_b, ids, scales=None, out=None, path="auto",

@@ -1037,28 +1037,30 @@ q2k_status check_path_flags(q2k_path path, uint32_t flags) {
     return Q2K_OK;
 }
 
-bool takes_tensor_path(q2k_path path, uint32_t m, uint32_t dtype) {
+bool takes_tensor_path(q2k_path path, uint32_t m, uint32_t dtype, uint32_t n_experts = 0) {
     if (path != Q2K_PATH_AUTO) return path == Q2K_PATH_TENSOR;
-    return !q2k::ffn_rows_path(static_cast<int>(m), dtype == Q2K_DTYPE_BF16);
+    return !q2k::ffn_rows_path(static_cast<int>(m), dtype == Q2K_DTYPE_BF16, static_cast<int>(n_experts));
 }
 
-q2k::GatedArgs gated_args(q2k_path path, const q2k_gated_ffn_params* p) {
+q2k::GatedArgs gated_args(q2k_path path, const q2k_gated_ffn_params* p, uint32_t n_experts) {
     q2k::GatedArgs a = {};
     a.M = static_cast<int>(p->m);
     a.N = static_cast<int>(p->n);
     a.K = static_cast<int>(p->k);
     a.act = static_cast<int>(p->act);
+    a.n_experts = static_cast<int>(n_experts);
     a.bf16 = p->dtype == Q2K_DTYPE_BF16;
-    a.tensor = takes_tensor_path(path, p->m, p->dtype);
+    a.tensor = takes_tensor_path(path, p->m, p->dtype, n_experts);
     return a;
 }
 
-q2k::GatedBackwardArgs gated_backward_args(const q2k_gated_ffn_params* p) {
+q2k::GatedBackwardArgs gated_backward_args(const q2k_gated_ffn_params* p, uint32_t n_experts) {
     q2k::GatedBackwardArgs a = {};
     a.M = static_cast<int>(p->m);
     a.N = static_cast<int>(p->n);
     a.K = static_cast<int>(p->k);
     a.act = static_cast<int>(p->act);
+    a.n_experts = static_cast<int>(n_experts);
     return a;
 }
 
@@ -1099,24 +1101,32 @@ q2k_status check_lora(const q2k_lora_params* p, FfnShape* s) {
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params* p) {
-    FfnShape s;
-    if (check_path_flags(path, 0) != Q2K_OK || check_gated(p, &s) != Q2K_OK) return 0;
-    return q2k::gated_workspace_bytes(gated_args(path, p));
+// Segments of a call's tokens: offsets and how many, both or neither.
+q2k_status check_segments(const int32_t* offsets, uint32_t n_experts) {
+    if (n_experts > Q2K_MOE_MAX_EXPERTS)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "n_experts must be <= %d, got %u", Q2K_MOE_MAX_EXPERTS, n_experts);
+    if ((offsets != nullptr) != (n_experts > 0))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, n_experts > 0 ? "offsets must be non-NULL" : "offsets must be NULL");
+    if (!aligned(offsets, 4)) return fail(Q2K_ERR_INVALID_ARGUMENT, "offsets must be 4-byte aligned");
+    return Q2K_OK;
+}
+Span offsets_span(const int32_t* offsets, uint32_t n_experts) {
+    return {offsets, offsets != nullptr ? (size_t(n_experts) + 1) * 4 : 0, "offsets"};
 }
 
-q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void* x, size_t x_elems,
-                         const void* w_gate, size_t w_gate_bytes, const void* w_up,
-                         size_t w_up_bytes, void* h, size_t h_elems, void* gate, void* up,
-                         const q2k_gated_ffn_params* p, void* workspace, size_t workspace_bytes,
-                         q2k_stream_t stream) {
-    g_last_error[0] = '\0';
+q2k_status gated_call(const char* what, q2k_path path, uint32_t flags, const void* x, size_t x_elems,
+                      const void* w_gate, size_t w_gate_bytes, const void* w_up, size_t w_up_bytes,
+                      void* h, size_t h_elems, void* gate, void* up, const int32_t* offsets,
+                      uint32_t n_experts, const q2k_gated_ffn_params* p, void* workspace,
+                      size_t workspace_bytes, q2k_stream_t stream) {
     FfnShape s;
     q2k_status st = check_gated(p, &s);
     if (st == Q2K_OK) st = check_path_flags(path, flags);
+    if (st == Q2K_OK) st = check_segments(offsets, n_experts);
     if (st != Q2K_OK) return st;
+    s.w_bytes *= n_experts > 0 ? n_experts : 1;
     if (x == nullptr || w_gate == nullptr || w_up == nullptr || h == nullptr)
         return fail(Q2K_ERR_INVALID_ARGUMENT, "x, w_gate, w_up and h must be non-NULL");
     if ((gate == nullptr) != (up == nullptr))
@@ -1128,15 +1138,15 @@ q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void* x, size_t x_
         return st;
     if (!aligned(x, 16) || !aligned(h, 16) || !aligned(gate, 16) || !aligned(up, 16))
         return fail(Q2K_ERR_INVALID_ARGUMENT, "x, h, gate and up must be 16-byte aligned");
-    q2k::GatedArgs a = gated_args(path, p);
+    q2k::GatedArgs a = gated_args(path, p, n_experts);
     const size_t need = q2k::gated_workspace_bytes(a);
     if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
     const size_t out_bytes = s.mn * s.elem, save_bytes = gate != nullptr ? out_bytes : 0;
     const Span out[] = {{h, out_bytes, "h"}, {gate, save_bytes, "gate"}, {up, save_bytes, "up"},
                         {workspace, need, "workspace"}};
     const Span in[] = {{x, s.mk * s.elem, "x"}, {w_gate, s.w_bytes, "w_gate"},
-                       {w_up, s.w_bytes, "w_up"}};
-    if ((st = check_disjoint(out, 4, in, 3)) != Q2K_OK) return st;
+                       {w_up, s.w_bytes, "w_up"}, offsets_span(offsets, n_experts)};
+    if ((st = check_disjoint(out, 4, in, 4)) != Q2K_OK) return st;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != Q2K_OK) return st;
     a.x = x;
@@ -1145,29 +1155,25 @@ q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void* x, size_t x_
     a.h = h;
     a.gate = gate;
     a.up = up;
+    a.offsets = offsets;
     a.const_weights = (flags & Q2K_FLAG_CONST_WEIGHTS) != 0;
     a.device = dev.device;
     a.sm_count = dev.sm_count;
     const cudaError_t e =
         q2k::launch_gated(a, need ? workspace : nullptr, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_gated_ffn launch");
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, what);
 }
 
-size_t q2k_gated_ffn_backward_workspace_bytes(const q2k_gated_ffn_params* p) {
-    FfnShape s;
-    if (check_gated(p, &s) != Q2K_OK) return 0;
-    return q2k::gated_backward_workspace_bytes(gated_backward_args(p));
-}
-
-q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* up, size_t h_elems,
-                                  const void* w_gate, size_t w_gate_bytes, const void* w_up,
-                                  size_t w_up_bytes, void* dx, size_t dx_elems, void* dgate,
-                                  void* dup, const q2k_gated_ffn_params* p, void* workspace,
-                                  size_t workspace_bytes, q2k_stream_t stream) {
-    g_last_error[0] = '\0';
+q2k_status gated_backward_call(const char* what, const void* dh, const void* gate, const void* up,
+                               size_t h_elems, const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                               size_t w_up_bytes, void* dx, size_t dx_elems, void* dgate, void* dup,
+                               const int32_t* offsets, uint32_t n_experts, const q2k_gated_ffn_params* p,
+                               void* workspace, size_t workspace_bytes, q2k_stream_t stream) {
     FfnShape s;
     q2k_status st = check_gated(p, &s);
+    if (st == Q2K_OK) st = check_segments(offsets, n_experts);
     if (st != Q2K_OK) return st;
+    s.w_bytes *= n_experts > 0 ? n_experts : 1;
     if (p->dtype != Q2K_DTYPE_BF16)
         return fail(Q2K_ERR_INVALID_ARGUMENT, "the backward pass takes bf16 activations only");
     if (dh == nullptr || gate == nullptr || up == nullptr || w_gate == nullptr || w_up == nullptr ||
@@ -1184,7 +1190,7 @@ q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* 
         !aligned(dgate, 16) || !aligned(dup, 16))
         return fail(Q2K_ERR_INVALID_ARGUMENT,
                     "dh, gate, up, dx, dgate and dup must be 16-byte aligned");
-    q2k::GatedBackwardArgs a = gated_backward_args(p);
+    q2k::GatedBackwardArgs a = gated_backward_args(p, n_experts);
     a.dgate = static_cast<__nv_bfloat16*>(dgate);
     const size_t need = q2k::gated_backward_workspace_bytes(a);
     if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
@@ -1192,8 +1198,9 @@ q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* 
     const Span out[] = {{dx, s.mk * 2, "dx"}, {dgate, save_bytes, "dgate"}, {dup, save_bytes, "dup"},
                         {workspace, need, "workspace"}};
     const Span in[] = {{dh, mn_bytes, "dh"}, {gate, mn_bytes, "gate"}, {up, mn_bytes, "up"},
-                       {w_gate, s.w_bytes, "w_gate"}, {w_up, s.w_bytes, "w_up"}};
-    if ((st = check_disjoint(out, 4, in, 5)) != Q2K_OK) return st;
+                       {w_gate, s.w_bytes, "w_gate"}, {w_up, s.w_bytes, "w_up"},
+                       offsets_span(offsets, n_experts)};
+    if ((st = check_disjoint(out, 4, in, 6)) != Q2K_OK) return st;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != Q2K_OK) return st;
     a.dh = static_cast<const __nv_bfloat16*>(dh);
@@ -1204,11 +1211,237 @@ q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* 
     a.dx = static_cast<__nv_bfloat16*>(dx);
     a.dgate = static_cast<__nv_bfloat16*>(dgate);
     a.dup = static_cast<__nv_bfloat16*>(dup);
+    a.offsets = offsets;
     a.device = dev.device;
     a.sm_count = dev.sm_count;
     const cudaError_t e =
         q2k::launch_gated_backward(a, workspace, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_gated_ffn_backward launch");
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, what);
+}
+
+q2k_status check_linear(const q2k_linear_params* p, FfnShape* s) {
+    if (p == nullptr) return fail(Q2K_ERR_INVALID_ARGUMENT, "params is NULL");
+    q2k_status st = check_ffn_shape(p->m, p->n, p->k, p->ggml_type, p->dtype, s);
+    if (st != Q2K_OK) return st;
+    if (p->act != Q2K_ACT_SILU && p->act != Q2K_ACT_GELU && p->act != Q2K_ACT_NONE)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "unknown act %u", p->act);
+    if (p->n_experts > Q2K_MOE_MAX_EXPERTS)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "n_experts must be <= %d, got %u", Q2K_MOE_MAX_EXPERTS,
+                    p->n_experts);
+    if (p->reserved != 0) return fail(Q2K_ERR_INVALID_ARGUMENT, "reserved must be 0");
+    s->w_bytes *= p->n_experts > 0 ? p->n_experts : 1;
+    return Q2K_OK;
+}
+
+q2k::LinearArgs linear_args(q2k_path path, const q2k_linear_params* p) {
+    q2k::LinearArgs a = {};
+    a.M = static_cast<int>(p->m);
+    a.N = static_cast<int>(p->n);
+    a.K = static_cast<int>(p->k);
+    a.act = static_cast<int>(p->act);
+    a.n_experts = static_cast<int>(p->n_experts);
+    a.bf16 = p->dtype == Q2K_DTYPE_BF16;
+    a.tensor = takes_tensor_path(path, p->m, p->dtype, p->n_experts);
+    return a;
+}
+
+q2k::LinearBackwardArgs linear_backward_args(const q2k_linear_params* p) {
+    q2k::LinearBackwardArgs a = {};
+    a.M = static_cast<int>(p->m);
+    a.N = static_cast<int>(p->n);
+    a.K = static_cast<int>(p->k);
+    a.act = static_cast<int>(p->act);
+    a.n_experts = static_cast<int>(p->n_experts);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q2k_gated_ffn_workspace_bytes(q2k_path path, const q2k_gated_ffn_params* p) {
+    FfnShape s;
+    if (check_path_flags(path, 0) != Q2K_OK || check_gated(p, &s) != Q2K_OK) return 0;
+    return q2k::gated_workspace_bytes(gated_args(path, p, 0));
+}
+
+q2k_status q2k_gated_ffn(q2k_path path, uint32_t flags, const void* x, size_t x_elems,
+                         const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                         size_t w_up_bytes, void* h, size_t h_elems, void* gate, void* up,
+                         const q2k_gated_ffn_params* p, void* workspace, size_t workspace_bytes,
+                         q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    return gated_call("q2k_gated_ffn launch", path, flags, x, x_elems, w_gate, w_gate_bytes, w_up,
+                      w_up_bytes, h, h_elems, gate, up, nullptr, 0, p, workspace, workspace_bytes, stream);
+}
+
+size_t q2k_gated_ffn_backward_workspace_bytes(const q2k_gated_ffn_params* p) {
+    FfnShape s;
+    if (check_gated(p, &s) != Q2K_OK) return 0;
+    return q2k::gated_backward_workspace_bytes(gated_backward_args(p, 0));
+}
+
+q2k_status q2k_gated_ffn_backward(const void* dh, const void* gate, const void* up, size_t h_elems,
+                                  const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                                  size_t w_up_bytes, void* dx, size_t dx_elems, void* dgate,
+                                  void* dup, const q2k_gated_ffn_params* p, void* workspace,
+                                  size_t workspace_bytes, q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    return gated_backward_call("q2k_gated_ffn_backward launch", dh, gate, up, h_elems, w_gate, w_gate_bytes,
+                               w_up, w_up_bytes, dx, dx_elems, dgate, dup, nullptr, 0, p, workspace,
+                               workspace_bytes, stream);
+}
+
+size_t q2k_gated_ffn_experts_workspace_bytes(q2k_path path, const q2k_gated_ffn_params* p,
+                                             uint32_t n_experts) {
+    FfnShape s;
+    if (check_path_flags(path, 0) != Q2K_OK || check_gated(p, &s) != Q2K_OK || n_experts == 0 ||
+        n_experts > Q2K_MOE_MAX_EXPERTS)
+        return 0;
+    return q2k::gated_workspace_bytes(gated_args(path, p, n_experts));
+}
+
+q2k_status q2k_gated_ffn_experts(q2k_path path, uint32_t flags, const void* x, size_t x_elems,
+                                 const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                                 size_t w_up_bytes, void* h, size_t h_elems, void* gate, void* up,
+                                 const int32_t* offsets, uint32_t n_experts,
+                                 const q2k_gated_ffn_params* p, void* workspace, size_t workspace_bytes,
+                                 q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    if (n_experts == 0) return fail(Q2K_ERR_INVALID_ARGUMENT, "n_experts must be >= 1");
+    return gated_call("q2k_gated_ffn_experts launch", path, flags, x, x_elems, w_gate, w_gate_bytes, w_up,
+                      w_up_bytes, h, h_elems, gate, up, offsets, n_experts, p, workspace, workspace_bytes,
+                      stream);
+}
+
+size_t q2k_gated_ffn_experts_backward_workspace_bytes(const q2k_gated_ffn_params* p, uint32_t n_experts) {
+    FfnShape s;
+    if (check_gated(p, &s) != Q2K_OK || n_experts == 0 || n_experts > Q2K_MOE_MAX_EXPERTS) return 0;
+    return q2k::gated_backward_workspace_bytes(gated_backward_args(p, n_experts));
+}
+
+q2k_status q2k_gated_ffn_experts_backward(const void* dh, const void* gate, const void* up, size_t h_elems,
+                                          const void* w_gate, size_t w_gate_bytes, const void* w_up,
+                                          size_t w_up_bytes, void* dx, size_t dx_elems, void* dgate,
+                                          void* dup, const int32_t* offsets, uint32_t n_experts,
+                                          const q2k_gated_ffn_params* p, void* workspace,
+                                          size_t workspace_bytes, q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    if (n_experts == 0) return fail(Q2K_ERR_INVALID_ARGUMENT, "n_experts must be >= 1");
+    return gated_backward_call("q2k_gated_ffn_experts_backward launch", dh, gate, up, h_elems, w_gate,
+                               w_gate_bytes, w_up, w_up_bytes, dx, dx_elems, dgate, dup, offsets, n_experts,
+                               p, workspace, workspace_bytes, stream);
+}
+
+size_t q2k_linear_workspace_bytes(q2k_path path, const q2k_linear_params* p) {
+    FfnShape s;
+    if (check_path_flags(path, 0) != Q2K_OK || check_linear(p, &s) != Q2K_OK) return 0;
+    return q2k::linear_workspace_bytes(linear_args(path, p));
+}
+
+q2k_status q2k_linear(q2k_path path, uint32_t flags, const void* x, size_t x_elems, const void* w,
+                      size_t w_bytes, const float* bias, const void* residual, void* y, size_t y_elems,
+                      void* z, const int32_t* offsets, const q2k_linear_params* p, void* workspace,
+                      size_t workspace_bytes, q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    FfnShape s;
+    q2k_status st = check_linear(p, &s);
+    if (st == Q2K_OK) st = check_path_flags(path, flags);
+    if (st == Q2K_OK) st = check_segments(offsets, p->n_experts);
+    if (st != Q2K_OK) return st;
+    if (x == nullptr || w == nullptr || y == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, w and y must be non-NULL");
+    if ((st = check_elems("x", x_elems, s.mk)) != Q2K_OK ||
+        (st = check_weights("w", w, w_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_elems("y", y_elems, s.mn)) != Q2K_OK)
+        return st;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(z, 16) || !aligned(residual, 16) || !aligned(bias, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "x, bias, residual, y and z must be 16-byte aligned");
+    q2k::LinearArgs a = linear_args(path, p);
+    const size_t need = q2k::linear_workspace_bytes(a);
+    if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
+    const size_t out_bytes = s.mn * s.elem, matrices = p->n_experts > 0 ? p->n_experts : 1;
+    const Span out[] = {{y, out_bytes, "y"}, {z, z != nullptr ? out_bytes : 0, "z"},
+                        {workspace, need, "workspace"}};
+    const Span in[] = {{x, s.mk * s.elem, "x"},
+                       {w, s.w_bytes, "w"},
+                       {bias, bias != nullptr ? matrices * p->n * 4 : 0, "bias"},
+                       {residual, residual != nullptr ? out_bytes : 0, "residual"},
+                       offsets_span(offsets, p->n_experts)};
+    if ((st = check_disjoint(out, 3, in, 5)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    a.x = x;
+    a.w = static_cast<const uint8_t*>(w);
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.z = z;
+    a.offsets = offsets;
+    a.const_weights = (flags & Q2K_FLAG_CONST_WEIGHTS) != 0;
+    a.device = dev.device;
+    a.sm_count = dev.sm_count;
+    const cudaError_t e =
+        q2k::launch_linear(a, need ? workspace : nullptr, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_linear launch");
+}
+
+size_t q2k_linear_backward_workspace_bytes(const q2k_linear_params* p) {
+    FfnShape s;
+    if (check_linear(p, &s) != Q2K_OK) return 0;
+    return q2k::linear_backward_workspace_bytes(linear_backward_args(p));
+}
+
+q2k_status q2k_linear_backward(const void* dy, size_t dy_elems, const void* z, const void* w, size_t w_bytes,
+                               void* dx, size_t dx_elems, void* dz, float* dbias, const int32_t* offsets,
+                               const q2k_linear_params* p, void* workspace, size_t workspace_bytes,
+                               q2k_stream_t stream) {
+    g_last_error[0] = '\0';
+    FfnShape s;
+    q2k_status st = check_linear(p, &s);
+    if (st == Q2K_OK) st = check_segments(offsets, p->n_experts);
+    if (st != Q2K_OK) return st;
+    if (p->dtype != Q2K_DTYPE_BF16)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "the backward pass takes bf16 activations only");
+    if (dy == nullptr || w == nullptr || dx == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "dy, w and dx must be non-NULL");
+    if (p->act == Q2K_ACT_NONE && (z != nullptr || dz != nullptr))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "without an activation z and dz must be NULL (dz is dy)");
+    if (p->act != Q2K_ACT_NONE && z == nullptr)
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "z must be non-NULL with an activation");
+    if ((st = check_elems("dy", dy_elems, s.mn)) != Q2K_OK ||
+        (st = check_weights("w", w, w_bytes, s.w_bytes)) != Q2K_OK ||
+        (st = check_elems("dx", dx_elems, s.mk)) != Q2K_OK)
+        return st;
+    if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dx, 16) || !aligned(dz, 16) || !aligned(dbias, 16))
+        return fail(Q2K_ERR_INVALID_ARGUMENT, "dy, z, dx, dz and dbias must be 16-byte aligned");
+    q2k::LinearBackwardArgs a = linear_backward_args(p);
+    a.dz = static_cast<__nv_bfloat16*>(dz);
+    const size_t need = q2k::linear_backward_workspace_bytes(a);
+    if ((st = check_ffn_workspace(workspace, workspace_bytes, need)) != Q2K_OK) return st;
+    const size_t mn_bytes = s.mn * 2, matrices = p->n_experts > 0 ? p->n_experts : 1;
+    const Span out[] = {{dx, s.mk * 2, "dx"},
+                        {dz, dz != nullptr ? mn_bytes : 0, "dz"},
+                        {dbias, dbias != nullptr ? matrices * p->n * 4 : 0, "dbias"},
+                        {workspace, need, "workspace"}};
+    const Span in[] = {{dy, mn_bytes, "dy"},
+                       {z, z != nullptr ? mn_bytes : 0, "z"},
+                       {w, s.w_bytes, "w"},
+                       offsets_span(offsets, p->n_experts)};
+    if ((st = check_disjoint(out, 4, in, 4)) != Q2K_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != Q2K_OK) return st;
+    a.dy = static_cast<const __nv_bfloat16*>(dy);
+    a.z = static_cast<const __nv_bfloat16*>(z);
+    a.w = static_cast<const uint8_t*>(w);
+    a.dx = static_cast<__nv_bfloat16*>(dx);
+    a.dbias = dbias;
+    a.offsets = offsets;
+    a.device = dev.device;
+    a.sm_count = dev.sm_count;
+    const cudaError_t e =
+        q2k::launch_linear_backward(a, need ? workspace : nullptr, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? Q2K_OK : cuda_fail(e, "q2k_linear_backward launch");
 }
 
 size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params* p) {
@@ -1285,7 +1518,7 @@ q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void* x, size_t 
 // ---- tokens to their experts and back -----------------------------------------------
 
 static_assert(Q2K_MOE_MAX_EXPERTS == q2k::kMoeMaxExperts, "header and library disagree");
-static_assert(sizeof(q2k_moe_params) == 24, "q2k_moe_params layout");
+static_assert(sizeof(q2k_moe_params) == 24 && sizeof(q2k_linear_params) == 32, "struct layouts");
 
 namespace {
 

@@ -3,6 +3,7 @@
 //
 //   gated     g = x Wg^T, u = x Wu^T, h = act(g) * u
 //   backward  dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu
+//   linear    z = x W^T + bias, y = act(z) + residual;  dz = dy act'(z), dx = dz W
 //   lora      y_i = W x_i + s_a B_a (A_a x_i), a the adapter of token i
 //
 // Every weight is formed in f32 (dl q - ml rounded once) and every sum is f32.
@@ -250,12 +251,24 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 bool ffn_rows_path(int m, bool bf16) { return m <= (bf16 ? 16 : 8); }
 
+bool ffn_rows_path(int m, bool bf16, int n_experts) {
+    return ffn_rows_path(m, bf16) || (n_experts > 0 && m <= (bf16 ? 4 : 2) * n_experts);
+}
+
 size_t gated_workspace_bytes(const GatedArgs& a) {
-    return a.tensor ? gated_tc_workspace_bytes(a) : 0;
+    return a.tensor ? gated_tc_workspace_bytes(a) : gated_rows_workspace_bytes(a);
 }
 
 cudaError_t launch_gated(const GatedArgs& a, void* workspace, cudaStream_t stream) {
-    return a.tensor ? launch_gated_tc(a, workspace, stream) : launch_gated_rows(a, stream);
+    return a.tensor ? launch_gated_tc(a, workspace, stream) : launch_gated_rows(a, workspace, stream);
+}
+
+size_t linear_workspace_bytes(const LinearArgs& a) {
+    return a.tensor ? linear_tc_workspace_bytes(a) : linear_rows_workspace_bytes(a);
+}
+
+cudaError_t launch_linear(const LinearArgs& a, void* workspace, cudaStream_t stream) {
+    return a.tensor ? launch_linear_tc(a, workspace, stream) : launch_linear_rows(a, workspace, stream);
 }
 
 // Workspace: t, then the tensor path's.

@@ -9,6 +9,7 @@ namespace q2k {
 
 constexpr int kActSilu = 0;
 constexpr int kActGelu = 1;  // the tanh form
+constexpr int kActNone = 2;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -77,6 +77,9 @@ struct Plan {
     size_t partial, counts;  // bytes of workspace
 };
 
+// The most tiles of `rows` tokens that M tokens in `segments` segments have.
+inline int segment_tiles(int M, int segments, int rows) { return M / rows + std::min(M, segments); }
+
 // rows: those of the product; quads: its K in blocks (backward: 256 weight rows).
 // Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,
 // whichever is expected to end first: a worker's stages times the time of a
@@ -131,6 +134,36 @@ inline Plan make_plan(int M, int rows, int tile_rows, int quads) {
         best.partial = static_cast<size_t>(2) * best.workers * best.ctas * best.x_rows * kPlanRows * 4;
         best.counts = (static_cast<size_t>(best.tiles - best.whole) * best.ctas * 4 + 255) & ~size_t(255);
     }
+    return best;
+}
+
+// The same for M tokens in `experts` segments of unknown lengths, each with matrices of
+// its own: a token tile belongs to one segment, so there are at most M / x_rows tiles
+// and one more for each segment that has tokens.  The kernel reads how many there are;
+// all are whole.  Tokens per tile: a stage takes as long for 128 tokens as for fewer
+// (the decode bounds it), and 0.7 of the time of 256 tokens; a segment of the mean
+// length and its last tile, half full, then cost
+//   (mean / x_rows + 1/2, at least 1) * (x_rows == 256 ? 1 : 0.7);
+// of equal ones the narrower tile, which reads fewer rows that are not its segment's.
+inline Plan make_segment_plan(int M, int rows, int tile_rows, int quads, int experts) {
+    Plan best = {};
+    double best_cost = 0;
+    const double mean = static_cast<double>(M) / std::min(M, experts);
+    for (int x_rows : {32, 64, 128, 256}) {
+        const double cost = std::max(1.0, mean / x_rows + 0.5) * (x_rows == 256 ? 1.0 : 0.7);
+        if (best_cost != 0 && cost >= best_cost) continue;
+        best_cost = cost;
+        best.x_rows = x_rows;
+    }
+    best.ctas = best.x_rows == 256 ? 2 : 1;
+    const int row_tiles = (rows + tile_rows - 1) / tile_rows;
+    best.row_units = (row_tiles + best.ctas - 1) / best.ctas;
+    best.tiles = best.row_units * segment_tiles(M, experts, best.x_rows);
+    best.whole = best.tiles;
+    const int most = kPlanSms / best.ctas;
+    best.workers = std::min(best.tiles, most);
+    // a cluster divides a tile's K while every tile still has a worker of its own
+    best.parts = std::max(1, std::min({kMaxParts / best.ctas, quads, most / best.tiles}));
     return best;
 }
 

@@ -43,6 +43,7 @@
 
 #include "q2k_device.cuh"
 #include "q2k_ffn.cuh"
+#include "q2k_ffn_plan.h"
 #include "q2k_internal.h"
 #include "q2k_tc.cuh"
 
@@ -468,13 +469,44 @@ struct RowsArgs {
     const int* ids;
     void* y;
     int R, n_adapters;
+    // one matrix (y as above)
+    const float* bias;    // [segments][N], or null
+    const void* residual;
+    void* z;              // or null
+    // tokens in segments with matrices of their own: the token tiles, how many there
+    // are and how many there could be; the first of this launch
+    const int4* table;
+    const int* table_count;
+    int capacity, entry0;
     // streamed tiles
     int depth;            // units in flight
     int parts;            // CTAs of a cluster that divide K
     unsigned int* err;
 };
 
-enum class Rows { kGated, kLora };
+enum class Rows { kGated, kLora, kLinear };
+
+// Whose tokens and matrices a CTA takes: all of the call's, or (kTable) a tile of a
+// segment's.
+struct Part {
+    int m0, M;  // first token, and the end of those that the CTA may take
+    int expert;
+    const uint8_t* w0;
+    const uint8_t* w1;
+};
+template <bool kTable>
+__device__ __forceinline__ bool take_part(const RowsArgs& p, int tokens, Part& part) {
+    if constexpr (kTable) {
+        const int at = p.entry0 + static_cast<int>(blockIdx.y);
+        if (at >= *p.table_count) return false;
+        const int4 t = p.table[at];
+        const size_t matrix = static_cast<size_t>(p.N) * (p.K / kQK) * kBlockBytes;
+        part = {t.y, t.y + t.z, t.x, p.w0 + t.x * matrix, p.w1 + t.x * matrix};
+    } else {
+        part = {static_cast<int>(blockIdx.y) * tokens, p.M, 0, p.w0, p.w1};
+    }
+    return true;
+}
 
 __device__ __forceinline__ void cp_async_word(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -557,17 +589,17 @@ __device__ __forceinline__ float sum_not_finite(const T* x, const uint8_t* row, 
 
 // Sum o of a unit's two tiles -> results.
 template <typename T, int NT, Rows kMode>
-__device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, int o, float (&v)[2], int unit,
-                                           int m0) {
+__device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, const Part& part, int o,
+                                           float (&v)[2], int unit) {
     constexpr bool kSplit = sizeof(T) == 4;
     const int f = o >> 5, l = o & 31;
     // fragment f of lane l: its row of the tile and its token
     const int r = NT == 0 ? o : (l >> 2) + 8 * (kSplit ? f & 1 : (f >> 1) & 1);
-    const int m = m0 + (NT == 0  ? 0
-                        : kSplit ? (f >> 1) * 4 + (l & 3)
-                                 : (f >> 2) * 8 + 2 * (l & 3) + (f & 1));
+    const int m = part.m0 + (NT == 0  ? 0
+                             : kSplit ? (f >> 1) * 4 + (l & 3)
+                                      : (f >> 2) * 8 + 2 * (l & 3) + (f & 1));
     const int n = unit * p.unit_step + r;
-    if (m >= p.M) return;
+    if (m >= part.M) return;
     if (!(fabsf(v[0]) + fabsf(v[1]) <= 3.402823466e38f)) {
         // (each by itself: a row past N is whatever the slot held before)
 #pragma unroll 1
@@ -575,7 +607,7 @@ __device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, int o,
             const int na = n + a * p.tile1_row;
             if (fabsf(a ? v[1] : v[0]) <= 3.402823466e38f || na >= p.N) continue;
             const float sum = sum_not_finite(x + static_cast<size_t>(m) * p.K,
-                                             (a ? p.w1 : p.w0) + static_cast<size_t>(na) * (p.K / kQK) * kBlockBytes,
+                                             (a ? part.w1 : part.w0) + static_cast<size_t>(na) * (p.K / kQK) * kBlockBytes,
                                              p.K);
             v[0] = a ? v[0] : sum;
             v[1] = a ? sum : v[1];
@@ -588,6 +620,19 @@ __device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, int o,
         if (p.gate != nullptr) {
             static_cast<T*>(p.gate)[at] = from_float<T>(v[0]);
             static_cast<T*>(p.up)[at] = from_float<T>(v[1]);
+        }
+    } else if (kMode == Rows::kLinear) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int na = n + a * p.tile1_row;
+            if (na >= p.N) continue;
+            const size_t at = static_cast<size_t>(m) * p.N + na;
+            float f = v[a];
+            if (p.bias != nullptr) f += __ldg(p.bias + static_cast<size_t>(part.expert) * p.N + na);
+            if (p.z != nullptr) static_cast<T*>(p.z)[at] = from_float<T>(f);
+            if (p.act != kActNone) f = act_value<!kSplit>(f, p.act);
+            if (p.residual != nullptr) f += to_float(static_cast<const T*>(p.residual)[at]);
+            static_cast<T*>(p.y)[at] = from_float<T>(f);
         }
     } else {
         const int id = p.ids[m];
@@ -636,7 +681,7 @@ __device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, int o,
     }
 }
 
-template <typename T, int NT, int S, Rows kMode>
+template <typename T, int NT, int S, Rows kMode, bool kTable>
 __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restrict__ x, RowsArgs p) {
     constexpr bool kSplit = sizeof(T) == 4;
     constexpr int kTokens = Pass<T, NT>::kTokens;       // tokens of a pass
@@ -648,7 +693,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     const int group = warp / p.kw, kw = warp - group * p.kw;
     pdl_allow_dependents();
     if (group >= p.groups) return;  // (no barrier counts these warps)
-    const int m0 = blockIdx.y * kTokens;
+    bool waited = kTable;
+    if (kTable) pdl_wait_prerequisites();
+    Part part;
+    if (!take_part<kTable>(p, kTokens, part)) return;
+    const int m0 = part.m0;
     const int blocks = p.K / kQK;
     const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
     const uint32_t ring = smem_u32(smem) + warp * kDepth * kItemBytes;
@@ -664,7 +713,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     const int group_threads = 32 * p.kw;
     const int gt = kw * 32 + lane;  // thread within the group
 
-    bool waited = false;
     for (int u0 = 0; u0 < my_units; u0 += (p.passes > 1 ? kGroupUnits : my_units)) {
         const int u1 = p.passes > 1 ? min(my_units, u0 + kGroupUnits) : my_units;
         for (int pass = 0; pass < p.passes; ++pass) {
@@ -679,7 +727,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                 if (issued < items) {
                     const int unit = worker + iu * workers;
                     const int row0 = unit * p.unit_step + (it ? p.tile1_row : 0);
-                    const uint8_t* src = (it ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes +
+                    const uint8_t* src = (it ? part.w1 : part.w0) + static_cast<size_t>(row0) * row_bytes +
                                          static_cast<size_t>(first + is) * kBlockBytes;
                     const uint32_t dst = ring + (issued % kDepth) * kItemBytes + 4 * lane;
                     const int valid = p.N - row0;
@@ -727,7 +775,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (s < slots)
-                        load_x_block(x, p.K, first + s, m0 + n * (kTokens / NT), p.M, lane, xb[s][n]);
+                        load_x_block(x, p.K, first + s, m0 + n * (kTokens / NT), part.M, lane, xb[s][n]);
             int item = 0;
             for (int u = u0; u < u1; ++u) {
                 float acc[2][NT][4];
@@ -781,7 +829,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                             continue;
                         }
                     }
-                    finish_row<T, NT, kMode>(x, p, o, v, unit, m0);
+                    finish_row<T, NT, kMode>(x, p, part, o, v, unit);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -795,10 +843,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
 // The passes over tokens are a grid's y: of more than it holds, the rest go to
 // further launches (of the same kernel: a token's result is the same in each).
 constexpr int kMaxPasses = 65535;
+constexpr int kTableWaves = 2;
 
-// Calls `launch(x, args)` for each run of at most kMaxPasses passes of kTokens.
+// CTAs (or clusters) of a launch that divide the weight rows' units: those that the GPU
+// holds, over the token tiles that there could be.
+int unit_ctas(const RowsArgs& p, int most, int units) {
+    if (p.table == nullptr) return std::min(most, units);
+    return std::min(units, std::max(1, (kTableWaves * most + p.capacity - 1) / p.capacity));
+}
+
+// Calls `launch(x, args, passes)` for each run of at most kMaxPasses passes of kTokens.
 template <typename T, int kTokens, typename Launch>
 cudaError_t launch_passes(const T* x, const RowsArgs& p, Launch&& launch) {
+    if (p.table != nullptr) {  // (tiles instead of passes)
+        for (int first = 0; first < p.capacity; first += kMaxPasses) {
+            RowsArgs q = p;
+            q.entry0 = first;
+            const cudaError_t e = launch(x, q, std::min(p.capacity - first, kMaxPasses));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
     for (int first = 0; first < p.M; first += kMaxPasses * kTokens) {
         RowsArgs q = p;
         q.M = std::min(p.M - first, kMaxPasses * kTokens);
@@ -809,13 +874,15 @@ cudaError_t launch_passes(const T* x, const RowsArgs& p, Launch&& launch) {
         if (p.y != nullptr) q.y = static_cast<T*>(p.y) + at;
         if (p.t != nullptr) q.t = p.t + static_cast<size_t>(first) * p.R;
         if (p.ids != nullptr) q.ids = p.ids + first;
-        const cudaError_t e = launch(x + static_cast<size_t>(first) * p.K, q);
+        if (p.z != nullptr) q.z = static_cast<T*>(p.z) + at;
+        if (p.residual != nullptr) q.residual = static_cast<const T*>(p.residual) + at;
+        const cudaError_t e = launch(x + static_cast<size_t>(first) * p.K, q, (q.M + kTokens - 1) / kTokens);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-template <typename T, int NT, int S, Rows kMode>
+template <typename T, int NT, int S, Rows kMode, bool kTable>
 cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cudaStream_t stream) {
     constexpr int kTokens = Pass<T, NT>::kTokens;
     constexpr int kOut = Pass<T, NT>::kSums;
@@ -824,7 +891,7 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     static std::atomic<bool> attr_done[64] = {};  // (set by any thread; setting twice does no harm)
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     if (!attr_done[device].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, NT, S, kMode>,
+        const cudaError_t e = cudaFuncSetAttribute(rows_kernel<T, NT, S, kMode, kTable>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         attr_done[device].store(true, std::memory_order_release);
@@ -843,10 +910,9 @@ cudaError_t launch_as(const void* x, RowsArgs& p, int device, int sm_count, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q) {
-        cfg.gridDim = dim3(std::min(sm_count, (p.units + p.groups - 1) / p.groups),
-                           (q.M + kTokens - 1) / kTokens);
-        return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode>, xs, q);
+    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q, int passes) {
+        cfg.gridDim = dim3(unit_ctas(p, sm_count, (p.units + p.groups - 1) / p.groups), passes);
+        return cudaLaunchKernelEx(&cfg, rows_kernel<T, NT, S, kMode, kTable>, xs, q);
     });
 }
 
@@ -882,14 +948,21 @@ __device__ __forceinline__ void send_pair(uint32_t addr, uint32_t bar, uint32_t 
 // CTA that sends for unit u has brought out u - 2, so its peers have sent theirs
 // for u - 2 and brought out u - 4: four buffers need no other bookkeeping.
 // NT = 0: one token, as integers (see XBytes).
-template <typename T, int NT, Rows kMode>
+template <typename T, int NT, Rows kMode, bool kTable>
 __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restrict__ x, RowsArgs p) {
     constexpr bool kBytes = NT == 0;
     constexpr int kTokens = Pass<T, NT>::kTokens, kOut = Pass<T, NT>::kSums;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
-    const int m0 = blockIdx.y * kTokens;
+    bool waited = kTable;
+    if (kTable) {
+        pdl_allow_dependents();
+        pdl_wait_prerequisites();
+    }
+    Part part;
+    if (!take_part<kTable>(p, kTokens, part)) return;  // (all of a cluster)
+    const int m0 = part.m0;
     const int rank = static_cast<int>(blockIdx.x) % p.parts, first_unit = static_cast<int>(blockIdx.x) / p.parts;
     const int unit_step = static_cast<int>(gridDim.x) / p.parts;
     const int blocks = p.K / kQK;
@@ -919,7 +992,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         const int tile = lane >> 4;
         const int row0 = unit * p.unit_step + (tile ? p.tile1_row : 0);
         const int valid = min(max(p.N - row0, 0), kUnitRows);
-        const uint8_t* src = (tile ? p.w1 : p.w0) + static_cast<size_t>(row0) * row_bytes;
+        const uint8_t* src = (tile ? part.w1 : part.w0) + static_cast<size_t>(row0) * row_bytes;
         uint8_t* dst = slot + tile * tile_bytes;
         uint32_t bytes = static_cast<uint32_t>(valid * pitch);
         if (p.parts == 1) {
@@ -940,8 +1013,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                           src + (lane & 15) * row_bytes + static_cast<size_t>(b0) * kBlockBytes, pitch, bar);
         }
     };
-    pdl_allow_dependents();
-    bool waited = false;
+    if (!kTable) pdl_allow_dependents();
     if (warp == 0) {
         if (lane == 0) {
             *abort_flag = 0;
@@ -951,7 +1023,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
-        if (!p.const_weights) {
+        if (!waited && !p.const_weights) {
             pdl_wait_prerequisites();
             waited = true;
         }
@@ -967,11 +1039,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     XBlock<T> xm[kBytes ? 1 : NT];
     if (warp < nb) {
         if constexpr (kBytes) {
-            wide = load_x_bytes(x, b0 + warp, lane, xs + warp * kXWords, xi, undo);
+            wide = load_x_bytes(kTable ? x + static_cast<size_t>(m0) * p.K : x, b0 + warp, lane,
+                                xs + warp * kXWords, xi, undo);
         } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                load_x_block(x, p.K, b0 + warp, m0 + n * (kTokens / NT), p.M, lane, xm[n]);
+                load_x_block(x, p.K, b0 + warp, m0 + n * (kTokens / NT), part.M, lane, xm[n]);
         }
     }
     const int o_first = kOut * rank / p.parts, o_count = kOut * (rank + 1) / p.parts - o_first;
@@ -994,7 +1067,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[1] += all[w * (2 * kOut) + kOut + o];
             }
             if (p.parts == 1) {
-                finish_row<T, NT, kMode>(x, p, o, v, first_unit + u * unit_step, m0);
+                finish_row<T, NT, kMode>(x, p, part, o, v, first_unit + u * unit_step);
             } else {
                 const int to = ((o + 1) * p.parts - 1) / kOut;  // whose share o is
                 const int at = ((u & 3) * p.parts + rank) * share + o - kOut * to / p.parts;
@@ -1015,7 +1088,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[0] += w.x;
                 v[1] += w.y;
             }
-            finish_row<T, NT, kMode>(x, p, o_first + o, v, first_unit + u * unit_step, m0);
+            finish_row<T, NT, kMode>(x, p, part, o_first + o, v, first_unit + u * unit_step);
         }
     };
     __syncthreads();
@@ -1095,6 +1168,7 @@ bool plan_stream(RowsArgs& p, size_t& smem) {
     const int blocks = p.K / kQK;
     if (blocks <= kWarps / 2) return false;
     if (((reinterpret_cast<uintptr_t>(p.w0) | reinterpret_cast<uintptr_t>(p.w1)) & 15) != 0) return false;
+    if (p.table != nullptr && static_cast<size_t>(p.N) * blocks * kBlockBytes % 16 != 0) return false;
     p.parts = (blocks + kWarps - 1) / kWarps;
     if (p.parts > 1 && (p.parts > kMaxRowParts || blocks % 4 != 0)) return false;
     const size_t fixed = kWarps * 2 * 2 * Pass<T, NT>::kSums * 4 + 4 * (Pass<T, NT>::kSums + kMaxRowParts) * 8 +
@@ -1105,7 +1179,7 @@ bool plan_stream(RowsArgs& p, size_t& smem) {
     return true;
 }
 
-template <typename T, int NT, Rows kMode>
+template <typename T, int NT, Rows kMode, bool kTable>
 cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, int sm_count,
                           cudaStream_t stream) {
     // clusters of a size that the GPU holds at once, 0: not known yet
@@ -1127,47 +1201,77 @@ cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, i
     cfg.numAttrs = p.parts > 1 ? 2 : 1;
     int most = resident[device][p.parts].load(std::memory_order_acquire);
     if (most == 0) {
-        e = cudaFuncSetAttribute(stream_kernel<T, NT, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(stream_kernel<T, NT, kMode, kTable>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kMaxSmem);
         if (e != cudaSuccess) return e;
         most = sm_count;
         if (p.parts > 1) {
             cfg.gridDim = dim3(sm_count / p.parts * p.parts);
-            e = cudaOccupancyMaxActiveClusters(&most, stream_kernel<T, NT, kMode>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&most, stream_kernel<T, NT, kMode, kTable>, &cfg);
             if (e != cudaSuccess) return e;
         }
         most = std::max(1, most);
         resident[device][p.parts].store(most, std::memory_order_release);
     }
     constexpr int kTokens = Pass<T, NT>::kTokens;
-    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q) {
-        cfg.gridDim = dim3(std::min(most, p.units) * p.parts, (q.M + kTokens - 1) / kTokens);
-        return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode>, xs, q);
+    return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q, int passes) {
+        cfg.gridDim = dim3(unit_ctas(p, most, p.units) * p.parts, passes);
+        return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode, kTable>, xs, q);
     });
 }
 
 // Columns of x in registers: one tile of eight and up to two blocks a warp, or
-// two tiles (more than 8 bf16 or 4 f32 tokens) and one block.
-template <typename T, Rows kMode>
-cudaError_t launch_rows_mode(const void* x, RowsArgs& p, int device, int sm_count,
+// two tiles (more than 8 bf16 or 4 f32 tokens) and one block.  `tokens`: of a pass.
+template <typename T, Rows kMode, bool kTable = false>
+cudaError_t launch_rows_mode(const void* x, RowsArgs& p, int tokens, int device, int sm_count,
                              cudaStream_t stream) {
     constexpr int kOne = sizeof(T) == 4 ? 4 : 8;
     size_t smem = 0;
-    if (p.M == 1 && plan_stream<T, 0>(p, smem))
-        return launch_stream<T, 0, kMode>(x, p, smem, device, sm_count, stream);
-    if (p.M <= kOne && plan_stream<T, 1>(p, smem))
-        return launch_stream<T, 1, kMode>(x, p, smem, device, sm_count, stream);
-    if (p.M > kOne && plan_stream<T, 2>(p, smem))
-        return launch_stream<T, 2, kMode>(x, p, smem, device, sm_count, stream);
-    if (p.M > kOne)
-        return launch_as<T, 2, 1, kMode>(x, p, device, sm_count, stream);
-    if (p.K / kQK > kWarps) return launch_as<T, 1, 2, kMode>(x, p, device, sm_count, stream);
-    return launch_as<T, 1, 1, kMode>(x, p, device, sm_count, stream);
+    if (tokens == 1 && plan_stream<T, 0>(p, smem))
+        return launch_stream<T, 0, kMode, kTable>(x, p, smem, device, sm_count, stream);
+    if (tokens <= kOne && plan_stream<T, 1>(p, smem))
+        return launch_stream<T, 1, kMode, kTable>(x, p, smem, device, sm_count, stream);
+    if (tokens > kOne && plan_stream<T, 2>(p, smem))
+        return launch_stream<T, 2, kMode, kTable>(x, p, smem, device, sm_count, stream);
+    if (tokens > kOne)
+        return launch_as<T, 2, 1, kMode, kTable>(x, p, device, sm_count, stream);
+    if (p.K / kQK > kWarps) return launch_as<T, 1, 2, kMode, kTable>(x, p, device, sm_count, stream);
+    return launch_as<T, 1, 1, kMode, kTable>(x, p, device, sm_count, stream);
+}
+
+// Tokens of a tile of a segment: one where most segments have one or none, else as many
+// as one or two tiles of eight columns hold.
+int tile_tokens(int M, int segments, bool bf16) {
+    const int one = bf16 ? 8 : 4;
+    if (4 * M <= segments) return 1;
+    return M <= one / 2 * segments ? one : 2 * one;
+}
+
+// p with a table of the call's segments in the workspace, which this launches.
+template <Rows kMode>
+cudaError_t launch_rows_table(const void* x, RowsArgs& p, const int* offsets, int segments, bool bf16,
+                              void* workspace, int device, int sm_count, cudaStream_t stream) {
+    const int tokens = tile_tokens(p.M, segments, bf16);
+    const cudaError_t e = launch_ffn_table(offsets, segments, p.M, tokens, workspace, sm_count, stream);
+    if (e != cudaSuccess) return e;
+    p.table_count = static_cast<const int*>(workspace);
+    p.table = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(workspace) + 16);
+    p.capacity = segment_tiles(p.M, segments, tokens);
+    return bf16 ? launch_rows_mode<__nv_bfloat16, kMode, true>(x, p, tokens, device, sm_count, stream)
+                : launch_rows_mode<float, kMode, true>(x, p, tokens, device, sm_count, stream);
+}
+
+size_t table_workspace_bytes(int M, int segments, bool bf16) {
+    return segments > 0 ? ffn_table_bytes(M, segments, tile_tokens(M, segments, bf16)) : 0;
 }
 
 }  // namespace
 
-cudaError_t launch_gated_rows(const GatedArgs& a, cudaStream_t stream) {
+size_t gated_rows_workspace_bytes(const GatedArgs& a) {
+    return table_workspace_bytes(a.M, a.n_experts, a.bf16);
+}
+
+cudaError_t launch_gated_rows(const GatedArgs& a, void* workspace, cudaStream_t stream) {
     RowsArgs p = {};
     p.w0 = a.wg;
     p.w1 = a.wu;
@@ -1182,8 +1286,37 @@ cudaError_t launch_gated_rows(const GatedArgs& a, cudaStream_t stream) {
     p.gate = a.gate;
     p.up = a.up;
     p.act = a.act;
-    return a.bf16 ? launch_rows_mode<__nv_bfloat16, Rows::kGated>(a.x, p, a.device, a.sm_count, stream)
-                  : launch_rows_mode<float, Rows::kGated>(a.x, p, a.device, a.sm_count, stream);
+    if (a.n_experts > 0)
+        return launch_rows_table<Rows::kGated>(a.x, p, a.offsets, a.n_experts, a.bf16, workspace, a.device,
+                                               a.sm_count, stream);
+    return a.bf16 ? launch_rows_mode<__nv_bfloat16, Rows::kGated>(a.x, p, p.M, a.device, a.sm_count, stream)
+                  : launch_rows_mode<float, Rows::kGated>(a.x, p, p.M, a.device, a.sm_count, stream);
+}
+
+size_t linear_rows_workspace_bytes(const LinearArgs& a) {
+    return table_workspace_bytes(a.M, a.n_experts, a.bf16);
+}
+
+cudaError_t launch_linear_rows(const LinearArgs& a, void* workspace, cudaStream_t stream) {
+    RowsArgs p = {};
+    p.w0 = p.w1 = a.w;
+    p.unit_step = 2 * kUnitRows;
+    p.tile1_row = kUnitRows;
+    p.M = a.M;
+    p.N = a.N;
+    p.K = a.K;
+    p.units = (a.N + 2 * kUnitRows - 1) / (2 * kUnitRows);
+    p.const_weights = a.const_weights;
+    p.bias = a.bias;
+    p.residual = a.residual;
+    p.y = a.y;
+    p.z = a.z;
+    p.act = a.act;
+    if (a.n_experts > 0)
+        return launch_rows_table<Rows::kLinear>(a.x, p, a.offsets, a.n_experts, a.bf16, workspace, a.device,
+                                                a.sm_count, stream);
+    return a.bf16 ? launch_rows_mode<__nv_bfloat16, Rows::kLinear>(a.x, p, p.M, a.device, a.sm_count, stream)
+                  : launch_rows_mode<float, Rows::kLinear>(a.x, p, p.M, a.device, a.sm_count, stream);
 }
 
 cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t stream) {
@@ -1203,8 +1336,8 @@ cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t str
     p.y = a.y;
     p.R = a.R;
     p.n_adapters = a.n_adapters;
-    return a.bf16 ? launch_rows_mode<__nv_bfloat16, Rows::kLora>(a.x, p, a.device, a.sm_count, stream)
-                  : launch_rows_mode<float, Rows::kLora>(a.x, p, a.device, a.sm_count, stream);
+    return a.bf16 ? launch_rows_mode<__nv_bfloat16, Rows::kLora>(a.x, p, p.M, a.device, a.sm_count, stream)
+                  : launch_rows_mode<float, Rows::kLora>(a.x, p, p.M, a.device, a.sm_count, stream);
 }
 
 }  // namespace q2k

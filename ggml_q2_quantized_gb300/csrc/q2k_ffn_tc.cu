@@ -73,18 +73,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group) {
+bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group,
+                     int matrices) {
     const uint64_t row_bytes = static_cast<uint64_t>(K / kQK) * kBlockBytes * group;
+    if (matrices > 1 && N % group != 0) return false;  // (the matrices do not start with a group)
     N /= group;
     if (N == 0) return false;
     if (row_bytes % 16 != 0 || (reinterpret_cast<uintptr_t>(w) & 15) != 0) return false;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {row_bytes, static_cast<cuuint64_t>(N)};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBoxBytes), static_cast<cuuint32_t>(rows)};
-    const cuuint32_t elem[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w), dims, strides, box,
+    const cuuint64_t dims[3] = {row_bytes, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(matrices)};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * static_cast<cuuint64_t>(N)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBoxBytes), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w), dims, strides, box,
                   elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -108,7 +110,8 @@ constexpr int kABytes = kStageK * kRows * 2;  // a decoded stage in shared memor
 constexpr int kSumPitch = kRows + 4;
 constexpr int kChunk = 32;
 
-enum class Tc { kGated, kLora, kBackward };
+// kLinear: one matrix, with bias, activation and residual; kBackward: one matrix or two.
+enum class Tc { kGated, kLora, kLinear, kBackward };
 
 // Tiles of kX tokens.
 // 256: two CTAs of a cluster (neighbouring row tiles) form one MMA of 256 rows
@@ -193,6 +196,14 @@ struct TcArgs {
     const int* ids;
     void* y;             // adapters: y; backward: dx
     int R, n_adapters;
+    // one matrix (y as above)
+    const float* bias;   // [n_experts][N], or null
+    const void* residual;
+    void* z;             // x W^T + bias, or null
+    // tokens in segments, each with matrices of its own: the token tiles and how
+    // many (null: one segment, tiles follow from M)
+    const int4* table;
+    const int* table_count;
 };
 
 struct TcMaps {
@@ -462,12 +473,12 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr, uint32_t rank) {
 // Backward, non-TMA: the words of 64 weight rows that a stage needs (two of
 // scales, eight of codes, d and dmin) packed into a raw slot, by the 128 threads
 // of a decoder group.  Rows past N are zero (they decode to 0).
-__device__ __forceinline__ void issue_raw_rows(const TcArgs& p, uint32_t dst, int stage, int block,
-                                               int half, int tg) {
+__device__ __forceinline__ void issue_raw_rows(const TcArgs& p, uint32_t dst, int stage, int expert,
+                                               int block, int half, int tg) {
     const bool up = stage >= p.half_stages;
     const int n0 = kStageK * (up ? stage - p.half_stages : stage);
-    const uint8_t* w = up ? p.w1 : p.w0;
     const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
+    const uint8_t* w = (up ? p.w1 : p.w0) + static_cast<size_t>(expert) * p.N * row_bytes;
     for (int f = tg; f < kStageK * 11; f += 128) {
         const int r = f / 11, i = f - 11 * r;
         const int word = i < 2 ? 2 * half + i : i < 10 ? 4 + 8 * half + (i - 2) : 20;
@@ -492,6 +503,73 @@ __device__ __forceinline__ void decode_segment(const uint32_t (&q)[4], uint32_t 
         const uint32_t sel = code_selectors<J>(q[e]);
         o[2 * e] = __byte_perm(lo, hi, sel);
         o[2 * e + 1] = __byte_perm(lo, hi, __umulhi(sel, 0x10000u));  // sel >> 16
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float2 load_pair(const T* src, int valid, bool vec);
+template <>
+__device__ __forceinline__ float2 load_pair(const float* src, int valid, bool vec) {
+    if (vec) return __ldg(reinterpret_cast<const float2*>(src));
+    return make_float2(valid > 0 ? __ldg(src) : 0.f, valid > 1 ? __ldg(src + 1) : 0.f);
+}
+template <>
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* src, int valid, bool vec) {
+    if (vec) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src));
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    return make_float2(valid > 0 ? to_float(src[0]) : 0.f, valid > 1 ? to_float(src[1]) : 0.f);
+}
+
+// The same for one matrix: z = sum + bias, y = act(z) + residual.  A warp takes four
+// tokens at a time, so that their residuals are on their way together.
+template <typename T>
+__device__ __forceinline__ void emit_linear(const TcArgs& p, const float* sums, int n0, int rows, int m0,
+                                            int count, int expert, const Team& team) {
+    constexpr int kAtOnce = 4;
+    const int lane = team.thread & 31, warps = team.threads >> 5;
+    const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
+    const int valid[2] = {rows - (n0 + 2 * lane), rows - (n0 + 2 * lane) - 64};
+    float2 bias[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        bias[q] = make_float2(0.f, 0.f);
+        if (p.bias != nullptr && valid[q] > 0)
+            bias[q] = load_pair(p.bias + static_cast<size_t>(expert) * rows + n0 + 2 * lane + 64 * q, valid[q],
+                                vec);
+    }
+    for (int c0 = team.thread >> 5; c0 < count; c0 += kAtOnce * warps) {
+        float2 r[kAtOnce][2];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = c0 + u * warps;
+                r[u][q] = make_float2(0.f, 0.f);
+                if (p.residual != nullptr && c < count && valid[q] > 0)
+                    r[u][q] = load_pair(static_cast<const T*>(p.residual) + static_cast<size_t>(m0 + c) * rows +
+                                            n0 + 2 * lane + 64 * q, valid[q], vec);
+            }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int c = c0 + u * warps;
+            if (c >= count) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (valid[q] <= 0) continue;
+                const size_t at = static_cast<size_t>(m0 + c) * rows + n0 + 2 * lane + 64 * q;
+                float2 v = *reinterpret_cast<const float2*>(sums + c * kSumPitch + 2 * lane + 64 * q);
+                v.x += bias[q].x;
+                v.y += bias[q].y;
+                if (p.z != nullptr) store_pair(static_cast<T*>(p.z) + at, v.x, v.y, valid[q], vec);
+                if (p.act != kActNone) {
+                    v.x = act_value<sizeof(T) == 2>(v.x, p.act);
+                    v.y = act_value<sizeof(T) == 2>(v.y, p.act);
+                }
+                store_pair(static_cast<T*>(p.y) + at, v.x + r[u][q].x, v.y + r[u][q].y, valid[q], vec);
+            }
+        }
     }
 }
 
@@ -535,6 +613,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     constexpr bool kDuo = C::kDuo;
     constexpr int S = C::kStages;
     constexpr int kSplit0 = kMode == Tc::kGated ? kRows / 2 : kRows;  // tile rows of w0
+    constexpr bool kTwo = kMode == Tc::kGated || kBack;  // (backward of one matrix: w1 is w0)
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -550,12 +629,25 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     work.quads = p.quads;
     work.tiles = p.tiles;
     work.whole = p.whole;
+    const int4* table = kMode == Tc::kLora ? nullptr : p.table;
+    if (table != nullptr) {
+        // (the plan counts what there could be; all are whole)
+        pdl_wait_prerequisites();
+        work.tiles = work.whole = *p.table_count * p.row_units;
+    }
     Segment sg;
-    // first row (backward: column k) and first token of a tile, its MMA N
+    // first row (backward: column k) of a tile, first token and how many, its MMA N,
+    // and whose matrices
     auto row0 = [&](int tile) { return (C::kCtas * (tile % p.row_units) + peer) * kSplit0; };
-    auto token0 = [&](int tile) { return tile / p.row_units * kX; };
+    auto token0 = [&](int tile) {
+        return table != nullptr ? table[tile / p.row_units].y : tile / p.row_units * kX;
+    };
+    auto tokens_of = [&](int tile) {
+        return table != nullptr ? table[tile / p.row_units].z : min(kX, p.M - tile / p.row_units * kX);
+    };
+    auto expert_of = [&](int tile) { return table != nullptr ? table[tile / p.row_units].x : 0; };
     auto mma_n = [&](int tile) {
-        const int tokens = min(kX, p.M - token0(tile));
+        const int tokens = tokens_of(tile);
         return kDuo ? (tokens + 31) & ~31 : (tokens + 15) & ~15;
     };
 
@@ -648,7 +740,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             [[maybe_unused]] auto fetch_next = [&]() {
                 if (more) {
                     issue_raw_rows(p, raw0 + (fetched % C::kRaw) * C::kRawBytes, 4 * fetch_q + own,
-                                   row0(fetch.tile) / kQK, (row0(fetch.tile) / kRows) & 1, tg);
+                                   expert_of(fetch.tile), row0(fetch.tile) / kQK,
+                                   (row0(fetch.tile) / kRows) & 1, tg);
                     fetched += 4;
                     if (++fetch_q == fetch.q1) {
                         more = work.segment(++fetch_index, fetch);
@@ -866,12 +959,12 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         // ---------------- raw weight blocks ----------------
         if (kTma && lane == 0) {
             tma_prefetch_map(&maps.w0);
-            if (kMode != Tc::kLora) tma_prefetch_map(&maps.w1);
+            if (kTwo) tma_prefetch_map(&maps.w1);
             if (!p.const_weights) pdl_wait_prerequisites();
             int b = 0;
             bool ok = true;
             for (int index = 0; ok && work.segment(index, sg); ++index) {
-                const int n0 = row0(sg.tile);
+                const int n0 = row0(sg.tile), expert = expert_of(sg.tile);
                 for (int r = 0; ok && r < (sg.q1 - sg.q0) * (kBack ? 4 : 1); ++r, ++b) {
                     const int buf = b % C::kRaw;
                     ok = b < C::kRaw ||
@@ -884,13 +977,13 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     if constexpr (kBack) {
                         const int stage = 4 * sg.q0 + r;
                         const bool up = stage >= p.half_stages;
-                        tma_load_2d(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
-                                    kStageK * (up ? stage - p.half_stages : stage), bar);
+                        tma_load_3d(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
+                                    kStageK * (up ? stage - p.half_stages : stage), expert, bar);
                     } else {
                         const int x = (kBlockBytes * (sg.q0 + r)) & ~15;
-                        tma_load_2d(dst, &maps.w0, x, n0, bar);
+                        tma_load_3d(dst, &maps.w0, x, n0, expert, bar);
                         if (kMode == Tc::kGated)
-                            tma_load_2d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, bar);
+                            tma_load_3d(dst + kSplit0 * kBoxBytes, &maps.w1, x, n0, expert, bar);
                     }
                 }
             }
@@ -904,14 +997,15 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             // 77 tokens, 22.4 us; a bulk copy for each row's block 42.)
             if (lane == 0 && p.groups > 0) {
                 tma_prefetch_map(&maps.w0);
-                if (kMode != Tc::kLora) tma_prefetch_map(&maps.w1);
+                if (kTwo) tma_prefetch_map(&maps.w1);
             }
             if (!p.const_weights) pdl_wait_prerequisites();
             const size_t row_bytes = static_cast<size_t>(p.K / kQK) * kBlockBytes;
             int b = 0;
             bool ok = true;
             for (int index = 0; ok && work.segment(index, sg); ++index) {
-                const int n0 = row0(sg.tile);
+                const int n0 = row0(sg.tile), expert = expert_of(sg.tile);
+                const size_t matrix = static_cast<size_t>(expert) * p.N * row_bytes;
                 const bool words = n0 + kSplit0 > 4 * p.groups;
                 for (int q = sg.q0; ok && q < sg.q1; ++q, ++b) {
                     const int buf = b % C::kRaw;
@@ -926,7 +1020,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                             const int n = n0 + r % kSplit0;
                             if (n < 4 * p.groups || n >= p.N) continue;
                             const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                                (r < kSplit0 ? p.w0 : p.w1) + n * row_bytes + static_cast<size_t>(kBlockBytes) * q);
+                                (r < kSplit0 ? p.w0 : p.w1) + matrix + n * row_bytes +
+                                static_cast<size_t>(kBlockBytes) * q);
                             const uint32_t dst = slot + raw_place<kSplit0>(r, p.groups > 0) * C::kRawPitch;
                             uint32_t v[kWordsPerBlock];
 #pragma unroll
@@ -943,10 +1038,10 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int x = static_cast<int>((j * row_bytes + kBlockBytes * q) & ~size_t(15));
-                            tma_load_2d(slot + j * (kSplit0 / 4) * kBoxBytes, &maps.w0, x, n0 / 4, bar);
+                            tma_load_3d(slot + j * (kSplit0 / 4) * kBoxBytes, &maps.w0, x, n0 / 4, expert, bar);
                             if (kMode == Tc::kGated)
-                                tma_load_2d(slot + (kSplit0 + j * (kSplit0 / 4)) * kBoxBytes, &maps.w1, x,
-                                            n0 / 4, bar);
+                                tma_load_3d(slot + (kSplit0 + j * (kSplit0 / 4)) * kBoxBytes, &maps.w1, x,
+                                            n0 / 4, expert, bar);
                         }
                     }
                 }
@@ -997,8 +1092,9 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     }
     // Results of `count` tokens (from m on) of a tile from their sums; the last
     // tile's (`final`) lie where the rings were, from token slot `slot` on.
-    auto bring_out = [&](float* base, bool final, int n0, int m, int count, const Team& team, int slot = 0,
+    auto bring_out = [&](float* base, bool final, int tile, int m, int count, const Team& team, int slot = 0,
                          int slot0 = 0) {
+        const int n0 = row0(tile);
         if constexpr (kMode == Tc::kLora) {
             uint32_t* tbuf = reinterpret_cast<uint32_t*>(final ? base + kX * kSumPitch
                                                                : reinterpret_cast<float*>(smem + C::kOffT));
@@ -1007,7 +1103,10 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             add_adapters(base - slot0 * kSumPitch, tbuf, id_buf + slot0 + slot, id_buf + kX + slot0 + slot,
                          p, n0, m - slot0, count, team);
         }
-        emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
+        if constexpr (kMode == Tc::kLinear)
+            emit_linear<T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, expert_of(tile), team);
+        else
+            emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
     };
     const bool brings_out = warp < kDecWarps || warp >= kEpiWarp0;
     if (brings_out) {
@@ -1017,7 +1116,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         if (p.tokens_ready) pdl_allow_dependents();
         const int segments = work.count();
         // the decoders come for the last segment
-        for (int index = warp < kDecWarps ? segments - 1 : 0; work.segment(index, sg); ++index) {
+        for (int index = warp < kDecWarps ? max(segments - 1, 0) : 0; work.segment(index, sg); ++index) {
             const bool final = index == segments - 1;
             Team team;
             team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
@@ -1048,8 +1147,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             // the last tile's sums take the place of the rings
             float* sums = reinterpret_cast<float*>(smem + (final ? 0 : C::kOffSums));
             const int chunk = final ? kX : kChunk;
-            const int n0 = row0(sg.tile), m0 = token0(sg.tile);
-            const int tokens = min(kX, p.M - m0);
+            const int m0 = token0(sg.tile), tokens = tokens_of(sg.tile);
             const int quarter = (team.thread >> 5) & 3, my_row = 32 * quarter + lane;
             const int strip = 16 * (team.thread >> 7), strips = 16 * (team.threads >> 7);
             const uint32_t t_lane = tmem + (index & 1) * C::kAccCols +
@@ -1146,7 +1244,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     }
                 }
                 team.sync();
-                bring_out(sums, final, n0, m0 + c0, count, team, 0, c0);
+                bring_out(sums, final, sg.tile, m0 + c0, count, team, 0, c0);
                 team.sync();
             }
             if (final && p.parts > 1 && sg.run < 0) {
@@ -1168,15 +1266,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         fence_before();
         __syncwarp();
         cluster_sync();
-        if (brings_out) {
+        if (brings_out && work.segment(0, sg)) {
             Team team;
             team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
                                            : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
             team.threads = 128 + kDecThreads;
             team.barrier = 7;
-            work.segment(0, sg);
-            const int n0 = row0(sg.tile), m0 = token0(sg.tile);
-            const int tokens = min(kX, p.M - m0), groups = (tokens + 7) / 8;
+            const int m0 = token0(sg.tile);
+            const int tokens = tokens_of(sg.tile), groups = (tokens + 7) / 8;
             const int first = 8 * (work.part * groups / p.parts);
             const int count = min(tokens, 8 * ((work.part + 1) * groups / p.parts)) - first;
             float* sums = reinterpret_cast<float*>(smem) + first * kSumPitch;
@@ -1200,7 +1297,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             }
             team.sync();
             if (*abort_flag == 0 && count > 0)
-                bring_out(reinterpret_cast<float*>(smem), true, n0, m0, count, team, first);
+                bring_out(reinterpret_cast<float*>(smem), true, sg.tile, m0, count, team, first);
         }
     }
 
@@ -1262,8 +1359,9 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
             const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
             __nv_bfloat16* __restrict__ du, int pitch, __nv_bfloat16* __restrict__ dgate,
             __nv_bfloat16* __restrict__ dup, int M, int N, int act,
-            unsigned int* __restrict__ counts, int n_counts) {
+            unsigned int* __restrict__ counts, int n_counts, const int* __restrict__ end) {
     pdl_allow_dependents();
+    if (end != nullptr) M = min(max(*end, 0), M);  // (tokens in segments: the last one's end)
     if (blockIdx.x == 0)
         for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
     const int per_row = pitch / 8;
@@ -1304,6 +1402,196 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
                 dup[at + e] = b[e];
             }
         }
+    }
+}
+
+// dz = dy act'(z) for one matrix, and its sums over the tokens (of each segment):
+// dbias.  A CTA takes 256 columns (a lane eight of them) and a share of a segment's
+// tokens, a warp every eighth; a cluster's CTAs share a segment and add their sums in
+// order.  dz goes to rows of `pitch`, and to the caller's own rows where those differ;
+// without an activation dz is dy, and only sums, or rows of `pitch`, may be asked for.
+// A sum takes dz before it is rounded.
+struct LinearGradArgs {
+    const __nv_bfloat16* dy;
+    const __nv_bfloat16* z;   // null: no activation
+    __nv_bfloat16* to;        // rows of `pitch`, or null
+    __nv_bfloat16* dz;        // the caller's, or null
+    float* dbias;             // [segments][N], or null
+    const int* offsets;       // of the segments, or null: one of M tokens
+    unsigned int* counts;
+    int n_counts;
+    int M, N, pitch, act;
+    int shares;               // CTAs of a segment and 256 columns (with dbias: a cluster)
+};
+constexpr int kGradCols = 256, kGradWarps = 8, kGradAtOnce = 4;
+
+__global__ void __launch_bounds__(32 * kGradWarps) linear_grad_kernel(LinearGradArgs p) {
+    __shared__ float red[kGradWarps][kGradCols];
+    __shared__ float part[kGradCols];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = blockIdx.x % p.shares, n = kGradCols * (blockIdx.x / p.shares) + 8 * lane;
+    const int segment = blockIdx.y;
+    pdl_wait_prerequisites();
+    pdl_allow_dependents();  // (later grids start when all before this one is complete)
+    if (blockIdx.x == 0 && segment == 0)
+        for (int c = threadIdx.x; c < p.n_counts; c += blockDim.x) p.counts[c] = 0u;
+    int lo = 0, hi = p.M;
+    if (p.offsets != nullptr) {
+        lo = min(max(p.offsets[segment], 0), p.M);
+        hi = min(max(p.offsets[segment + 1], lo), p.M);
+    }
+    const long long len = hi - lo;
+    hi = lo + static_cast<int>(len * (share + 1) / p.shares);
+    lo += static_cast<int>(len * share / p.shares);
+    const bool vec = (p.N & 7) == 0;
+    float sum[8] = {};
+    for (int m0 = lo + warp; m0 < hi && n < p.pitch; m0 += kGradAtOnce * kGradWarps) {
+        __nv_bfloat16 g[kGradAtOnce][8], z[kGradAtOnce][8];
+#pragma unroll
+        for (int u = 0; u < kGradAtOnce; ++u) {
+            const int m = m0 + u * kGradWarps;
+            const size_t at = static_cast<size_t>(m) * p.N + n;
+            if (m >= hi) continue;
+            if (vec) {
+                *reinterpret_cast<uint4*>(g[u]) = __ldg(reinterpret_cast<const uint4*>(p.dy + at));
+                if (p.z != nullptr) *reinterpret_cast<uint4*>(z[u]) = __ldg(reinterpret_cast<const uint4*>(p.z + at));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool ok = n + e < p.N;
+                    g[u][e] = ok ? p.dy[at + e] : __float2bfloat16_rn(0.f);
+                    z[u][e] = ok && p.z != nullptr ? p.z[at + e] : __float2bfloat16_rn(0.f);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGradAtOnce; ++u) {
+            const int m = m0 + u * kGradWarps;
+            if (m >= hi) continue;
+            __nv_bfloat16 d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = to_float(g[u][e]);
+                if (p.z != nullptr) {
+                    float value, slope;
+                    act_value_slope<true>(to_float(z[u][e]), p.act, value, slope);
+                    v *= slope;
+                }
+                sum[e] += v;
+                d[e] = __float2bfloat16_rn(v);
+            }
+            if (p.to != nullptr)
+                *reinterpret_cast<uint4*>(p.to + static_cast<size_t>(m) * p.pitch + n) = *reinterpret_cast<const uint4*>(d);
+            if (p.dz != nullptr)
+                for (int e = 0; e < 8 && n + e < p.N; ++e) p.dz[static_cast<size_t>(m) * p.N + n + e] = d[e];
+        }
+    }
+    if (p.dbias == nullptr) return;  // (all CTAs alike)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[warp][8 * lane + e] = sum[e];
+    __syncthreads();
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGradWarps; ++w) v += red[w][threadIdx.x];
+    part[threadIdx.x] = v;
+    if (p.shares > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (share == 0) {
+            v = 0.f;
+            for (int c = 0; c < p.shares; ++c) {
+                float w;
+                asm volatile(
+                    "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+                    "ld.shared::cluster.f32 %0, [ra];\n\t}"
+                    : "=f"(w)
+                    : "r"(smem_u32(part + threadIdx.x)), "r"(c)
+                    : "memory");
+                v += w;
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // the sums are read before their CTA leaves
+    }
+    const int col = n - 8 * lane + static_cast<int>(threadIdx.x);
+    if (share == 0 && col < p.N) p.dbias[static_cast<size_t>(segment) * p.N + col] = v;
+}
+
+// The token tiles of segments [offsets[e], offsets[e + 1]): {segment, first token,
+// tokens} of `rows` tokens at most, segment after segment.  Offsets that do not ascend
+// within 0 .. M give other tiles, but none outside the tokens, and not more than there
+// is room for.  f32 tokens are rounded to bf16 on the way, by all CTAs (the first
+// makes the table).
+constexpr int kTableThreads = 1024;
+struct TableArgs {
+    const int* offsets;
+    int segments, M, rows, capacity;
+    int4* table;
+    int* count;
+    const float* x;
+    __nv_bfloat16* xb;
+    size_t chunks;  // of eight values
+};
+
+__device__ __forceinline__ void make_table(const TableArgs& p, int* first) {  // first: [segments + 1]
+    __shared__ int sums[kTableThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int carry = 0;
+    for (int e0 = 0; e0 < p.segments; e0 += kTableThreads) {
+        const int e = e0 + tid;
+        int tiles = 0;
+        if (e < p.segments) {
+            const int lo = min(max(p.offsets[e], 0), p.M), hi = min(max(p.offsets[e + 1], lo), p.M);
+            tiles = (hi - lo + p.rows - 1) / p.rows;
+        }
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int before = carry, all = carry;
+        for (int w = 0; w < kTableThreads / 32; ++w) {
+            before += w < warp ? sums[w] : 0;
+            all += sums[w];
+        }
+        // (kept at the room there is: no sum of lengths overflows)
+        if (e < p.segments) first[e] = min(before + sum - tiles, p.capacity);
+        carry = min(all, p.capacity);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        first[p.segments] = carry;
+        *p.count = carry;
+    }
+    __syncthreads();
+    for (int t = tid; t < carry; t += kTableThreads) {
+        int a = 0, b = p.segments;  // the last segment that begins at t or before has it
+        while (b - a > 1) {
+            const int mid = (a + b) / 2;
+            if (first[mid] <= t) a = mid;
+            else b = mid;
+        }
+        const int lo = min(max(p.offsets[a], 0), p.M), hi = min(max(p.offsets[a + 1], lo), p.M);
+        const int m = lo + (t - first[a]) * p.rows;
+        p.table[t] = make_int4(a, m, min(p.rows, hi - m), 0);
+    }
+}
+
+__global__ void __launch_bounds__(kTableThreads) table_kernel(TableArgs p) {
+    extern __shared__ int table_smem[];
+    pdl_allow_dependents();
+    pdl_wait_prerequisites();
+    if (blockIdx.x == 0) make_table(p, table_smem);
+    if (p.xb == nullptr) return;
+    for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.chunks;
+         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i + 1);
+        reinterpret_cast<uint4*>(p.xb)[i] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
+                                                       pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
     }
 }
 
@@ -1360,7 +1648,7 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
 // `x_pitch` apart (x1: backward, du), or null with a.xa an image.
 template <Tc kMode, typename T>
 cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void* x0, const void* x1,
-                      int x_cols, int x_pitch, int device, cudaStream_t stream) {
+                      int x_cols, int x_pitch, int device, cudaStream_t stream, int experts = 1) {
     a.tiles = plan.tiles;
     a.row_units = plan.row_units;
     a.whole = plan.whole;
@@ -1369,10 +1657,11 @@ cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void
     a.counts = reinterpret_cast<unsigned int*>(workspace + plan.partial);
     alignas(64) TcMaps maps;
     memset(&maps, 0, sizeof maps);
-    const int rows = kMode == Tc::kLora ? kRows : 64;
+    constexpr bool kTwo = kMode == Tc::kGated || kMode == Tc::kBackward;
+    const int rows = kTwo ? 64 : kRows;
     auto make_maps = [&](int group) {
-        return make_weight_map(&maps.w0, a.w0, a.N, a.K, rows / group, group) &&
-               (kMode == Tc::kLora || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows / group, group));
+        return make_weight_map(&maps.w0, a.w0, a.N, a.K, rows / group, group, experts) &&
+               (!kTwo || make_weight_map(&maps.w1, a.w1, a.N, a.K, rows / group, group, experts));
     };
     const bool tma = make_maps(1);
     a.groups = !tma && kMode != Tc::kBackward && make_maps(4) ? a.N / 4 : 0;
@@ -1399,21 +1688,91 @@ size_t image_bytes(int M, int K) {
     return static_cast<size_t>((M + kSuperRows - 1) / kSuperRows) * kSuperRows * K * 2;
 }
 
-Plan forward_plan(int M, int N, int K, bool gated) {
-    return make_plan(M, N, gated ? kRows / 2 : kRows, K / kQK);
+// The segments of a call's tokens: as many as matrices, or none (offsets null).
+struct Segments {
+    const int* offsets;
+    int count;
+};
+
+Plan forward_plan(int M, int N, int K, bool gated, int experts = 0) {
+    const int tile_rows = gated ? kRows / 2 : kRows;
+    return experts > 0 ? make_segment_plan(M, N, tile_rows, K / kQK, experts)
+                       : make_plan(M, N, tile_rows, K / kQK);
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+// The count and the table of tiles.
+size_t table_bytes(const Plan& plan) {
+    return align256(16 + static_cast<size_t>(plan.tiles / plan.row_units) * sizeof(int4));
+}
+
+template <typename Args>
+cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, int threads, size_t smem, int cluster,
+                       cudaStream_t stream, const Args& args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+// The table at `workspace` for tiles of `rows` tokens; x: f32 tokens that xb gets.
+cudaError_t launch_table(const Segments& seg, int M, int rows, int capacity, uint8_t* workspace,
+                         const float* x, __nv_bfloat16* xb, int K, int sm_count, cudaStream_t stream) {
+    TableArgs p = {};
+    p.offsets = seg.offsets;
+    p.segments = seg.count;
+    p.M = M;
+    p.rows = rows;
+    p.capacity = capacity;
+    p.count = reinterpret_cast<int*>(workspace);
+    p.table = reinterpret_cast<int4*>(workspace + 16);
+    p.x = x;
+    p.xb = xb;
+    p.chunks = xb != nullptr ? static_cast<size_t>(M) * (K / 8) : 0;
+    const size_t wanted = (p.chunks + 2 * kTableThreads - 1) / (2 * kTableThreads);
+    const unsigned ctas = static_cast<unsigned>(std::min<size_t>(std::max<size_t>(wanted, 1), 2 * sm_count));
+    return launch_pdl(table_kernel, dim3(ctas), kTableThreads, (seg.count + 1) * sizeof(int), 1, stream, p);
 }
 
 // x W^T: bf16 tokens go to the kernel by their own tensor map, f32 tokens by an
-// image.  behind_grid: one of this call's own grids (which does not write x, and
-// zeroes the counts) is before, and lets its dependents start only when x is
-// complete.  Workspace: plan_bytes, then (f32) the image.
+// image (in segments, which begin anywhere, by a bf16 copy).  behind_grid: one of this
+// call's own grids (which does not write x, and zeroes the counts) is before, and lets
+// its dependents start only when x is complete.  Workspace: plan_bytes, then (f32) the
+// image; in segments the table, then (f32) the copy.
+size_t forward_workspace_bytes(int M, int N, int K, bool gated, bool bf16, int experts) {
+    const Plan plan = forward_plan(M, N, K, gated, experts);
+    if (experts > 0) return table_bytes(plan) + (bf16 ? 0 : static_cast<size_t>(M) * K * 2);
+    return plan_bytes(plan) + (bf16 ? 0 : image_bytes(M, K));
+}
+
 template <Tc kMode>
 cudaError_t launch_forward(TcArgs a, bool bf16, const void* x, void* workspace, int device,
-                           int sm_count, bool behind_grid, cudaStream_t stream) {
-    const Plan plan = forward_plan(a.M, a.N, a.K, kMode == Tc::kGated);
+                           int sm_count, bool behind_grid, cudaStream_t stream, Segments seg = {nullptr, 0}) {
+    const Plan plan = forward_plan(a.M, a.N, a.K, kMode == Tc::kGated, seg.count);
     a.quads = a.K / kQK;
     a.tokens_ready = bf16 && behind_grid;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (seg.count > 0) {
+        __nv_bfloat16* xb = bf16 ? nullptr : reinterpret_cast<__nv_bfloat16*>(ws + table_bytes(plan));
+        const cudaError_t e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws,
+                                           static_cast<const float*>(x), xb, a.K, sm_count, stream);
+        if (e != cudaSuccess) return e;
+        a.table_count = reinterpret_cast<const int*>(ws);
+        a.table = reinterpret_cast<const int4*>(ws + 16);
+        a.const_weights = a.tokens_ready = true;  // (the kernel waits before it reads the table)
+        return bf16 ? launch_tc<kMode, __nv_bfloat16>(a, plan, ws, x, nullptr, a.K, a.K, device, stream, seg.count)
+                    : launch_tc<kMode, float>(a, plan, ws, xb, nullptr, a.K, a.K, device, stream, seg.count);
+    }
     unsigned int* counts = reinterpret_cast<unsigned int*>(ws + plan.partial);
     if (bf16) {
         if (!behind_grid && plan.counts != 0) {
@@ -1442,15 +1801,29 @@ cudaError_t launch_forward(TcArgs a, bool bf16, const void* x, void* workspace, 
     return launch_tc<kMode, float>(a, plan, ws, nullptr, nullptr, 0, 0, device, stream);
 }
 
-// Columns of dg and du as the product's K: whole parts of two stages each.
-int backward_cols(int N) { return (N + 2 * kStageK - 1) / (2 * kStageK) * (2 * kStageK); }
+// Columns of one of the token matrices as the product's K: over both of two, or in the
+// one, whole fours of stages.
+int backward_cols(int N, int matrices) {
+    const int unit = 4 / matrices * kStageK;
+    return (N + unit - 1) / unit * unit;
+}
 // Their rows' pitch: the caller's own when those are whole 16 bytes.
 int backward_pitch(int N) { return (N + 7) & ~7; }
 
 }  // namespace
 
+size_t ffn_table_bytes(int M, int segments, int rows) {
+    return align256(16 + static_cast<size_t>(segment_tiles(M, segments, rows)) * sizeof(int4));
+}
+
+cudaError_t launch_ffn_table(const int* offsets, int segments, int M, int rows, void* workspace,
+                             int sm_count, cudaStream_t stream) {
+    return launch_table({offsets, segments}, M, rows, segment_tiles(M, segments, rows),
+                        static_cast<uint8_t*>(workspace), nullptr, nullptr, 0, sm_count, stream);
+}
+
 size_t gated_tc_workspace_bytes(const GatedArgs& a) {
-    return plan_bytes(forward_plan(a.M, a.N, a.K, true)) + (a.bf16 ? 0 : image_bytes(a.M, a.K));
+    return forward_workspace_bytes(a.M, a.N, a.K, true, a.bf16, a.n_experts);
 }
 
 cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream) {
@@ -1465,11 +1838,32 @@ cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t st
     t.gate = a.gate;
     t.up = a.up;
     t.act = a.act;
-    return launch_forward<Tc::kGated>(t, a.bf16, a.x, workspace, a.device, a.sm_count, false, stream);
+    return launch_forward<Tc::kGated>(t, a.bf16, a.x, workspace, a.device, a.sm_count, false, stream,
+                                      {a.offsets, a.n_experts});
+}
+
+size_t linear_tc_workspace_bytes(const LinearArgs& a) {
+    return forward_workspace_bytes(a.M, a.N, a.K, false, a.bf16, a.n_experts);
+}
+
+cudaError_t launch_linear_tc(const LinearArgs& a, void* workspace, cudaStream_t stream) {
+    TcArgs t = {};
+    t.w0 = t.w1 = a.w;
+    t.M = a.M;
+    t.N = a.N;
+    t.K = a.K;
+    t.const_weights = a.const_weights;
+    t.bias = a.bias;
+    t.residual = a.residual;
+    t.y = a.y;
+    t.z = a.z;
+    t.act = a.act;
+    return launch_forward<Tc::kLinear>(t, a.bf16, a.x, workspace, a.device, a.sm_count, false, stream,
+                                       {a.offsets, a.n_experts});
 }
 
 size_t lora_tc_workspace_bytes(const LoraArgs& a) {
-    return plan_bytes(forward_plan(a.M, a.N, a.K, false)) + (a.bf16 ? 0 : image_bytes(a.M, a.K));
+    return forward_workspace_bytes(a.M, a.N, a.K, false, a.bf16, 0);
 }
 
 void lora_tc_counts(const LoraArgs& a, void* workspace, unsigned int** counts, int* n_counts) {
@@ -1499,44 +1893,131 @@ cudaError_t launch_lora_tc(const LoraArgs& a, const float* t, void* workspace, c
 static bool backward_in_place(const GatedBackwardArgs& a) {
     return a.dgate != nullptr && backward_pitch(a.N) == a.N;
 }
-static size_t backward_matrix_bytes(const GatedBackwardArgs& a) {
-    return (static_cast<size_t>(a.M) * backward_pitch(a.N) * 2 + 255) & ~size_t(255);
+static size_t backward_matrix_bytes(int M, int N) {
+    return align256(static_cast<size_t>(M) * backward_pitch(N) * 2);
 }
-static Plan backward_plan(const GatedBackwardArgs& a) {
-    return make_plan(a.M, a.K, kRows, 2 * backward_cols(a.N) / (4 * kStageK));
+static Plan backward_plan(int M, int N, int K, int matrices, int experts) {
+    const int quads = matrices * backward_cols(N, matrices) / (4 * kStageK);
+    return experts > 0 ? make_segment_plan(M, K, kRows, quads, experts) : make_plan(M, K, kRows, quads);
+}
+// Of the product alone: plan_bytes, or the table.
+static size_t backward_plan_bytes(const Plan& plan, int experts) {
+    return experts > 0 ? table_bytes(plan) : plan_bytes(plan);
 }
 size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a) {
-    return plan_bytes(backward_plan(a)) + (backward_in_place(a) ? 0 : 2 * backward_matrix_bytes(a));
+    return backward_plan_bytes(backward_plan(a.M, a.N, a.K, 2, a.n_experts), a.n_experts) +
+           (backward_in_place(a) ? 0 : 2 * backward_matrix_bytes(a.M, a.N));
+}
+
+// dx = sum over the matrices (w1: the second, or w0 again) of their tokens d0 (and d1),
+// rows of `pitch`.  The counts are zeroed.  const_weights: the grid before started when
+// all before it was complete.
+static cudaError_t launch_backward_product(const uint8_t* w0, const uint8_t* w1, const void* d0,
+                                           const void* d1, __nv_bfloat16* dx, const Plan& plan, int M, int N,
+                                           int K, int matrices, int pitch, Segments seg, bool const_weights,
+                                           uint8_t* ws, int device, cudaStream_t stream) {
+    TcArgs t = {};
+    t.w0 = w0;
+    t.w1 = w1;
+    t.M = M;
+    t.N = N;
+    t.K = K;
+    t.const_weights = const_weights;
+    t.half_stages = backward_cols(N, matrices) / kStageK;
+    t.quads = matrices * t.half_stages / 4;
+    t.y = dx;
+    if (seg.count > 0) {
+        t.table_count = reinterpret_cast<const int*>(ws);
+        t.table = reinterpret_cast<const int4*>(ws + 16);
+    }
+    return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, ws, d0, d1, N, pitch, device, stream,
+                                                   std::max(1, seg.count));
 }
 
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream) {
-    const Plan plan = backward_plan(a);
-    const int pitch = backward_pitch(a.N), cols = backward_cols(a.N);
+    const Segments seg = {a.offsets, a.n_experts};
+    const Plan plan = backward_plan(a.M, a.N, a.K, 2, seg.count);
+    const int pitch = backward_pitch(a.N);
     const bool own = backward_in_place(a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    uint8_t* copies = ws + plan_bytes(plan);
+    uint8_t* copies = ws + backward_plan_bytes(plan, seg.count);
     __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(copies);
     __nv_bfloat16* du = own ? a.dup
-                            : reinterpret_cast<__nv_bfloat16*>(copies + backward_matrix_bytes(a));
+                            : reinterpret_cast<__nv_bfloat16*>(copies + backward_matrix_bytes(a.M, a.N));
     const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
     const unsigned blocks =
         static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));
+    if (seg.count > 0) {
+        const cudaError_t e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws, nullptr,
+                                           nullptr, 0, a.sm_count, stream);
+        if (e != cudaSuccess) return e;
+    }
     grad_kernel<<<blocks, 256, 0, stream>>>(
         a.dh, a.gate, a.up, dg, du, pitch, own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
-        a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan));
+        a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan),
+        seg.count > 0 ? seg.offsets + seg.count : nullptr);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    TcArgs t = {};
-    t.w0 = a.wg;
-    t.w1 = a.wu;
-    t.M = a.M;
-    t.N = a.N;
-    t.K = a.K;
-    t.const_weights = true;  // the grid before started when all before it was complete
-    t.half_stages = cols / kStageK;
-    t.quads = 2 * t.half_stages / 4;
-    t.y = a.dx;
-    return launch_tc<Tc::kBackward, __nv_bfloat16>(t, plan, ws, dg, du, a.N, pitch, a.device, stream);
+    return launch_backward_product(a.wg, a.wu, dg, du, a.dx, plan, a.M, a.N, a.K, 2, pitch, seg, true, ws,
+                                   a.device, stream);
+}
+
+// Workspace: the product's, then dz where it is neither the caller's own (dz given, or
+// dy without an activation) nor in rows of whole 16 bytes.
+static bool linear_backward_in_place(const LinearBackwardArgs& a) {
+    return backward_pitch(a.N) == a.N && (a.act == kActNone || a.dz != nullptr);
+}
+size_t linear_backward_workspace_bytes(const LinearBackwardArgs& a) {
+    return backward_plan_bytes(backward_plan(a.M, a.N, a.K, 1, a.n_experts), a.n_experts) +
+           (linear_backward_in_place(a) ? 0 : backward_matrix_bytes(a.M, a.N));
+}
+
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, void* workspace, cudaStream_t stream) {
+    const Segments seg = {a.offsets, a.n_experts};
+    const Plan plan = backward_plan(a.M, a.N, a.K, 1, seg.count);
+    const bool own = linear_backward_in_place(a);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaError_t e = cudaSuccess;
+    if (seg.count > 0) {
+        e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws, nullptr, nullptr, 0, a.sm_count,
+                         stream);
+        if (e != cudaSuccess) return e;
+    }
+    LinearGradArgs g = {};
+    g.dy = a.dy;
+    g.z = a.act == kActNone ? nullptr : a.z;
+    g.M = a.M;
+    g.N = a.N;
+    g.pitch = backward_pitch(a.N);
+    g.act = a.act;
+    g.offsets = a.offsets;
+    g.dbias = a.dbias;
+    g.counts = reinterpret_cast<unsigned int*>(ws + plan.partial);
+    g.n_counts = count_words(plan);
+    const __nv_bfloat16* d0 = a.dy;
+    if (!own) {
+        d0 = g.to = reinterpret_cast<__nv_bfloat16*>(ws + backward_plan_bytes(plan, seg.count));
+        g.dz = a.dz;
+    } else if (g.z != nullptr) {
+        d0 = g.to = a.dz;
+    }
+    const bool grads = g.to != nullptr || g.dbias != nullptr;
+    if (grads) {
+        // a warp's rows at once are the least a share is worth; a cluster's eight at most
+        // where sums meet
+        const int segments = std::max(1, seg.count);
+        const int rows = std::max(1, a.M / segments);
+        const int strips = (g.pitch + kGradCols - 1) / kGradCols;
+        const int most = g.dbias != nullptr ? kMaxParts : std::max(1, 16 * a.sm_count / strips);
+        g.shares = std::min(most, std::max(1, rows / (kGradAtOnce * kGradWarps)));
+        e = launch_pdl(linear_grad_kernel, dim3(strips * g.shares, segments), 32 * kGradWarps, 0,
+                       g.dbias != nullptr ? g.shares : 1, stream, g);
+    } else if (plan.counts != 0) {
+        e = cudaMemsetAsync(ws + plan.partial, 0, plan.counts, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_backward_product(a.w, a.w, d0, d0, a.dx, plan, a.M, a.N, a.K, 1, g.pitch, seg,
+                                   grads || seg.count > 0, ws, a.device, stream);
 }
 
 // (the address of a module's variable: the same for a device as long as it lasts)

@@ -167,6 +167,8 @@ cudaError_t read_and_clear_tc_error(uint32_t* out, cudaStream_t stream);
 // Whether a call of m tokens takes the exact-weights kernel (q2k_ffn.cu) by
 // itself, rather than the tensor path.
 bool ffn_rows_path(int m, bool bf16);
+// The same in segments (n_experts > 0).
+bool ffn_rows_path(int m, bool bf16, int n_experts);
 
 // h = act(x Wg^T) * (x Wu^T); gate and up (both or neither) get the projections.
 // Activations f32 or bf16 (one type for all).
@@ -182,6 +184,10 @@ struct GatedArgs {
     bool tensor;         // the tensor path
     bool const_weights;  // the kernel before does not write Wg or Wu
     int device, sm_count;
+    // tokens in segments [offsets[e], offsets[e + 1]), e < n_experts, each with
+    // matrices of its own (one after another in wg and wu); 0: one for all tokens
+    const int* offsets;
+    int n_experts;
 };
 size_t gated_workspace_bytes(const GatedArgs& a);
 cudaError_t launch_gated(const GatedArgs& a, void* workspace, cudaStream_t stream);
@@ -199,9 +205,46 @@ struct GatedBackwardArgs {
     __nv_bfloat16* dup;
     int M, N, K, act;
     int device, sm_count;
+    const int* offsets;  // as GatedArgs
+    int n_experts;
 };
 size_t gated_backward_workspace_bytes(const GatedBackwardArgs& a);
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, cudaStream_t stream);
+
+// z = x W^T + bias, y = act(z) + residual.
+struct LinearArgs {
+    const void* x;
+    const uint8_t* w;
+    const float* bias;     // [N] (segments: [n_experts, N]) or null
+    const void* residual;  // [M, N] or null
+    void* y;
+    void* z;               // [M, N] or null
+    int M, N, K, act;
+    bool bf16;
+    bool tensor;
+    bool const_weights;
+    int device, sm_count;
+    const int* offsets;    // as GatedArgs
+    int n_experts;
+};
+size_t linear_workspace_bytes(const LinearArgs& a);
+cudaError_t launch_linear(const LinearArgs& a, void* workspace, cudaStream_t stream);
+
+// dz = dy act'(z), dx = dz W, dbias = the sum of dz over the tokens (of each segment).
+struct LinearBackwardArgs {
+    const __nv_bfloat16* dy;
+    const __nv_bfloat16* z;  // with an activation
+    const uint8_t* w;
+    __nv_bfloat16* dx;
+    __nv_bfloat16* dz;       // or null (without an activation dz is dy)
+    float* dbias;            // or null
+    int M, N, K, act;
+    int device, sm_count;
+    const int* offsets;      // as GatedArgs
+    int n_experts;
+};
+size_t linear_backward_workspace_bytes(const LinearBackwardArgs& a);
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, void* workspace, cudaStream_t stream);
 
 // y_i = W x_i + s_a B_a (A_a x_i) with a = ids[i]; -1: no adapter, any other id
 // out of range: a zero row, counted in *bad_ids (written, not added to).
@@ -225,13 +268,23 @@ cudaError_t launch_lora(const LoraArgs& a, void* workspace, cudaStream_t stream)
 
 // The exact-weights kernels (q2k_ffn_rows.cu).  t: f32 [M, R], s_a A_a x_i,
 // written by the grid before (zeros for a token without an adapter).
-cudaError_t launch_gated_rows(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_rows(const GatedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_lora_rows(const LoraArgs& a, const float* t, cudaStream_t stream);
+size_t gated_rows_workspace_bytes(const GatedArgs& a);
+size_t linear_rows_workspace_bytes(const LinearArgs& a);
+cudaError_t launch_linear_rows(const LinearArgs& a, void* workspace, cudaStream_t stream);
 
 // The tensor path (q2k_ffn_tc.cu).  t as above, written by the grid before,
 // which must let its dependents start only when x is complete.
 size_t gated_tc_workspace_bytes(const GatedArgs& a);
 cudaError_t launch_gated_tc(const GatedArgs& a, void* workspace, cudaStream_t stream);
+size_t linear_tc_workspace_bytes(const LinearArgs& a);
+cudaError_t launch_linear_tc(const LinearArgs& a, void* workspace, cudaStream_t stream);
+// The tiles of at most `rows` tokens of a call's segments: {segment, first token,
+// tokens} each, 16 bytes behind their count, in a workspace of ffn_table_bytes.
+size_t ffn_table_bytes(int M, int segments, int rows);
+cudaError_t launch_ffn_table(const int* offsets, int segments, int M, int rows, void* workspace,
+                             int sm_count, cudaStream_t stream);
 size_t lora_tc_workspace_bytes(const LoraArgs& a);
 // words of its workspace that must be zero (none: *n_counts = 0)
 void lora_tc_counts(const LoraArgs& a, void* workspace, unsigned int** counts, int* n_counts);

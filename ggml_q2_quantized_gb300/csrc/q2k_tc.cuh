@@ -197,6 +197,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// The same of a 3-D map.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -253,11 +262,12 @@ __device__ __forceinline__ uint32_t code_selectors(uint32_t word) {
 // cuTensorMapEncodeTiled through the runtime's driver entry point (null when
 // the driver has none).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
-// Raw Q2_K weights as a 2-D byte tensor (N rows of K/256 * 84 bytes) with a box
-// of `rows` rows x 112 bytes; false unless rows are multiples of 16 bytes (K a
-// multiple of 1024) and the base is 16-byte aligned.
+// Raw Q2_K weights as a 3-D byte tensor (`matrices` of N rows of K/256 * 84 bytes, one
+// after another) with a box of `rows` rows x 112 bytes of one matrix; false unless rows
+// are multiples of 16 bytes (K a multiple of 1024) and the base is 16-byte aligned.
 // (of `group` rows together as one of the map's; false if those do not start at 16 bytes)
-bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group);
+bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group,
+                     int matrices = 1);
 
 }  // namespace tc
 }  // namespace q2k

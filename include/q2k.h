@@ -542,11 +542,14 @@ enum {
     Q2K_FFN_MAX_TOKENS = 1 << 20, /* most tokens of a feed-forward call */
     Q2K_FFN_MAX_WIDTH = 1 << 20,  /* largest n and k of one */
     Q2K_LORA_MAX_RANK = 256,
-    Q2K_LORA_MAX_ADAPTERS = 65535
+    Q2K_LORA_MAX_ADAPTERS = 65535,
+    Q2K_MOE_MAX_TOP_K = 256,
+    Q2K_MOE_MAX_EXPERTS = 4096
 };
 typedef enum q2k_act {
     Q2K_ACT_SILU = 0, /* g / (1 + e^-g) */
-    Q2K_ACT_GELU = 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+    Q2K_ACT_GELU = 1, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+    Q2K_ACT_NONE = 2  /* g (q2k_linear only) */
 } q2k_act;
 
 typedef struct q2k_gated_ffn_params {
@@ -623,6 +626,81 @@ q2k_status q2k_matmul_lora(q2k_path path, uint32_t flags, const void *x, size_t 
                            void *workspace, size_t workspace_bytes, q2k_stream_t stream);
 size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *params);
 
+/* ---- tokens in segments ----
+ * The calls below take, beside the plain form, tokens that lie in segments: tokens
+ * offsets[e] .. offsets[e + 1] - 1 are multiplied by expert e's matrices, which lie one
+ * after another (expert e's n rows at byte e * n * k/256 * 84).  q2k_moe_route makes
+ * such offsets, and q2k_moe_sort rows in that order.
+ *   offsets    device i32 [n_experts + 1], ascending within 0 .. m
+ *   n_experts  1..Q2K_MOE_MAX_EXPERTS
+ * Tokens in no segment (before the first, behind the last) are not read, and their
+ * rows of every output stay as they are.  Offsets that do not ascend within 0 .. m give
+ * wrong results, but touch nothing outside the buffers.  Q2K_PATH_AUTO takes the exact
+ * weights up to 16 (bf16) or 8 (f32) tokens, or four (two) for each expert. */
+
+typedef struct q2k_linear_params {
+    uint32_t m;         /* tokens, >= 1 */
+    uint32_t n;         /* weight rows = output columns, >= 1 */
+    uint32_t k;         /* reduction length, a positive multiple of 256 */
+    uint32_t ggml_type; /* must be Q2K_GGML_TYPE_Q2_K */
+    uint32_t dtype;     /* q2k_dtype */
+    uint32_t act;       /* q2k_act */
+    uint32_t n_experts; /* segments, or 0: one matrix for all tokens */
+    uint32_t reserved;  /* must be 0 */
+} q2k_linear_params;
+
+/* q2k_linear - z = x W^T + bias, y = act(z) + residual in one kernel.
+ *   flags     Q2K_FLAG_CONST_WEIGHTS or 0 (as q2k_matmul_ex)
+ *   x         [m, k]
+ *   w         device, max(1, n_experts) * n * k/256 * 84 bytes, 4-byte aligned
+ *   bias      device f32 [n], in segments [n_experts, n], 16-byte aligned; or NULL
+ *   residual  [m, n], or NULL
+ *   y         [m, n]; every row of a segment overwritten
+ *   z         [m, n], or NULL: what q2k_linear_backward reads
+ *   offsets   see above; NULL with n_experts = 0
+ * No output may alias an input, the workspace or another output. */
+q2k_status q2k_linear(q2k_path path, uint32_t flags, const void *x, size_t x_elems,
+                      const void *w, size_t w_bytes, const float *bias, const void *residual,
+                      void *y, size_t y_elems, void *z, const int32_t *offsets,
+                      const q2k_linear_params *params, void *workspace, size_t workspace_bytes,
+                      q2k_stream_t stream);
+size_t q2k_linear_workspace_bytes(q2k_path path, const q2k_linear_params *params);
+
+/* q2k_linear_backward - its backward pass with the weights frozen: dz = dy * act'(z),
+ * dx = dz W and dbias = the sum of dz over the tokens (in segments, of each).  bf16 only
+ * (params.dtype); the product runs on the tensor cores with dz and W rounded to bf16,
+ * dbias is summed in f32 from dz as computed.  The residual's gradient is dy.
+ *   dy     [m, n]
+ *   z      [m, n]; NULL with Q2K_ACT_NONE
+ *   dx     [m, k]; every row of a segment overwritten
+ *   dz     [m, n] or NULL; NULL with Q2K_ACT_NONE, where dz is dy
+ *   dbias  device f32 [n], in segments [n_experts, n], 16-byte aligned; or NULL */
+q2k_status q2k_linear_backward(const void *dy, size_t dy_elems, const void *z, const void *w,
+                               size_t w_bytes, void *dx, size_t dx_elems, void *dz,
+                               float *dbias, const int32_t *offsets,
+                               const q2k_linear_params *params, void *workspace,
+                               size_t workspace_bytes, q2k_stream_t stream);
+size_t q2k_linear_backward_workspace_bytes(const q2k_linear_params *params);
+
+/* q2k_gated_ffn and its backward pass over tokens in segments (see above); w_gate and
+ * w_up hold n_experts matrices each.  Else as the calls without segments. */
+q2k_status q2k_gated_ffn_experts(q2k_path path, uint32_t flags, const void *x, size_t x_elems,
+                                 const void *w_gate, size_t w_gate_bytes, const void *w_up,
+                                 size_t w_up_bytes, void *h, size_t h_elems, void *gate,
+                                 void *up, const int32_t *offsets, uint32_t n_experts,
+                                 const q2k_gated_ffn_params *params, void *workspace,
+                                 size_t workspace_bytes, q2k_stream_t stream);
+size_t q2k_gated_ffn_experts_workspace_bytes(q2k_path path, const q2k_gated_ffn_params *params,
+                                             uint32_t n_experts);
+q2k_status q2k_gated_ffn_experts_backward(
+    const void *dh, const void *gate, const void *up, size_t h_elems, const void *w_gate,
+    size_t w_gate_bytes, const void *w_up, size_t w_up_bytes, void *dx, size_t dx_elems,
+    void *dgate, void *dup, const int32_t *offsets, uint32_t n_experts,
+    const q2k_gated_ffn_params *params, void *workspace, size_t workspace_bytes,
+    q2k_stream_t stream);
+size_t q2k_gated_ffn_experts_backward_workspace_bytes(const q2k_gated_ffn_params *params,
+                                                      uint32_t n_experts);
+
 /* ---- tokens to their experts and back --------------------------------------
  * The parts of a mixture-of-experts layer around the experts' products: which
  * place each of a router's choices has in expert order, the tokens' rows moved
@@ -639,11 +717,6 @@ size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *par
  * expert have the places from offsets[n_experts] on, which these calls write as
  * zeros and never read.  The other calls take any `rows` and `offsets`: a place
  * outside 0 .. n_tokens * top_k - 1 is neither read nor written. */
-enum {
-    Q2K_MOE_MAX_TOP_K = 256,
-    Q2K_MOE_MAX_EXPERTS = 4096
-};
-
 typedef struct q2k_moe_params {
     uint32_t n_tokens;  /* 1..Q2K_FFN_MAX_TOKENS */
     uint32_t top_k;     /* choices of a token, 1..Q2K_MOE_MAX_TOP_K */
