@@ -871,6 +871,12 @@ def _quick():
             "q2k_gated_ffn", "q2k_gated_ffn_workspace_bytes", "q2k_gated_ffn_backward",
             "q2k_gated_ffn_backward_workspace_bytes", "q2k_matmul_lora",
             "q2k_matmul_lora_workspace_bytes")))
+        mod.bind_experts(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+            "q2k_linear", "q2k_linear_workspace_bytes", "q2k_linear_backward",
+            "q2k_linear_backward_workspace_bytes", "q2k_gated_ffn_experts",
+            "q2k_gated_ffn_experts_workspace_bytes", "q2k_gated_ffn_experts_backward",
+            "q2k_gated_ffn_experts_backward_workspace_bytes", "q2k_moe_route", "q2k_moe_sort",
+            "q2k_moe_sort_backward", "q2k_moe_combine", "q2k_moe_combine_backward")))
         _quick_mod = mod
     return _quick_mod
 
@@ -895,9 +901,10 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     last expert's are not read, and their results not written.  The weights are exact
     up to four bf16 or two f32 tokens for each expert.
     """
-    if routes is None and out is None and workspace.__class__ is str:
+    if out is None and workspace.__class__ is str:
         quick = _quick_mod or _quick()
-        done = (quick.gated(x, w_gate, w_up, n, act, save, path, const_weights)
+        done = (quick.gated(x, w_gate, w_up, n, act, save, path, const_weights,
+                            routes if routes is None else routes.offsets)
                 if quick else None)
         if done.__class__ is int:
             _check(_lib, done)
@@ -939,9 +946,11 @@ def gated_ffn_backward(dh, gate, up, w_gate, w_up, k: int, act="silu", workspace
     ``[m, k]`` and the gradients ``[m, n]`` of the two projections.  ``routes`` as in
     ``gated_ffn``.
     """
-    if routes is None and workspace.__class__ is str:
+    if workspace.__class__ is str:
         quick = _quick_mod or _quick()
-        done = quick.backward(dh, gate, up, w_gate, w_up, k, act) if quick else None
+        done = (quick.backward(dh, gate, up, w_gate, w_up, k, act,
+                               routes if routes is None else routes.offsets)
+                if quick else None)
         if done.__class__ is int:
             _check(_lib, done)
         elif done is not None:
@@ -983,6 +992,15 @@ def linear(x, w, n: int, bias=None, act=None, residual=None, save: bool = False,
     autograd.  ``routes`` as in ``gated_ffn``: ``w`` then holds ``n_experts`` matrices
     and ``bias`` is ``[n_experts, n]``.
     """
+    if out is None and workspace.__class__ is str:
+        quick = _quick_mod or _quick()
+        done = (quick.linear(x, w, n, bias, act, residual, save, path, const_weights,
+                             routes if routes is None else routes.offsets)
+                if quick else None)
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     torch = _torch_mod or _torch()
     _need_activations(x, "x")
     if x.dim() != 2:
@@ -1021,6 +1039,17 @@ def linear_backward(dy, w, k: int, z=None, act=None, bias: bool = False, workspa
     the tokens, f32 ``[n]`` (with ``routes`` over each expert's, ``[n_experts, n]``), else
     None.  The residual's gradient is ``dy``.  ``routes`` as in ``gated_ffn``.
     """
+    if workspace.__class__ is str:
+        quick = _quick_mod or _quick()
+        done = (quick.linear_backward(dy, w, k, z, act, bias,
+                                      routes if routes is None else routes.offsets)
+                if quick else None)
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            if act is not None:
+                return done if bias else (*done, None)
+            return (done[0], dy, done[1]) if bias else (done, dy, None)
     torch = _torch_mod or _torch()
     bf16 = torch.bfloat16
     _need_activations(dy, "dy", bf16)
@@ -1122,6 +1151,12 @@ def moe_route(ids, n_experts: int, check: bool = True):
     n_experts; with ``check=False`` it returns ``(routes, bad_id_count)`` without
     waiting (such a choice has no expert).
     """
+    quick = _quick_mod or _quick()
+    done = quick.route(ids, n_experts) if quick else None
+    if done.__class__ is int:
+        _check(_lib, done)
+    elif done is not None:
+        return _routed(Routes(*done[:3]), done[3], n_experts, check)
     torch = _torch_mod or _torch()
     i32 = torch.int32
     _require_cuda(ids, "ids", i32)
@@ -1140,7 +1175,10 @@ def moe_route(ids, n_experts: int, check: bool = True):
     lib = _lib if _lib is not None else load()
     _ffn_call(ids.get_device(), lib.q2k_moe_route, ids.data_ptr(), choices, rows.data_ptr(),
               order.data_ptr(), offsets.data_ptr(), ctypes.byref(p), bad.data_ptr())
-    routes = Routes(rows, order, offsets)
+    return _routed(Routes(rows, order, offsets), bad, n_experts, check)
+
+
+def _routed(routes, bad, n_experts, check):
     if not check:
         return routes, bad
     n_bad = int(bad.item())
@@ -1182,6 +1220,13 @@ def moe_sort(x, routes, out=None):
     rows of expert e at ``routes.offsets[e]`` up to ``offsets[e + 1]``, ready for
     ``linear`` and ``gated_ffn`` with ``routes``; rows behind the last are zeros.
     """
+    if out is None:
+        quick = _quick_mod or _quick()
+        done = quick.sort(x, routes.rows, routes.offsets) if quick else None
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     p, rows, offsets = _moe_params(x, routes, "x", "tokens")
     out = _moe_out(out, x, (p.n_tokens * p.top_k, p.width))
     lib = _lib if _lib is not None else load()
@@ -1193,6 +1238,13 @@ def moe_sort(x, routes, out=None):
 def moe_sort_backward(dxs, routes, out=None):
     """The gradient of ``moe_sort``'s x from that of its result: ``dx[t]``, the sum of
     ``dxs[routes.rows[t, s]]`` over the token's choices that have an expert."""
+    if out is None:
+        quick = _quick_mod or _quick()
+        done = quick.sort_backward(dxs, routes.rows, routes.offsets) if quick else None
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     p, rows, offsets = _moe_params(dxs, routes, "dxs", "choices")
     out = _moe_out(out, dxs, (p.n_tokens, p.width))
     lib = _lib if _lib is not None else load()
@@ -1208,6 +1260,13 @@ def moe_combine(ys, routes, weights=None, residual=None, out=None):
     ``ys`` f32 or bf16 ``[n_tokens * top_k, width]``; ``weights`` f32 ``[n_tokens,
     top_k]`` or None (all 1); ``residual`` ``[n_tokens, width]`` in ys' dtype or None.
     """
+    if out is None:
+        quick = _quick_mod or _quick()
+        done = quick.combine(ys, routes.rows, routes.offsets, weights, residual) if quick else None
+        if done.__class__ is int:
+            _check(_lib, done)
+        elif done is not None:
+            return done
     torch = _torch_mod or _torch()
     p, rows, offsets = _moe_params(ys, routes, "ys", "choices")
     if weights is not None:
@@ -1227,6 +1286,12 @@ def moe_combine_backward(dy, ys, routes, weights):
     """The gradients of ``moe_combine``: ``(dys, dweights)`` from that of y.  ``dys`` as
     ``ys`` (zeros in rows without an expert), ``dweights`` f32 as ``weights``.  The
     residual's gradient is ``dy``."""
+    quick = _quick_mod or _quick()
+    done = quick.combine_backward(dy, ys, routes.rows, routes.offsets, weights) if quick else None
+    if done.__class__ is int:
+        _check(_lib, done)
+    elif done is not None:
+        return done
     torch = _torch_mod or _torch()
     p, rows, offsets = _moe_params(ys, routes, "ys", "choices")
     _need_like(ys, dy=(ys.dtype, (p.n_tokens, p.width), dy),

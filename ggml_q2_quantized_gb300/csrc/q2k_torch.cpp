@@ -35,6 +35,19 @@ struct Calls {
     decltype(&q2k_gated_ffn_backward_workspace_bytes) backward_bytes;
     decltype(&q2k_matmul_lora) lora;
     decltype(&q2k_matmul_lora_workspace_bytes) lora_bytes;
+    decltype(&q2k_linear) linear;
+    decltype(&q2k_linear_workspace_bytes) linear_bytes;
+    decltype(&q2k_linear_backward) linear_backward;
+    decltype(&q2k_linear_backward_workspace_bytes) linear_backward_bytes;
+    decltype(&q2k_gated_ffn_experts) gated_experts;
+    decltype(&q2k_gated_ffn_experts_workspace_bytes) gated_experts_bytes;
+    decltype(&q2k_gated_ffn_experts_backward) experts_backward;
+    decltype(&q2k_gated_ffn_experts_backward_workspace_bytes) experts_backward_bytes;
+    decltype(&q2k_moe_route) route;
+    decltype(&q2k_moe_sort) sort;
+    decltype(&q2k_moe_sort_backward) sort_backward;
+    decltype(&q2k_moe_combine) combine;
+    decltype(&q2k_moe_combine_backward) combine_backward;
 } calls;
 
 // A contiguous tensor of a type and number of dimensions on `device` (-1: any), or
@@ -90,6 +103,34 @@ bool take_act(PyObject* o, uint32_t& act) {
     act = i == 0 ? Q2K_ACT_SILU : Q2K_ACT_GELU;
     return true;
 }
+
+// An activation's name, or None.
+bool take_linear_act(PyObject* o, uint32_t& act) {
+    act = Q2K_ACT_NONE;
+    return o == Py_None || take_act(o, act);
+}
+
+// A tensor or None (then `out` is null); false for anything else.
+bool take_optional(PyObject* o, c10::ScalarType type, int dims, int device, const Tensor*& out) {
+    out = o == Py_None ? nullptr : take(o, type, dims, device);
+    return o == Py_None || out != nullptr;
+}
+
+// The offsets of a call's segments, or None: their address and how many segments.
+bool take_offsets(PyObject* o, int device, const int32_t*& offsets, uint32_t& experts) {
+    const Tensor* t;
+    if (!take_optional(o, at::kInt, 1, device, t)) return false;
+    offsets = nullptr;
+    experts = 0;
+    if (t == nullptr) return true;
+    if (t->size(0) < 2 || t->size(0) > INT_MAX) return false;
+    offsets = t->const_data_ptr<int32_t>();
+    experts = static_cast<uint32_t>(t->size(0) - 1);
+    return true;
+}
+
+void* at_or_null(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+const void* at_or_null(const Tensor* t) { return t != nullptr ? t->const_data_ptr() : nullptr; }
 
 uint32_t code(const Tensor& t) { return t.scalar_type() == at::kFloat ? Q2K_DTYPE_F32 : Q2K_DTYPE_BF16; }
 
@@ -156,9 +197,9 @@ PyObject* guarded(Body&& body) {
     return nullptr;
 }
 
-// gated(x, w_gate, w_up, n, act, save, path, const_weights)
+// gated(x, w_gate, w_up, n, act, save, path, const_weights[, offsets])
 PyObject* gated(PyObject*, PyObject* const* v, Py_ssize_t count) {
-    if (count != 8) Py_RETURN_NONE;
+    if (count != 8 && count != 9) Py_RETURN_NONE;
     return guarded([&]() -> PyObject* {
         q2k_gated_ffn_params p = {};
         q2k_path path;
@@ -167,8 +208,11 @@ PyObject* gated(PyObject*, PyObject* const* v, Py_ssize_t count) {
         const int device = x->get_device();
         const Tensor *wg = take(v[1], at::kByte, -1, device), *wu = take(v[2], at::kByte, -1, device);
         const int save = PyObject_IsTrue(v[5]), constant = PyObject_IsTrue(v[7]);
+        const int32_t* offsets = nullptr;
+        uint32_t experts = 0;
         if (wg == nullptr || wu == nullptr || !take_size(v[3], p.n) || !take_act(v[4], p.act) ||
-            !take_path(v[6], path) || save < 0 || constant < 0) {
+            !take_path(v[6], path) || save < 0 || constant < 0 ||
+            (count == 9 && !take_offsets(v[8], device, offsets, experts))) {
             PyErr_Clear();
             Py_RETURN_NONE;
         }
@@ -182,20 +226,26 @@ PyObject* gated(PyObject*, PyObject* const* v, Py_ssize_t count) {
             g = at::empty({m, n}, x->options());
             u = at::empty({m, n}, x->options());
         }
-        const Workspace ws(calls.gated_bytes(path, &p), *x);
+        const Workspace ws(offsets != nullptr ? calls.gated_experts_bytes(path, &p, experts)
+                                              : calls.gated_bytes(path, &p), *x);
         auto call = [&](q2k_stream_t stream) {
-            return calls.gated(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->const_data_ptr(), x->numel(),
-                               wg->const_data_ptr(), wg->numel(), wu->const_data_ptr(), wu->numel(), h.data_ptr(),
-                               h.numel(), save ? g.data_ptr() : nullptr, save ? u.data_ptr() : nullptr,
-                               &p, ws.at, ws.bytes, stream);
+            const uint32_t flags = constant ? Q2K_FLAG_CONST_WEIGHTS : 0u;
+            return offsets != nullptr
+                       ? calls.gated_experts(path, flags, x->const_data_ptr(), x->numel(), wg->const_data_ptr(),
+                                             wg->numel(), wu->const_data_ptr(), wu->numel(), h.data_ptr(),
+                                             h.numel(), at_or_null(g), at_or_null(u), offsets, experts, &p,
+                                             ws.at, ws.bytes, stream)
+                       : calls.gated(path, flags, x->const_data_ptr(), x->numel(), wg->const_data_ptr(),
+                                     wg->numel(), wu->const_data_ptr(), wu->numel(), h.data_ptr(), h.numel(),
+                                     at_or_null(g), at_or_null(u), &p, ws.at, ws.bytes, stream);
         };
         return save ? finish(call, *x, {h, g, u}) : finish(call, *x, {h});
     });
 }
 
-// backward(dh, gate, up, w_gate, w_up, k, act)
+// backward(dh, gate, up, w_gate, w_up, k, act[, offsets])
 PyObject* backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
-    if (count != 7) Py_RETURN_NONE;
+    if (count != 7 && count != 8) Py_RETURN_NONE;
     return guarded([&]() -> PyObject* {
         q2k_gated_ffn_params p = {};
         const Tensor* dh = take_activations(v[0]);
@@ -203,8 +253,11 @@ PyObject* backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
         const int device = dh->get_device();
         const Tensor *g = take(v[1], at::kBFloat16, 2, device), *u = take(v[2], at::kBFloat16, 2, device);
         const Tensor *wg = take(v[3], at::kByte, -1, device), *wu = take(v[4], at::kByte, -1, device);
+        const int32_t* offsets = nullptr;
+        uint32_t experts = 0;
         if (g == nullptr || u == nullptr || wg == nullptr || wu == nullptr || !take_size(v[5], p.k) ||
-            !take_act(v[6], p.act) || g->sizes() != dh->sizes() || u->sizes() != dh->sizes())
+            !take_act(v[6], p.act) || g->sizes() != dh->sizes() || u->sizes() != dh->sizes() ||
+            (count == 8 && !take_offsets(v[7], device, offsets, experts)))
             Py_RETURN_NONE;
         p.m = static_cast<uint32_t>(dh->size(0));
         p.n = static_cast<uint32_t>(dh->size(1));
@@ -213,15 +266,227 @@ PyObject* backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
         const int64_t m = p.m, n = p.n, k = p.k;
         Tensor dx = at::empty({m, k}, dh->options()), dg = at::empty({m, n}, dh->options()),
                du = at::empty({m, n}, dh->options());
-        const Workspace ws(calls.backward_bytes(&p), *dh);
+        const Workspace ws(offsets != nullptr ? calls.experts_backward_bytes(&p, experts)
+                                              : calls.backward_bytes(&p), *dh);
         return finish(
             [&](q2k_stream_t stream) {
-                return calls.backward(dh->const_data_ptr(), g->const_data_ptr(), u->const_data_ptr(), dh->numel(),
-                                      wg->const_data_ptr(), wg->numel(), wu->const_data_ptr(), wu->numel(),
-                                      dx.data_ptr(), dx.numel(), dg.data_ptr(), du.data_ptr(), &p, ws.at,
-                                      ws.bytes, stream);
+                return offsets != nullptr
+                           ? calls.experts_backward(dh->const_data_ptr(), g->const_data_ptr(), u->const_data_ptr(),
+                                                    dh->numel(), wg->const_data_ptr(), wg->numel(),
+                                                    wu->const_data_ptr(), wu->numel(), dx.data_ptr(), dx.numel(),
+                                                    dg.data_ptr(), du.data_ptr(), offsets, experts, &p, ws.at,
+                                                    ws.bytes, stream)
+                           : calls.backward(dh->const_data_ptr(), g->const_data_ptr(), u->const_data_ptr(),
+                                            dh->numel(), wg->const_data_ptr(), wg->numel(), wu->const_data_ptr(),
+                                            wu->numel(), dx.data_ptr(), dx.numel(), dg.data_ptr(), du.data_ptr(),
+                                            &p, ws.at, ws.bytes, stream);
             },
             *dh, {dx, dg, du});
+    });
+}
+
+// linear(x, w, n, bias, act, residual, save, path, const_weights, offsets)
+PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 10) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        q2k_linear_params p = {};
+        q2k_path path;
+        const Tensor* x = take_activations(v[0]);
+        if (x == nullptr) Py_RETURN_NONE;
+        const int device = x->get_device();
+        const Tensor *w = take(v[1], at::kByte, -1, device), *bias = nullptr, *residual = nullptr;
+        const int save = PyObject_IsTrue(v[6]), constant = PyObject_IsTrue(v[8]);
+        const int32_t* offsets = nullptr;
+        if (w == nullptr || !take_size(v[2], p.n) || !take_linear_act(v[4], p.act) || !take_path(v[7], path) ||
+            save < 0 || constant < 0 || !take_offsets(v[9], device, offsets, p.n_experts) ||
+            !take_optional(v[3], at::kFloat, offsets != nullptr ? 2 : 1, device, bias) ||
+            !take_optional(v[5], x->scalar_type(), 2, device, residual)) {
+            PyErr_Clear();
+            Py_RETURN_NONE;
+        }
+        p.m = static_cast<uint32_t>(x->size(0));
+        p.k = static_cast<uint32_t>(x->size(1));
+        p.ggml_type = Q2K_GGML_TYPE_Q2_K;
+        p.dtype = code(*x);
+        const int64_t m = p.m, n = p.n;
+        if ((bias != nullptr && (bias->size(-1) != n || (offsets != nullptr && bias->size(0) != p.n_experts))) ||
+            (residual != nullptr && (residual->size(0) != m || residual->size(1) != n)))
+            Py_RETURN_NONE;
+        Tensor y = at::empty({m, n}, x->options()), z;
+        if (save) z = at::empty({m, n}, x->options());
+        const Workspace ws(calls.linear_bytes(path, &p), *x);
+        auto call = [&](q2k_stream_t stream) {
+            return calls.linear(path, constant ? Q2K_FLAG_CONST_WEIGHTS : 0u, x->const_data_ptr(), x->numel(),
+                                w->const_data_ptr(), w->numel(), static_cast<const float*>(at_or_null(bias)),
+                                at_or_null(residual), y.data_ptr(), y.numel(), at_or_null(z), offsets, &p,
+                                ws.at, ws.bytes, stream);
+        };
+        return save ? finish(call, *x, {y, z}) : finish(call, *x, {y});
+    });
+}
+
+// linear_backward(dy, w, k, z, act, bias, offsets): (dx, dz, dbias), without dz where
+// there is no activation and without dbias unless it is asked for
+PyObject* linear_backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 7) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        q2k_linear_params p = {};
+        const Tensor* dy = take_activations(v[0]);
+        if (dy == nullptr || dy->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
+        const int device = dy->get_device();
+        const Tensor *w = take(v[1], at::kByte, -1, device), *z = nullptr;
+        const int bias = PyObject_IsTrue(v[5]);
+        const int32_t* offsets = nullptr;
+        if (w == nullptr || bias < 0 || !take_size(v[2], p.k) || !take_linear_act(v[4], p.act) ||
+            !take_offsets(v[6], device, offsets, p.n_experts)) {
+            PyErr_Clear();
+            Py_RETURN_NONE;
+        }
+        if (p.act != Q2K_ACT_NONE) {
+            z = take(v[3], at::kBFloat16, 2, device);
+            if (z == nullptr || z->sizes() != dy->sizes()) Py_RETURN_NONE;
+        }
+        p.m = static_cast<uint32_t>(dy->size(0));
+        p.n = static_cast<uint32_t>(dy->size(1));
+        p.ggml_type = Q2K_GGML_TYPE_Q2_K;
+        p.dtype = Q2K_DTYPE_BF16;
+        const int64_t m = p.m, n = p.n, k = p.k, experts = p.n_experts;
+        Tensor dx = at::empty({m, k}, dy->options()), dz, dbias;
+        if (z != nullptr) dz = at::empty({m, n}, dy->options());
+        if (bias) {
+            const auto f32 = dy->options().dtype(at::kFloat);
+            dbias = offsets != nullptr ? at::empty({experts, n}, f32) : at::empty({n}, f32);
+        }
+        const Workspace ws(calls.linear_backward_bytes(&p), *dy);
+        auto call = [&](q2k_stream_t stream) {
+            return calls.linear_backward(dy->const_data_ptr(), dy->numel(), at_or_null(z), w->const_data_ptr(),
+                                         w->numel(), dx.data_ptr(), dx.numel(), at_or_null(dz),
+                                         static_cast<float*>(at_or_null(dbias)), offsets, &p, ws.at, ws.bytes,
+                                         stream);
+        };
+        if (z != nullptr) return bias ? finish(call, *dy, {dx, dz, dbias}) : finish(call, *dy, {dx, dz});
+        return bias ? finish(call, *dy, {dx, dbias}) : finish(call, *dy, {dx});
+    });
+}
+
+// route(ids, n_experts): (rows, order, offsets, bad)
+PyObject* route(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 2) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        q2k_moe_params p = {};
+        const Tensor* ids = take(v[0], at::kInt, 2, -1);
+        if (ids == nullptr || ids->get_device() != c10::cuda::current_device() || !take_size(v[1], p.n_experts) ||
+            p.n_experts > Q2K_MOE_MAX_EXPERTS || ids->size(0) > INT_MAX || ids->size(1) > Q2K_MOE_MAX_TOP_K)
+            Py_RETURN_NONE;
+        const int64_t tokens = ids->size(0), top_k = ids->size(1);
+        p.n_tokens = static_cast<uint32_t>(tokens);
+        p.top_k = static_cast<uint32_t>(top_k);
+        Tensor rows = at::empty({tokens, top_k}, ids->options()), order = at::empty({tokens * top_k}, ids->options()),
+               offsets = at::empty({int64_t(p.n_experts) + 1}, ids->options()), bad = at::empty({1}, ids->options());
+        return finish(
+            [&](q2k_stream_t stream) {
+                return calls.route(ids->const_data_ptr<int32_t>(), ids->numel(), rows.data_ptr<int32_t>(),
+                                   order.data_ptr<int32_t>(), offsets.data_ptr<int32_t>(), &p,
+                                   static_cast<uint32_t*>(bad.data_ptr()), stream);
+            },
+            *ids, {rows, order, offsets, bad});
+    });
+}
+
+// The activations of a move (one row for each token, or `wide` for each choice) and its
+// rows and offsets; false if they are not ordinary.
+struct Move {
+    q2k_moe_params p = {};
+    const Tensor *t, *rows, *offsets;
+    bool take_all(PyObject* o, PyObject* r, PyObject* f, bool wide) {
+        t = take_activations(o);
+        if (t == nullptr) return false;
+        rows = take(r, at::kInt, 2, t->get_device());
+        offsets = take(f, at::kInt, 1, t->get_device());
+        if (rows == nullptr || offsets == nullptr || offsets->size(0) < 2 || offsets->size(0) > INT_MAX ||
+            rows->size(0) > INT_MAX || rows->size(1) > INT_MAX ||
+            t->size(0) != (wide ? rows->numel() : rows->size(0)))
+            return false;
+        p.n_tokens = static_cast<uint32_t>(rows->size(0));
+        p.top_k = static_cast<uint32_t>(rows->size(1));
+        p.n_experts = static_cast<uint32_t>(offsets->size(0) - 1);
+        p.width = static_cast<uint32_t>(t->size(1));
+        p.dtype = code(*t);
+        return true;
+    }
+    Tensor out(bool wide) const {
+        return at::empty({wide ? rows->numel() : rows->size(0), t->size(1)}, t->options());
+    }
+    const int32_t* rows_at() const { return rows->const_data_ptr<int32_t>(); }
+    const int32_t* offsets_at() const { return offsets->const_data_ptr<int32_t>(); }
+};
+
+// sort(x, rows, offsets), sort_backward(dxs, rows, offsets)
+template <bool kBack>
+PyObject* sort(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 3) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        Move m;
+        if (!m.take_all(v[0], v[1], v[2], kBack)) Py_RETURN_NONE;
+        Tensor out = m.out(!kBack);
+        return finish(
+            [&](q2k_stream_t stream) {
+                return (kBack ? calls.sort_backward : calls.sort)(m.t->const_data_ptr(), m.t->numel(), m.rows_at(),
+                                                                  m.offsets_at(), out.data_ptr(), out.numel(),
+                                                                  &m.p, stream);
+            },
+            *m.t, {out});
+    });
+}
+
+bool same_shape(const Tensor* t, int64_t rows, int64_t columns) {
+    return t->size(0) == rows && t->size(1) == columns;
+}
+
+// combine(ys, rows, offsets, weights or None, residual or None)
+PyObject* combine(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 5) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        Move m;
+        if (!m.take_all(v[0], v[1], v[2], true)) Py_RETURN_NONE;
+        const int device = m.t->get_device();
+        const Tensor *weights, *residual;
+        if (!take_optional(v[3], at::kFloat, 2, device, weights) ||
+            !take_optional(v[4], m.t->scalar_type(), 2, device, residual) ||
+            (weights != nullptr && weights->sizes() != m.rows->sizes()) ||
+            (residual != nullptr && !same_shape(residual, m.rows->size(0), m.t->size(1))))
+            Py_RETURN_NONE;
+        Tensor out = m.out(false);
+        return finish(
+            [&](q2k_stream_t stream) {
+                return calls.combine(m.t->const_data_ptr(), m.t->numel(), m.rows_at(), m.offsets_at(),
+                                     static_cast<const float*>(at_or_null(weights)), at_or_null(residual),
+                                     out.data_ptr(), out.numel(), &m.p, stream);
+            },
+            *m.t, {out});
+    });
+}
+
+// combine_backward(dy, ys, rows, offsets, weights)
+PyObject* combine_backward(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    if (count != 5) Py_RETURN_NONE;
+    return guarded([&]() -> PyObject* {
+        Move m;
+        if (!m.take_all(v[1], v[2], v[3], true)) Py_RETURN_NONE;
+        const int device = m.t->get_device();
+        const Tensor *dy = take(v[0], m.t->scalar_type(), 2, device), *weights = take(v[4], at::kFloat, 2, device);
+        if (dy == nullptr || weights == nullptr || weights->sizes() != m.rows->sizes() ||
+            !same_shape(dy, m.rows->size(0), m.t->size(1)))
+            Py_RETURN_NONE;
+        Tensor dys = m.out(true), dweights = at::empty(weights->sizes(), weights->options());
+        return finish(
+            [&](q2k_stream_t stream) {
+                return calls.combine_backward(dy->const_data_ptr(), dy->numel(), m.t->const_data_ptr(),
+                                              m.t->numel(), m.rows_at(), m.offsets_at(),
+                                              weights->const_data_ptr<float>(), dys.data_ptr(),
+                                              dweights.data_ptr<float>(), &m.p, stream);
+            },
+            *m.t, {dys, dweights});
     });
 }
 
@@ -270,41 +535,82 @@ PyObject* lora(PyObject*, PyObject* const* v, Py_ssize_t count) {
     });
 }
 
-// bind(addresses): the six functions of Calls, in its order
-PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
-    void* at[6];
-    if (count != 6) {
-        PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
-        return nullptr;
+template <typename F>
+void set_call(F& f, void* at) { f = reinterpret_cast<F>(at); }
+
+// `want` addresses, none of them null, into `at`.
+bool take_addresses(PyObject* const* v, Py_ssize_t count, Py_ssize_t want, const char* complaint, void** at) {
+    if (count != want) {
+        PyErr_SetString(PyExc_TypeError, complaint);
+        return false;
     }
-    for (int i = 0; i < 6; ++i) {
+    for (Py_ssize_t i = 0; i < want; ++i) {
         at[i] = PyLong_AsVoidPtr(v[i]);
         if (at[i] == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
-            return nullptr;
+            return false;
         }
     }
-    calls.gated = reinterpret_cast<decltype(calls.gated)>(at[0]);
-    calls.gated_bytes = reinterpret_cast<decltype(calls.gated_bytes)>(at[1]);
-    calls.backward = reinterpret_cast<decltype(calls.backward)>(at[2]);
-    calls.backward_bytes = reinterpret_cast<decltype(calls.backward_bytes)>(at[3]);
-    calls.lora = reinterpret_cast<decltype(calls.lora)>(at[4]);
-    calls.lora_bytes = reinterpret_cast<decltype(calls.lora_bytes)>(at[5]);
+    return true;
+}
+
+// bind(addresses): the first six functions of Calls, in its order
+PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    void* at[6];
+    if (!take_addresses(v, count, 6, "bind takes six addresses", at)) return nullptr;
+    set_call(calls.gated, at[0]);
+    set_call(calls.gated_bytes, at[1]);
+    set_call(calls.backward, at[2]);
+    set_call(calls.backward_bytes, at[3]);
+    set_call(calls.lora, at[4]);
+    set_call(calls.lora_bytes, at[5]);
     Py_RETURN_NONE;
 }
+
+// bind_experts(addresses): the other thirteen
+PyObject* bind_experts(PyObject*, PyObject* const* v, Py_ssize_t count) {
+    void* at[13];
+    if (!take_addresses(v, count, 13, "bind_experts takes thirteen addresses", at)) return nullptr;
+    set_call(calls.linear, at[0]);
+    set_call(calls.linear_bytes, at[1]);
+    set_call(calls.linear_backward, at[2]);
+    set_call(calls.linear_backward_bytes, at[3]);
+    set_call(calls.gated_experts, at[4]);
+    set_call(calls.gated_experts_bytes, at[5]);
+    set_call(calls.experts_backward, at[6]);
+    set_call(calls.experts_backward_bytes, at[7]);
+    set_call(calls.route, at[8]);
+    set_call(calls.sort, at[9]);
+    set_call(calls.sort_backward, at[10]);
+    set_call(calls.combine, at[11]);
+    set_call(calls.combine_backward, at[12]);
+    Py_RETURN_NONE;
+}
+
+using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
+PyCFunction fast(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
 }  // namespace
 
 PyMODINIT_FUNC PyInit_q2k_torch() {
     static PyMethodDef methods[] = {
-        {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL,
-         "bind(addresses)"},
-        {"gated", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gated)), METH_FASTCALL,
-         "gated(x, w_gate, w_up, n, act, save, path, const_weights)"},
-        {"backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(backward)), METH_FASTCALL,
-         "backward(dh, gate, up, w_gate, w_up, k, act)"},
-        {"lora", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(lora)), METH_FASTCALL,
+        {"bind", fast(bind), METH_FASTCALL, "bind(addresses)"},
+        {"bind_experts", fast(bind_experts), METH_FASTCALL, "bind_experts(addresses)"},
+        {"gated", fast(gated), METH_FASTCALL,
+         "gated(x, w_gate, w_up, n, act, save, path, const_weights[, offsets])"},
+        {"backward", fast(backward), METH_FASTCALL, "backward(dh, gate, up, w_gate, w_up, k, act[, offsets])"},
+        {"lora", fast(lora), METH_FASTCALL,
          "lora(x, w, n, lora_a, lora_b, ids, scales, path, const_weights)"},
+        {"linear", fast(linear), METH_FASTCALL,
+         "linear(x, w, n, bias, act, residual, save, path, const_weights, offsets)"},
+        {"linear_backward", fast(linear_backward), METH_FASTCALL,
+         "linear_backward(dy, w, k, z, act, bias, offsets)"},
+        {"route", fast(route), METH_FASTCALL, "route(ids, n_experts)"},
+        {"sort", fast(sort<false>), METH_FASTCALL, "sort(x, rows, offsets)"},
+        {"sort_backward", fast(sort<true>), METH_FASTCALL, "sort_backward(dxs, rows, offsets)"},
+        {"combine", fast(combine), METH_FASTCALL, "combine(ys, rows, offsets, weights, residual)"},
+        {"combine_backward", fast(combine_backward), METH_FASTCALL,
+         "combine_backward(dy, ys, rows, offsets, weights)"},
         {nullptr, nullptr, 0, nullptr}};
     static PyModuleDef module = {PyModuleDef_HEAD_INIT, "q2k_torch",
                                  "libq2k's feed-forward calls for PyTorch tensors.", -1, methods,
