@@ -77,8 +77,12 @@ struct Plan {
     size_t partial, counts;  // bytes of workspace
 };
 
-// The most tiles of `rows` tokens that M tokens in `segments` segments have.
-inline int segment_tiles(int M, int segments, int rows) { return M / rows + std::min(M, segments); }
+// The most tiles of `rows` tokens that M tokens in `segments` segments have: every
+// segment's last one may be a token's.
+inline int segment_tiles(int M, int segments, int rows) {
+    const int last = std::min(M, segments);
+    return last + (M - last) / rows;
+}
 
 // rows: those of the product; quads: its K in blocks (backward: 256 weight rows).
 // Tokens per tile: as few as hold them all up to 64.  Above, 128 or 256,

@@ -843,13 +843,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
 // The passes over tokens are a grid's y: of more than it holds, the rest go to
 // further launches (of the same kernel: a token's result is the same in each).
 constexpr int kMaxPasses = 65535;
-constexpr int kTableWaves = 2;
+constexpr int kTableWaves = 1;
 
 // CTAs (or clusters) of a launch that divide the weight rows' units: those that the GPU
 // holds, over the token tiles that there could be.
 int unit_ctas(const RowsArgs& p, int most, int units) {
     if (p.table == nullptr) return std::min(most, units);
-    return std::min(units, std::max(1, (kTableWaves * most + p.capacity - 1) / p.capacity));
+    return std::min(units, std::max(1, kTableWaves * most / p.capacity));
 }
 
 // Calls `launch(x, args, passes)` for each run of at most kMaxPasses passes of kTokens.

@@ -434,27 +434,6 @@ __device__ __forceinline__ void add_adapters(float* sums, uint32_t* tbuf, const 
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_pair(T* dst, float a, float b, int valid, bool vec);
-template <>
-__device__ __forceinline__ void store_pair(float* dst, float a, float b, int valid, bool vec) {
-    if (vec) {
-        *reinterpret_cast<float2*>(dst) = make_float2(a, b);
-    } else {
-        if (valid > 0) dst[0] = a;
-        if (valid > 1) dst[1] = b;
-    }
-}
-template <>
-__device__ __forceinline__ void store_pair(__nv_bfloat16* dst, float a, float b, int valid, bool vec) {
-    if (vec) {
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(a, b);
-    } else {
-        if (valid > 0) dst[0] = __float2bfloat16_rn(a);
-        if (valid > 1) dst[1] = __float2bfloat16_rn(b);
-    }
-}
-
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -506,100 +485,104 @@ __device__ __forceinline__ void decode_segment(const uint32_t (&q)[4], uint32_t 
     }
 }
 
+// Four neighbouring values of a row, `valid` (1 or more) of them inside it; `run`: how
+// many of them are one aligned word (the rows' length in 4, 2 or 1 values).
 template <typename T>
-__device__ __forceinline__ float2 load_pair(const T* src, int valid, bool vec);
-template <>
-__device__ __forceinline__ float2 load_pair(const float* src, int valid, bool vec) {
-    if (vec) return __ldg(reinterpret_cast<const float2*>(src));
-    return make_float2(valid > 0 ? __ldg(src) : 0.f, valid > 1 ? __ldg(src + 1) : 0.f);
-}
-template <>
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* src, int valid, bool vec) {
-    if (vec) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src));
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+__device__ __forceinline__ void store_quad(T* dst, float4 v, int valid, int run) {
+    if (run == 4) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(dst) = v;
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    } else if (run == 2) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2*>(dst) = make_float2(v.x, v.y);
+            if (valid > 2) *reinterpret_cast<float2*>(dst + 2) = make_float2(v.z, v.w);
+        } else {
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v.x, v.y);
+            if (valid > 2) *reinterpret_cast<uint32_t*>(dst + 2) = pack_bf16(v.z, v.w);
+        }
+    } else {
+        dst[0] = from_float<T>(v.x);
+        if (valid > 1) dst[1] = from_float<T>(v.y);
+        if (valid > 2) dst[2] = from_float<T>(v.z);
+        if (valid > 3) dst[3] = from_float<T>(v.w);
     }
-    return make_float2(valid > 0 ? to_float(src[0]) : 0.f, valid > 1 ? to_float(src[1]) : 0.f);
+}
+template <typename T>
+__device__ __forceinline__ float4 load_quad(const T* src, int valid, int run) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (run == 4) {
+        if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const float4*>(src));
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    }
+    v.x = to_float(src[0]);
+    if (valid > 1) v.y = to_float(src[1]);
+    if (valid > 2) v.z = to_float(src[2]);
+    if (valid > 3) v.w = to_float(src[3]);
+    return v;
 }
 
-// The same for one matrix: z = sum + bias, y = act(z) + residual.  A warp takes four
-// tokens at a time, so that their residuals are on their way together.
-template <typename T>
-__device__ __forceinline__ void emit_linear(const TcArgs& p, const float* sums, int n0, int rows, int m0,
-                                            int count, int expert, const Team& team) {
-    constexpr int kAtOnce = 4;
-    const int lane = team.thread & 31, warps = team.threads >> 5;
-    const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
-    const int valid[2] = {rows - (n0 + 2 * lane), rows - (n0 + 2 * lane) - 64};
-    float2 bias[2];
+// Results of `count` tokens (m0 on) of a tile from their sums.  A lane takes four
+// neighbouring rows of a token, a warp a token's 128 rows (gated: two tokens' 64).
+// (In twos the four warps' instructions bounded short products: 64 experts of 64
+// tokens, 7168 x 2048, 343 us against 311.)
+template <Tc kMode, typename T>
+__device__ __forceinline__ void emit(const TcArgs& p, const float* sums, int n0, int rows, int m0,
+                                     int count, int expert, const Team& team) {
+    constexpr int kLanes = kMode == Tc::kGated ? 16 : 32;  // of a token
+    // tokens of a lane at a time: their residuals are on their way together
+    constexpr int kAtOnce = kMode == Tc::kLinear ? 4 : 1;
+    const int lane = team.thread & 31, at = 4 * (lane % kLanes);
+    const int first = (team.thread >> 5) * (32 / kLanes) + lane / kLanes, step = (team.threads >> 5) * (32 / kLanes);
+    const int valid = rows - (n0 + at);
+    const int run = (rows & 3) == 0 ? 4 : (rows & 1) == 0 ? 2 : 1;  // (n0 + at is a multiple of four)
+    if (valid <= 0) return;
+    [[maybe_unused]] float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (kMode == Tc::kLinear && p.bias != nullptr)
+        bias = load_quad(p.bias + static_cast<size_t>(expert) * rows + n0 + at, valid, run);
+    for (int c0 = first; c0 < count; c0 += kAtOnce * step) {
+        [[maybe_unused]] float4 r[kAtOnce];
+        if constexpr (kMode == Tc::kLinear) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        bias[q] = make_float2(0.f, 0.f);
-        if (p.bias != nullptr && valid[q] > 0)
-            bias[q] = load_pair(p.bias + static_cast<size_t>(expert) * rows + n0 + 2 * lane + 64 * q, valid[q],
-                                vec);
-    }
-    for (int c0 = team.thread >> 5; c0 < count; c0 += kAtOnce * warps) {
-        float2 r[kAtOnce][2];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int c = c0 + u * warps;
-                r[u][q] = make_float2(0.f, 0.f);
-                if (p.residual != nullptr && c < count && valid[q] > 0)
-                    r[u][q] = load_pair(static_cast<const T*>(p.residual) + static_cast<size_t>(m0 + c) * rows +
-                                            n0 + 2 * lane + 64 * q, valid[q], vec);
+            for (int u = 0; u < kAtOnce; ++u) {
+                r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.residual != nullptr && c0 + u * step < count)
+                    r[u] = load_quad(static_cast<const T*>(p.residual) +
+                                         static_cast<size_t>(m0 + c0 + u * step) * rows + n0 + at, valid, run);
             }
+        }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int c = c0 + u * warps;
+            const int c = c0 + u * step;
             if (c >= count) break;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (valid[q] <= 0) continue;
-                const size_t at = static_cast<size_t>(m0 + c) * rows + n0 + 2 * lane + 64 * q;
-                float2 v = *reinterpret_cast<const float2*>(sums + c * kSumPitch + 2 * lane + 64 * q);
-                v.x += bias[q].x;
-                v.y += bias[q].y;
-                if (p.z != nullptr) store_pair(static_cast<T*>(p.z) + at, v.x, v.y, valid[q], vec);
+            const float* row = sums + c * kSumPitch + at;
+            const size_t to = static_cast<size_t>(m0 + c) * rows + n0 + at;
+            float4 v = *reinterpret_cast<const float4*>(row);
+            if constexpr (kMode == Tc::kGated) {
+                const float4 w = *reinterpret_cast<const float4*>(row + kRows / 2);
+                if (p.gate != nullptr) {
+                    store_quad(static_cast<T*>(p.gate) + to, v, valid, run);
+                    store_quad(static_cast<T*>(p.up) + to, w, valid, run);
+                }
+                v.x = act_value<sizeof(T) == 2>(v.x, p.act) * w.x;
+                v.y = act_value<sizeof(T) == 2>(v.y, p.act) * w.y;
+                v.z = act_value<sizeof(T) == 2>(v.z, p.act) * w.z;
+                v.w = act_value<sizeof(T) == 2>(v.w, p.act) * w.w;
+                store_quad(static_cast<T*>(p.h) + to, v, valid, run);
+            } else if constexpr (kMode == Tc::kLinear) {
+                v = make_float4(v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w);
+                if (p.z != nullptr) store_quad(static_cast<T*>(p.z) + to, v, valid, run);
                 if (p.act != kActNone) {
                     v.x = act_value<sizeof(T) == 2>(v.x, p.act);
                     v.y = act_value<sizeof(T) == 2>(v.y, p.act);
+                    v.z = act_value<sizeof(T) == 2>(v.z, p.act);
+                    v.w = act_value<sizeof(T) == 2>(v.w, p.act);
                 }
-                store_pair(static_cast<T*>(p.y) + at, v.x + r[u][q].x, v.y + r[u][q].y, valid[q], vec);
-            }
-        }
-    }
-}
-
-// Results of `count` tokens (m0 on) of a tile from their sums.
-template <Tc kMode, typename T>
-__device__ __forceinline__ void emit(const TcArgs& p, const float* sums, int n0, int rows, int m0,
-                                     int count, const Team& team) {
-    const int lane = team.thread & 31;
-    const bool vec = (rows & 1) == 0;  // (n0 is even: pairs are aligned)
-    // a warp takes a token at a time, a lane neighbouring rows
-    for (int c = team.thread >> 5; c < count; c += team.threads >> 5) {
-        const float* row = sums + c * kSumPitch + 2 * lane;
-        const size_t at = static_cast<size_t>(m0 + c) * rows + n0 + 2 * lane;
-        const int valid = rows - (n0 + 2 * lane);
-        if constexpr (kMode == Tc::kGated) {
-            if (valid <= 0) continue;
-            const float2 g = *reinterpret_cast<const float2*>(row);
-            const float2 u = *reinterpret_cast<const float2*>(row + kRows / 2);
-            store_pair(static_cast<T*>(p.h) + at, act_value<sizeof(T) == 2>(g.x, p.act) * u.x,
-                       act_value<sizeof(T) == 2>(g.y, p.act) * u.y, valid, vec);
-            if (p.gate != nullptr) {
-                store_pair(static_cast<T*>(p.gate) + at, g.x, g.y, valid, vec);
-                store_pair(static_cast<T*>(p.up) + at, u.x, u.y, valid, vec);
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float2 v = *reinterpret_cast<const float2*>(row + 64 * q);
-                if (valid - 64 * q > 0)
-                    store_pair(static_cast<T*>(p.y) + at + 64 * q, v.x, v.y, valid - 64 * q, vec);
+                store_quad(static_cast<T*>(p.y) + to,
+                           make_float4(v.x + r[u].x, v.y + r[u].y, v.z + r[u].z, v.w + r[u].w), valid, run);
+            } else {
+                store_quad(static_cast<T*>(p.y) + to, v, valid, run);
             }
         }
     }
@@ -1103,10 +1086,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             add_adapters(base - slot0 * kSumPitch, tbuf, id_buf + slot0 + slot, id_buf + kX + slot0 + slot,
                          p, n0, m - slot0, count, team);
         }
-        if constexpr (kMode == Tc::kLinear)
-            emit_linear<T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, expert_of(tile), team);
-        else
-            emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
+        emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count,
+                       kMode == Tc::kLinear ? expert_of(tile) : 0, team);
     };
     const bool brings_out = warp < kDecWarps || warp >= kEpiWarp0;
     if (brings_out) {
@@ -1423,9 +1404,9 @@ struct LinearGradArgs {
     int M, N, pitch, act;
     int shares;               // CTAs of a segment and 256 columns (with dbias: a cluster)
 };
-constexpr int kGradCols = 256, kGradWarps = 8, kGradAtOnce = 4;
+constexpr int kGradCols = 256, kGradWarps = 8, kGradAtOnce = 2;
 
-__global__ void __launch_bounds__(32 * kGradWarps) linear_grad_kernel(LinearGradArgs p) {
+__global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearGradArgs p) {
     __shared__ float red[kGradWarps][kGradCols];
     __shared__ float part[kGradCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

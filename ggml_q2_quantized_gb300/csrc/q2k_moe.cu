@@ -57,6 +57,7 @@ __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr, uint32_t ran
 constexpr int kRouteMaxCtas = 8;
 constexpr int kRouteWarps = 16, kRouteWarpsMany = 8;  // (more bins than kRouteFewBins)
 constexpr int kRouteFewBins = 2048;
+constexpr int kRouteEach = 32;
 
 struct RouteArgs {
     const int* ids;
@@ -86,13 +87,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs p) {
     int* mine = count + warp * bins;
     int bad = 0;
     constexpr int kAhead = 4;
-    for (int base = first; base < last; base += 32 * kAhead) {
-        int id[kAhead];
+    int id[kAhead];
+    auto load = [&](int base) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = base + 32 * u + lane;
             id[u] = i < last ? __ldg(p.ids + i) : -2;
         }
+    };
+    for (int base = first; base < last; base += 32 * kAhead) {
+        load(base);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const bool in = base + 32 * u + lane < last;
@@ -165,12 +169,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs p) {
     if (ctas > 1) cluster_arrive();  // (the others' totals are read)
     __syncthreads();
     for (int base = first; base < last; base += 32 * kAhead) {
-        int id[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = base + 32 * u + lane;
-            id[u] = i < last ? __ldg(p.ids + i) : -2;
-        }
+        if (p.each > 32 * kAhead) load(base);  // (else they are here)
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = base + 32 * u + lane;
@@ -215,6 +214,32 @@ struct Pack {
     };
     __device__ __forceinline__ Pack() : word() {}
     __device__ __forceinline__ void load(const T* p) { word = __ldg(reinterpret_cast<const W*>(p)); }
+    // Load if `in`, without a branch, and where it stands: loads of several rows are then
+    // all asked for before the first is used.  (Left to itself the compiler moved each
+    // to its use.)
+    __device__ __forceinline__ void load_if(const T* p, bool in) {
+        const int ok = in;
+        if constexpr (sizeof(W) == 16)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
+                "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                : "+r"(bits[0]), "+r"(bits[1]), "+r"(bits[2]), "+r"(bits[3])
+                : "l"(p), "r"(ok));
+        else if constexpr (sizeof(W) == 8)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+                "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                : "+r"(bits[0]), "+r"(bits[1])
+                : "l"(p), "r"(ok));
+        else if constexpr (sizeof(W) == 4)
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                         : "+r"(bits[0])
+                         : "l"(p), "r"(ok));
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+                         : "+h"(half[0])
+                         : "l"(p), "r"(ok));
+    }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<W*>(p) = word; }
     __device__ __forceinline__ float get(int v) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(bits[v]);
@@ -267,44 +292,48 @@ __global__ void __launch_bounds__(kMoveThreads) sort_kernel(MoveArgs p) {
 }
 
 // y[t] = residual[t] + sum_s weights[t, s] ys[rows[t, s]], over the slots that have an
-// expert (what another's place holds is not read).
+// expert (what another's place holds is not read).  A thread has eight rows' words on
+// their way at once; of eight bytes each, so that many CTAs fit: between the places'
+// arrival and the rows' a CTA asks for nothing.  (512 tokens of eight rows of 14336
+// bytes, 66 MB: words of 16 bytes 23 us, of 8 bytes 14.)
 template <typename T, int V>
 __global__ void __launch_bounds__(kMoveThreads) combine_kernel(MoveArgs p) {
     pdl_allow_dependents();
     pdl_wait_prerequisites();
-    const int t = blockIdx.x / p.chunks;
+    const int t = blockIdx.x / p.chunks, lane = threadIdx.x & 31;
     const int u = (blockIdx.x - t * p.chunks) * blockDim.x + threadIdx.x;
-    if (u >= p.units) return;
+    const bool in = u < p.units;
     const size_t mine = static_cast<size_t>(t) * p.width + static_cast<size_t>(u) * V;
     const T* ys = static_cast<const T*>(p.in) + static_cast<size_t>(u) * V;
     const size_t slot0 = static_cast<size_t>(t) * p.top_k;
     const unsigned end = static_cast<unsigned>(min(max(__ldg(p.offsets + p.experts), 0), p.routes));
     float sum[V];
     Pack<T, V> r;
-    if (p.residual != nullptr) r.load(static_cast<const T*>(p.residual) + mine);
+    if (in && p.residual != nullptr) r.load(static_cast<const T*>(p.residual) + mine);
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[v] = r.get(v);
     for (int s0 = 0; s0 < p.top_k; s0 += kSlots) {
+        // a lane has one of the places and weights
+        const bool slot = lane < kSlots && s0 + lane < p.top_k;
+        const int place = slot ? __ldg(p.rows + slot0 + s0 + lane) : -1;
+        const float weight = slot && p.weights != nullptr ? __ldg(p.weights + slot0 + s0 + lane) : 1.f;
+        int at[kSlots];
         Pack<T, V> a[kSlots];
-        float w[kSlots];
-        bool in[kSlots];
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            const int at = s0 + s < p.top_k ? __ldg(p.rows + slot0 + s0 + s) : -1;
-            in[s] = static_cast<unsigned>(at) < end;
-            w[s] = 1.f;
-            if (in[s]) {
-                a[s].load(ys + static_cast<size_t>(at) * p.width);
-                if (p.weights != nullptr) w[s] = __ldg(p.weights + slot0 + s0 + s);
-            }
+            at[s] = __shfl_sync(0xFFFFFFFFu, place, s);
+            a[s].load_if(ys + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width,
+                         in && static_cast<unsigned>(at[s]) < end);
         }
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            if (!in[s]) continue;
+            const float w = __shfl_sync(0xFFFFFFFFu, weight, s);
+            if (static_cast<unsigned>(at[s]) >= end) continue;
 #pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] = fmaf(w[s], a[s].get(v), sum[v]);
+            for (int v = 0; v < V; ++v) sum[v] = fmaf(w, a[s].get(v), sum[v]);
         }
     }
+    if (!in) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) r.set(v, sum[v]);
     r.store(static_cast<T*>(p.out) + mine);
@@ -354,8 +383,8 @@ __global__ void __launch_bounds__(kMoveThreads) combine_backward_kernel(BackArgs
             g.load(dy + col);
 #pragma unroll
             for (int s = 0; s < kSlots; ++s)
-                if (static_cast<unsigned>(at[s]) < end)
-                    a[s].load(static_cast<const T*>(p.ys) + static_cast<size_t>(at[s]) * p.width + col);
+                a[s].load_if(static_cast<const T*>(p.ys) + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width + col,
+                             static_cast<unsigned>(at[s]) < end);
 #pragma unroll
             for (int s = 0; s < kSlots; ++s) {
                 if (static_cast<unsigned>(at[s]) >= static_cast<unsigned>(p.routes)) continue;
@@ -456,9 +485,10 @@ cudaError_t launch_move(const MoeMoveArgs& a, cudaStream_t stream) {
     p.routes = a.n_tokens * a.top_k;
     p.experts = a.n_experts;
     p.width = a.width;
-    const int bytes = word_bytes(static_cast<size_t>(a.width) * sizeof(T),
-                                 reinterpret_cast<uintptr_t>(a.in) | reinterpret_cast<uintptr_t>(a.out) |
-                                     reinterpret_cast<uintptr_t>(a.residual));
+    const int bytes = std::min(kCombine ? 8 : 16,
+                               word_bytes(static_cast<size_t>(a.width) * sizeof(T),
+                                          reinterpret_cast<uintptr_t>(a.in) | reinterpret_cast<uintptr_t>(a.out) |
+                                              reinterpret_cast<uintptr_t>(a.residual)));
     return with_values<T>(bytes, [&](auto values) {
         constexpr int V = decltype(values)::value;
         p.units = a.width / V;
@@ -504,7 +534,6 @@ cudaError_t launch_back(const MoeBackArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
     const int bins = a.n_experts + 1;
-    const int warps = bins <= kRouteFewBins ? kRouteWarps : kRouteWarpsMany;
     RouteArgs p = {};
     p.ids = a.ids;
     p.rows = a.rows;
@@ -513,9 +542,12 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
     p.bad_ids = a.bad_ids;
     p.routes = a.n_tokens * a.top_k;
     p.experts = a.n_experts;
-    // as many CTAs as leave a warp 32 choices or more
+    // a warp takes 32 choices, and up to kRouteEach before further CTAs share them: the
+    // walks over warps and CTAs cost as much as the steps that they save
+    const int most = bins <= kRouteFewBins ? kRouteWarps : kRouteWarpsMany;
+    const int warps = std::min(most, (p.routes + 31) / 32);
     int ctas = 1;
-    while (ctas < kRouteMaxCtas && ctas * warps * 32 < p.routes) ctas *= 2;
+    while (ctas < kRouteMaxCtas && ctas * warps * kRouteEach < p.routes) ctas *= 2;
     p.each = ((p.routes + ctas * warps - 1) / (ctas * warps) + 31) & ~31;
     const size_t smem = (static_cast<size_t>(warps + 2) * bins + 1) * 4;
     static std::atomic<bool> attr_done[64] = {};  // (set by any thread; setting twice does no harm)
