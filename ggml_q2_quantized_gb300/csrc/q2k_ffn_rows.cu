@@ -478,6 +478,8 @@ struct RowsArgs {
     const int4* table;
     const int* table_count;
     int capacity, entry0;
+    const int* offsets;   // of the segments (tiles of one token, without a table)
+    int segments;
     // streamed tiles
     int depth;            // units in flight
     int parts;            // CTAs of a cluster that divide K
@@ -486,20 +488,44 @@ struct RowsArgs {
 
 enum class Rows { kGated, kLora, kLinear };
 
+// The segment of token m: the last that begins at it or before, or -1.  By a warp: a
+// thirty-second of the offsets each, then those of the part that it falls in.
+__device__ __forceinline__ int segment_of(const int* __restrict__ offsets, int segments, int m) {
+    const int lane = threadIdx.x & 31, each = (segments + 32) / 32;
+    const int i = lane * each;
+    const bool from = i <= segments && offsets[min(i, segments)] <= m;
+    const int part = __popc(__ballot_sync(0xFFFFFFFFu, from)) - 1;
+    if (part < 0) return -1;
+    int before = 0;
+    for (int j = lane; j < each; j += 32) {
+        const int at = part * each + j;
+        before += at <= segments && offsets[min(at, segments)] <= m;
+    }
+    const int e = part * each + __reduce_add_sync(0xFFFFFFFFu, before) - 1;
+    return e < segments ? e : -1;
+}
+
 // Whose tokens and matrices a CTA takes: all of the call's, or (kTable) a tile of a
-// segment's.
+// segment's: of the table, or where a tile is one token (kOne) the token itself, whose
+// segment costs two loads to find and the table a launch.
 struct Part {
     int m0, M;  // first token, and the end of those that the CTA may take
     int expert;
     const uint8_t* w0;
     const uint8_t* w1;
 };
-template <bool kTable>
+template <bool kTable, bool kOne>
 __device__ __forceinline__ bool take_part(const RowsArgs& p, int tokens, Part& part) {
     if constexpr (kTable) {
         const int at = p.entry0 + static_cast<int>(blockIdx.y);
-        if (at >= *p.table_count) return false;
-        const int4 t = p.table[at];
+        int4 t;
+        if constexpr (kOne) {
+            t = make_int4(segment_of(p.offsets, p.segments, at), at, 1, 0);
+            if (t.x < 0) return false;
+        } else {
+            if (at >= *p.table_count) return false;
+            t = p.table[at];
+        }
         const size_t matrix = static_cast<size_t>(p.N) * (p.K / kQK) * kBlockBytes;
         part = {t.y, t.y + t.z, t.x, p.w0 + t.x * matrix, p.w1 + t.x * matrix};
     } else {
@@ -691,12 +717,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const int group = warp / p.kw, kw = warp - group * p.kw;
-    pdl_allow_dependents();
+    if (!kTable && kMode != Rows::kLinear) pdl_allow_dependents();
     if (group >= p.groups) return;  // (no barrier counts these warps)
     bool waited = kTable;
-    if (kTable) pdl_wait_prerequisites();
+    if (kTable) {
+        pdl_wait_prerequisites();
+        pdl_allow_dependents();
+    }
     Part part;
-    if (!take_part<kTable>(p, kTokens, part)) return;
+    if (!take_part<kTable, false>(p, kTokens, part)) return;
     const int m0 = part.m0;
     const int blocks = p.K / kQK;
     const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
@@ -768,6 +797,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
             if (!waited && !p.x_ready) {
                 pdl_wait_prerequisites();
                 waited = true;
+                if (kMode == Rows::kLinear) pdl_allow_dependents();
             }
             XBlock<T> xb[S][NT];
 #pragma unroll
@@ -848,14 +878,14 @@ constexpr int kTableWaves = 1;
 // CTAs (or clusters) of a launch that divide the weight rows' units: those that the GPU
 // holds, over the token tiles that there could be.
 int unit_ctas(const RowsArgs& p, int most, int units) {
-    if (p.table == nullptr) return std::min(most, units);
+    if (p.capacity == 0) return std::min(most, units);
     return std::min(units, std::max(1, kTableWaves * most / p.capacity));
 }
 
 // Calls `launch(x, args, passes)` for each run of at most kMaxPasses passes of kTokens.
 template <typename T, int kTokens, typename Launch>
 cudaError_t launch_passes(const T* x, const RowsArgs& p, Launch&& launch) {
-    if (p.table != nullptr) {  // (tiles instead of passes)
+    if (p.capacity != 0) {  // (tiles instead of passes)
         for (int first = 0; first < p.capacity; first += kMaxPasses) {
             RowsArgs q = p;
             q.entry0 = first;
@@ -957,11 +987,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     const int lane = threadIdx.x & 31;
     bool waited = kTable;
     if (kTable) {
-        pdl_allow_dependents();
         pdl_wait_prerequisites();
+        pdl_allow_dependents();
     }
     Part part;
-    if (!take_part<kTable>(p, kTokens, part)) return;  // (all of a cluster)
+    if (!take_part<kTable, NT == 0>(p, kTokens, part)) return;  // (all of a cluster)
     const int m0 = part.m0;
     const int rank = static_cast<int>(blockIdx.x) % p.parts, first_unit = static_cast<int>(blockIdx.x) / p.parts;
     const int unit_step = static_cast<int>(gridDim.x) / p.parts;
@@ -1013,7 +1043,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                           src + (lane & 15) * row_bytes + static_cast<size_t>(b0) * kBlockBytes, pitch, bar);
         }
     };
-    if (!kTable) pdl_allow_dependents();
+    // (one matrix: below, once all before this grid is complete, so that a call behind it
+    // that reads its weights early finds them written)
+    if (!kTable && kMode != Rows::kLinear) pdl_allow_dependents();
     if (warp == 0) {
         if (lane == 0) {
             *abort_flag = 0;
@@ -1033,6 +1065,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         pdl_wait_prerequisites();
         waited = true;
     }
+    if (!kTable && kMode == Rows::kLinear) pdl_allow_dependents();
     XBytes xi;
     [[maybe_unused]] float undo = 0.f;
     [[maybe_unused]] bool wide = false;
@@ -1168,7 +1201,7 @@ bool plan_stream(RowsArgs& p, size_t& smem) {
     const int blocks = p.K / kQK;
     if (blocks <= kWarps / 2) return false;
     if (((reinterpret_cast<uintptr_t>(p.w0) | reinterpret_cast<uintptr_t>(p.w1)) & 15) != 0) return false;
-    if (p.table != nullptr && static_cast<size_t>(p.N) * blocks * kBlockBytes % 16 != 0) return false;
+    if (p.capacity != 0 && static_cast<size_t>(p.N) * blocks * kBlockBytes % 16 != 0) return false;
     p.parts = (blocks + kWarps - 1) / kWarps;
     if (p.parts > 1 && (p.parts > kMaxRowParts || blocks % 4 != 0)) return false;
     const size_t fixed = kWarps * 2 * 2 * Pass<T, NT>::kSums * 4 + 4 * (Pass<T, NT>::kSums + kMaxRowParts) * 8 +
@@ -1252,11 +1285,17 @@ template <Rows kMode>
 cudaError_t launch_rows_table(const void* x, RowsArgs& p, const int* offsets, int segments, bool bf16,
                               void* workspace, int device, int sm_count, cudaStream_t stream) {
     const int tokens = tile_tokens(p.M, segments, bf16);
-    const cudaError_t e = launch_ffn_table(offsets, segments, p.M, tokens, workspace, sm_count, stream);
-    if (e != cudaSuccess) return e;
-    p.table_count = static_cast<const int*>(workspace);
-    p.table = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(workspace) + 16);
     p.capacity = segment_tiles(p.M, segments, tokens);
+    p.offsets = offsets;
+    p.segments = segments;
+    size_t smem = 0;
+    const bool one = tokens == 1 && (bf16 ? plan_stream<__nv_bfloat16, 0>(p, smem) : plan_stream<float, 0>(p, smem));
+    if (!one) {
+        const cudaError_t e = launch_ffn_table(offsets, segments, p.M, tokens, workspace, sm_count, stream);
+        if (e != cudaSuccess) return e;
+        p.table_count = static_cast<const int*>(workspace);
+        p.table = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(workspace) + 16);
+    }
     return bf16 ? launch_rows_mode<__nv_bfloat16, kMode, true>(x, p, tokens, device, sm_count, stream)
                 : launch_rows_mode<float, kMode, true>(x, p, tokens, device, sm_count, stream);
 }

@@ -16,6 +16,9 @@
 // `rows` is a permutation of all n_tokens * top_k places: choices without an expert
 // come last, from offsets[n_experts] on.  Their places are written as zeros and
 // never read.
+//
+// Each kernel lets the next grid start once all before itself are complete: a call
+// behind it that reads its weights early then finds them written.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -78,9 +81,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs p) {
     int* count = route_smem;               // [warps][bins]
     int* total = count + warps * bins;     // [bins + 1]: this CTA's, and its bad ids
     int* start = total + bins + 1;         // [bins]
-    pdl_allow_dependents();
     for (int i = tid; i < (warps + 1) * bins + 1; i += threads) count[i] = 0;
     pdl_wait_prerequisites();
+    pdl_allow_dependents();
     __syncthreads();
     const int first = (rank * warps + warp) * p.each;
     const int last = min(p.routes, first + p.each);
@@ -269,8 +272,8 @@ constexpr int kSlots = 8;  // places taken together: that many loads on their wa
 // xs[rows[t, s]] = x[t]; a place without an expert gets zeros.
 template <typename T, int V>
 __global__ void __launch_bounds__(kMoveThreads) sort_kernel(MoveArgs p) {
-    pdl_allow_dependents();
     pdl_wait_prerequisites();
+    pdl_allow_dependents();
     const int t = blockIdx.x / p.chunks;
     const int u = (blockIdx.x - t * p.chunks) * blockDim.x + threadIdx.x;
     if (u >= p.units) return;
@@ -298,8 +301,8 @@ __global__ void __launch_bounds__(kMoveThreads) sort_kernel(MoveArgs p) {
 // bytes, 66 MB: words of 16 bytes 23 us, of 8 bytes 14.)
 template <typename T, int V>
 __global__ void __launch_bounds__(kMoveThreads) combine_kernel(MoveArgs p) {
-    pdl_allow_dependents();
     pdl_wait_prerequisites();
+    pdl_allow_dependents();
     const int t = blockIdx.x / p.chunks, lane = threadIdx.x & 31;
     const int u = (blockIdx.x - t * p.chunks) * blockDim.x + threadIdx.x;
     const bool in = u < p.units;
@@ -359,8 +362,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kMoveThreads) combine_backward_kernel(BackArgs p) {
     __shared__ float part[kMoveThreads / 32][kSlots];
     __shared__ float mine[kSlots];
-    pdl_allow_dependents();
     pdl_wait_prerequisites();
+    pdl_allow_dependents();
     const int t = blockIdx.x / p.parts, rank = blockIdx.x - t * p.parts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const size_t slot0 = static_cast<size_t>(t) * p.top_k;
