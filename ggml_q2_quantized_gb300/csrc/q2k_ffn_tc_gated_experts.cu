@@ -1,0 +1,11 @@
+// The tensor-core kernel's gated block of tokens in segments.
+#include "q2k_ffn_tc_kernel.cuh"
+
+namespace q2k {
+
+template cudaError_t launch_tc<Tc::kGated, __nv_bfloat16, true>(TcArgs, const Plan&, uint8_t*, const void*, const void*,
+                                                       int, int, int, cudaStream_t, int);
+template cudaError_t launch_tc<Tc::kGated, float, true>(TcArgs, const Plan&, uint8_t*, const void*, const void*,
+                                                       int, int, int, cudaStream_t, int);
+
+}  // namespace q2k

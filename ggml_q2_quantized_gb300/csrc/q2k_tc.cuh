@@ -262,12 +262,13 @@ __device__ __forceinline__ uint32_t code_selectors(uint32_t word) {
 // cuTensorMapEncodeTiled through the runtime's driver entry point (null when
 // the driver has none).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
-// Raw Q2_K weights as a 3-D byte tensor (`matrices` of N rows of K/256 * 84 bytes, one
-// after another) with a box of `rows` rows x 112 bytes of one matrix; false unless rows
-// are multiples of 16 bytes (K a multiple of 1024) and the base is 16-byte aligned.
+// Raw Q2_K weights as a 2-D byte tensor (N rows of K/256 * 84 bytes) with a box
+// of `rows` rows x 112 bytes; false unless rows are multiples of 16 bytes (K a
+// multiple of 1024) and the base is 16-byte aligned.
 // (of `group` rows together as one of the map's; false if those do not start at 16 bytes)
-bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group,
-                     int matrices = 1);
+// matrices > 0: that many such matrices, one after another, as a 3-D tensor with boxes
+// of one.
+bool make_weight_map(CUtensorMap* map, const uint8_t* w, int N, int K, int rows, int group, int matrices);
 
 }  // namespace tc
 }  // namespace q2k
