@@ -251,8 +251,12 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 bool ffn_rows_path(int m, bool bf16) { return m <= (bf16 ? 16 : 8); }
 
+// In segments it reads a segment's weights once for 16 (8) tokens, the tensor kernel once
+// for up to 256 but half as fast.  64 experts, one of 2048 x 7168, us here and there:
+// bf16 256 tokens 152 and 198, 512 181 and 227, 1024 261 and 262; f32 256 tokens 172 and
+// 200, 512 238 and 231.  (7168 x 2048: bf16 512 192 and 224, 1024 279 and 253.)
 bool ffn_rows_path(int m, bool bf16, int n_experts) {
-    return ffn_rows_path(m, bf16) || (n_experts > 0 && m <= (bf16 ? 4 : 2) * n_experts);
+    return ffn_rows_path(m, bf16) || (n_experts > 0 && m <= (bf16 ? 8 : 4) * n_experts);
 }
 
 size_t gated_workspace_bytes(const GatedArgs& a) {

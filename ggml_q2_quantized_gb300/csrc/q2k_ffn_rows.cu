@@ -505,33 +505,24 @@ __device__ __forceinline__ int segment_of(const int* __restrict__ offsets, int s
     return e < segments ? e : -1;
 }
 
-// Whose tokens and matrices a CTA takes: all of the call's, or (kTable) a tile of a
-// segment's: of the table, or where a tile is one token (kOne) the token itself, whose
-// segment costs two loads to find and the table a launch.
+// Whose tokens and matrices a CTA takes: all of the call's, or a tile of a segment's.
 struct Part {
     int m0, M;  // first token, and the end of those that the CTA may take
     int expert;
-    const uint8_t* w0;
-    const uint8_t* w1;
-};
-template <bool kTable, bool kOne>
-__device__ __forceinline__ bool take_part(const RowsArgs& p, int tokens, Part& part) {
-    if constexpr (kTable) {
-        const int at = p.entry0 + static_cast<int>(blockIdx.y);
-        int4 t;
-        if constexpr (kOne) {
-            t = make_int4(segment_of(p.offsets, p.segments, at), at, 1, 0);
-            if (t.x < 0) return false;
-        } else {
-            if (at >= *p.table_count) return false;
-            t = p.table[at];
-        }
-        const size_t matrix = static_cast<size_t>(p.N) * (p.K / kQK) * kBlockBytes;
-        part = {t.y, t.y + t.z, t.x, p.w0 + t.x * matrix, p.w1 + t.x * matrix};
-    } else {
-        part = {static_cast<int>(blockIdx.y) * tokens, p.M, 0, p.w0, p.w1};
+    __device__ __forceinline__ const uint8_t* of(const uint8_t* w, const RowsArgs& p) const {
+        return w + static_cast<size_t>(p.N) * (p.K / kQK) * kBlockBytes * expert;
     }
-    return true;
+};
+// Tile `at` of the table.
+__device__ __forceinline__ Part table_part(const RowsArgs& p, int at) {
+    const int4 t = p.table[at];
+    return {t.y, t.y + t.z, t.x};
+}
+// Token m as a tile of its own (by a warp): its segment costs two loads to find, where a
+// table costs a launch.
+__device__ __forceinline__ Part token_part(const RowsArgs& p, int m) {
+    const int e = segment_of(p.offsets, p.segments, m);
+    return {m, e < 0 ? m : m + 1, max(e, 0)};
 }
 
 __device__ __forceinline__ void cp_async_word(uint32_t dst, const void* src, uint32_t bytes) {
@@ -633,7 +624,7 @@ __device__ __forceinline__ void finish_row(const T* x, const RowsArgs& p, const 
             const int na = n + a * p.tile1_row;
             if (fabsf(a ? v[1] : v[0]) <= 3.402823466e38f || na >= p.N) continue;
             const float sum = sum_not_finite(x + static_cast<size_t>(m) * p.K,
-                                             (a ? part.w1 : part.w0) + static_cast<size_t>(na) * (p.K / kQK) * kBlockBytes,
+                                             part.of(a ? p.w1 : p.w0, p) + static_cast<size_t>(na) * (p.K / kQK) * kBlockBytes,
                                              p.K);
             v[0] = a ? v[0] : sum;
             v[1] = a ? sum : v[1];
@@ -724,9 +715,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
         pdl_wait_prerequisites();
         pdl_allow_dependents();
     }
-    Part part;
-    if (!take_part<kTable, false>(p, kTokens, part)) return;
+    Part part = {static_cast<int>(blockIdx.y) * kTokens, p.M, 0};
+    if (kTable) {
+        const int at = p.entry0 + static_cast<int>(blockIdx.y);
+        if (at >= *p.table_count) return;
+        part = table_part(p, at);
+    }
     const int m0 = part.m0;
+    const uint8_t *const w0 = part.of(p.w0, p), *const w1 = part.of(p.w1, p);
     const int blocks = p.K / kQK;
     const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
     const uint32_t ring = smem_u32(smem) + warp * kDepth * kItemBytes;
@@ -756,7 +752,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
                 if (issued < items) {
                     const int unit = worker + iu * workers;
                     const int row0 = unit * p.unit_step + (it ? p.tile1_row : 0);
-                    const uint8_t* src = (it ? part.w1 : part.w0) + static_cast<size_t>(row0) * row_bytes +
+                    const uint8_t* src = (it ? w1 : w0) + static_cast<size_t>(row0) * row_bytes +
                                          static_cast<size_t>(first + is) * kBlockBytes;
                     const uint32_t dst = ring + (issued % kDepth) * kItemBytes + 4 * lane;
                     const int valid = p.N - row0;
@@ -873,13 +869,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const T* __restric
 // The passes over tokens are a grid's y: of more than it holds, the rest go to
 // further launches (of the same kernel: a token's result is the same in each).
 constexpr int kMaxPasses = 65535;
-constexpr int kTableWaves = 1;
 
-// CTAs (or clusters) of a launch that divide the weight rows' units: those that the GPU
-// holds, over the token tiles that there could be.
+// CTAs of a rows_kernel that divide the weight rows' units: those that the GPU holds; in
+// segments those over the token tiles that there could be, or a few times as many, since
+// not all are, of eight units or more.  (64 experts, 7168 x 2048, bf16, us with the
+// GPU's CTAs once, twice, four and eight times: 64 tokens 144 77 102 94, 128 145 145
+// 116 118, 512 378 251 200 202.)
 int unit_ctas(const RowsArgs& p, int most, int units) {
     if (p.capacity == 0) return std::min(most, units);
-    return std::min(units, std::max(1, kTableWaves * most / p.capacity));
+    const int once = std::max(1, std::min(units, most / p.capacity));
+    if (p.capacity == p.M) return once;  // (tiles of one token: all are)
+    return std::max(once, std::min(units / 8, 4 * most / p.capacity));
 }
 
 // Calls `launch(x, args, passes)` for each run of at most kMaxPasses passes of kTokens.
@@ -990,11 +990,85 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         pdl_wait_prerequisites();
         pdl_allow_dependents();
     }
-    Part part;
-    if (!take_part<kTable, NT == 0>(p, kTokens, part)) return;  // (all of a cluster)
-    const int m0 = part.m0;
     const int rank = static_cast<int>(blockIdx.x) % p.parts, first_unit = static_cast<int>(blockIdx.x) / p.parts;
     const int unit_step = static_cast<int>(gridDim.x) / p.parts;
+    // Segments: the CTAs (or clusters) divide the units of all tiles among them, here,
+    // where the tiles are known.  Either as many for each tile, or all units in equal
+    // runs, tile after tile: going over to a tile costs about three units (its tokens
+    // are loaded and converted, and nothing is multiplied meanwhile).  (64 experts, two of
+    // 2048 x 7168, us in runs and by tiles: 8 tiles 42 and 36, 48 tiles 207 and 292.)
+    int my_units;
+    // (as many for each tile: always where a tile is one token, of which the grid is a
+    // multiple, so that this costs nothing)
+    [[maybe_unused]] bool even = kBytes;
+    [[maybe_unused]] int tile0 = 0, unit0 = 0;
+    if constexpr (kTable) {
+        const int tiles = kBytes ? p.M : *p.table_count;
+        const long long items = static_cast<long long>(tiles) * p.units;
+        const int each = tiles > 0 ? unit_step / tiles : 0;  // CTAs of a tile
+        if (!kBytes) even = each > 0 && (p.units + each - 1) / each <= (items + unit_step - 1) / unit_step + 3;
+        if (kBytes || even) {
+            tile0 = first_unit / each;
+            const int share = first_unit - tile0 * each;
+            unit0 = static_cast<int>(static_cast<long long>(p.units) * share / each);
+            my_units = tile0 < tiles ? static_cast<int>(static_cast<long long>(p.units) * (share + 1) / each) - unit0
+                                     : 0;
+        } else {
+            const long long item0 = items * first_unit / unit_step;
+            my_units = static_cast<int>(items * (first_unit + 1) / unit_step - item0);
+            tile0 = static_cast<int>(item0 / p.units);
+            unit0 = static_cast<int>(item0 - static_cast<long long>(tile0) * p.units);
+        }
+        if (my_units == 0) return;  // (all of a cluster)
+    } else {
+        my_units = (p.units - 1 - first_unit) / unit_step + 1;
+    }
+    // The CTA's unit u: which of the weight rows', and whose tokens and matrices.  Counted
+    // from the unit that is being multiplied, a few units from which all others lie: a
+    // division for each of them cost 0.2 us a unit.
+    int now = 0, now_tile = tile0, now_unit = unit0;
+    struct Place {
+        int tile, unit;
+    };
+    auto place_at = [&](int u) -> Place {
+        Place at = {now_tile, now_unit + (u - now)};
+        if (kBytes || even) return at;
+        while (at.unit >= p.units) at.unit -= p.units, ++at.tile;
+        while (at.unit < 0) at.unit += p.units, --at.tile;
+        return at;
+    };
+    auto unit_at = [&](int u) {
+        if constexpr (!kTable) return first_unit + u * unit_step;
+        else return place_at(u).unit;
+    };
+    // (by a warp.  The tile being multiplied is at hand, that before it, and the one last
+    // asked for beyond: a warp asks seldom, and finding a token's segment takes 1 us.)
+    struct Whose {
+        int tile;
+        Part part;
+    };
+    Whose present = {-1, {static_cast<int>(blockIdx.y) * kTokens, p.M, 0}};
+    [[maybe_unused]] Whose past = present, next = present;
+    auto find = [&](Whose& w, int tile) {
+        w.tile = tile;
+        if constexpr (kTable && kBytes) w.part = token_part(p, tile);
+        else if constexpr (kTable) w.part = table_part(p, tile);
+    };
+    auto whose = [&](int u) -> Part {
+        if constexpr (!kTable) {
+            return present.part;
+        } else {
+            if (kBytes || even) return present.part;
+            const int tile = place_at(u).tile;
+            if (tile == present.tile) return present.part;
+            if (tile == past.tile) return past.part;
+            if (tile != next.tile) find(next, tile);
+            return next.part;
+        }
+    };
+    if (kTable) find(present, tile0);
+    const Part& part = present.part;
+    if (kTable && even && part.M == part.m0) return;  // (a token in no segment; all of a cluster)
     const int blocks = p.K / kQK;
     const size_t row_bytes = static_cast<size_t>(blocks) * kBlockBytes;
     // this CTA's blocks
@@ -1012,17 +1086,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     const uint32_t bar_sums = bars + 8 * kMaxDepth, bar_inbox = bar_sums + 8;
     volatile int* abort_flag =
         reinterpret_cast<volatile int*>(slots + static_cast<size_t>(p.depth) * slot_bytes + 8 * (kMaxDepth + 5));
-    const int my_units = (p.units - 1 - first_unit) / unit_step + 1;
     // by a whole warp
     auto issue = [&](int u) {
         if (u >= my_units) return;
-        const int unit = first_unit + u * unit_step;
+        const int unit = unit_at(u);
+        const Part from = whose(u);
         uint8_t* slot = slots + static_cast<size_t>(u % p.depth) * slot_bytes;
         const uint32_t bar = bars + 8 * (u % p.depth);
         const int tile = lane >> 4;
         const int row0 = unit * p.unit_step + (tile ? p.tile1_row : 0);
         const int valid = min(max(p.N - row0, 0), kUnitRows);
-        const uint8_t* src = (tile ? part.w1 : part.w0) + static_cast<size_t>(row0) * row_bytes;
+        const uint8_t* src = from.of(tile ? p.w1 : p.w0, p) + static_cast<size_t>(row0) * row_bytes;
         uint8_t* dst = slot + tile * tile_bytes;
         uint32_t bytes = static_cast<uint32_t>(valid * pitch);
         if (p.parts == 1) {
@@ -1070,16 +1144,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
     [[maybe_unused]] float undo = 0.f;
     [[maybe_unused]] bool wide = false;
     XBlock<T> xm[kBytes ? 1 : NT];
-    if (warp < nb) {
+    auto load_x = [&]() {
+        if (warp >= nb) return;
         if constexpr (kBytes) {
-            wide = load_x_bytes(kTable ? x + static_cast<size_t>(m0) * p.K : x, b0 + warp, lane,
+            wide = load_x_bytes(kTable ? x + static_cast<size_t>(part.m0) * p.K : x, b0 + warp, lane,
                                 xs + warp * kXWords, xi, undo);
         } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                load_x_block(x, p.K, b0 + warp, m0 + n * (kTokens / NT), part.M, lane, xm[n]);
+                load_x_block(x, p.K, b0 + warp, part.m0 + n * (kTokens / NT), part.M, lane, xm[n]);
         }
-    }
+    };
+    load_x();
     const int o_first = kOut * rank / p.parts, o_count = kOut * (rank + 1) / p.parts - o_first;
     // the warps take turns at the outputs of a unit, and at refilling its slot
     auto turn_at = [&](int u) { return (warp + u) & (kWarps - 1); };
@@ -1091,6 +1167,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
             pdl_wait_prerequisites();  // t
             waited = true;
         }
+        if (32 * turn_at(u) >= kOut) return;
+        const Part to_part = whose(u);
         const float* all = red + (u & 1) * kWarps * (2 * kOut);
         for (int o = 32 * turn_at(u) + lane; o < kOut; o += 32 * kWarps) {
             float v[2] = {0.f, 0.f};
@@ -1100,7 +1178,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[1] += all[w * (2 * kOut) + kOut + o];
             }
             if (p.parts == 1) {
-                finish_row<T, NT, kMode>(x, p, part, o, v, first_unit + u * unit_step);
+                finish_row<T, NT, kMode>(x, p, to_part, o, v, unit_at(u));
             } else {
                 const int to = ((o + 1) * p.parts - 1) / kOut;  // whose share o is
                 const int at = ((u & 3) * p.parts + rank) * share + o - kOut * to / p.parts;
@@ -1113,6 +1191,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         if (turn_at(u) == kWarps - 1 && lane == 0)
             mbar_arrive_expect_tx(bar_inbox + 8 * (u & 3), 8 * p.parts * o_count);
         if (32 * turn_at(u) >= o_count) return;
+        const Part to_part = whose(u);
         tc::wait_peer_bounded(bar_inbox + 8 * (u & 3), (u >> 2) & 1, abort_flag, p.err, kErrTimeoutFull);
         for (int o = 32 * turn_at(u) + lane; o < o_count; o += 32 * kWarps) {
             float v[2] = {0.f, 0.f};
@@ -1121,7 +1200,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
                 v[0] += w.x;
                 v[1] += w.y;
             }
-            finish_row<T, NT, kMode>(x, p, part, o_first + o, v, first_unit + u * unit_step);
+            finish_row<T, NT, kMode>(x, p, to_part, o_first + o, v, unit_at(u));
         }
     };
     __syncthreads();
@@ -1130,6 +1209,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) stream_kernel(const T* __restr
         cluster_wait();
     }
     for (int u = 0; u < my_units; ++u) {
+        if (kTable && u > 0) {
+            ++now;
+            if (++now_unit == p.units && !kBytes) {  // the next tile's tokens
+                now_unit = 0;
+                ++now_tile;
+                past = present;
+                if (next.tile == now_tile) present = next;
+                else find(present, now_tile);
+                load_x();
+            }
+        }
         const uint32_t slot = smem_u32(slots) + (u % p.depth) * slot_bytes;
         mbar_wait_bounded(bars + 8 * (u % p.depth), (u / p.depth) & 1, abort_flag, p.err, kErrTimeoutFull);
         float* mine = red + ((u & 1) * kWarps + warp) * (2 * kOut);
@@ -1247,8 +1337,15 @@ cudaError_t launch_stream(const void* x, RowsArgs& p, size_t smem, int device, i
         resident[device][p.parts].store(most, std::memory_order_release);
     }
     constexpr int kTokens = Pass<T, NT>::kTokens;
+    if constexpr (kTable) {  // (all tiles in one grid)
+        const long long items = static_cast<long long>(p.capacity) * p.units;
+        const int clusters = NT == 0 ? p.capacity * std::max(1, std::min(p.units, most / p.capacity))
+                                     : static_cast<int>(std::min<long long>(most, items));
+        cfg.gridDim = dim3(static_cast<unsigned>(clusters * p.parts));
+        return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode, kTable>, static_cast<const T*>(x), p);
+    }
     return launch_passes<T, kTokens>(static_cast<const T*>(x), p, [&](const T* xs, const RowsArgs& q, int passes) {
-        cfg.gridDim = dim3(unit_ctas(p, most, p.units) * p.parts, passes);
+        cfg.gridDim = dim3(std::min(most, p.units) * p.parts, passes);
         return cudaLaunchKernelEx(&cfg, stream_kernel<T, NT, kMode, kTable>, xs, q);
     });
 }

@@ -636,7 +636,7 @@ size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *par
  * Tokens in no segment (before the first, behind the last) are not read, and their
  * rows of every output stay as they are.  Offsets that do not ascend within 0 .. m give
  * wrong results, but touch nothing outside the buffers.  Q2K_PATH_AUTO takes the exact
- * weights up to 16 (bf16) or 8 (f32) tokens, or four (two) for each expert. */
+ * weights up to 16 (bf16) or 8 (f32) tokens, or eight (four) for each expert. */
 
 typedef struct q2k_linear_params {
     uint32_t m;         /* tokens, >= 1 */

@@ -43,7 +43,7 @@ def close(got, ref, bound, what):
 def takes_rows(m, dtype, experts, path):
     if path != "auto":
         return path == "gemv"
-    few, each = (16, 4) if dtype == "bf16" else (8, 2)
+    few, each = (16, 8) if dtype == "bf16" else (8, 4)
     return m <= few or (experts > 0 and m <= each * experts)
 
 
