@@ -295,51 +295,66 @@ __global__ void __launch_bounds__(kMoveThreads) sort_kernel(MoveArgs p) {
 }
 
 // y[t] = residual[t] + sum_s weights[t, s] ys[rows[t, s]], over the slots that have an
-// expert (what another's place holds is not read).  A thread has eight rows' words on
-// their way at once; of eight bytes each, so that many CTAs fit: between the places'
-// arrival and the rows' a CTA asks for nothing.  (512 tokens of eight rows of 14336
-// bytes, 66 MB: words of 16 bytes 23 us, of 8 bytes 14.)
-template <typename T, int V>
+// expert (what another's place holds is not read).  A thread has kS rows' words on their
+// way at once, kW of each row: between the places' arrival and the rows' a CTA asks for
+// nothing, so many loads have to follow.  Words of eight bytes, so that many CTAs fit.
+// (512 tokens of eight rows of 14336 bytes, 73 MB: words of 16 bytes 16.6 us, of eight
+// bytes 16.3, two of them 15.1; 4096 tokens of two rows of 8192 bytes, 134 MB: one
+// word of each row 47 us, eight 27.)
+template <typename T, int V, int kS, int kW>
 __global__ void __launch_bounds__(kMoveThreads) combine_kernel(MoveArgs p) {
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int t = blockIdx.x / p.chunks, lane = threadIdx.x & 31;
-    const int u = (blockIdx.x - t * p.chunks) * blockDim.x + threadIdx.x;
-    const bool in = u < p.units;
+    const int u = (blockIdx.x - t * p.chunks) * kW * blockDim.x + threadIdx.x;
     const size_t mine = static_cast<size_t>(t) * p.width + static_cast<size_t>(u) * V;
+    const int step = blockDim.x * V;  // from one of the thread's words to the next
     const T* ys = static_cast<const T*>(p.in) + static_cast<size_t>(u) * V;
     const size_t slot0 = static_cast<size_t>(t) * p.top_k;
     const unsigned end = static_cast<unsigned>(min(max(__ldg(p.offsets + p.experts), 0), p.routes));
-    float sum[V];
-    Pack<T, V> r;
-    if (in && p.residual != nullptr) r.load(static_cast<const T*>(p.residual) + mine);
+    bool in[kW];
+    float sum[kW][V];
+    Pack<T, V> r[kW];
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = r.get(v);
-    for (int s0 = 0; s0 < p.top_k; s0 += kSlots) {
+    for (int w = 0; w < kW; ++w) {
+        in[w] = u + w * static_cast<int>(blockDim.x) < p.units;
+        r[w].load_if(static_cast<const T*>(p.residual) + mine + w * step, in[w] && p.residual != nullptr);
+    }
+#pragma unroll
+    for (int w = 0; w < kW; ++w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum[w][v] = r[w].get(v);
+    for (int s0 = 0; s0 < p.top_k; s0 += kS) {
         // a lane has one of the places and weights
-        const bool slot = lane < kSlots && s0 + lane < p.top_k;
+        const bool slot = lane < kS && s0 + lane < p.top_k;
         const int place = slot ? __ldg(p.rows + slot0 + s0 + lane) : -1;
         const float weight = slot && p.weights != nullptr ? __ldg(p.weights + slot0 + s0 + lane) : 1.f;
-        int at[kSlots];
-        Pack<T, V> a[kSlots];
+        int at[kS];
+        Pack<T, V> a[kS][kW];
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < kS; ++s) {
             at[s] = __shfl_sync(0xFFFFFFFFu, place, s);
-            a[s].load_if(ys + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width,
-                         in && static_cast<unsigned>(at[s]) < end);
+            const T* row = ys + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) a[s][w].load_if(row + w * step, in[w] && static_cast<unsigned>(at[s]) < end);
         }
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            const float w = __shfl_sync(0xFFFFFFFFu, weight, s);
+        for (int s = 0; s < kS; ++s) {
+            const float f = __shfl_sync(0xFFFFFFFFu, weight, s);
             if (static_cast<unsigned>(at[s]) >= end) continue;
 #pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] = fmaf(w, a[s].get(v), sum[v]);
+            for (int w = 0; w < kW; ++w)
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[w][v] = fmaf(f, a[s][w].get(v), sum[w][v]);
         }
     }
-    if (!in) return;
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.set(v, sum[v]);
-    r.store(static_cast<T*>(p.out) + mine);
+    for (int w = 0; w < kW; ++w) {
+        if (!in[w]) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[w].set(v, sum[w][v]);
+        r[w].store(static_cast<T*>(p.out) + mine + w * step);
+    }
 }
 
 struct BackArgs {
@@ -436,8 +451,8 @@ __global__ void __launch_bounds__(kMoveThreads) combine_backward_kernel(BackArgs
 
 // ---- launches --------------------------------------------------------------------
 
-template <typename Kernel, typename Args>
-cudaError_t launch_pdl(Kernel kernel, dim3 grid, int threads, size_t smem, int cluster,
+template <typename Args>
+cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, int threads, size_t smem, int cluster,
                        cudaStream_t stream, const Args& args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -495,11 +510,20 @@ cudaError_t launch_move(const MoeMoveArgs& a, cudaStream_t stream) {
     return with_values<T>(bytes, [&](auto values) {
         constexpr int V = decltype(values)::value;
         p.units = a.width / V;
-        // a row's words in equal chunks, whole warps each
-        p.chunks = (p.units + kMoveThreads - 1) / kMoveThreads;
-        const int threads = ((p.units + p.chunks - 1) / p.chunks + 31) & ~31;
-        const dim3 grid(static_cast<unsigned>(a.n_tokens) * p.chunks);
-        return launch_pdl(kCombine ? combine_kernel<T, V> : sort_kernel<T, V>, grid, threads, 0, 1, stream, p);
+        // a row's words in equal chunks of `each` a thread, whole warps each
+        auto go = [&](void (*kernel)(MoveArgs), int each) {
+            p.chunks = (p.units + each * kMoveThreads - 1) / (each * kMoveThreads);
+            const int chunk = (p.units + p.chunks - 1) / p.chunks;
+            const int threads = ((chunk + each - 1) / each + 31) & ~31;
+            return launch_pdl(kernel, dim3(static_cast<unsigned>(a.n_tokens) * p.chunks), threads, 0, 1, stream, p);
+        };
+        if constexpr (kCombine) {
+            if constexpr (V * sizeof(T) > 8) return cudaErrorInvalidValue;  // (no such words here)
+            else if (a.top_k <= 2) return go(combine_kernel<T, V, 2, 8>, 8);
+            else return go(combine_kernel<T, V, kSlots, V * sizeof(T) == 8 ? 2 : 4>, V * sizeof(T) == 8 ? 2 : 4);
+        } else {
+            return go(sort_kernel<T, V>, 1);
+        }
     });
 }
 
