@@ -898,7 +898,7 @@ def gated_ffn(x, w_gate, w_up, n: int, act="silu", save: bool = False, out=None,
     ``routes`` (of ``moe_route``): x holds rows in expert order, as ``moe_sort`` makes
     them, and each row is multiplied by its own expert's matrices; ``w_gate`` and
     ``w_up`` then hold ``n_experts`` matrices each, one after another.  Rows behind the
-    last expert's are not read, and their results not written.  The weights are exact
+    last expert's reach no result, and theirs are not written.  The weights are exact
     up to eight bf16 or four f32 tokens for each expert.
     """
     if out is None and workspace.__class__ is str:

@@ -99,16 +99,20 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
             const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
             __nv_bfloat16* __restrict__ du, int pitch, __nv_bfloat16* __restrict__ dgate,
             __nv_bfloat16* __restrict__ dup, int M, int N, int act,
-            unsigned int* __restrict__ counts, int n_counts, const int* __restrict__ end) {
+            unsigned int* __restrict__ counts, int n_counts, const int* __restrict__ offsets, int segments) {
     pdl_allow_dependents();
-    if (end != nullptr) M = min(max(*end, 0), M);  // (tokens in segments: the last one's end)
+    int first = 0;
+    if (offsets != nullptr) {  // tokens in segments: from the first to the last one's end
+        first = min(max(offsets[0], 0), M);
+        M = min(max(offsets[segments], 0), M);
+    }
     if (blockIdx.x == 0)
         for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
     const int per_row = pitch / 8;
     const bool vec = (N & 7) == 0;
     const size_t chunks = static_cast<size_t>(M) * per_row;
-    for (size_t id = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; id < chunks;
-         id += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    for (size_t id = static_cast<size_t>(first) * per_row + static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+         id < chunks; id += static_cast<size_t>(gridDim.x) * blockDim.x) {
         const int m = static_cast<int>(id / per_row);
         const int n = 8 * static_cast<int>(id - static_cast<size_t>(m) * per_row);
         const size_t at = static_cast<size_t>(m) * N + n;
@@ -669,7 +673,7 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     grad_kernel<<<blocks, 256, 0, stream>>>(
         a.dh, a.gate, a.up, dg, du, pitch, own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
         a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan),
-        seg.count > 0 ? seg.offsets + seg.count : nullptr);
+        seg.offsets, seg.count);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_backward_product(a.wg, a.wu, dg, du, a.dx, plan, a.M, a.N, a.K, 2, pitch, seg, true, ws,

@@ -633,8 +633,8 @@ size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *par
  * such offsets, and q2k_moe_sort rows in that order.
  *   offsets    device i32 [n_experts + 1], ascending within 0 .. m
  *   n_experts  1..Q2K_MOE_MAX_EXPERTS
- * Tokens in no segment (before the first, behind the last) are not read, and their
- * rows of every output stay as they are.  Offsets that do not ascend within 0 .. m give
+ * Tokens in no segment (before the first, behind the last) reach no result, and
+ * their rows of every output stay as they are.  Offsets that do not ascend within 0 .. m give
  * wrong results, but touch nothing outside the buffers.  Q2K_PATH_AUTO takes the exact
  * weights up to 16 (bf16) or 8 (f32) tokens, or eight (four) for each expert. */
 

@@ -262,3 +262,44 @@ def test_segments_backward(case, kind):
         ref = a @ w1 + c @ wu
         close(gx[lo:hi], ref, 8e-3 * (np.abs(a) @ np.abs(w1) + np.abs(c) @ np.abs(wu))
               + ea @ np.abs(w1) + ec @ np.abs(wu) + U16 * np.abs(ref), f"dx of {e}")
+
+
+@pytest.mark.parametrize("n,k", [(40, 1024), (37, 1280), (132, 768)])
+@pytest.mark.parametrize("before,lengths,behind", [(3, [5, 0, 40], 4), (2, [0, 0], 6), (0, [130, 7], 1)])
+def test_segments_leave_other_rows(n, k, before, lengths, behind):
+    """Through the C calls, every output prefilled: rows in no segment stay."""
+    import ctypes
+    lib, bf16 = q2k.load(), DT["bf16"]
+    rng = np.random.default_rng([6, n, before])
+    routes, offsets = routes_of(lengths, before)
+    m, experts = int(offsets[-1]) + behind, len(lengths)
+    _, w = pool(rng, experts, n, k)
+    _, w2 = pool(rng, experts, n, k)
+    dy, z, u = (activations(rng, m, n, bf16)[0] for _ in range(3))
+    full = lambda cols: torch.full((m, cols), 7.0, dtype=bf16, device="cuda:0")  # noqa: E731
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda:0")
+    dx, dz, gx, dg, du, px = full(k), full(n), full(k), full(n), full(n), full(k)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def linear(act, dxx, zz, dzz):
+        p = q2k.LinearParams(m, n, k, 10, 1, act, experts, 0)
+        return lib.q2k_linear_backward(dy.data_ptr(), m * n, zz, w.data_ptr(), w.numel(), dxx.data_ptr(),
+                                       m * k, dzz, None, routes.offsets.data_ptr(), ctypes.byref(p),
+                                       ws.data_ptr(), ws.numel(), stream)
+
+    assert linear(1, dx, z.data_ptr(), dz.data_ptr()) == 0
+    assert linear(2, px, None, None) == 0
+    p = q2k.GatedFfnParams(m, n, k, 10, 1, 0)
+    assert lib.q2k_gated_ffn_experts_backward(
+        dy.data_ptr(), z.data_ptr(), u.data_ptr(), m * n, w.data_ptr(), w.numel(), w2.data_ptr(),
+        w2.numel(), gx.data_ptr(), m * k, dg.data_ptr(), du.data_ptr(), routes.offsets.data_ptr(),
+        experts, ctypes.byref(p), ws.data_ptr(), ws.numel(), stream) == 0
+    for t in (dx, dz, gx, dg, du, px):
+        assert untouched(t, offsets, 7)
+    real = slice(int(offsets[0]), int(offsets[-1]))
+    if sum(lengths):
+        want = q2k.linear_backward(dy, w, k, z=z, act="gelu", routes=routes)
+        assert torch.equal(dx[real], want[0][real]) and torch.equal(dz[real], want[1][real])
+        assert torch.equal(px[real], q2k.linear_backward(dy, w, k, routes=routes)[0][real])
+        want = q2k.gated_ffn_backward(dy, z, u, w, w2, k, routes=routes)
+        assert all(torch.equal(a[real], b[real]) for a, b in zip((gx, dg, du), want))
