@@ -56,7 +56,10 @@ __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr, uint32_t ran
 // at a time, with counts of its own per expert (bins).  A first walk counts; the
 // counts become places (over the warps, the CTAs of the cluster, the experts); a
 // second walk gives each choice its place, its rank among the 32 from the mask of
-// those with the same expert.  Nothing depends on the order in which warps run.
+// those with the same expert, which a ballot for each bit of the expert gives (262144
+// choices of 64 experts, us: with `match` in both walks 62, counting by atomics in
+// shared memory 40, with ballots 33).  Nothing depends on the order in which warps
+// run.
 constexpr int kRouteMaxCtas = 8;
 constexpr int kRouteWarps = 16, kRouteWarpsMany = 8;  // (more bins than kRouteFewBins)
 constexpr int kRouteFewBins = 2048;
@@ -69,6 +72,7 @@ struct RouteArgs {
     int* offsets;
     unsigned int* bad_ids;
     int routes, experts;
+    int bits;  // of an expert's number, and of `experts`
     int each;  // choices of a warp, a multiple of 32
 };
 
@@ -105,10 +109,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs p) {
             const bool in = base + 32 * u + lane < last;
             const bool known = static_cast<unsigned>(id[u]) < static_cast<unsigned>(p.experts);
             bad += in && !known && id[u] != -1;
-            const int key = !in ? -1 : known ? id[u] : p.experts;
-            const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-            if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-            __syncwarp();
+            if (in) atomicAdd(mine + (known ? id[u] : p.experts), 1);  // (a count: any order)
         }
     }
     bad = __reduce_add_sync(0xFFFFFFFFu, bad);
@@ -178,7 +179,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(RouteArgs p) {
             const int i = base + 32 * u + lane;
             const bool known = static_cast<unsigned>(id[u]) < static_cast<unsigned>(p.experts);
             const int key = i >= last ? -1 : known ? id[u] : p.experts;
-            const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+            unsigned same = __ballot_sync(0xFFFFFFFFu, key >= 0);
+            for (int b = 0; b < p.bits; ++b) {
+                const unsigned set = __ballot_sync(0xFFFFFFFFu, (key >> b) & 1);
+                same &= (key >> b) & 1 ? set : ~set;
+            }
             int at = 0;
             if (key >= 0) {
                 at = start[key] + mine[key] + __popc(same & ((1u << lane) - 1u));
@@ -569,6 +574,7 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
     p.bad_ids = a.bad_ids;
     p.routes = a.n_tokens * a.top_k;
     p.experts = a.n_experts;
+    while (p.experts >> p.bits) ++p.bits;
     // a warp takes 32 choices, and up to kRouteEach before further CTAs share them: the
     // walks over warps and CTAs cost as much as the steps that they save
     const int most = bins <= kRouteFewBins ? kRouteWarps : kRouteWarpsMany;
