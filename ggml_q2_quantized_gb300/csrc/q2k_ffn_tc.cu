@@ -754,16 +754,38 @@ cudaError_t ffn_error_word(int device, unsigned int** word) {
     return cudaSuccess;
 }
 
+// The error words: this file's, and those of the tensor kernel's files (added while the
+// library is loaded, only read after).
+constexpr int kMaxErrorWords = 16;
+static const void* g_tc_error_words[kMaxErrorWords];
+static int g_tc_error_count;
+
+bool add_tc_error_word(const void* symbol) {
+    if (g_tc_error_count == kMaxErrorWords) return false;
+    g_tc_error_words[g_tc_error_count++] = symbol;
+    return true;
+}
+
 cudaError_t read_and_clear_ffn_error(uint32_t* out, cudaStream_t stream) {
-    unsigned int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_ffn_error, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess)
-        e = cudaMemcpyToSymbolAsync(g_ffn_error, &zero, sizeof(unsigned int), 0,
-                                    cudaMemcpyHostToDevice, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    return e;
+    unsigned int bits[kMaxErrorWords + 1] = {};
+    const unsigned int zero = 0;
+    auto word = [](int i) { return i < g_tc_error_count ? g_tc_error_words[i] : &g_ffn_error; };
+    for (int i = 0; i <= g_tc_error_count; ++i) {
+        const cudaError_t e = cudaMemcpyFromSymbolAsync(bits + i, word(i), sizeof(unsigned int), 0,
+                                                        cudaMemcpyDeviceToHost, stream);
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    *out = 0;
+    for (int i = 0; i <= g_tc_error_count; ++i) {
+        *out |= bits[i];
+        if (bits[i] == 0) continue;
+        e = cudaMemcpyToSymbolAsync(word(i), &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q2k

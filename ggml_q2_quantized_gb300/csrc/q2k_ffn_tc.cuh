@@ -24,7 +24,6 @@ struct TcArgs {
     int whole;           // tiles [0, whole) go to the workers in turn, the rest is cut
     int parts;           // CTAs (pairs) of a cluster that divide K (then one tile each)
     float* partial;      // sums of a cut tile's runs, two slots per CTA
-    unsigned int* err;   // the device's error word
     unsigned int* counts;  // per cut tile and CTA of a worker: runs finished (zeroed)
     bool const_weights;  // the grid before does not write the weights
     bool tokens_ready;   // nor the tokens
@@ -48,6 +47,10 @@ struct TcArgs {
     const int4* table;
     const int* table_count;
 };
+
+// Makes the address of a file's error word (a __device__ variable) known to
+// read_and_clear_ffn_error; true.
+bool add_tc_error_word(const void* symbol);
 
 // Launch the kernel: results of type T; with kSeg tokens in segments.
 //   workspace    the plan's sums and counts (zeroed)

@@ -55,6 +55,11 @@ namespace q2k {
 
 namespace {
 
+// This file's error word (a word of its own in each file, since a pointer to a shared
+// one costs a register that the kernel does not have: 0.5 % of its time).
+__device__ unsigned int g_tc_error;
+const bool g_tc_error_known = add_tc_error_word(&g_tc_error);
+
 using namespace tc;
 
 constexpr int kDecWarps = 16;
@@ -625,7 +630,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     volatile int* shared_word = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-    unsigned int* err = p.err;
+    unsigned int* err = &g_tc_error;
 
     if (warp == 0) {
         for (int s = lane; s < S; s += 32) {
@@ -940,7 +945,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                         const int stage = 4 * sg.q0 + r;
                         const bool up = stage >= p.half_stages;
                         load_weights<kSeg>(dst, up ? &maps.w1 : &maps.w0, (kBlockBytes * (n0 / kQK)) & ~15,
-                                    kStageK * (up ? stage - p.half_stages : stage), expert, bar);
+                                           kStageK * (up ? stage - p.half_stages : stage), expert, bar);
                     } else {
                         const int x = (kBlockBytes * (sg.q0 + r)) & ~15;
                         load_weights<kSeg>(dst, &maps.w0, x, n0, expert, bar);
@@ -1054,9 +1059,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
     }
     // Results of `count` tokens (from m on) of a tile from their sums; the last
     // tile's (`final`) lie where the rings were, from token slot `slot` on.
-    auto bring_out = [&](float* base, bool final, int tile, int m, int count, const Team& team, int slot = 0,
-                         int slot0 = 0) {
-        const int n0 = row0(tile);
+    auto bring_out = [&](float* base, bool final, int n0, [[maybe_unused]] int expert, int m, int count,
+                         const Team& team, int slot = 0, int slot0 = 0) {
         if constexpr (kMode == Tc::kLora) {
             uint32_t* tbuf = reinterpret_cast<uint32_t*>(final ? base + kX * kSumPitch
                                                                : reinterpret_cast<float*>(smem + C::kOffT));
@@ -1066,7 +1070,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                          p, n0, m - slot0, count, team);
         }
         if constexpr (kMode == Tc::kLinear)
-            emit_linear<T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, expert_of(tile), team);
+            emit_linear<T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, expert, team);
         else
             emit<kMode, T>(p, base + slot * kSumPitch, n0, rows, m + slot, count, team);
     };
@@ -1078,7 +1082,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         if (p.tokens_ready) pdl_allow_dependents();
         const int segments = work.count();
         // the decoders come for the last segment
-        for (int index = warp < kDecWarps ? max(segments - 1, 0) : 0; work.segment(index, sg); ++index) {
+        for (int index = warp < kDecWarps ? (kSeg ? max(segments - 1, 0) : segments - 1) : 0;
+             work.segment(index, sg); ++index) {
             const bool final = index == segments - 1;
             Team team;
             team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
@@ -1109,7 +1114,8 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             // the last tile's sums take the place of the rings
             float* sums = reinterpret_cast<float*>(smem + (final ? 0 : C::kOffSums));
             const int chunk = final ? kX : kChunk;
-            const int m0 = token0(sg.tile), tokens = tokens_of(sg.tile);
+            const int n0 = row0(sg.tile), m0 = token0(sg.tile), expert = expert_of(sg.tile);
+            const int tokens = tokens_of(sg.tile);
             const int quarter = (team.thread >> 5) & 3, my_row = 32 * quarter + lane;
             const int strip = 16 * (team.thread >> 7), strips = 16 * (team.threads >> 7);
             const uint32_t t_lane = tmem + (index & 1) * C::kAccCols +
@@ -1206,7 +1212,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
                     }
                 }
                 team.sync();
-                bring_out(sums, final, sg.tile, m0 + c0, count, team, 0, c0);
+                bring_out(sums, final, n0, expert, m0 + c0, count, team, 0, c0);
                 team.sync();
             }
             if (final && p.parts > 1 && sg.run < 0) {
@@ -1228,13 +1234,14 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
         fence_before();
         __syncwarp();
         cluster_sync();
-        if (brings_out && work.segment(0, sg)) {
+        const bool any = work.segment(0, sg);
+        if (brings_out && (any || !kSeg)) {
             Team team;
             team.thread = warp < kDecWarps ? static_cast<int>(threadIdx.x) + 128
                                            : static_cast<int>(threadIdx.x) - 32 * kEpiWarp0;
             team.threads = 128 + kDecThreads;
             team.barrier = 7;
-            const int m0 = token0(sg.tile);
+            const int n0 = row0(sg.tile), m0 = token0(sg.tile), expert = expert_of(sg.tile);
             const int tokens = tokens_of(sg.tile), groups = (tokens + 7) / 8;
             const int first = 8 * (work.part * groups / p.parts);
             const int count = min(tokens, 8 * ((work.part + 1) * groups / p.parts)) - first;
@@ -1259,7 +1266,7 @@ ffn_tc_kernel(TcArgs p, const __grid_constant__ TcMaps maps) {
             }
             team.sync();
             if (*abort_flag == 0 && count > 0)
-                bring_out(reinterpret_cast<float*>(smem), true, sg.tile, m0, count, team, first);
+                bring_out(reinterpret_cast<float*>(smem), true, n0, expert, m0, count, team, first);
         }
     }
 
@@ -1322,8 +1329,6 @@ cudaError_t launch_tc_as(const TcArgs& a, const Plan& plan, const TcMaps& maps, 
 template <Tc kMode, typename T, bool kSeg>
 cudaError_t launch_tc(TcArgs a, const Plan& plan, uint8_t* workspace, const void* x0, const void* x1,
                       int x_cols, int x_pitch, int device, cudaStream_t stream, int experts) {
-    const cudaError_t known = ffn_error_word(device, &a.err);
-    if (known != cudaSuccess) return known;
     a.tiles = plan.tiles;
     a.row_units = plan.row_units;
     a.whole = plan.whole;
