@@ -329,24 +329,32 @@ def test_a_pool_past_4_gb():
     offsets[0], offsets[-1] = 0, 43
     routes = q2k.Routes(offsets[:0], offsets[:0], offsets)
     x = bf16(rng, 43, k)
+    whole = [q2k.dequantize(w).view(n, k).double() for w in (first, last)]
+    where = (slice(0, 3), slice(3, 43))
     for path in ("gemv", "tensor"):
         y = q2k.linear(x, pool, n, path=path, routes=routes)
-        h = q2k.gated_ffn(x, pool, pool, n, path=path, routes=routes)
-        for part, w in ((slice(0, 3), first), (slice(3, 43), last)):
-            want = q2k.linear(x[part].contiguous(), w, n, path=path)
-            # (K may be summed in other parts: both within the path's bound)
-            a = host(x[part])
-            wf = decoded(w[:64 * (k // 256) * 84].cpu().numpy(), 64, k)[0]
-            bound = (2e-5 * np.sqrt(k) if path == "gemv" else 8e-3) * (np.abs(a) @ np.abs(wf).T)
-            ref = a @ wf.T
-            assert np.all(np.abs(host(y[part])[:, :64] - ref) <= bound + U16 * np.abs(ref) * 1.01)
-            assert float((y[part].float() - want.float()).abs().max()) <= 0.1
-            assert bool(h[part].isfinite().all())
+        h, gate, up = q2k.gated_ffn(x, pool, pool, n, save=True, path=path, routes=routes)
+        assert torch.equal(gate, up) and bool(h.isfinite().all())
+        for part, w, wf in zip(where, (first, last), whole):
+            a = x[part].double()
+            ref, bound = a @ wf.T, 8e-3 * (a.abs() @ wf.abs().T)
+            if path == "gemv":  # the exact weights' bound, of the first and last rows
+                bytes_of = 64 * (k // 256) * 84
+                parts = [torch.from_numpy(decoded(v.cpu().numpy(), 64, k)[1]).to("cuda:0")
+                         for v in (w[:bytes_of], w[-bytes_of:])]
+                cols = torch.cat([torch.arange(64), torch.arange(n - 64, n)]).to("cuda:0")
+                ref, bound = ref[:, cols], 1e-5 * (a.abs() @ torch.cat(parts).T)
+            for got in (y, gate):
+                got = got[part].double() if path == "tensor" else got[part][:, cols].double()
+                assert bool(((got - ref).abs() <= bound + U16 * (ref.abs() + bound)).all())
     dy = bf16(rng, 43, n, scale=0.1)
     dx, _, dbias = q2k.linear_backward(dy, pool, k, bias=True, routes=routes)
-    want = q2k.linear_backward(dy[3:].contiguous(), last, k)[0]
-    assert float((dx[3:].float() - want.float()).abs().max()) <= 0.1
-    assert not bool(dbias[1:-1].any()) and bool(dbias[-1].any())
+    for part, wf, at in zip(where, whole, (0, experts - 1)):
+        d = dy[part].double()
+        ref, bound = d @ wf, 8e-3 * (d.abs() @ wf.abs())
+        assert bool(((dx[part].double() - ref).abs() <= bound + U16 * (ref.abs() + bound)).all())
+        assert bool(((dbias[at].double() - d.sum(0)).abs() <= 41 * U * d.abs().sum(0)).all())
+    assert not bool(dbias[1:-1].any())
 
 
 def test_rows_past_2_31():
