@@ -91,28 +91,117 @@ x_image_kernel(const float* __restrict__ x, uint8_t* __restrict__ xa, int M, int
     pdl_wait_prerequisites();
 }
 
+// The token tiles of segments [offsets[e], offsets[e + 1]): {segment, first token,
+// tokens} of `rows` tokens at most, segment after segment.  Offsets that do not ascend
+// within 0 .. M give other tiles, but none outside the tokens, and not more than there
+// is room for.  f32 tokens are rounded to bf16 on the way, by all CTAs (the first
+// makes the table).
+constexpr int kTableThreads = 1024;
+struct TableArgs {
+    const int* offsets;
+    int segments, M, rows, capacity;
+    int4* table;
+    int* count;
+    const float* x;
+    __nv_bfloat16* xb;
+    size_t chunks;  // of eight values
+};
+
+__device__ __forceinline__ void make_table(const TableArgs& p, int* first) {  // first: [segments + 1]
+    __shared__ int sums[kTableThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+    int carry = 0;
+    for (int e0 = 0; e0 < p.segments; e0 += threads) {
+        const int e = e0 + tid;
+        int tiles = 0;
+        if (e < p.segments) {
+            const int lo = min(max(p.offsets[e], 0), p.M), hi = min(max(p.offsets[e + 1], lo), p.M);
+            tiles = (hi - lo + p.rows - 1) / p.rows;
+        }
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int before = carry, all = carry;
+        for (int w = 0; w < threads / 32; ++w) {
+            before += w < warp ? sums[w] : 0;
+            all += sums[w];
+        }
+        // (kept at the room there is: no sum of lengths overflows)
+        if (e < p.segments) first[e] = min(before + sum - tiles, p.capacity);
+        carry = min(all, p.capacity);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        first[p.segments] = carry;
+        *p.count = carry;
+    }
+    __syncthreads();
+    for (int t = tid; t < carry; t += threads) {
+        int a = 0, b = p.segments;  // the last segment that begins at t or before has it
+        while (b - a > 1) {
+            const int mid = (a + b) / 2;
+            if (first[mid] <= t) a = mid;
+            else b = mid;
+        }
+        const int lo = min(max(p.offsets[a], 0), p.M), hi = min(max(p.offsets[a + 1], lo), p.M);
+        const int m = lo + (t - first[a]) * p.rows;
+        p.table[t] = make_int4(a, m, min(p.rows, hi - m), 0);
+    }
+}
+
+__global__ void __launch_bounds__(kTableThreads) table_kernel(TableArgs p) {
+    extern __shared__ int table_smem[];
+    pdl_allow_dependents();
+    pdl_wait_prerequisites();
+    if (blockIdx.x == 0) make_table(p, table_smem);
+    if (p.xb == nullptr) return;
+    for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.chunks;
+         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i + 1);
+        reinterpret_cast<uint4*>(p.xb)[i] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
+                                                       pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+    }
+}
+
 // dg = dh u act'(g) and du = dh act(g), rounded to bf16 as the MMA's operands:
 // rows of `pitch` (the products' token matrices) and, where the caller's own
-// rows are not those, of N.  A thread takes eight consecutive n of a row.
+// rows are not those, of N.  A thread takes eight consecutive n of a row.  With segments
+// a CTA of its own makes the table meanwhile (225 rows of 10 segments, the whole backward
+// pass of 1001x1280, us: with a kernel of its own 24.8, so 23.2).
+template <bool kSeg>
 __global__ void __launch_bounds__(256)
 grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ gate,
             const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
             __nv_bfloat16* __restrict__ du, int pitch, __nv_bfloat16* __restrict__ dgate,
             __nv_bfloat16* __restrict__ dup, int M, int N, int act,
-            unsigned int* __restrict__ counts, int n_counts, const int* __restrict__ offsets, int segments) {
+            unsigned int* __restrict__ counts, int n_counts, TableArgs t) {
+    extern __shared__ int table_smem[];
     pdl_allow_dependents();
-    int first = 0;
-    if (offsets != nullptr) {  // tokens in segments: from the first to the last one's end
-        first = min(max(offsets[0], 0), M);
-        M = min(max(offsets[segments], 0), M);
+    int first = 0, block = blockIdx.x, blocks = gridDim.x;
+    if constexpr (kSeg) {
+        if (block == 0) {
+            make_table(t, table_smem);
+            return;
+        }
+        --block;
+        --blocks;
+        // tokens in segments: from the first to the last one's end
+        first = min(max(t.offsets[0], 0), M);
+        M = min(max(t.offsets[t.segments], 0), M);
     }
-    if (blockIdx.x == 0)
+    if (block == 0)
         for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
     const int per_row = pitch / 8;
     const bool vec = (N & 7) == 0;
     const size_t chunks = static_cast<size_t>(M) * per_row;
-    for (size_t id = static_cast<size_t>(first) * per_row + static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-         id < chunks; id += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    for (size_t id = static_cast<size_t>(first) * per_row + static_cast<size_t>(block) * blockDim.x + threadIdx.x;
+         id < chunks; id += static_cast<size_t>(blocks) * blockDim.x) {
         const int m = static_cast<int>(id / per_row);
         const int n = 8 * static_cast<int>(id - static_cast<size_t>(m) * per_row);
         const size_t at = static_cast<size_t>(m) * N + n;
@@ -154,14 +243,15 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 // tokens, a warp every eighth; a cluster's CTAs share a segment and add their sums in
 // order.  dz goes to rows of `pitch`, and to the caller's own rows where those differ;
 // without an activation dz is dy, and only sums, or rows of `pitch`, may be asked for.
-// A sum takes dz before it is rounded.
+// A sum takes dz before it is rounded.  With segments the first CTA of a row of CTAs in
+// front makes the table meanwhile.
 struct LinearGradArgs {
     const __nv_bfloat16* dy;
     const __nv_bfloat16* z;   // with an activation
     __nv_bfloat16* to;        // rows of `pitch`, or null
     __nv_bfloat16* dz;        // the caller's, or null
     float* dbias;             // [segments][N], or null
-    const int* offsets;       // of the segments, or null: one of M tokens
+    TableArgs table;          // of the segments (offsets null: one of M tokens)
     unsigned int* counts;
     int n_counts;
     int M, N, pitch;
@@ -209,19 +299,25 @@ struct Eight {
 
 template <int kAct>
 __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearGradArgs p) {
+    extern __shared__ int table_smem[];
     __shared__ float red[kGradWarps][kGradCols];
     __shared__ float part[kGradCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int share = blockIdx.x % p.shares, n0 = kGradCols * (blockIdx.x / p.shares);
-    const int n = n0 + kGradEach * lane, segment = blockIdx.y;
+    const bool segments = p.table.offsets != nullptr;
+    const int n = n0 + kGradEach * lane, segment = static_cast<int>(blockIdx.y) - segments;
     pdl_wait_prerequisites();
     pdl_allow_dependents();  // (later grids start when all before this one is complete)
+    if (segment < 0) {  // (whole clusters)
+        if (blockIdx.x == 0) make_table(p.table, table_smem);
+        return;
+    }
     if (blockIdx.x == 0 && segment == 0)
         for (int c = threadIdx.x; c < p.n_counts; c += blockDim.x) p.counts[c] = 0u;
     int lo = 0, hi = p.M;
-    if (p.offsets != nullptr) {
-        lo = min(max(p.offsets[segment], 0), p.M);
-        hi = min(max(p.offsets[segment + 1], lo), p.M);
+    if (segments) {
+        lo = min(max(p.table.offsets[segment], 0), p.M);
+        hi = min(max(p.table.offsets[segment + 1], lo), p.M);
     }
     const long long len = hi - lo;
     hi = lo + static_cast<int>(len * (share + 1) / p.shares);
@@ -302,84 +398,6 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
     if (share == 0 && threadIdx.x < kGradCols && col < p.N) p.dbias[static_cast<size_t>(segment) * p.N + col] = v;
 }
 
-// The token tiles of segments [offsets[e], offsets[e + 1]): {segment, first token,
-// tokens} of `rows` tokens at most, segment after segment.  Offsets that do not ascend
-// within 0 .. M give other tiles, but none outside the tokens, and not more than there
-// is room for.  f32 tokens are rounded to bf16 on the way, by all CTAs (the first
-// makes the table).
-constexpr int kTableThreads = 1024;
-struct TableArgs {
-    const int* offsets;
-    int segments, M, rows, capacity;
-    int4* table;
-    int* count;
-    const float* x;
-    __nv_bfloat16* xb;
-    size_t chunks;  // of eight values
-};
-
-__device__ __forceinline__ void make_table(const TableArgs& p, int* first) {  // first: [segments + 1]
-    __shared__ int sums[kTableThreads / 32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
-    int carry = 0;
-    for (int e0 = 0; e0 < p.segments; e0 += threads) {
-        const int e = e0 + tid;
-        int tiles = 0;
-        if (e < p.segments) {
-            const int lo = min(max(p.offsets[e], 0), p.M), hi = min(max(p.offsets[e + 1], lo), p.M);
-            tiles = (hi - lo + p.rows - 1) / p.rows;
-        }
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-            if (lane >= d) sum += v;
-        }
-        if (lane == 31) sums[warp] = sum;
-        __syncthreads();
-        int before = carry, all = carry;
-        for (int w = 0; w < threads / 32; ++w) {
-            before += w < warp ? sums[w] : 0;
-            all += sums[w];
-        }
-        // (kept at the room there is: no sum of lengths overflows)
-        if (e < p.segments) first[e] = min(before + sum - tiles, p.capacity);
-        carry = min(all, p.capacity);
-        __syncthreads();
-    }
-    if (tid == 0) {
-        first[p.segments] = carry;
-        *p.count = carry;
-    }
-    __syncthreads();
-    for (int t = tid; t < carry; t += threads) {
-        int a = 0, b = p.segments;  // the last segment that begins at t or before has it
-        while (b - a > 1) {
-            const int mid = (a + b) / 2;
-            if (first[mid] <= t) a = mid;
-            else b = mid;
-        }
-        const int lo = min(max(p.offsets[a], 0), p.M), hi = min(max(p.offsets[a + 1], lo), p.M);
-        const int m = lo + (t - first[a]) * p.rows;
-        p.table[t] = make_int4(a, m, min(p.rows, hi - m), 0);
-    }
-}
-
-__global__ void __launch_bounds__(kTableThreads) table_kernel(TableArgs p) {
-    extern __shared__ int table_smem[];
-    pdl_allow_dependents();
-    pdl_wait_prerequisites();
-    if (blockIdx.x == 0) make_table(p, table_smem);
-    if (p.xb == nullptr) return;
-    for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < p.chunks;
-         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p.x) + 2 * i + 1);
-        reinterpret_cast<uint4*>(p.xb)[i] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
-                                                       pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-    }
-}
-
 // ---- plan ----------------------------------------------------------------------
 
 size_t plan_bytes(const Plan& p) { return p.partial + p.counts; }
@@ -426,9 +444,8 @@ cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, int threads, size_t smem
     return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
-// The table at `workspace` for tiles of `rows` tokens; x: f32 tokens that xb gets.
-cudaError_t launch_table(const Segments& seg, int M, int rows, int capacity, uint8_t* workspace,
-                         const float* x, __nv_bfloat16* xb, int K, int sm_count, cudaStream_t stream) {
+// The table at `workspace`, of tiles of `rows` tokens.
+TableArgs table_args(const Segments& seg, int M, int rows, int capacity, uint8_t* workspace) {
     TableArgs p = {};
     p.offsets = seg.offsets;
     p.segments = seg.count;
@@ -437,14 +454,24 @@ cudaError_t launch_table(const Segments& seg, int M, int rows, int capacity, uin
     p.capacity = capacity;
     p.count = reinterpret_cast<int*>(workspace);
     p.table = reinterpret_cast<int4*>(workspace + 16);
+    return p;
+}
+TableArgs table_args(const Segments& seg, int M, const Plan& plan, uint8_t* workspace) {
+    return table_args(seg, M, plan.x_rows, plan.tiles / plan.row_units, workspace);
+}
+size_t table_smem_bytes(const Segments& seg) { return (seg.count + 1) * sizeof(int); }
+
+// The table in a kernel of its own; x: f32 tokens that xb gets.
+cudaError_t launch_table(TableArgs p, const Segments& seg, const float* x, __nv_bfloat16* xb, int K, int sm_count,
+                         cudaStream_t stream) {
     p.x = x;
     p.xb = xb;
-    p.chunks = xb != nullptr ? static_cast<size_t>(M) * (K / 8) : 0;
+    p.chunks = xb != nullptr ? static_cast<size_t>(p.M) * (K / 8) : 0;
     const size_t wanted = (p.chunks + 2 * kTableThreads - 1) / (2 * kTableThreads);
     const unsigned ctas = static_cast<unsigned>(std::min<size_t>(std::max<size_t>(wanted, 1), 2 * sm_count));
     // (few warps meet sooner)
-    const int threads = xb != nullptr ? kTableThreads : std::min(kTableThreads, (std::max(seg.count, capacity) + 31) & ~31);
-    return launch_pdl(table_kernel, dim3(ctas), threads, (seg.count + 1) * sizeof(int), 1, stream, p);
+    const int threads = xb != nullptr ? kTableThreads : std::min(kTableThreads, (std::max(seg.count, p.capacity) + 31) & ~31);
+    return launch_pdl(table_kernel, dim3(ctas), threads, table_smem_bytes(seg), 1, stream, p);
 }
 
 // Workspace of x W^T: plan_bytes, then (f32) the tokens' image; in segments the table,
@@ -463,8 +490,8 @@ cudaError_t launch_segments(TcArgs a, bool bf16, const void* x, void* workspace,
     a.quads = a.K / kQK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     __nv_bfloat16* xb = bf16 ? nullptr : reinterpret_cast<__nv_bfloat16*>(ws + table_bytes(plan));
-    const cudaError_t e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws,
-                                       static_cast<const float*>(x), xb, a.K, sm_count, stream);
+    const cudaError_t e = launch_table(table_args(seg, a.M, plan, ws), seg, static_cast<const float*>(x), xb, a.K,
+                                       sm_count, stream);
     if (e != cudaSuccess) return e;
     a.table_count = reinterpret_cast<const int*>(ws);
     a.table = reinterpret_cast<const int4*>(ws + 16);
@@ -530,8 +557,9 @@ size_t ffn_table_bytes(int M, int segments, int rows) {
 
 cudaError_t launch_ffn_table(const int* offsets, int segments, int M, int rows, void* workspace,
                              int sm_count, cudaStream_t stream) {
-    return launch_table({offsets, segments}, M, rows, segment_tiles(M, segments, rows),
-                        static_cast<uint8_t*>(workspace), nullptr, nullptr, 0, sm_count, stream);
+    const Segments seg = {offsets, segments};
+    return launch_table(table_args(seg, M, rows, segment_tiles(M, segments, rows), static_cast<uint8_t*>(workspace)),
+                        seg, nullptr, nullptr, 0, sm_count, stream);
 }
 
 size_t gated_tc_workspace_bytes(const GatedArgs& a) {
@@ -665,15 +693,12 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
     const unsigned blocks =
         static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));
-    if (seg.count > 0) {
-        const cudaError_t e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws, nullptr,
-                                           nullptr, 0, a.sm_count, stream);
-        if (e != cudaSuccess) return e;
-    }
-    grad_kernel<<<blocks, 256, 0, stream>>>(
+    const bool in_segments = seg.count > 0;
+    const TableArgs table = in_segments ? table_args(seg, a.M, plan, ws) : TableArgs{};
+    (in_segments ? grad_kernel<true> : grad_kernel<false>)<<<blocks + in_segments, 256,
+                                                             in_segments ? table_smem_bytes(seg) : 0, stream>>>(
         a.dh, a.gate, a.up, dg, du, pitch, own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
-        a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan),
-        seg.offsets, seg.count);
+        a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan), table);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_backward_product(a.wg, a.wu, dg, du, a.dx, plan, a.M, a.N, a.K, 2, pitch, seg, true, ws,
@@ -696,18 +721,13 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, void* workspace,
     const bool own = linear_backward_in_place(a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaError_t e = cudaSuccess;
-    if (seg.count > 0) {
-        e = launch_table(seg, a.M, plan.x_rows, plan.tiles / plan.row_units, ws, nullptr, nullptr, 0, a.sm_count,
-                         stream);
-        if (e != cudaSuccess) return e;
-    }
     LinearGradArgs g = {};
     g.dy = a.dy;
     g.z = a.act == kActNone ? nullptr : a.z;
     g.M = a.M;
     g.N = a.N;
     g.pitch = backward_pitch(a.N);
-    g.offsets = a.offsets;
+    if (seg.count > 0) g.table = table_args(seg, a.M, plan, ws);
     g.dbias = a.dbias;
     g.counts = reinterpret_cast<unsigned int*>(ws + plan.partial);
     g.n_counts = count_words(plan);
@@ -730,8 +750,10 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, void* workspace,
         e = launch_pdl(a.act == kActNone   ? linear_grad_kernel<kActNone>
                        : a.act == kActGelu ? linear_grad_kernel<kActGelu>
                                            : linear_grad_kernel<kActSilu>,
-                       dim3(strips * g.shares, segments), 32 * kGradWarps, 0,
-                       g.dbias != nullptr ? g.shares : 1, stream, g);
+                       dim3(strips * g.shares, segments + (seg.count > 0)), 32 * kGradWarps,
+                       seg.count > 0 ? table_smem_bytes(seg) : 0, g.dbias != nullptr ? g.shares : 1, stream, g);
+    } else if (seg.count > 0) {
+        e = launch_table(table_args(seg, a.M, plan, ws), seg, nullptr, nullptr, 0, a.sm_count, stream);
     } else if (plan.counts != 0) {
         e = cudaMemsetAsync(ws + plan.partial, 0, plan.counts, stream);
     }
