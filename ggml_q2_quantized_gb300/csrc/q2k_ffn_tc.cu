@@ -239,8 +239,10 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
 }
 
 // dz = dy act'(z) for one matrix, and its sums over the tokens (of each segment):
-// dbias.  A CTA takes 256 columns (a lane eight of them) and a share of a segment's
-// tokens, a warp every eighth; a cluster's CTAs share a segment and add their sums in
+// dbias.  A CTA takes 128 columns (a lane four of them) and a share of a segment's
+// tokens, a warp every eighth, four at once (lanes of eight columns, two tokens at once,
+// the whole backward pass, us: 225 rows of 10 segments of 1001x1280 25.2, so 17.4; 4096 of
+// 64 of 2048x2048 112.4, so 109; 2048 tokens of 14336x4096 198, so 194; 512 the same); a cluster's CTAs share a segment and add their sums in
 // order.  dz goes to rows of `pitch`, and to the caller's own rows where those differ;
 // without an activation dz is dy, and only sums, or rows of `pitch`, may be asked for.
 // A sum takes dz before it is rounded.  With segments the first CTA of a row of CTAs in
@@ -257,8 +259,8 @@ struct LinearGradArgs {
     int M, N, pitch;
     int shares;               // CTAs of a segment and kGradCols columns (with dbias: a cluster)
 };
-constexpr int kGradCols = 256, kGradWarps = 8, kGradAtOnce = 2;
-constexpr int kGradEach = 8;  // columns of a lane
+constexpr int kGradCols = 128, kGradWarps = 8, kGradAtOnce = 4;
+constexpr int kGradEach = 4;  // columns of a lane
 static_assert(kGradCols == 32 * kGradEach, "a warp's columns");
 
 // act'(g) in few instructions, which bound this kernel beside its loads (7.3 million
@@ -284,14 +286,14 @@ __device__ __forceinline__ float act_slope(float g) {
     return fmaf(r, fmaf(-r, q, q), r);
 }
 
-// Eight bf16 values.
-struct Eight {
+// A lane's bf16 values of a row.
+struct Lane {
     union {
-        uint4 word;
-        uint32_t bits[4];
-        __nv_bfloat16 value[8];
+        uint2 word;
+        uint32_t bits[kGradEach / 2];
+        __nv_bfloat16 value[kGradEach];
     };
-    __device__ __forceinline__ Eight() : word() {}
+    __device__ __forceinline__ Lane() : word() {}
     __device__ __forceinline__ float get(int e) const {
         return __uint_as_float(e & 1 ? bits[e / 2] & 0xFFFF0000u : bits[e / 2] << 16);
     }
@@ -323,18 +325,18 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
     hi = lo + static_cast<int>(len * (share + 1) / p.shares);
     lo += static_cast<int>(len * share / p.shares);
     constexpr bool kZ = kAct != kActNone;
-    const bool vec = (p.N & 7) == 0;
+    const bool vec = p.N % kGradEach == 0;
     float sum[kGradEach] = {};
     for (int m0 = lo + warp; m0 < hi && n < p.pitch; m0 += kGradAtOnce * kGradWarps) {
-        Eight g[kGradAtOnce], z[kGradAtOnce];
+        Lane g[kGradAtOnce], z[kGradAtOnce];
 #pragma unroll
         for (int u = 0; u < kGradAtOnce; ++u) {
             // (a token past the end is the last one again, which counts for nothing)
             const int m = min(m0 + u * kGradWarps, hi - 1);
             const size_t at = static_cast<size_t>(m) * p.N + n;
             if (vec) {
-                g[u].word = __ldg(reinterpret_cast<const uint4*>(p.dy + at));
-                if (kZ) z[u].word = __ldg(reinterpret_cast<const uint4*>(p.z + at));
+                g[u].word = __ldg(reinterpret_cast<const uint2*>(p.dy + at));
+                if (kZ) z[u].word = __ldg(reinterpret_cast<const uint2*>(p.z + at));
             } else {
 #pragma unroll
                 for (int e = 0; e < kGradEach; ++e) {
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
         for (int u = 0; u < kGradAtOnce; ++u) {
             const int m = m0 + u * kGradWarps;
             if (m >= hi) break;
-            Eight d;
+            Lane d;
 #pragma unroll
             for (int e = 0; e < kGradEach; e += 2) {
                 float v = g[u].get(e), w = g[u].get(e + 1);
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
                 sum[e + 1] += w;
                 d.bits[e / 2] = pack_bf16(v, w);
             }
-            if (p.to != nullptr) *reinterpret_cast<uint4*>(p.to + static_cast<size_t>(m) * p.pitch + n) = d.word;
+            if (p.to != nullptr) *reinterpret_cast<uint2*>(p.to + static_cast<size_t>(m) * p.pitch + n) = d.word;
             if (p.dz != nullptr)
                 for (int e = 0; e < kGradEach && n + e < p.N; ++e) p.dz[static_cast<size_t>(m) * p.N + n + e] = d.value[e];
         }
