@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "q2k_ffn_tc.cuh"
 
@@ -171,10 +172,12 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(TableArgs p) {
 
 // dg = dh u act'(g) and du = dh act(g), rounded to bf16 as the MMA's operands:
 // rows of `pitch` (the products' token matrices) and, where the caller's own
-// rows are not those, of N.  A thread takes eight consecutive n of a row.  With segments
+// rows are not those, of N.  A thread takes kEach consecutive n of a row: eight where
+// rows are whole 16 bytes, else two, since it then loads them one by one (512 tokens of
+// 4999x2816, the whole backward pass, us: eight 55.2, two 44.9).  With segments
 // a CTA of its own makes the table meanwhile (225 rows of 10 segments, the whole backward
 // pass of 1001x1280, us: with a kernel of its own 24.8, so 23.2).
-template <bool kSeg>
+template <bool kSeg, int kEach>
 __global__ void __launch_bounds__(256)
 grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ gate,
             const __nv_bfloat16* __restrict__ up, __nv_bfloat16* __restrict__ dg,
@@ -197,22 +200,22 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
     }
     if (block == 0)
         for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
-    const int per_row = pitch / 8;
-    const bool vec = (N & 7) == 0;
+    const int per_row = pitch / kEach;  // (pitch: a multiple of eight)
     const size_t chunks = static_cast<size_t>(M) * per_row;
     for (size_t id = static_cast<size_t>(first) * per_row + static_cast<size_t>(block) * blockDim.x + threadIdx.x;
          id < chunks; id += static_cast<size_t>(blocks) * blockDim.x) {
         const int m = static_cast<int>(id / per_row);
-        const int n = 8 * static_cast<int>(id - static_cast<size_t>(m) * per_row);
+        const int n = kEach * static_cast<int>(id - static_cast<size_t>(m) * per_row);
         const size_t at = static_cast<size_t>(m) * N + n;
-        __nv_bfloat16 h[8], g[8], u[8], a[8], b[8];
-        if (vec) {
+        alignas(16) __nv_bfloat16 h[kEach], g[kEach], u[kEach];
+        alignas(16) __nv_bfloat16 a[kEach], b[kEach];
+        if constexpr (kEach == 8) {
             *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(dh + at));
             *reinterpret_cast<uint4*>(g) = __ldg(reinterpret_cast<const uint4*>(gate + at));
             *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(up + at));
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kEach; ++e) {
                 const bool ok = n + e < N;
                 h[e] = ok ? dh[at + e] : __float2bfloat16_rn(0.f);
                 g[e] = ok ? gate[at + e] : __float2bfloat16_rn(0.f);
@@ -220,17 +223,18 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
             }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kEach; ++e) {
             float value, slope;
             act_value_slope<true>(to_float(g[e]), act, value, slope);
             a[e] = __float2bfloat16_rn(to_float(h[e]) * to_float(u[e]) * slope);
             b[e] = __float2bfloat16_rn(to_float(h[e]) * value);
         }
         const size_t to = static_cast<size_t>(m) * pitch + n;
-        *reinterpret_cast<uint4*>(dg + to) = *reinterpret_cast<const uint4*>(a);
-        *reinterpret_cast<uint4*>(du + to) = *reinterpret_cast<const uint4*>(b);
+        using W = std::conditional_t<kEach == 8, uint4, uint32_t>;
+        *reinterpret_cast<W*>(dg + to) = *reinterpret_cast<const W*>(a);
+        *reinterpret_cast<W*>(du + to) = *reinterpret_cast<const W*>(b);
         if (dgate != nullptr) {
-            for (int e = 0; e < 8 && n + e < N; ++e) {
+            for (int e = 0; e < kEach && n + e < N; ++e) {
                 dgate[at + e] = a[e];
                 dup[at + e] = b[e];
             }
@@ -692,13 +696,14 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, c
     __nv_bfloat16* dg = own ? a.dgate : reinterpret_cast<__nv_bfloat16*>(copies);
     __nv_bfloat16* du = own ? a.dup
                             : reinterpret_cast<__nv_bfloat16*>(copies + backward_matrix_bytes(a.M, a.N));
-    const size_t chunks = static_cast<size_t>(a.M) * (pitch / 8);
+    const bool whole = (a.N & 7) == 0, in_segments = seg.count > 0;
+    const size_t chunks = static_cast<size_t>(a.M) * (pitch / (whole ? 8 : 2));
     const unsigned blocks =
         static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, static_cast<size_t>(a.sm_count) * 8));
-    const bool in_segments = seg.count > 0;
     const TableArgs table = in_segments ? table_args(seg, a.M, plan, ws) : TableArgs{};
-    (in_segments ? grad_kernel<true> : grad_kernel<false>)<<<blocks + in_segments, 256,
-                                                             in_segments ? table_smem_bytes(seg) : 0, stream>>>(
+    const auto kernel = in_segments ? (whole ? grad_kernel<true, 8> : grad_kernel<true, 2>)
+                                    : (whole ? grad_kernel<false, 8> : grad_kernel<false, 2>);
+    kernel<<<blocks + in_segments, 256, in_segments ? table_smem_bytes(seg) : 0, stream>>>(
         a.dh, a.gate, a.up, dg, du, pitch, own ? nullptr : a.dgate, own ? nullptr : a.dup, a.M, a.N,
         a.act, reinterpret_cast<unsigned int*>(ws + plan.partial), count_words(plan), table);
     const cudaError_t e = cudaGetLastError();
