@@ -274,28 +274,40 @@ struct MoveArgs {
 constexpr int kMoveThreads = 256;
 constexpr int kSlots = 8;  // places taken together: that many loads on their way
 
-// xs[rows[t, s]] = x[t]; a place without an expert gets zeros.
-template <typename T, int V>
+// xs[rows[t, s]] = x[t]; a place without an expert gets zeros.  A thread has kW words of
+// the row on their way: sixteen bytes (4096 tokens of two rows of 4097 bf16, words of two
+// bytes: one 71.6 us, eight 22).
+template <typename T, int V, int kW>
 __global__ void __launch_bounds__(kMoveThreads) sort_kernel(MoveArgs p) {
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int t = blockIdx.x / p.chunks;
-    const int u = (blockIdx.x - t * p.chunks) * blockDim.x + threadIdx.x;
+    const int u = (blockIdx.x - t * p.chunks) * kW * blockDim.x + threadIdx.x;
     if (u >= p.units) return;
     const T* x = static_cast<const T*>(p.in) + static_cast<size_t>(t) * p.width + static_cast<size_t>(u) * V;
     T* xs = static_cast<T*>(p.out) + static_cast<size_t>(u) * V;
     const int* rows = p.rows + static_cast<size_t>(t) * p.top_k;
-    Pack<T, V> v, none;
-    v.load(x);
+    const int step = blockDim.x * V;  // from one of the thread's words to the next
+    Pack<T, V> v[kW], none;
+    bool in[kW];
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        in[w] = u + w * static_cast<int>(blockDim.x) < p.units;
+        v[w].load_if(x + w * step, in[w]);
+    }
     const int end = __ldg(p.offsets + p.experts);
     for (int s0 = 0; s0 < p.top_k; s0 += kSlots) {
         int at[kSlots];
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) at[s] = s0 + s < p.top_k ? __ldg(rows + s0 + s) : -1;
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            if (static_cast<unsigned>(at[s]) < static_cast<unsigned>(p.routes))
-                (at[s] < end ? v : none).store(xs + static_cast<size_t>(at[s]) * p.width);
+        for (int s = 0; s < kSlots; ++s) {
+            if (static_cast<unsigned>(at[s]) >= static_cast<unsigned>(p.routes)) continue;
+            T* row = xs + static_cast<size_t>(at[s]) * p.width;
+#pragma unroll
+            for (int w = 0; w < kW; ++w)
+                if (in[w]) (at[s] < end ? v[w] : none).store(row + w * step);
+        }
     }
 }
 
@@ -376,12 +388,17 @@ struct BackArgs {
 };
 
 // dys[rows[t, s]] = weights[t, s] dy[t] and dweights[t, s] = <dy[t], ys[rows[t, s]]>:
-// dy and ys are read once for both.  A thread's sums, the warp's, the CTA's and the
-// cluster's are added in that order, whatever runs when.
-template <typename T, int V>
-__global__ void __launch_bounds__(kMoveThreads) combine_backward_kernel(BackArgs p) {
-    __shared__ float part[kMoveThreads / 32][kSlots];
-    __shared__ float mine[kSlots];
+// dy and ys are read once for both, kW words of a thread from each of kS rows at once.  A
+// thread's sums, the warp's, the CTA's and the cluster's are added in that order, whatever
+// runs when.  Eight rows' words of 16 bytes leave room for three CTAs of an SM (1024 tokens
+// of eight rows of 7168 bf16: three 43.8 us, two 46).  With one or two choices of a token
+// two rows at once (4096 tokens of 4096 bf16: eight 54 us, two 30; of 4097 106 and 45), and
+// of words of one value two from each of four (1024 tokens of four rows of 4097 bf16: one of
+// eight 26 us, so 17; eight of 7169 37 and 35).
+template <typename T, int V, int kS, int kW>
+__global__ void __launch_bounds__(kMoveThreads, kS == 2 || V <= 2 ? 4 : 3) combine_backward_kernel(BackArgs p) {
+    __shared__ float part[kMoveThreads / 32][kS];
+    __shared__ float mine[kS];
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int t = blockIdx.x / p.parts, rank = blockIdx.x - t * p.parts;
@@ -391,59 +408,72 @@ __global__ void __launch_bounds__(kMoveThreads) combine_backward_kernel(BackArgs
     const int u0 = static_cast<int>(static_cast<long long>(p.units) * rank / p.parts);
     const int u1 = static_cast<int>(static_cast<long long>(p.units) * (rank + 1) / p.parts);
     const T* dy = static_cast<const T*>(p.dy) + static_cast<size_t>(t) * p.width;
-    for (int s0 = 0; s0 < p.top_k; s0 += kSlots) {
-        int at[kSlots];
-        float w[kSlots], dot[kSlots];
+    const int step = blockDim.x * V;  // from one of the thread's words to the next
+    for (int s0 = 0; s0 < p.top_k; s0 += kS) {
+        int at[kS];
+        float w[kS], dot[kS];
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < kS; ++s) {
             at[s] = s0 + s < p.top_k ? __ldg(p.rows + slot0 + s0 + s) : -1;
             w[s] = s0 + s < p.top_k ? __ldg(p.weights + slot0 + s0 + s) : 0.f;
             dot[s] = 0.f;
         }
-        for (int u = u0 + threadIdx.x; u < u1; u += blockDim.x) {
+        for (int u = u0 + threadIdx.x; u < u1; u += kW * blockDim.x) {
             const size_t col = static_cast<size_t>(u) * V;
-            Pack<T, V> g, a[kSlots];
-            g.load(dy + col);
+            Pack<T, V> g[kW], a[kS][kW];
+            bool in[kW];
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s)
-                a[s].load_if(static_cast<const T*>(p.ys) + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width + col,
-                             static_cast<unsigned>(at[s]) < end);
+            for (int i = 0; i < kW; ++i) {
+                in[i] = i == 0 || u + i * static_cast<int>(blockDim.x) < u1;
+                if (i == 0) g[i].load(dy + col);
+                else g[i].load_if(dy + col + i * step, in[i]);
+            }
 #pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
+            for (int s = 0; s < kS; ++s) {
+                const T* row = static_cast<const T*>(p.ys) + static_cast<size_t>(static_cast<unsigned>(at[s])) * p.width + col;
+#pragma unroll
+                for (int i = 0; i < kW; ++i) a[s][i].load_if(row + i * step, in[i] && static_cast<unsigned>(at[s]) < end);
+            }
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
                 if (static_cast<unsigned>(at[s]) >= static_cast<unsigned>(p.routes)) continue;
-                Pack<T, V> d;
-                if (static_cast<unsigned>(at[s]) < end) {
+                T* to = static_cast<T*>(p.dys) + static_cast<size_t>(at[s]) * p.width + col;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        dot[s] = fmaf(g.get(v), a[s].get(v), dot[s]);
-                        d.set(v, w[s] * g.get(v));
+                for (int i = 0; i < kW; ++i) {
+                    Pack<T, V> d;
+                    if (static_cast<unsigned>(at[s]) < end) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            dot[s] = fmaf(g[i].get(v), a[s][i].get(v), dot[s]);
+                            d.set(v, w[s] * g[i].get(v));
+                        }
                     }
+                    if (in[i]) d.store(to + i * step);
                 }
-                d.store(static_cast<T*>(p.dys) + static_cast<size_t>(at[s]) * p.width + col);
             }
         }
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < kS; ++s) {
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) dot[s] += __shfl_xor_sync(0xFFFFFFFFu, dot[s], d);
             if (lane == 0) part[warp][s] = dot[s];
         }
         __syncthreads();
         float sum = 0.f;
-        if (threadIdx.x < kSlots) {
+        if (threadIdx.x < kS) {
             for (int i = 0; i < warps; ++i) sum += part[i][threadIdx.x];
             mine[threadIdx.x] = sum;
         }
         if (p.parts > 1) {
             cluster_arrive();
             cluster_wait();
-            if (rank == 0 && threadIdx.x < kSlots) {
+            if (rank == 0 && threadIdx.x < kS) {
                 sum = 0.f;
                 for (int c = 0; c < p.parts; ++c)
                     sum += __uint_as_float(load_cluster_u32(smem_u32(mine + threadIdx.x), c));
             }
         }
-        if (rank == 0 && threadIdx.x < kSlots && s0 + static_cast<int>(threadIdx.x) < p.top_k)
+        if (rank == 0 && threadIdx.x < kS && s0 + static_cast<int>(threadIdx.x) < p.top_k)
             p.dweights[slot0 + s0 + threadIdx.x] = sum;
         if (p.parts > 1) {  // the sums are read before they change or their CTA leaves
             cluster_arrive();
@@ -527,7 +557,8 @@ cudaError_t launch_move(const MoeMoveArgs& a, cudaStream_t stream) {
             else if (a.top_k <= 2) return go(combine_kernel<T, V, 2, 8>, 8);
             else return go(combine_kernel<T, V, kSlots, V * sizeof(T) == 8 ? 2 : 4>, V * sizeof(T) == 8 ? 2 : 4);
         } else {
-            return go(sort_kernel<T, V>, 1);
+            constexpr int kW = 16 / (V * sizeof(T));
+            return go(sort_kernel<T, V, kW>, kW);
         }
     });
 }
@@ -552,13 +583,20 @@ cudaError_t launch_back(const MoeBackArgs& a, cudaStream_t stream) {
     return with_values<T>(bytes, [&](auto values) {
         constexpr int V = decltype(values)::value;
         p.units = a.width / V;
-        const int threads = std::min(kMoveThreads, (p.units + 31) & ~31);
-        p.parts = 1;
-        while (p.parts < kRouteMaxCtas && a.n_tokens * p.parts < 2 * a.sm_count &&
-               2 * p.parts * threads <= p.units)
-            p.parts *= 2;
-        const dim3 grid(static_cast<unsigned>(a.n_tokens) * p.parts);
-        return launch_pdl(combine_backward_kernel<T, V>, grid, threads, 0, p.parts, stream, p);
+        auto go = [&](void (*kernel)(BackArgs), int each) {
+            // (`each` words of a thread at once)
+            const int threads = std::min(kMoveThreads, ((p.units + each - 1) / each + 31) & ~31);
+            p.parts = 1;
+            while (p.parts < kRouteMaxCtas && a.n_tokens * p.parts < 2 * a.sm_count &&
+                   2 * p.parts * threads * each <= p.units)
+                p.parts *= 2;
+            const dim3 grid(static_cast<unsigned>(a.n_tokens) * p.parts);
+            return launch_pdl(kernel, grid, threads, 0, p.parts, stream, p);
+        };
+        constexpr int kW = std::min(4, static_cast<int>(32 / (V * sizeof(T))));
+        if (a.top_k <= 2) return go(combine_backward_kernel<T, V, 2, kW>, kW);
+        if constexpr (V == 1) return go(combine_backward_kernel<T, V, 4, 2>, 2);
+        else return go(combine_backward_kernel<T, V, kSlots, 1>, 1);
     });
 }
 

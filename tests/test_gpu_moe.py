@@ -94,7 +94,11 @@ def test_route_counts_bad_ids():
 
 MOVES = [(1, 8, 64, 7168, 0), (1, 1, 1, 1, 0), (5, 2, 3, 33, 0.3), (77, 3, 10, 1001, 0.2),
          (64, 8, 64, 256, 0), (130, 6, 17, 2050, 0.1), (9, 11, 4, 520, 0.4), (40, 4, 8, 4100, 1.0),
-         (300, 8, 60, 7168, 0.1), (2, 20, 7, 14336, 0)]
+         (300, 8, 60, 7168, 0.1), (2, 20, 7, 14336, 0),
+         # words of every size, one row of them more or less than a CTA's or a cluster's
+         (1, 2, 9, 14335, 0), (3, 1, 4, 2047, 0), (3, 4, 9, 2049, 0.2), (6, 5, 9, 4097, 0.2),
+         (2, 3, 9, 14334, 0.3), (400, 2, 5, 2046, 0.1), (400, 1, 5, 4100, 0.1), (401, 4, 5, 513, 0.1),
+         (700, 2, 64, 4104, 0.1), (700, 9, 64, 515, 0.1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
