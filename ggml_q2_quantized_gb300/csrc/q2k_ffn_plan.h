@@ -171,6 +171,14 @@ inline Plan make_segment_plan(int M, int rows, int tile_rows, int quads, int exp
     return best;
 }
 
+// A lane of the kernel that forms a projection's dz has the kGradEach columns from n on, of
+// rows of N values that lie one behind the other.  How many of them are the row's: in rows
+// of whole words all or none, so that a lane reads a word or nothing.  (Its rows of the
+// workspace are longer, up to a multiple of eight: with N = 4 mod 8 a lane begins where
+// the row ends.)
+constexpr int kGradEach = 4;
+Q2K_BOTH int grad_inside(int n, int N) { return N - n >= kGradEach ? kGradEach : N > n ? N - n : 0; }
+
 #undef Q2K_BOTH
 
 }  // namespace q2k

@@ -264,7 +264,6 @@ struct LinearGradArgs {
     int shares;               // CTAs of a segment and kGradCols columns (with dbias: a cluster)
 };
 constexpr int kGradCols = 128, kGradWarps = 8, kGradAtOnce = 4;
-constexpr int kGradEach = 4;  // columns of a lane
 static_assert(kGradCols == 32 * kGradEach, "a warp's columns");
 
 // act'(g) in few instructions, which bound this kernel beside its loads (7.3 million
@@ -330,6 +329,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
     lo += static_cast<int>(len * share / p.shares);
     constexpr bool kZ = kAct != kActNone;
     const bool vec = p.N % kGradEach == 0;
+    const int inside = grad_inside(n, p.N);  // (the lane's other columns are zeros)
     float sum[kGradEach] = {};
     for (int m0 = lo + warp; m0 < hi && n < p.pitch; m0 += kGradAtOnce * kGradWarps) {
         Lane g[kGradAtOnce], z[kGradAtOnce];
@@ -339,12 +339,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
             const int m = min(m0 + u * kGradWarps, hi - 1);
             const size_t at = static_cast<size_t>(m) * p.N + n;
             if (vec) {
+                if (inside == 0) continue;
                 g[u].word = __ldg(reinterpret_cast<const uint2*>(p.dy + at));
                 if (kZ) z[u].word = __ldg(reinterpret_cast<const uint2*>(p.z + at));
             } else {
 #pragma unroll
                 for (int e = 0; e < kGradEach; ++e) {
-                    const bool ok = n + e < p.N;
+                    const bool ok = e < inside;
                     g[u].value[e] = ok ? p.dy[at + e] : __float2bfloat16_rn(0.f);
                     z[u].value[e] = ok && kZ ? p.z[at + e] : __float2bfloat16_rn(0.f);
                 }
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
             }
             if (p.to != nullptr) *reinterpret_cast<uint2*>(p.to + static_cast<size_t>(m) * p.pitch + n) = d.word;
             if (p.dz != nullptr)
-                for (int e = 0; e < kGradEach && n + e < p.N; ++e) p.dz[static_cast<size_t>(m) * p.N + n + e] = d.value[e];
+                for (int e = 0; e < kGradEach && e < inside; ++e) p.dz[static_cast<size_t>(m) * p.N + n + e] = d.value[e];
         }
     }
     if (p.dbias == nullptr) return;  // (all CTAs alike)
