@@ -171,6 +171,55 @@ inline Plan make_segment_plan(int M, int rows, int tile_rows, int quads, int exp
     return best;
 }
 
+// ---- tokens in segments --------------------------------------------------------
+// The offsets are data of the GPU that no call has seen: whatever they are, what follows
+// gives tokens of the M, segments that there are, and no more tiles than there is room for.
+
+Q2K_BOTH int held(int v, int least, int most) { return v < least ? least : v > most ? most : v; }
+
+struct Tokens {
+    int lo, hi;  // 0 <= lo <= hi <= M
+};
+// Those of segment e: [offsets[e], offsets[e + 1]).
+Q2K_BOTH Tokens segment_tokens(const int* offsets, int e, int M) {
+    Tokens t;
+    t.lo = held(offsets[e], 0, M);
+    t.hi = held(offsets[e + 1], t.lo, M);
+    return t;
+}
+Q2K_BOTH int tiles_of(Tokens t, int rows) { return (t.hi - t.lo + rows - 1) / rows; }
+
+struct TableEntry {
+    int segment, first, tokens;
+};
+// Tile t of the table, t < begins[segments]: the last segment whose tiles begin at t or
+// before has it.  begins: for each segment the tiles before it, held at the room there is;
+// then their count, held the same.
+Q2K_BOTH TableEntry table_entry(const int* begins, const int* offsets, int segments, int M, int rows, int t) {
+    int a = 0, b = segments;
+    while (b - a > 1) {
+        const int mid = (a + b) / 2;
+        if (begins[mid] <= t) a = mid;
+        else b = mid;
+    }
+    const Tokens tokens = segment_tokens(offsets, a, M);
+    TableEntry entry;
+    entry.segment = a;
+    entry.first = tokens.lo + (t - begins[a]) * rows;
+    entry.tokens = held(tokens.hi - entry.first, 0, rows);
+    return entry;
+}
+
+// The segment of a token that a warp looks for: its lanes found part `part` of `each`
+// offsets, the last that begins at the token or before (-1: none), and `before` of that
+// part's offsets there.  -1: no segment's.
+Q2K_BOTH int segment_found(int part, int each, int before, int segments) {
+    const int e = part * each + before - 1;
+    return part >= 0 && e >= 0 && e < segments ? e : -1;
+}
+
+// ---- the gradient of a projection's activation ---------------------------------
+
 // A lane of the kernel that forms a projection's dz has the kGradEach columns from n on, of
 // rows of N values that lie one behind the other.  How many of them are the row's: in rows
 // of whole words all or none, so that a lane reads a word or nothing.  (Its rows of the

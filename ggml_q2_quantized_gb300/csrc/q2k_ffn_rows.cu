@@ -501,8 +501,7 @@ __device__ __forceinline__ int segment_of(const int* __restrict__ offsets, int s
         const int at = part * each + j;
         before += at <= segments && offsets[min(at, segments)] <= m;
     }
-    const int e = part * each + __reduce_add_sync(0xFFFFFFFFu, before) - 1;
-    return e < segments ? e : -1;
+    return segment_found(part, each, __reduce_add_sync(0xFFFFFFFFu, before), segments);
 }
 
 // Whose tokens and matrices a CTA takes: all of the call's, or a tile of a segment's.

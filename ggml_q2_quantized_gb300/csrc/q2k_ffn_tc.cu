@@ -114,11 +114,7 @@ __device__ __forceinline__ void make_table(const TableArgs& p, int* first) {  //
     int carry = 0;
     for (int e0 = 0; e0 < p.segments; e0 += threads) {
         const int e = e0 + tid;
-        int tiles = 0;
-        if (e < p.segments) {
-            const int lo = min(max(p.offsets[e], 0), p.M), hi = min(max(p.offsets[e + 1], lo), p.M);
-            tiles = (hi - lo + p.rows - 1) / p.rows;
-        }
+        const int tiles = e < p.segments ? tiles_of(segment_tokens(p.offsets, e, p.M), p.rows) : 0;
         int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -143,15 +139,8 @@ __device__ __forceinline__ void make_table(const TableArgs& p, int* first) {  //
     }
     __syncthreads();
     for (int t = tid; t < carry; t += threads) {
-        int a = 0, b = p.segments;  // the last segment that begins at t or before has it
-        while (b - a > 1) {
-            const int mid = (a + b) / 2;
-            if (first[mid] <= t) a = mid;
-            else b = mid;
-        }
-        const int lo = min(max(p.offsets[a], 0), p.M), hi = min(max(p.offsets[a + 1], lo), p.M);
-        const int m = lo + (t - first[a]) * p.rows;
-        p.table[t] = make_int4(a, m, min(p.rows, hi - m), 0);
+        const TableEntry entry = table_entry(first, p.offsets, p.segments, p.M, p.rows, t);
+        p.table[t] = make_int4(entry.segment, entry.first, entry.tokens, 0);
     }
 }
 
@@ -195,8 +184,8 @@ grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restric
         --block;
         --blocks;
         // tokens in segments: from the first to the last one's end
-        first = min(max(t.offsets[0], 0), M);
-        M = min(max(t.offsets[t.segments], 0), M);
+        first = held(t.offsets[0], 0, M);
+        M = held(t.offsets[t.segments], 0, M);
     }
     if (block == 0)
         for (int c = threadIdx.x; c < n_counts; c += blockDim.x) counts[c] = 0u;
@@ -319,14 +308,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) linear_grad_kernel(LinearG
     }
     if (blockIdx.x == 0 && segment == 0)
         for (int c = threadIdx.x; c < p.n_counts; c += blockDim.x) p.counts[c] = 0u;
-    int lo = 0, hi = p.M;
-    if (segments) {
-        lo = min(max(p.table.offsets[segment], 0), p.M);
-        hi = min(max(p.table.offsets[segment + 1], lo), p.M);
-    }
-    const long long len = hi - lo;
-    hi = lo + static_cast<int>(len * (share + 1) / p.shares);
-    lo += static_cast<int>(len * share / p.shares);
+    const Tokens tokens = segments ? segment_tokens(p.table.offsets, segment, p.M) : Tokens{0, p.M};
+    const long long len = tokens.hi - tokens.lo;
+    const int lo = tokens.lo + static_cast<int>(len * share / p.shares);
+    const int hi = tokens.lo + static_cast<int>(len * (share + 1) / p.shares);
     constexpr bool kZ = kAct != kActNone;
     const bool vec = p.N % kGradEach == 0;
     const int inside = grad_inside(n, p.N);  // (the lane's other columns are zeros)
