@@ -1259,6 +1259,8 @@ def moe_combine(ys, routes, weights=None, residual=None, out=None):
 
     ``ys`` f32 or bf16 ``[n_tokens * top_k, width]``; ``weights`` f32 ``[n_tokens,
     top_k]`` or None (all 1); ``residual`` ``[n_tokens, width]`` in ys' dtype or None.
+    The gradients are ``moe_combine_backward``'s; without weights ys' is ``moe_sort`` of
+    y's.
     """
     if out is None:
         quick = _quick_mod or _quick()
@@ -1285,7 +1287,8 @@ def moe_combine(ys, routes, weights=None, residual=None, out=None):
 def moe_combine_backward(dy, ys, routes, weights):
     """The gradients of ``moe_combine``: ``(dys, dweights)`` from that of y.  ``dys`` as
     ``ys`` (zeros in rows without an expert), ``dweights`` f32 as ``weights``.  The
-    residual's gradient is ``dy``."""
+    residual's gradient is ``dy``.  Where ``moe_combine`` had no weights, ``dys`` is
+    ``moe_sort(dy, routes)``."""
     quick = _quick_mod or _quick()
     done = quick.combine_backward(dy, ys, routes.rows, routes.offsets, weights) if quick else None
     if done.__class__ is int:

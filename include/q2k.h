@@ -709,7 +709,8 @@ size_t q2k_gated_ffn_experts_backward_workspace_bytes(const q2k_gated_ffn_params
  * call's), contiguous rows of `width`, aligned to their element (16-byte aligned
  * rows are the fast ones); sums are f32, in the order of the slots, rounded once.
  * Calls are asynchronous on `stream`, allocate nothing, take no workspace and may
- * be captured; the same inputs give the same bits.
+ * be captured; the same inputs give the same bits.  No output may alias an input or
+ * another output.
  *
  * Choice i = token * top_k + slot.  `rows` (i32 [n_tokens, top_k]) is each
  * choice's place, `offsets` (i32 [n_experts + 1]) where each expert's places
@@ -765,7 +766,7 @@ q2k_status q2k_moe_combine(const void *ys, size_t ys_elems, const int32_t *rows,
 
 /* q2k_moe_combine_backward - dys[rows[t, s]] = weights[t, s] dy[t] and dweights[t, s]
  * = sum over the row of dy[t] ys[rows[t, s]] (0 for a choice without an expert).  The
- * residual's gradient is dy.
+ * residual's gradient is dy.  Without weights (all 1) dys is q2k_moe_sort of dy.
  *   dy        [n_tokens, width]
  *   dys       [n_tokens * top_k, width]; fully overwritten (with the `rows` of a route)
  *   dweights  device f32 [n_tokens, top_k] */
