@@ -991,6 +991,10 @@ def linear(x, w, n: int, bias=None, act=None, residual=None, save: bool = False,
     ``const_weights`` and ``workspace`` as in ``gated_ffn``; nothing is recorded for
     autograd.  ``routes`` as in ``gated_ffn``: ``w`` then holds ``n_experts`` matrices
     and ``bias`` is ``[n_experts, n]``.
+
+    Above 16 bf16 or 8 f32 tokens "auto" rounds x and W to bf16, also where x is f32;
+    ``path="gemv"`` keeps the weights exact, in a time that grows with every 16 (8)
+    tokens (4096 x 4096, 64 f32 tokens: 61 us against 16).
     """
     if out is None and workspace.__class__ is str:
         quick = _quick_mod or _quick()

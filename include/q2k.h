@@ -636,7 +636,8 @@ size_t q2k_matmul_lora_workspace_bytes(q2k_path path, const q2k_lora_params *par
  * Tokens in no segment (before the first, behind the last) reach no result, and
  * their rows of every output stay as they are.  Offsets that do not ascend within 0 .. m give
  * wrong results, but touch nothing outside the buffers.  Q2K_PATH_AUTO takes the exact
- * weights up to 16 (bf16) or 8 (f32) tokens, or eight (four) for each expert. */
+ * weights up to 16 (bf16) or 8 (f32) tokens, or eight (four) for each expert; above, x and
+ * W are rounded to bf16, f32 activations too, unless Q2K_PATH_GEMV is asked for. */
 
 typedef struct q2k_linear_params {
     uint32_t m;         /* tokens, >= 1 */
@@ -717,7 +718,8 @@ size_t q2k_gated_ffn_experts_backward_workspace_bytes(const q2k_gated_ffn_params
  * begin and the last one's end: q2k_moe_route writes them.  Choices without an
  * expert have the places from offsets[n_experts] on, which these calls write as
  * zeros and never read.  The other calls take any `rows` and `offsets`: a place
- * outside 0 .. n_tokens * top_k - 1 is neither read nor written. */
+ * outside 0 .. n_tokens * top_k - 1 is neither read nor written, and a place that two
+ * choices share is written by one or the other. */
 typedef struct q2k_moe_params {
     uint32_t n_tokens;  /* 1..Q2K_FFN_MAX_TOKENS */
     uint32_t top_k;     /* choices of a token, 1..Q2K_MOE_MAX_TOP_K */
